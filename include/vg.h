@@ -387,6 +387,143 @@ VG_API int vg_subm_conv3d_fwd_noalloc(const void* nbr_ws, const uint32_t* nbr, c
  * address cannot be looked up or the copy fails.  Allocates nothing. */
 VG_API int vg_subm_conv3d_fwd_noalloc_status(void* stream);
 
+/* ======================================================================================
+ * Attention-block operators
+ * The pages stop at the convolution; the models that use it put blocks between the
+ * convolutions in which the voxel tokens attend to an encoder's states (an image's or a
+ * text's), and train both.  The calls below are that block's own arithmetic: the norm and
+ * rotation of queries and keys, the attention, and the optimizer step.
+ * ====================================================================================== */
+
+/* Rows of heads: element (row, head, i) of a [rows][heads][head_dim] tensor lies at
+ * data + row * row_stride + head * head_stride + i (strides in elements).  Tokens may
+ * come first (row_stride = heads * head_dim or more, as in a packed projection) or heads
+ * (head_stride = rows * row_stride).  data is 16-byte aligned and both strides are
+ * multiples of 16 bytes and at least head_dim; the elements of an output do not overlap. */
+typedef struct {
+    void* data;
+    int64_t row_stride, head_stride;
+} vg_heads;
+
+/* --------------------------------------------------------------------------------------
+ * Norm of queries and keys for each head and rotary positions with up to three axes, in one
+ * pass (neither q nor k is read twice; either may be absent, with 0 heads).
+ *   n = x / sqrt(mean_i x_i^2 + eps) * weight            (skipped with VG_QK_NO_NORM)
+ *   pair p of axis a turns by t = (float)coords[row][1 + a] * freqs[p]:
+ *   (y0, y1) = (n0 cos t - n1 sin t, n0 sin t + n1 cos t)
+ * Axis a owns axis_pairs[a] consecutive pairs, axis 0 first; pairs beyond their sum are not
+ * turned.  Pair p is elements (2p, 2p + 1), or (p, p + head_dim/2) with VG_ROPE_HALVES.
+ * coords is the neighbour map's [N][4] int32 (b, x, y, z), or (b, time, height, width) of
+ * another encoder's tokens; column 0 is not used.  coords and freqs NULL: norm alone.
+ * Weights are [heads][head_dim] ([head_dim] with VG_QK_SHARED_WEIGHT), of `dtype`, 16-byte
+ * aligned; NULL: ones.  head_dim is a multiple of 8, at most 256; 0 < heads <= 4096 in all.
+ * Sums and angles are fp32; outputs are rounded once.  The forward may run in place
+ * (an output with its input's data and strides).
+ * -------------------------------------------------------------------------------------- */
+#define VG_ROPE_HALVES      0x200u
+#define VG_QK_NO_NORM       0x400u
+#define VG_QK_SHARED_WEIGHT 0x800u
+
+VG_API int vg_qk_norm_rope_fwd(int64_t N, int heads_q, int heads_k, int head_dim, int dtype, const vg_heads* q,
+                               const vg_heads* k, const void* q_weight, const void* k_weight,
+                               const int32_t* coords, const float* freqs, const int axis_pairs[3], double eps,
+                               unsigned flags, const vg_heads* q_out, const vg_heads* k_out, void* stream);
+/* Bytes of workspace of the backward pass (0 if the arguments are invalid). */
+VG_API size_t vg_qk_norm_rope_workspace_bytes(int64_t N, int heads_q, int heads_k, int head_dim);
+/* Gradients of the forward's inputs q, k (the unnormed ones; not read with VG_QK_NO_NORM)
+ * and of its weights, summed over the rows (and over the heads that share a weight) in a
+ * fixed order.  grad_q_weight / grad_k_weight NULL: not wanted.  ws: 256-byte aligned,
+ * needed when a weight gradient is wanted. */
+VG_API int vg_qk_norm_rope_bwd(int64_t N, int heads_q, int heads_k, int head_dim, int dtype, const vg_heads* q,
+                               const vg_heads* k, const void* q_weight, const void* k_weight,
+                               const int32_t* coords, const float* freqs, const int axis_pairs[3], double eps,
+                               unsigned flags, const vg_heads* grad_q_out, const vg_heads* grad_k_out,
+                               const vg_heads* grad_q, const vg_heads* grad_k, void* grad_q_weight,
+                               void* grad_k_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * Cross attention: the tokens of each sample attend to that sample's encoder states.
+ *   out = softmax(scale q k^T) v over the sample's valid keys; lse = log sum exp(scale q k^T).
+ * Sample b has the query rows [q_offsets[b], q_offsets[b+1]) and the key rows
+ * [k_offsets[b], k_offsets[b+1]), of which the first k_lens[b] are valid (k_lens NULL: all).
+ * Rows past the valid ones are never used, whatever they hold; their gradients are zero.  A
+ * sample without valid keys gives out = 0 and lse = -inf, and takes no part in any gradient.
+ * heads_q is a multiple of heads_k: query head h reads key head h / (heads_q / heads_k), and
+ * the gradient of a key head is the sum over its query heads.
+ *   dtype VG_F16 / VG_BF16: tensor cores, fp32 softmax and sums, the scores' weights rounded
+ *   to dtype before the second product.  VG_F32: fp32 multiply-adds throughout.
+ *   head_dim is a multiple of 8, at most 128; scale > 0 and finite; lse is [heads_q][n_q].
+ * With few query rows the keys are cut into parts that run side by side, with few keys the
+ * queries (backward); parts are joined in a fixed order, so every result is the same from
+ * run to run.
+ * -------------------------------------------------------------------------------------- */
+typedef struct {
+    int64_t n_q, n_k;            /* rows of q, of k and v: q_offsets[batch], k_offsets[batch]  */
+    int batch, heads_q, heads_k, head_dim, dtype;
+    float scale;
+    const int32_t* q_offsets;    /* [batch + 1], device                                       */
+    const int32_t* k_offsets;    /* [batch + 1], device                                       */
+    const int32_t* k_lens;       /* [batch], device, or NULL                                   */
+} vg_attn;
+
+/* Bytes of workspace (0 if the arguments are invalid; the offset pointers are not looked
+ * at).  backward: 1 for a workspace that vg_cross_attn_bwd takes too. */
+VG_API size_t vg_cross_attn_workspace_bytes(const vg_attn* a, int backward);
+/* ws: 256-byte aligned; its first 4 bytes, the error record, are zero before the first
+ * call.  lse may be NULL.  Asynchronous.  Offsets or lengths that are no partition of the
+ * rows are found on the device: nothing is written and vg_cross_attn_status says so. */
+VG_API int vg_cross_attn_fwd(const vg_attn* a, const vg_heads* q, const vg_heads* k, const vg_heads* v,
+                             const vg_heads* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+/* out and lse are the forward's. */
+VG_API int vg_cross_attn_bwd(const vg_attn* a, const vg_heads* q, const vg_heads* k, const vg_heads* v,
+                             const vg_heads* out, const float* lse, const vg_heads* grad_out, const vg_heads* grad_q,
+                             const vg_heads* grad_k, const vg_heads* grad_v, void* ws, size_t ws_bytes,
+                             void* stream);
+/* Synchronises `stream`; VG_ERR_INVALID_ARG if a call on ws found bad offsets,
+ * VG_ERR_DEVICE_TIMEOUT if a bounded device-side wait gave up, else VG_OK.  Clears the record. */
+VG_API int vg_cross_attn_status(void* ws, void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * AdamW step over many tensors at once.
+ *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr/(1 - beta1^step) m / (sqrt(v)/sqrt(1 - beta2^step) + eps)
+ * p is master where given (param then gets p rounded to its dtype), else param.  Every
+ * operation is one fp32 rounding, in the order written.
+ * state_bits 32: m and v are fp32 [n].  state_bits 8: m and v are codes, uint8 [n], with
+ * one fp32 scale for every VG_ADAMW_BLOCK elements in m_scale and v_scale [ceil(n/256)];
+ * codes 0 with any scale are zero states.  Scales are powers of two.  A code c stands for
+ *   m: (c & 128 ? -1 : 1) * x * scale, a = c & 127: x = a / 512 below 8, else
+ *      (1 + (a & 7)/8) 2^((a >> 3) - 7); 127 is NaN;
+ *   v: (x * scale)^2, x = 0 at c = 0, else (1 + ((c - 1) & 15)/16) 2^((c - 1) >> 4); 255 is NaN.
+ * New states take the nearest value (ties to even mantissas; a positive v never becomes
+ * zero); a state that is not finite is held as NaN.  The step itself uses the moments
+ * before they are rounded.
+ * -------------------------------------------------------------------------------------- */
+#define VG_ADAMW_BLOCK 256
+
+typedef struct {
+    void* param;            /* [n] of dtype, updated                                   */
+    const void* grad;       /* [n] of dtype                                            */
+    float* master;          /* [n] or NULL, updated                                    */
+    void* m;                /* [n] fp32 or codes, updated                              */
+    void* v;
+    float* m_scale;         /* [ceil(n / 256)], 8-bit states only, updated             */
+    float* v_scale;
+    int64_t n;
+    double weight_decay;
+    int dtype;
+} vg_adamw_tensor;
+
+/* tensors: HOST array of `count` (read before the call returns; the pointers in it are
+ * device pointers).  step counts from 1.  Asynchronous; one launch for up to 384 tensors.
+ * Pointers aligned to 16 bytes (codes: 8) take the wide path, others are served element by
+ * element. */
+VG_API int vg_adamw_step(const vg_adamw_tensor* tensors, int count, int state_bits, int64_t step, double lr,
+                         double beta1, double beta2, double eps, double grad_scale, void* stream);
+/* out[i] = the value that 8-bit state code i stands for; second: 0 for m, 1 for v. */
+VG_API int vg_adamw_decode(const uint8_t* codes, const float* scales, int64_t n, int second, float* out,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif

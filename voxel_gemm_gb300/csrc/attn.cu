@@ -1,0 +1,233 @@
+// Cross attention: the plan of a call (how rows are packed, how long axes are cut,
+// where the scratch lies), the row sums that the backward pass starts from, and the
+// joins of split work.
+#include "attn.cuh"
+
+namespace vg {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// 8 consecutive elements of a head's row, 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = to_f32<T>(e[j]);
+    }
+}
+
+// stats[packed row] = (lse * log2 e, sum_d dO O): a group of 1..16 lanes per row,
+// 16-byte loads; reads O and dO once, bound by memory.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int lanes) {
+    const int lane = threadIdx.x & (lanes - 1);
+    const int64_t rows = a.n_q * a.hq;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / lanes);
+    const int64_t first = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+    for (int64_t r0 = first - threadIdx.x / lanes; r0 < rows; r0 += step) {  // the same trips for the whole block
+        const int64_t r = r0 + threadIdx.x / lanes;
+        const int64_t i = r / a.hq;
+        const int h = (int)(r - i * a.hq);
+        float sum = 0.f;
+        if (r < rows && lane * 8 < a.d) {
+            float o[8], g[8];
+            load8<T>(head_row<const T>(a.o, i, h) + lane * 8, o);
+            load8<T>(head_row<const T>(a.go, i, h) + lane * 8, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fmaf(o[j], g[j], sum);
+        }
+        for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (r < rows && lane == 0) {
+            const int hs = h / a.gp;
+            a.stats[((int64_t)hs * a.n_q + i) * a.gp + (h - hs * a.gp)] =
+                make_float2(a.lse[(int64_t)h * a.n_q + i] * 1.4426950408889634f, sum);
+        }
+    }
+}
+
+// The splits' outputs, each normalised by its own sum, weighed by exp(lse_s - max lse).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_attn_join_out(const AttnArgs a) {
+    if (!attn_offsets_ok(a)) return;
+    const int q4 = a.d / 4;
+    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (e >= a.n_q * a.hq * q4) return;
+    const int64_t r = e / q4;
+    const int c = (int)(e - r * q4) * 4;
+    const int64_t i = r / a.hq;
+    const int h = (int)(r - i * a.hq);
+    const float* lse = a.part_lse + (int64_t)h * a.n_q + i;
+    const int64_t lstep = (int64_t)a.hq * a.n_q;
+    float top = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) top = fmaxf(top, lse[s * lstep]);
+    const float base = top == -INFINITY ? 0.f : top;
+    const float* src = a.part + r * a.d + c;
+    const int64_t step = a.n_q * a.hq * a.d;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const float w = expf(lse[s * lstep] - base);
+        const float4 v = *reinterpret_cast<const float4*>(src + s * step);
+        sum += w;
+        if (top == -INFINITY) {  // no keys in any part (zeros), or scores of -inf alone (NaN)
+            acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+        } else if (w != 0.f) {   // a part without keys, or of scores -inf alone, weighs nothing
+            acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
+        }
+    }
+    const float inv = top == -INFINITY ? 1.f : 1.f / sum;
+    T* o = head_row<T>(a.o, i, h) + c;
+    o[0] = from_f32<T>(acc.x * inv);
+    o[1] = from_f32<T>(acc.y * inv);
+    o[2] = from_f32<T>(acc.z * inv);
+    o[3] = from_f32<T>(acc.w * inv);
+    if (c == 0 && a.lse) a.lse[(int64_t)h * a.n_q + i] = base + logf(sum);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_attn_join_sum(const AttnArgs a, const float* part, int splits,
+                                                            int64_t rows, int heads, vg_heads dst) {
+    if (!attn_offsets_ok(a)) return;
+    const int q4 = a.d / 4;
+    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (e >= rows * heads * q4) return;
+    const int64_t r = e / q4;
+    const int c = (int)(e - r * q4) * 4;
+    const float* src = part + r * a.d + c;
+    const int64_t step = rows * heads * a.d;
+    float4 acc = *reinterpret_cast<const float4*>(src);
+#pragma unroll 4
+    for (int s = 1; s < splits; ++s) {
+        const float4 v = *reinterpret_cast<const float4*>(src + s * step);
+        acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+    const int64_t i = r / heads;
+    T* o = head_row<T>(dst, i, (int)(r - i * heads)) + c;
+    o[0] = from_f32<T>(acc.x);
+    o[1] = from_f32<T>(acc.y);
+    o[2] = from_f32<T>(acc.z);
+    o[3] = from_f32<T>(acc.w);
+}
+
+int launched() { return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA; }
+
+template <typename T>
+int stats(const AttnArgs& a, cudaStream_t s) {
+    int lanes = 1;
+    while (lanes * 8 < a.d) lanes <<= 1;
+    const int64_t blocks = (a.n_q * a.hq + kThreads / lanes - 1) / (kThreads / lanes);
+    k_attn_stats<T><<<(unsigned)std::min<int64_t>(blocks, 152 * 16), kThreads, 0, s>>>(a, lanes);
+    return launched();
+}
+template <typename T>
+int join_out(const AttnArgs& a, cudaStream_t s) {
+    const int64_t n = a.n_q * a.hq * (a.d / 4);
+    k_attn_join_out<T><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+    return launched();
+}
+template <typename T>
+int join_sum(const AttnArgs& a, const float* part, int splits, int64_t rows, int heads, const vg_heads& dst,
+             cudaStream_t s) {
+    const int64_t n = rows * heads * (a.d / 4);
+    const unsigned blocks = (unsigned)((n + kThreads - 1) / kThreads);
+    k_attn_join_sum<T><<<blocks, kThreads, 0, s>>>(a, part, splits, rows, heads, dst);
+    return launched();
+}
+
+#define VG_BY_TYPE(f, ...)                                \
+    (dtype == VG_F32 ? f<float>(__VA_ARGS__)              \
+     : dtype == VG_F16 ? f<__half>(__VA_ARGS__) : f<__nv_bfloat16>(__VA_ARGS__))
+
+// Parts to cut an axis of `tiles` tiles into, when there are `units` independent
+// tiles of work along the other one: enough that every SM has two blocks, but at
+// least four tiles in a part.
+int parts(int64_t units, int64_t tiles, int sms) {
+    if (units <= 0) return 1;
+    const int64_t want = (2 * (int64_t)sms + units - 1) / units;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles / 4, 256}));
+}
+
+}  // namespace
+
+int attn_plan(const AttnShape& c, AttnPlan* P) {
+    if (c.n_q < 0 || c.n_k < 0 || c.n_q >= (int64_t(1) << 31) || c.n_k >= (int64_t(1) << 31)) return VG_ERR_INVALID_ARG;
+    if (c.batch <= 0 || c.hq <= 0 || c.hk <= 0 || c.hq % c.hk || c.d <= 0) return VG_ERR_INVALID_ARG;
+    if (c.dtype != VG_F32 && c.dtype != VG_F16 && c.dtype != VG_BF16) return VG_ERR_INVALID_ARG;
+    if (c.d % 8 || c.d > 128 || c.hq > 65535) return VG_ERR_UNSUPPORTED;
+    AttnPlan p;
+    p.sms = plan_sms(0);
+    p.gp = 1;
+    const int64_t qt = attn_max_tiles(c.n_q, c.batch, 1, 64), kt = attn_max_tiles(c.n_k, c.batch, 1, 64);
+    p.s_fwd = parts(qt * c.hq, kt / c.batch, p.sms);
+    p.s_dq = p.s_fwd;
+    p.s_dkv = parts(kt * c.hk, qt / c.batch, p.sms);
+    const size_t vq = (size_t)c.n_q * c.hq, vk = (size_t)c.n_k * c.hk;
+    size_t fwd = 0, bwd = 0;
+    if (p.s_fwd > 1) {
+        fwd = align_up(p.s_fwd * vq * c.d * 4, 256);
+        p.off_lse = 256 + fwd;
+        fwd += align_up(p.s_fwd * vq * 4, 256);
+    }
+    if (c.backward) {
+        size_t o = align_up(vq * sizeof(float2), 256);
+        p.off_dq = 256 + o;
+        if (p.s_dq > 1) o += align_up(p.s_dq * vq * c.d * 4, 256);
+        p.off_dk = 256 + o;
+        if (p.s_dkv > 1) o += align_up(p.s_dkv * vk * c.d * 4, 256);
+        p.off_dv = 256 + o;
+        if (p.s_dkv > 1) o += align_up(p.s_dkv * vk * c.d * 4, 256);
+        bwd = o;
+    }
+    p.total = 256 + std::max(fwd, bwd);
+    *P = p;
+    return VG_OK;
+}
+
+int attn_fwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s) {
+    if (a.n_q == 0) return VG_OK;
+    a.gp = p.gp;
+    a.err = reinterpret_cast<uint32_t*>(ws);
+    a.splits = p.s_fwd;
+    a.part = reinterpret_cast<float*>(ws + 256);
+    a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
+    const int st = attn_simt_fwd(a, dtype, s);
+    if (st != VG_OK || a.splits == 1) return st;
+    return VG_BY_TYPE(join_out, a, s);
+}
+
+int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s) {
+    a.gp = p.gp;
+    a.err = reinterpret_cast<uint32_t*>(ws);
+    a.stats = reinterpret_cast<float2*>(ws + 256);
+    int st;
+    if (a.n_q > 0) {
+        if ((st = VG_BY_TYPE(stats, a, s)) != VG_OK) return st;
+        a.splits = p.s_dq;
+        a.part = reinterpret_cast<float*>(ws + p.off_dq);
+        if ((st = attn_simt_dq(a, dtype, s)) != VG_OK) return st;
+        if (a.splits > 1 && (st = VG_BY_TYPE(join_sum, a, a.part, a.splits, a.n_q, a.hq, a.gq, s)) != VG_OK) return st;
+    }
+    if (a.n_k > 0) {
+        a.splits = p.s_dkv;
+        a.part = reinterpret_cast<float*>(ws + p.off_dk);
+        float* part_dv = reinterpret_cast<float*>(ws + p.off_dv);
+        if ((st = attn_simt_dkv(a, part_dv, dtype, s)) != VG_OK) return st;
+        if (a.splits > 1) {
+            if ((st = VG_BY_TYPE(join_sum, a, a.part, a.splits, a.n_k, a.hk, a.gk, s)) != VG_OK) return st;
+            if ((st = VG_BY_TYPE(join_sum, a, part_dv, a.splits, a.n_k, a.hk, a.gv, s)) != VG_OK) return st;
+        }
+    }
+    return VG_OK;
+}
+
+}  // namespace vg

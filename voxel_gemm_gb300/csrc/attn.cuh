@@ -1,0 +1,136 @@
+// Cross attention: what the fp32 and the tensor-core kernels share -- arguments,
+// the layout of the work, the lookup of a tile's sample and the joins of split
+// work.
+//
+// Rows of work.  G = heads_q / heads_k query heads read one key head.  When G is a
+// power of two up to 16, a sample's queries and those G heads are taken together
+// as "packed rows" r = i * gp + g (query i, head g of the group; gp = G), so the
+// keys and values are read once for all of them; otherwise gp = 1 and each query
+// head is its own list of rows.  A "head set" hs in [0, heads_q / gp) is gp
+// consecutive query heads; its key head is hs * gp / G.
+#pragma once
+#include "common.cuh"
+#include "internal.h"
+
+namespace vg {
+
+struct AttnArgs {
+    // shapes
+    int64_t n_q, n_k;
+    int batch, hq, hk, d;
+    int gp;                      // query heads packed into rows
+    const int32_t* q_off;        // [batch + 1]
+    const int32_t* k_off;        // [batch + 1]
+    const int32_t* k_len;        // [batch] or null: every row between offsets is valid
+    float scale;                 // of the scores
+    float scale_log2;            // scale * log2(e)
+    // tensors ([rows][heads][d], strides in elements)
+    vg_heads q, k, v, o, go, gq, gk, gv;
+    float* lse;                  // [hq][n_q]
+    // workspace
+    uint32_t* err;               // error record; words 1, 2: bits of the largest |dO row|, |V row| (fp16)
+    float2* stats;               // [hq / gp][n_q * gp]: (lse * log2 e, sum_d dO O) of every packed row
+    int splits;                  // parts of the axis that the kernel runs along
+    float* part;                 // split partial results (layouts at their kernels)
+    float* part_lse;
+};
+
+// The tile of one sample that a block works on.
+struct AttnTile {
+    int b;          // sample, -1: none
+    int first;      // first row of the tile within the sample's rows
+    int q0, lq;     // the sample's queries
+    int k0, lk;     // its keys: first row, valid rows
+    int krows;      // its key rows, valid or not
+};
+
+// Whether the offsets are a partition of the rows and the lengths fit it; by all
+// threads of the block, the same answer in each.  A bad array is recorded and the
+// kernel writes nothing, so that no wrong offset becomes a wrong address.
+__device__ __forceinline__ bool attn_offsets_ok(const AttnArgs& a) {
+    bool bad = false;
+    for (int b = threadIdx.x; b < a.batch; b += blockDim.x) {
+        const int q = a.q_off[b], q1 = a.q_off[b + 1], k = a.k_off[b], k1 = a.k_off[b + 1];
+        bad |= q < 0 || q1 < q || q1 > a.n_q || k < 0 || k1 < k || k1 > a.n_k;
+        bad |= b == 0 && (q != 0 || k != 0);
+        bad |= b == a.batch - 1 && (q1 != a.n_q || k1 != a.n_k);
+        if (a.k_len) bad |= a.k_len[b] < 0 || a.k_len[b] > k1 - k;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) atomicOr(a.err, kErrRange);
+    return !bad;
+}
+
+// Sample and first row of tile `t`, when every sample's rows (len * mult of them,
+// len from `off`) are cut into tiles of `rows`; by a whole warp, every lane gets
+// the answer.  Lanes take 32 samples at a time and prefix-sum their tile counts.
+__device__ __forceinline__ AttnTile attn_find_tile(const AttnArgs& a, const int32_t* off, int mult, int rows, int t) {
+    const int lane = threadIdx.x & 31;
+    AttnTile r;
+    r.b = -1;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const int64_t len = b < a.batch ? off[b + 1] - off[b] : 0;
+        const int tiles = (int)((len * mult + rows - 1) / rows);
+        int incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const uint32_t at = __ballot_sync(0xffffffffu, t < incl);
+        if (at) {
+            const int src = __ffs(at) - 1;
+            r.b = b0 + src;
+            r.first = (t - __shfl_sync(0xffffffffu, incl - tiles, src)) * rows;
+            r.q0 = a.q_off[r.b];
+            r.lq = a.q_off[r.b + 1] - r.q0;
+            r.k0 = a.k_off[r.b];
+            r.krows = a.k_off[r.b + 1] - r.k0;
+            r.lk = a.k_len ? a.k_len[r.b] : r.krows;
+            return r;
+        }
+        t -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return r;
+}
+
+// Most tiles that `total` rows in `batch` samples can make.
+inline int64_t attn_max_tiles(int64_t total, int batch, int mult, int rows) {
+    return total * mult / rows + std::min<int64_t>(batch, total);
+}
+
+// How a call is cut and where its scratch lies (byte offsets in the workspace; the
+// first 256 bytes are the error record).
+struct AttnShape {
+    int64_t n_q, n_k;
+    int batch, hq, hk, d, dtype;
+    bool backward;
+};
+struct AttnPlan {
+    int sms = 0, gp = 1;
+    int s_fwd = 1, s_dq = 1, s_dkv = 1;  // parts of the key axis (forward, dQ) and of the query axis (dK, dV)
+    size_t off_lse = 0, off_dq = 0, off_dk = 0, off_dv = 0, total = 0;
+};
+int attn_plan(const AttnShape& c, AttnPlan* P);
+int attn_fwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s);
+int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s);
+
+// Part `s` of `splits` of n tiles.
+__device__ __forceinline__ void attn_split(int n, int splits, int s, int* lo, int* hi) {
+    const int per = (n + splits - 1) / splits;
+    *lo = min(n, per * s);
+    *hi = min(n, *lo + per);
+}
+
+template <typename T>
+__device__ __forceinline__ T* head_row(const vg_heads& h, int64_t row, int head) {
+    return static_cast<T*>(h.data) + row * h.row_stride + head * h.head_stride;
+}
+
+// ---- fp32 path (attn_simt.cu) ----
+int attn_simt_fwd(const AttnArgs& a, int dtype, cudaStream_t s);
+int attn_simt_dq(const AttnArgs& a, int dtype, cudaStream_t s);
+int attn_simt_dkv(const AttnArgs& a, float* part_dv, int dtype, cudaStream_t s);
+
+}  // namespace vg

@@ -1,0 +1,400 @@
+// Cross attention on the CUDA cores, exact fp32: forward, query gradient, and key
+// and value gradient.
+//
+//   S = scale q k^T over a sample's valid keys, P = softmax(S), O = P V
+//   dP = dO V^T, dS = P (dP - delta), delta = sum_d dO O
+//   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
+//
+// One block of 256 threads per 64 queries (forward, dQ) or 64 keys (dK, dV) of a
+// sample and head, running along the other axis in tiles of 64 with the running
+// maximum and sum of the softmax; scores are recomputed from the saved log-sum in
+// the backward pass, so nothing of size queries x keys is stored.  Each thread
+// holds 4 x 4 of a 64 x 64 product, so every float4 read from shared memory feeds
+// 8 multiply-adds; row pitches of d + 4 and 68 floats keep those reads free of
+// bank conflicts.  Bound by the fp32 multiply-add rate.
+#include "attn.cuh"
+
+namespace vg {
+
+namespace {
+
+constexpr int kT = 64;             // rows and columns of a tile
+constexpr int kThreads = 256;
+constexpr int kPP = kT + 4;        // pitch of a score tile
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+    if constexpr (sizeof(T) == 4) {
+        return *reinterpret_cast<const float4*>(p);
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        const T* e = reinterpret_cast<const T*>(&u);
+        return make_float4(to_f32<T>(e[0]), to_f32<T>(e[1]), to_f32<T>(e[2]), to_f32<T>(e[3]));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = v;
+    } else {
+        uint2 u;
+        T* e = reinterpret_cast<T*>(&u);
+        e[0] = from_f32<T>(v.x); e[1] = from_f32<T>(v.y); e[2] = from_f32<T>(v.z); e[3] = from_f32<T>(v.w);
+        *reinterpret_cast<uint2*>(p) = u;
+    }
+}
+
+// 64 rows from `row` on of one head into shared memory; rows from `rows` on are zero.
+template <typename T>
+__device__ __forceinline__ void load_tile(float* dst, const vg_heads& h, int64_t row, int head, int rows, int d) {
+    const int q4 = d / 4;
+    for (int e = threadIdx.x; e < kT * q4; e += kThreads) {
+        const int r = e / q4, c = (e - r * q4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) v = load4<T>(head_row<const T>(h, row + r, head) + c);
+        *reinterpret_cast<float4*>(dst + r * (d + 4) + c) = v;
+    }
+}
+
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+    c = fmaf(a.x, b.x, c);
+    c = fmaf(a.y, b.y, c);
+    c = fmaf(a.z, b.z, c);
+    return fmaf(a.w, b.w, c);
+}
+
+// acc[a][b] = sum_d A[ty + 16 a][d] B[tx + 16 b][d]
+__device__ __forceinline__ void product_nt(const float* A, const float* B, int d, int ty, int tx, float (&acc)[4][4]) {
+    const int p = d + 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 2
+    for (int c = 0; c < d; c += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * p + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * p + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = dot4(x[i], y[j], acc[i][j]);
+    }
+}
+
+// acc[a][c] (columns 4 tx + 64 c ..) += sum_j W[ty + 16 a][j] B[j][columns]
+template <int NC>
+__device__ __forceinline__ void product_nn(const float* W, const float* B, int d, int ty, int tx,
+                                           float4 (&acc)[4][NC]) {
+    const int p = d + 4;
+#pragma unroll 2
+    for (int j = 0; j < kT; j += 4) {
+        float4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty + 16 * i) * kPP + j);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int col = tx * 4 + 64 * c;
+            if (col >= d) continue;
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const float4 v = *reinterpret_cast<const float4*>(B + (j + jj) * p + col);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float s = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
+                    acc[i][c].x = fmaf(s, v.x, acc[i][c].x);
+                    acc[i][c].y = fmaf(s, v.y, acc[i][c].y);
+                    acc[i][c].z = fmaf(s, v.z, acc[i][c].z);
+                    acc[i][c].w = fmaf(s, v.w, acc[i][c].w);
+                }
+            }
+        }
+    }
+}
+
+template <int NC>
+__device__ __forceinline__ void zero(float4 (&acc)[4][NC]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+__device__ __forceinline__ float4 times(float4 v, float s) { return make_float4(v.x * s, v.y * s, v.z * s, v.w * s); }
+
+__device__ __forceinline__ AttnTile block_tile(const AttnArgs& a, const int32_t* off) {
+    return attn_find_tile(a, off, 1, kT, (int)blockIdx.x);
+}
+
+// ---------------------------------------------------------------- forward
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
+    extern __shared__ float sm[];
+    const int p = a.d + 4;
+    float *sQ = sm, *sK = sQ + kT * p, *sV = sK + kT * p, *sP = sV + kT * p;
+    if (!attn_offsets_ok(a)) return;
+    const AttnTile t = block_tile(a, a.q_off);
+    if (t.b < 0) return;
+    const int h = blockIdx.y, hk = h / (a.hq / a.hk);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    load_tile<T>(sQ, a.q, t.q0 + t.first, h, t.lq - t.first, a.d);
+    float m[4], l[4];
+    float4 acc[4][NC];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    zero<NC>(acc);
+    int lo, hi;
+    attn_split((t.lk + kT - 1) / kT, a.splits, blockIdx.z, &lo, &hi);
+    for (int kt = lo; kt < hi; ++kt) {
+        const int left = t.lk - kt * kT;  // valid keys of the tile
+        __syncthreads();
+        load_tile<T>(sK, a.k, t.k0 + kt * kT, hk, left, a.d);
+        load_tile<T>(sV, a.v, t.k0 + kt * kT, hk, left, a.d);
+        __syncthreads();
+        float s[4][4];
+        product_nt(sQ, sK, a.d, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float top = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = tx + 16 * j < left ? s[i][j] * a.scale_log2 : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float base = top == -INFINITY ? 0.f : top;  // a row of scores -inf so far
+            const float shrink = exp2f(m[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = exp2f(s[i][j] - base);
+                sum += s[i][j];
+                sP[(ty + 16 * i) * kPP + tx + 16 * j] = s[i][j];
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l[i] = l[i] * shrink + sum;
+            m[i] = top;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[i][c] = times(acc[i][c], shrink);
+        }
+        __syncthreads();
+        product_nn<NC>(sP, sV, a.d, ty, tx, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = t.first + ty + 16 * i;
+        if (r >= t.lq) continue;
+        const int64_t row = t.q0 + r;
+        const float inv = hi > lo ? 1.f / l[i] : 0.f;  // no keys: zero; only keys of weight zero: NaN
+        const float lse = hi > lo ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
+        if (tx == 0) {
+            float* dst = a.splits > 1 ? a.part_lse + (size_t)blockIdx.z * a.hq * a.n_q : a.lse;
+            if (dst) dst[(int64_t)h * a.n_q + row] = lse;
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int col = tx * 4 + 64 * c;
+            if (col >= a.d) continue;
+            const float4 v = times(acc[i][c], inv);
+            if (a.splits > 1)
+                store4<float>(a.part + (((size_t)blockIdx.z * a.n_q + row) * a.hq + h) * a.d + col, v);
+            else
+                store4<T>(head_row<T>(a.o, row, h) + col, v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- query gradient
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
+    extern __shared__ float sm[];
+    const int p = a.d + 4;
+    float *sQ = sm, *sG = sQ + kT * p, *sK = sG + kT * p, *sV = sK + kT * p, *sS = sV + kT * p;
+    if (!attn_offsets_ok(a)) return;
+    const AttnTile t = block_tile(a, a.q_off);
+    if (t.b < 0) return;
+    const int h = blockIdx.y, hk = h / (a.hq / a.hk);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    load_tile<T>(sQ, a.q, t.q0 + t.first, h, t.lq - t.first, a.d);
+    load_tile<T>(sG, a.go, t.q0 + t.first, h, t.lq - t.first, a.d);
+    float2 st[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = t.first + ty + 16 * i;
+        st[i] = r < t.lq ? a.stats[(int64_t)h * a.n_q + t.q0 + r] : make_float2(0.f, 0.f);
+    }
+    float4 acc[4][NC];
+    zero<NC>(acc);
+    int lo, hi;
+    attn_split((t.lk + kT - 1) / kT, a.splits, blockIdx.z, &lo, &hi);
+    for (int kt = lo; kt < hi; ++kt) {
+        const int left = t.lk - kt * kT;
+        __syncthreads();
+        load_tile<T>(sK, a.k, t.k0 + kt * kT, hk, left, a.d);
+        load_tile<T>(sV, a.v, t.k0 + kt * kT, hk, left, a.d);
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        product_nt(sQ, sK, a.d, ty, tx, s);
+        product_nt(sG, sV, a.d, ty, tx, dp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float pr = exp2f(s[i][j] * a.scale_log2 - st[i].x);
+                sS[(ty + 16 * i) * kPP + tx + 16 * j] = tx + 16 * j < left ? pr * (dp[i][j] - st[i].y) : 0.f;
+            }
+        __syncthreads();
+        product_nn<NC>(sS, sK, a.d, ty, tx, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = t.first + ty + 16 * i;
+        if (r >= t.lq) continue;
+        const int64_t row = t.q0 + r;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int col = tx * 4 + 64 * c;
+            if (col >= a.d) continue;
+            const float4 v = times(acc[i][c], a.scale);
+            if (a.splits > 1)
+                store4<float>(a.part + (((size_t)blockIdx.z * a.n_q + row) * a.hq + h) * a.d + col, v);
+            else
+                store4<T>(head_row<T>(a.gq, row, h) + col, v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- key and value gradient
+// The block's 64 keys run along the sample's queries of every head that reads
+// them, in head order: gradients of shared heads are sums in one accumulator.
+template <typename T, int NC>
+__global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* part_dv) {
+    extern __shared__ float sm[];
+    const int p = a.d + 4;
+    float *sQ = sm, *sG = sQ + kT * p, *sK = sG + kT * p, *sV = sK + kT * p;
+    float *sP = sV + kT * p, *sS = sP + kT * kPP;
+    if (!attn_offsets_ok(a)) return;
+    const AttnTile t = block_tile(a, a.k_off);
+    if (t.b < 0) return;
+    const int hk = blockIdx.y, group = a.hq / a.hk;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    load_tile<T>(sK, a.k, t.k0 + t.first, hk, t.lk - t.first, a.d);
+    load_tile<T>(sV, a.v, t.k0 + t.first, hk, t.lk - t.first, a.d);
+    float4 dk[4][NC], dv[4][NC];
+    zero<NC>(dk);
+    zero<NC>(dv);
+    int lo, hi;
+    attn_split((t.lq + kT - 1) / kT, a.splits, blockIdx.z, &lo, &hi);
+    if (t.first >= t.lk) hi = lo;  // no valid key in the tile
+    for (int g = 0; g < group; ++g) {
+        const int h = hk * group + g;
+        for (int qt = lo; qt < hi; ++qt) {
+            const int left = t.lq - qt * kT;
+            __syncthreads();
+            load_tile<T>(sQ, a.q, t.q0 + qt * kT, h, left, a.d);
+            load_tile<T>(sG, a.go, t.q0 + qt * kT, h, left, a.d);
+            __syncthreads();
+            float s[4][4], dp[4][4];
+            product_nt(sK, sQ, a.d, ty, tx, s);
+            product_nt(sV, sG, a.d, ty, tx, dp);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = tx + 16 * j;
+                const float2 st = c < left ? a.stats[(int64_t)h * a.n_q + t.q0 + qt * kT + c] : make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool in = c < left && t.first + ty + 16 * i < t.lk;
+                    const float pr = in ? exp2f(s[i][j] * a.scale_log2 - st.x) : 0.f;
+                    sP[(ty + 16 * i) * kPP + c] = pr;
+                    sS[(ty + 16 * i) * kPP + c] = in ? pr * (dp[i][j] - st.y) : 0.f;
+                }
+            }
+            __syncthreads();
+            product_nn<NC>(sP, sG, a.d, ty, tx, dv);
+            product_nn<NC>(sS, sQ, a.d, ty, tx, dk);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = t.first + ty + 16 * i;
+        if (r >= t.krows) continue;  // rows past the valid keys get zeros
+        const int64_t row = t.k0 + r;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int col = tx * 4 + 64 * c;
+            if (col >= a.d) continue;
+            const float4 vk = times(dk[i][c], a.scale), vv = dv[i][c];
+            if (a.splits > 1) {
+                const size_t at = (((size_t)blockIdx.z * a.n_k + row) * a.hk + hk) * a.d + col;
+                store4<float>(a.part + at, vk);
+                store4<float>(part_dv + at, vv);
+            } else {
+                store4<T>(head_row<T>(a.gk, row, hk) + col, vk);
+                store4<T>(head_row<T>(a.gv, row, hk) + col, vv);
+            }
+        }
+    }
+}
+
+size_t smem_bytes(int d, int tiles, int scores) {
+    return ((size_t)tiles * kT * (d + 4) + (size_t)scores * kT * kPP) * sizeof(float);
+}
+
+template <typename K>
+bool allow_smem(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
+template <typename T, int NC>
+int fwd(const AttnArgs& a, cudaStream_t s) {
+    const size_t smem = smem_bytes(a.d, 3, 1);
+    if (!allow_smem(k_attn_fwd<T, NC>, smem)) return VG_ERR_CUDA;
+    const dim3 grid((unsigned)attn_max_tiles(a.n_q, a.batch, 1, kT), a.hq, a.splits);
+    k_attn_fwd<T, NC><<<grid, kThreads, smem, s>>>(a);
+    return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+}
+template <typename T, int NC>
+int dq(const AttnArgs& a, cudaStream_t s) {
+    const size_t smem = smem_bytes(a.d, 4, 1);
+    if (!allow_smem(k_attn_dq<T, NC>, smem)) return VG_ERR_CUDA;
+    const dim3 grid((unsigned)attn_max_tiles(a.n_q, a.batch, 1, kT), a.hq, a.splits);
+    k_attn_dq<T, NC><<<grid, kThreads, smem, s>>>(a);
+    return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+}
+template <typename T, int NC>
+int dkv(const AttnArgs& a, float* part_dv, cudaStream_t s) {
+    const size_t smem = smem_bytes(a.d, 4, 2);
+    if (!allow_smem(k_attn_dkv<T, NC>, smem)) return VG_ERR_CUDA;
+    const dim3 grid((unsigned)attn_max_tiles(a.n_k, a.batch, 1, kT), a.hk, a.splits);
+    k_attn_dkv<T, NC><<<grid, kThreads, smem, s>>>(a, part_dv);
+    return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+}
+
+}  // namespace
+
+#define VG_ATTN_TYPES(call)                                                                      \
+    (dtype == VG_F32 ? (a.d <= 64 ? call(float, 1) : call(float, 2))                             \
+     : dtype == VG_F16 ? (a.d <= 64 ? call(__half, 1) : call(__half, 2))                         \
+                       : (a.d <= 64 ? call(__nv_bfloat16, 1) : call(__nv_bfloat16, 2)))
+int attn_simt_fwd(const AttnArgs& a, int dtype, cudaStream_t s) {
+#define VG_CALL(T, NC) fwd<T, NC>(a, s)
+    return VG_ATTN_TYPES(VG_CALL);
+#undef VG_CALL
+}
+int attn_simt_dq(const AttnArgs& a, int dtype, cudaStream_t s) {
+#define VG_CALL(T, NC) dq<T, NC>(a, s)
+    return VG_ATTN_TYPES(VG_CALL);
+#undef VG_CALL
+}
+int attn_simt_dkv(const AttnArgs& a, float* part_dv, int dtype, cudaStream_t s) {
+#define VG_CALL(T, NC) dkv<T, NC>(a, part_dv, s)
+    return VG_ATTN_TYPES(VG_CALL);
+#undef VG_CALL
+}
+
+}  // namespace vg

@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "vg.h"
+
 namespace vg {
 
 struct NbrLayout;
@@ -155,5 +157,28 @@ size_t tc_wgrad_sorted_dy_bytes(int64_t n, int Cout);
 int tc_gather_splits(int64_t n, int Ndim, int sms);
 int tc_fwd_launches(int ksplit);  // kernels per forward call on the tensor-core path
 int tc_bwd_launches(int Cout);    // kernels per full backward call on the tensor-core path
+
+// ---- attention-block operators ----
+// One query/key norm and rotation call (pointers as in vg_qk_norm_rope_fwd / _bwd).
+struct QkRope {
+    int64_t n;
+    int heads_q, heads_k, head_dim, dtype;
+    const vg_heads *q, *k, *q_out, *k_out, *grad_q, *grad_k;  // backward: out = dx, grad = dy
+    const void *q_weight, *k_weight;
+    const int32_t* coords;
+    const float* freqs;
+    int axis_pairs[3];
+    double eps;
+    unsigned flags;
+    void *grad_q_weight, *grad_k_weight;
+    float* partial;  // rope_workspace_bytes
+    int sms;
+};
+size_t rope_workspace_bytes(int64_t n, int heads_q, int heads_k, int head_dim, int sms);
+int qk_norm_rope(const QkRope& c, bool bwd, cudaStream_t s);
+
+int adamw_step(const vg_adamw_tensor* ts, int count, int bits, int64_t step, double lr, double beta1, double beta2,
+               double eps, double grad_scale, cudaStream_t s);
+int adamw_decode(const uint8_t* codes, const float* scales, int64_t n, int second, float* out, cudaStream_t s);
 
 }  // namespace vg

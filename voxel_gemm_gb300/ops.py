@@ -28,6 +28,8 @@ VG_CURVE_ZORDER, VG_CURVE_HILBERT = 0, 1
 VG_ALLOW_TF32, VG_NO_SMALL_N_SPLIT = 0x10, 0x20
 VG_NONE = 0xFFFFFFFF
 VG_TILE_ROWS = 128
+VG_ROPE_HALVES, VG_QK_NO_NORM, VG_QK_SHARED_WEIGHT = 0x200, 0x400, 0x800
+VG_ADAMW_BLOCK = 256
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvoxelgemm.so")
 _lock = threading.Lock()
@@ -43,6 +45,27 @@ class SparseMapStruct(ctypes.Structure):
                 ("side_in", ctypes.c_void_p), ("side_out", ctypes.c_void_p), ("down", ctypes.c_void_p),
                 ("down_mask", ctypes.c_void_p), ("up", ctypes.c_void_p), ("up_mask", ctypes.c_void_p),
                 ("coords_out", ctypes.c_void_p)]
+
+
+class HeadsStruct(ctypes.Structure):
+    """Mirror of vg_heads (include/vg.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class AttnStruct(ctypes.Structure):
+    """Mirror of vg_attn (include/vg.h)."""
+    _fields_ = [("n_q", ctypes.c_int64), ("n_k", ctypes.c_int64), ("batch", ctypes.c_int), ("heads_q", ctypes.c_int),
+                ("heads_k", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("scale", ctypes.c_float), ("q_offsets", ctypes.c_void_p), ("k_offsets", ctypes.c_void_p),
+                ("k_lens", ctypes.c_void_p)]
+
+
+class AdamWTensorStruct(ctypes.Structure):
+    """Mirror of vg_adamw_tensor (include/vg.h)."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+                ("dtype", ctypes.c_int)]
 
 
 class VGError(RuntimeError):
@@ -61,6 +84,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is not built; run `python -m voxel_gemm_gb300.build`")
         L = ctypes.CDLL(LIB_PATH)
         P, I, I64, U, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint, ctypes.c_size_t
+        D, H = ctypes.c_double, ctypes.POINTER(HeadsStruct)
         sig = {
             "vg_strerror": ([I], ctypes.c_char_p),
             "vg_version": ([], I),
@@ -87,6 +111,16 @@ def lib():
             "vg_sparse_conv3d_bwd": ([ctypes.POINTER(SparseMapStruct), I, I, P, P, P, P, P, P, I, I, U, P, SZ, P],
                                      I),
             "vg_decode_seq": ([P, I64, I, I, P, P], I),
+            "vg_qk_norm_rope_fwd": ([I64, I, I, I, I, H, H, P, P, P, P, ctypes.POINTER(I), D, U, H, H, P], I),
+            "vg_qk_norm_rope_workspace_bytes": ([I64, I, I, I], SZ),
+            "vg_qk_norm_rope_bwd": ([I64, I, I, I, I, H, H, P, P, P, P, ctypes.POINTER(I), D, U, H, H, H, H, P, P, P,
+                                     SZ, P], I),
+            "vg_cross_attn_workspace_bytes": ([ctypes.POINTER(AttnStruct), I], SZ),
+            "vg_cross_attn_fwd": ([ctypes.POINTER(AttnStruct), H, H, H, H, P, P, SZ, P], I),
+            "vg_cross_attn_bwd": ([ctypes.POINTER(AttnStruct), H, H, H, H, P, H, H, H, H, P, SZ, P], I),
+            "vg_cross_attn_status": ([P, P], I),
+            "vg_adamw_step": ([ctypes.POINTER(AdamWTensorStruct), I, I, I64, D, D, D, D, D, P], I),
+            "vg_adamw_decode": ([P, P, I64, I, P, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -343,3 +377,212 @@ class SparseMap:
                                           Cin, Cout, flags, _p(conv_ws), conv_ws.numel(), _s(stream)),
                "vg_sparse_conv3d_bwd")
 
+
+# ---------------------------------------------------------------- attention-block operators
+def _heads(t, dtype, shape, what):
+    """vg_heads of a [rows, heads, head_dim] tensor (any row and head strides), None for None."""
+    if t is None:
+        return None
+    if t.dim() != 3 or t.dtype != dtype or tuple(t.shape) != shape or (t.stride(2) != 1 and t.numel() > 0):
+        raise ValueError(f"{what}: expected {dtype} {list(shape)} with contiguous elements, got {t.dtype} "
+                         f"{list(t.shape)} of strides {t.stride()}")
+    return HeadsStruct(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def rope_freqs(head_dim: int, axes: int = 3, theta: float = 10000.0, device="cuda"):
+    """(freqs, axis_pairs): theta^(-i / pairs) for each of `axes` axes, head_dim // (2 axes) pairs apiece."""
+    pairs = head_dim // (2 * axes)
+    one = theta ** (-torch.arange(pairs, dtype=torch.float64) / max(pairs, 1))
+    return one.repeat(axes).to(device, torch.float32), tuple(pairs if a < axes else 0 for a in range(3))
+
+
+def _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags):
+    """(N, heads_q, heads_k, head_dim, dtype, pairs) of a call, checked."""
+    x = q if q is not None else k
+    if x is None or x.dim() != 3:
+        raise ValueError("q and k are [rows, heads, head_dim]; one of them may be None")
+    n, d = x.shape[0], x.shape[2]
+    hq, hk = (0 if t is None else t.shape[1] for t in (q, k))
+    if (coords is None) != (freqs is None):
+        raise ValueError("coords and freqs come together")
+    pairs = None
+    if coords is not None:
+        if coords.dtype != torch.int32 or tuple(coords.shape) != (n, 4) or not coords.is_contiguous():
+            raise ValueError("coords must be contiguous int32 [rows, 4]")
+        if freqs.dtype != torch.float32 or not freqs.is_contiguous() or freqs.numel() != sum(axis_pairs):
+            raise ValueError("freqs must be contiguous float32 of sum(axis_pairs) elements")
+        pairs = (ctypes.c_int * 3)(*axis_pairs)
+    for w, h, name in ((q_weight, hq, "q_weight"), (k_weight, hk, "k_weight")):
+        if w is not None:
+            want = (d,) if flags & VG_QK_SHARED_WEIGHT else (h, d)
+            if w.dtype != x.dtype or tuple(w.shape) != want or not w.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {x.dtype} {list(want)}")
+    return n, hq, hk, d, x.dtype, pairs
+
+
+def _rope_flags(q_weight, k_weight, flags):
+    """A one-dimensional weight is shared by the heads."""
+    shared = any(w is not None and w.dim() == 1 for w in (q_weight, k_weight))
+    return flags | (VG_QK_SHARED_WEIGHT if shared else 0)
+
+
+def vg_qk_norm_rope_fwd(q, k, q_weight, k_weight, coords, freqs, axis_pairs, q_out, k_out, eps=1e-6, flags=0,
+                        stream=None) -> None:
+    """Norm of each head's queries and keys ([rows, heads, head_dim]; either may be None) and their rotation by
+    coords [rows, 4]; weights [heads, head_dim], or [head_dim] for all heads, or None for ones."""
+    flags = _rope_flags(q_weight, k_weight, flags)
+    n, hq, hk, d, dt, pairs = _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags)
+    _check(lib().vg_qk_norm_rope_fwd(n, hq, hk, d, _DT.get(dt, -1), _heads(q, dt, (n, hq, d), "q"),
+                                     _heads(k, dt, (n, hk, d), "k"), _p(q_weight), _p(k_weight), _p(coords), _p(freqs),
+                                     pairs, eps, flags, _heads(q_out, dt, (n, hq, d), "q_out"),
+                                     _heads(k_out, dt, (n, hk, d), "k_out"), _s(stream)), "vg_qk_norm_rope_fwd")
+
+
+def vg_qk_norm_rope_bwd(q, k, q_weight, k_weight, coords, freqs, axis_pairs, grad_q_out, grad_k_out, grad_q, grad_k,
+                        grad_q_weight, grad_k_weight, ws, eps=1e-6, flags=0, stream=None) -> None:
+    """Gradients of vg_qk_norm_rope_fwd's inputs and weights (weight gradients None: not wanted; ws then None too)."""
+    flags = _rope_flags(q_weight if q_weight is not None else grad_q_weight,
+                        k_weight if k_weight is not None else grad_k_weight, flags)
+    n, hq, hk, d, dt, pairs = _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags)
+    _rope_shapes(q, k, coords, freqs, axis_pairs, grad_q_weight, grad_k_weight, flags)
+    _check(lib().vg_qk_norm_rope_bwd(n, hq, hk, d, _DT.get(dt, -1), _heads(q, dt, (n, hq, d), "q"),
+                                     _heads(k, dt, (n, hk, d), "k"), _p(q_weight), _p(k_weight), _p(coords), _p(freqs),
+                                     pairs, eps, flags, _heads(grad_q_out, dt, (n, hq, d), "grad_q_out"),
+                                     _heads(grad_k_out, dt, (n, hk, d), "grad_k_out"),
+                                     _heads(grad_q, dt, (n, hq, d), "grad_q"), _heads(grad_k, dt, (n, hk, d), "grad_k"),
+                                     _p(grad_q_weight), _p(grad_k_weight), _p(ws),
+                                     0 if ws is None else ws.numel() * ws.element_size(), _s(stream)),
+           "vg_qk_norm_rope_bwd")
+
+
+def qk_norm_rope_workspace(n, heads_q, heads_k, head_dim, device="cuda") -> torch.Tensor:
+    nb = int(lib().vg_qk_norm_rope_workspace_bytes(n, heads_q, heads_k, head_dim))
+    if nb == 0:
+        raise VGError(VG_ERR_INVALID_ARG, "vg_qk_norm_rope_workspace_bytes")
+    return torch.empty(nb, dtype=torch.uint8, device=device)
+
+
+def cross_attn_workspace(n_q, n_k, batch, heads_q, heads_k, head_dim, dtype, backward=False,
+                         device="cuda") -> torch.Tensor:
+    """Workspace of vg_cross_attn_fwd (and, with backward, of vg_cross_attn_bwd), its error record zero."""
+    a = AttnStruct(n_q, n_k, batch, heads_q, heads_k, head_dim, _DT.get(dtype, -1), 1.0, None, None, None)
+    nb = int(lib().vg_cross_attn_workspace_bytes(ctypes.byref(a), int(backward)))
+    if nb == 0:
+        raise VGError(VG_ERR_INVALID_ARG, "vg_cross_attn_workspace_bytes")
+    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _attn(q, k, q_offsets, k_offsets, k_lens, lse, scale, what):
+    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != k.shape[2]:
+        raise ValueError(f"{what}: q and k are [rows, heads, head_dim] of one head_dim")
+    batch = q_offsets.numel() - 1
+    for t, n, name in ((q_offsets, batch + 1, "q_offsets"), (k_offsets, batch + 1, "k_offsets"),
+                       (k_lens, batch, "k_lens")):
+        if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda):
+            raise ValueError(f"{what}: {name} must be contiguous int32 [{n}] on the GPU")
+    n_q, hq, d = q.shape
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (hq, n_q) or not lse.is_contiguous()):
+        raise ValueError(f"{what}: lse must be contiguous float32 [heads_q, n_q]")
+    return AttnStruct(n_q, k.shape[0], batch, hq, k.shape[1], d, _DT.get(q.dtype, -1),
+                      d ** -0.5 if scale is None else scale, q_offsets.data_ptr(), k_offsets.data_ptr(),
+                      None if k_lens is None else k_lens.data_ptr())
+
+
+def vg_cross_attn_fwd(q, k, v, q_offsets, k_offsets, k_lens, out, lse, ws, scale=None, stream=None) -> None:
+    """out = softmax(scale q k^T) v of each sample's queries over its first k_lens keys (None: all of them).
+
+    q, out [n_q, heads_q, head_dim]; k, v [n_k, heads_k, head_dim] (any row and head strides); offsets int32
+    [batch + 1]; lse float32 [heads_q, n_q] or None; scale head_dim ** -0.5 by default."""
+    a = _attn(q, k, q_offsets, k_offsets, k_lens, lse, scale, "vg_cross_attn_fwd")
+    sq, sk = (a.n_q, a.heads_q, a.head_dim), (a.n_k, a.heads_k, a.head_dim)
+    _check(lib().vg_cross_attn_fwd(a, _heads(q, q.dtype, sq, "q"), _heads(k, q.dtype, sk, "k"),
+                                   _heads(v, q.dtype, sk, "v"), _heads(out, q.dtype, sq, "out"), _p(lse), _p(ws),
+                                   ws.numel() * ws.element_size(), _s(stream)), "vg_cross_attn_fwd")
+
+
+def vg_cross_attn_bwd(q, k, v, q_offsets, k_offsets, k_lens, out, lse, grad_out, grad_q, grad_k, grad_v, ws,
+                      scale=None, stream=None) -> None:
+    """Gradients of vg_cross_attn_fwd's q, k and v, from its out and lse."""
+    a = _attn(q, k, q_offsets, k_offsets, k_lens, lse, scale, "vg_cross_attn_bwd")
+    dt, sq, sk = q.dtype, (a.n_q, a.heads_q, a.head_dim), (a.n_k, a.heads_k, a.head_dim)
+    _check(lib().vg_cross_attn_bwd(a, _heads(q, dt, sq, "q"), _heads(k, dt, sk, "k"), _heads(v, dt, sk, "v"),
+                                   _heads(out, dt, sq, "out"), _p(lse), _heads(grad_out, dt, sq, "grad_out"),
+                                   _heads(grad_q, dt, sq, "grad_q"), _heads(grad_k, dt, sk, "grad_k"),
+                                   _heads(grad_v, dt, sk, "grad_v"), _p(ws), ws.numel() * ws.element_size(),
+                                   _s(stream)), "vg_cross_attn_bwd")
+
+
+def vg_cross_attn_status(ws, stream=None) -> int:
+    return lib().vg_cross_attn_status(_p(ws), _s(stream))
+
+
+class AdamWState:
+    """Moments of many parameters and the table that vg_adamw_step takes.
+
+    params and grads are lists of contiguous tensors of one dtype each (written and read at every step, so they
+    stay where they are); masters, a list of fp32 tensors or None; weight_decay, a number or a list.  The moments
+    lie in two arenas m and v, each tensor's at the next multiple of 256 elements (`offsets`), as fp32 or, with
+    bits = 8, as uint8 codes beside m_scale and v_scale.  Arenas that are not given start at zero."""
+
+    def __init__(self, params, grads, masters=None, bits=32, weight_decay=0.0, m=None, v=None, m_scale=None,
+                 v_scale=None):
+        if len(params) != len(grads) or (masters is not None and len(masters) != len(params)):
+            raise ValueError("AdamWState: params, grads and masters must be as many")
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * len(params)
+        if len(decay) != len(params):
+            raise ValueError("AdamWState: weight_decay must be a number or one per parameter")
+        if bits not in (8, 32):
+            raise VGError(VG_ERR_UNSUPPORTED, "AdamWState")
+        self.bits, self.offsets, total = bits, [], 0
+        for p, g in zip(params, grads):
+            if p.dtype not in _DT or g.dtype != p.dtype or g.shape != p.shape or not p.is_contiguous() \
+                    or not g.is_contiguous() or not p.is_cuda or g.device != p.device:
+                raise ValueError("AdamWState: params and grads must be contiguous CUDA tensors of one shape and dtype")
+            self.offsets.append(total)
+            total += -(-p.numel() // VG_ADAMW_BLOCK) * VG_ADAMW_BLOCK
+        for p, x in zip(params, masters or []):
+            if x.dtype != torch.float32 or x.shape != p.shape or not x.is_contiguous() or x.device != p.device:
+                raise ValueError("AdamWState: masters must be contiguous float32 of their parameter's shape")
+        device = params[0].device if params else "cuda"
+        code, blocks = torch.uint8 if bits == 8 else torch.float32, total // VG_ADAMW_BLOCK
+
+        def arena(t, n, dtype):
+            if t is None:
+                return torch.zeros(n, dtype=dtype, device=device)
+            if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or t.device != torch.device(device):
+                raise ValueError(f"AdamWState: an arena must be contiguous {dtype} of {n} elements")
+            return t
+        self.m, self.v = arena(m, total, code), arena(v, total, code)
+        self.m_scale = arena(m_scale, blocks, torch.float32) if bits == 8 else None
+        self.v_scale = arena(v_scale, blocks, torch.float32) if bits == 8 else None
+        self._keep = (list(params), list(grads), None if masters is None else list(masters))
+        size = 1 if bits == 8 else 4
+
+        def at(t, n):
+            return None if t is None else t.data_ptr() + n
+        self.table = (AdamWTensorStruct * len(params))()
+        for i, (p, g, o) in enumerate(zip(params, grads, self.offsets)):
+            s = o // VG_ADAMW_BLOCK * 4
+            self.table[i] = AdamWTensorStruct(p.data_ptr(), g.data_ptr(),
+                                              None if masters is None else masters[i].data_ptr(),
+                                              at(self.m, size * o), at(self.v, size * o), at(self.m_scale, s),
+                                              at(self.v_scale, s), p.numel(), decay[i], _DT[p.dtype])
+
+
+def vg_adamw_step(state: AdamWState, step: int, lr: float, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=1.0,
+                  stream=None) -> None:
+    """One AdamW step (counted from 1) over all of the state's parameters, in place."""
+    _check(lib().vg_adamw_step(state.table, len(state.table), state.bits, step, lr, beta1, beta2, eps, grad_scale,
+                               _s(stream)), "vg_adamw_step")
+
+
+def vg_adamw_decode(codes, scales, out, second: bool, stream=None) -> None:
+    """out[i] = the value of 8-bit moment code i (second: of v, else of m); one scale per 256 codes."""
+    n = codes.numel()
+    if codes.dtype != torch.uint8 or scales.dtype != torch.float32 or out.dtype != torch.float32 \
+            or out.numel() != n or scales.numel() < -(-n // VG_ADAMW_BLOCK) \
+            or not (codes.is_contiguous() and scales.is_contiguous() and out.is_contiguous()):
+        raise ValueError("vg_adamw_decode: codes uint8 [n], scales float32 [ceil(n / 256)], out float32 [n]")
+    _check(lib().vg_adamw_decode(_p(codes), _p(scales), n, int(second), _p(out), _s(stream)), "vg_adamw_decode")
