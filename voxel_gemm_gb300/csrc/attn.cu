@@ -149,12 +149,11 @@ int join_sum(const AttnArgs& a, const float* part, int splits, int64_t rows, int
      : dtype == VG_F16 ? f<__half>(__VA_ARGS__) : f<__nv_bfloat16>(__VA_ARGS__))
 
 // Parts to cut an axis of `tiles` tiles into, when there are `units` independent
-// tiles of work along the other one: enough that every SM has two blocks, but at
-// least four tiles in a part.
-int parts(int64_t units, int64_t tiles, int sms) {
+// tiles of work along the other one and `slots` of them run at a time: as many as
+// fill the slots once, but at least four tiles in a part.
+int parts(int64_t units, int64_t tiles, int slots) {
     if (units <= 0) return 1;
-    const int64_t want = (2 * (int64_t)sms + units - 1) / units;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles / 4, 256}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({slots / units, tiles / 4, 256}));
 }
 
 }  // namespace
@@ -166,11 +165,19 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
     if (c.d % 8 || c.d > 128 || c.hq > 65535) return VG_ERR_UNSUPPORTED;
     AttnPlan p;
     p.sms = plan_sms(0);
-    p.gp = 1;
+    p.tc = c.dtype != VG_F32;
+    const int group = c.hq / c.hk;
+    if (p.tc && group <= 16 && !(group & (group - 1)) && c.n_q * group < (int64_t(1) << 31)) p.gp = group;
     const int64_t qt = attn_max_tiles(c.n_q, c.batch, 1, 64), kt = attn_max_tiles(c.n_k, c.batch, 1, 64);
-    p.s_fwd = parts(qt * c.hq, kt / c.batch, p.sms);
-    p.s_dq = p.s_fwd;
-    p.s_dkv = parts(kt * c.hk, qt / c.batch, p.sms);
+    p.s_dq = parts(qt * c.hq, kt / c.batch, 2 * p.sms);
+    p.s_dkv = parts(kt * c.hk, qt / c.batch, 2 * p.sms);
+    p.s_fwd = p.s_dq;
+    if (p.tc) {
+        const int sets = c.hq / p.gp;
+        p.nq = attn_max_tiles(c.n_q, c.batch, p.gp, 256) * sets >= p.sms ? 2 : 1;
+        p.s_fwd = parts(attn_max_tiles(c.n_q, c.batch, p.gp, 128 * p.nq) * sets, c.n_k / c.batch / 128,
+                        p.nq == 1 ? 2 * p.sms : p.sms);
+    }
     const size_t vq = (size_t)c.n_q * c.hq, vk = (size_t)c.n_k * c.hk;
     size_t fwd = 0, bwd = 0;
     if (p.s_fwd > 1) {
@@ -200,13 +207,13 @@ int attn_fwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
     a.splits = p.s_fwd;
     a.part = reinterpret_cast<float*>(ws + 256);
     a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
-    const int st = attn_simt_fwd(a, dtype, s);
+    const int st = p.tc ? attn_tc_fwd(a, dtype, p.nq, p.sms, s) : attn_simt_fwd(a, dtype, s);
     if (st != VG_OK || a.splits == 1) return st;
     return VG_BY_TYPE(join_out, a, s);
 }
 
 int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s) {
-    a.gp = p.gp;
+    a.gp = 1;
     a.err = reinterpret_cast<uint32_t*>(ws);
     a.stats = reinterpret_cast<float2*>(ws + 256);
     int st;

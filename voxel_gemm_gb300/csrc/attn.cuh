@@ -108,7 +108,10 @@ struct AttnShape {
     bool backward;
 };
 struct AttnPlan {
-    int sms = 0, gp = 1;
+    int sms = 0;
+    int tc = 0;                          // 16-bit types: tensor cores
+    int gp = 1;                          // query heads packed into rows
+    int nq = 1;                          // row tiles of a forward block
     int s_fwd = 1, s_dq = 1, s_dkv = 1;  // parts of the key axis (forward, dQ) and of the query axis (dK, dV)
     size_t off_lse = 0, off_dq = 0, off_dk = 0, off_dv = 0, total = 0;
 };
@@ -132,5 +135,8 @@ __device__ __forceinline__ T* head_row(const vg_heads& h, int64_t row, int head)
 int attn_simt_fwd(const AttnArgs& a, int dtype, cudaStream_t s);
 int attn_simt_dq(const AttnArgs& a, int dtype, cudaStream_t s);
 int attn_simt_dkv(const AttnArgs& a, float* part_dv, int dtype, cudaStream_t s);
+
+// ---- 16-bit path (attn_tc_fwd.cu) ----
+int attn_tc_fwd(const AttnArgs& a, int dtype, int nq, int sms, cudaStream_t s);
 
 }  // namespace vg

@@ -1,0 +1,105 @@
+// Cross attention on the tensor cores: what the 16-bit forward and backward kernels
+// share.
+//
+// Every operand tile is a box of a [rows][heads][d] tensor, copied by the TMA engine
+// into rows of 128 bytes (64 channels) in the 128-byte swizzle; d > 64 takes two such
+// blocks.  Channels past d and rows past the tensor read as zero.  The same tile
+// serves as a K-major operand (contraction over channels) and as an MN-major one
+// (contraction over rows), so nothing is transposed.  Boxes of query rows hold gp
+// heads of 128/gp queries: the packed rows of attn.cuh, in order.
+#pragma once
+#include <cuda.h>
+
+#include "attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace vg {
+
+struct AttnMaps {
+    CUtensorMap q, k, v, go;
+};
+
+// Tensor map over a [rows][heads][d] operand with boxes of 64 channels x `box_heads`
+// heads x `box_rows` rows.  VG_OK, VG_ERR_UNSUPPORTED (strides beyond what the engine
+// takes) or VG_ERR_CUDA.
+int attn_make_map(CUtensorMap* map, const vg_heads& h, int64_t rows, int heads, int d, int dtype, int box_heads,
+                  int box_rows);
+
+namespace attn_tc {
+
+using namespace ptx;
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Zero rows [from, to) of a tile of `blocks` 64-channel blocks, `block_bytes` apart, by one warp.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to, int blocks, int block_bytes) {
+    const int per = (to - from) * 8;  // 16-byte pieces of a block
+    for (int e = threadIdx.x & 31; e < per * blocks; e += 32) {
+        const int b = e / per, i = e - b * per;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + b * block_bytes + from * 128 + i * 16),
+                     "r"(0)
+                     : "memory");
+    }
+}
+
+// Write 32 fp32 columns of a row as 16-bit values; `n` of them exist (a multiple of 8).
+template <bool BF16>
+__device__ __forceinline__ void store_cols32(void* dst, const uint32_t (&acc)[32], float mul, int n) {
+    uint4* d4 = static_cast<uint4*>(dst);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (8 * i >= n) break;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t* two = acc + 8 * i + 2 * j;
+            w[j] = pack2<BF16>(__uint_as_float(two[0]) * mul, __uint_as_float(two[1]) * mul);
+        }
+        d4[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void store_cols32_f32(float* dst, const uint32_t (&acc)[32], float mul, int n) {
+    float4* d4 = reinterpret_cast<float4*>(dst);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (4 * i >= n) break;
+        d4[i] = make_float4(__uint_as_float(acc[4 * i]) * mul, __uint_as_float(acc[4 * i + 1]) * mul,
+                            __uint_as_float(acc[4 * i + 2]) * mul, __uint_as_float(acc[4 * i + 3]) * mul);
+    }
+}
+
+// One bounded wait of a role; a wait that gives up raises the block's abort flag.
+struct Waiter {
+    volatile uint32_t* abort;
+    bool ok = true;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, abort)) {
+            ok = false;
+            *abort = 1;
+        }
+        return ok;
+    }
+    // The whole warp goes on or gives up together.
+    __device__ __forceinline__ bool agree() {
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+    }
+};
+
+}  // namespace attn_tc
+
+}  // namespace vg
