@@ -1,6 +1,8 @@
 // Cross attention: the plan of a call (how rows are packed, how long axes are cut,
 // where the scratch lies), the row sums that the backward pass starts from, and the
 // joins of split work.
+#include <type_traits>
+
 #include "attn.cuh"
 
 namespace vg {
@@ -24,32 +26,85 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
     }
 }
 
+// Whether key row j is one of its sample's valid rows.
+__device__ __forceinline__ bool valid_key(const AttnArgs& a, int64_t j) {
+    if (!a.k_len) return true;
+    int lo = 0, hi = a.batch;  // the last sample that does not start past j
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.k_off[mid] <= j) lo = mid;
+        else hi = mid;
+    }
+    return j - a.k_off[lo] < a.k_len[lo];
+}
+
+// Largest value of the block into *word, as the bits of a non-negative float (their
+// order is the floats' own, so the result does not depend on the order of arrival).
+__device__ __forceinline__ void block_max(float x, uint32_t* word) {
+    __shared__ uint32_t s[kThreads / 32];
+    const uint32_t v = __reduce_max_sync(0xffffffffu, __float_as_uint(x));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t m = 0;
+        for (int i = 0; i < kThreads / 32; ++i) m = max(m, s[i]);
+        atomicMax(word, m);
+    }
+}
+
 // stats[packed row] = (lse * log2 e, sum_d dO O): a group of 1..16 lanes per row,
-// 16-byte loads; reads O and dO once, bound by memory.
+// 16-byte loads; reads O and dO once, bound by memory.  fp16: also the largest norms
+// of a row of dO and of a valid row of V, which bound dP.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int lanes) {
     const int lane = threadIdx.x & (lanes - 1);
     const int64_t rows = a.n_q * a.hq;
     const int64_t step = (int64_t)gridDim.x * (kThreads / lanes);
-    const int64_t first = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
-    for (int64_t r0 = first - threadIdx.x / lanes; r0 < rows; r0 += step) {  // the same trips for the whole block
+    const int64_t first = (int64_t)blockIdx.x * (kThreads / lanes);
+    constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+    float big = 0.f;
+    for (int64_t r0 = first; r0 < rows; r0 += step) {  // the same trips for the whole block
         const int64_t r = r0 + threadIdx.x / lanes;
         const int64_t i = r / a.hq;
         const int h = (int)(r - i * a.hq);
-        float sum = 0.f;
+        float sum = 0.f, sq = 0.f;
         if (r < rows && lane * 8 < a.d) {
             float o[8], g[8];
             load8<T>(head_row<const T>(a.o, i, h) + lane * 8, o);
             load8<T>(head_row<const T>(a.go, i, h) + lane * 8, g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(o[j], g[j], sum);
+            for (int j = 0; j < 8; ++j) sum = fmaf(o[j], g[j], sum), sq = fmaf(g[j], g[j], sq);
         }
         for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if constexpr (kHalf) {
+            for (int o = 1; o < lanes; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            big = fmaxf(big, sq);
+        }
         if (r < rows && lane == 0) {
             const int hs = h / a.gp;
             a.stats[((int64_t)hs * a.n_q + i) * a.gp + (h - hs * a.gp)] =
                 make_float2(a.lse[(int64_t)h * a.n_q + i] * 1.4426950408889634f, sum);
         }
+    }
+    if constexpr (kHalf) {
+        block_max(sqrtf(big), a.err + 1);
+        big = 0.f;
+        const int64_t krows = a.n_k * a.hk;
+        for (int64_t r0 = first; r0 < krows; r0 += step) {
+            const int64_t r = r0 + threadIdx.x / lanes;
+            const int64_t j = r / a.hk;
+            float sq = 0.f;
+            if (r < krows && lane * 8 < a.d && valid_key(a, j)) {
+                float v[8];
+                load8<T>(head_row<const T>(a.v, j, (int)(r - j * a.hk)) + lane * 8, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sq = fmaf(v[i], v[i], sq);
+            }
+            for (int o = 1; o < lanes; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            big = fmaxf(big, sq);
+        }
+        block_max(sqrtf(big), a.err + 2);
     }
 }
 
@@ -156,6 +211,22 @@ int parts(int64_t units, int64_t tiles, int slots) {
     return (int)std::max<int64_t>(1, std::min<int64_t>({slots / units, tiles / 4, 256}));
 }
 
+// The same for units that may already fill the slots: cut on, up to eight parts, while
+// that evens out the last wave (a wave's idle slots cost more than the parts' fp32 sums).
+int balanced(int64_t units, int64_t tiles, int slots) {
+    const int first = parts(units, tiles, slots);
+    if (units <= 0) return 1;
+    int best = first;
+    double best_fill = 0.0;
+    for (int s = first; s <= std::max(first, 8) && (s == first || tiles / s >= 4); ++s) {
+        const int64_t n = units * s, waves = (n + slots - 1) / slots;
+        const double fill = (double)n / (double)(waves * slots);
+        if (fill > best_fill + 0.03) best = s, best_fill = fill;
+        if (best_fill > 0.93) break;
+    }
+    return best;
+}
+
 }  // namespace
 
 int attn_plan(const AttnShape& c, AttnPlan* P) {
@@ -175,8 +246,10 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
     if (p.tc) {
         const int sets = c.hq / p.gp;
         p.nq = attn_max_tiles(c.n_q, c.batch, p.gp, 256) * sets >= p.sms ? 2 : 1;
-        p.s_fwd = parts(attn_max_tiles(c.n_q, c.batch, p.gp, 128 * p.nq) * sets, c.n_k / c.batch / 128,
-                        p.nq == 1 ? 2 * p.sms : p.sms);
+        const int64_t units = attn_max_tiles(c.n_q, c.batch, p.gp, 128 * p.nq) * sets;
+        p.s_fwd = parts(units, c.n_k / c.batch / 128, p.nq == 1 ? 2 * p.sms : p.sms);
+        p.s_dq = parts(units, c.n_k / c.batch / 64, p.nq == 1 && c.d <= 64 ? 2 * p.sms : p.sms);
+        p.s_dkv = balanced(attn_max_tiles(c.n_k, c.batch, 1, 128) * c.hk, c.n_q * p.gp / c.batch / 64, p.sms);
     }
     const size_t vq = (size_t)c.n_q * c.hq, vk = (size_t)c.n_k * c.hk;
     size_t fwd = 0, bwd = 0;
@@ -207,28 +280,31 @@ int attn_fwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
     a.splits = p.s_fwd;
     a.part = reinterpret_cast<float*>(ws + 256);
     a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
-    const int st = p.tc ? attn_tc_fwd(a, dtype, p.nq, p.sms, s) : attn_simt_fwd(a, dtype, s);
+    const int st = p.tc ? attn_tc_fwd(a, dtype, p.nq, p.sms, s) : attn_simt_fwd(a, s);
     if (st != VG_OK || a.splits == 1) return st;
     return VG_BY_TYPE(join_out, a, s);
 }
 
 int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s) {
-    a.gp = 1;
+    a.gp = p.gp;
     a.err = reinterpret_cast<uint32_t*>(ws);
     a.stats = reinterpret_cast<float2*>(ws + 256);
     int st;
+    if (dtype == VG_F16) cudaMemsetAsync(a.err + 1, 0, 8, s);  // the largest norms, taken by the statistics kernel
     if (a.n_q > 0) {
         if ((st = VG_BY_TYPE(stats, a, s)) != VG_OK) return st;
         a.splits = p.s_dq;
         a.part = reinterpret_cast<float*>(ws + p.off_dq);
-        if ((st = attn_simt_dq(a, dtype, s)) != VG_OK) return st;
+        st = p.tc ? attn_tc_dq(a, dtype, p.nq, p.sms, s) : attn_simt_dq(a, s);
+        if (st != VG_OK) return st;
         if (a.splits > 1 && (st = VG_BY_TYPE(join_sum, a, a.part, a.splits, a.n_q, a.hq, a.gq, s)) != VG_OK) return st;
     }
     if (a.n_k > 0) {
         a.splits = p.s_dkv;
         a.part = reinterpret_cast<float*>(ws + p.off_dk);
         float* part_dv = reinterpret_cast<float*>(ws + p.off_dv);
-        if ((st = attn_simt_dkv(a, part_dv, dtype, s)) != VG_OK) return st;
+        st = p.tc ? attn_tc_dkv(a, part_dv, dtype, p.sms, s) : attn_simt_dkv(a, part_dv, s);
+        if (st != VG_OK) return st;
         if (a.splits > 1) {
             if ((st = VG_BY_TYPE(join_sum, a, a.part, a.splits, a.n_k, a.hk, a.gk, s)) != VG_OK) return st;
             if ((st = VG_BY_TYPE(join_sum, a, part_dv, a.splits, a.n_k, a.hk, a.gv, s)) != VG_OK) return st;

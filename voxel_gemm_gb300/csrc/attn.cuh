@@ -28,7 +28,7 @@ struct AttnArgs {
     vg_heads q, k, v, o, go, gq, gk, gv;
     float* lse;                  // [hq][n_q]
     // workspace
-    uint32_t* err;               // error record; words 1, 2: bits of the largest |dO row|, |V row| (fp16)
+    uint32_t* err;               // error record; words 1, 2: fp32 bits of the largest |dO row|, |V row| (fp16)
     float2* stats;               // [hq / gp][n_q * gp]: (lse * log2 e, sum_d dO O) of every packed row
     int splits;                  // parts of the axis that the kernel runs along
     float* part;                 // split partial results (layouts at their kernels)
@@ -132,11 +132,13 @@ __device__ __forceinline__ T* head_row(const vg_heads& h, int64_t row, int head)
 }
 
 // ---- fp32 path (attn_simt.cu) ----
-int attn_simt_fwd(const AttnArgs& a, int dtype, cudaStream_t s);
-int attn_simt_dq(const AttnArgs& a, int dtype, cudaStream_t s);
-int attn_simt_dkv(const AttnArgs& a, float* part_dv, int dtype, cudaStream_t s);
+int attn_simt_fwd(const AttnArgs& a, cudaStream_t s);
+int attn_simt_dq(const AttnArgs& a, cudaStream_t s);
+int attn_simt_dkv(const AttnArgs& a, float* part_dv, cudaStream_t s);
 
-// ---- 16-bit path (attn_tc_fwd.cu) ----
+// ---- 16-bit path (attn_tc_fwd.cu, attn_tc_bwd.cu); nq: row tiles of a block ----
 int attn_tc_fwd(const AttnArgs& a, int dtype, int nq, int sms, cudaStream_t s);
+int attn_tc_dq(const AttnArgs& a, int dtype, int nq, int sms, cudaStream_t s);
+int attn_tc_dkv(const AttnArgs& a, float* part_dv, int dtype, int sms, cudaStream_t s);
 
 }  // namespace vg

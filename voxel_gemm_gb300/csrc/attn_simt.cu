@@ -23,36 +23,13 @@ constexpr int kThreads = 256;
 constexpr int kPP = kT + 4;        // pitch of a score tile
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p) {
-    if constexpr (sizeof(T) == 4) {
-        return *reinterpret_cast<const float4*>(p);
-    } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        const T* e = reinterpret_cast<const T*>(&u);
-        return make_float4(to_f32<T>(e[0]), to_f32<T>(e[1]), to_f32<T>(e[2]), to_f32<T>(e[3]));
-    }
-}
-template <typename T>
-__device__ __forceinline__ void store4(T* p, float4 v) {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(p) = v;
-    } else {
-        uint2 u;
-        T* e = reinterpret_cast<T*>(&u);
-        e[0] = from_f32<T>(v.x); e[1] = from_f32<T>(v.y); e[2] = from_f32<T>(v.z); e[3] = from_f32<T>(v.w);
-        *reinterpret_cast<uint2*>(p) = u;
-    }
-}
-
 // 64 rows from `row` on of one head into shared memory; rows from `rows` on are zero.
-template <typename T>
 __device__ __forceinline__ void load_tile(float* dst, const vg_heads& h, int64_t row, int head, int rows, int d) {
     const int q4 = d / 4;
     for (int e = threadIdx.x; e < kT * q4; e += kThreads) {
         const int r = e / q4, c = (e - r * q4) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) v = load4<T>(head_row<const T>(h, row + r, head) + c);
+        if (r < rows) v = *reinterpret_cast<const float4*>(head_row<const float>(h, row + r, head) + c);
         *reinterpret_cast<float4*>(dst + r * (d + 4) + c) = v;
     }
 }
@@ -123,6 +100,7 @@ __device__ __forceinline__ void zero(float4 (&acc)[4][NC]) {
         for (int c = 0; c < NC; ++c) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
+__device__ __forceinline__ void put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ float4 times(float4 v, float s) { return make_float4(v.x * s, v.y * s, v.z * s, v.w * s); }
 
 __device__ __forceinline__ AttnTile block_tile(const AttnArgs& a, const int32_t* off) {
@@ -130,7 +108,7 @@ __device__ __forceinline__ AttnTile block_tile(const AttnArgs& a, const int32_t*
 }
 
 // ---------------------------------------------------------------- forward
-template <typename T, int NC>
+template <int NC>
 __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
     extern __shared__ float sm[];
     const int p = a.d + 4;
@@ -140,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
     if (t.b < 0) return;
     const int h = blockIdx.y, hk = h / (a.hq / a.hk);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_tile<T>(sQ, a.q, t.q0 + t.first, h, t.lq - t.first, a.d);
+    load_tile(sQ, a.q, t.q0 + t.first, h, t.lq - t.first, a.d);
     float m[4], l[4];
     float4 acc[4][NC];
 #pragma unroll
@@ -151,8 +129,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
     for (int kt = lo; kt < hi; ++kt) {
         const int left = t.lk - kt * kT;  // valid keys of the tile
         __syncthreads();
-        load_tile<T>(sK, a.k, t.k0 + kt * kT, hk, left, a.d);
-        load_tile<T>(sV, a.v, t.k0 + kt * kT, hk, left, a.d);
+        load_tile(sK, a.k, t.k0 + kt * kT, hk, left, a.d);
+        load_tile(sV, a.v, t.k0 + kt * kT, hk, left, a.d);
         __syncthreads();
         float s[4][4];
         product_nt(sQ, sK, a.d, ty, tx, s);
@@ -202,15 +180,15 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
             if (col >= a.d) continue;
             const float4 v = times(acc[i][c], inv);
             if (a.splits > 1)
-                store4<float>(a.part + (((size_t)blockIdx.z * a.n_q + row) * a.hq + h) * a.d + col, v);
+                put4(a.part + (((size_t)blockIdx.z * a.n_q + row) * a.hq + h) * a.d + col, v);
             else
-                store4<T>(head_row<T>(a.o, row, h) + col, v);
+                put4(head_row<float>(a.o, row, h) + col, v);
         }
     }
 }
 
 // ---------------------------------------------------------------- query gradient
-template <typename T, int NC>
+template <int NC>
 __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
     extern __shared__ float sm[];
     const int p = a.d + 4;
@@ -220,8 +198,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
     if (t.b < 0) return;
     const int h = blockIdx.y, hk = h / (a.hq / a.hk);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_tile<T>(sQ, a.q, t.q0 + t.first, h, t.lq - t.first, a.d);
-    load_tile<T>(sG, a.go, t.q0 + t.first, h, t.lq - t.first, a.d);
+    load_tile(sQ, a.q, t.q0 + t.first, h, t.lq - t.first, a.d);
+    load_tile(sG, a.go, t.q0 + t.first, h, t.lq - t.first, a.d);
     float2 st[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -235,8 +213,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
     for (int kt = lo; kt < hi; ++kt) {
         const int left = t.lk - kt * kT;
         __syncthreads();
-        load_tile<T>(sK, a.k, t.k0 + kt * kT, hk, left, a.d);
-        load_tile<T>(sV, a.v, t.k0 + kt * kT, hk, left, a.d);
+        load_tile(sK, a.k, t.k0 + kt * kT, hk, left, a.d);
+        load_tile(sV, a.v, t.k0 + kt * kT, hk, left, a.d);
         __syncthreads();
         float s[4][4], dp[4][4];
         product_nt(sQ, sK, a.d, ty, tx, s);
@@ -262,9 +240,9 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
             if (col >= a.d) continue;
             const float4 v = times(acc[i][c], a.scale);
             if (a.splits > 1)
-                store4<float>(a.part + (((size_t)blockIdx.z * a.n_q + row) * a.hq + h) * a.d + col, v);
+                put4(a.part + (((size_t)blockIdx.z * a.n_q + row) * a.hq + h) * a.d + col, v);
             else
-                store4<T>(head_row<T>(a.gq, row, h) + col, v);
+                put4(head_row<float>(a.gq, row, h) + col, v);
         }
     }
 }
@@ -272,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
 // ---------------------------------------------------------------- key and value gradient
 // The block's 64 keys run along the sample's queries of every head that reads
 // them, in head order: gradients of shared heads are sums in one accumulator.
-template <typename T, int NC>
+template <int NC>
 __global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* part_dv) {
     extern __shared__ float sm[];
     const int p = a.d + 4;
@@ -283,8 +261,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* 
     if (t.b < 0) return;
     const int hk = blockIdx.y, group = a.hq / a.hk;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_tile<T>(sK, a.k, t.k0 + t.first, hk, t.lk - t.first, a.d);
-    load_tile<T>(sV, a.v, t.k0 + t.first, hk, t.lk - t.first, a.d);
+    load_tile(sK, a.k, t.k0 + t.first, hk, t.lk - t.first, a.d);
+    load_tile(sV, a.v, t.k0 + t.first, hk, t.lk - t.first, a.d);
     float4 dk[4][NC], dv[4][NC];
     zero<NC>(dk);
     zero<NC>(dv);
@@ -296,8 +274,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* 
         for (int qt = lo; qt < hi; ++qt) {
             const int left = t.lq - qt * kT;
             __syncthreads();
-            load_tile<T>(sQ, a.q, t.q0 + qt * kT, h, left, a.d);
-            load_tile<T>(sG, a.go, t.q0 + qt * kT, h, left, a.d);
+            load_tile(sQ, a.q, t.q0 + qt * kT, h, left, a.d);
+            load_tile(sG, a.go, t.q0 + qt * kT, h, left, a.d);
             __syncthreads();
             float s[4][4], dp[4][4];
             product_nt(sK, sQ, a.d, ty, tx, s);
@@ -331,11 +309,11 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* 
             const float4 vk = times(dk[i][c], a.scale), vv = dv[i][c];
             if (a.splits > 1) {
                 const size_t at = (((size_t)blockIdx.z * a.n_k + row) * a.hk + hk) * a.d + col;
-                store4<float>(a.part + at, vk);
-                store4<float>(part_dv + at, vv);
+                put4(a.part + at, vk);
+                put4(part_dv + at, vv);
             } else {
-                store4<T>(head_row<T>(a.gk, row, hk) + col, vk);
-                store4<T>(head_row<T>(a.gv, row, hk) + col, vv);
+                put4(head_row<float>(a.gk, row, hk) + col, vk);
+                put4(head_row<float>(a.gv, row, hk) + col, vv);
             }
         }
     }
@@ -350,51 +328,37 @@ bool allow_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
-template <typename T, int NC>
+template <int NC>
 int fwd(const AttnArgs& a, cudaStream_t s) {
     const size_t smem = smem_bytes(a.d, 3, 1);
-    if (!allow_smem(k_attn_fwd<T, NC>, smem)) return VG_ERR_CUDA;
+    if (!allow_smem(k_attn_fwd<NC>, smem)) return VG_ERR_CUDA;
     const dim3 grid((unsigned)attn_max_tiles(a.n_q, a.batch, 1, kT), a.hq, a.splits);
-    k_attn_fwd<T, NC><<<grid, kThreads, smem, s>>>(a);
+    k_attn_fwd<NC><<<grid, kThreads, smem, s>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
-template <typename T, int NC>
+template <int NC>
 int dq(const AttnArgs& a, cudaStream_t s) {
     const size_t smem = smem_bytes(a.d, 4, 1);
-    if (!allow_smem(k_attn_dq<T, NC>, smem)) return VG_ERR_CUDA;
+    if (!allow_smem(k_attn_dq<NC>, smem)) return VG_ERR_CUDA;
     const dim3 grid((unsigned)attn_max_tiles(a.n_q, a.batch, 1, kT), a.hq, a.splits);
-    k_attn_dq<T, NC><<<grid, kThreads, smem, s>>>(a);
+    k_attn_dq<NC><<<grid, kThreads, smem, s>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
-template <typename T, int NC>
+template <int NC>
 int dkv(const AttnArgs& a, float* part_dv, cudaStream_t s) {
     const size_t smem = smem_bytes(a.d, 4, 2);
-    if (!allow_smem(k_attn_dkv<T, NC>, smem)) return VG_ERR_CUDA;
+    if (!allow_smem(k_attn_dkv<NC>, smem)) return VG_ERR_CUDA;
     const dim3 grid((unsigned)attn_max_tiles(a.n_k, a.batch, 1, kT), a.hk, a.splits);
-    k_attn_dkv<T, NC><<<grid, kThreads, smem, s>>>(a, part_dv);
+    k_attn_dkv<NC><<<grid, kThreads, smem, s>>>(a, part_dv);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 
 }  // namespace
 
-#define VG_ATTN_TYPES(call)                                                                      \
-    (dtype == VG_F32 ? (a.d <= 64 ? call(float, 1) : call(float, 2))                             \
-     : dtype == VG_F16 ? (a.d <= 64 ? call(__half, 1) : call(__half, 2))                         \
-                       : (a.d <= 64 ? call(__nv_bfloat16, 1) : call(__nv_bfloat16, 2)))
-int attn_simt_fwd(const AttnArgs& a, int dtype, cudaStream_t s) {
-#define VG_CALL(T, NC) fwd<T, NC>(a, s)
-    return VG_ATTN_TYPES(VG_CALL);
-#undef VG_CALL
-}
-int attn_simt_dq(const AttnArgs& a, int dtype, cudaStream_t s) {
-#define VG_CALL(T, NC) dq<T, NC>(a, s)
-    return VG_ATTN_TYPES(VG_CALL);
-#undef VG_CALL
-}
-int attn_simt_dkv(const AttnArgs& a, float* part_dv, int dtype, cudaStream_t s) {
-#define VG_CALL(T, NC) dkv<T, NC>(a, part_dv, s)
-    return VG_ATTN_TYPES(VG_CALL);
-#undef VG_CALL
+int attn_simt_fwd(const AttnArgs& a, cudaStream_t s) { return a.d <= 64 ? fwd<1>(a, s) : fwd<2>(a, s); }
+int attn_simt_dq(const AttnArgs& a, cudaStream_t s) { return a.d <= 64 ? dq<1>(a, s) : dq<2>(a, s); }
+int attn_simt_dkv(const AttnArgs& a, float* part_dv, cudaStream_t s) {
+    return a.d <= 64 ? dkv<1>(a, part_dv, s) : dkv<2>(a, part_dv, s);
 }
 
 }  // namespace vg
