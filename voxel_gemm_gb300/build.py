@@ -48,8 +48,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    newest_hdr = max(os.path.getmtime(p) for p in glob.glob(os.path.join(CSRC, "*.h*")) +
-                     glob.glob(os.path.join(INCLUDE, "*.h")))
+    newest_hdr = max(os.path.getmtime(p) for p in glob.glob(os.path.join(CSRC, "*.h")) +
+                     glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
     def obj_of(src):
         return os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")

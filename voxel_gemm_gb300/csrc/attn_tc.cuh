@@ -45,6 +45,38 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ float2 two(const uint32_t* r) {
+    return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// ---- products, issued by lane 0 of a converged warp (`on`).  A short product leaves the
+// warp a few dozen cycles, so the steps are unrolled and a step's descriptors are its tile's
+// plus a constant.
+
+// D (+)= A B^T over `steps` (<= STEPS) K = 16 steps, both K-major in shared memory; ABLK, BBLK: bytes
+// between the operands' 64-channel blocks.
+template <int STEPS, int ABLK, int BBLK>
+__device__ __forceinline__ void mma_channels(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             int steps) {
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+        if (j >= steps) break;
+        const uint32_t ao = ((j >> 2) * ABLK + (j & 3) * 32) >> 4, bo = ((j >> 2) * BBLK + (j & 3) * 32) >> 4;
+        mma_f16_on(on, d, a + ao, b + bo, idesc, j > 0);
+    }
+}
+// D (+)= A B over `steps` (<= STEPS) K = 16 steps of rows, A in TMEM, B MN-major in shared memory.
+template <int STEPS>
+__device__ __forceinline__ void mma_rows(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int steps,
+                                         uint32_t acc) {
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+        if (j >= steps) break;
+        if (j == 0) mma_f16_ta_on(on, d, a, b, idesc, acc);
+        else mma_f16_ta_on(on, d, a + 8 * j, b + j * (2048 >> 4), idesc, 1);
+    }
+}
+
 // Zero rows [from, to) of a tile of `blocks` 64-channel blocks, `block_bytes` apart, by one warp.
 __device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to, int blocks, int block_bytes) {
     const int per = (to - from) * 8;  // 16-byte pieces of a block
@@ -87,13 +119,13 @@ struct Waiter {
     volatile uint32_t* abort;
     bool ok = true;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, abort)) {
+        if (ok && !mbar_wait_cycles(bar, parity, abort)) {
             ok = false;
             *abort = 1;
         }
         return ok;
     }
-    // The whole warp goes on or gives up together.
+    // The whole warp goes on or gives up together, converged.
     __device__ __forceinline__ bool agree() {
         ok = __all_sync(0xffffffffu, ok);
         return ok;

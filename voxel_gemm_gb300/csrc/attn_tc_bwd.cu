@@ -133,57 +133,56 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
     };
     Waiter wait{s_abort};
 
+    const uint32_t on = lane == 0;  // the lane that carries out a role warp's copies and products
     if (warp == kLoader) {
         uint32_t it = 0, uc = 0;
-        for (int64_t u = blockIdx.x; u < units && wait.agree(); u += gridDim.x) {
+        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
-            if (x.hi <= x.lo || lane != 0 || !wait(q_empty, (uc & 1u) ^ 1u)) continue;
+            if (x.hi <= x.lo) continue;
+            wait(q_empty, (uc & 1u) ^ 1u);
+            if (!wait.agree()) break;
             const int nq = x.rows > kM ? NQ : 1;
-            mbar_arrive_expect_tx(q_full, 2 * nq * C::kRowTile);
+            mbar_arrive_expect_tx_on(on, q_full, 2 * nq * C::kRowTile);
             for (int w = 0; w < nq; ++w)
                 for (int b = 0; b < C::kBlocks; ++b) {
                     const int row = x.t.q0 + (x.t.first + w * kM) / a.gp;
                     const uint32_t off = w * C::kRowTile + b * kM * 128;
-                    tma_load_3d(sQ + off, &maps.q, b * 64, x.hs * a.gp, row, q_full);
-                    tma_load_3d(sG + off, &maps.go, b * 64, x.hs * a.gp, row, q_full);
+                    tma_load_3d_on(on, sQ + off, &maps.q, b * 64, x.hs * a.gp, row, q_full);
+                    tma_load_3d_on(on, sG + off, &maps.go, b * 64, x.hs * a.gp, row, q_full);
                 }
             ++uc;
             const int kh = x.hs * a.gp / group;
             for (int e = x.lo; e < x.hi; ++e, ++it) {
                 const uint32_t st = it % S;
-                if (!wait(kv_empty + 8 * st, ((it / S) & 1u) ^ 1u)) break;
-                mbar_arrive_expect_tx(kv_full + 8 * st, 2 * C::kKeyTile);
+                wait(kv_empty + 8 * st, ((it / S) & 1u) ^ 1u);
+                if (!wait.agree()) break;
+                mbar_arrive_expect_tx_on(on, kv_full + 8 * st, 2 * C::kKeyTile);
                 for (int b = 0; b < C::kBlocks; ++b) {
                     const uint32_t dst = sKV + 2 * st * C::kKeyTile + b * kN * 128;
-                    tma_load_3d(dst, &maps.k, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
-                    tma_load_3d(dst + C::kKeyTile, &maps.v, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
+                    tma_load_3d_on(on, dst, &maps.k, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
+                    tma_load_3d_on(on, dst + C::kKeyTile, &maps.v, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
                 }
             }
         }
         // every copy has landed before the block may exit
-        if (lane == 0) {
-            if (uc > 0 && !mbar_wait_timed(q_full, (uc - 1) & 1u)) wait.ok = false;
-            for (uint32_t i = 0; i < (uint32_t)S && i < it; ++i) {
-                const uint32_t last = it - 1 - i;
-                if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
-            }
-            if (!wait.ok) atomicOr(a.err, kErrTimeout);
+        if (uc > 0 && !mbar_wait_timed(q_full, (uc - 1) & 1u)) wait.ok = false;
+        for (uint32_t i = 0; i < (uint32_t)S && i < it; ++i) {
+            const uint32_t last = it - 1 - i;
+            if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
-        __syncwarp();
+        if (!wait.agree() && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;
         const uint32_t idesc_o = idesc_f16_bn(BF16, ksteps * 16);
         uint32_t it = 0, uc = 0, pc[NQ] = {}, oc[NQ] = {};
         auto scores = [&](int w, uint32_t st, int n) {  // S_w = Q_w K^T and dP_w = dO_w V^T
-            const uint32_t id = idesc_f16(BF16, n);
-            const uint32_t k = sKV + 2 * st * C::kKeyTile, v = k + C::kKeyTile;
-            for (int j = 0; j < ksteps; ++j) {
-                const uint32_t ra = w * C::kRowTile + (j >> 2) * kM * 128 + (j & 3) * 32;
-                const uint32_t rb = (j >> 2) * kN * 128 + (j & 3) * 32;
-                mma_f16(tmem + w * 2 * kN, sw128_kmajor_desc(sQ + ra), sw128_kmajor_desc(k + rb), id, j);
-                mma_f16(tmem + w * 2 * kN + kN, sw128_kmajor_desc(sG + ra), sw128_kmajor_desc(v + rb), id, j);
-            }
-            mma_commit(s_full + 8 * w);
+            const uint32_t id = idesc_f16(BF16, n), d = tmem + w * 2 * kN;
+            const uint32_t k = sKV + 2 * st * C::kKeyTile;
+            mma_channels<DP / 16, kM * 128, kN * 128>(on, d, sw128_kmajor_desc(sQ + w * C::kRowTile),
+                                                      sw128_kmajor_desc(k), id, ksteps);
+            mma_channels<DP / 16, kM * 128, kN * 128>(on, d + kN, sw128_kmajor_desc(sG + w * C::kRowTile),
+                                                      sw128_kmajor_desc(k + C::kKeyTile), id, ksteps);
+            mma_commit_on(on, s_full + 8 * w);
         };
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
@@ -204,46 +203,41 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
             arrive(x.lo, it);
             if (!wait.agree()) break;
             tc_fence_after();
-            if (lane == 0) {
-                for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
-                if (x.hi - x.lo == 1) mma_commit(q_empty);
-            }
+            for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
+            if (x.hi - x.lo == 1) mma_commit_on(on, q_empty);
             for (int e = x.lo; e < x.hi; ++e, ++it) {
                 const uint32_t st = it % S, nx = (it + 1) % S;
                 const bool more = e + 1 < x.hi;
                 if (more) arrive(e + 1, it + 1);
-                if (!wait.agree()) break;
                 const int n16 = padded(e);
                 for (int w = 0; w < nq; ++w) {
                     wait(p_full + 8 * w, pc[w]++ & 1u);
                     if (e == x.lo) wait(o_empty + 8 * w, (oc[w] & 1u) ^ 1u);
                     if (!wait.agree()) break;
                     tc_fence_after();
-                    if (lane == 0) {
-                        for (int j = 0; j < n16 / 16; ++j)
-                            mma_f16_ta(tmem + C::kOCol + w * DP, tmem + w * 2 * kN + 8 * j,
-                                       sw128_mnmajor_desc(sKV + 2 * st * C::kKeyTile + j * 2048, kN * 128), idesc_o,
-                                       e > x.lo || j > 0);
-                        if (more) scores(w, nx, padded(e + 1));
-                        else mma_commit(o_full + 8 * w);
+                    mma_rows<kN / 16>(on, tmem + C::kOCol + w * DP, tmem + w * 2 * kN,
+                                      sw128_mnmajor_desc(sKV + 2 * st * C::kKeyTile, kN * 128), idesc_o, n16 / 16,
+                                      e > x.lo);
+                    if (more) {
+                        scores(w, nx, padded(e + 1));
+                    } else {
+                        mma_commit_on(on, o_full + 8 * w);
+                        ++oc[w];
                     }
-                    if (!more) ++oc[w];
                 }
-                if (lane == 0 && wait.ok) {
-                    mma_commit(kv_empty + 8 * st);
-                    if (e + 2 == x.hi) mma_commit(q_empty);
-                }
+                if (!wait.ok) break;
+                mma_commit_on(on, kv_empty + 8 * st);
+                if (e + 2 == x.hi) mma_commit_on(on, q_empty);
             }
             ++uc;
         }
-        if (lane == 0) {  // every product has finished before TMEM is released
-            mma_commit(done);
-            if (!mbar_wait_timed(done, 0) || !wait.ok) {
-                *s_abort = 1;
-                atomicOr(a.err, kErrTimeout);
-            }
+        // every product has finished before TMEM is released
+        mma_commit_on(on, done);
+        if (!mbar_wait_timed(done, 0)) wait.ok = false;
+        if (!wait.agree() && lane == 0) {
+            *s_abort = 1;
+            atomicOr(a.err, kErrTimeout);
         }
-        __syncwarp();
     } else {
         const int w = warp >> 2, quad = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
@@ -260,6 +254,8 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
             float2 st = make_float2(0.f, 0.f);
             if (mine) st = a.stats[((int64_t)x.hs * a.n_q + x.t.q0) * a.gp + pr];
             const float base = st.x - kLift<BF16>, delta = st.y * lift.x;
+            const float2 c2 = make_float2(c, c), base2 = make_float2(-base, -base);
+            const float2 lift2 = make_float2(lift.x, lift.x), delta2 = make_float2(-delta, -delta);
             for (int e = x.lo; e < x.hi; ++e) {
                 wait(s_full + 8 * w, sc & 1u);
                 if (!wait.agree()) break;
@@ -273,19 +269,20 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
                         tmem_ld32(t_s + kN + 32 * i, g[i]);
                     }
                     tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) tmem_ld_done(s[i]), tmem_ld_done(g[i]);
                     const int left = x.t.lk - e * kN;
                     uint32_t d[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        float ds[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int i = 2 * j + k;
-                            const float p = ex2(fmaf(__uint_as_float(s[i >> 5][i & 31]), c, -base));
-                            ds[k] = p * fmaf(__uint_as_float(g[i >> 5][i & 31]), lift.x, -delta);
-                            if (i >= left) ds[k] = 0.f;
-                        }
-                        d[j] = pack2<BF16>(ds[0], ds[1]);
+                        const int r = j >> 4, i = 2 * (j & 15);
+                        float2 p = fma2(two(&s[r][i]), c2, base2);
+                        p = make_float2(ex2(p.x), ex2(p.y));
+                        float2 ds = BF16 ? add2(two(&g[r][i]), delta2) : fma2(two(&g[r][i]), lift2, delta2);
+                        ds = mul2(p, ds);
+                        if (2 * j >= left) ds.x = 0.f;
+                        if (2 * j + 1 >= left) ds.y = 0.f;
+                        d[j] = pack2<BF16>(ds.x, ds.y);
                     }
                     tmem_st32(t_s, d);
                     tmem_st_wait();
@@ -313,13 +310,16 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
                     if (x.hi > x.lo) {
                         tmem_ld32(t_o + 32 * i, o);
                         tmem_ld_wait();
+                        tmem_ld_done(o);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) o[j] = 0u;
                     }
-                    if (!mine) continue;
-                    if (a.splits > 1) store_cols32_f32(dst_p + 32 * i, o, mul, a.d - 32 * i);
-                    else store_cols32<BF16>(dst + 32 * i, o, mul, a.d - 32 * i);
+                    if (mine) {
+                        if (a.splits > 1) store_cols32_f32(dst_p + 32 * i, o, mul, a.d - 32 * i);
+                        else store_cols32<BF16>(dst + 32 * i, o, mul, a.d - 32 * i);
+                    }
+                    __syncwarp();
                 }
             }
             if (x.hi > x.lo) {
@@ -426,54 +426,53 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     };
     Waiter wait{s_abort};
 
+    const uint32_t on = lane == 0;  // the lane that carries out a role warp's copies and products
     if (warp == kLoader) {
         uint32_t it = 0, uc = 0;
-        for (int64_t u = blockIdx.x; u < units && wait.agree(); u += gridDim.x) {
+        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
-            if (x.steps == 0 || lane != 0 || !wait(k_empty, (uc & 1u) ^ 1u)) continue;
-            mbar_arrive_expect_tx(k_full, 2 * C::kKeyTile);
+            if (x.steps == 0) continue;
+            wait(k_empty, (uc & 1u) ^ 1u);
+            if (!wait.agree()) break;
+            mbar_arrive_expect_tx_on(on, k_full, 2 * C::kKeyTile);
             for (int b = 0; b < C::kBlocks; ++b) {
-                tma_load_3d(sK + b * kM * 128, &maps.k, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
-                tma_load_3d(sV + b * kM * 128, &maps.v, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
+                tma_load_3d_on(on, sK + b * kM * 128, &maps.k, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
+                tma_load_3d_on(on, sV + b * kM * 128, &maps.v, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
             }
             ++uc;
             for (int hs = 0; hs < sets_per_key && wait.ok; ++hs)
                 for (int e = x.lo; e < x.hi; ++e, ++it) {
                     const uint32_t st = it % S;
-                    if (!wait(r_empty + 8 * st, ((it / S) & 1u) ^ 1u)) break;
-                    mbar_arrive_expect_tx(r_full + 8 * st, 2 * C::kRowTile);
+                    wait(r_empty + 8 * st, ((it / S) & 1u) ^ 1u);
+                    if (!wait.agree()) break;
+                    mbar_arrive_expect_tx_on(on, r_full + 8 * st, 2 * C::kRowTile);
                     const int head = (x.kh * sets_per_key + hs) * a.gp, row = x.t.q0 + e * kN / a.gp;
                     for (int b = 0; b < C::kBlocks; ++b) {
                         const uint32_t dst = sQG + 2 * st * C::kRowTile + b * kN * 128;
-                        tma_load_3d(dst, &maps.q, b * 64, head, row, r_full + 8 * st);
-                        tma_load_3d(dst + C::kRowTile, &maps.go, b * 64, head, row, r_full + 8 * st);
+                        tma_load_3d_on(on, dst, &maps.q, b * 64, head, row, r_full + 8 * st);
+                        tma_load_3d_on(on, dst + C::kRowTile, &maps.go, b * 64, head, row, r_full + 8 * st);
                     }
                 }
         }
         // every copy has landed before the block may exit
-        if (lane == 0) {
-            if (uc > 0 && !mbar_wait_timed(k_full, (uc - 1) & 1u)) wait.ok = false;
-            for (uint32_t i = 0; i < (uint32_t)S && i < it; ++i) {
-                const uint32_t last = it - 1 - i;
-                if (!mbar_wait_timed(r_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
-            }
-            if (!wait.ok) atomicOr(a.err, kErrTimeout);
+        if (uc > 0 && !mbar_wait_timed(k_full, (uc - 1) & 1u)) wait.ok = false;
+        for (uint32_t i = 0; i < (uint32_t)S && i < it; ++i) {
+            const uint32_t last = it - 1 - i;
+            if (!mbar_wait_timed(r_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
-        __syncwarp();
+        if (!wait.agree() && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;
         const uint32_t idesc_o = idesc_f16_bn(BF16, ksteps * 16);
         uint32_t it = 0, uc = 0, pc[2] = {0, 0};
         // steps alternate between the two score buffers across units too: step i of the block uses i & 1
         auto scores = [&](uint32_t i, int n) {  // S^T = K Q^T and dP^T = V dO^T of step i
-            const uint32_t id = idesc_f16(BF16, n), st = i % S, w = i & 1u;
-            const uint32_t q = sQG + 2 * st * C::kRowTile, g = q + C::kRowTile;
-            for (int j = 0; j < ksteps; ++j) {
-                const uint32_t ra = (j >> 2) * kM * 128 + (j & 3) * 32, rb = (j >> 2) * kN * 128 + (j & 3) * 32;
-                mma_f16(tmem + w * 2 * kN, sw128_kmajor_desc(sK + ra), sw128_kmajor_desc(q + rb), id, j);
-                mma_f16(tmem + w * 2 * kN + kN, sw128_kmajor_desc(sV + ra), sw128_kmajor_desc(g + rb), id, j);
-            }
-            mma_commit(s_full + 8 * w);
+            const uint32_t id = idesc_f16(BF16, n), st = i % S, w = i & 1u, d = tmem + w * 2 * kN;
+            const uint32_t q = sQG + 2 * st * C::kRowTile;
+            mma_channels<DP / 16, kM * 128, kN * 128>(on, d, sw128_kmajor_desc(sK), sw128_kmajor_desc(q), id, ksteps);
+            mma_channels<DP / 16, kM * 128, kN * 128>(on, d + kN, sw128_kmajor_desc(sV),
+                                                      sw128_kmajor_desc(q + C::kRowTile), id, ksteps);
+            mma_commit_on(on, s_full + 8 * w);
         };
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
@@ -495,11 +494,12 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             wait(k_full, uc & 1u);
             for (int i = 0; i < 2 && i < x.steps; ++i) {
                 arrive(i, it + i);
-                if (!wait.agree()) break;
+                if (!wait.ok) break;
                 tc_fence_after();
-                if (lane == 0) scores(it + i, padded(i));
+                scores(it + i, padded(i));
             }
-            if (lane == 0 && wait.ok && x.steps <= 2) mma_commit(k_empty);
+            if (!wait.agree()) break;
+            if (x.steps <= 2) mma_commit_on(on, k_empty);
             wait(o_empty, (uc & 1u) ^ 1u);
             for (int i = 0; i < x.steps; ++i, ++it) {
                 const uint32_t st = it % S, w = it & 1u;
@@ -509,42 +509,38 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                 wait(p_full + 8 * w, pc[w]++ & 1u);
                 if (!wait.agree()) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    for (int j = 0; j < n16 / 16; ++j) {
-                        const uint32_t acc = i > 0 || j > 0;
-                        const uint32_t pt = tmem + w * 2 * kN + 8 * j;
-                        mma_f16_ta(tmem + C::kVCol, pt, sw128_mnmajor_desc(g + j * 2048, kN * 128), idesc_o, acc);
-                        mma_f16_ta(tmem + C::kKCol, pt + kN, sw128_mnmajor_desc(q + j * 2048, kN * 128), idesc_o, acc);
-                    }
-                    mma_commit(r_empty + 8 * st);
-                    if (i + 2 < x.steps) scores(it + 2, padded(i + 2));
-                    if (i + 3 == x.steps) mma_commit(k_empty);
-                    if (i + 1 == x.steps) mma_commit(o_full);
-                }
+                const uint32_t pt = tmem + w * 2 * kN;
+                mma_rows<kN / 16>(on, tmem + C::kVCol, pt, sw128_mnmajor_desc(g, kN * 128), idesc_o, n16 / 16, i > 0);
+                mma_rows<kN / 16>(on, tmem + C::kKCol, pt + kN, sw128_mnmajor_desc(q, kN * 128), idesc_o, n16 / 16,
+                                  i > 0);
+                mma_commit_on(on, r_empty + 8 * st);
+                if (i + 2 < x.steps) scores(it + 2, padded(i + 2));
+                if (i + 3 == x.steps) mma_commit_on(on, k_empty);
+                if (i + 1 == x.steps) mma_commit_on(on, o_full);
             }
             ++uc;
         }
-        if (lane == 0) {  // every product has finished before TMEM is released
-            mma_commit(done);
-            if (!mbar_wait_timed(done, 0) || !wait.ok) {
-                *s_abort = 1;
-                atomicOr(a.err, kErrTimeout);
-            }
+        // every product has finished before TMEM is released
+        mma_commit_on(on, done);
+        if (!mbar_wait_timed(done, 0)) wait.ok = false;
+        if (!wait.agree() && lane == 0) {
+            *s_abort = 1;
+            atomicOr(a.err, kErrTimeout);
         }
-        __syncwarp();
     } else {
         const int w = warp >> 2, quad = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t t_s = t_lane + w * 2 * kN;
         const float c = a.scale_log2;
         const float2 lift = grad_lift<BF16>(a);
+        const float2 c2 = make_float2(c, c), lift2 = make_float2(lift.x, lift.x);
         float2* my_stats = s_stats + warp * 2 * kN;
         uint32_t it = 0, sc = 0, uc = 0;
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
             if (x.t.b < 0) continue;
             const int rows = x.t.lq * a.gp, per = x.hi - x.lo;
-            // statistics (lse log2 e, delta) of rows lane and lane + 32 of step i; each warp keeps its own copy
+            // statistics (lse log2 e, delta) of rows lane and lane + 32 of step i, kept negated, a copy per warp
             auto stat = [&](int i, int r0) {
                 float2 v = make_float2(0.f, 0.f);
                 if (i < x.steps) {
@@ -557,8 +553,8 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             float2 next0 = stat(i, 0), next1 = stat(i, 32);
             for (; i < x.steps; i += 2) {
                 float2* cur = my_stats + (sc & 1u) * kN;
-                cur[lane] = make_float2(next0.x - kLift<BF16>, next0.y * lift.x);
-                cur[lane + 32] = make_float2(next1.x - kLift<BF16>, next1.y * lift.x);
+                cur[lane] = make_float2(kLift<BF16> - next0.x, -next0.y * lift.x);
+                cur[lane + 32] = make_float2(kLift<BF16> - next1.x, -next1.y * lift.x);
                 __syncwarp();
                 next0 = stat(i + 2, 0);
                 next1 = stat(i + 2, 32);
@@ -573,17 +569,20 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                     tmem_ld32(t_s + 32 * half, s);
                     tmem_ld32(t_s + kN + 32 * half, g);
                     tmem_ld_wait();
+                    tmem_ld_done(s);
+                    tmem_ld_done(g);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float4 st = *reinterpret_cast<const float4*>(cur + 32 * half + 2 * j);
-                        float p0 = ex2(fmaf(__uint_as_float(s[2 * j]), c, -st.x));
-                        float p1 = ex2(fmaf(__uint_as_float(s[2 * j + 1]), c, -st.z));
-                        float d0 = p0 * fmaf(__uint_as_float(g[2 * j]), lift.x, -st.y);
-                        float d1 = p1 * fmaf(__uint_as_float(g[2 * j + 1]), lift.x, -st.w);
-                        if (32 * half + 2 * j >= left) p0 = d0 = 0.f;
-                        if (32 * half + 2 * j + 1 >= left) p1 = d1 = 0.f;
-                        p[j] = pack2<BF16>(p0, p1);
-                        d[j] = pack2<BF16>(d0, d1);
+                        float2 pr = fma2(two(s + 2 * j), c2, make_float2(st.x, st.z));
+                        pr = make_float2(ex2(pr.x), ex2(pr.y));
+                        const float2 minus = make_float2(st.y, st.w);
+                        float2 ds = BF16 ? add2(two(g + 2 * j), minus) : fma2(two(g + 2 * j), lift2, minus);
+                        ds = mul2(pr, ds);
+                        if (32 * half + 2 * j >= left) pr.x = ds.x = 0.f;
+                        if (32 * half + 2 * j + 1 >= left) pr.y = ds.y = 0.f;
+                        p[j] = pack2<BF16>(pr.x, pr.y);
+                        d[j] = pack2<BF16>(ds.x, ds.y);
                     }
                     tmem_st16(t_s + 16 * half, p);
                     tmem_st16(t_s + kN + 16 * half, d);
@@ -614,13 +613,16 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                 if (x.steps > 0) {
                     tmem_ld32(t_lane + (w == 0 ? C::kVCol : C::kKCol) + 32 * i2, o);
                     tmem_ld_wait();
+                    tmem_ld_done(o);
                 }
                 if (!live)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = 0u;
-                if (!mine) continue;
-                if (a.splits > 1) store_cols32_f32(dst_p + 32 * i2, o, mul, a.d - 32 * i2);
-                else store_cols32<BF16>(dst + 32 * i2, o, mul, a.d - 32 * i2);
+                if (mine) {
+                    if (a.splits > 1) store_cols32_f32(dst_p + 32 * i2, o, mul, a.d - 32 * i2);
+                    else store_cols32<BF16>(dst + 32 * i2, o, mul, a.d - 32 * i2);
+                }
+                __syncwarp();
             }
             if (x.steps > 0) {
                 tc_fence_before();

@@ -11,6 +11,7 @@
 //   then one warp        loader: TMA copies of Q (per unit) and of K and V tiles (a ring).
 //   then one warp        the MMA-issuing thread: S into TMEM, then O += P V with P read
 //                        from TMEM.
+//   two idle warps       fill the last warpgroup, whose registers go to the softmax warps.
 // With NQ = 2 the two row tiles take turns: one's products run while the other's
 // exponentials do, and both read each K and V tile from the same copy.  NQ = 1 leaves
 // room for two blocks on an SM and serves calls with few rows per sample.
@@ -34,7 +35,7 @@ constexpr int kN = 128;   // keys of a tile
 
 template <int DP, int NQ>
 struct Cfg {
-    static constexpr int kThreads = NQ * 128 + 64;
+    static constexpr int kThreads = NQ * 128 + 128;
     static constexpr int kBlocks = DP / 64;
     static constexpr int kTile = kM * 128 * kBlocks;               // bytes of a Q, K or V tile
     static constexpr int S = NQ == 2 ? (DP == 64 ? 6 : 4) : (DP == 64 ? 4 : 2);  // ring stages
@@ -47,7 +48,7 @@ struct Cfg {
 static_assert(Cfg<128, 2>::kSmem <= 232448 && 2 * (Cfg<128, 1>::kSmem + 1024) <= 233472, "shared memory");
 
 template <bool BF16, int DP, int NQ>
-__global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
+__global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     k_attn_tc_fwd(const AttnArgs a, const __grid_constant__ AttnMaps maps, const int tiles) {
     using C = Cfg<DP, NQ>;
     constexpr int S = C::S;
@@ -118,53 +119,53 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
         return x;
     };
     Waiter wait{s_abort};
-
+    // the block was launched with 168 registers a thread (NQ = 1: 128); the softmax warps,
+    // which hold a row of scores each, take what the last warpgroup leaves
+    if (warp >= kLoader) reg_shrink<NQ == 2 ? 72 : 56>();
+    const uint32_t on = lane == 0;  // the lane that carries out a role warp's copies and products
     if (warp == kLoader) {
         uint32_t it = 0, uc = 0;
-        for (int64_t u = blockIdx.x; u < units && wait.agree(); u += gridDim.x) {
+        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
-            if (x.hi <= x.lo || lane != 0 || !wait(q_empty, (uc & 1u) ^ 1u)) continue;
+            if (x.hi <= x.lo) continue;
+            wait(q_empty, (uc & 1u) ^ 1u);
+            if (!wait.agree()) break;
             const int nq = x.rows > kM ? NQ : 1;
-            mbar_arrive_expect_tx(q_full, nq * C::kTile);
+            mbar_arrive_expect_tx_on(on, q_full, nq * C::kTile);
             for (int w = 0; w < nq; ++w)
                 for (int b = 0; b < C::kBlocks; ++b)
-                    tma_load_3d(sQ + w * C::kTile + b * kM * 128, &maps.q, b * 64, x.hs * a.gp,
-                                x.t.q0 + (x.t.first + w * kM) / a.gp, q_full);
+                    tma_load_3d_on(on, sQ + w * C::kTile + b * kM * 128, &maps.q, b * 64, x.hs * a.gp,
+                                   x.t.q0 + (x.t.first + w * kM) / a.gp, q_full);
             ++uc;
             const int kh = x.hs * a.gp / group;
             for (int e = 2 * x.lo; e < 2 * x.hi; ++e, ++it) {  // K and V tiles in turn
                 const uint32_t st = it % S;
-                if (!wait(kv_empty + 8 * st, ((it / S) & 1u) ^ 1u)) break;
-                mbar_arrive_expect_tx(kv_full + 8 * st, C::kTile);
+                wait(kv_empty + 8 * st, ((it / S) & 1u) ^ 1u);
+                if (!wait.agree()) break;
+                mbar_arrive_expect_tx_on(on, kv_full + 8 * st, C::kTile);
                 for (int b = 0; b < C::kBlocks; ++b)
-                    tma_load_3d(sKV + st * C::kTile + b * kN * 128, e & 1 ? &maps.v : &maps.k, b * 64, kh,
-                                x.t.k0 + (e >> 1) * kN, kv_full + 8 * st);
+                    tma_load_3d_on(on, sKV + st * C::kTile + b * kN * 128, e & 1 ? &maps.v : &maps.k, b * 64, kh,
+                                   x.t.k0 + (e >> 1) * kN, kv_full + 8 * st);
             }
         }
         // every copy has landed before the block may exit
-        if (lane == 0) {
-            if (uc > 0 && !mbar_wait_timed(q_full, (uc - 1) & 1u)) wait.ok = false;
-            for (uint32_t i = 0; i < (uint32_t)S && i < it; ++i) {
-                const uint32_t last = it - 1 - i;
-                if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
-            }
-            if (!wait.ok) atomicOr(a.err, kErrTimeout);
+        if (uc > 0 && !mbar_wait_timed(q_full, (uc - 1) & 1u)) wait.ok = false;
+        for (uint32_t i = 0; i < (uint32_t)S && i < it; ++i) {
+            const uint32_t last = it - 1 - i;
+            if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
-        __syncwarp();
+        if (!wait.agree() && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;          // K = 16 steps over the channels
-        const int on = ksteps * 16;                  // columns of O
-        const uint32_t idesc_o = idesc_f16_bn(BF16, on);
+        const int o_cols = ksteps * 16;              // columns of O
+        const uint32_t idesc_o = idesc_f16_bn(BF16, o_cols);
         uint32_t it = 0, uc = 0, pc[NQ] = {}, oc[NQ] = {};
         // S_w = Q_w K^T of the tile in stage st, `n` keys
         auto scores = [&](int w, uint32_t st, int n) {
-            const uint32_t id = idesc_f16(BF16, n);
-            for (int j = 0; j < ksteps; ++j) {
-                const uint32_t off = (j >> 2) * kM * 128 + (j & 3) * 32;
-                mma_f16(tmem + w * kN, sw128_kmajor_desc(sQ + w * C::kTile + off),
-                        sw128_kmajor_desc(sKV + st * C::kTile + off), id, j);
-            }
-            mma_commit(s_full + 8 * w);
+            mma_channels<DP / 16, kM * 128, kN * 128>(on, tmem + w * kN, sw128_kmajor_desc(sQ + w * C::kTile),
+                                                      sw128_kmajor_desc(sKV + st * C::kTile), idesc_f16(BF16, n),
+                                                      ksteps);
+            mma_commit_on(on, s_full + 8 * w);
         };
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
@@ -176,11 +177,9 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
             wait(kv_full + 8 * (it % S), (it / S) & 1u);
             if (!wait.agree()) break;
             tc_fence_after();
-            if (lane == 0) {
-                for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
-                mma_commit(kv_empty + 8 * (it % S));
-                if (x.hi - x.lo == 1) mma_commit(q_empty);
-            }
+            for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
+            mma_commit_on(on, kv_empty + 8 * (it % S));
+            if (x.hi - x.lo == 1) mma_commit_on(on, q_empty);
             ++it;
             for (int e = x.lo; e < x.hi; ++e) {
                 const uint32_t sv = it % S, pv = (it / S) & 1u;
@@ -200,36 +199,32 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
                     if (e == x.lo) wait(o_empty + 8 * w, (oc[w] & 1u) ^ 1u);
                     if (!wait.agree()) break;
                     tc_fence_after();
-                    if (lane == 0) {
-                        for (int j = 0; j < n16 / 16; ++j)
-                            mma_f16_ta(tmem + C::kOCol + w * DP, tmem + w * kN + 8 * j,
-                                       sw128_mnmajor_desc(sKV + sv * C::kTile + j * 2048, kN * 128), idesc_o,
-                                       e > x.lo || j > 0);
-                        if (more) scores(w, sk, padded(e + 1));
-                        else mma_commit(o_full + 8 * w);
-                    }
-                    if (!more) ++oc[w];
-                }
-                if (lane == 0 && wait.ok) {
-                    mma_commit(kv_empty + 8 * sv);
+                    mma_rows<kN / 16>(on, tmem + C::kOCol + w * DP, tmem + w * kN,
+                                      sw128_mnmajor_desc(sKV + sv * C::kTile, kN * 128), idesc_o, n16 / 16, e > x.lo);
                     if (more) {
-                        mma_commit(kv_empty + 8 * sk);
-                        if (e + 2 == x.hi) mma_commit(q_empty);
+                        scores(w, sk, padded(e + 1));
+                    } else {
+                        mma_commit_on(on, o_full + 8 * w);
+                        ++oc[w];
                     }
                 }
+                if (!wait.ok) break;
+                mma_commit_on(on, kv_empty + 8 * sv);
+                if (more) mma_commit_on(on, kv_empty + 8 * sk);
+                if (e + 2 == x.hi) mma_commit_on(on, q_empty);
                 it += more ? 2 : 1;
             }
             ++uc;
         }
-        if (lane == 0) {  // every product has finished before TMEM is released
-            mma_commit(done);
-            if (!mbar_wait_timed(done, 0) || !wait.ok) {
-                *s_abort = 1;
-                atomicOr(a.err, kErrTimeout);
-            }
+        // every product has finished before TMEM is released
+        mma_commit_on(on, done);
+        if (!mbar_wait_timed(done, 0)) wait.ok = false;
+        if (!wait.agree() && lane == 0) {
+            *s_abort = 1;
+            atomicOr(a.err, kErrTimeout);
         }
-        __syncwarp();
-    } else {
+    } else if (warp < kLoader) {
+        reg_grow<NQ == 2 ? 216 : 200>();
         const int w = warp >> 2, quad = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t t_s = t_lane + w * kN, t_o = t_lane + C::kOCol + w * DP;
@@ -253,6 +248,8 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32 * i, s[i]);
                     tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld_done(s[i]);
                     const int left = x.t.lk - e * kN;
                     if (left < kN) {
 #pragma unroll
@@ -262,9 +259,10 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
                     float top[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        top[i] = __uint_as_float(s[i][0]);
+                        top[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
 #pragma unroll
-                        for (int j = 1; j < 32; ++j) top[i] = fmaxf(top[i], __uint_as_float(s[i][j]));
+                        for (int j = 2; j < 32; j += 2)
+                            top[i] = max3(top[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
                     }
                     const float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     const bool grow = big > m + lazy || (m == -INFINITY && big > m);
@@ -279,6 +277,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
                                 uint32_t o[16];
                                 tmem_ld16(t_o + 16 * i, o);
                                 tmem_ld_wait();
+                                tmem_ld_done(o);
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
                                 tmem_st16(t_o + 16 * i, o);
@@ -286,22 +285,22 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
                         }
                     }
                     const float base = (m == -INFINITY ? 0.f : m * c) - kLift;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 c2 = make_float2(c, c), base2 = make_float2(-base, -base);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t p[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            const uint32_t* two = &s[2 * i + (j >> 4)][2 * (j & 15)];
-                            const float p0 = ex2(fmaf(__uint_as_float(two[0]), c, -base));
-                            const float p1 = ex2(fmaf(__uint_as_float(two[1]), c, -base));
-                            sum[2 * (j & 1)] += p0;
-                            sum[2 * (j & 1) + 1] += p1;
-                            p[j] = pack2<BF16>(p0, p1);
+                            float2 x2 = fma2(two(&s[2 * i + (j >> 4)][2 * (j & 15)]), c2, base2);
+                            x2 = make_float2(ex2(x2.x), ex2(x2.y));
+                            sum[j & 1] = add2(sum[j & 1], x2);
+                            p[j] = pack2<BF16>(x2.x, x2.y);
                         }
                         tmem_st32(t_s + 32 * i, p);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 both = add2(sum[0], sum[1]);
+                    l += both.x + both.y;
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -325,6 +324,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
                 if (mine && dst_l) dst_l[(int64_t)h * a.n_q + qi] = lse;
                 float* dst_p = a.part + (((size_t)x.part * a.n_q + qi) * a.hq + h) * a.d;
                 uint16_t* dst = head_row<uint16_t>(a.o, qi, h);
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < DP / 32; ++i) {
                     if (32 * i >= a.d) break;
@@ -332,13 +332,16 @@ __global__ void __launch_bounds__(NQ * 128 + 64, NQ == 1 ? 2 : 1)
                     if (x.hi > x.lo) {
                         tmem_ld32(t_o + 32 * i, o);
                         tmem_ld_wait();
+                        tmem_ld_done(o);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) o[j] = 0u;
                     }
-                    if (!mine) continue;
-                    if (a.splits > 1) store_cols32_f32(dst_p + 32 * i, o, inv, a.d - 32 * i);
-                    else store_cols32<BF16>(dst + 32 * i, o, inv, a.d - 32 * i);
+                    if (mine) {
+                        if (a.splits > 1) store_cols32_f32(dst_p + 32 * i, o, inv, a.d - 32 * i);
+                        else store_cols32<BF16>(dst + 32 * i, o, inv, a.d - 32 * i);
+                    }
+                    __syncwarp();
                 }
             }
             if (x.hi > x.lo) {
