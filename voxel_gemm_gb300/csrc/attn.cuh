@@ -83,11 +83,15 @@ __device__ __forceinline__ AttnTile attn_find_tile(const AttnArgs& a, const int3
             const int src = __ffs(at) - 1;
             r.b = b0 + src;
             r.first = (t - __shfl_sync(0xffffffffu, incl - tiles, src)) * rows;
-            r.q0 = a.q_off[r.b];
-            r.lq = a.q_off[r.b + 1] - r.q0;
-            r.k0 = a.k_off[r.b];
-            r.krows = a.k_off[r.b + 1] - r.k0;
-            r.lk = a.k_len ? a.k_len[r.b] : r.krows;
+            // one load each, shared out by a shuffle: the compiler knows the result to be uniform
+            const int32_t* p = lane < 2 ? a.q_off + r.b + lane : lane < 4 ? a.k_off + r.b + (lane - 2)
+                               : a.k_len ? a.k_len + r.b : nullptr;
+            const int v = p ? *p : 0;
+            r.q0 = __shfl_sync(0xffffffffu, v, 0);
+            r.lq = __shfl_sync(0xffffffffu, v, 1) - r.q0;
+            r.k0 = __shfl_sync(0xffffffffu, v, 2);
+            r.krows = __shfl_sync(0xffffffffu, v, 3) - r.k0;
+            r.lk = a.k_len ? __shfl_sync(0xffffffffu, v, 4) : r.krows;
             return r;
         }
         t -= __shfl_sync(0xffffffffu, incl, 31);

@@ -49,31 +49,30 @@ __device__ __forceinline__ float2 two(const uint32_t* r) {
     return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// ---- products, issued by lane 0 of a converged warp (`on`).  A short product leaves the
-// warp a few dozen cycles, so the steps are unrolled and a step's descriptors are its tile's
-// plus a constant.
+// ---- products, issued by an elected lane.  A short product leaves it a few dozen cycles, so
+// the steps are unrolled and a step's descriptors are its tile's plus a constant.
 
 // D (+)= A B^T over `steps` (<= STEPS) K = 16 steps, both K-major in shared memory; ABLK, BBLK: bytes
 // between the operands' 64-channel blocks.
 template <int STEPS, int ABLK, int BBLK>
-__device__ __forceinline__ void mma_channels(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_channels(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                              int steps) {
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
         if (j >= steps) break;
         const uint32_t ao = ((j >> 2) * ABLK + (j & 3) * 32) >> 4, bo = ((j >> 2) * BBLK + (j & 3) * 32) >> 4;
-        mma_f16_on(on, d, a + ao, b + bo, idesc, j > 0);
+        mma_f16(d, a + ao, b + bo, idesc, j > 0);
     }
 }
 // D (+)= A B over `steps` (<= STEPS) K = 16 steps of rows, A in TMEM, B MN-major in shared memory.
 template <int STEPS>
-__device__ __forceinline__ void mma_rows(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int steps,
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int steps,
                                          uint32_t acc) {
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
         if (j >= steps) break;
-        if (j == 0) mma_f16_ta_on(on, d, a, b, idesc, acc);
-        else mma_f16_ta_on(on, d, a + 8 * j, b + j * (2048 >> 4), idesc, 1);
+        if (j == 0) mma_f16_ta(d, a, b, idesc, acc);
+        else mma_f16_ta(d, a + 8 * j, b + j * (2048 >> 4), idesc, 1);
     }
 }
 
@@ -114,23 +113,37 @@ __device__ __forceinline__ void store_cols32_f32(float* dst, const uint32_t (&ac
     }
 }
 
-// One bounded wait of a role; a wait that gives up raises the block's abort flag.
+// Bounded waits of a whole warp, which goes on or gives up together; a wait that gives
+// up (after about 2 s of the SM's cycle counter) raises the block's abort flag, and the
+// warp's later waits return at once.  Every branch is on a vote, so that the compiler knows
+// the warp to be converged and keeps what follows (descriptors, addresses, loop counts) in
+// uniform registers.
 struct Waiter {
     volatile uint32_t* abort;
     bool ok = true;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {
-        if (ok && !mbar_wait_cycles(bar, parity, abort)) {
-            ok = false;
-            *abort = 1;
+        if (!ok || __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return ok;
+        const int64_t t0 = clock64();
+        while (true) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+            if (__any_sync(0xffffffffu, *abort != 0 || clock64() - t0 > kWaitCycles)) break;
         }
-        return ok;
-    }
-    // The whole warp goes on or gives up together, converged.
-    __device__ __forceinline__ bool agree() {
-        ok = __all_sync(0xffffffffu, ok);
-        return ok;
+        *abort = 1;
+        ok = false;
+        return false;
     }
 };
+
+// Run f in one lane of a converged warp.
+template <typename F>
+__device__ __forceinline__ void one_lane(F f) {
+    if (elect_one()) f();
+    __syncwarp();
+}
+
+// The value of lane 0 in every lane, as one that the compiler knows to be uniform.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 }  // namespace attn_tc
 

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
     const uint32_t s_full = bar0 + 16, p_full = s_full + 8 * NQ, o_full = p_full + 8 * NQ, o_empty = o_full + 8 * NQ;
     const uint32_t kv_full = o_empty + 8 * NQ, kv_empty = kv_full + 8 * S, done = kv_empty + 8 * S;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kLoader = NQ * 4, kIssuer = NQ * 4 + 1;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
     tc_fence_before();
     const bool good = attn_offsets_ok(a);  // a barrier of the whole block
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = uniform(*s_tmem);
 
     const int sets = a.hq / a.gp;
     const int group = a.hq / a.hk;
@@ -133,35 +133,38 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
     };
     Waiter wait{s_abort};
 
-    const uint32_t on = lane == 0;  // the lane that carries out a role warp's copies and products
     if (warp == kLoader) {
         uint32_t it = 0, uc = 0;
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
             if (x.hi <= x.lo) continue;
             wait(q_empty, (uc & 1u) ^ 1u);
-            if (!wait.agree()) break;
+            if (!wait.ok) break;
             const int nq = x.rows > kM ? NQ : 1;
-            mbar_arrive_expect_tx_on(on, q_full, 2 * nq * C::kRowTile);
-            for (int w = 0; w < nq; ++w)
-                for (int b = 0; b < C::kBlocks; ++b) {
-                    const int row = x.t.q0 + (x.t.first + w * kM) / a.gp;
-                    const uint32_t off = w * C::kRowTile + b * kM * 128;
-                    tma_load_3d_on(on, sQ + off, &maps.q, b * 64, x.hs * a.gp, row, q_full);
-                    tma_load_3d_on(on, sG + off, &maps.go, b * 64, x.hs * a.gp, row, q_full);
-                }
+            one_lane([&] {
+                mbar_arrive_expect_tx(q_full, 2 * nq * C::kRowTile);
+                for (int w = 0; w < nq; ++w)
+                    for (int b = 0; b < C::kBlocks; ++b) {
+                        const int row = x.t.q0 + (x.t.first + w * kM) / a.gp;
+                        const uint32_t off = w * C::kRowTile + b * kM * 128;
+                        tma_load_3d(sQ + off, &maps.q, b * 64, x.hs * a.gp, row, q_full);
+                        tma_load_3d(sG + off, &maps.go, b * 64, x.hs * a.gp, row, q_full);
+                    }
+            });
             ++uc;
             const int kh = x.hs * a.gp / group;
             for (int e = x.lo; e < x.hi; ++e, ++it) {
                 const uint32_t st = it % S;
                 wait(kv_empty + 8 * st, ((it / S) & 1u) ^ 1u);
-                if (!wait.agree()) break;
-                mbar_arrive_expect_tx_on(on, kv_full + 8 * st, 2 * C::kKeyTile);
-                for (int b = 0; b < C::kBlocks; ++b) {
-                    const uint32_t dst = sKV + 2 * st * C::kKeyTile + b * kN * 128;
-                    tma_load_3d_on(on, dst, &maps.k, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
-                    tma_load_3d_on(on, dst + C::kKeyTile, &maps.v, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
-                }
+                if (!wait.ok) break;
+                one_lane([&] {
+                    mbar_arrive_expect_tx(kv_full + 8 * st, 2 * C::kKeyTile);
+                    for (int b = 0; b < C::kBlocks; ++b) {
+                        const uint32_t dst = sKV + 2 * st * C::kKeyTile + b * kN * 128;
+                        tma_load_3d(dst, &maps.k, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
+                        tma_load_3d(dst + C::kKeyTile, &maps.v, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
+                    }
+                });
             }
         }
         // every copy has landed before the block may exit
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
             const uint32_t last = it - 1 - i;
             if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
-        if (!wait.agree() && lane == 0) atomicOr(a.err, kErrTimeout);
+        if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;
         const uint32_t idesc_o = idesc_f16_bn(BF16, ksteps * 16);
@@ -178,11 +181,11 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
         auto scores = [&](int w, uint32_t st, int n) {  // S_w = Q_w K^T and dP_w = dO_w V^T
             const uint32_t id = idesc_f16(BF16, n), d = tmem + w * 2 * kN;
             const uint32_t k = sKV + 2 * st * C::kKeyTile;
-            mma_channels<DP / 16, kM * 128, kN * 128>(on, d, sw128_kmajor_desc(sQ + w * C::kRowTile),
+            mma_channels<DP / 16, kM * 128, kN * 128>(d, sw128_kmajor_desc(sQ + w * C::kRowTile),
                                                       sw128_kmajor_desc(k), id, ksteps);
-            mma_channels<DP / 16, kM * 128, kN * 128>(on, d + kN, sw128_kmajor_desc(sG + w * C::kRowTile),
+            mma_channels<DP / 16, kM * 128, kN * 128>(d + kN, sw128_kmajor_desc(sG + w * C::kRowTile),
                                                       sw128_kmajor_desc(k + C::kKeyTile), id, ksteps);
-            mma_commit_on(on, s_full + 8 * w);
+            mma_commit(s_full + 8 * w);
         };
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
             // K rows past the sample's keys may hold anything, and 0 x them must be 0 in dS K
             auto arrive = [&](int e, uint32_t i) {
                 wait(kv_full + 8 * (i % S), (i / S) & 1u);
-                if (wait.agree() && padded(e) != left(e)) {
+                if (wait.ok && padded(e) != left(e)) {
                     zero_rows(sKV + 2 * (i % S) * C::kKeyTile, left(e), padded(e), C::kBlocks, kN * 128);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -201,10 +204,12 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
             };
             wait(q_full, uc & 1u);
             arrive(x.lo, it);
-            if (!wait.agree()) break;
+            if (!wait.ok) break;
             tc_fence_after();
-            for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
-            if (x.hi - x.lo == 1) mma_commit_on(on, q_empty);
+            one_lane([&] {
+                for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
+                if (x.hi - x.lo == 1) mma_commit(q_empty);
+            });
             for (int e = x.lo; e < x.hi; ++e, ++it) {
                 const uint32_t st = it % S, nx = (it + 1) % S;
                 const bool more = e + 1 < x.hi;
@@ -213,28 +218,29 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
                 for (int w = 0; w < nq; ++w) {
                     wait(p_full + 8 * w, pc[w]++ & 1u);
                     if (e == x.lo) wait(o_empty + 8 * w, (oc[w] & 1u) ^ 1u);
-                    if (!wait.agree()) break;
+                    if (!wait.ok) break;
                     tc_fence_after();
-                    mma_rows<kN / 16>(on, tmem + C::kOCol + w * DP, tmem + w * 2 * kN,
-                                      sw128_mnmajor_desc(sKV + 2 * st * C::kKeyTile, kN * 128), idesc_o, n16 / 16,
-                                      e > x.lo);
-                    if (more) {
-                        scores(w, nx, padded(e + 1));
-                    } else {
-                        mma_commit_on(on, o_full + 8 * w);
-                        ++oc[w];
-                    }
+                    one_lane([&] {
+                        mma_rows<kN / 16>(tmem + C::kOCol + w * DP, tmem + w * 2 * kN,
+                                          sw128_mnmajor_desc(sKV + 2 * st * C::kKeyTile, kN * 128), idesc_o, n16 / 16,
+                                          e > x.lo);
+                        if (more) scores(w, nx, padded(e + 1));
+                        else mma_commit(o_full + 8 * w);
+                        if (w + 1 == nq) {
+                            mma_commit(kv_empty + 8 * st);
+                            if (e + 2 == x.hi) mma_commit(q_empty);
+                        }
+                    });
+                    if (!more) ++oc[w];
                 }
                 if (!wait.ok) break;
-                mma_commit_on(on, kv_empty + 8 * st);
-                if (e + 2 == x.hi) mma_commit_on(on, q_empty);
             }
             ++uc;
         }
         // every product has finished before TMEM is released
-        mma_commit_on(on, done);
+        one_lane([&] { mma_commit(done); });
         if (!mbar_wait_timed(done, 0)) wait.ok = false;
-        if (!wait.agree() && lane == 0) {
+        if (!wait.ok && lane == 0) {
             *s_abort = 1;
             atomicOr(a.err, kErrTimeout);
         }
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
             const float2 lift2 = make_float2(lift.x, lift.x), delta2 = make_float2(-delta, -delta);
             for (int e = x.lo; e < x.hi; ++e) {
                 wait(s_full + 8 * w, sc & 1u);
-                if (!wait.agree()) break;
+                if (!wait.ok) break;
                 ++sc;
                 tc_fence_after();
                 if (any) {
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
             }
             if (x.hi > x.lo) {
                 wait(o_full + 8 * w, oc & 1u);
-                if (!wait.agree()) break;
+                if (!wait.ok) break;
                 ++oc;
                 tc_fence_after();
             }
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     const uint32_t o_full = bar0 + 48, o_empty = bar0 + 56, r_full = bar0 + 64, r_empty = r_full + 8 * S;
     const uint32_t done = r_empty + 8 * S;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kLoader = 8, kIssuer = 9;
     if (threadIdx.x == 0) {
         mbar_init(k_full, 1);
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     tc_fence_before();
     const bool good = attn_offsets_ok(a);  // a barrier of the whole block
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = uniform(*s_tmem);
 
     const int sets_per_key = a.hq / a.hk / a.gp;  // head sets that read a key head
     const int64_t units = good ? (int64_t)tiles * a.hk * a.splits : 0;
@@ -426,32 +432,35 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     };
     Waiter wait{s_abort};
 
-    const uint32_t on = lane == 0;  // the lane that carries out a role warp's copies and products
     if (warp == kLoader) {
         uint32_t it = 0, uc = 0;
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
             if (x.steps == 0) continue;
             wait(k_empty, (uc & 1u) ^ 1u);
-            if (!wait.agree()) break;
-            mbar_arrive_expect_tx_on(on, k_full, 2 * C::kKeyTile);
-            for (int b = 0; b < C::kBlocks; ++b) {
-                tma_load_3d_on(on, sK + b * kM * 128, &maps.k, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
-                tma_load_3d_on(on, sV + b * kM * 128, &maps.v, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
-            }
+            if (!wait.ok) break;
+            one_lane([&] {
+                mbar_arrive_expect_tx(k_full, 2 * C::kKeyTile);
+                for (int b = 0; b < C::kBlocks; ++b) {
+                    tma_load_3d(sK + b * kM * 128, &maps.k, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
+                    tma_load_3d(sV + b * kM * 128, &maps.v, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
+                }
+            });
             ++uc;
             for (int hs = 0; hs < sets_per_key && wait.ok; ++hs)
                 for (int e = x.lo; e < x.hi; ++e, ++it) {
                     const uint32_t st = it % S;
                     wait(r_empty + 8 * st, ((it / S) & 1u) ^ 1u);
-                    if (!wait.agree()) break;
-                    mbar_arrive_expect_tx_on(on, r_full + 8 * st, 2 * C::kRowTile);
+                    if (!wait.ok) break;
                     const int head = (x.kh * sets_per_key + hs) * a.gp, row = x.t.q0 + e * kN / a.gp;
-                    for (int b = 0; b < C::kBlocks; ++b) {
-                        const uint32_t dst = sQG + 2 * st * C::kRowTile + b * kN * 128;
-                        tma_load_3d_on(on, dst, &maps.q, b * 64, head, row, r_full + 8 * st);
-                        tma_load_3d_on(on, dst + C::kRowTile, &maps.go, b * 64, head, row, r_full + 8 * st);
-                    }
+                    one_lane([&] {
+                        mbar_arrive_expect_tx(r_full + 8 * st, 2 * C::kRowTile);
+                        for (int b = 0; b < C::kBlocks; ++b) {
+                            const uint32_t dst = sQG + 2 * st * C::kRowTile + b * kN * 128;
+                            tma_load_3d(dst, &maps.q, b * 64, head, row, r_full + 8 * st);
+                            tma_load_3d(dst + C::kRowTile, &maps.go, b * 64, head, row, r_full + 8 * st);
+                        }
+                    });
                 }
         }
         // every copy has landed before the block may exit
@@ -460,7 +469,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             const uint32_t last = it - 1 - i;
             if (!mbar_wait_timed(r_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
-        if (!wait.agree() && lane == 0) atomicOr(a.err, kErrTimeout);
+        if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;
         const uint32_t idesc_o = idesc_f16_bn(BF16, ksteps * 16);
@@ -469,10 +478,10 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         auto scores = [&](uint32_t i, int n) {  // S^T = K Q^T and dP^T = V dO^T of step i
             const uint32_t id = idesc_f16(BF16, n), st = i % S, w = i & 1u, d = tmem + w * 2 * kN;
             const uint32_t q = sQG + 2 * st * C::kRowTile;
-            mma_channels<DP / 16, kM * 128, kN * 128>(on, d, sw128_kmajor_desc(sK), sw128_kmajor_desc(q), id, ksteps);
-            mma_channels<DP / 16, kM * 128, kN * 128>(on, d + kN, sw128_kmajor_desc(sV),
+            mma_channels<DP / 16, kM * 128, kN * 128>(d, sw128_kmajor_desc(sK), sw128_kmajor_desc(q), id, ksteps);
+            mma_channels<DP / 16, kM * 128, kN * 128>(d + kN, sw128_kmajor_desc(sV),
                                                       sw128_kmajor_desc(q + C::kRowTile), id, ksteps);
-            mma_commit_on(on, s_full + 8 * w);
+            mma_commit(s_full + 8 * w);
         };
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             // the last rows of a step may be the next sample's, and 0 x them must be 0 in dS^T Q and P^T dO
             auto arrive = [&](int i, uint32_t n) {
                 wait(r_full + 8 * (n % S), (n / S) & 1u);
-                if (wait.agree() && padded(i) != left(i)) {
+                if (wait.ok && padded(i) != left(i)) {
                     const uint32_t q = sQG + 2 * (n % S) * C::kRowTile;
                     zero_rows(q, left(i), padded(i), C::kBlocks, kN * 128);
                     zero_rows(q + C::kRowTile, left(i), padded(i), C::kBlocks, kN * 128);
@@ -496,10 +505,12 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                 arrive(i, it + i);
                 if (!wait.ok) break;
                 tc_fence_after();
-                scores(it + i, padded(i));
+                one_lane([&] {
+                    scores(it + i, padded(i));
+                    if (x.steps <= 2 && i + 1 == x.steps) mma_commit(k_empty);
+                });
             }
-            if (!wait.agree()) break;
-            if (x.steps <= 2) mma_commit_on(on, k_empty);
+            if (!wait.ok) break;
             wait(o_empty, (uc & 1u) ^ 1u);
             for (int i = 0; i < x.steps; ++i, ++it) {
                 const uint32_t st = it % S, w = it & 1u;
@@ -507,23 +518,25 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                 const int n16 = padded(i);
                 if (i + 2 < x.steps) arrive(i + 2, it + 2);
                 wait(p_full + 8 * w, pc[w]++ & 1u);
-                if (!wait.agree()) break;
+                if (!wait.ok) break;
                 tc_fence_after();
                 const uint32_t pt = tmem + w * 2 * kN;
-                mma_rows<kN / 16>(on, tmem + C::kVCol, pt, sw128_mnmajor_desc(g, kN * 128), idesc_o, n16 / 16, i > 0);
-                mma_rows<kN / 16>(on, tmem + C::kKCol, pt + kN, sw128_mnmajor_desc(q, kN * 128), idesc_o, n16 / 16,
-                                  i > 0);
-                mma_commit_on(on, r_empty + 8 * st);
-                if (i + 2 < x.steps) scores(it + 2, padded(i + 2));
-                if (i + 3 == x.steps) mma_commit_on(on, k_empty);
-                if (i + 1 == x.steps) mma_commit_on(on, o_full);
+                one_lane([&] {
+                    mma_rows<kN / 16>(tmem + C::kVCol, pt, sw128_mnmajor_desc(g, kN * 128), idesc_o, n16 / 16, i > 0);
+                    mma_rows<kN / 16>(tmem + C::kKCol, pt + kN, sw128_mnmajor_desc(q, kN * 128), idesc_o, n16 / 16,
+                                      i > 0);
+                    mma_commit(r_empty + 8 * st);
+                    if (i + 2 < x.steps) scores(it + 2, padded(i + 2));
+                    if (i + 3 == x.steps) mma_commit(k_empty);
+                    if (i + 1 == x.steps) mma_commit(o_full);
+                });
             }
             ++uc;
         }
         // every product has finished before TMEM is released
-        mma_commit_on(on, done);
+        one_lane([&] { mma_commit(done); });
         if (!mbar_wait_timed(done, 0)) wait.ok = false;
-        if (!wait.agree() && lane == 0) {
+        if (!wait.ok && lane == 0) {
             *s_abort = 1;
             atomicOr(a.err, kErrTimeout);
         }
@@ -559,7 +572,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                 next0 = stat(i + 2, 0);
                 next1 = stat(i + 2, 32);
                 wait(s_full + 8 * w, sc & 1u);
-                if (!wait.agree()) break;
+                if (!wait.ok) break;
                 ++sc;
                 tc_fence_after();
                 const int left = rows - (x.lo + i % per) * kN;
@@ -595,7 +608,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             it += x.steps;
             if (x.steps > 0) {
                 wait(o_full, uc & 1u);
-                if (!wait.agree()) break;
+                if (!wait.ok) break;
                 ++uc;
                 tc_fence_after();
             }

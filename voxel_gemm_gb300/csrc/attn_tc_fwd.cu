@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     const uint32_t s_full = bar0 + 16, p_full = s_full + 8 * NQ, o_full = p_full + 8 * NQ, o_empty = o_full + 8 * NQ;
     const uint32_t kv_full = o_empty + 8 * NQ, kv_empty = kv_full + 8 * S, done = kv_empty + 8 * S;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kLoader = NQ * 4, kIssuer = NQ * 4 + 1;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     tc_fence_before();
     const bool good = attn_offsets_ok(a);  // a barrier of the whole block
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = uniform(*s_tmem);
 
     const int sets = a.hq / a.gp;
     const int group = a.hq / a.hk;
@@ -121,31 +121,34 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
     Waiter wait{s_abort};
     // the block was launched with 168 registers a thread (NQ = 1: 128); the softmax warps,
     // which hold a row of scores each, take what the last warpgroup leaves
-    if (warp >= kLoader) reg_shrink<NQ == 2 ? 72 : 56>();
-    const uint32_t on = lane == 0;  // the lane that carries out a role warp's copies and products
+    if (warp >= kLoader) reg_shrink<NQ == 2 ? 88 : 72>();
     if (warp == kLoader) {
         uint32_t it = 0, uc = 0;
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
             if (x.hi <= x.lo) continue;
             wait(q_empty, (uc & 1u) ^ 1u);
-            if (!wait.agree()) break;
+            if (!wait.ok) break;
             const int nq = x.rows > kM ? NQ : 1;
-            mbar_arrive_expect_tx_on(on, q_full, nq * C::kTile);
-            for (int w = 0; w < nq; ++w)
-                for (int b = 0; b < C::kBlocks; ++b)
-                    tma_load_3d_on(on, sQ + w * C::kTile + b * kM * 128, &maps.q, b * 64, x.hs * a.gp,
-                                   x.t.q0 + (x.t.first + w * kM) / a.gp, q_full);
+            one_lane([&] {
+                mbar_arrive_expect_tx(q_full, nq * C::kTile);
+                for (int w = 0; w < nq; ++w)
+                    for (int b = 0; b < C::kBlocks; ++b)
+                        tma_load_3d(sQ + w * C::kTile + b * kM * 128, &maps.q, b * 64, x.hs * a.gp,
+                                    x.t.q0 + (x.t.first + w * kM) / a.gp, q_full);
+            });
             ++uc;
             const int kh = x.hs * a.gp / group;
             for (int e = 2 * x.lo; e < 2 * x.hi; ++e, ++it) {  // K and V tiles in turn
                 const uint32_t st = it % S;
                 wait(kv_empty + 8 * st, ((it / S) & 1u) ^ 1u);
-                if (!wait.agree()) break;
-                mbar_arrive_expect_tx_on(on, kv_full + 8 * st, C::kTile);
-                for (int b = 0; b < C::kBlocks; ++b)
-                    tma_load_3d_on(on, sKV + st * C::kTile + b * kN * 128, e & 1 ? &maps.v : &maps.k, b * 64, kh,
-                                   x.t.k0 + (e >> 1) * kN, kv_full + 8 * st);
+                if (!wait.ok) break;
+                one_lane([&] {
+                    mbar_arrive_expect_tx(kv_full + 8 * st, C::kTile);
+                    for (int b = 0; b < C::kBlocks; ++b)
+                        tma_load_3d(sKV + st * C::kTile + b * kN * 128, e & 1 ? &maps.v : &maps.k, b * 64, kh,
+                                    x.t.k0 + (e >> 1) * kN, kv_full + 8 * st);
+                });
             }
         }
         // every copy has landed before the block may exit
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
             const uint32_t last = it - 1 - i;
             if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
-        if (!wait.agree() && lane == 0) atomicOr(a.err, kErrTimeout);
+        if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;          // K = 16 steps over the channels
         const int o_cols = ksteps * 16;              // columns of O
@@ -162,10 +165,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
         uint32_t it = 0, uc = 0, pc[NQ] = {}, oc[NQ] = {};
         // S_w = Q_w K^T of the tile in stage st, `n` keys
         auto scores = [&](int w, uint32_t st, int n) {
-            mma_channels<DP / 16, kM * 128, kN * 128>(on, tmem + w * kN, sw128_kmajor_desc(sQ + w * C::kTile),
+            mma_channels<DP / 16, kM * 128, kN * 128>(tmem + w * kN, sw128_kmajor_desc(sQ + w * C::kTile),
                                                       sw128_kmajor_desc(sKV + st * C::kTile), idesc_f16(BF16, n),
                                                       ksteps);
-            mma_commit_on(on, s_full + 8 * w);
+            mma_commit(s_full + 8 * w);
         };
         for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
             const Unit x = find(u);
@@ -175,11 +178,13 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
             auto padded = [&](int e) { return (left(e) + 15) / 16 * 16; };
             wait(q_full, uc & 1u);
             wait(kv_full + 8 * (it % S), (it / S) & 1u);
-            if (!wait.agree()) break;
+            if (!wait.ok) break;
             tc_fence_after();
-            for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
-            mma_commit_on(on, kv_empty + 8 * (it % S));
-            if (x.hi - x.lo == 1) mma_commit_on(on, q_empty);
+            one_lane([&] {
+                for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
+                mma_commit(kv_empty + 8 * (it % S));
+                if (x.hi - x.lo == 1) mma_commit(q_empty);
+            });
             ++it;
             for (int e = x.lo; e < x.hi; ++e) {
                 const uint32_t sv = it % S, pv = (it / S) & 1u;
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
                 const bool more = e + 1 < x.hi;
                 wait(kv_full + 8 * sv, pv);
                 if (more) wait(kv_full + 8 * sk, pk);
-                if (!wait.agree()) break;
+                if (!wait.ok) break;
                 const int n16 = padded(e);
                 if (n16 != left(e)) {  // V rows past the sample's keys may hold anything: 0 x them must be 0
                     zero_rows(sKV + sv * C::kTile, left(e), n16, C::kBlocks, kN * 128);
@@ -197,34 +202,36 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
                 for (int w = 0; w < nq; ++w) {
                     wait(p_full + 8 * w, pc[w]++ & 1u);
                     if (e == x.lo) wait(o_empty + 8 * w, (oc[w] & 1u) ^ 1u);
-                    if (!wait.agree()) break;
+                    if (!wait.ok) break;
                     tc_fence_after();
-                    mma_rows<kN / 16>(on, tmem + C::kOCol + w * DP, tmem + w * kN,
-                                      sw128_mnmajor_desc(sKV + sv * C::kTile, kN * 128), idesc_o, n16 / 16, e > x.lo);
-                    if (more) {
-                        scores(w, sk, padded(e + 1));
-                    } else {
-                        mma_commit_on(on, o_full + 8 * w);
-                        ++oc[w];
-                    }
+                    one_lane([&] {
+                        mma_rows<kN / 16>(tmem + C::kOCol + w * DP, tmem + w * kN,
+                                          sw128_mnmajor_desc(sKV + sv * C::kTile, kN * 128), idesc_o, n16 / 16,
+                                          e > x.lo);
+                        if (more) scores(w, sk, padded(e + 1));
+                        else mma_commit(o_full + 8 * w);
+                        if (w + 1 == nq) {
+                            mma_commit(kv_empty + 8 * sv);
+                            if (more) mma_commit(kv_empty + 8 * sk);
+                            if (e + 2 == x.hi) mma_commit(q_empty);
+                        }
+                    });
+                    if (!more) ++oc[w];
                 }
                 if (!wait.ok) break;
-                mma_commit_on(on, kv_empty + 8 * sv);
-                if (more) mma_commit_on(on, kv_empty + 8 * sk);
-                if (e + 2 == x.hi) mma_commit_on(on, q_empty);
                 it += more ? 2 : 1;
             }
             ++uc;
         }
         // every product has finished before TMEM is released
-        mma_commit_on(on, done);
+        one_lane([&] { mma_commit(done); });
         if (!mbar_wait_timed(done, 0)) wait.ok = false;
-        if (!wait.agree() && lane == 0) {
+        if (!wait.ok && lane == 0) {
             *s_abort = 1;
             atomicOr(a.err, kErrTimeout);
         }
     } else if (warp < kLoader) {
-        reg_grow<NQ == 2 ? 216 : 200>();
+        reg_grow<NQ == 2 ? 208 : 184>();
         const int w = warp >> 2, quad = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t t_s = t_lane + w * kN, t_o = t_lane + C::kOCol + w * DP;
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
             float m = -INFINITY, l = 0.f;
             for (int e = x.lo; e < x.hi; ++e) {
                 wait(s_full + 8 * w, sc & 1u);
-                if (!wait.agree()) break;
+                if (!wait.ok) break;
                 ++sc;
                 tc_fence_after();
                 if (any) {
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, NQ == 1 ? 2 : 1)
             }
             if (x.hi > x.lo) {
                 wait(o_full + 8 * w, oc & 1u);
-                if (!wait.agree()) break;
+                if (!wait.ok) break;
                 ++oc;
                 tc_fence_after();
             }

@@ -56,19 +56,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const v
     }
 }
 
-// The same with the SM's own cycle counter for the limit (about 2 s): reading it costs a
-// few cycles where the global timer costs hundreds, which is what a wait on the critical
-// path of a step would lose.
-constexpr int64_t kWaitCycles = 4000000000ll;
-__device__ __forceinline__ bool mbar_wait_cycles(uint32_t bar, uint32_t parity, const volatile uint32_t* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const int64_t t0 = clock64();
-    while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (clock64() - t0 > kWaitCycles) return false;
-    }
-}
+constexpr int64_t kWaitCycles = 4000000000ll;  // about 2 s of an SM's cycle counter
 
 // Time-bounded wait that ignores the abort flag (used to drain in-flight work).
 __device__ __forceinline__ bool mbar_wait_timed(uint32_t bar, uint32_t parity) {
@@ -273,58 +261,36 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// The forms below are run by a whole converged warp and carried out by the lanes with
-// `on` set (one lane).  These instructions take descriptors, addresses and coordinates
-// from the warp's uniform registers, one set for all 32 lanes, so the other lanes must not run on
-// while one lane issues: the warp stays together and the instruction alone is predicated.
-__device__ __forceinline__ void mma_f16_on(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// D[tmem] (+)= A[tmem] * B[smem]^T, 16-bit inputs, fp32 accumulate.  A row lies in the
+// TMEM lane of its number, two consecutive K values to a 32-bit column (8 columns per K = 16).
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
-        : "memory");
-}
-// A in TMEM: a row lies in the lane of its number, two consecutive K values to a 32-bit
-// column (8 columns per K = 16).
-__device__ __forceinline__ void mma_f16_ta_on(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                              uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
-        : "memory");
-}
-__device__ __forceinline__ void mma_commit_on(uint32_t on, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-        "r"(on)
-        : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect_tx_on(uint32_t on, uint32_t bar, uint32_t bytes) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %2, 0;\n\t"
-        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
-        "r"(bytes), "r"(on)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // Box of a 3-D tensor map (TMA engine) into shared memory, completing on an mbarrier transaction count.
-__device__ __forceinline__ void tma_load_3d_on(uint32_t on, uint32_t dst, const void* map, int x, int y, int z,
-                                               uint32_t bar) {
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %6, 0;\n\t"
-        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];\n\t}" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(on)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+// One lane of a converged warp, the same at every call.  tcgen05.mma and the copies take
+// descriptors, addresses and coordinates from the warp's uniform registers, one set for
+// all 32 lanes: the other lanes must not run on while one issues, so a warp that issues runs
+// its control flow in all lanes, puts each batch into `if (elect_one()) { ... }` and a
+// __syncwarp() behind it.  (Measured, M = 128, K = 16, clk per product: 64 / 48 / 32 for
+// N = 128 / N = 64 / N = 64 with A in TMEM, the hardware's rates; 71 to 101 with the
+// instruction predicated on a lane instead.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void prefetch_map(const void* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
