@@ -134,6 +134,18 @@ struct Waiter {
     }
 };
 
+// Named barrier of `threads` threads, and the same with an or over their predicates.
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
 // Run f in one lane of a converged warp.
 template <typename F>
 __device__ __forceinline__ void one_lane(F f) {
