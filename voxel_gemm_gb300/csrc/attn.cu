@@ -26,16 +26,30 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
     }
 }
 
-// Whether key row j is one of its sample's valid rows.
-__device__ __forceinline__ bool valid_key(const AttnArgs& a, int64_t j) {
-    if (!a.k_len) return true;
+// The sample that holds row j.
+__device__ __forceinline__ int sample_of(const AttnArgs& a, const int32_t* off, int64_t j) {
     int lo = 0, hi = a.batch;  // the last sample that does not start past j
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.k_off[mid] <= j) lo = mid;
+        if (off[mid] <= j) lo = mid;
         else hi = mid;
     }
-    return j - a.k_off[lo] < a.k_len[lo];
+    return lo;
+}
+
+// Whether key row j is one of its sample's valid rows.
+__device__ __forceinline__ bool valid_key(const AttnArgs& a, int64_t j) {
+    if (!a.k_len) return true;
+    const int b = sample_of(a, a.k_off, j);
+    return j - a.k_off[b] < a.k_len[b];
+}
+
+// Parts that the results of query row (kKeys: key row) j lie in.
+template <bool kKeys>
+__device__ __forceinline__ int parts_of(const AttnArgs& a, int64_t j) {
+    const int b = sample_of(a, kKeys ? a.k_off : a.q_off, j);
+    if (kKeys) return attn_parts(a, (int64_t)(a.q_off[b + 1] - a.q_off[b]) * a.gp);
+    return attn_parts(a, a.k_len ? a.k_len[b] : a.k_off[b + 1] - a.k_off[b]);
 }
 
 // Largest value of the block into *word, as the bits of a non-negative float (their
@@ -108,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int l
     }
 }
 
-// The splits' outputs, each normalised by its own sum, weighed by exp(lse_s - max lse).
+// The parts' outputs, each normalised by its own sum, weighed by exp(lse_s - max lse).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_attn_join_out(const AttnArgs a) {
     if (!attn_offsets_ok(a)) return;
@@ -121,15 +135,16 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_out(const AttnArgs a) {
     const int h = (int)(r - i * a.hq);
     const float* lse = a.part_lse + (int64_t)h * a.n_q + i;
     const int64_t lstep = (int64_t)a.hq * a.n_q;
+    const int parts = parts_of<false>(a, i);
     float top = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) top = fmaxf(top, lse[s * lstep]);
+    for (int s = 0; s < parts; ++s) top = fmaxf(top, lse[s * lstep]);
     const float base = top == -INFINITY ? 0.f : top;
     const float* src = a.part + r * a.d + c;
     const int64_t step = a.n_q * a.hq * a.d;
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
+    for (int s = 0; s < parts; ++s) {
         const float w = expf(lse[s * lstep] - base);
         const float4 v = *reinterpret_cast<const float4*>(src + s * step);
         sum += w;
@@ -149,24 +164,26 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_out(const AttnArgs a) {
     if (c == 0 && a.lse) a.lse[(int64_t)h * a.n_q + i] = base + logf(sum);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_attn_join_sum(const AttnArgs a, const float* part, int splits,
-                                                            int64_t rows, int heads, vg_heads dst) {
+template <typename T, bool kKeys>
+__global__ void __launch_bounds__(kThreads) k_attn_join_sum(const AttnArgs a, const float* part, vg_heads dst) {
     if (!attn_offsets_ok(a)) return;
     const int q4 = a.d / 4;
+    const int64_t rows = kKeys ? a.n_k : a.n_q;
+    const int heads = kKeys ? a.hk : a.hq;
     const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (e >= rows * heads * q4) return;
     const int64_t r = e / q4;
     const int c = (int)(e - r * q4) * 4;
+    const int64_t i = r / heads;
+    const int parts = parts_of<kKeys>(a, i);
     const float* src = part + r * a.d + c;
     const int64_t step = rows * heads * a.d;
     float4 acc = *reinterpret_cast<const float4*>(src);
 #pragma unroll 4
-    for (int s = 1; s < splits; ++s) {
+    for (int s = 1; s < parts; ++s) {
         const float4 v = *reinterpret_cast<const float4*>(src + s * step);
         acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
     }
-    const int64_t i = r / heads;
     T* o = head_row<T>(dst, i, (int)(r - i * heads)) + c;
     o[0] = from_f32<T>(acc.x);
     o[1] = from_f32<T>(acc.y);
@@ -190,41 +207,51 @@ int join_out(const AttnArgs& a, cudaStream_t s) {
     k_attn_join_out<T><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
     return launched();
 }
-template <typename T>
-int join_sum(const AttnArgs& a, const float* part, int splits, int64_t rows, int heads, const vg_heads& dst,
-             cudaStream_t s) {
-    const int64_t n = rows * heads * (a.d / 4);
+template <typename T, bool kKeys>
+int join_rows(const AttnArgs& a, const float* part, const vg_heads& dst, cudaStream_t s) {
+    const int64_t n = (kKeys ? a.n_k * a.hk : a.n_q * a.hq) * (a.d / 4);
     const unsigned blocks = (unsigned)((n + kThreads - 1) / kThreads);
-    k_attn_join_sum<T><<<blocks, kThreads, 0, s>>>(a, part, splits, rows, heads, dst);
+    k_attn_join_sum<T, kKeys><<<blocks, kThreads, 0, s>>>(a, part, dst);
     return launched();
+}
+template <typename T>
+int join_queries(const AttnArgs& a, const float* part, const vg_heads& dst, cudaStream_t s) {
+    return join_rows<T, false>(a, part, dst, s);
+}
+template <typename T>
+int join_keys(const AttnArgs& a, const float* part, const vg_heads& dst, cudaStream_t s) {
+    return join_rows<T, true>(a, part, dst, s);
 }
 
 #define VG_BY_TYPE(f, ...)                                \
     (dtype == VG_F32 ? f<float>(__VA_ARGS__)              \
      : dtype == VG_F16 ? f<__half>(__VA_ARGS__) : f<__nv_bfloat16>(__VA_ARGS__))
 
-// Parts to cut an axis of `tiles` tiles into, when there are `units` independent
-// tiles of work along the other one and `slots` of them run at a time: as many as
-// fill the slots once, but at least four tiles in a part.
-int parts(int64_t units, int64_t tiles, int slots) {
-    if (units <= 0) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({slots / units, tiles / 4, 256}));
-}
-
-// The same for units that may already fill the slots: cut on, up to eight parts, while
-// that evens out the last wave (a wave's idle slots cost more than the parts' fp32 sums).
-int balanced(int64_t units, int64_t tiles, int slots) {
-    const int first = parts(units, tiles, slots);
-    if (units <= 0) return 1;
-    int best = first;
-    double best_fill = 0.0;
-    for (int s = first; s <= std::max(first, 8) && (s == first || tiles / s >= 4); ++s) {
-        const int64_t n = units * s, waves = (n + slots - 1) / slots;
-        const double fill = (double)n / (double)(waves * slots);
-        if (fill > best_fill + 0.03) best = s, best_fill = fill;
-        if (best_fill > 0.93) break;
+// How to cut an axis of `tiles` tiles in all (every sample's together) when there are
+// `units` independent tiles of work along the other one, in `batch` samples, and `slots` run at a time.
+// Parts have one size for all samples, so that a call with one long sample and short ones is even
+// too.  Not cut when the units fill the slots (or, with `fill`, when cutting evens out the last
+// wave by less than the parts' fp32 results cost); a part has at least four tiles.
+struct Cut { int parts, per; };
+Cut cut_axis(int64_t units, int64_t tiles, int batch, int slots, bool fill) {
+    if (units <= 0 || tiles <= 0) return {1, 0};
+    int64_t want = slots / units;
+    if (fill) {
+        double best = 0.0;
+        for (int64_t s = std::max<int64_t>(1, want), end = std::max<int64_t>(8, s); s <= end; ++s) {
+            const int64_t n = units * s, waves = (n + slots - 1) / slots;
+            const double full = (double)n / (double)(waves * slots);
+            if (full > best + 0.03) want = s, best = full;
+            if (best > 0.93) break;
+        }
     }
-    return best;
+    if (want <= 1) return {1, 0};
+    // `want` parts of a sample of average length; a sample that holds all rows has batch times as many, of
+    // which the scratch takes up to four times the average
+    const int64_t most = std::min<int64_t>(want * std::min(batch, 4), 1024);
+    const int64_t per = std::max<int64_t>({4, (tiles + want * batch - 1) / (want * batch), (tiles + most - 1) / most});
+    const int64_t parts = (tiles + per - 1) / per;
+    return parts <= 1 ? Cut{1, 0} : Cut{(int)parts, (int)per};
 }
 
 }  // namespace
@@ -239,18 +266,27 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
     p.tc = c.dtype != VG_F32;
     const int group = c.hq / c.hk;
     if (p.tc && group <= 16 && !(group & (group - 1)) && c.n_q * group < (int64_t(1) << 31)) p.gp = group;
+    const auto tiles = [](int64_t rows, int tile) { return (rows + tile - 1) / tile; };
     const int64_t qt = attn_max_tiles(c.n_q, c.batch, 1, 64), kt = attn_max_tiles(c.n_k, c.batch, 1, 64);
-    p.s_dq = parts(qt * c.hq, kt / c.batch, 2 * p.sms);
-    p.s_dkv = parts(kt * c.hk, qt / c.batch, 2 * p.sms);
-    p.s_fwd = p.s_dq;
+    Cut f, q, k;
     if (p.tc) {
         const int sets = c.hq / p.gp;
         p.nq = attn_max_tiles(c.n_q, c.batch, p.gp, 256) * sets >= p.sms ? 2 : 1;
         const int64_t units = attn_max_tiles(c.n_q, c.batch, p.gp, 128 * p.nq) * sets;
-        p.s_fwd = parts(units, c.n_k / c.batch / 128, p.nq == 1 ? 2 * p.sms : p.sms);
-        p.s_dq = parts(units, c.n_k / c.batch / 64, p.nq == 1 && c.d <= 64 ? 2 * p.sms : p.sms);
-        p.s_dkv = balanced(attn_max_tiles(c.n_k, c.batch, 1, 128) * c.hk, c.n_q * p.gp / c.batch / 64, p.sms);
+        const int slots = p.nq == 1 && c.d <= 64 ? 2 * p.sms : p.sms;
+        f = cut_axis(units, tiles(c.n_k, 128), c.batch, slots, false);
+        q = cut_axis(units, tiles(c.n_k, 64), c.batch, slots, false);
+        k = cut_axis(attn_max_tiles(c.n_k, c.batch, 1, 128) * c.hk, tiles(c.n_q * p.gp, 64), c.batch, p.sms, true);
+    } else {
+        f = q = cut_axis(qt * c.hq, tiles(c.n_k, 64), c.batch, 2 * p.sms, false);
+        k = cut_axis(kt * c.hk, tiles(c.n_q, 64), c.batch, 2 * p.sms, false);
     }
+    p.s_fwd = f.parts;
+    p.per_fwd = f.per;
+    p.s_dq = q.parts;
+    p.per_dq = q.per;
+    p.s_dkv = k.parts;
+    p.per_dkv = k.per;
     const size_t vq = (size_t)c.n_q * c.hq, vk = (size_t)c.n_k * c.hk;
     size_t fwd = 0, bwd = 0;
     if (p.s_fwd > 1) {
@@ -276,8 +312,11 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
 int attn_fwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s) {
     if (a.n_q == 0) return VG_OK;
     a.gp = p.gp;
+    a.gp_log2 = __builtin_ctz((unsigned)p.gp);
     a.err = reinterpret_cast<uint32_t*>(ws);
     a.splits = p.s_fwd;
+    a.per_part = p.per_fwd;
+    a.tile = p.tc ? 128 : 64;
     a.part = reinterpret_cast<float*>(ws + 256);
     a.part_lse = reinterpret_cast<float*>(ws + p.off_lse);
     const int st = p.tc ? attn_tc_fwd(a, dtype, p.nq, p.sms, s) : attn_simt_fwd(a, s);
@@ -287,6 +326,7 @@ int attn_fwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
 
 int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s) {
     a.gp = p.gp;
+    a.gp_log2 = __builtin_ctz((unsigned)p.gp);
     a.err = reinterpret_cast<uint32_t*>(ws);
     a.stats = reinterpret_cast<float2*>(ws + 256);
     int st;
@@ -294,20 +334,24 @@ int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
     if (a.n_q > 0) {
         if ((st = VG_BY_TYPE(stats, a, s)) != VG_OK) return st;
         a.splits = p.s_dq;
+        a.per_part = p.per_dq;
+        a.tile = 64;
         a.part = reinterpret_cast<float*>(ws + p.off_dq);
         st = p.tc ? attn_tc_dq(a, dtype, p.nq, p.sms, s) : attn_simt_dq(a, s);
         if (st != VG_OK) return st;
-        if (a.splits > 1 && (st = VG_BY_TYPE(join_sum, a, a.part, a.splits, a.n_q, a.hq, a.gq, s)) != VG_OK) return st;
+        if (a.splits > 1 && (st = VG_BY_TYPE(join_queries, a, a.part, a.gq, s)) != VG_OK) return st;
     }
     if (a.n_k > 0) {
         a.splits = p.s_dkv;
+        a.per_part = p.per_dkv;
+        a.tile = 64;
         a.part = reinterpret_cast<float*>(ws + p.off_dk);
         float* part_dv = reinterpret_cast<float*>(ws + p.off_dv);
         st = p.tc ? attn_tc_dkv(a, part_dv, dtype, p.sms, s) : attn_simt_dkv(a, part_dv, s);
         if (st != VG_OK) return st;
         if (a.splits > 1) {
-            if ((st = VG_BY_TYPE(join_sum, a, a.part, a.splits, a.n_k, a.hk, a.gk, s)) != VG_OK) return st;
-            if ((st = VG_BY_TYPE(join_sum, a, part_dv, a.splits, a.n_k, a.hk, a.gv, s)) != VG_OK) return st;
+            if ((st = VG_BY_TYPE(join_keys, a, a.part, a.gk, s)) != VG_OK) return st;
+            if ((st = VG_BY_TYPE(join_keys, a, part_dv, a.gv, s)) != VG_OK) return st;
         }
     }
     return VG_OK;

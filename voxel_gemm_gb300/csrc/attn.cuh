@@ -18,7 +18,7 @@ struct AttnArgs {
     // shapes
     int64_t n_q, n_k;
     int batch, hq, hk, d;
-    int gp;                      // query heads packed into rows
+    int gp, gp_log2;             // query heads packed into rows
     const int32_t* q_off;        // [batch + 1]
     const int32_t* k_off;        // [batch + 1]
     const int32_t* k_len;        // [batch] or null: every row between offsets is valid
@@ -30,8 +30,10 @@ struct AttnArgs {
     // workspace
     uint32_t* err;               // error record; words 1, 2: fp32 bits of the largest |dO row|, |V row| (fp16)
     float2* stats;               // [hq / gp][n_q * gp]: (lse * log2 e, sum_d dO O) of every packed row
-    int splits;                  // parts of the axis that the kernel runs along
-    float* part;                 // split partial results (layouts at their kernels)
+    // The axis that a kernel runs along is cut into parts of `per_part` tiles of `tile` rows, so that a sample has
+    // attn_parts of them; splits bounds that number (1: not cut, results go to their place at once).
+    int splits, per_part, tile;
+    float* part;                 // results of the parts (layouts at their kernels)
     float* part_lse;
 };
 
@@ -39,6 +41,7 @@ struct AttnArgs {
 struct AttnTile {
     int b;          // sample, -1: none
     int first;      // first row of the tile within the sample's rows
+    int part;       // part of the other axis
     int q0, lq;     // the sample's queries
     int k0, lk;     // its keys: first row, valid rows
     int krows;      // its key rows, valid or not
@@ -61,28 +64,45 @@ __device__ __forceinline__ bool attn_offsets_ok(const AttnArgs& a) {
     return !bad;
 }
 
-// Sample and first row of tile `t`, when every sample's rows (len * mult of them,
-// len from `off`) are cut into tiles of `rows`; by a whole warp, every lane gets
-// the answer.  Lanes take 32 samples at a time and prefix-sum their tile counts.
-__device__ __forceinline__ AttnTile attn_find_tile(const AttnArgs& a, const int32_t* off, int mult, int rows, int t) {
+// Parts of an axis of `len` rows.
+__device__ __forceinline__ int attn_parts(const AttnArgs& a, int64_t len) {
+    if (a.splits == 1) return 1;
+    const int64_t step = (int64_t)a.per_part * a.tile;
+    return max(1, (int)((len + step - 1) / step));
+}
+
+// Tile `t` of the work: sample by sample, the sample's tiles of `rows` rows (its queries times gp; kKeys: its key
+// rows) for each part of the other axis.  By a whole warp, every lane gets the answer: lanes take 32 samples at a
+// time and prefix-sum their tile counts.
+template <bool kKeys>
+__device__ __forceinline__ AttnTile attn_find_tile(const AttnArgs& a, int rows, int64_t t) {
     const int lane = threadIdx.x & 31;
     AttnTile r;
     r.b = -1;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int b = b0 + lane;
-        const int64_t len = b < a.batch ? off[b + 1] - off[b] : 0;
-        const int tiles = (int)((len * mult + rows - 1) / rows);
-        int incl = tiles;
+        int64_t lq = 0, lk = 0, kr = 0;
+        if (b < a.batch) {
+            lq = (int64_t)(a.q_off[b + 1] - a.q_off[b]) * a.gp;
+            kr = a.k_off[b + 1] - a.k_off[b];
+            lk = a.k_len ? a.k_len[b] : kr;
+        }
+        const int tiles = (int)(((kKeys ? kr : lq) + rows - 1) / rows);
+        const int64_t count = (int64_t)tiles * attn_parts(a, kKeys ? lq : lk);
+        int64_t incl = count;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
         const uint32_t at = __ballot_sync(0xffffffffu, t < incl);
         if (at) {
             const int src = __ffs(at) - 1;
+            const int n = __shfl_sync(0xffffffffu, tiles, src);
+            const int64_t i = t - __shfl_sync(0xffffffffu, incl - count, src);
             r.b = b0 + src;
-            r.first = (t - __shfl_sync(0xffffffffu, incl - tiles, src)) * rows;
+            r.part = (int)(i / n);
+            r.first = (int)(i - (int64_t)r.part * n) * rows;
             // one load each, shared out by a shuffle: the compiler knows the result to be uniform
             const int32_t* p = lane < 2 ? a.q_off + r.b + lane : lane < 4 ? a.k_off + r.b + (lane - 2)
                                : a.k_len ? a.k_len + r.b : nullptr;
@@ -116,18 +136,20 @@ struct AttnPlan {
     int tc = 0;                          // 16-bit types: tensor cores
     int gp = 1;                          // query heads packed into rows
     int nq = 1;                          // row tiles of a forward block
-    int s_fwd = 1, s_dq = 1, s_dkv = 1;  // parts of the key axis (forward, dQ) and of the query axis (dK, dV)
+    // most parts of the key axis (forward, dQ) and of the query axis (dK, dV), and the tiles of a part
+    int s_fwd = 1, s_dq = 1, s_dkv = 1;
+    int per_fwd = 0, per_dq = 0, per_dkv = 0;
     size_t off_lse = 0, off_dq = 0, off_dk = 0, off_dv = 0, total = 0;
 };
 int attn_plan(const AttnShape& c, AttnPlan* P);
 int attn_fwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s);
 int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s);
 
-// Part `s` of `splits` of n tiles.
-__device__ __forceinline__ void attn_split(int n, int splits, int s, int* lo, int* hi) {
-    const int per = (n + splits - 1) / splits;
-    *lo = min(n, per * s);
-    *hi = min(n, *lo + per);
+// Tiles [lo, hi) of part `part` of an axis of `len` rows.
+__device__ __forceinline__ void attn_split(const AttnArgs& a, int64_t len, int part, int* lo, int* hi) {
+    const int n = (int)((len + a.tile - 1) / a.tile);
+    *lo = a.splits == 1 ? 0 : min(n, a.per_part * part);
+    *hi = a.splits == 1 ? n : min(n, *lo + a.per_part);
 }
 
 template <typename T>

@@ -103,10 +103,6 @@ __device__ __forceinline__ void zero(float4 (&acc)[4][NC]) {
 __device__ __forceinline__ void put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ float4 times(float4 v, float s) { return make_float4(v.x * s, v.y * s, v.z * s, v.w * s); }
 
-__device__ __forceinline__ AttnTile block_tile(const AttnArgs& a, const int32_t* off) {
-    return attn_find_tile(a, off, 1, kT, (int)blockIdx.x);
-}
-
 // ---------------------------------------------------------------- forward
 template <int NC>
 __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
@@ -114,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
     const int p = a.d + 4;
     float *sQ = sm, *sK = sQ + kT * p, *sV = sK + kT * p, *sP = sV + kT * p;
     if (!attn_offsets_ok(a)) return;
-    const AttnTile t = block_tile(a, a.q_off);
+    const AttnTile t = attn_find_tile<false>(a, kT, blockIdx.x);
     if (t.b < 0) return;
     const int h = blockIdx.y, hk = h / (a.hq / a.hk);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -125,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
     for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
     zero<NC>(acc);
     int lo, hi;
-    attn_split((t.lk + kT - 1) / kT, a.splits, blockIdx.z, &lo, &hi);
+    attn_split(a, t.lk, t.part, &lo, &hi);
     for (int kt = lo; kt < hi; ++kt) {
         const int left = t.lk - kt * kT;  // valid keys of the tile
         __syncthreads();
@@ -171,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
         const float inv = hi > lo ? 1.f / l[i] : 0.f;  // no keys: zero; only keys of weight zero: NaN
         const float lse = hi > lo ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
         if (tx == 0) {
-            float* dst = a.splits > 1 ? a.part_lse + (size_t)blockIdx.z * a.hq * a.n_q : a.lse;
+            float* dst = a.splits > 1 ? a.part_lse + (size_t)t.part * a.hq * a.n_q : a.lse;
             if (dst) dst[(int64_t)h * a.n_q + row] = lse;
         }
 #pragma unroll
@@ -180,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
             if (col >= a.d) continue;
             const float4 v = times(acc[i][c], inv);
             if (a.splits > 1)
-                put4(a.part + (((size_t)blockIdx.z * a.n_q + row) * a.hq + h) * a.d + col, v);
+                put4(a.part + (((size_t)t.part * a.n_q + row) * a.hq + h) * a.d + col, v);
             else
                 put4(head_row<float>(a.o, row, h) + col, v);
         }
@@ -194,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
     const int p = a.d + 4;
     float *sQ = sm, *sG = sQ + kT * p, *sK = sG + kT * p, *sV = sK + kT * p, *sS = sV + kT * p;
     if (!attn_offsets_ok(a)) return;
-    const AttnTile t = block_tile(a, a.q_off);
+    const AttnTile t = attn_find_tile<false>(a, kT, blockIdx.x);
     if (t.b < 0) return;
     const int h = blockIdx.y, hk = h / (a.hq / a.hk);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -209,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
     float4 acc[4][NC];
     zero<NC>(acc);
     int lo, hi;
-    attn_split((t.lk + kT - 1) / kT, a.splits, blockIdx.z, &lo, &hi);
+    attn_split(a, t.lk, t.part, &lo, &hi);
     for (int kt = lo; kt < hi; ++kt) {
         const int left = t.lk - kt * kT;
         __syncthreads();
@@ -240,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
             if (col >= a.d) continue;
             const float4 v = times(acc[i][c], a.scale);
             if (a.splits > 1)
-                put4(a.part + (((size_t)blockIdx.z * a.n_q + row) * a.hq + h) * a.d + col, v);
+                put4(a.part + (((size_t)t.part * a.n_q + row) * a.hq + h) * a.d + col, v);
             else
                 put4(head_row<float>(a.gq, row, h) + col, v);
         }
@@ -257,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* 
     float *sQ = sm, *sG = sQ + kT * p, *sK = sG + kT * p, *sV = sK + kT * p;
     float *sP = sV + kT * p, *sS = sP + kT * kPP;
     if (!attn_offsets_ok(a)) return;
-    const AttnTile t = block_tile(a, a.k_off);
+    const AttnTile t = attn_find_tile<true>(a, kT, blockIdx.x);
     if (t.b < 0) return;
     const int hk = blockIdx.y, group = a.hq / a.hk;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -267,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* 
     zero<NC>(dk);
     zero<NC>(dv);
     int lo, hi;
-    attn_split((t.lq + kT - 1) / kT, a.splits, blockIdx.z, &lo, &hi);
+    attn_split(a, t.lq, t.part, &lo, &hi);
     if (t.first >= t.lk) hi = lo;  // no valid key in the tile
     for (int g = 0; g < group; ++g) {
         const int h = hk * group + g;
@@ -308,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* 
             if (col >= a.d) continue;
             const float4 vk = times(dk[i][c], a.scale), vv = dv[i][c];
             if (a.splits > 1) {
-                const size_t at = (((size_t)blockIdx.z * a.n_k + row) * a.hk + hk) * a.d + col;
+                const size_t at = (((size_t)t.part * a.n_k + row) * a.hk + hk) * a.d + col;
                 put4(a.part + at, vk);
                 put4(part_dv + at, vv);
             } else {
@@ -332,7 +328,7 @@ template <int NC>
 int fwd(const AttnArgs& a, cudaStream_t s) {
     const size_t smem = smem_bytes(a.d, 3, 1);
     if (!allow_smem(k_attn_fwd<NC>, smem)) return VG_ERR_CUDA;
-    const dim3 grid((unsigned)attn_max_tiles(a.n_q, a.batch, 1, kT), a.hq, a.splits);
+    const dim3 grid((unsigned)(attn_max_tiles(a.n_q, a.batch, 1, kT) * a.splits), a.hq);
     k_attn_fwd<NC><<<grid, kThreads, smem, s>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
@@ -340,7 +336,7 @@ template <int NC>
 int dq(const AttnArgs& a, cudaStream_t s) {
     const size_t smem = smem_bytes(a.d, 4, 1);
     if (!allow_smem(k_attn_dq<NC>, smem)) return VG_ERR_CUDA;
-    const dim3 grid((unsigned)attn_max_tiles(a.n_q, a.batch, 1, kT), a.hq, a.splits);
+    const dim3 grid((unsigned)(attn_max_tiles(a.n_q, a.batch, 1, kT) * a.splits), a.hq);
     k_attn_dq<NC><<<grid, kThreads, smem, s>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
@@ -348,7 +344,7 @@ template <int NC>
 int dkv(const AttnArgs& a, float* part_dv, cudaStream_t s) {
     const size_t smem = smem_bytes(a.d, 4, 2);
     if (!allow_smem(k_attn_dkv<NC>, smem)) return VG_ERR_CUDA;
-    const dim3 grid((unsigned)attn_max_tiles(a.n_k, a.batch, 1, kT), a.hk, a.splits);
+    const dim3 grid((unsigned)(attn_max_tiles(a.n_k, a.batch, 1, kT) * a.splits), a.hk);
     k_attn_dkv<NC><<<grid, kThreads, smem, s>>>(a, part_dv);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }

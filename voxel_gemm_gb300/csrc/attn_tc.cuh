@@ -10,6 +10,8 @@
 #pragma once
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -134,17 +136,16 @@ struct Waiter {
     }
 };
 
-// Named barrier of `threads` threads, and the same with an or over their predicates.
-__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t threads, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-        "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(threads), "r"((uint32_t)v)
-        : "memory");
-    return r != 0;
-}
+template <int V> using Const = std::integral_constant<int, V>;
+
+// A position in a ring of S slots and the parity of the pass over it.
+template <int S>
+struct RingPos {
+    uint32_t i = 0, phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++i == S) i = 0, phase ^= 1u;
+    }
+};
 
 // Run f in one lane of a converged warp.
 template <typename F>
@@ -156,6 +157,58 @@ __device__ __forceinline__ void one_lane(F f) {
 // The value of lane 0 in every lane, as one that the compiler knows to be uniform.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Work unit of a block: a few ints, found once by the scheduler warp (looking a tile's
+// sample up takes a few dependent loads and divisions, some 2,400 cycles) and handed to
+// the other warps through a ring of slots in shared memory.
+struct Unit {
+    int first, rows;   // first row of the unit within its sample, how many it has; rows < 0: no more units
+    int head, part;    // head set or key head; part of the split axis
+    int lo, hi;        // tiles of the axis that the unit runs along
+    int q0, lq;        // the sample's queries
+    int k0, lk;        // its keys: first row, valid rows
+    int unused0, unused1;
+};
+constexpr int kUnitSlots = 4;
+
+struct UnitRing {
+    int4* slots;          // [kUnitSlots][3]
+    uint32_t full, empty;  // barriers, 8 bytes apart
+    uint32_t at = 0;
+
+    __device__ __forceinline__ void put(Waiter& wait, const Unit& x) {
+        const uint32_t i = at % kUnitSlots;
+        wait(empty + 8 * i, ((at / kUnitSlots) & 1u) ^ 1u);
+        if ((threadIdx.x & 31) == 0) {
+            const int4* src = reinterpret_cast<const int4*>(&x);
+            for (int j = 0; j < 3; ++j) slots[3 * i + j] = src[j];
+            mbar_arrive(full + 8 * i);
+        }
+        __syncwarp();
+        ++at;
+    }
+    // The next unit; false at the end, or when the wait gave up.
+    __device__ __forceinline__ bool get(Waiter& wait, Unit& x) {
+        const uint32_t i = at % kUnitSlots;
+        if (!wait(full + 8 * i, (at / kUnitSlots) & 1u)) return false;
+        int4* dst = reinterpret_cast<int4*>(&x);
+        for (int j = 0; j < 3; ++j) dst[j] = slots[3 * i + j];
+        x.first = uniform(x.first);
+        x.rows = uniform(x.rows);
+        x.head = uniform(x.head);
+        x.part = uniform(x.part);
+        x.lo = uniform(x.lo);
+        x.hi = uniform(x.hi);
+        x.q0 = uniform(x.q0);
+        x.lq = uniform(x.lq);
+        x.k0 = uniform(x.k0);
+        x.lk = uniform(x.lk);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * i);
+        __syncwarp();
+        ++at;
+        return x.rows >= 0;
+    }
+};
 
 }  // namespace attn_tc
 

@@ -119,15 +119,14 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
     };
     auto find = [&](int64_t u) {
         Unit x;
-        const int64_t v = u / tiles;
-        x.t = attn_find_tile(a, a.q_off, a.gp, NQ * kM, (int)(u - v * tiles));
-        x.hs = (int)(v % sets);
-        x.part = (int)(v / sets);
+        x.t = attn_find_tile<false>(a, NQ * kM, u / sets);
+        x.hs = (int)(u % sets);
+        x.part = x.t.part;
         x.rows = 0;
         x.lo = x.hi = 0;
         if (x.t.b >= 0) {
             x.rows = min(NQ * kM, x.t.lq * a.gp - x.t.first);
-            attn_split((x.t.lk + kN - 1) / kN, a.splits, x.part, &x.lo, &x.hi);
+            attn_split(a, x.t.lk, x.part, &x.lo, &x.hi);
         }
         return x;
     };
@@ -420,13 +419,11 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     };
     auto find = [&](int64_t u) {
         Unit x;
-        const int64_t v = u / tiles;
-        x.t = attn_find_tile(a, a.k_off, 1, kM, (int)(u - v * tiles));
-        x.kh = (int)(v % a.hk);
-        x.part = (int)(v / a.hk);
+        x.t = attn_find_tile<true>(a, kM, u / a.hk);
+        x.kh = (int)(u % a.hk);
+        x.part = x.t.part;
         x.lo = x.hi = 0;
-        if (x.t.b >= 0 && x.t.first < x.t.lk)
-            attn_split((x.t.lq * a.gp + kN - 1) / kN, a.splits, x.part, &x.lo, &x.hi);
+        if (x.t.b >= 0 && x.t.first < x.t.lk) attn_split(a, (int64_t)x.t.lq * a.gp, x.part, &x.lo, &x.hi);
         x.steps = (x.hi - x.lo) * sets_per_key;
         return x;
     };

@@ -5,20 +5,21 @@
 //
 // A persistent block takes units of NQ x 128 packed query rows of one sample and head
 // set, and runs along the sample's keys in tiles of 128:
-//   warps 0 .. 8 NQ - 1  softmax: two threads per row, 64 keys of a tile each.  A thread
-//                        reads its scores from TMEM, writes P as 16-bit pairs over them,
-//                        and at the end scales and stores a part of its row of O.
+//   warps 0 .. 4 NQ - 1  softmax: one thread per row.  Reads its 128 scores from TMEM,
+//                        writes P as 16-bit pairs over them, and at the end scales and
+//                        stores its row of O.
 //   then one warp        loader: TMA copies of Q (per unit) and of K and V tiles (a ring).
 //   then one warp        issues the products: S into TMEM, then O += P V with P read from
 //                        TMEM.
-//   two idle warps       fill the last warpgroup, whose registers go to the softmax warps.
+//   then one warp        scheduler: finds the block's next units.
+//   one idle warp        fills the last warpgroup, whose registers go to the softmax warps.
 // With NQ = 2 the two row tiles take turns: one's products run while the other's
 // exponentials do, and both read each K and V tile from the same copy.  NQ = 1 leaves
 // room for two blocks on an SM and serves calls with few rows per sample.
 //
 // The row maximum only keeps the weights in range, and O and l carry the same factor
 // whatever it is.  So it is taken from the first tile and kept: later tiles are weighed
-// with it right away, and only where a half row's sum of weights leaves the range (2^64 in
+// with it right away, and only where a row's sum of weights over a tile leaves the range (2^64 in
 // bf16, 2^14 in fp16) are the maximum renewed, O (in TMEM) and l rescaled and the tile
 // weighed again.  P is rounded to the inputs' type for the second product (l sums
 // the unrounded values); fp16 weights carry a factor 2^7 more, so that a weight down to
@@ -34,57 +35,66 @@ using namespace attn_tc;
 constexpr int kM = 128;   // rows of an MMA tile
 constexpr int kN = 128;   // keys of a tile
 
-constexpr int kH = kN / 2;  // keys of a softmax thread
-
 template <int DP, int NQ>
 struct Cfg {
-    static constexpr int kThreads = NQ * 256 + 128;
+    static constexpr int kSoftWarps = NQ * 4;
+    static constexpr int kThreads = 32 * kSoftWarps + 128;
     static constexpr int kBlocks = DP / 64;
-    static constexpr int kTile = kM * 128 * kBlocks;               // bytes of a Q, K or V tile
-    static constexpr int S = NQ == 2 ? (DP == 64 ? 6 : 4) : (DP == 64 ? 4 : 2);  // ring stages
-    static constexpr int kOCol = NQ * kN;                           // O's first TMEM column
+    static constexpr int kTile = kM * 128 * kBlocks;       // bytes of a Q, K or V tile
+    static constexpr int S = DP == 64 && NQ == 2 ? 5 : 2;  // ring stages, a K and a V tile each
+    static constexpr int kPerSm = DP == 64 && NQ == 1 ? 2 : 1;
+    static constexpr int kOCol = NQ * kN;                   // O's first TMEM column
     static constexpr int kTmem = NQ * (kN + DP) <= 256 ? 256 : 512;
-    // q full, q empty, (s full, p full, o full, o empty) x NQ, kv full x S, kv empty x S, tail, done
-    static constexpr int kBars = 2 + 4 * NQ + 2 * S + 2;
-    static constexpr size_t kSwap = (size_t)NQ * 2 * 2 * kM * sizeof(float);  // maxima and sums of the row halves
-    static constexpr size_t kSmem = 1024 + (size_t)(NQ + S) * kTile + kSwap + 8 * kBars + 16;
+    // q full, q empty, (s full, p full, o full, o empty) x NQ, (k full, v full, k empty, v empty) x S, tail, done,
+    // unit ring
+    static constexpr int kBars = 2 + 4 * NQ + 4 * S + 2 + 2 * kUnitSlots;
+    static constexpr size_t kSmem = 1024 + (size_t)(NQ + 2 * S) * kTile + kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
     // registers: launched with kRegs a thread; the softmax warps take what the last warpgroup gives up
-    static constexpr int kRegs = NQ == 2 ? 96 : 80, kSoft = NQ == 2 ? 104 : 96, kAux = NQ == 2 ? 64 : 48;
-    static_assert(NQ * 256 * kSoft + 128 * kAux <= kThreads * kRegs, "register split");
+    static constexpr int kRegs = NQ == 2 ? 168 : 128, kSoft = NQ == 2 ? 200 : 184, kAux = NQ == 2 ? 104 : 72;
+    static_assert(32 * kSoftWarps * kSoft + 128 * kAux <= kThreads * kRegs, "register split");
 };
-static_assert(Cfg<128, 2>::kSmem <= 232448 && 2 * (Cfg<128, 1>::kSmem + 1024) <= 233472, "shared memory");
+static_assert(Cfg<128, 2>::kSmem <= 232448 && 2 * (Cfg<64, 1>::kSmem + 1024) <= 233472 &&
+                  Cfg<128, 1>::kSmem <= 232448, "shared memory");
 
 template <bool BF16, int DP, int NQ>
-__global__ void __launch_bounds__(NQ * 256 + 128, NQ == 1 ? 2 : 1)
-    k_attn_tc_fwd(const AttnArgs a, const __grid_constant__ AttnMaps maps, const int tiles) {
+__global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
+    k_attn_tc_fwd(const AttnArgs a, const __grid_constant__ AttnMaps maps) {
     using C = Cfg<DP, NQ>;
     constexpr int S = C::S;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sQ = smem_u32(smem), sKV = sQ + NQ * C::kTile;
-    float* s_swap = reinterpret_cast<float*>(smem + (size_t)(NQ + S) * C::kTile);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_swap) + C::kSwap);
+    int4* s_units = reinterpret_cast<int4*>(smem + (size_t)(NQ + 2 * S) * C::kTile);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_units + 3 * kUnitSlots);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile uint32_t* s_abort = s_tmem + 1;
     const uint32_t bar0 = smem_u32(bars);
     const uint32_t q_full = bar0, q_empty = bar0 + 8;
     const uint32_t s_full = bar0 + 16, p_full = s_full + 8 * NQ, o_full = p_full + 8 * NQ, o_empty = o_full + 8 * NQ;
-    const uint32_t kv_full = o_empty + 8 * NQ, kv_empty = kv_full + 8 * S, tail = kv_empty + 8 * S, done = tail + 8;
+    const uint32_t k_full = o_empty + 8 * NQ, v_full = k_full + 8 * S, k_empty = v_full + 8 * S;
+    const uint32_t v_empty = k_empty + 8 * S, tail = v_empty + 8 * S;
+    const uint32_t done = tail + 8, u_full = done + 8, u_empty = u_full + 8 * kUnitSlots;
 
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kLoader = NQ * 8, kIssuer = NQ * 8 + 1;
+    constexpr int kLoader = C::kSoftWarps, kIssuer = kLoader + 1, kScheduler = kLoader + 2;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int w = 0; w < NQ; ++w) {
             mbar_init(s_full + 8 * w, 1);
-            mbar_init(p_full + 8 * w, 8);
+            mbar_init(p_full + 8 * w, 4);
             mbar_init(o_full + 8 * w, 1);
-            mbar_init(o_empty + 8 * w, 8);
+            mbar_init(o_empty + 8 * w, 4);
         }
         for (int i = 0; i < S; ++i) {
-            mbar_init(kv_full + 8 * i, 1);
-            mbar_init(kv_empty + 8 * i, 1);
+            mbar_init(k_full + 8 * i, 1);
+            mbar_init(v_full + 8 * i, 1);
+            mbar_init(k_empty + 8 * i, 1);
+            mbar_init(v_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < kUnitSlots; ++i) {
+            mbar_init(u_full + 8 * i, 1);
+            mbar_init(u_empty + 8 * i, C::kSoftWarps + 2);  // every reader: softmax warps, loader, issuer
         }
         mbar_init(tail, 1);
         mbar_init(done, 1);
@@ -105,133 +115,134 @@ __global__ void __launch_bounds__(NQ * 256 + 128, NQ == 1 ? 2 : 1)
     tc_fence_after();
     const uint32_t tmem = uniform(*s_tmem);
 
-    const int sets = a.hq / a.gp;
     const int group = a.hq / a.hk;
-    const int64_t units = good ? (int64_t)tiles * sets * a.splits : 0;
-    // unit u = (part, head set, row tile); its key tiles [lo, hi) and the row tiles it fills
-    struct Unit {
-        AttnTile t;
-        int hs, part, lo, hi, rows;
-    };
-    auto find = [&](int64_t u) {
-        Unit x;
-        const int64_t v = u / tiles;
-        x.t = attn_find_tile(a, a.q_off, a.gp, NQ * kM, (int)(u - v * tiles));
-        x.hs = (int)(v % sets);
-        x.part = (int)(v / sets);
-        x.rows = 0;
-        x.lo = x.hi = 0;
-        if (x.t.b >= 0) {
-            x.rows = min(NQ * kM, x.t.lq * a.gp - x.t.first);
-            attn_split((x.t.lk + kN - 1) / kN, a.splits, x.part, &x.lo, &x.hi);
-        }
-        return x;
-    };
     Waiter wait{s_abort};
+    UnitRing ring{s_units, u_full, u_empty};
+    Unit x;
     if (warp >= kLoader) reg_shrink<C::kAux>();
-    if (warp == kLoader) {
-        uint32_t it = 0, uc = 0, tc = 0;
-        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
-            const Unit x = find(u);
+    if (warp == kScheduler) {
+        // unit u = (row tile and part, head set): its rows and its key tiles [lo, hi)
+        const int sets = a.hq / a.gp;
+        for (int64_t u = blockIdx.x; good && wait.ok; u += gridDim.x) {
+            const AttnTile t = attn_find_tile<false>(a, NQ * kM, u / sets);
+            if (t.b < 0) break;
+            x = Unit{t.first, min(NQ * kM, t.lq * a.gp - t.first), (int)(u % sets), t.part, 0, 0,
+                     t.q0, t.lq, t.k0, t.lk, 0, 0};
+            attn_split(a, t.lk, t.part, &x.lo, &x.hi);
+            ring.put(wait, x);
+        }
+        x.rows = -1;
+        ring.put(wait, x);
+    } else if (warp == kLoader) {
+        RingPos<S> pos;
+        uint32_t n = 0, uc = 0, tc = 0;  // tiles and units loaded
+        while (ring.get(wait, x)) {
             if (x.hi <= x.lo) continue;
             wait(q_empty, (uc & 1u) ^ 1u);
             if (!wait.ok) break;
-            const int nq = x.rows > kM ? NQ : 1;
+            const int nq = x.rows > kM ? NQ : 1, kh = x.head * a.gp / group;
             one_lane([&] {
                 mbar_arrive_expect_tx(q_full, nq * C::kTile);
                 for (int w = 0; w < nq; ++w)
                     for (int b = 0; b < C::kBlocks; ++b)
-                        tma_load_3d(sQ + w * C::kTile + b * kM * 128, &maps.q, b * 64, x.hs * a.gp,
-                                    x.t.q0 + (x.t.first + w * kM) / a.gp, q_full);
+                        tma_load_3d(sQ + w * C::kTile + b * kM * 128, &maps.q, b * 64, x.head * a.gp,
+                                    x.q0 + ((x.first + w * kM) >> a.gp_log2), q_full);
             });
             ++uc;
-            const int kh = x.hs * a.gp / group;
-            for (int e = 2 * x.lo; e < 2 * x.hi; ++e, ++it) {  // K and V tiles in turn
-                const uint32_t st = it % S, dst = sKV + st * C::kTile;
-                wait(kv_empty + 8 * st, ((it / S) & 1u) ^ 1u);
+            for (int e = x.lo; e < x.hi; ++e) {
+                const uint32_t k = sKV + 2 * pos.i * C::kTile, v = k + C::kTile;
+                wait(k_empty + 8 * pos.i, pos.phase ^ 1u);
                 if (!wait.ok) break;
-                const int left = min(kN, x.t.lk - (e >> 1) * kN), n16 = (left + 15) / 16 * 16;
-                const bool cut = (e & 1) && n16 != left;
-                const void* map = e & 1 ? &maps.v : &maps.k;
-                const uint32_t bar = cut ? tail : kv_full + 8 * st;
+                one_lane([&] {
+                    mbar_arrive_expect_tx(k_full + 8 * pos.i, C::kTile);
+                    for (int b = 0; b < C::kBlocks; ++b)
+                        tma_load_3d(k + b * kN * 128, &maps.k, b * 64, kh, x.k0 + e * kN, k_full + 8 * pos.i);
+                });
+                wait(v_empty + 8 * pos.i, pos.phase ^ 1u);
+                if (!wait.ok) break;
+                const int left = min(kN, x.lk - e * kN), n16 = (left + 15) / 16 * 16;
+                const uint32_t bar = n16 != left ? tail : v_full + 8 * pos.i;
                 one_lane([&] {
                     mbar_arrive_expect_tx(bar, C::kTile);
                     for (int b = 0; b < C::kBlocks; ++b)
-                        tma_load_3d(dst + b * kN * 128, map, b * 64, kh, x.t.k0 + (e >> 1) * kN, bar);
+                        tma_load_3d(v + b * kN * 128, &maps.v, b * 64, kh, x.k0 + e * kN, bar);
                 });
-                if (cut) {  // V rows past the sample's keys may hold anything, and 0 x them must be 0 in P V
+                if (n16 != left) {  // V rows past the sample's keys may hold anything: 0 x them must be 0 in P V
                     wait(tail, tc++ & 1u);
-                    zero_rows(dst, left, n16, C::kBlocks, kN * 128);
+                    zero_rows(v, left, n16, C::kBlocks, kN * 128);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(kv_full + 8 * st);
+                    if (lane == 0) mbar_arrive(v_full + 8 * pos.i);
                     __syncwarp();
                 }
+                pos.step();
+                ++n;
             }
         }
         // every copy has landed before the block may exit
         if (uc > 0 && !mbar_wait_timed(q_full, (uc - 1) & 1u)) wait.ok = false;
-        for (uint32_t i = 0; i < (uint32_t)S && i < it; ++i) {
-            const uint32_t last = it - 1 - i;
-            if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
+        for (uint32_t i = 0; i < (uint32_t)S && i < n; ++i) {
+            const uint32_t last = n - 1 - i;
+            if (!mbar_wait_timed(k_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
+            if (!mbar_wait_timed(v_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;          // K = 16 steps over the channels
-        const int o_cols = ksteps * 16;              // columns of O
-        const uint32_t idesc_o = idesc_f16_bn(BF16, o_cols);
-        uint32_t it = 0, uc = 0, pc[NQ] = {}, oc[NQ] = {};
-        // S_w = Q_w K^T of the tile in stage st, `n` keys
-        auto scores = [&](int w, uint32_t st, int n) {
-            mma_channels<DP / 16, kM * 128, kN * 128>(tmem + w * kN, sw128_kmajor_desc(sQ + w * C::kTile),
-                                                      sw128_kmajor_desc(sKV + st * C::kTile), idesc_f16(BF16, n),
-                                                      ksteps);
-            mma_commit(s_full + 8 * w);
-        };
-        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
-            const Unit x = find(u);
+        const uint32_t idesc_s = idesc_f16(BF16, kN), idesc_o = idesc_f16_bn(BF16, ksteps * 16);
+        const uint64_t dq = sw128_kmajor_desc(sQ), dk = sw128_kmajor_desc(sKV);
+        const uint64_t dv = sw128_mnmajor_desc(sKV + C::kTile, kN * 128);
+        RingPos<S> pos;
+        uint32_t uc = 0, pc[NQ] = {}, oc[NQ] = {};
+        while (ring.get(wait, x)) {
             if (x.hi <= x.lo) continue;
-            const int nq = x.rows > kM ? NQ : 1;
-            auto padded = [&](int e) { return (min(kN, x.t.lk - e * kN) + 15) / 16 * 16; };  // keys of tile e
+            const bool both = NQ == 2 && x.rows > kM;
+            const int last16 = (min(kN, x.lk - (x.hi - 1) * kN) + 15) / 16;   // K = 16 steps of the last tile
+            // S_w = Q_w K^T of the stage at `at`
+            auto scores = [&](auto wc, uint32_t at, bool last) {
+                constexpr int w = decltype(wc)::value;
+                mma_channels<DP / 16, kM * 128, kN * 128>(tmem + w * kN, dq + w * (C::kTile >> 4),
+                                                          dk + at * (2 * C::kTile >> 4),
+                                                          last ? idesc_f16(BF16, last16 * 16) : idesc_s, ksteps);
+                mma_commit(s_full + 8 * w);
+            };
             wait(q_full, uc & 1u);
-            wait(kv_full + 8 * (it % S), (it / S) & 1u);
+            wait(k_full + 8 * pos.i, pos.phase);
             if (!wait.ok) break;
             tc_fence_after();
             one_lane([&] {
-                for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
-                mma_commit(kv_empty + 8 * (it % S));
+                scores(Const<0>(), pos.i, x.hi - x.lo == 1);
+                if (both) scores(Const<NQ - 1>(), pos.i, x.hi - x.lo == 1);
+                mma_commit(k_empty + 8 * pos.i);
                 if (x.hi - x.lo == 1) mma_commit(q_empty);
             });
-            ++it;
             for (int e = x.lo; e < x.hi; ++e) {
-                const uint32_t sv = it % S, pv = (it / S) & 1u;
-                const uint32_t sk = (it + 1) % S, pk = ((it + 1) / S) & 1u;
+                const uint32_t at = pos.i;
                 const bool more = e + 1 < x.hi;
-                wait(kv_full + 8 * sv, pv);
-                if (more) wait(kv_full + 8 * sk, pk);
-                if (!wait.ok) break;
-                const int n16 = padded(e);
-                for (int w = 0; w < nq; ++w) {
-                    wait(p_full + 8 * w, pc[w]++ & 1u);
-                    if (e == x.lo) wait(o_empty + 8 * w, (oc[w] & 1u) ^ 1u);
-                    if (!wait.ok) break;
+                wait(v_full + 8 * at, pos.phase);
+                pos.step();
+                if (more) wait(k_full + 8 * pos.i, pos.phase);
+                // O_w += P_w V, then the next tile's scores
+                auto tile = [&](auto wc, bool final) {
+                    constexpr int w = decltype(wc)::value;
+                    if (e == x.lo) wait(o_empty + 8 * w, (oc[w]++ & 1u) ^ 1u);
+                    if (!wait(p_full + 8 * w, pc[w]++ & 1u)) return;
                     tc_fence_after();
                     one_lane([&] {
-                        mma_rows<kN / 16>(tmem + C::kOCol + w * DP, tmem + w * kN,
-                                          sw128_mnmajor_desc(sKV + sv * C::kTile, kN * 128), idesc_o, n16 / 16,
-                                          e > x.lo);
-                        if (more) scores(w, sk, padded(e + 1));
+                        mma_rows<kN / 16>(tmem + C::kOCol + w * DP, tmem + w * kN, dv + at * (2 * C::kTile >> 4),
+                                          idesc_o, more ? kN / 16 : last16, e > x.lo);
+                        if (more) scores(wc, pos.i, e + 2 == x.hi);
                         else mma_commit(o_full + 8 * w);
-                        if (w + 1 == nq) {
-                            mma_commit(kv_empty + 8 * sv);
-                            if (more) mma_commit(kv_empty + 8 * sk);
+                        if (final) {
+                            mma_commit(v_empty + 8 * at);
+                            if (more) mma_commit(k_empty + 8 * pos.i);
                             if (e + 2 == x.hi) mma_commit(q_empty);
                         }
                     });
-                    if (!more) ++oc[w];
-                }
+                };
+                tile(Const<0>(), !both);
+                if (both) tile(Const<NQ - 1>(), true);
                 if (!wait.ok) break;
-                it += more ? 2 : 1;
             }
             ++uc;
         }
@@ -244,44 +255,36 @@ __global__ void __launch_bounds__(NQ * 256 + 128, NQ == 1 ? 2 : 1)
         }
     } else if (warp < kLoader) {
         reg_grow<C::kSoft>();
-        // Thread (tile w, quadrant quad, lane) and half: 64 keys of one row.  The two warps that share a
-        // quadrant's rows meet at a named barrier, so none of them may leave its loops early: after a wait that
-        // gave up they only skip work.
-        const int w = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
-        const uint32_t pair = 1 + w * 4 + quad;
-        float* swap_max = s_swap + w * 4 * kM + quad * 32 + lane;  // [half][row] maxima, then [half][row] sums
-        float* swap_sum = swap_max + 2 * kM;
+        const int w = warp >> 2, quad = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t t_s = t_lane + w * kN + half * kH, t_p = t_lane + w * kN + half * (kH / 2);
-        const uint32_t t_o = t_lane + C::kOCol + w * DP;
+        const uint32_t t_s = t_lane + w * kN, t_o = t_lane + C::kOCol + w * DP;
         const float c = a.scale_log2;
         constexpr float kLift = BF16 ? 0.f : 7.f;            // exponent added to the weights
-        constexpr float kMost = BF16 ? 0x1p64f : 0x1p14f;    // of a half row's sum before the maximum is replaced
+        constexpr float kMost = BF16 ? 0x1p64f : 0x1p14f;    // of a tile's sum before the maximum is replaced
         const bool v8ok = ((reinterpret_cast<uintptr_t>(a.o.data) | (uintptr_t)(a.o.row_stride * 2) |
                             (uintptr_t)(a.o.head_stride * 2)) & 31u) == 0;
+        const int row = w * kM + quad * 32 + lane;           // within the unit
         uint32_t sc = 0, oc = 0;
-        for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-            const Unit x = find(u);
+        while (ring.get(wait, x)) {
             if (x.rows <= w * kM) continue;
-            const int row = w * kM + quad * 32 + lane;                // within the unit
             const bool any = x.rows > w * kM + quad * 32, mine = row < x.rows;  // the warp, the thread has a row
             float m = -INFINITY, l = 0.f;
             for (int e = x.lo; e < x.hi; ++e) {
-                wait(s_full + 8 * w, sc++ & 1u);
+                if (!wait(s_full + 8 * w, sc++ & 1u)) break;
                 tc_fence_after();
                 if (any) {
-                    const int left = x.t.lk - e * kN - half * kH;     // valid keys of the half
-                    uint32_t s[2][32], p[32];
+                    const int left = x.lk - e * kN;                   // valid keys of the tile
+                    uint32_t s[kN / 32][32], p[kN / 64][32];
                     float sum;
                     auto load = [&] {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) tmem_ld32(t_s + 32 * i, s[i]);
+                        for (int i = 0; i < kN / 32; ++i) tmem_ld32(t_s + 32 * i, s[i]);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) tmem_ld_done(s[i]);
-                        if (left < kH) {
+                        for (int i = 0; i < kN / 32; ++i) tmem_ld_done(s[i]);
+                        if (left < kN) {
 #pragma unroll
-                            for (int i = 0; i < kH; ++i)
+                            for (int i = 0; i < kN; ++i)
                                 if (i >= left) s[i >> 5][i & 31] = 0xff800000u;
                         }
                     };
@@ -290,42 +293,33 @@ __global__ void __launch_bounds__(NQ * 256 + 128, NQ == 1 ? 2 : 1)
                         const float2 c2 = make_float2(c, c), base2 = make_float2(base, base);
                         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
+                        for (int j = 0; j < kN / 2; ++j) {
                             float2 x2 = fma2(two(&s[j >> 4][2 * (j & 15)]), c2, base2);
                             x2 = make_float2(ex2(x2.x), ex2(x2.y));
                             acc[j & 1] = add2(acc[j & 1], x2);
-                            p[j] = pack2<BF16>(x2.x, x2.y);
+                            p[j >> 5][j & 31] = pack2<BF16>(x2.x, x2.y);
                         }
                         const float2 both = add2(acc[0], acc[1]);
                         sum = both.x + both.y;
                     };
-                    load();
-                    bool renew = e == x.lo;
-                    if (!renew) {
-                        weights();
-                        renew = named_bar_or(pair, 64, mine && (!(sum <= kMost) || m == -INFINITY));
-                        if (renew) load();  // nobody has written P over the scores yet
-                    }
-                    if (renew) {
-                        float top[2];
+                    auto renew_max = [&](bool rescale) {
+                        float top[kN / 32];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < kN / 32; ++i) {
                             top[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
 #pragma unroll
                             for (int j = 2; j < 32; j += 2)
                                 top[i] = max3(top[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
                         }
-                        swap_max[half * kM] = fmaxf(top[0], top[1]);
-                        named_bar_sync(pair, 64);
-                        const float next = fmaxf(m, fmaxf(swap_max[0], swap_max[kM]));
+                        const float next = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
                         const float f = next == m ? 1.f : ex2((m - next) * c);
                         m = next;
                         l *= f;
-                        if (e > x.lo) {  // O holds the earlier tiles' sum, whose products have finished
+                        if (rescale) {  // O holds the earlier tiles' sum, whose products have finished
 #pragma unroll 1
-                            for (int i = 0; i < DP / 32; ++i) {
+                            for (int i = 0; i < DP / 16; ++i) {
                                 uint32_t o[16];
-                                const uint32_t at = t_o + half * (DP / 2) + 16 * i;
+                                const uint32_t at = t_o + 16 * i;
                                 tmem_ld16(at, o);
                                 tmem_ld_wait();
                                 tmem_ld_done(o);
@@ -334,10 +328,17 @@ __global__ void __launch_bounds__(NQ * 256 + 128, NQ == 1 ? 2 : 1)
                                 tmem_st16(at, o);
                             }
                         }
+                    };
+                    // a second pass only where the maximum has to be renewed (P is not yet over the scores)
+                    for (bool renew = e == x.lo;; renew = true) {
+                        load();
+                        if (renew) renew_max(e > x.lo);
                         weights();
+                        if (renew || !__any_sync(0xffffffffu, mine && (!(sum <= kMost) || m == -INFINITY))) break;
                     }
                     l += sum;
-                    tmem_st32(t_p, p);
+#pragma unroll
+                    for (int i = 0; i < kN / 64; ++i) tmem_st32(t_s + 32 * i, p[i]);
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -345,23 +346,18 @@ __global__ void __launch_bounds__(NQ * 256 + 128, NQ == 1 ? 2 : 1)
                 if (lane == 0) mbar_arrive(p_full + 8 * w);
             }
             if (x.hi > x.lo) {
-                wait(o_full + 8 * w, oc++ & 1u);
+                if (!wait(o_full + 8 * w, oc++ & 1u)) break;
                 tc_fence_after();
             }
             if (any) {
-                if (x.hi > x.lo) {  // the row's sum is both halves'
-                    swap_sum[half * kM] = l;
-                    named_bar_sync(pair, 64);
-                    l = swap_sum[0] + swap_sum[kM];
-                }
                 const bool store = mine && wait.ok;
-                const int pr = x.t.first + row;                       // packed row of the sample
-                const int64_t qi = x.t.q0 + pr / a.gp;
-                const int h = x.hs * a.gp + pr % a.gp;
+                const int pr = x.first + row;                       // packed row of the sample
+                const int64_t qi = x.q0 + (pr >> a.gp_log2);
+                const int h = x.head * a.gp + (pr & (a.gp - 1));
                 const float inv = x.hi > x.lo ? 1.f / l : 0.f;
                 const float lse = x.hi > x.lo ? (m * c + (log2f(l) - kLift)) * kLn2 : -INFINITY;
                 float* dst_l = a.splits > 1 ? a.part_lse + (size_t)x.part * a.hq * a.n_q : a.lse;
-                if (store && half == 0 && dst_l) dst_l[(int64_t)h * a.n_q + qi] = lse;
+                if (store && dst_l) dst_l[(int64_t)h * a.n_q + qi] = lse;
                 float* dst_p = a.part + (((size_t)x.part * a.n_q + qi) * a.hq + h) * a.d;
                 uint16_t* dst = head_row<uint16_t>(a.o, qi, h);
                 __syncwarp();
@@ -376,24 +372,25 @@ __global__ void __launch_bounds__(NQ * 256 + 128, NQ == 1 ? 2 : 1)
                     }
                 };
                 if (a.splits == 1 && a.d == DP) {
-                    // whole 128-byte lines of 64 columns: d = 128 one line a half, d = 64 the row by half 0
-                    if (DP == 128 || half == 0) {
+                    // whole 128-byte lines of 64 columns
+#pragma unroll 1
+                    for (int line = 0; line < DP / 64; ++line) {
                         uint32_t z[32];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             uint32_t o[32];
-                            columns(half * 64 + 32 * i, o);
+                            columns(line * 64 + 32 * i, o);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 const float2 v = two(o + 2 * j);
                                 z[16 * i + j] = pack2<BF16>(v.x * inv, v.y * inv);
                             }
                         }
-                        store_lines_quad(store ? reinterpret_cast<uint8_t*>(dst + half * 64) : nullptr, z, lane, v8ok);
+                        store_lines_quad(store ? reinterpret_cast<uint8_t*>(dst + line * 64) : nullptr, z, lane, v8ok);
                     }
                 } else {
 #pragma unroll 1
-                    for (int col = half * (DP / 2); col < min(a.d, (half + 1) * (DP / 2)); col += 32) {
+                    for (int col = 0; col < a.d; col += 32) {
                         uint32_t o[32];
                         columns(col, o);
                         if (store) {
@@ -424,10 +421,9 @@ int launch(const AttnArgs& a, const AttnMaps& maps, int sms, cudaStream_t s) {
     auto kernel = k_attn_tc_fwd<BF16, DP, NQ>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess)
         return VG_ERR_CUDA;
-    const int64_t tiles = attn_max_tiles(a.n_q, a.batch, a.gp, NQ * kM);
-    const int64_t units = tiles * (a.hq / a.gp) * a.splits;
-    const int64_t grid = std::min<int64_t>(units, (int64_t)sms * (NQ == 1 ? 2 : 1));
-    kernel<<<(unsigned)grid, C::kThreads, C::kSmem, s>>>(a, maps, (int)tiles);
+    const int64_t units = attn_max_tiles(a.n_q, a.batch, a.gp, NQ * kM) * (a.hq / a.gp) * a.splits;
+    const int64_t grid = std::min<int64_t>(units, (int64_t)sms * C::kPerSm);
+    kernel<<<(unsigned)grid, C::kThreads, C::kSmem, s>>>(a, maps);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 
