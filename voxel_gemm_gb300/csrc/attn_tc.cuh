@@ -115,6 +115,61 @@ __device__ __forceinline__ void store_cols32_f32(float* dst, const uint32_t (&ac
     }
 }
 
+// Whether whole 32-byte pieces of an output's rows can be stored.
+__device__ __forceinline__ bool lines_ok(const vg_heads& h) {
+    return ((reinterpret_cast<uintptr_t>(h.data) | (uintptr_t)(h.row_stride * 2) | (uintptr_t)(h.head_stride * 2)) &
+            31u) == 0;
+}
+
+// A thread's row of an accumulator of DP columns at `t` (lanes of its warp), times `mul`: to `dst` in 16 bits, or to
+// `part` in fp32 when the axis is cut.  have: the accumulator holds something (else zeros); store: the thread
+// has a row; live: the row is not zeros by definition.  By the whole warp.
+template <bool BF16, int DP>
+__device__ __forceinline__ void store_row(const AttnArgs& a, bool have, uint32_t t, float mul, bool store,
+                                          uint16_t* dst, float* part, int lane, bool v8ok, bool live = true) {
+    __syncwarp();
+    auto columns = [&](int col, uint32_t (&o)[32]) {
+        if (have) {
+            tmem_ld32(t + col, o);
+            tmem_ld_wait();
+            tmem_ld_done(o);
+        }
+        if (!have || !live) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+        __syncwarp();
+    };
+    if (a.splits == 1 && a.d == DP) {  // whole 128-byte lines of 64 columns
+#pragma unroll 1
+        for (int line = 0; line < DP / 64; ++line) {
+            uint32_t z[32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t o[32];
+                columns(line * 64 + 32 * i, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float2 v = two(o + 2 * j);
+                    z[16 * i + j] = pack2<BF16>(v.x * mul, v.y * mul);
+                }
+            }
+            store_lines_quad(store ? reinterpret_cast<uint8_t*>(dst + line * 64) : nullptr, z, lane, v8ok);
+        }
+    } else {
+#pragma unroll 1
+        for (int col = 0; col < a.d; col += 32) {
+            uint32_t o[32];
+            columns(col, o);
+            if (store) {
+                if (a.splits > 1) store_cols32_f32(part + col, o, mul, a.d - col);
+                else store_cols32<BF16>(dst + col, o, mul, a.d - col);
+            }
+            __syncwarp();
+        }
+    }
+}
+
 // Bounded waits of a whole warp, which goes on or gives up together; a wait that gives
 // up (after about 2 s of the SM's cycle counter) raises the block's abort flag, and the
 // warp's later waits return at once.  Every branch is on a vote, so that the compiler knows

@@ -47,43 +47,59 @@ template <bool BF16> constexpr float kDrop = BF16 ? 1.f : 1.f / 32768.f;
 // ================================================================ query gradient
 template <int DP, int NQ>
 struct CfgQ {
-    static constexpr int kThreads = NQ * 128 + 64;
+    static constexpr int kSoftWarps = NQ * 4;
+    static constexpr int kThreads = 32 * kSoftWarps + 128;
     static constexpr int kBlocks = DP / 64;
     static constexpr int kRowTile = kM * 128 * kBlocks;    // bytes of a Q or dO tile
     static constexpr int kKeyTile = kN * 128 * kBlocks;    // bytes of a K or V tile
-    static constexpr int S = DP == 64 ? 4 : 3;             // ring stages (a K and a V tile each)
-    static constexpr int kOCol = NQ * 2 * kN;
-    static constexpr int kTmem = NQ * (2 * kN + DP) <= 256 ? 256 : 512;
+    static constexpr int S = DP == 64 ? (NQ == 2 ? 6 : 4) : (NQ == 2 ? 3 : 4);  // ring stages (a K and a V tile each)
     static constexpr int kPerSm = NQ == 1 && DP == 64 ? 2 : 1;
-    static constexpr int kBars = 2 + 4 * NQ + 2 * S + 1;
-    static constexpr size_t kSmem = 1024 + (size_t)2 * NQ * kRowTile + (size_t)2 * S * kKeyTile + 8 * kBars + 16;
+    // dS in columns of its own where there is room (d <= 64), so that the next scores need not wait for the product
+    // that reads it; else over the scores
+    static constexpr bool kOwn = DP == 64;
+    static constexpr int kOCol = NQ * 2 * kN, kPCol = kOCol + NQ * DP;
+    static constexpr int kTmem = NQ * 256;
+    // q full, q empty, (s full, s empty, p full, p empty, o full, o empty) x NQ, (kv full, kv empty) x S, tail, done,
+    // unit ring
+    static constexpr int kBars = 2 + 6 * NQ + 2 * S + 2 + 2 * kUnitSlots;
+    static constexpr size_t kSmem = 1024 + (size_t)2 * NQ * kRowTile + (size_t)2 * S * kKeyTile +
+                                    kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
+    static constexpr int kRegs = NQ == 2 ? 168 : 128, kSoft = NQ == 2 ? 200 : 184, kAux = NQ == 2 ? 104 : 72;
+    static_assert(32 * kSoftWarps * kSoft + 128 * kAux <= kThreads * kRegs, "register split");
 };
-static_assert(CfgQ<128, 2>::kSmem <= 232448 && 2 * (CfgQ<64, 1>::kSmem + 1024) <= 233472, "shared memory");
+static_assert(CfgQ<128, 2>::kSmem <= 232448 && CfgQ<128, 1>::kSmem <= 232448 && CfgQ<64, 2>::kSmem <= 232448 &&
+                  2 * (CfgQ<64, 1>::kSmem + 1024) <= 233472,
+              "shared memory");
 
 template <bool BF16, int DP, int NQ>
-__global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
-    k_attn_tc_dq(const AttnArgs a, const __grid_constant__ AttnMaps maps, const int tiles) {
+__global__ void __launch_bounds__(CfgQ<DP, NQ>::kThreads, CfgQ<DP, NQ>::kPerSm)
+    k_attn_tc_dq(const AttnArgs a, const __grid_constant__ AttnMaps maps) {
     using C = CfgQ<DP, NQ>;
     constexpr int S = C::S;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sQ = smem_u32(smem), sG = sQ + NQ * C::kRowTile, sKV = sG + NQ * C::kRowTile;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)2 * NQ * C::kRowTile + (size_t)2 * S * C::kKeyTile);
+    int4* s_units = reinterpret_cast<int4*>(smem + (size_t)2 * NQ * C::kRowTile + (size_t)2 * S * C::kKeyTile);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_units + 3 * kUnitSlots);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile uint32_t* s_abort = s_tmem + 1;
     const uint32_t bar0 = smem_u32(bars);
     const uint32_t q_full = bar0, q_empty = bar0 + 8;
-    const uint32_t s_full = bar0 + 16, p_full = s_full + 8 * NQ, o_full = p_full + 8 * NQ, o_empty = o_full + 8 * NQ;
-    const uint32_t kv_full = o_empty + 8 * NQ, kv_empty = kv_full + 8 * S, done = kv_empty + 8 * S;
+    const uint32_t s_full = bar0 + 16, s_empty = s_full + 8 * NQ, p_full = s_empty + 8 * NQ, p_empty = p_full + 8 * NQ;
+    const uint32_t o_full = p_empty + 8 * NQ, o_empty = o_full + 8 * NQ;
+    const uint32_t kv_full = o_empty + 8 * NQ, kv_empty = kv_full + 8 * S, tail = kv_empty + 8 * S;
+    const uint32_t done = tail + 8, u_full = done + 8, u_empty = u_full + 8 * kUnitSlots;
 
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kLoader = NQ * 4, kIssuer = NQ * 4 + 1;
+    constexpr int kLoader = C::kSoftWarps, kIssuer = kLoader + 1, kScheduler = kLoader + 2;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int w = 0; w < NQ; ++w) {
             mbar_init(s_full + 8 * w, 1);
+            mbar_init(s_empty + 8 * w, 4);
             mbar_init(p_full + 8 * w, 4);
+            mbar_init(p_empty + 8 * w, 1);
             mbar_init(o_full + 8 * w, 1);
             mbar_init(o_empty + 8 * w, 4);
         }
@@ -91,6 +107,11 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
             mbar_init(kv_full + 8 * i, 1);
             mbar_init(kv_empty + 8 * i, 1);
         }
+        for (int i = 0; i < kUnitSlots; ++i) {
+            mbar_init(u_full + 8 * i, 1);
+            mbar_init(u_empty + 8 * i, C::kSoftWarps + 2);  // every reader: softmax warps, loader, issuer
+        }
+        mbar_init(tail, 1);
         mbar_init(done, 1);
         *s_abort = 0;
         fence_mbar_init();
@@ -110,128 +131,154 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
     tc_fence_after();
     const uint32_t tmem = uniform(*s_tmem);
 
-    const int sets = a.hq / a.gp;
     const int group = a.hq / a.hk;
-    const int64_t units = good ? (int64_t)tiles * sets * a.splits : 0;
-    struct Unit {
-        AttnTile t;
-        int hs, part, lo, hi, rows;
-    };
-    auto find = [&](int64_t u) {
-        Unit x;
-        x.t = attn_find_tile<false>(a, NQ * kM, u / sets);
-        x.hs = (int)(u % sets);
-        x.part = x.t.part;
-        x.rows = 0;
-        x.lo = x.hi = 0;
-        if (x.t.b >= 0) {
-            x.rows = min(NQ * kM, x.t.lq * a.gp - x.t.first);
-            attn_split(a, x.t.lk, x.part, &x.lo, &x.hi);
-        }
-        return x;
-    };
     Waiter wait{s_abort};
-
-    if (warp == kLoader) {
-        uint32_t it = 0, uc = 0;
-        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
-            const Unit x = find(u);
+    UnitRing ring{s_units, u_full, u_empty};
+    Unit x;
+    if (warp >= kLoader) reg_shrink<C::kAux>();
+    if (warp == kScheduler) {
+        // unit u = (row tile and part, head set): its rows and its key tiles [lo, hi)
+        const int sets = a.hq / a.gp;
+        for (int64_t u = blockIdx.x; good && wait.ok; u += gridDim.x) {
+            const AttnTile t = attn_find_tile<false>(a, NQ * kM, u / sets);
+            if (t.b < 0) break;
+            x = Unit{t.first, min(NQ * kM, t.lq * a.gp - t.first), (int)(u % sets), t.part, 0, 0,
+                     t.q0, t.lq, t.k0, t.lk, 0, 0};
+            attn_split(a, t.lk, t.part, &x.lo, &x.hi);
+            ring.put(wait, x);
+        }
+        x.rows = -1;
+        ring.put(wait, x);
+    } else if (warp == kLoader) {
+        RingPos<S> pos;
+        uint32_t n = 0, uc = 0, tc = 0;  // tiles and units loaded
+        while (ring.get(wait, x)) {
             if (x.hi <= x.lo) continue;
             wait(q_empty, (uc & 1u) ^ 1u);
             if (!wait.ok) break;
-            const int nq = x.rows > kM ? NQ : 1;
+            const int nq = x.rows > kM ? NQ : 1, kh = x.head * a.gp / group;
             one_lane([&] {
                 mbar_arrive_expect_tx(q_full, 2 * nq * C::kRowTile);
                 for (int w = 0; w < nq; ++w)
                     for (int b = 0; b < C::kBlocks; ++b) {
-                        const int row = x.t.q0 + (x.t.first + w * kM) / a.gp;
+                        const int row = x.q0 + ((x.first + w * kM) >> a.gp_log2);
                         const uint32_t off = w * C::kRowTile + b * kM * 128;
-                        tma_load_3d(sQ + off, &maps.q, b * 64, x.hs * a.gp, row, q_full);
-                        tma_load_3d(sG + off, &maps.go, b * 64, x.hs * a.gp, row, q_full);
+                        tma_load_3d(sQ + off, &maps.q, b * 64, x.head * a.gp, row, q_full);
+                        tma_load_3d(sG + off, &maps.go, b * 64, x.head * a.gp, row, q_full);
                     }
             });
             ++uc;
-            const int kh = x.hs * a.gp / group;
-            for (int e = x.lo; e < x.hi; ++e, ++it) {
-                const uint32_t st = it % S;
-                wait(kv_empty + 8 * st, ((it / S) & 1u) ^ 1u);
+            for (int e = x.lo; e < x.hi; ++e) {
+                const uint32_t k = sKV + 2 * pos.i * C::kKeyTile;
+                wait(kv_empty + 8 * pos.i, pos.phase ^ 1u);
                 if (!wait.ok) break;
+                const int left = min(kN, x.lk - e * kN), n16 = (left + 15) / 16 * 16;
+                const uint32_t bar = n16 != left ? tail : kv_full + 8 * pos.i;
                 one_lane([&] {
-                    mbar_arrive_expect_tx(kv_full + 8 * st, 2 * C::kKeyTile);
+                    mbar_arrive_expect_tx(bar, 2 * C::kKeyTile);
                     for (int b = 0; b < C::kBlocks; ++b) {
-                        const uint32_t dst = sKV + 2 * st * C::kKeyTile + b * kN * 128;
-                        tma_load_3d(dst, &maps.k, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
-                        tma_load_3d(dst + C::kKeyTile, &maps.v, b * 64, kh, x.t.k0 + e * kN, kv_full + 8 * st);
+                        tma_load_3d(k + b * kN * 128, &maps.k, b * 64, kh, x.k0 + e * kN, bar);
+                        tma_load_3d(k + C::kKeyTile + b * kN * 128, &maps.v, b * 64, kh, x.k0 + e * kN, bar);
                     }
                 });
+                if (n16 != left) {  // K rows past the sample's keys may hold anything: 0 x them must be 0 in dS K
+                    wait(tail, tc++ & 1u);
+                    zero_rows(k, left, n16, C::kBlocks, kN * 128);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kv_full + 8 * pos.i);
+                    __syncwarp();
+                }
+                pos.step();
+                ++n;
             }
         }
         // every copy has landed before the block may exit
         if (uc > 0 && !mbar_wait_timed(q_full, (uc - 1) & 1u)) wait.ok = false;
-        for (uint32_t i = 0; i < (uint32_t)S && i < it; ++i) {
-            const uint32_t last = it - 1 - i;
+        for (uint32_t i = 0; i < (uint32_t)S && i < n; ++i) {
+            const uint32_t last = n - 1 - i;
             if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;
-        const uint32_t idesc_o = idesc_f16_bn(BF16, ksteps * 16);
-        uint32_t it = 0, uc = 0, pc[NQ] = {}, oc[NQ] = {};
-        auto scores = [&](int w, uint32_t st, int n) {  // S_w = Q_w K^T and dP_w = dO_w V^T
-            const uint32_t id = idesc_f16(BF16, n), d = tmem + w * 2 * kN;
-            const uint32_t k = sKV + 2 * st * C::kKeyTile;
-            mma_channels<DP / 16, kM * 128, kN * 128>(d, sw128_kmajor_desc(sQ + w * C::kRowTile),
-                                                      sw128_kmajor_desc(k), id, ksteps);
-            mma_channels<DP / 16, kM * 128, kN * 128>(d + kN, sw128_kmajor_desc(sG + w * C::kRowTile),
-                                                      sw128_kmajor_desc(k + C::kKeyTile), id, ksteps);
-            mma_commit(s_full + 8 * w);
-        };
-        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
-            const Unit x = find(u);
+        const uint32_t idesc_s = idesc_f16(BF16, kN), idesc_o = idesc_f16_bn(BF16, ksteps * 16);
+        const uint64_t dq = sw128_kmajor_desc(sQ), dg = sw128_kmajor_desc(sG), dk = sw128_kmajor_desc(sKV);
+        const uint64_t dv = sw128_kmajor_desc(sKV + C::kKeyTile), dkt = sw128_mnmajor_desc(sKV, kN * 128);
+        RingPos<S> pos;
+        uint32_t uc = 0, pc[NQ] = {}, oc[NQ] = {}, sc[NQ] = {};
+        while (ring.get(wait, x)) {
             if (x.hi <= x.lo) continue;
-            const int nq = x.rows > kM ? NQ : 1;
-            auto left = [&](int e) { return min(kN, x.t.lk - e * kN); };
-            auto padded = [&](int e) { return (left(e) + 15) / 16 * 16; };
-            // K rows past the sample's keys may hold anything, and 0 x them must be 0 in dS K
-            auto arrive = [&](int e, uint32_t i) {
-                wait(kv_full + 8 * (i % S), (i / S) & 1u);
-                if (wait.ok && padded(e) != left(e)) {
-                    zero_rows(sKV + 2 * (i % S) * C::kKeyTile, left(e), padded(e), C::kBlocks, kN * 128);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
+            const bool both = NQ == 2 && x.rows > kM;
+            const int last16 = (min(kN, x.lk - (x.hi - 1) * kN) + 15) / 16;   // K = 16 steps of the last tile
+            // S_w = Q_w K^T and dP_w = dO_w V^T of the stage at `at`; `last`: the unit's last tile
+            auto scores = [&](auto wc, uint32_t at, bool last) {
+                constexpr int w = decltype(wc)::value;
+                const uint32_t id = last ? idesc_f16(BF16, last16 * 16) : idesc_s, ko = at * (2 * C::kKeyTile >> 4);
+                mma_channels<DP / 16, kM * 128, kN * 128>(tmem + w * 2 * kN, dq + w * (C::kRowTile >> 4), dk + ko, id,
+                                                          ksteps);
+                mma_channels<DP / 16, kM * 128, kN * 128>(tmem + w * 2 * kN + kN, dg + w * (C::kRowTile >> 4), dv + ko,
+                                                          id, ksteps);
+                mma_commit(s_full + 8 * w);
+            };
+            // the same behind the reads of the tile's previous scores (kOwn)
+            auto early = [&](auto wc, uint32_t at, bool last, bool final) {
+                constexpr int w = decltype(wc)::value;
+                if (!wait(s_empty + 8 * w, (sc[w]++ & 1u) ^ 1u)) return;
+                tc_fence_after();
+                one_lane([&] {
+                    scores(wc, at, last);
+                    if (final && last) mma_commit(q_empty);
+                });
             };
             wait(q_full, uc & 1u);
-            arrive(x.lo, it);
+            wait(kv_full + 8 * pos.i, pos.phase);
             if (!wait.ok) break;
-            tc_fence_after();
-            one_lane([&] {
-                for (int w = 0; w < nq; ++w) scores(w, it % S, padded(x.lo));
-                if (x.hi - x.lo == 1) mma_commit(q_empty);
-            });
-            for (int e = x.lo; e < x.hi; ++e, ++it) {
-                const uint32_t st = it % S, nx = (it + 1) % S;
-                const bool more = e + 1 < x.hi;
-                if (more) arrive(e + 1, it + 1);
-                const int n16 = padded(e);
-                for (int w = 0; w < nq; ++w) {
-                    wait(p_full + 8 * w, pc[w]++ & 1u);
-                    if (e == x.lo) wait(o_empty + 8 * w, (oc[w] & 1u) ^ 1u);
-                    if (!wait.ok) break;
+            const bool single = x.hi - x.lo == 1;
+            if constexpr (C::kOwn) {
+                early(Const<0>(), pos.i, single, !both);
+                if (both) early(Const<NQ - 1>(), pos.i, single, true);
+            } else {
+                tc_fence_after();
+                one_lane([&] {
+                    scores(Const<0>(), pos.i, single);
+                    if (both) scores(Const<NQ - 1>(), pos.i, single);
+                    if (single) mma_commit(q_empty);
+                });
+            }
+            for (int e = x.lo; e < x.hi; ++e) {
+                const uint32_t at = pos.i;
+                const bool more = e + 1 < x.hi, next_last = e + 2 == x.hi;
+                pos.step();
+                if (more) {
+                    wait(kv_full + 8 * pos.i, pos.phase);
+                    if constexpr (C::kOwn) {
+                        early(Const<0>(), pos.i, next_last, !both);
+                        if (both) early(Const<NQ - 1>(), pos.i, next_last, true);
+                    }
+                }
+                // dQ_w += dS_w K, then (over the scores' columns) the next scores
+                auto tile = [&](auto wc, bool final) {
+                    constexpr int w = decltype(wc)::value;
+                    if (e == x.lo) wait(o_empty + 8 * w, (oc[w]++ & 1u) ^ 1u);
+                    if (!wait(p_full + 8 * w, pc[w]++ & 1u)) return;
                     tc_fence_after();
                     one_lane([&] {
-                        mma_rows<kN / 16>(tmem + C::kOCol + w * DP, tmem + w * 2 * kN,
-                                          sw128_mnmajor_desc(sKV + 2 * st * C::kKeyTile, kN * 128), idesc_o, n16 / 16,
+                        mma_rows<kN / 16>(tmem + C::kOCol + w * DP,
+                                          tmem + (C::kOwn ? C::kPCol + w * (kN / 2) : w * 2 * kN),
+                                          dkt + at * (2 * C::kKeyTile >> 4), idesc_o, more ? kN / 16 : last16,
                                           e > x.lo);
-                        if (more) scores(w, nx, padded(e + 1));
-                        else mma_commit(o_full + 8 * w);
-                        if (w + 1 == nq) {
-                            mma_commit(kv_empty + 8 * st);
-                            if (e + 2 == x.hi) mma_commit(q_empty);
+                        if (C::kOwn) mma_commit(p_empty + 8 * w);
+                        if (!C::kOwn && more) scores(wc, pos.i, next_last);
+                        if (!more) mma_commit(o_full + 8 * w);
+                        if (final) {
+                            mma_commit(kv_empty + 8 * at);
+                            if (!C::kOwn && next_last) mma_commit(q_empty);
                         }
                     });
-                    if (!more) ++oc[w];
-                }
+                };
+                tile(Const<0>(), !both);
+                if (both) tile(Const<NQ - 1>(), true);
                 if (!wait.ok) break;
             }
             ++uc;
@@ -243,29 +290,30 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
             *s_abort = 1;
             atomicOr(a.err, kErrTimeout);
         }
-    } else {
+    } else if (warp < kLoader) {
+        reg_grow<C::kSoft>();
         const int w = warp >> 2, quad = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t t_s = t_lane + w * 2 * kN, t_o = t_lane + C::kOCol + w * DP;
+        const uint32_t t_p = C::kOwn ? t_lane + C::kPCol + w * (kN / 2) : t_s;
         const float c = a.scale_log2;
         const float2 lift = grad_lift<BF16>(a);
-        uint32_t sc = 0, oc = 0;
-        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
-            const Unit x = find(u);
+        const bool v8ok = lines_ok(a.gq);
+        const int row = w * kM + quad * 32 + lane;  // within the unit
+        uint32_t sc = 0, oc = 0, vc = 0;            // vc: tiles whose dS has been written
+        while (ring.get(wait, x)) {
             if (x.rows <= w * kM) continue;
-            const int row = w * kM + quad * 32 + lane;
-            const bool any = x.rows > w * kM + quad * 32, mine = row < x.rows;
-            const int pr = x.t.first + row;
+            const bool any = x.rows > w * kM + quad * 32, mine = row < x.rows;  // the warp, the thread has a row
+            const int pr = x.first + row;                                       // packed row of the sample
             float2 st = make_float2(0.f, 0.f);
-            if (mine) st = a.stats[((int64_t)x.hs * a.n_q + x.t.q0) * a.gp + pr];
-            const float base = st.x - kLift<BF16>, delta = st.y * lift.x;
-            const float2 c2 = make_float2(c, c), base2 = make_float2(-base, -base);
-            const float2 lift2 = make_float2(lift.x, lift.x), delta2 = make_float2(-delta, -delta);
+            if (mine) st = a.stats[((int64_t)x.head * a.n_q + x.q0) * a.gp + pr];
+            const float base = kLift<BF16> - st.x, delta = -st.y * lift.x;
+            const float2 c2 = make_float2(c, c), base2 = make_float2(base, base);
+            const float2 lift2 = make_float2(lift.x, lift.x), delta2 = make_float2(delta, delta);
             for (int e = x.lo; e < x.hi; ++e) {
-                wait(s_full + 8 * w, sc & 1u);
-                if (!wait.ok) break;
-                ++sc;
+                if (!wait(s_full + 8 * w, sc++ & 1u)) break;
                 tc_fence_after();
+                uint32_t d[32];
                 if (any) {
                     uint32_t s[2][32], g[2][32];
 #pragma unroll
@@ -276,20 +324,38 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 2; ++i) tmem_ld_done(s[i]), tmem_ld_done(g[i]);
-                    const int left = x.t.lk - e * kN;
-                    uint32_t d[32];
+                    if (C::kOwn) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_empty + 8 * w);
+                    }
+                    const int left = x.lk - e * kN;  // columns from there on are not scores: weight 0, gradient 0
+                    if (left < kN) {
+#pragma unroll
+                        for (int i = 0; i < kN; ++i)
+                            if (i >= left) s[i >> 5][i & 31] = 0xff800000u, g[i >> 5][i & 31] = 0u;
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const int r = j >> 4, i = 2 * (j & 15);
                         float2 p = fma2(two(&s[r][i]), c2, base2);
                         p = make_float2(ex2(p.x), ex2(p.y));
-                        float2 ds = BF16 ? add2(two(&g[r][i]), delta2) : fma2(two(&g[r][i]), lift2, delta2);
-                        ds = mul2(p, ds);
-                        if (2 * j >= left) ds.x = 0.f;
-                        if (2 * j + 1 >= left) ds.y = 0.f;
+                        const float2 dp = two(&g[r][i]);
+                        const float2 ds = mul2(p, BF16 ? add2(dp, delta2) : fma2(dp, lift2, delta2));
                         d[j] = pack2<BF16>(ds.x, ds.y);
                     }
-                    tmem_st32(t_s, d);
+                } else if (C::kOwn) {
+                    if (lane == 0) mbar_arrive(s_empty + 8 * w);
+                }
+                if (C::kOwn && vc > 0) {
+                    // the product that reads the last dS has finished.  Warps without rows wait as well: ahead of
+                    // the others, their arrivals for two tiles would add up to one early phase
+                    if (!wait(p_empty + 8 * w, (vc - 1) & 1u)) break;
+                    tc_fence_after();
+                }
+                ++vc;
+                if (any) {
+                    tmem_st32(t_p, d);
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -297,35 +363,16 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
                 if (lane == 0) mbar_arrive(p_full + 8 * w);
             }
             if (x.hi > x.lo) {
-                wait(o_full + 8 * w, oc & 1u);
-                if (!wait.ok) break;
-                ++oc;
+                if (!wait(o_full + 8 * w, oc++ & 1u)) break;
                 tc_fence_after();
             }
             if (any) {
-                const int64_t qi = x.t.q0 + pr / a.gp;
-                const int h = x.hs * a.gp + pr % a.gp;
-                const float mul = a.scale * kDrop<BF16> * lift.y;
-                float* dst_p = a.part + (((size_t)x.part * a.n_q + qi) * a.hq + h) * a.d;
-                uint16_t* dst = head_row<uint16_t>(a.gq, qi, h);
-#pragma unroll
-                for (int i = 0; i < DP / 32; ++i) {
-                    if (32 * i >= a.d) break;
-                    uint32_t o[32];
-                    if (x.hi > x.lo) {
-                        tmem_ld32(t_o + 32 * i, o);
-                        tmem_ld_wait();
-                        tmem_ld_done(o);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0u;
-                    }
-                    if (mine) {
-                        if (a.splits > 1) store_cols32_f32(dst_p + 32 * i, o, mul, a.d - 32 * i);
-                        else store_cols32<BF16>(dst + 32 * i, o, mul, a.d - 32 * i);
-                    }
-                    __syncwarp();
-                }
+                const bool store = mine && wait.ok;
+                const int64_t qi = x.q0 + (pr >> a.gp_log2);
+                const int h = x.head * a.gp + (pr & (a.gp - 1));
+                store_row<BF16, DP>(a, x.hi > x.lo, t_o, a.scale * kDrop<BF16> * lift.y, store,
+                                    head_row<uint16_t>(a.gq, qi, h),
+                                    a.part + (((size_t)x.part * a.n_q + qi) * a.hq + h) * a.d, lane, v8ok);
             }
             if (x.hi > x.lo) {
                 tc_fence_before();
@@ -342,42 +389,47 @@ __global__ void __launch_bounds__(NQ * 128 + 64, CfgQ<DP, NQ>::kPerSm)
 }
 
 // ================================================================ key and value gradients
-constexpr int kThreadsKV = 2 * 128 + 64;
+constexpr int kThreadsKV = 2 * 128 + 128;
 
 template <int DP>
 struct CfgKV {
     static constexpr int kBlocks = DP / 64;
     static constexpr int kKeyTile = kM * 128 * kBlocks;  // bytes of the K or V tile
     static constexpr int kRowTile = kN * 128 * kBlocks;  // bytes of a Q or dO step
-    static constexpr int S = 4;                          // ring stages (a Q and a dO step each)
+    static constexpr int S = DP == 64 ? 8 : 4;           // ring stages (a Q and a dO step each)
     static constexpr int kVCol = 4 * kN, kKCol = kVCol + DP;
     static constexpr int kTmem = 512;
-    // key tiles full, empty; S full x 2, P full x 2; gradients full, empty; ring full, empty; done
-    static constexpr int kBars = 2 + 4 + 2 + 2 * S + 1;
+    // key tiles full, empty; (S full, P full) x 2; gradients full, empty; (ring full, empty) x S; tail; done; unit ring
+    static constexpr int kBars = 2 + 4 + 2 + 2 * S + 2 + 2 * kUnitSlots;
     static constexpr size_t kStats = 8 * 2 * kN * sizeof(float2);  // eight warps, two steps each
-    static constexpr size_t kSmem = 1024 + 2 * kKeyTile + (size_t)2 * S * kRowTile + kStats + 8 * kBars + 16;
+    static constexpr size_t kSmem = 1024 + 2 * kKeyTile + (size_t)2 * S * kRowTile + kStats +
+                                    kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
+    static constexpr int kSoft = 200, kAux = 104;
+    static_assert(256 * kSoft + 128 * kAux <= kThreadsKV * 168, "register split");
 };
-static_assert(CfgKV<128>::kSmem <= 232448 && CfgKV<128>::kKCol + 128 <= 512, "shared memory, TMEM");
+static_assert(CfgKV<128>::kSmem <= 232448 && CfgKV<64>::kSmem <= 232448 && CfgKV<128>::kKCol + 128 <= 512,
+              "shared memory, TMEM");
 
 template <bool BF16, int DP>
 __global__ void __launch_bounds__(kThreadsKV, 1)
-    k_attn_tc_dkv(const AttnArgs a, const __grid_constant__ AttnMaps maps, const int tiles, float* part_dv) {
+    k_attn_tc_dkv(const AttnArgs a, const __grid_constant__ AttnMaps maps, float* part_dv) {
     using C = CfgKV<DP>;
     constexpr int S = C::S;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sK = smem_u32(smem), sV = sK + C::kKeyTile, sQG = sV + C::kKeyTile;
     float2* s_stats = reinterpret_cast<float2*>(smem + 2 * C::kKeyTile + (size_t)2 * S * C::kRowTile);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s_stats + 16 * kN);
+    int4* s_units = reinterpret_cast<int4*>(s_stats + 16 * kN);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_units + 3 * kUnitSlots);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile uint32_t* s_abort = s_tmem + 1;
     const uint32_t bar0 = smem_u32(bars);
     const uint32_t k_full = bar0, k_empty = bar0 + 8, s_full = bar0 + 16, p_full = bar0 + 32;
     const uint32_t o_full = bar0 + 48, o_empty = bar0 + 56, r_full = bar0 + 64, r_empty = r_full + 8 * S;
-    const uint32_t done = r_empty + 8 * S;
+    const uint32_t tail = r_empty + 8 * S, done = tail + 8, u_full = done + 8, u_empty = u_full + 8 * kUnitSlots;
 
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kLoader = 8, kIssuer = 9;
+    constexpr int kLoader = 8, kIssuer = 9, kScheduler = 10;
     if (threadIdx.x == 0) {
         mbar_init(k_full, 1);
         mbar_init(k_empty, 1);
@@ -391,6 +443,11 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             mbar_init(r_full + 8 * i, 1);
             mbar_init(r_empty + 8 * i, 1);
         }
+        for (int i = 0; i < kUnitSlots; ++i) {
+            mbar_init(u_full + 8 * i, 1);
+            mbar_init(u_empty + 8 * i, 8 + 2);  // every reader: softmax warps, loader, issuer
+        }
+        mbar_init(tail, 1);
         mbar_init(done, 1);
         *s_abort = 0;
         fence_mbar_init();
@@ -410,124 +467,131 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     tc_fence_after();
     const uint32_t tmem = uniform(*s_tmem);
 
-    const int sets_per_key = a.hq / a.hk / a.gp;  // head sets that read a key head
-    const int64_t units = good ? (int64_t)tiles * a.hk * a.splits : 0;
-    // unit u = (part, key head, key tile); its steps run over (head set, row tile in [lo, hi))
-    struct Unit {
-        AttnTile t;
-        int kh, part, lo, hi, steps;
-    };
-    auto find = [&](int64_t u) {
-        Unit x;
-        x.t = attn_find_tile<true>(a, kM, u / a.hk);
-        x.kh = (int)(u % a.hk);
-        x.part = x.t.part;
-        x.lo = x.hi = 0;
-        if (x.t.b >= 0 && x.t.first < x.t.lk) attn_split(a, (int64_t)x.t.lq * a.gp, x.part, &x.lo, &x.hi);
-        x.steps = (x.hi - x.lo) * sets_per_key;
-        return x;
-    };
+    const int sets = a.hq / a.hk / a.gp;  // head sets that read a key head
+    // A unit is (part and key tile, key head): rows = key rows of the tile, valid or not, [lo, hi) its row tiles of
+    // each head set.  Its steps run over (head set, row tile).
     Waiter wait{s_abort};
-
-    if (warp == kLoader) {
-        uint32_t it = 0, uc = 0;
-        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
-            const Unit x = find(u);
-            if (x.steps == 0) continue;
+    UnitRing ring{s_units, u_full, u_empty};
+    Unit x;
+    if (warp >= kLoader) reg_shrink<C::kAux>();
+    if (warp == kScheduler) {
+        for (int64_t u = blockIdx.x; good && wait.ok; u += gridDim.x) {
+            const AttnTile t = attn_find_tile<true>(a, kM, u / a.hk);
+            if (t.b < 0) break;
+            x = Unit{t.first, min(kM, t.krows - t.first), (int)(u % a.hk), t.part, 0, 0, t.q0, t.lq, t.k0, t.lk, 0, 0};
+            if (t.first < t.lk) attn_split(a, (int64_t)t.lq * a.gp, t.part, &x.lo, &x.hi);
+            ring.put(wait, x);
+        }
+        x.rows = -1;
+        ring.put(wait, x);
+    } else if (warp == kLoader) {
+        RingPos<S> pos;
+        uint32_t n = 0, uc = 0, tc = 0;  // steps and units loaded
+        while (ring.get(wait, x)) {
+            if (x.hi <= x.lo) continue;
             wait(k_empty, (uc & 1u) ^ 1u);
             if (!wait.ok) break;
             one_lane([&] {
                 mbar_arrive_expect_tx(k_full, 2 * C::kKeyTile);
                 for (int b = 0; b < C::kBlocks; ++b) {
-                    tma_load_3d(sK + b * kM * 128, &maps.k, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
-                    tma_load_3d(sV + b * kM * 128, &maps.v, b * 64, x.kh, x.t.k0 + x.t.first, k_full);
+                    tma_load_3d(sK + b * kM * 128, &maps.k, b * 64, x.head, x.k0 + x.first, k_full);
+                    tma_load_3d(sV + b * kM * 128, &maps.v, b * 64, x.head, x.k0 + x.first, k_full);
                 }
             });
             ++uc;
-            for (int hs = 0; hs < sets_per_key && wait.ok; ++hs)
-                for (int e = x.lo; e < x.hi; ++e, ++it) {
-                    const uint32_t st = it % S;
-                    wait(r_empty + 8 * st, ((it / S) & 1u) ^ 1u);
+            for (int hs = 0; hs < sets && wait.ok; ++hs)
+                for (int e = x.lo; e < x.hi; ++e) {
+                    const uint32_t q = sQG + 2 * pos.i * C::kRowTile;
+                    wait(r_empty + 8 * pos.i, pos.phase ^ 1u);
                     if (!wait.ok) break;
-                    const int head = (x.kh * sets_per_key + hs) * a.gp, row = x.t.q0 + e * kN / a.gp;
+                    const int left = min(kN, x.lq * a.gp - e * kN), n16 = (left + 15) / 16 * 16;
+                    const uint32_t bar = n16 != left ? tail : r_full + 8 * pos.i;
+                    const int head = (x.head * sets + hs) * a.gp, row = x.q0 + ((e * kN) >> a.gp_log2);
                     one_lane([&] {
-                        mbar_arrive_expect_tx(r_full + 8 * st, 2 * C::kRowTile);
+                        mbar_arrive_expect_tx(bar, 2 * C::kRowTile);
                         for (int b = 0; b < C::kBlocks; ++b) {
-                            const uint32_t dst = sQG + 2 * st * C::kRowTile + b * kN * 128;
-                            tma_load_3d(dst, &maps.q, b * 64, head, row, r_full + 8 * st);
-                            tma_load_3d(dst + C::kRowTile, &maps.go, b * 64, head, row, r_full + 8 * st);
+                            tma_load_3d(q + b * kN * 128, &maps.q, b * 64, head, row, bar);
+                            tma_load_3d(q + C::kRowTile + b * kN * 128, &maps.go, b * 64, head, row, bar);
                         }
                     });
+                    if (n16 != left) {  // rows of the next sample: 0 x them must be 0 in dS^T Q and P^T dO
+                        wait(tail, tc++ & 1u);
+                        zero_rows(q, left, n16, C::kBlocks, kN * 128);
+                        zero_rows(q + C::kRowTile, left, n16, C::kBlocks, kN * 128);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(r_full + 8 * pos.i);
+                        __syncwarp();
+                    }
+                    pos.step();
+                    ++n;
                 }
         }
         // every copy has landed before the block may exit
         if (uc > 0 && !mbar_wait_timed(k_full, (uc - 1) & 1u)) wait.ok = false;
-        for (uint32_t i = 0; i < (uint32_t)S && i < it; ++i) {
-            const uint32_t last = it - 1 - i;
+        for (uint32_t i = 0; i < (uint32_t)S && i < n; ++i) {
+            const uint32_t last = n - 1 - i;
             if (!mbar_wait_timed(r_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;
-        const uint32_t idesc_o = idesc_f16_bn(BF16, ksteps * 16);
-        uint32_t it = 0, uc = 0, pc[2] = {0, 0};
-        // steps alternate between the two score buffers across units too: step i of the block uses i & 1
-        auto scores = [&](uint32_t i, int n) {  // S^T = K Q^T and dP^T = V dO^T of step i
-            const uint32_t id = idesc_f16(BF16, n), st = i % S, w = i & 1u, d = tmem + w * 2 * kN;
-            const uint32_t q = sQG + 2 * st * C::kRowTile;
-            mma_channels<DP / 16, kM * 128, kN * 128>(d, sw128_kmajor_desc(sK), sw128_kmajor_desc(q), id, ksteps);
-            mma_channels<DP / 16, kM * 128, kN * 128>(d + kN, sw128_kmajor_desc(sV),
-                                                      sw128_kmajor_desc(q + C::kRowTile), id, ksteps);
-            mma_commit(s_full + 8 * w);
-        };
-        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
-            const Unit x = find(u);
-            if (x.steps == 0) continue;
-            const int rows = x.t.lq * a.gp, per = x.hi - x.lo;
-            auto left = [&](int i) { return min(kN, rows - (x.lo + i % per) * kN); };  // rows of step i of the unit
-            auto padded = [&](int i) { return (left(i) + 15) / 16 * 16; };
-            // the last rows of a step may be the next sample's, and 0 x them must be 0 in dS^T Q and P^T dO
-            auto arrive = [&](int i, uint32_t n) {
-                wait(r_full + 8 * (n % S), (n / S) & 1u);
-                if (wait.ok && padded(i) != left(i)) {
-                    const uint32_t q = sQG + 2 * (n % S) * C::kRowTile;
-                    zero_rows(q, left(i), padded(i), C::kBlocks, kN * 128);
-                    zero_rows(q + C::kRowTile, left(i), padded(i), C::kBlocks, kN * 128);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
+        const uint32_t idesc_s = idesc_f16(BF16, kN), idesc_o = idesc_f16_bn(BF16, ksteps * 16);
+        const uint64_t dk = sw128_kmajor_desc(sK), dv = sw128_kmajor_desc(sV), dq = sw128_kmajor_desc(sQG);
+        const uint64_t dqt = sw128_mnmajor_desc(sQG, kN * 128);
+        constexpr uint32_t kStage = 2 * C::kRowTile >> 4, kSecond = C::kRowTile >> 4;  // to the next stage, to dO
+        RingPos<S> ahead, pos;                // of the scores, two steps ahead, and of the gradients
+        uint32_t uc = 0, it = 0;              // it: steps of the block; step `it` uses score buffer it & 1
+        while (ring.get(wait, x)) {
+            if (x.hi <= x.lo) continue;
+            const int per = x.hi - x.lo, steps = per * sets;
+            const int rest = min(kN, x.lq * a.gp - (x.hi - 1) * kN), last16 = (rest + 15) / 16;
+            int ea = 0, eg = 0;               // row tiles (from lo) of the next scores and gradients
+            // S^T = K Q^T and dP^T = V dO^T of the next step, into buffer w
+            auto scores = [&](uint32_t w) {
+                const uint32_t id = ea + 1 == per ? idesc_f16(BF16, last16 * 16) : idesc_s, d = tmem + w * 2 * kN;
+                const uint64_t q = dq + ahead.i * kStage;
+                mma_channels<DP / 16, kM * 128, kN * 128>(d, dk, q, id, ksteps);
+                mma_channels<DP / 16, kM * 128, kN * 128>(d + kN, dv, q + kSecond, id, ksteps);
+                mma_commit(s_full + 8 * w);
+            };
+            auto advance = [&] {
+                ahead.step();
+                if (++ea == per) ea = 0;
             };
             wait(k_full, uc & 1u);
-            for (int i = 0; i < 2 && i < x.steps; ++i) {
-                arrive(i, it + i);
-                if (!wait.ok) break;
+            for (int i = 0; i < 2 && i < steps; ++i) {
+                if (!wait(r_full + 8 * ahead.i, ahead.phase)) break;
                 tc_fence_after();
                 one_lane([&] {
-                    scores(it + i, padded(i));
-                    if (x.steps <= 2 && i + 1 == x.steps) mma_commit(k_empty);
+                    scores((it + i) & 1u);
+                    if (i + 1 == steps) mma_commit(k_empty);
                 });
+                advance();
+            }
+            wait(o_empty, (uc & 1u) ^ 1u);
+            if (!wait.ok) break;
+            for (int i = 0; i < steps; ++i, ++it) {
+                const uint32_t w = it & 1u, pt = tmem + w * 2 * kN;
+                const bool more = i + 2 < steps;
+                const int n = eg + 1 == per ? last16 : kN / 16;
+                if (more) wait(r_full + 8 * ahead.i, ahead.phase);
+                if (!wait(p_full + 8 * w, (it >> 1) & 1u)) break;
+                tc_fence_after();
+                one_lane([&] {
+                    const uint64_t q = dqt + pos.i * kStage;
+                    mma_rows<kN / 16>(tmem + C::kVCol, pt, q + kSecond, idesc_o, n, i > 0);
+                    mma_rows<kN / 16>(tmem + C::kKCol, pt + kN, q, idesc_o, n, i > 0);
+                    mma_commit(r_empty + 8 * pos.i);
+                    if (more) scores(w);
+                    if (i + 3 == steps) mma_commit(k_empty);
+                    if (i + 1 == steps) mma_commit(o_full);
+                });
+                if (more) advance();
+                pos.step();
+                if (++eg == per) eg = 0;
             }
             if (!wait.ok) break;
-            wait(o_empty, (uc & 1u) ^ 1u);
-            for (int i = 0; i < x.steps; ++i, ++it) {
-                const uint32_t st = it % S, w = it & 1u;
-                const uint32_t q = sQG + 2 * st * C::kRowTile, g = q + C::kRowTile;
-                const int n16 = padded(i);
-                if (i + 2 < x.steps) arrive(i + 2, it + 2);
-                wait(p_full + 8 * w, pc[w]++ & 1u);
-                if (!wait.ok) break;
-                tc_fence_after();
-                const uint32_t pt = tmem + w * 2 * kN;
-                one_lane([&] {
-                    mma_rows<kN / 16>(tmem + C::kVCol, pt, sw128_mnmajor_desc(g, kN * 128), idesc_o, n16 / 16, i > 0);
-                    mma_rows<kN / 16>(tmem + C::kKCol, pt + kN, sw128_mnmajor_desc(q, kN * 128), idesc_o, n16 / 16,
-                                      i > 0);
-                    mma_commit(r_empty + 8 * st);
-                    if (i + 2 < x.steps) scores(it + 2, padded(i + 2));
-                    if (i + 3 == x.steps) mma_commit(k_empty);
-                    if (i + 1 == x.steps) mma_commit(o_full);
-                });
-            }
             ++uc;
         }
         // every product has finished before TMEM is released
@@ -537,104 +601,94 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             *s_abort = 1;
             atomicOr(a.err, kErrTimeout);
         }
-    } else {
+    } else if (warp < kLoader) {
+        reg_grow<C::kSoft>();
         const int w = warp >> 2, quad = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t t_s = t_lane + w * 2 * kN;
         const float c = a.scale_log2;
         const float2 lift = grad_lift<BF16>(a);
         const float2 c2 = make_float2(c, c), lift2 = make_float2(lift.x, lift.x);
+        const bool v8ok = lines_ok(w == 0 ? a.gv : a.gk);
         float2* my_stats = s_stats + warp * 2 * kN;
         uint32_t it = 0, sc = 0, uc = 0;
-        for (int64_t u = blockIdx.x; u < units && wait.ok; u += gridDim.x) {
-            const Unit x = find(u);
-            if (x.t.b < 0) continue;
-            const int rows = x.t.lq * a.gp, per = x.hi - x.lo;
-            // statistics (lse log2 e, delta) of rows lane and lane + 32 of step i, kept negated, a copy per warp
-            auto stat = [&](int i, int r0) {
+        while (ring.get(wait, x)) {
+            const int rows = x.lq * a.gp, per = x.hi - x.lo, steps = per * sets;
+            // Statistics (lse log2 e, delta) of rows lane and lane + 32 of a row tile, kept negated, a copy per warp;
+            // (hs, e): head set and row tile of the group's next step
+            int hs = x.head * sets, e = x.lo;
+            auto skip = [&] {
+                if (++e == x.hi) e = x.lo, ++hs;
+            };
+            auto stat = [&](bool have, int r0) {
+                const int r = e * kN + r0 + lane;
                 float2 v = make_float2(0.f, 0.f);
-                if (i < x.steps) {
-                    const int hs = x.kh * sets_per_key + i / per, r = (x.lo + i % per) * kN + r0 + lane;
-                    if (r < rows) v = a.stats[((int64_t)hs * a.n_q + x.t.q0) * a.gp + r];
-                }
+                if (have && r < rows) v = a.stats[((int64_t)hs * a.n_q + x.q0) * a.gp + r];
                 return v;
             };
             int i = (int)((w ^ it) & 1u);  // this group's first step of the unit
-            float2 next0 = stat(i, 0), next1 = stat(i, 32);
-            for (; i < x.steps; i += 2) {
+            if (i == 1 && steps > 0) skip();
+            float2 next0 = stat(i < steps, 0), next1 = stat(i < steps, 32);
+            for (; i < steps; i += 2) {
+                const int left = rows - e * kN;
                 float2* cur = my_stats + (sc & 1u) * kN;
                 cur[lane] = make_float2(kLift<BF16> - next0.x, -next0.y * lift.x);
                 cur[lane + 32] = make_float2(kLift<BF16> - next1.x, -next1.y * lift.x);
                 __syncwarp();
-                next0 = stat(i + 2, 0);
-                next1 = stat(i + 2, 32);
-                wait(s_full + 8 * w, sc & 1u);
-                if (!wait.ok) break;
+                skip();
+                skip();
+                next0 = stat(i + 2 < steps, 0);
+                next1 = stat(i + 2 < steps, 32);
+                if (!wait(s_full + 8 * w, sc & 1u)) break;
                 ++sc;
                 tc_fence_after();
-                const int left = rows - (x.lo + i % per) * kN;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t s[32], g[32], p[16], d[16];
-                    tmem_ld32(t_s + 32 * half, s);
-                    tmem_ld32(t_s + kN + 32 * half, g);
-                    tmem_ld_wait();
-                    tmem_ld_done(s);
-                    tmem_ld_done(g);
+                uint32_t s[2][32], g[2][32], p[32], d[32];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float4 st = *reinterpret_cast<const float4*>(cur + 32 * half + 2 * j);
-                        float2 pr = fma2(two(s + 2 * j), c2, make_float2(st.x, st.z));
-                        pr = make_float2(ex2(pr.x), ex2(pr.y));
-                        const float2 minus = make_float2(st.y, st.w);
-                        float2 ds = BF16 ? add2(two(g + 2 * j), minus) : fma2(two(g + 2 * j), lift2, minus);
-                        ds = mul2(pr, ds);
-                        if (32 * half + 2 * j >= left) pr.x = ds.x = 0.f;
-                        if (32 * half + 2 * j + 1 >= left) pr.y = ds.y = 0.f;
-                        p[j] = pack2<BF16>(pr.x, pr.y);
-                        d[j] = pack2<BF16>(ds.x, ds.y);
-                    }
-                    tmem_st16(t_s + 16 * half, p);
-                    tmem_st16(t_s + kN + 16 * half, d);
+                for (int h = 0; h < 2; ++h) {
+                    tmem_ld32(t_s + 32 * h, s[h]);
+                    tmem_ld32(t_s + kN + 32 * h, g[h]);
                 }
+                tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) tmem_ld_done(s[h]), tmem_ld_done(g[h]);
+                if (left < kN) {  // columns from there on are no rows of the sample: weight 0, gradient 0
+#pragma unroll
+                    for (int j = 0; j < kN; ++j)
+                        if (j >= left) s[j >> 5][j & 31] = 0xff800000u, g[j >> 5][j & 31] = 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int h = j >> 4, k = 2 * (j & 15);
+                    const float4 st = *reinterpret_cast<const float4*>(cur + 2 * j);
+                    float2 pr = fma2(two(&s[h][k]), c2, make_float2(st.x, st.z));
+                    pr = make_float2(ex2(pr.x), ex2(pr.y));
+                    const float2 minus = make_float2(st.y, st.w);
+                    const float2 ds = mul2(pr, BF16 ? add2(two(&g[h][k]), minus) : fma2(two(&g[h][k]), lift2, minus));
+                    p[j] = pack2<BF16>(pr.x, pr.y);
+                    d[j] = pack2<BF16>(ds.x, ds.y);
+                }
+                tmem_st32(t_s, p);
+                tmem_st32(t_s + kN, d);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * w);
             }
-            it += x.steps;
-            if (x.steps > 0) {
-                wait(o_full, uc & 1u);
-                if (!wait.ok) break;
+            it += steps;
+            if (steps > 0) {
+                if (!wait(o_full, uc & 1u)) break;
                 ++uc;
                 tc_fence_after();
             }
-            // group 0 writes dV, group 1 dK
-            const int r = x.t.first + quad * 32 + lane;
-            const bool mine = r < x.t.krows, live = r < x.t.lk && x.steps > 0;
-            const int64_t row = x.t.k0 + r;
+            // group 0 writes dV, group 1 dK; key rows past the valid ones get zeros
+            const int r = quad * 32 + lane;
+            const int64_t row = x.k0 + x.first + r;
             const float mul = w == 0 ? kDrop<BF16> : a.scale * kDrop<BF16> * lift.y;
-            float* dst_p = (w == 0 ? part_dv : a.part) + (((size_t)x.part * a.n_k + row) * a.hk + x.kh) * a.d;
-            uint16_t* dst = head_row<uint16_t>(w == 0 ? a.gv : a.gk, row, x.kh);
-#pragma unroll
-            for (int i2 = 0; i2 < DP / 32; ++i2) {
-                if (32 * i2 >= a.d) break;
-                uint32_t o[32];
-                if (x.steps > 0) {
-                    tmem_ld32(t_lane + (w == 0 ? C::kVCol : C::kKCol) + 32 * i2, o);
-                    tmem_ld_wait();
-                    tmem_ld_done(o);
-                }
-                if (!live)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0u;
-                if (mine) {
-                    if (a.splits > 1) store_cols32_f32(dst_p + 32 * i2, o, mul, a.d - 32 * i2);
-                    else store_cols32<BF16>(dst + 32 * i2, o, mul, a.d - 32 * i2);
-                }
-                __syncwarp();
-            }
-            if (x.steps > 0) {
+            float* dst_p = (w == 0 ? part_dv : a.part) + (((size_t)x.part * a.n_k + row) * a.hk + x.head) * a.d;
+            store_row<BF16, DP>(a, steps > 0, t_lane + (w == 0 ? C::kVCol : C::kKCol), mul, r < x.rows && wait.ok,
+                                head_row<uint16_t>(w == 0 ? a.gv : a.gk, row, x.head), dst_p, lane, v8ok,
+                                x.first + r < x.lk);
+            if (steps > 0) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(o_empty);
@@ -654,10 +708,9 @@ int launch_dq(const AttnArgs& a, const AttnMaps& maps, int sms, cudaStream_t s) 
     auto kernel = k_attn_tc_dq<BF16, DP, NQ>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess)
         return VG_ERR_CUDA;
-    const int64_t tiles = attn_max_tiles(a.n_q, a.batch, a.gp, NQ * kM);
-    const int64_t units = tiles * (a.hq / a.gp) * a.splits;
+    const int64_t units = attn_max_tiles(a.n_q, a.batch, a.gp, NQ * kM) * (a.hq / a.gp) * a.splits;
     const int64_t grid = std::min<int64_t>(units, (int64_t)sms * C::kPerSm);
-    kernel<<<(unsigned)grid, C::kThreads, C::kSmem, s>>>(a, maps, (int)tiles);
+    kernel<<<(unsigned)grid, C::kThreads, C::kSmem, s>>>(a, maps);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 
@@ -667,9 +720,8 @@ int launch_dkv(const AttnArgs& a, const AttnMaps& maps, float* part_dv, int sms,
     auto kernel = k_attn_tc_dkv<BF16, DP>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess)
         return VG_ERR_CUDA;
-    const int64_t tiles = attn_max_tiles(a.n_k, a.batch, 1, kM);
-    const int64_t units = tiles * a.hk * a.splits;
-    kernel<<<(unsigned)std::min<int64_t>(units, sms), kThreadsKV, C::kSmem, s>>>(a, maps, (int)tiles, part_dv);
+    const int64_t units = attn_max_tiles(a.n_k, a.batch, 1, kM) * a.hk * a.splits;
+    kernel<<<(unsigned)std::min<int64_t>(units, sms), kThreadsKV, C::kSmem, s>>>(a, maps, part_dv);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 

@@ -261,8 +261,7 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
         const float c = a.scale_log2;
         constexpr float kLift = BF16 ? 0.f : 7.f;            // exponent added to the weights
         constexpr float kMost = BF16 ? 0x1p64f : 0x1p14f;    // of a tile's sum before the maximum is replaced
-        const bool v8ok = ((reinterpret_cast<uintptr_t>(a.o.data) | (uintptr_t)(a.o.row_stride * 2) |
-                            (uintptr_t)(a.o.head_stride * 2)) & 31u) == 0;
+        const bool v8ok = lines_ok(a.o);
         const int row = w * kM + quad * 32 + lane;           // within the unit
         uint32_t sc = 0, oc = 0;
         while (ring.get(wait, x)) {
@@ -358,48 +357,8 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                 const float lse = x.hi > x.lo ? (m * c + (log2f(l) - kLift)) * kLn2 : -INFINITY;
                 float* dst_l = a.splits > 1 ? a.part_lse + (size_t)x.part * a.hq * a.n_q : a.lse;
                 if (store && dst_l) dst_l[(int64_t)h * a.n_q + qi] = lse;
-                float* dst_p = a.part + (((size_t)x.part * a.n_q + qi) * a.hq + h) * a.d;
-                uint16_t* dst = head_row<uint16_t>(a.o, qi, h);
-                __syncwarp();
-                auto columns = [&](int col, uint32_t (&o)[32]) {
-                    if (x.hi > x.lo) {
-                        tmem_ld32(t_o + col, o);
-                        tmem_ld_wait();
-                        tmem_ld_done(o);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0u;
-                    }
-                };
-                if (a.splits == 1 && a.d == DP) {
-                    // whole 128-byte lines of 64 columns
-#pragma unroll 1
-                    for (int line = 0; line < DP / 64; ++line) {
-                        uint32_t z[32];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t o[32];
-                            columns(line * 64 + 32 * i, o);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float2 v = two(o + 2 * j);
-                                z[16 * i + j] = pack2<BF16>(v.x * inv, v.y * inv);
-                            }
-                        }
-                        store_lines_quad(store ? reinterpret_cast<uint8_t*>(dst + line * 64) : nullptr, z, lane, v8ok);
-                    }
-                } else {
-#pragma unroll 1
-                    for (int col = 0; col < a.d; col += 32) {
-                        uint32_t o[32];
-                        columns(col, o);
-                        if (store) {
-                            if (a.splits > 1) store_cols32_f32(dst_p + col, o, inv, a.d - col);
-                            else store_cols32<BF16>(dst + col, o, inv, a.d - col);
-                        }
-                        __syncwarp();
-                    }
-                }
+                store_row<BF16, DP>(a, x.hi > x.lo, t_o, inv, store, head_row<uint16_t>(a.o, qi, h),
+                                    a.part + (((size_t)x.part * a.n_q + qi) * a.hq + h) * a.d, lane, v8ok);
             }
             if (x.hi > x.lo) {
                 tc_fence_before();
