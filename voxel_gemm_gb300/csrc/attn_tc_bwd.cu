@@ -61,7 +61,7 @@ struct CfgQ {
     static constexpr int kTmem = NQ * 256;
     // q full, q empty, (s full, s empty, p full, p empty, o full, o empty) x NQ, (kv full, kv empty) x S, tail, done,
     // unit ring
-    static constexpr int kBars = 2 + 6 * NQ + 2 * S + 2 + 2 * kUnitSlots;
+    static constexpr int kBars = 2 + 6 * NQ + 2 * S + 3 + 2 * kUnitSlots;
     static constexpr size_t kSmem = 1024 + (size_t)2 * NQ * kRowTile + (size_t)2 * S * kKeyTile +
                                     kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
     static constexpr int kRegs = NQ == 2 ? 168 : 128, kSoft = NQ == 2 ? 200 : 184, kAux = NQ == 2 ? 104 : 72;
@@ -88,10 +88,10 @@ __global__ void __launch_bounds__(CfgQ<DP, NQ>::kThreads, CfgQ<DP, NQ>::kPerSm)
     const uint32_t s_full = bar0 + 16, s_empty = s_full + 8 * NQ, p_full = s_empty + 8 * NQ, p_empty = p_full + 8 * NQ;
     const uint32_t o_full = p_empty + 8 * NQ, o_empty = o_full + 8 * NQ;
     const uint32_t kv_full = o_empty + 8 * NQ, kv_empty = kv_full + 8 * S, tail = kv_empty + 8 * S;
-    const uint32_t done = tail + 8, u_full = done + 8, u_empty = u_full + 8 * kUnitSlots;
+    const uint32_t done = tail + 8, u_full = done + 16, u_empty = u_full + 8 * kUnitSlots;
 
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kLoader = C::kSoftWarps, kIssuer = kLoader + 1, kScheduler = kLoader + 2;
+    constexpr int kLoader = C::kSoftWarps, kIssuer = kLoader + 1, kIssuer2 = kLoader + 2, kScheduler = kLoader + 3;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
@@ -109,10 +109,11 @@ __global__ void __launch_bounds__(CfgQ<DP, NQ>::kThreads, CfgQ<DP, NQ>::kPerSm)
         }
         for (int i = 0; i < kUnitSlots; ++i) {
             mbar_init(u_full + 8 * i, 1);
-            mbar_init(u_empty + 8 * i, C::kSoftWarps + 2);  // every reader: softmax warps, loader, issuer
+            mbar_init(u_empty + 8 * i, C::kSoftWarps + 2 + C::kOwn);  // every reader: softmax warps, loader, issuers
         }
         mbar_init(tail, 1);
         mbar_init(done, 1);
+        mbar_init(done + 8, 1);
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(CfgQ<DP, NQ>::kThreads, CfgQ<DP, NQ>::kPerSm)
             if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
-    } else if (warp == kIssuer) {
+    } else if (warp == kIssuer || (C::kOwn && warp == kIssuer2)) {
         const int ksteps = (a.d + 15) / 16;
         const uint32_t idesc_s = idesc_f16(BF16, kN), idesc_o = idesc_f16_bn(BF16, ksteps * 16);
         const uint64_t dq = sw128_kmajor_desc(sQ), dg = sw128_kmajor_desc(sG), dk = sw128_kmajor_desc(sKV);
@@ -231,61 +232,72 @@ __global__ void __launch_bounds__(CfgQ<DP, NQ>::kThreads, CfgQ<DP, NQ>::kPerSm)
                     if (final && last) mma_commit(q_empty);
                 });
             };
-            wait(q_full, uc & 1u);
-            wait(kv_full + 8 * pos.i, pos.phase);
-            if (!wait.ok) break;
-            const bool single = x.hi - x.lo == 1;
-            if constexpr (C::kOwn) {
-                early(Const<0>(), pos.i, single, !both);
-                if (both) early(Const<NQ - 1>(), pos.i, single, true);
-            } else {
+            // dQ_w += dS_w K of tile e in the stage at `at`, then (kOver) the next scores
+            auto grads = [&](auto wc, int e, uint32_t at, uint32_t next, bool final) {
+                constexpr int w = decltype(wc)::value;
+                const bool more = e + 1 < x.hi, next_last = e + 2 == x.hi;
+                if (e == x.lo) wait(o_empty + 8 * w, (oc[w]++ & 1u) ^ 1u);
+                if (!wait(p_full + 8 * w, pc[w]++ & 1u)) return;
                 tc_fence_after();
                 one_lane([&] {
-                    scores(Const<0>(), pos.i, single);
-                    if (both) scores(Const<NQ - 1>(), pos.i, single);
-                    if (single) mma_commit(q_empty);
+                    mma_rows<kN / 16>(tmem + C::kOCol + w * DP, tmem + (C::kOwn ? C::kPCol + w * (kN / 2) : w * 2 * kN),
+                                      dkt + at * (2 * C::kKeyTile >> 4), idesc_o, more ? kN / 16 : last16, e > x.lo);
+                    if (C::kOwn) mma_commit(p_empty + 8 * w);
+                    if (!C::kOwn && more) scores(wc, next, next_last);
+                    if (!more) mma_commit(o_full + 8 * w);
+                    if (final) {
+                        mma_commit(kv_empty + 8 * at);
+                        if (!C::kOwn && next_last) mma_commit(q_empty);
+                    }
                 });
-            }
-            for (int e = x.lo; e < x.hi; ++e) {
-                const uint32_t at = pos.i;
-                const bool more = e + 1 < x.hi, next_last = e + 2 == x.hi;
-                pos.step();
-                if (more) {
-                    wait(kv_full + 8 * pos.i, pos.phase);
-                    if constexpr (C::kOwn) {
-                        early(Const<0>(), pos.i, next_last, !both);
-                        if (both) early(Const<NQ - 1>(), pos.i, next_last, true);
+            };
+            const Const<0> first;
+            const Const<NQ - 1> second;
+            if constexpr (C::kOwn) {
+                // one warp issues the scores, another one the products with K: neither waits for the other's
+                if (warp == kIssuer) {
+                    wait(q_full, uc & 1u);
+                    for (int e = x.lo; e < x.hi && wait.ok; ++e) {
+                        const bool last = e + 1 == x.hi;
+                        wait(kv_full + 8 * pos.i, pos.phase);
+                        early(first, pos.i, last, !both);
+                        if (both) early(second, pos.i, last, true);
+                        pos.step();
+                    }
+                } else {
+                    for (int e = x.lo; e < x.hi && wait.ok; ++e) {
+                        wait(kv_full + 8 * pos.i, pos.phase);
+                        grads(first, e, pos.i, 0, !both);
+                        if (both) grads(second, e, pos.i, 0, true);
+                        pos.step();
                     }
                 }
-                // dQ_w += dS_w K, then (over the scores' columns) the next scores
-                auto tile = [&](auto wc, bool final) {
-                    constexpr int w = decltype(wc)::value;
-                    if (e == x.lo) wait(o_empty + 8 * w, (oc[w]++ & 1u) ^ 1u);
-                    if (!wait(p_full + 8 * w, pc[w]++ & 1u)) return;
-                    tc_fence_after();
-                    one_lane([&] {
-                        mma_rows<kN / 16>(tmem + C::kOCol + w * DP,
-                                          tmem + (C::kOwn ? C::kPCol + w * (kN / 2) : w * 2 * kN),
-                                          dkt + at * (2 * C::kKeyTile >> 4), idesc_o, more ? kN / 16 : last16,
-                                          e > x.lo);
-                        if (C::kOwn) mma_commit(p_empty + 8 * w);
-                        if (!C::kOwn && more) scores(wc, pos.i, next_last);
-                        if (!more) mma_commit(o_full + 8 * w);
-                        if (final) {
-                            mma_commit(kv_empty + 8 * at);
-                            if (!C::kOwn && next_last) mma_commit(q_empty);
-                        }
-                    });
-                };
-                tile(Const<0>(), !both);
-                if (both) tile(Const<NQ - 1>(), true);
+            } else {
+                const bool single = x.hi - x.lo == 1;
+                wait(q_full, uc & 1u);
+                wait(kv_full + 8 * pos.i, pos.phase);
                 if (!wait.ok) break;
+                tc_fence_after();
+                one_lane([&] {
+                    scores(first, pos.i, single);
+                    if (both) scores(second, pos.i, single);
+                    if (single) mma_commit(q_empty);
+                });
+                for (int e = x.lo; e < x.hi && wait.ok; ++e) {
+                    const uint32_t at = pos.i;
+                    pos.step();
+                    if (e + 1 < x.hi) wait(kv_full + 8 * pos.i, pos.phase);
+                    grads(first, e, at, pos.i, !both);
+                    if (both) grads(second, e, at, pos.i, true);
+                }
             }
+            if (!wait.ok) break;
             ++uc;
         }
         // every product has finished before TMEM is released
-        one_lane([&] { mma_commit(done); });
-        if (!mbar_wait_timed(done, 0)) wait.ok = false;
+        const uint32_t mine = done + 8 * (warp - kIssuer);
+        one_lane([&] { mma_commit(mine); });
+        if (!mbar_wait_timed(mine, 0)) wait.ok = false;
         if (!wait.ok && lane == 0) {
             *s_abort = 1;
             atomicOr(a.err, kErrTimeout);
@@ -398,10 +410,14 @@ struct CfgKV {
     static constexpr int kRowTile = kN * 128 * kBlocks;  // bytes of a Q or dO step
     static constexpr int S = DP == 64 ? 8 : 4;           // ring stages (a Q and a dO step each)
     static constexpr int kVCol = 4 * kN, kKCol = kVCol + DP;
+    // P and dS in columns of their own where there is room (d <= 64), else over the scores
+    static constexpr bool kOwn = DP == 64;
+    static constexpr int kPCol = kKCol + DP;
     static constexpr int kTmem = 512;
-    // key tiles full, empty; (S full, P full) x 2; gradients full, empty; (ring full, empty) x S; tail; done; unit ring
-    static constexpr int kBars = 2 + 4 + 2 + 2 * S + 2 + 2 * kUnitSlots;
-    static constexpr size_t kStats = 8 * 2 * kN * sizeof(float2);  // eight warps, two steps each
+    // key tiles full, empty; (S full, S empty, P full, P empty) x 2; gradients full, empty; (ring full, empty) x S;
+    // tail; done; unit ring
+    static constexpr int kBars = 2 + 8 + 2 + 2 * S + 3 + 2 * kUnitSlots;
+    static constexpr size_t kStats = 8 * 2 * 2 * kN * sizeof(float);  // eight warps, two steps, two numbers a row
     static constexpr size_t kSmem = 1024 + 2 * kKeyTile + (size_t)2 * S * kRowTile + kStats +
                                     kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
     static constexpr int kSoft = 200, kAux = 104;
@@ -418,24 +434,27 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sK = smem_u32(smem), sV = sK + C::kKeyTile, sQG = sV + C::kKeyTile;
-    float2* s_stats = reinterpret_cast<float2*>(smem + 2 * C::kKeyTile + (size_t)2 * S * C::kRowTile);
-    int4* s_units = reinterpret_cast<int4*>(s_stats + 16 * kN);
+    float* s_stats = reinterpret_cast<float*>(smem + 2 * C::kKeyTile + (size_t)2 * S * C::kRowTile);
+    int4* s_units = reinterpret_cast<int4*>(s_stats + 32 * kN);
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_units + 3 * kUnitSlots);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile uint32_t* s_abort = s_tmem + 1;
     const uint32_t bar0 = smem_u32(bars);
     const uint32_t k_full = bar0, k_empty = bar0 + 8, s_full = bar0 + 16, p_full = bar0 + 32;
-    const uint32_t o_full = bar0 + 48, o_empty = bar0 + 56, r_full = bar0 + 64, r_empty = r_full + 8 * S;
-    const uint32_t tail = r_empty + 8 * S, done = tail + 8, u_full = done + 8, u_empty = u_full + 8 * kUnitSlots;
+    const uint32_t s_empty = bar0 + 48, p_empty = bar0 + 64, o_full = bar0 + 80, o_empty = bar0 + 88;
+    const uint32_t r_full = bar0 + 96, r_empty = r_full + 8 * S;
+    const uint32_t tail = r_empty + 8 * S, done = tail + 8, u_full = done + 16, u_empty = u_full + 8 * kUnitSlots;
 
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kLoader = 8, kIssuer = 9, kScheduler = 10;
+    constexpr int kLoader = 8, kIssuer = 9, kIssuer2 = 10, kScheduler = 11;
     if (threadIdx.x == 0) {
         mbar_init(k_full, 1);
         mbar_init(k_empty, 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(s_full + 8 * w, 1);
             mbar_init(p_full + 8 * w, 4);
+            mbar_init(s_empty + 8 * w, 4);
+            mbar_init(p_empty + 8 * w, 1);
         }
         mbar_init(o_full, 1);
         mbar_init(o_empty, 8);
@@ -445,10 +464,11 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         }
         for (int i = 0; i < kUnitSlots; ++i) {
             mbar_init(u_full + 8 * i, 1);
-            mbar_init(u_empty + 8 * i, 8 + 2);  // every reader: softmax warps, loader, issuer
+            mbar_init(u_empty + 8 * i, 8 + 2 + C::kOwn);  // every reader: softmax warps, loader, issuers
         }
         mbar_init(tail, 1);
         mbar_init(done, 1);
+        mbar_init(done + 8, 1);
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -534,7 +554,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             if (!mbar_wait_timed(r_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
-    } else if (warp == kIssuer) {
+    } else if (warp == kIssuer || (C::kOwn && warp == kIssuer2)) {
         const int ksteps = (a.d + 15) / 16;
         const uint32_t idesc_s = idesc_f16(BF16, kN), idesc_o = idesc_f16_bn(BF16, ksteps * 16);
         const uint64_t dk = sw128_kmajor_desc(sK), dv = sw128_kmajor_desc(sV), dq = sw128_kmajor_desc(sQG);
@@ -559,35 +579,52 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                 ahead.step();
                 if (++ea == per) ea = 0;
             };
-            wait(k_full, uc & 1u);
-            for (int i = 0; i < 2 && i < steps; ++i) {
-                if (!wait(r_full + 8 * ahead.i, ahead.phase)) break;
+            // scores of step `n` of the block (kOwn: once the buffer's last ones have been read)
+            auto issue_scores = [&](uint32_t n, bool last) {
+                const uint32_t w = n & 1u;
+                wait(r_full + 8 * ahead.i, ahead.phase);
+                if (C::kOwn) wait(s_empty + 8 * w, ((n >> 1) & 1u) ^ 1u);
+                if (!wait.ok) return;
                 tc_fence_after();
                 one_lane([&] {
-                    scores((it + i) & 1u);
-                    if (i + 1 == steps) mma_commit(k_empty);
+                    scores(w);
+                    if (last) mma_commit(k_empty);
                 });
                 advance();
+            };
+            if (C::kOwn && warp == kIssuer) {  // the scores alone
+                wait(k_full, uc & 1u);
+                for (int i = 0; i < steps && wait.ok; ++i, ++it) issue_scores(it, i + 1 == steps);
+                if (!wait.ok) break;
+                ++uc;
+                continue;
+            }
+            if (!C::kOwn) {
+                wait(k_full, uc & 1u);
+                for (int i = 0; i < 2 && i < steps; ++i) issue_scores(it + i, i + 1 == steps);
             }
             wait(o_empty, (uc & 1u) ^ 1u);
             if (!wait.ok) break;
             for (int i = 0; i < steps; ++i, ++it) {
-                const uint32_t w = it & 1u, pt = tmem + w * 2 * kN;
+                const uint32_t w = it & 1u, sw = tmem + w * 2 * kN;
+                const uint32_t pt = C::kOwn ? tmem + C::kPCol + w * kN : sw, st = C::kOwn ? pt + kN / 2 : sw + kN;
                 const bool more = i + 2 < steps;
                 const int n = eg + 1 == per ? last16 : kN / 16;
-                if (more) wait(r_full + 8 * ahead.i, ahead.phase);
+                if (C::kOwn) wait(r_full + 8 * pos.i, pos.phase);
+                if (!C::kOwn && more) wait(r_full + 8 * ahead.i, ahead.phase);
                 if (!wait(p_full + 8 * w, (it >> 1) & 1u)) break;
                 tc_fence_after();
                 one_lane([&] {
                     const uint64_t q = dqt + pos.i * kStage;
                     mma_rows<kN / 16>(tmem + C::kVCol, pt, q + kSecond, idesc_o, n, i > 0);
-                    mma_rows<kN / 16>(tmem + C::kKCol, pt + kN, q, idesc_o, n, i > 0);
+                    mma_rows<kN / 16>(tmem + C::kKCol, st, q, idesc_o, n, i > 0);
                     mma_commit(r_empty + 8 * pos.i);
-                    if (more) scores(w);
-                    if (i + 3 == steps) mma_commit(k_empty);
+                    if (C::kOwn) mma_commit(p_empty + 8 * w);
+                    if (!C::kOwn && more) scores(w);
+                    if (!C::kOwn && i + 3 == steps) mma_commit(k_empty);
                     if (i + 1 == steps) mma_commit(o_full);
                 });
-                if (more) advance();
+                if (!C::kOwn && more) advance();
                 pos.step();
                 if (++eg == per) eg = 0;
             }
@@ -595,8 +632,9 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             ++uc;
         }
         // every product has finished before TMEM is released
-        one_lane([&] { mma_commit(done); });
-        if (!mbar_wait_timed(done, 0)) wait.ok = false;
+        const uint32_t mine = done + 8 * (warp - kIssuer);
+        one_lane([&] { mma_commit(mine); });
+        if (!mbar_wait_timed(mine, 0)) wait.ok = false;
         if (!wait.ok && lane == 0) {
             *s_abort = 1;
             atomicOr(a.err, kErrTimeout);
@@ -610,7 +648,8 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         const float2 lift = grad_lift<BF16>(a);
         const float2 c2 = make_float2(c, c), lift2 = make_float2(lift.x, lift.x);
         const bool v8ok = lines_ok(w == 0 ? a.gv : a.gk);
-        float2* my_stats = s_stats + warp * 2 * kN;
+        const uint32_t t_p = C::kOwn ? t_lane + C::kPCol + w * kN : t_s, t_d = C::kOwn ? t_p + kN / 2 : t_s + kN;
+        float* my_stats = s_stats + warp * 4 * kN;
         uint32_t it = 0, sc = 0, uc = 0;
         while (ring.get(wait, x)) {
             const int rows = x.lq * a.gp, per = x.hi - x.lo, steps = per * sets;
@@ -631,9 +670,11 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             float2 next0 = stat(i < steps, 0), next1 = stat(i < steps, 32);
             for (; i < steps; i += 2) {
                 const int left = rows - e * kN;
-                float2* cur = my_stats + (sc & 1u) * kN;
-                cur[lane] = make_float2(kLift<BF16> - next0.x, -next0.y * lift.x);
-                cur[lane + 32] = make_float2(kLift<BF16> - next1.x, -next1.y * lift.x);
+                float* cur = my_stats + (sc & 1u) * 2 * kN;  // [kN] of the first number, [kN] of the second
+                cur[lane] = kLift<BF16> - next0.x;
+                cur[lane + 32] = kLift<BF16> - next1.x;
+                cur[lane + kN] = -next0.y * lift.x;
+                cur[lane + kN + 32] = -next1.y * lift.x;
                 __syncwarp();
                 skip();
                 skip();
@@ -656,19 +697,34 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                     for (int j = 0; j < kN; ++j)
                         if (j >= left) s[j >> 5][j & 31] = 0xff800000u, g[j >> 5][j & 31] = 0u;
                 }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int h = j >> 4, k = 2 * (j & 15);
-                    const float4 st = *reinterpret_cast<const float4*>(cur + 2 * j);
-                    float2 pr = fma2(two(&s[h][k]), c2, make_float2(st.x, st.z));
-                    pr = make_float2(ex2(pr.x), ex2(pr.y));
-                    const float2 minus = make_float2(st.y, st.w);
-                    const float2 ds = mul2(pr, BF16 ? add2(two(&g[h][k]), minus) : fma2(two(&g[h][k]), lift2, minus));
-                    p[j] = pack2<BF16>(pr.x, pr.y);
-                    d[j] = pack2<BF16>(ds.x, ds.y);
+                if (C::kOwn) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty + 8 * w);
                 }
-                tmem_st32(t_s, p);
-                tmem_st32(t_s + kN, d);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float4 lse = *reinterpret_cast<const float4*>(cur + 2 * j);
+                    const float4 del = *reinterpret_cast<const float4*>(cur + kN + 2 * j);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int h = (j + t) >> 4, k = 2 * ((j + t) & 15);
+                        const float2 base = t == 0 ? make_float2(lse.x, lse.y) : make_float2(lse.z, lse.w);
+                        float2 pr = fma2(two(&s[h][k]), c2, base);
+                        pr = make_float2(ex2(pr.x), ex2(pr.y));
+                        const float2 minus = t == 0 ? make_float2(del.x, del.y) : make_float2(del.z, del.w);
+                        const float2 dp = two(&g[h][k]);
+                        const float2 ds = mul2(pr, BF16 ? add2(dp, minus) : fma2(dp, lift2, minus));
+                        p[j + t] = pack2<BF16>(pr.x, pr.y);
+                        d[j + t] = pack2<BF16>(ds.x, ds.y);
+                    }
+                }
+                if (C::kOwn && sc > 1) {  // the products that read the buffer's last P and dS have finished
+                    if (!wait(p_empty + 8 * w, sc & 1u)) break;
+                    tc_fence_after();
+                }
+                tmem_st32(t_p, p);
+                tmem_st32(t_d, d);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
