@@ -275,8 +275,8 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
         const int64_t units = attn_max_tiles(c.n_q, c.batch, p.gp, 128 * p.nq) * sets;
         const int slots = p.nq == 1 && c.d <= 64 ? 2 * p.sms : p.sms;
         f = cut_axis(units, tiles(c.n_k, 128), c.batch, slots, false);
-        q = cut_axis(units, tiles(c.n_k, 64), c.batch, slots, false);
-        k = cut_axis(attn_max_tiles(c.n_k, c.batch, 1, 128) * c.hk, tiles(c.n_q * p.gp, 64), c.batch, p.sms, true);
+        q = cut_axis(attn_max_tiles(c.n_q, c.batch, p.gp, 128) * sets, tiles(c.n_k, 128), c.batch, p.sms, false);
+        k = cut_axis(attn_max_tiles(c.n_k, c.batch, 1, 128) * c.hk, tiles(c.n_q * p.gp, 128), c.batch, p.sms, true);
     } else {
         f = q = cut_axis(qt * c.hq, tiles(c.n_k, 64), c.batch, 2 * p.sms, false);
         k = cut_axis(kt * c.hk, tiles(c.n_q, 64), c.batch, 2 * p.sms, false);
@@ -335,16 +335,16 @@ int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
         if ((st = VG_BY_TYPE(stats, a, s)) != VG_OK) return st;
         a.splits = p.s_dq;
         a.per_part = p.per_dq;
-        a.tile = 64;
+        a.tile = p.tc ? 128 : 64;
         a.part = reinterpret_cast<float*>(ws + p.off_dq);
-        st = p.tc ? attn_tc_dq(a, dtype, p.nq, p.sms, s) : attn_simt_dq(a, s);
+        st = p.tc ? attn_tc_dq(a, dtype, p.sms, s) : attn_simt_dq(a, s);
         if (st != VG_OK) return st;
         if (a.splits > 1 && (st = VG_BY_TYPE(join_queries, a, a.part, a.gq, s)) != VG_OK) return st;
     }
     if (a.n_k > 0) {
         a.splits = p.s_dkv;
         a.per_part = p.per_dkv;
-        a.tile = 64;
+        a.tile = p.tc ? 128 : 64;
         a.part = reinterpret_cast<float*>(ws + p.off_dk);
         float* part_dv = reinterpret_cast<float*>(ws + p.off_dv);
         st = p.tc ? attn_tc_dkv(a, part_dv, dtype, p.sms, s) : attn_simt_dkv(a, part_dv, s);

@@ -162,9 +162,9 @@ int attn_simt_fwd(const AttnArgs& a, cudaStream_t s);
 int attn_simt_dq(const AttnArgs& a, cudaStream_t s);
 int attn_simt_dkv(const AttnArgs& a, float* part_dv, cudaStream_t s);
 
-// ---- 16-bit path (attn_tc_fwd.cu, attn_tc_bwd.cu); nq: row tiles of a block ----
+// ---- 16-bit path (attn_tc_fwd.cu, attn_tc_bwd.cu); nq: row tiles of a forward block ----
 int attn_tc_fwd(const AttnArgs& a, int dtype, int nq, int sms, cudaStream_t s);
-int attn_tc_dq(const AttnArgs& a, int dtype, int nq, int sms, cudaStream_t s);
+int attn_tc_dq(const AttnArgs& a, int dtype, int sms, cudaStream_t s);
 int attn_tc_dkv(const AttnArgs& a, float* part_dv, int dtype, int sms, cudaStream_t s);
 
 }  // namespace vg

@@ -66,15 +66,16 @@ __device__ __forceinline__ void mma_channels(uint32_t d, uint64_t a, uint64_t b,
         mma_f16(d, a + ao, b + bo, idesc, j > 0);
     }
 }
-// D (+)= A B over `steps` (<= STEPS) K = 16 steps of rows, A in TMEM, B MN-major in shared memory.
-template <int STEPS>
+// D (+)= A B over `steps` (<= STEPS) K = 16 steps of rows, A in TMEM, B MN-major in shared memory.  GAP columns are
+// left out behind every second step's 8 of A.
+template <int STEPS, int GAP = 0>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int steps,
                                          uint32_t acc) {
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
         if (j >= steps) break;
         if (j == 0) mma_f16_ta(d, a, b, idesc, acc);
-        else mma_f16_ta(d, a + 8 * j, b + j * (2048 >> 4), idesc, 1);
+        else mma_f16_ta(d, a + 8 * j + (j >> 1) * GAP, b + j * (2048 >> 4), idesc, 1);
     }
 }
 
@@ -123,10 +124,12 @@ __device__ __forceinline__ bool lines_ok(const vg_heads& h) {
 
 // A thread's row of an accumulator of DP columns at `t` (lanes of its warp), times `mul`: to `dst` in 16 bits, or to
 // `part` in fp32 when the axis is cut.  have: the accumulator holds something (else zeros); store: the thread
-// has a row; live: the row is not zeros by definition.  By the whole warp.
+// has a row; live: the row is not zeros by definition; of, ofs: this warp does every ofs-th piece from `of` on.  By
+// the whole warp.
 template <bool BF16, int DP>
 __device__ __forceinline__ void store_row(const AttnArgs& a, bool have, uint32_t t, float mul, bool store,
-                                          uint16_t* dst, float* part, int lane, bool v8ok, bool live = true) {
+                                          uint16_t* dst, float* part, int lane, bool v8ok, bool live = true,
+                                          int of = 0, int ofs = 1) {
     __syncwarp();
     auto columns = [&](int col, uint32_t (&o)[32]) {
         if (have) {
@@ -142,7 +145,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, bool have, uint32_t
     };
     if (a.splits == 1 && a.d == DP) {  // whole 128-byte lines of 64 columns
 #pragma unroll 1
-        for (int line = 0; line < DP / 64; ++line) {
+        for (int line = of; line < DP / 64; line += ofs) {
             uint32_t z[32];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -158,7 +161,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, bool have, uint32_t
         }
     } else {
 #pragma unroll 1
-        for (int col = 0; col < a.d; col += 32) {
+        for (int col = 32 * of; col < a.d; col += 32 * ofs) {
             uint32_t o[32];
             columns(col, o);
             if (store) {
