@@ -67,9 +67,9 @@ __device__ __forceinline__ void block_max(float x, uint32_t* word) {
     }
 }
 
-// stats[packed row] = (lse * log2 e, sum_d dO O): a group of 1..16 lanes per row,
-// 16-byte loads; reads O and dO once, bound by memory.  fp16: also the largest norms
-// of a row of dO and of a valid row of V, which bound dP.
+// stats[packed row] = -lse * log2 e (+ 15 in fp16: the weights' exponent), -sum_d dO O: a group
+// of 1..16 lanes per row, 16-byte loads; reads O and dO once, bound by memory.  fp16: also
+// the largest norms of a row of dO and of a valid row of V, which bound dP.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int lanes) {
     const int lane = threadIdx.x & (lanes - 1);
@@ -97,8 +97,9 @@ __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int l
         }
         if (r < rows && lane == 0) {
             const int hs = h / a.gp;
-            a.stats[((int64_t)hs * a.n_q + i) * a.gp + (h - hs * a.gp)] =
-                make_float2(a.lse[(int64_t)h * a.n_q + i] * 1.4426950408889634f, sum);
+            float* st = a.stats + ((int64_t)hs * a.n_q + i) * a.gp + (h - hs * a.gp);
+            st[0] = fmaf(a.lse[(int64_t)h * a.n_q + i], -1.4426950408889634f, kHalf ? kHalfLift : 0.f);
+            st[rows] = -sum;
         }
     }
     if constexpr (kHalf) {
@@ -276,7 +277,7 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
         const int slots = p.nq == 1 && c.d <= 64 ? 2 * p.sms : p.sms;
         f = cut_axis(units, tiles(c.n_k, 128), c.batch, slots, false);
         q = cut_axis(attn_max_tiles(c.n_q, c.batch, p.gp, 128) * sets, tiles(c.n_k, 128), c.batch, p.sms, false);
-        k = cut_axis(attn_max_tiles(c.n_k, c.batch, 1, 128) * c.hk, tiles(c.n_q * p.gp, 128), c.batch, p.sms, true);
+        k = cut_axis(attn_max_tiles(c.n_k, c.batch, 1, 128) * c.hk, tiles(c.n_q * p.gp, 64), c.batch, p.sms, true);
     } else {
         f = q = cut_axis(qt * c.hq, tiles(c.n_k, 64), c.batch, 2 * p.sms, false);
         k = cut_axis(kt * c.hk, tiles(c.n_q, 64), c.batch, 2 * p.sms, false);
@@ -328,7 +329,7 @@ int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
     a.gp = p.gp;
     a.gp_log2 = __builtin_ctz((unsigned)p.gp);
     a.err = reinterpret_cast<uint32_t*>(ws);
-    a.stats = reinterpret_cast<float2*>(ws + 256);
+    a.stats = reinterpret_cast<float*>(ws + 256);
     int st;
     if (dtype == VG_F16) cudaMemsetAsync(a.err + 1, 0, 8, s);  // the largest norms, taken by the statistics kernel
     if (a.n_q > 0) {
@@ -344,7 +345,7 @@ int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
     if (a.n_k > 0) {
         a.splits = p.s_dkv;
         a.per_part = p.per_dkv;
-        a.tile = p.tc ? 128 : 64;
+        a.tile = 64;
         a.part = reinterpret_cast<float*>(ws + p.off_dk);
         float* part_dv = reinterpret_cast<float*>(ws + p.off_dv);
         st = p.tc ? attn_tc_dkv(a, part_dv, dtype, p.sms, s) : attn_simt_dkv(a, part_dv, s);

@@ -29,13 +29,21 @@ struct AttnArgs {
     float* lse;                  // [hq][n_q]
     // workspace
     uint32_t* err;               // error record; words 1, 2: fp32 bits of the largest |dO row|, |V row| (fp16)
-    float2* stats;               // [hq / gp][n_q * gp]: (lse * log2 e, sum_d dO O) of every packed row
+    float* stats;                // [2][hq / gp][n_q * gp], negated: lse * log2 e and sum_d dO O of every packed row
     // The axis that a kernel runs along is cut into parts of `per_part` tiles of `tile` rows, so that a sample has
     // attn_parts of them; splits bounds that number (1: not cut, results go to their place at once).
     int splits, per_part, tile;
     float* part;                 // results of the parts (layouts at their kernels)
     float* part_lse;
 };
+
+// fp16 has no exponent range to spare: the backward pass's weights (<= 1) carry 2^15.
+constexpr float kHalfLift = 15.f;
+
+// A packed row's statistics.
+__device__ __forceinline__ float2 attn_stats(const AttnArgs& a, int64_t row) {
+    return make_float2(a.stats[row], a.stats[a.n_q * a.hq + row]);
+}
 
 // The tile of one sample that a block works on.
 struct AttnTile {

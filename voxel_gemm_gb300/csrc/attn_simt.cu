@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = t.first + ty + 16 * i;
-        st[i] = r < t.lq ? a.stats[(int64_t)h * a.n_q + t.q0 + r] : make_float2(0.f, 0.f);
+        st[i] = r < t.lq ? attn_stats(a, (int64_t)h * a.n_q + t.q0 + r) : make_float2(0.f, 0.f);
     }
     float4 acc[4][NC];
     zero<NC>(acc);
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float pr = exp2f(s[i][j] * a.scale_log2 - st[i].x);
-                sS[(ty + 16 * i) * kPP + tx + 16 * j] = tx + 16 * j < left ? pr * (dp[i][j] - st[i].y) : 0.f;
+                const float pr = exp2f(s[i][j] * a.scale_log2 + st[i].x);
+                sS[(ty + 16 * i) * kPP + tx + 16 * j] = tx + 16 * j < left ? pr * (dp[i][j] + st[i].y) : 0.f;
             }
         __syncthreads();
         product_nn<NC>(sS, sK, a.d, ty, tx, acc);
@@ -279,13 +279,14 @@ __global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* 
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = tx + 16 * j;
-                const float2 st = c < left ? a.stats[(int64_t)h * a.n_q + t.q0 + qt * kT + c] : make_float2(0.f, 0.f);
+                const int64_t at = (int64_t)h * a.n_q + t.q0 + qt * kT + c;
+                const float2 st = c < left ? attn_stats(a, at) : make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const bool in = c < left && t.first + ty + 16 * i < t.lk;
-                    const float pr = in ? exp2f(s[i][j] * a.scale_log2 - st.x) : 0.f;
+                    const float pr = in ? exp2f(s[i][j] * a.scale_log2 + st.x) : 0.f;
                     sP[(ty + 16 * i) * kPP + c] = pr;
-                    sS[(ty + 16 * i) * kPP + c] = in ? pr * (dp[i][j] - st.y) : 0.f;
+                    sS[(ty + 16 * i) * kPP + c] = in ? pr * (dp[i][j] + st.y) : 0.f;
                 }
             }
             __syncthreads();

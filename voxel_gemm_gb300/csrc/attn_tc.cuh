@@ -66,16 +66,15 @@ __device__ __forceinline__ void mma_channels(uint32_t d, uint64_t a, uint64_t b,
         mma_f16(d, a + ao, b + bo, idesc, j > 0);
     }
 }
-// D (+)= A B over `steps` (<= STEPS) K = 16 steps of rows, A in TMEM, B MN-major in shared memory.  GAP columns are
-// left out behind every second step's 8 of A.
-template <int STEPS, int GAP = 0>
+// D (+)= A B over `steps` (<= STEPS) K = 16 steps of rows, A in TMEM, B MN-major in shared memory.
+template <int STEPS>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int steps,
                                          uint32_t acc) {
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
         if (j >= steps) break;
         if (j == 0) mma_f16_ta(d, a, b, idesc, acc);
-        else mma_f16_ta(d, a + 8 * j + (j >> 1) * GAP, b + j * (2048 >> 4), idesc, 1);
+        else mma_f16_ta(d, a + 8 * j, b + j * (2048 >> 4), idesc, 1);
     }
 }
 

@@ -10,18 +10,17 @@
 //
 // dQ: a persistent block takes 128 packed query rows and runs along the keys in tiles of
 // 128.  dK, dV: it takes 128 keys and runs along the packed rows of every query head that
-// reads them, 128 at a time, so gradients of shared heads are sums in the same accumulators.
-// Both have
-//   warps 0 .. 15   softmax: four threads per row of a 128 x 128 tile, 32 columns each
-//   then one warp   loader: TMA copies of the block's own tiles and of the tiles it runs along
-//   then two warps  issue the products: one S and dP, the other one the gradients (d > 64 in
-//                   dK, dV: one warp for all)
-//   then one warp   scheduler: finds the block's next units
+// reads them, 64 at a time, so gradients of shared heads are sums in the same accumulators.
+// Both have softmax warps, one warp that loads with TMA, one that finds the block's next
+// units, and two that issue the products: one S and dP, the other one the gradients.
+//   dQ        16 softmax warps, four threads per row, 32 columns each
+//   dK, dV    two groups of four, one thread per row, each group every second step
 // The 16-bit dS (and P) go to TMEM columns of their own, as first operands of the gradient
-// products: the next S and dP are computed while this tile's exponentials are.  (dK, dV with
-// d > 64 has no columns left: there they lie over the scores.)  Tiles are 128 wide because a
-// product of two shared-memory operands runs at the tensor cores' rate only from N = 128
-// on: at N = 64 it takes 48 cycles instead of 32 to read its operands.
+// products: the next S and dP are computed while this tile's exponentials are.  dK, dV with
+// d > 64 has no columns left: there they lie over the scores, and one warp issues all.
+// dQ's tiles are 128 wide because a product of two shared-memory operands runs at the tensor
+// cores' rate only from N = 128 on: at N = 64 it takes 48 cycles instead of 32 to read its
+// operands.
 //
 // fp16 has no exponent range to spare: P carries 2^15 (P <= 1), and dP - delta is divided by
 // a power of two above 2 max|dO row| max|V row|, which bounds it; both leave with the
@@ -35,12 +34,9 @@ namespace {
 using namespace attn_tc;
 
 constexpr int kM = 128;  // rows of the products
-constexpr int kN = 128;  // columns of a step
-constexpr int kH = 32;   // columns of a softmax thread
+constexpr int kN = 128;  // columns of dQ's steps
+constexpr int kH = 32;   // columns of its softmax threads
 constexpr int kThreads = 512 + 128;
-// A thread's 16-bit values take half the columns of its scores: packed when they have a place of their own, else over
-// the first half of those scores, which no other thread reads.
-template <bool OWN> constexpr int kGap = OWN ? 0 : kH / 2;
 
 // The power of two that dP - delta is multiplied by, and its inverse.
 template <bool BF16>
@@ -52,8 +48,7 @@ __device__ __forceinline__ float2 grad_lift(const AttnArgs& a) {
     return make_float2(__uint_as_float((uint32_t)(126 - e) << 23), __uint_as_float((uint32_t)(128 + e) << 23));
 }
 
-template <bool BF16> constexpr float kLift = BF16 ? 0.f : 15.f;             // exponent added to P
-template <bool BF16> constexpr float kDrop = BF16 ? 1.f : 1.f / 32768.f;
+template <bool BF16> constexpr float kDrop = BF16 ? 1.f : 1.f / (1 << (int)kHalfLift);  // what P carries, taken out
 
 // ================================================================ query gradient
 template <int DP>
@@ -254,8 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool any = x.rows > quad * 32, mine = row < x.rows;  // the warp, the thread has a row
             const int pr = x.first + row;                              // packed row of the sample
             float2 st = make_float2(0.f, 0.f);
-            if (mine) st = a.stats[((int64_t)x.head * a.n_q + x.q0) * a.gp + pr];
-            const float base = kLift<BF16> - st.x, delta = -st.y * lift.x;
+            if (mine) st = attn_stats(a, ((int64_t)x.head * a.n_q + x.q0) * a.gp + pr);
+            const float base = st.x, delta = st.y * lift.x;
             const float2 c2 = make_float2(c, c), base2 = make_float2(base, base);
             const float2 lift2 = make_float2(lift.x, lift.x), delta2 = make_float2(delta, delta);
             for (int e = x.lo; e < x.hi; ++e, ++n) {
@@ -327,62 +322,72 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ================================================================ key and value gradients
+constexpr int kNK = 64;  // rows of a step
+constexpr int kThreadsKV = 2 * 128 + 128;
+
 template <int DP>
 struct CfgKV {
     static constexpr int kBlocks = DP / 64;
-    static constexpr int kTile = kM * 128 * kBlocks;     // bytes of a K, V, Q or dO tile
-    static constexpr int S = DP == 64 ? 4 : 2;           // ring stages (a Q and a dO step each)
-    static constexpr int kVCol = 2 * kN, kKCol = kVCol + DP;
+    static constexpr int kKeyTile = kM * 128 * kBlocks;  // bytes of the K or V tile
+    static constexpr int kRowTile = kNK * 128 * kBlocks;  // bytes of a Q or dO step
+    static constexpr int S = DP == 64 ? 8 : 4;           // ring stages (a Q and a dO step each)
+    static constexpr int kVCol = 4 * kNK, kKCol = kVCol + DP;
     // P and dS in columns of their own where there is room (d <= 64), else over the scores
     static constexpr bool kOwn = DP == 64;
     static constexpr int kPCol = kKCol + DP;
-    // k, s, p and o (full, empty), (ring full, empty) x S, tail, done x 2, unit ring
-    static constexpr int kBars = 8 + 2 * S + 3 + 2 * kUnitSlots;
-    static constexpr size_t kStats = 16 * 2 * 2 * kH * sizeof(float);  // sixteen warps, two steps, two numbers a row
-    static constexpr size_t kSmem =
-        1024 + (size_t)(2 + 2 * S) * kTile + kStats + kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
+    static constexpr int kTmem = 512;
+    // key tiles full, empty; (S full, S empty, P full, P empty) x 2; gradients full, empty; (ring full, empty) x S;
+    // tail; done; unit ring
+    static constexpr int kBars = 2 + 8 + 2 + 2 * S + 3 + 2 * kUnitSlots;
+    static constexpr size_t kStats = S * 2 * kNK * sizeof(float);  // two numbers per row of a ring stage
+    static constexpr size_t kSmem = 1024 + 2 * kKeyTile + (size_t)2 * S * kRowTile + kStats +
+                                    kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
+    static constexpr int kSoft = 200, kAux = 104;
+    static_assert(256 * kSoft + 128 * kAux <= kThreadsKV * 168, "register split");
 };
-static_assert(CfgKV<128>::kSmem <= 232448 && CfgKV<64>::kSmem <= 232448 && CfgKV<128>::kKCol + 128 <= 512 &&
-                  CfgKV<64>::kPCol + kN <= 512,
+static_assert((CfgKV<64>::S & (CfgKV<64>::S - 1)) == 0 && (CfgKV<128>::S & (CfgKV<128>::S - 1)) == 0, "ring stages");
+static_assert(CfgKV<128>::kSmem <= 232448 && CfgKV<64>::kSmem <= 232448 && CfgKV<128>::kKCol + 128 <= 512,
               "shared memory, TMEM");
 
 template <bool BF16, int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsKV, 1)
     k_attn_tc_dkv(const AttnArgs a, const __grid_constant__ AttnMaps maps, float* part_dv) {
     using C = CfgKV<DP>;
     constexpr int S = C::S;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sK = smem_u32(smem), sV = sK + C::kTile, sQG = sV + C::kTile;
-    float* s_stats = reinterpret_cast<float*>(smem + (size_t)(2 + 2 * S) * C::kTile);
-    int4* s_units = reinterpret_cast<int4*>(s_stats + 64 * kH);
+    const uint32_t sK = smem_u32(smem), sV = sK + C::kKeyTile, sQG = sV + C::kKeyTile;
+    float* s_stats = reinterpret_cast<float*>(smem + 2 * C::kKeyTile + (size_t)2 * S * C::kRowTile);
+    int4* s_units = reinterpret_cast<int4*>(s_stats + S * 2 * kNK);
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_units + 3 * kUnitSlots);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile uint32_t* s_abort = s_tmem + 1;
     const uint32_t bar0 = smem_u32(bars);
-    const uint32_t k_full = bar0, k_empty = bar0 + 8, s_full = bar0 + 16, s_empty = bar0 + 24, p_full = bar0 + 32;
-    const uint32_t p_empty = bar0 + 40, o_full = bar0 + 48, o_empty = bar0 + 56;
-    const uint32_t r_full = bar0 + 64, r_empty = r_full + 8 * S, tail = r_empty + 8 * S;
-    const uint32_t done = tail + 8, u_full = done + 16, u_empty = u_full + 8 * kUnitSlots;
+    const uint32_t k_full = bar0, k_empty = bar0 + 8, s_full = bar0 + 16, p_full = bar0 + 32;
+    const uint32_t s_empty = bar0 + 48, p_empty = bar0 + 64, o_full = bar0 + 80, o_empty = bar0 + 88;
+    const uint32_t r_full = bar0 + 96, r_empty = r_full + 8 * S;
+    const uint32_t tail = r_empty + 8 * S, done = tail + 8, u_full = done + 16, u_empty = u_full + 8 * kUnitSlots;
 
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kLoader = 16, kIssuer = 17, kIssuer2 = 18, kScheduler = 19;
+    constexpr int kLoader = 8, kIssuer = 9, kIssuer2 = 10, kScheduler = 11;
     if (threadIdx.x == 0) {
         mbar_init(k_full, 1);
         mbar_init(k_empty, 1);
-        mbar_init(s_full, 1);
-        mbar_init(s_empty, 16);
-        mbar_init(p_full, 16);
-        mbar_init(p_empty, 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(s_full + 8 * w, 1);
+            mbar_init(p_full + 8 * w, 4);
+            mbar_init(s_empty + 8 * w, 4);
+            mbar_init(p_empty + 8 * w, 1);
+        }
         mbar_init(o_full, 1);
-        mbar_init(o_empty, 16);
+        mbar_init(o_empty, 8);
         for (int i = 0; i < S; ++i) {
-            mbar_init(r_full + 8 * i, 1);
+            mbar_init(r_full + 8 * i, 1 + 32);  // the tiles, and each lane's statistics
             mbar_init(r_empty + 8 * i, 1);
         }
         for (int i = 0; i < kUnitSlots; ++i) {
             mbar_init(u_full + 8 * i, 1);
-            mbar_init(u_empty + 8 * i, 16 + 2 + C::kOwn);  // every reader: softmax warps, loader, issuers
+            mbar_init(u_empty + 8 * i, 8 + 2 + C::kOwn);  // every reader: softmax warps, loader, issuers
         }
         mbar_init(tail, 1);
         mbar_init(done, 1);
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == kIssuer) {
-        tmem_alloc(smem_u32(s_tmem), 512);
+        tmem_alloc(smem_u32(s_tmem), C::kTmem);
         tmem_relinquish();
     }
     if (warp == kLoader && lane == 0) {
@@ -406,11 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = uniform(*s_tmem);
 
     const int sets = a.hq / a.hk / a.gp;  // head sets that read a key head
+    const int64_t plane = a.n_q * a.hq;   // from a row's first statistic to its second
     // A unit is (part and key tile, key head): rows = key rows of the tile, valid or not, [lo, hi) its row tiles of
     // each head set.  Its steps run over (head set, row tile).
     Waiter wait{s_abort};
     UnitRing ring{s_units, u_full, u_empty};
     Unit x;
+    if (warp >= kLoader) reg_shrink<C::kAux>();
     if (warp == kScheduler) {
         for (int64_t u = blockIdx.x; good && wait.ok; u += gridDim.x) {
             const AttnTile t = attn_find_tile<true>(a, kM, u / a.hk);
@@ -429,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(k_empty, (uc & 1u) ^ 1u);
             if (!wait.ok) break;
             one_lane([&] {
-                mbar_arrive_expect_tx(k_full, 2 * C::kTile);
+                mbar_arrive_expect_tx(k_full, 2 * C::kKeyTile);
                 for (int b = 0; b < C::kBlocks; ++b) {
                     tma_load_3d(sK + b * kM * 128, &maps.k, b * 64, x.head, x.k0 + x.first, k_full);
                     tma_load_3d(sV + b * kM * 128, &maps.v, b * 64, x.head, x.k0 + x.first, k_full);
@@ -438,23 +445,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++uc;
             for (int hs = 0; hs < sets && wait.ok; ++hs)
                 for (int e = x.lo; e < x.hi; ++e) {
-                    const uint32_t q = sQG + 2 * pos.i * C::kTile;
+                    const uint32_t q = sQG + 2 * pos.i * C::kRowTile;
                     wait(r_empty + 8 * pos.i, pos.phase ^ 1u);
                     if (!wait.ok) break;
-                    const int left = min(kN, x.lq * a.gp - e * kN), n16 = (left + 15) / 16 * 16;
+                    const int left = min(kNK, x.lq * a.gp - e * kNK), n16 = (left + 15) / 16 * 16;
                     const uint32_t bar = n16 != left ? tail : r_full + 8 * pos.i;
-                    const int head = (x.head * sets + hs) * a.gp, row = x.q0 + ((e * kN) >> a.gp_log2);
+                    const int head = (x.head * sets + hs) * a.gp, row = x.q0 + ((e * kNK) >> a.gp_log2);
                     one_lane([&] {
-                        mbar_arrive_expect_tx(bar, 2 * C::kTile);
+                        mbar_arrive_expect_tx(bar, 2 * C::kRowTile);
                         for (int b = 0; b < C::kBlocks; ++b) {
-                            tma_load_3d(q + b * kN * 128, &maps.q, b * 64, head, row, bar);
-                            tma_load_3d(q + C::kTile + b * kN * 128, &maps.go, b * 64, head, row, bar);
+                            tma_load_3d(q + b * kNK * 128, &maps.q, b * 64, head, row, bar);
+                            tma_load_3d(q + C::kRowTile + b * kNK * 128, &maps.go, b * 64, head, row, bar);
                         }
                     });
+                    const float* st = a.stats + ((int64_t)(x.head * sets + hs) * a.n_q + x.q0) * a.gp + e * kNK;
+                    const uint32_t to = smem_u32(s_stats + pos.i * 2 * kNK);
+                    for (int r = lane; r < kNK; r += 32) {  // rows past the sample: 0
+                        const bool in = r < left;
+                        cp_async4(to + 4 * r, in ? st + r : a.stats, in ? 4 : 0);
+                        cp_async4(to + 4 * (kNK + r), in ? st + plane + r : a.stats, in ? 4 : 0);
+                    }
+                    cp_async_arrive_noinc(r_full + 8 * pos.i);
+                    __syncwarp();
                     if (n16 != left) {  // rows of the next sample: 0 x them must be 0 in dS^T Q and P^T dO
                         wait(tail, tc++ & 1u);
-                        zero_rows(q, left, n16, C::kBlocks, kN * 128);
-                        zero_rows(q + C::kTile, left, n16, C::kBlocks, kN * 128);
+                        zero_rows(q, left, n16, C::kBlocks, kNK * 128);
+                        zero_rows(q + C::kRowTile, left, n16, C::kBlocks, kNK * 128);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(r_full + 8 * pos.i);
@@ -473,77 +489,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer || (C::kOwn && warp == kIssuer2)) {
         const int ksteps = (a.d + 15) / 16;
-        const uint32_t idesc_s = idesc_f16(BF16, kN), idesc_o = idesc_f16_bn(BF16, ksteps * 16);
+        const uint32_t idesc_s = idesc_f16(BF16, kNK), idesc_o = idesc_f16_bn(BF16, ksteps * 16);
         const uint64_t dk = sw128_kmajor_desc(sK), dv = sw128_kmajor_desc(sV), dq = sw128_kmajor_desc(sQG);
-        const uint64_t dqt = sw128_mnmajor_desc(sQG, kN * 128);
-        constexpr uint32_t kStage = 2 * C::kTile >> 4, kSecond = C::kTile >> 4;  // to the next stage, to dO
-        constexpr int G = kGap<C::kOwn>;
-        const uint32_t t_p = C::kOwn ? tmem + C::kPCol : tmem, t_d = C::kOwn ? t_p + kN / 2 : tmem + kN;
-        const bool do_scores = warp == kIssuer, do_grads = !C::kOwn || warp == kIssuer2;
-        RingPos<S> ahead, pos;                // stages of the scores and of the gradients
-        uint32_t uc = 0, n = 0;               // units and steps done
+        const uint64_t dqt = sw128_mnmajor_desc(sQG, kNK * 128);
+        constexpr uint32_t kStage = 2 * C::kRowTile >> 4, kSecond = C::kRowTile >> 4;  // to the next stage, to dO
+        RingPos<S> ahead, pos;                // of the scores, two steps ahead, and of the gradients
+        uint32_t uc = 0, it = 0;              // it: steps of the block; step `it` uses score buffer it & 1
         while (ring.get(wait, x)) {
             if (x.hi <= x.lo) continue;
             const int per = x.hi - x.lo, steps = per * sets;
-            const int last16 = (min(kN, x.lq * a.gp - (x.hi - 1) * kN) + 15) / 16;
+            const int rest = min(kNK, x.lq * a.gp - (x.hi - 1) * kNK), last16 = (rest + 15) / 16;
             int ea = 0, eg = 0;               // row tiles (from lo) of the next scores and gradients
-            // S^T = K Q^T and dP^T = V dO^T
-            auto s_product = [&] {
-                const uint32_t id = ea + 1 == per ? idesc_f16(BF16, last16 * 16) : idesc_s;
-                mma_channels<DP / 16, kM * 128, kN * 128>(tmem, dk, dq + ahead.i * kStage, id, ksteps);
-            };
-            auto dp_product = [&](bool last) {
-                const uint32_t id = ea + 1 == per ? idesc_f16(BF16, last16 * 16) : idesc_s;
-                mma_channels<DP / 16, kM * 128, kN * 128>(tmem + kN, dv, dq + ahead.i * kStage + kSecond, id, ksteps);
-                mma_commit(s_full);
-                if (last) mma_commit(k_empty);
+            // S^T = K Q^T and dP^T = V dO^T of the next step, into buffer w
+            auto scores = [&](uint32_t w) {
+                const uint32_t id = ea + 1 == per ? idesc_f16(BF16, last16 * 16) : idesc_s, d = tmem + w * 2 * kNK;
+                const uint64_t q = dq + ahead.i * kStage;
+                mma_channels<DP / 16, kM * 128, kNK * 128>(d, dk, q, id, ksteps);
+                mma_channels<DP / 16, kM * 128, kNK * 128>(d + kNK, dv, q + kSecond, id, ksteps);
+                mma_commit(s_full + 8 * w);
             };
             auto advance = [&] {
                 ahead.step();
                 if (++ea == per) ea = 0;
             };
-            if (do_scores) {
+            // scores of step `n` of the block (kOwn: once the buffer's last ones have been read)
+            auto issue_scores = [&](uint32_t n, bool last) {
+                const uint32_t w = n & 1u;
+                wait(r_full + 8 * ahead.i, ahead.phase);
+                if (C::kOwn) wait(s_empty + 8 * w, ((n >> 1) & 1u) ^ 1u);
+                if (!wait.ok) return;
+                tc_fence_after();
+                one_lane([&] {
+                    scores(w);
+                    if (last) mma_commit(k_empty);
+                });
+                advance();
+            };
+            if (C::kOwn && warp == kIssuer) {  // the scores alone
                 wait(k_full, uc & 1u);
-                const int first = C::kOwn ? steps : 1;
-                for (int i = 0; i < first; ++i) {
-                    wait(r_full + 8 * ahead.i, ahead.phase);
-                    if (C::kOwn) wait(s_empty, ((n + i) & 1u) ^ 1u);  // the last ones have been read
-                    if (!wait.ok) break;
-                    tc_fence_after();
-                    one_lane([&] {
-                        s_product();
-                        dp_product(i + 1 == steps);
-                    });
-                    advance();
-                }
+                for (int i = 0; i < steps && wait.ok; ++i, ++it) issue_scores(it, i + 1 == steps);
+                if (!wait.ok) break;
+                ++uc;
+                continue;
             }
-            if (do_grads) {
-                wait(o_empty, (uc & 1u) ^ 1u);
-                for (int i = 0; i < steps && wait.ok; ++i) {
-                    const bool next = !C::kOwn && i + 1 < steps;
-                    const int k16 = eg + 1 == per ? last16 : kN / 16;
-                    if (C::kOwn) wait(r_full + 8 * pos.i, pos.phase);
-                    if (next) wait(r_full + 8 * ahead.i, ahead.phase);
-                    if (!wait(p_full, (n + i) & 1u)) break;
-                    tc_fence_after();
-                    // dV += P^T dO and dK += dS^T Q; over the scores' columns, the next scores follow in issue order
-                    one_lane([&] {
-                        const uint64_t q = dqt + pos.i * kStage;
-                        mma_rows<kN / 16, G>(tmem + C::kVCol, t_p, q + kSecond, idesc_o, k16, i > 0);
-                        if (next) s_product();
-                        mma_rows<kN / 16, G>(tmem + C::kKCol, t_d, q, idesc_o, k16, i > 0);
-                        if (C::kOwn) mma_commit(p_empty);
-                        mma_commit(r_empty + 8 * pos.i);
-                        if (next) dp_product(i + 2 == steps);
-                        if (i + 1 == steps) mma_commit(o_full);
-                    });
-                    if (next) advance();
-                    pos.step();
-                    if (++eg == per) eg = 0;
-                }
+            if (!C::kOwn) {
+                wait(k_full, uc & 1u);
+                for (int i = 0; i < 2 && i < steps; ++i) issue_scores(it + i, i + 1 == steps);
+            }
+            wait(o_empty, (uc & 1u) ^ 1u);
+            if (!wait.ok) break;
+            for (int i = 0; i < steps; ++i, ++it) {
+                const uint32_t w = it & 1u, sw = tmem + w * 2 * kNK;
+                const uint32_t pt = C::kOwn ? tmem + C::kPCol + w * kNK : sw, st = C::kOwn ? pt + kNK / 2 : sw + kNK;
+                const bool more = i + 2 < steps;
+                const int n = eg + 1 == per ? last16 : kNK / 16;
+                if (C::kOwn) wait(r_full + 8 * pos.i, pos.phase);
+                if (!C::kOwn && more) wait(r_full + 8 * ahead.i, ahead.phase);
+                if (!wait(p_full + 8 * w, (it >> 1) & 1u)) break;
+                tc_fence_after();
+                one_lane([&] {
+                    const uint64_t q = dqt + pos.i * kStage;
+                    mma_rows<kNK / 16>(tmem + C::kVCol, pt, q + kSecond, idesc_o, n, i > 0);
+                    mma_rows<kNK / 16>(tmem + C::kKCol, st, q, idesc_o, n, i > 0);
+                    mma_commit(r_empty + 8 * pos.i);
+                    if (C::kOwn) mma_commit(p_empty + 8 * w);
+                    if (!C::kOwn && more) scores(w);
+                    if (!C::kOwn && i + 3 == steps) mma_commit(k_empty);
+                    if (i + 1 == steps) mma_commit(o_full);
+                });
+                if (!C::kOwn && more) advance();
+                pos.step();
+                if (++eg == per) eg = 0;
             }
             if (!wait.ok) break;
-            n += steps;
             ++uc;
         }
         // every product has finished before TMEM is released
@@ -555,96 +573,92 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(a.err, kErrTimeout);
         }
     } else if (warp < kLoader) {
-        const int quarter = warp >> 2, quad = warp & 3;
+        reg_grow<C::kSoft>();
+        const int w = warp >> 2, quad = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t t_s = t_lane + quarter * kH;
-        const uint32_t t_p = C::kOwn ? t_lane + C::kPCol + quarter * (kH / 2) : t_s;
-        const uint32_t t_d = t_p + (C::kOwn ? kN / 2 : kN);
+        const uint32_t t_s = t_lane + w * 2 * kNK;
         const float c = a.scale_log2;
         const float2 lift = grad_lift<BF16>(a);
         const float2 c2 = make_float2(c, c), lift2 = make_float2(lift.x, lift.x);
-        // quarters 0 and 1 write dV, 2 and 3 dK
-        const vg_heads grad = quarter < 2 ? a.gv : a.gk;
-        float* part = quarter < 2 ? part_dv : a.part;
-        const bool v8ok = lines_ok(grad);
-        float* my_stats = s_stats + warp * 4 * kH;
-        uint32_t n = 0, uc = 0;  // steps and units done
+        const bool v8ok = lines_ok(w == 0 ? a.gv : a.gk);
+        const uint32_t t_p = C::kOwn ? t_lane + C::kPCol + w * kNK : t_s, t_d = C::kOwn ? t_p + kNK / 2 : t_s + kNK;
+        uint32_t it = 0, sc = 0, uc = 0;
         while (ring.get(wait, x)) {
             const int rows = x.lq * a.gp, per = x.hi - x.lo, steps = per * sets;
-            // Statistics (lse log2 e, delta) of the warp's 32 rows of a row tile, one per lane, kept negated.  (hs, e):
-            // head set and row tile of the next step
-            int hs = x.head * sets, e = x.lo;
-            auto stat = [&](bool have) {
-                const int r = e * kN + quarter * kH + lane;
-                float2 v = make_float2(0.f, 0.f);
-                if (have && r < rows) v = a.stats[((int64_t)hs * a.n_q + x.q0) * a.gp + r];
-                return v;
-            };
-            float2 next = stat(steps > 0);
-            for (int i = 0; i < steps; ++i, ++n) {
-                const int left = rows - e * kN - quarter * kH;
-                float* cur = my_stats + (n & 1u) * 2 * kH;  // [kH] of the first number, [kH] of the second
-                cur[lane] = kLift<BF16> - next.x;
-                cur[lane + kH] = -next.y * lift.x;
-                __syncwarp();
-                if (++e == x.hi) e = x.lo, ++hs;
-                next = stat(i + 1 < steps);
-                if (!wait(s_full, n & 1u)) break;
+            // this group's steps of the unit: every second one
+            int i = (int)((w ^ it) & 1u), e = x.lo + (per == 1 ? 0 : i);
+            for (; i < steps; i += 2) {
+                const int left = rows - e * kNK;
+                for (e += 2; e >= x.hi; e -= per) {}
+                const uint32_t stage = (it + i) & (S - 1);
+                const float* cur = s_stats + stage * 2 * kNK;
+                if (!wait(s_full + 8 * w, sc & 1u)) break;
+                wait(r_full + 8 * stage, (it + i) / S & 1u);  // the statistics: the scores waited for it as well
+                ++sc;
                 tc_fence_after();
-                uint32_t s[kH], g[kH], p[kH / 2], d[kH / 2];
-                tmem_ld32(t_s, s);
-                tmem_ld32(t_s + kN, g);
+                uint32_t s[2][32], g[2][32], p[32], d[32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    tmem_ld32(t_s + 32 * h, s[h]);
+                    tmem_ld32(t_s + kNK + 32 * h, g[h]);
+                }
                 tmem_ld_wait();
-                tmem_ld_done(s);
-                tmem_ld_done(g);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) tmem_ld_done(s[h]), tmem_ld_done(g[h]);
+                if (left < kNK) {  // columns from there on are no rows of the sample: weight 0, gradient 0
+#pragma unroll
+                    for (int j = 0; j < kNK; ++j)
+                        if (j >= left) s[j >> 5][j & 31] = 0xff800000u, g[j >> 5][j & 31] = 0u;
+                }
                 if (C::kOwn) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(s_empty);
-                }
-                if (left < kH) {  // columns from there on are no rows of the sample: weight 0, gradient 0
-#pragma unroll
-                    for (int j = 0; j < kH; ++j)
-                        if (j >= left) s[j] = 0xff800000u, g[j] = 0u;
+                    if (lane == 0) mbar_arrive(s_empty + 8 * w);
                 }
 #pragma unroll
-                for (int j = 0; j < kH / 2; j += 2) {
+                for (int j = 0; j < 32; j += 2) {
                     const float4 lse = *reinterpret_cast<const float4*>(cur + 2 * j);
-                    const float4 del = *reinterpret_cast<const float4*>(cur + kH + 2 * j);
+                    const float4 del = *reinterpret_cast<const float4*>(cur + kNK + 2 * j);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
+                        const int h = (j + t) >> 4, k = 2 * ((j + t) & 15);
                         const float2 base = t == 0 ? make_float2(lse.x, lse.y) : make_float2(lse.z, lse.w);
-                        float2 pr = fma2(two(s + 2 * (j + t)), c2, base);
+                        float2 pr = fma2(two(&s[h][k]), c2, base);
                         pr = make_float2(ex2(pr.x), ex2(pr.y));
                         const float2 minus = t == 0 ? make_float2(del.x, del.y) : make_float2(del.z, del.w);
-                        const float2 dp = two(g + 2 * (j + t));
-                        const float2 ds = mul2(pr, BF16 ? add2(dp, minus) : fma2(dp, lift2, minus));
+                        const float2 dp = two(&g[h][k]);
+                        float2 ds = add2(dp, minus);
+                        if (!BF16) ds = mul2(ds, lift2);
+                        ds = mul2(pr, ds);
                         p[j + t] = pack2<BF16>(pr.x, pr.y);
                         d[j + t] = pack2<BF16>(ds.x, ds.y);
                     }
                 }
-                if (C::kOwn && n > 0) {  // the products that read the last P and dS have finished
-                    if (!wait(p_empty, (n - 1) & 1u)) break;
+                if (C::kOwn && sc > 1) {  // the products that read the buffer's last P and dS have finished
+                    if (!wait(p_empty + 8 * w, sc & 1u)) break;
                     tc_fence_after();
                 }
-                tmem_st16(t_p, p);
-                tmem_st16(t_d, d);
+                tmem_st32(t_p, p);
+                tmem_st32(t_d, d);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full);
+                if (lane == 0) mbar_arrive(p_full + 8 * w);
             }
+            it += steps;
             if (steps > 0) {
-                if (!wait(o_full, uc++ & 1u)) break;
+                if (!wait(o_full, uc & 1u)) break;
+                ++uc;
                 tc_fence_after();
             }
-            const int r = quad * 32 + lane;  // key rows past the valid ones get zeros
+            // group 0 writes dV, group 1 dK; key rows past the valid ones get zeros
+            const int r = quad * 32 + lane;
             const int64_t row = x.k0 + x.first + r;
-            const float mul = quarter < 2 ? kDrop<BF16> : a.scale * kDrop<BF16> * lift.y;
-            store_row<BF16, DP>(a, steps > 0, t_lane + (quarter < 2 ? C::kVCol : C::kKCol), mul, r < x.rows && wait.ok,
-                                head_row<uint16_t>(grad, row, x.head),
-                                part + (((size_t)x.part * a.n_k + row) * a.hk + x.head) * a.d, lane, v8ok,
-                                x.first + r < x.lk, quarter & 1, 2);
+            const float mul = w == 0 ? kDrop<BF16> : a.scale * kDrop<BF16> * lift.y;
+            float* dst_p = (w == 0 ? part_dv : a.part) + (((size_t)x.part * a.n_k + row) * a.hk + x.head) * a.d;
+            store_row<BF16, DP>(a, steps > 0, t_lane + (w == 0 ? C::kVCol : C::kKCol), mul, r < x.rows && wait.ok,
+                                head_row<uint16_t>(w == 0 ? a.gv : a.gk, row, x.head), dst_p, lane, v8ok,
+                                x.first + r < x.lk);
             if (steps > 0) {
                 tc_fence_before();
                 __syncwarp();
@@ -656,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kIssuer) tmem_dealloc(tmem, 512);
+    if (warp == kIssuer) tmem_dealloc(tmem, C::kTmem);
 }
 
 template <bool BF16, int DP>
@@ -677,16 +691,16 @@ int launch_dkv(const AttnArgs& a, const AttnMaps& maps, float* part_dv, int sms,
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) != cudaSuccess)
         return VG_ERR_CUDA;
     const int64_t units = attn_max_tiles(a.n_k, a.batch, 1, kM) * a.hk * a.splits;
-    kernel<<<(unsigned)std::min<int64_t>(units, sms), kThreads, C::kSmem, s>>>(a, maps, part_dv);
+    kernel<<<(unsigned)std::min<int64_t>(units, sms), kThreadsKV, C::kSmem, s>>>(a, maps, part_dv);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 
-// Maps of the four operands, in boxes of 128 (packed) rows.
-int make_maps(AttnMaps* m, const AttnArgs& a, int dtype) {
+// Maps of the four operands; queries in boxes of `qrows` packed rows.
+int make_maps(AttnMaps* m, const AttnArgs& a, int dtype, int qrows) {
     int st = VG_OK;
     if (a.n_q > 0) {
-        if ((st = attn_make_map(&m->q, a.q, a.n_q, a.hq, a.d, dtype, a.gp, kM / a.gp)) != VG_OK) return st;
-        if ((st = attn_make_map(&m->go, a.go, a.n_q, a.hq, a.d, dtype, a.gp, kM / a.gp)) != VG_OK) return st;
+        if ((st = attn_make_map(&m->q, a.q, a.n_q, a.hq, a.d, dtype, a.gp, qrows / a.gp)) != VG_OK) return st;
+        if ((st = attn_make_map(&m->go, a.go, a.n_q, a.hq, a.d, dtype, a.gp, qrows / a.gp)) != VG_OK) return st;
     }
     if (a.n_k > 0) {
         if ((st = attn_make_map(&m->k, a.k, a.n_k, a.hk, a.d, dtype, 1, kM)) != VG_OK) return st;
@@ -699,7 +713,7 @@ int make_maps(AttnMaps* m, const AttnArgs& a, int dtype) {
 
 int attn_tc_dq(const AttnArgs& a, int dtype, int sms, cudaStream_t s) {
     AttnMaps m{};
-    const int st = make_maps(&m, a, dtype);
+    const int st = make_maps(&m, a, dtype, kM);
     if (st != VG_OK) return st;
     if (dtype == VG_BF16) return a.d <= 64 ? launch_dq<true, 64>(a, m, sms, s) : launch_dq<true, 128>(a, m, sms, s);
     return a.d <= 64 ? launch_dq<false, 64>(a, m, sms, s) : launch_dq<false, 128>(a, m, sms, s);
@@ -707,7 +721,7 @@ int attn_tc_dq(const AttnArgs& a, int dtype, int sms, cudaStream_t s) {
 
 int attn_tc_dkv(const AttnArgs& a, float* part_dv, int dtype, int sms, cudaStream_t s) {
     AttnMaps m{};
-    const int st = make_maps(&m, a, dtype);
+    const int st = make_maps(&m, a, dtype, kNK);
     if (st != VG_OK) return st;
     if (dtype == VG_BF16)
         return a.d <= 64 ? launch_dkv<true, 64>(a, m, part_dv, sms, s) : launch_dkv<true, 128>(a, m, part_dv, sms, s);
