@@ -44,14 +44,10 @@ struct Cfg {
     static constexpr int S = DP == 64 && NQ == 2 ? 5 : 2;  // ring stages, a K and a V tile each
     static constexpr int kPerSm = DP == 64 && NQ == 1 ? 2 : 1;
     static constexpr int kOCol = NQ * kN;                   // O's first TMEM column
-    // P in columns of its own where there is room (d <= 64), so that the next scores need not wait for the product that
-    // reads it; else over the scores
-    static constexpr bool kOwn = DP == 64;
-    static constexpr int kPCol = kOCol + NQ * DP;
     static constexpr int kTmem = NQ * 256;
-    // q full, q empty, (s full, s empty, p full, p empty, o full, o empty) x NQ, (k full, v full, k empty, v empty)
-    // x S, tail, done, unit ring
-    static constexpr int kBars = 2 + 6 * NQ + 4 * S + 3 + 2 * kUnitSlots;
+    // q full, q empty, (s full, p full, o full, o empty) x NQ, (k full, v full, k empty, v empty) x S, tail, done,
+    // unit ring
+    static constexpr int kBars = 2 + 4 * NQ + 4 * S + 2 + 2 * kUnitSlots;
     static constexpr size_t kSmem = 1024 + (size_t)(NQ + 2 * S) * kTile + kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
     // registers: launched with kRegs a thread; the softmax warps take what the last warpgroup gives up
     static constexpr int kRegs = NQ == 2 ? 168 : 128, kSoft = NQ == 2 ? 200 : 184, kAux = NQ == 2 ? 104 : 72;
@@ -74,22 +70,19 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
     volatile uint32_t* s_abort = s_tmem + 1;
     const uint32_t bar0 = smem_u32(bars);
     const uint32_t q_full = bar0, q_empty = bar0 + 8;
-    const uint32_t s_full = bar0 + 16, s_empty = s_full + 8 * NQ, p_full = s_empty + 8 * NQ, p_empty = p_full + 8 * NQ;
-    const uint32_t o_full = p_empty + 8 * NQ, o_empty = o_full + 8 * NQ;
+    const uint32_t s_full = bar0 + 16, p_full = s_full + 8 * NQ, o_full = p_full + 8 * NQ, o_empty = o_full + 8 * NQ;
     const uint32_t k_full = o_empty + 8 * NQ, v_full = k_full + 8 * S, k_empty = v_full + 8 * S;
     const uint32_t v_empty = k_empty + 8 * S, tail = v_empty + 8 * S;
-    const uint32_t done = tail + 8, u_full = done + 16, u_empty = u_full + 8 * kUnitSlots;
+    const uint32_t done = tail + 8, u_full = done + 8, u_empty = u_full + 8 * kUnitSlots;
 
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kLoader = C::kSoftWarps, kIssuer = kLoader + 1, kIssuer2 = kLoader + 2, kScheduler = kLoader + 3;
+    constexpr int kLoader = C::kSoftWarps, kIssuer = kLoader + 1, kScheduler = kLoader + 2;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int w = 0; w < NQ; ++w) {
             mbar_init(s_full + 8 * w, 1);
-            mbar_init(s_empty + 8 * w, 4);
             mbar_init(p_full + 8 * w, 4);
-            mbar_init(p_empty + 8 * w, 1);
             mbar_init(o_full + 8 * w, 1);
             mbar_init(o_empty + 8 * w, 4);
         }
@@ -101,11 +94,10 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
         }
         for (int i = 0; i < kUnitSlots; ++i) {
             mbar_init(u_full + 8 * i, 1);
-            mbar_init(u_empty + 8 * i, C::kSoftWarps + 2 + C::kOwn);  // every reader: softmax warps, loader, issuers
+            mbar_init(u_empty + 8 * i, C::kSoftWarps + 2);  // every reader: softmax warps, loader, issuer
         }
         mbar_init(tail, 1);
         mbar_init(done, 1);
-        mbar_init(done + 8, 1);
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -195,13 +187,13 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
             if (!mbar_wait_timed(v_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
         }
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
-    } else if (warp == kIssuer || (C::kOwn && warp == kIssuer2)) {
+    } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;          // K = 16 steps over the channels
         const uint32_t idesc_s = idesc_f16(BF16, kN), idesc_o = idesc_f16_bn(BF16, ksteps * 16);
         const uint64_t dq = sw128_kmajor_desc(sQ), dk = sw128_kmajor_desc(sKV);
         const uint64_t dv = sw128_mnmajor_desc(sKV + C::kTile, kN * 128);
         RingPos<S> pos;
-        uint32_t uc = 0, pc[NQ] = {}, oc[NQ] = {}, sc[NQ] = {};
+        uint32_t uc = 0, pc[NQ] = {}, oc[NQ] = {};
         while (ring.get(wait, x)) {
             if (x.hi <= x.lo) continue;
             const bool both = NQ == 2 && x.rows > kM;
@@ -214,20 +206,7 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                                                           last ? idesc_f16(BF16, last16 * 16) : idesc_s, ksteps);
                 mma_commit(s_full + 8 * w);
             };
-            // the same behind the reads of the tile's previous scores (kOwn); final: the last tile's
-            auto early = [&](auto wc, uint32_t at, bool last, bool final) {
-                constexpr int w = decltype(wc)::value;
-                if (!wait(s_empty + 8 * w, (sc[w]++ & 1u) ^ 1u)) return;
-                tc_fence_after();
-                one_lane([&] {
-                    scores(wc, at, last);
-                    if (final) {
-                        mma_commit(k_empty + 8 * at);
-                        if (last) mma_commit(q_empty);
-                    }
-                });
-            };
-            // O_w += P_w V of tile e in the stage at `at`, then (over the scores' columns) the next scores
+            // O_w += P_w V of tile e in the stage at `at`, then the next scores, over P's columns
             auto values = [&](auto wc, int e, uint32_t at, uint32_t next, bool final) {
                 constexpr int w = decltype(wc)::value;
                 const bool more = e + 1 < x.hi;
@@ -235,67 +214,44 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                 if (!wait(p_full + 8 * w, pc[w]++ & 1u)) return;
                 tc_fence_after();
                 one_lane([&] {
-                    mma_rows<kN / 16>(tmem + C::kOCol + w * DP, tmem + (C::kOwn ? C::kPCol + w * (kN / 2) : w * kN),
-                                      dv + at * (2 * C::kTile >> 4), idesc_o, more ? kN / 16 : last16, e > x.lo);
-                    if (C::kOwn) mma_commit(p_empty + 8 * w);
-                    if (!C::kOwn && more) scores(wc, next, e + 2 == x.hi);
-                    if (!more) mma_commit(o_full + 8 * w);
+                    mma_rows<kN / 16>(tmem + C::kOCol + w * DP, tmem + w * kN, dv + at * (2 * C::kTile >> 4), idesc_o,
+                                      more ? kN / 16 : last16, e > x.lo);
+                    if (more) scores(wc, next, e + 2 == x.hi);
+                    else mma_commit(o_full + 8 * w);
                     if (final) {
                         mma_commit(v_empty + 8 * at);
-                        if (!C::kOwn && more) mma_commit(k_empty + 8 * next);
-                        if (!C::kOwn && e + 2 == x.hi) mma_commit(q_empty);
+                        if (more) mma_commit(k_empty + 8 * next);
+                        if (e + 2 == x.hi) mma_commit(q_empty);
                     }
                 });
             };
             const Const<0> first;
             const Const<NQ - 1> second;
-            if constexpr (C::kOwn) {
-                // one warp issues the scores, another one the products with V: neither waits for the other's
-                if (warp == kIssuer) {
-                    wait(q_full, uc & 1u);
-                    for (int e = x.lo; e < x.hi && wait.ok; ++e) {
-                        const bool last = e + 1 == x.hi;
-                        wait(k_full + 8 * pos.i, pos.phase);
-                        early(first, pos.i, last, !both);
-                        if (both) early(second, pos.i, last, true);
-                        pos.step();
-                    }
-                } else {
-                    for (int e = x.lo; e < x.hi && wait.ok; ++e) {
-                        wait(v_full + 8 * pos.i, pos.phase);
-                        values(first, e, pos.i, 0, !both);
-                        if (both) values(second, e, pos.i, 0, true);
-                        pos.step();
-                    }
-                }
-            } else {
-                const bool single = x.hi - x.lo == 1;
-                wait(q_full, uc & 1u);
-                wait(k_full + 8 * pos.i, pos.phase);
-                if (!wait.ok) break;
-                tc_fence_after();
-                one_lane([&] {
-                    scores(first, pos.i, single);
-                    if (both) scores(second, pos.i, single);
-                    mma_commit(k_empty + 8 * pos.i);
-                    if (single) mma_commit(q_empty);
-                });
-                for (int e = x.lo; e < x.hi && wait.ok; ++e) {
-                    const uint32_t at = pos.i;
-                    wait(v_full + 8 * at, pos.phase);
-                    pos.step();
-                    if (e + 1 < x.hi) wait(k_full + 8 * pos.i, pos.phase);
-                    values(first, e, at, pos.i, !both);
-                    if (both) values(second, e, at, pos.i, true);
-                }
+            const bool single = x.hi - x.lo == 1;
+            wait(q_full, uc & 1u);
+            wait(k_full + 8 * pos.i, pos.phase);
+            if (!wait.ok) break;
+            tc_fence_after();
+            one_lane([&] {
+                scores(first, pos.i, single);
+                if (both) scores(second, pos.i, single);
+                mma_commit(k_empty + 8 * pos.i);
+                if (single) mma_commit(q_empty);
+            });
+            for (int e = x.lo; e < x.hi && wait.ok; ++e) {
+                const uint32_t at = pos.i;
+                wait(v_full + 8 * at, pos.phase);
+                pos.step();
+                if (e + 1 < x.hi) wait(k_full + 8 * pos.i, pos.phase);
+                values(first, e, at, pos.i, !both);
+                if (both) values(second, e, at, pos.i, true);
             }
             if (!wait.ok) break;
             ++uc;
         }
         // every product has finished before TMEM is released
-        const uint32_t mine = done + 8 * (warp - kIssuer);
-        one_lane([&] { mma_commit(mine); });
-        if (!mbar_wait_timed(mine, 0)) wait.ok = false;
+        one_lane([&] { mma_commit(done); });
+        if (!mbar_wait_timed(done, 0)) wait.ok = false;
         if (!wait.ok && lane == 0) {
             *s_abort = 1;
             atomicOr(a.err, kErrTimeout);
@@ -305,13 +261,12 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
         const int w = warp >> 2, quad = warp & 3;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t t_s = t_lane + w * kN, t_o = t_lane + C::kOCol + w * DP;
-        const uint32_t t_p = C::kOwn ? t_lane + C::kPCol + w * (kN / 2) : t_s;
         const float c = a.scale_log2;
         constexpr float kLift = BF16 ? 0.f : 7.f;            // exponent added to the weights
         constexpr float kMost = BF16 ? 0x1p64f : 0x1p14f;    // of a tile's sum before the maximum is replaced
         const bool v8ok = lines_ok(a.o);
         const int row = w * kM + quad * 32 + lane;           // within the unit
-        uint32_t sc = 0, oc = 0, vc = 0;                     // vc: tiles whose P has been written
+        uint32_t sc = 0, oc = 0;
         while (ring.get(wait, x)) {
             if (x.rows <= w * kM) continue;
             const bool any = x.rows > w * kM + quad * 32, mine = row < x.rows;  // the warp, the thread has a row
@@ -327,24 +282,11 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < kN / 32; ++i) tmem_ld_done(s[i]);
-                    if (C::kOwn) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(s_empty + 8 * w);
-                    }
                     if (left < kN) {
 #pragma unroll
                         for (int i = 0; i < kN; ++i)
                             if (i >= left) s[i >> 5][i & 31] = 0xff800000u;
                     }
-                    // O holds the sum of the tiles before, and P's columns are free, once the last product has finished
-                    bool free = !C::kOwn || vc == 0;
-                    auto wait_free = [&] {
-                        if (free) return;
-                        free = true;
-                        wait(p_empty + 8 * w, (vc - 1) & 1u);
-                        tc_fence_after();
-                    };
                     // P, 64 keys at a time, and its sum
                     auto weights = [&] {
                         const float base = kLift - (m == -INFINITY ? 0.f : m * c);
@@ -360,8 +302,7 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                                 acc[j & 1] = add2(acc[j & 1], x2);
                                 p[j] = pack2<BF16>(x2.x, x2.y);
                             }
-                            wait_free();
-                            tmem_st32(t_p + 32 * i, p);
+                            tmem_st32(t_s + 32 * i, p);
                         }
                         const float2 both = add2(acc[0], acc[1]);
                         return both.x + both.y;
@@ -395,21 +336,13 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                     };
                     float sum;  // weighed twice only where the maximum has to be renewed
                     for (bool renew = e == x.lo;; renew = true) {
-                        if (renew) {
-                            if (e > x.lo) wait_free();
-                            renew_max(e > x.lo);
-                        }
+                        if (renew) renew_max(e > x.lo);
                         sum = weights();
                         if (renew || !__any_sync(0xffffffffu, mine && (!(sum <= kMost) || m == -INFINITY))) break;
                     }
                     l += sum;
                     tmem_st_wait();
-                } else if (C::kOwn) {
-                    if (lane == 0) mbar_arrive(s_empty + 8 * w);
-                    // not ahead of the warps with rows: their arrivals for two tiles would add up to one early phase
-                    if (vc > 0) wait(p_empty + 8 * w, (vc - 1) & 1u);
                 }
-                ++vc;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * w);
