@@ -22,6 +22,12 @@
 // cores' rate only from N = 128 on: at N = 64 it takes 48 cycles instead of 32 to read its
 // operands.
 //
+// delta is the sum of dO O, with O as the caller has it, rounded to 16 bits.  Over many keys
+// that is exact enough (O is an average, small beside V), over few it is not: over five
+// keys it adds as much to dQ's error as the rounding of dS.  So a sample of at most one
+// tile of keys gets delta as the row's sum of P dP, which the dQ kernel has in registers
+// there; it hands it to the dK, dV kernel too.
+//
 // fp16 has no exponent range to spare: P carries 2^15 (P <= 1), and dP - delta is divided by
 // a power of two above 2 max|dO row| max|V row|, which bounds it; both leave with the
 // fp32 result.  bf16 needs neither.
@@ -57,9 +63,11 @@ struct CfgQ {
     static constexpr int kTile = kM * 128 * kBlocks;       // bytes of a Q, dO, K or V tile
     static constexpr int S = DP == 64 ? 4 : 2;             // ring stages (a K and a V tile each)
     static constexpr int kOCol = 2 * kN, kPCol = kOCol + DP;  // dQ's and dS's first TMEM column
-    // q, s, p and o (full, empty), (kv full, kv empty) x S, tail, done x 2, unit ring
-    static constexpr int kBars = 8 + 2 * S + 3 + 2 * kUnitSlots;
-    static constexpr size_t kSmem = 1024 + (size_t)(2 + 2 * S) * kTile + kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
+    // q, s, p and o (full, empty), (kv full, kv empty) x S, tail, done x 2, unit ring, exchanges x 4
+    static constexpr int kBars = 8 + 2 * S + 3 + 2 * kUnitSlots + 4;
+    static constexpr size_t kSums = 2 * 4 * kM * sizeof(float);  // two exchanges between the threads of a row
+    static constexpr size_t kSmem =
+        1024 + (size_t)(2 + 2 * S) * kTile + kSums + kUnitSlots * sizeof(Unit) + 8 * kBars + 16;
 };
 static_assert(CfgQ<128>::kSmem <= 232448 && CfgQ<64>::kSmem <= 232448 && CfgQ<128>::kPCol + kN / 2 <= 512,
               "shared memory, TMEM");
@@ -72,7 +80,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sQ = smem_u32(smem), sG = sQ + C::kTile, sKV = sG + C::kTile;
-    int4* s_units = reinterpret_cast<int4*>(smem + (size_t)(2 + 2 * S) * C::kTile);
+    float* s_sums = reinterpret_cast<float*>(smem + (size_t)(2 + 2 * S) * C::kTile);
+    int4* s_units = reinterpret_cast<int4*>(s_sums + 2 * 4 * kM);
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_units + 3 * kUnitSlots);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + C::kBars);
     volatile uint32_t* s_abort = s_tmem + 1;
@@ -81,6 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_empty = bar0 + 40, o_full = bar0 + 48, o_empty = bar0 + 56;
     const uint32_t kv_full = bar0 + 64, kv_empty = kv_full + 8 * S, tail = kv_empty + 8 * S;
     const uint32_t done = tail + 8, u_full = done + 16, u_empty = u_full + 8 * kUnitSlots;
+    const uint32_t summed = u_empty + 8 * kUnitSlots;
 
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kLoader = 16, kIssuer = 17, kIssuer2 = 18, kScheduler = 19;
@@ -101,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(u_full + 8 * i, 1);
             mbar_init(u_empty + 8 * i, 16 + 3);  // every reader: softmax warps, loader, issuers
         }
+        for (int i = 0; i < 4; ++i) mbar_init(summed + 8 * i, 4);
         mbar_init(tail, 1);
         mbar_init(done, 1);
         mbar_init(done + 8, 1);
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 lift = grad_lift<BF16>(a);
         const bool v8ok = lines_ok(a.gq);
         const int row = quad * 32 + lane;  // within the unit
-        uint32_t n = 0, uc = 0;            // tiles and units done
+        uint32_t n = 0, uc = 0, sums = 0;  // tiles, units and exchanges done
         while (ring.get(wait, x)) {
             const bool any = x.rows > quad * 32, mine = row < x.rows;  // the warp, the thread has a row
             const int pr = x.first + row;                              // packed row of the sample
@@ -253,48 +264,96 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float base = st.x, delta = st.y * lift.x;
             const float2 c2 = make_float2(c, c), base2 = make_float2(base, base);
             const float2 lift2 = make_float2(lift.x, lift.x), delta2 = make_float2(delta, delta);
-            for (int e = x.lo; e < x.hi; ++e, ++n) {
+            if (x.lk <= kN && x.lo < x.hi && any) {  // the one tile of a sample
                 if (!wait(s_full, n & 1u)) break;
                 tc_fence_after();
-                uint32_t d[kH / 2];
-                if (any) {
-                    uint32_t s[kH], g[kH];
-                    tmem_ld32(t_s, s);
-                    tmem_ld32(t_s + kN, g);
-                    tmem_ld_wait();
-                    tmem_ld_done(s);
-                    tmem_ld_done(g);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s_empty);
-                    const int left = x.lk - e * kN - quarter * kH;  // columns from there on are not scores: weight 0,
-                    if (left < kH) {                                // gradient 0
+                uint32_t s[kH], g[kH];
+                tmem_ld32(t_s, s);
+                tmem_ld32(t_s + kN, g);
+                tmem_ld_wait();
+                tmem_ld_done(s);
+                tmem_ld_done(g);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty);
+                float w[kH], sum = 0.f;
+                const int left = x.lk - quarter * kH;
 #pragma unroll
-                        for (int i = 0; i < kH; ++i)
-                            if (i >= left) s[i] = 0xff800000u, g[i] = 0u;
-                    }
-#pragma unroll
-                    for (int j = 0; j < kH / 2; ++j) {
-                        float2 p = fma2(two(s + 2 * j), c2, base2);
-                        p = make_float2(ex2(p.x), ex2(p.y));
-                        const float2 dp = two(g + 2 * j);
-                        const float2 ds = mul2(p, BF16 ? add2(dp, delta2) : fma2(dp, lift2, delta2));
-                        d[j] = pack2<BF16>(ds.x, ds.y);
-                    }
-                } else if (lane == 0) {
-                    mbar_arrive(s_empty);
+                for (int i = 0; i < kH; ++i) {
+                    const float dp = i < left ? __uint_as_float(g[i]) : 0.f;
+                    w[i] = i < left ? ex2(fmaf(__uint_as_float(s[i]), c, base)) : 0.f;
+                    sum = fmaf(w[i], dp, sum);
+                    g[i] = __float_as_uint(dp);
                 }
-                // The product that reads the last dS has finished.  Warps without rows wait as well: ahead of the
-                // others, their arrivals for two tiles would add up to one early phase.
+                // delta, to all threads of the row
+                float* slot = s_sums + (sums & 1u) * 4 * kM + row;
+                slot[quarter * kM] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(summed + 8 * quad);
+                if (!wait(summed + 8 * quad, sums++ & 1u)) break;
+                sum = -kDrop<BF16> * (slot[0] + slot[kM] + (slot[2 * kM] + slot[3 * kM]));
+                if (mine && quarter == 0)
+                    a.stats[a.n_q * a.hq + ((int64_t)x.head * a.n_q + x.q0) * a.gp + pr] = sum;
                 if (n > 0 && !wait(p_empty, (n - 1) & 1u)) break;
                 tc_fence_after();
-                if (any) {
-                    tmem_st16(t_p, d);
-                    tmem_st_wait();
+                uint32_t d[kH / 2];
+#pragma unroll
+                for (int i = 0; i < kH / 2; ++i) {
+                    const float d0 = w[2 * i] * ((__uint_as_float(g[2 * i]) + sum) * lift.x);
+                    const float d1 = w[2 * i + 1] * ((__uint_as_float(g[2 * i + 1]) + sum) * lift.x);
+                    d[i] = pack2<BF16>(d0, d1);
                 }
+                tmem_st16(t_p, d);
+                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
+                ++n;
+            } else {
+                for (int e = x.lo; e < x.hi; ++e, ++n) {
+                    if (!wait(s_full, n & 1u)) break;
+                    tc_fence_after();
+                    uint32_t d[kH / 2];
+                    if (any) {
+                        uint32_t s[kH], g[kH];
+                        tmem_ld32(t_s, s);
+                        tmem_ld32(t_s + kN, g);
+                        tmem_ld_wait();
+                        tmem_ld_done(s);
+                        tmem_ld_done(g);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_empty);
+                        // columns from there on are not scores: weight 0, gradient 0
+                        const int left = x.lk - e * kN - quarter * kH;
+                        if (left < kH) {
+#pragma unroll
+                            for (int i = 0; i < kH; ++i)
+                                if (i >= left) s[i] = 0xff800000u, g[i] = 0u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < kH / 2; ++j) {
+                            float2 p = fma2(two(s + 2 * j), c2, base2);
+                            p = make_float2(ex2(p.x), ex2(p.y));
+                            const float2 dp = two(g + 2 * j);
+                            const float2 ds = mul2(p, BF16 ? add2(dp, delta2) : fma2(dp, lift2, delta2));
+                            d[j] = pack2<BF16>(ds.x, ds.y);
+                        }
+                    } else if (lane == 0) {
+                        mbar_arrive(s_empty);
+                    }
+                    // The product that reads the last dS has finished.  Warps without rows wait as well: ahead of the
+                    // others, their arrivals for two tiles would add up to one early phase.
+                    if (n > 0 && !wait(p_empty, (n - 1) & 1u)) break;
+                    tc_fence_after();
+                    if (any) {
+                        tmem_st16(t_p, d);
+                        tmem_st_wait();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full);
+                }
             }
             if (x.hi > x.lo) {
                 if (!wait(o_full, uc++ & 1u)) break;
