@@ -77,6 +77,8 @@ class VGError(RuntimeError):
 def lib():
     """The loaded libvoxelgemm.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -131,13 +133,15 @@ def lib():
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _s(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if torch.cuda.is_initialized():  # the current stream's handle without an object around it: 0.3 us instead of 3
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(st: int, where: str):
@@ -379,14 +383,18 @@ class SparseMap:
 
 
 # ---------------------------------------------------------------- attention-block operators
+_Int3 = ctypes.c_int * 3
+
+
 def _heads(t, dtype, shape, what):
     """vg_heads of a [rows, heads, head_dim] tensor (any row and head strides), None for None."""
     if t is None:
         return None
-    if t.dim() != 3 or t.dtype != dtype or tuple(t.shape) != shape or (t.stride(2) != 1 and t.numel() > 0):
+    s = t.stride()
+    if t.dtype != dtype or t.shape != shape or (s[2] != 1 and t.numel() > 0):
         raise ValueError(f"{what}: expected {dtype} {list(shape)} with contiguous elements, got {t.dtype} "
-                         f"{list(t.shape)} of strides {t.stride()}")
-    return HeadsStruct(t.data_ptr(), t.stride(0), t.stride(1))
+                         f"{list(t.shape)} of strides {s}")
+    return HeadsStruct(t.data_ptr(), s[0], s[1])
 
 
 def rope_freqs(head_dim: int, axes: int = 3, theta: float = 10000.0, device="cuda"):
@@ -407,23 +415,24 @@ def _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags):
         raise ValueError("coords and freqs come together")
     pairs = None
     if coords is not None:
-        if coords.dtype != torch.int32 or tuple(coords.shape) != (n, 4) or not coords.is_contiguous():
+        if coords.dtype != torch.int32 or coords.shape != (n, 4) or not coords.is_contiguous():
             raise ValueError("coords must be contiguous int32 [rows, 4]")
         if freqs.dtype != torch.float32 or not freqs.is_contiguous() or freqs.numel() != sum(axis_pairs):
             raise ValueError("freqs must be contiguous float32 of sum(axis_pairs) elements")
-        pairs = (ctypes.c_int * 3)(*axis_pairs)
+        pairs = _Int3(*axis_pairs)
     for w, h, name in ((q_weight, hq, "q_weight"), (k_weight, hk, "k_weight")):
         if w is not None:
             want = (d,) if flags & VG_QK_SHARED_WEIGHT else (h, d)
-            if w.dtype != x.dtype or tuple(w.shape) != want or not w.is_contiguous():
+            if w.dtype != x.dtype or w.shape != want or not w.is_contiguous():
                 raise ValueError(f"{name} must be contiguous {x.dtype} {list(want)}")
     return n, hq, hk, d, x.dtype, pairs
 
 
 def _rope_flags(q_weight, k_weight, flags):
     """A one-dimensional weight is shared by the heads."""
-    shared = any(w is not None and w.dim() == 1 for w in (q_weight, k_weight))
-    return flags | (VG_QK_SHARED_WEIGHT if shared else 0)
+    if (q_weight is not None and q_weight.dim() == 1) or (k_weight is not None and k_weight.dim() == 1):
+        return flags | VG_QK_SHARED_WEIGHT
+    return flags
 
 
 def vg_qk_norm_rope_fwd(q, k, q_weight, k_weight, coords, freqs, axis_pairs, q_out, k_out, eps=1e-6, flags=0,
@@ -483,7 +492,7 @@ def _attn(q, k, q_offsets, k_offsets, k_lens, lse, scale, what):
         if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda):
             raise ValueError(f"{what}: {name} must be contiguous int32 [{n}] on the GPU")
     n_q, hq, d = q.shape
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (hq, n_q) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (hq, n_q) or not lse.is_contiguous()):
         raise ValueError(f"{what}: lse must be contiguous float32 [heads_q, n_q]")
     return AttnStruct(n_q, k.shape[0], batch, hq, k.shape[1], d, _DT.get(q.dtype, -1),
                       d ** -0.5 if scale is None else scale, q_offsets.data_ptr(), k_offsets.data_ptr(),
