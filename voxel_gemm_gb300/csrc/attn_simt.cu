@@ -10,9 +10,13 @@
 // maximum and sum of the softmax; scores are recomputed from the saved log-sum in
 // the backward pass, so nothing of size queries x keys is stored.  Each thread
 // holds 4 x 4 of a 64 x 64 product, so every float4 read from shared memory feeds
-// 8 multiply-adds; row pitches of d + 4 and 68 floats keep those reads free of
-// bank conflicts.  Bound by the fp32 multiply-add rate.
+// 8 multiply-adds, issued two to an instruction; row pitches of d + 4 and 68 floats keep
+// those reads free of bank conflicts.  Bound by the reads of shared memory and, at two
+// blocks per SM, their latency: 20,000 queries over 2 x 2,000 keys, 8 heads of 64, take
+// 2.6 ms forward (32 TFLOP/s), 3.6 for dQ and 6.2 for dK and dV.  8 x 4 per thread with half
+// the threads takes fewer reads but was slower (3.3, 5.2, 8.6 ms): too few warps.
 #include "attn.cuh"
+#include "tc_ptx.cuh"
 
 namespace vg {
 
@@ -34,20 +38,14 @@ __device__ __forceinline__ void load_tile(float* dst, const vg_heads& h, int64_t
     }
 }
 
-__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
-    c = fmaf(a.x, b.x, c);
-    c = fmaf(a.y, b.y, c);
-    c = fmaf(a.z, b.z, c);
-    return fmaf(a.w, b.w, c);
-}
-
-// acc[a][b] = sum_d A[ty + 16 a][d] B[tx + 16 b][d]
+// acc[a][b] = sum_d A[ty + 16 a][d] B[tx + 16 b][d]; even and odd channels have sums of their own
 __device__ __forceinline__ void product_nt(const float* A, const float* B, int d, int ty, int tx, float (&acc)[4][4]) {
     const int p = d + 4;
+    float2 sum[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) sum[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 2
     for (int c = 0; c < d; c += 4) {
         float4 x[4], y[4];
@@ -58,8 +56,15 @@ __device__ __forceinline__ void product_nt(const float* A, const float* B, int d
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = dot4(x[i], y[j], acc[i][j]);
+            for (int j = 0; j < 4; ++j) {
+                sum[i][j] = ptx::fma2(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), sum[i][j]);
+                sum[i][j] = ptx::fma2(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), sum[i][j]);
+            }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = sum[i][j].x + sum[i][j].y;
 }
 
 // acc[a][c] (columns 4 tx + 64 c ..) += sum_j W[ty + 16 a][j] B[j][columns]
@@ -82,10 +87,11 @@ __device__ __forceinline__ void product_nn(const float* W, const float* B, int d
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float s = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
-                    acc[i][c].x = fmaf(s, v.x, acc[i][c].x);
-                    acc[i][c].y = fmaf(s, v.y, acc[i][c].y);
-                    acc[i][c].z = fmaf(s, v.z, acc[i][c].z);
-                    acc[i][c].w = fmaf(s, v.w, acc[i][c].w);
+                    const float2 s2 = make_float2(s, s);
+                    float4& o = acc[i][c];
+                    const float2 lo = ptx::fma2(s2, make_float2(v.x, v.y), make_float2(o.x, o.y));
+                    const float2 hi = ptx::fma2(s2, make_float2(v.z, v.w), make_float2(o.z, o.w));
+                    o = make_float4(lo.x, lo.y, hi.x, hi.y);
                 }
             }
         }
@@ -105,7 +111,7 @@ __device__ __forceinline__ float4 times(float4 v, float s) { return make_float4(
 
 // ---------------------------------------------------------------- forward
 template <int NC>
-__global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_attn_fwd(const AttnArgs a) {
     extern __shared__ float sm[];
     const int p = a.d + 4;
     float *sQ = sm, *sK = sQ + kT * p, *sV = sK + kT * p, *sP = sV + kT * p;
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_fwd(const AttnArgs a) {
 
 // ---------------------------------------------------------------- query gradient
 template <int NC>
-__global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) k_attn_dq(const AttnArgs a) {
     extern __shared__ float sm[];
     const int p = a.d + 4;
     float *sQ = sm, *sG = sQ + kT * p, *sK = sG + kT * p, *sV = sK + kT * p, *sS = sV + kT * p;
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_dq(const AttnArgs a) {
 // The block's 64 keys run along the sample's queries of every head that reads
 // them, in head order: gradients of shared heads are sums in one accumulator.
 template <int NC>
-__global__ void __launch_bounds__(kThreads) k_attn_dkv(const AttnArgs a, float* part_dv) {
+__global__ void __launch_bounds__(kThreads, NC == 1 ? 2 : 1) k_attn_dkv(const AttnArgs a, float* part_dv) {
     extern __shared__ float sm[];
     const int p = a.d + 4;
     float *sQ = sm, *sG = sQ + kT * p, *sK = sG + kT * p, *sV = sK + kT * p;
