@@ -277,7 +277,8 @@ Cut cut_axis(int64_t units, int64_t tiles, int batch, int slots, int least, bool
     // `want` parts of a sample of average length; a sample that holds all rows has batch times as many, of
     // which the scratch takes up to four times the average
     const int64_t most = std::min<int64_t>(want * std::min(batch, 4), 1024);
-    const int64_t per = std::max<int64_t>({least, (tiles + want * batch - 1) / (want * batch), (tiles + most - 1) / most});
+    const int64_t even = (tiles + want * batch - 1) / (want * batch);
+    const int64_t per = std::max<int64_t>({least, even, (tiles + most - 1) / most});
     const int64_t parts = (tiles + per - 1) / per;
     return parts <= 1 ? Cut{1, 0} : Cut{(int)parts, (int)per};
 }

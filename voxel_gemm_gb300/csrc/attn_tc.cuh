@@ -202,6 +202,11 @@ struct RingPos {
     __device__ __forceinline__ void step() {
         if (++i == S) i = 0, phase ^= 1u;
     }
+    __device__ __forceinline__ void skip(uint32_t n) {
+        i += n;
+        phase ^= (i / S) & 1u;
+        i %= S;
+    }
 };
 
 // Run f in one lane of a converged warp.
@@ -209,6 +214,30 @@ template <typename F>
 __device__ __forceinline__ void one_lane(F f) {
     if (elect_one()) f();
     __syncwarp();
+}
+
+// f in one lane of a converged warp, with waits of that lane alone: a warp's wait takes its vote as well, and between
+// two batches of products every cycle counts.
+struct LaneWaiter {
+    volatile uint32_t* abort;
+    bool ok = true;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {
+        if (!ok || mbar_try_wait(bar, parity)) return ok;
+        const int64_t t0 = clock64();
+        while (!mbar_try_wait(bar, parity)) {
+            if (*abort != 0 || clock64() - t0 > kWaitCycles) {
+                *abort = 1;
+                return ok = false;
+            }
+        }
+        return true;
+    }
+};
+template <typename F>
+__device__ __forceinline__ void by_one_lane(Waiter& wait, F f) {
+    LaneWaiter w{wait.abort, wait.ok};
+    if (elect_one()) f(w);
+    wait.ok = __all_sync(0xffffffffu, w.ok);
 }
 
 // The value of lane 0 in every lane, as one that the compiler knows to be uniform.

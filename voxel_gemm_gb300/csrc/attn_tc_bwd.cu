@@ -558,69 +558,59 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             if (x.hi <= x.lo) continue;
             const int per = x.hi - x.lo, steps = per * sets;
             const int rest = min(kNK, x.lq * a.gp - (x.hi - 1) * kNK), last16 = (rest + 15) / 16;
-            int ea = 0, eg = 0;               // row tiles (from lo) of the next scores and gradients
-            // S^T = K Q^T and dP^T = V dO^T of the next step, into buffer w
-            auto scores = [&](uint32_t w) {
-                const uint32_t id = ea + 1 == per ? idesc_f16(BF16, last16 * 16) : idesc_s, d = tmem + w * 2 * kNK;
-                const uint64_t q = dq + ahead.i * kStage;
-                mma_channels<DP / 16, kM * 128, kNK * 128>(d, dk, q, id, ksteps);
-                mma_channels<DP / 16, kM * 128, kNK * 128>(d + kNK, dv, q + kSecond, id, ksteps);
-                mma_commit(s_full + 8 * w);
-            };
-            auto advance = [&] {
-                ahead.step();
-                if (++ea == per) ea = 0;
-            };
-            // scores of step `n` of the block (kOwn: once the buffer's last ones have been read)
-            auto issue_scores = [&](uint32_t n, bool last) {
-                const uint32_t w = n & 1u;
-                wait(r_full + 8 * ahead.i, ahead.phase);
-                if (C::kOwn) wait(s_empty + 8 * w, ((n >> 1) & 1u) ^ 1u);
-                if (!wait.ok) return;
-                tc_fence_after();
-                one_lane([&] {
-                    scores(w);
+            by_one_lane(wait, [&](LaneWaiter& w) {
+                RingPos<S> ra = ahead, rg = pos;
+                uint32_t na = it, ng = it;    // steps of the block: of the next scores, of the next gradients
+                int ea = 0, eg = 0;           // their row tiles (from lo)
+                // S^T = K Q^T and dP^T = V dO^T of the next step
+                auto scores = [&](bool last) {
+                    const uint32_t id = ea + 1 == per ? idesc_f16(BF16, last16 * 16) : idesc_s, b = na++ & 1u;
+                    const uint32_t d = tmem + b * 2 * kNK;
+                    const uint64_t q = dq + ra.i * kStage;
+                    mma_channels<DP / 16, kM * 128, kNK * 128>(d, dk, q, id, ksteps);
+                    mma_channels<DP / 16, kM * 128, kNK * 128>(d + kNK, dv, q + kSecond, id, ksteps);
+                    mma_commit(s_full + 8 * b);
                     if (last) mma_commit(k_empty);
-                });
-                advance();
-            };
-            if (C::kOwn && warp == kIssuer) {  // the scores alone
-                wait(k_full, uc & 1u);
-                for (int i = 0; i < steps && wait.ok; ++i, ++it) issue_scores(it, i + 1 == steps);
-                if (!wait.ok) break;
-                ++uc;
-                continue;
-            }
-            if (!C::kOwn) {
-                wait(k_full, uc & 1u);
-                for (int i = 0; i < 2 && i < steps; ++i) issue_scores(it + i, i + 1 == steps);
-            }
-            wait(o_empty, (uc & 1u) ^ 1u);
-            if (!wait.ok) break;
-            for (int i = 0; i < steps; ++i, ++it) {
-                const uint32_t w = it & 1u, sw = tmem + w * 2 * kNK;
-                const uint32_t pt = C::kOwn ? tmem + C::kPCol + w * kNK : sw, st = C::kOwn ? pt + kNK / 2 : sw + kNK;
-                const bool more = i + 2 < steps;
-                const int n = eg + 1 == per ? last16 : kNK / 16;
-                if (C::kOwn) wait(r_full + 8 * pos.i, pos.phase);
-                if (!C::kOwn && more) wait(r_full + 8 * ahead.i, ahead.phase);
-                if (!wait(p_full + 8 * w, (it >> 1) & 1u)) break;
-                tc_fence_after();
-                one_lane([&] {
-                    const uint64_t q = dqt + pos.i * kStage;
-                    mma_rows<kNK / 16>(tmem + C::kVCol, pt, q + kSecond, idesc_o, n, i > 0);
-                    mma_rows<kNK / 16>(tmem + C::kKCol, st, q, idesc_o, n, i > 0);
-                    mma_commit(r_empty + 8 * pos.i);
-                    if (C::kOwn) mma_commit(p_empty + 8 * w);
-                    if (!C::kOwn && more) scores(w);
-                    if (!C::kOwn && i + 3 == steps) mma_commit(k_empty);
+                    ra.step();
+                    if (++ea == per) ea = 0;
+                };
+                if (!C::kOwn || warp == kIssuer) {
+                    w(k_full, uc & 1u);
+                    for (int i = 0; i < (C::kOwn ? steps : min(2, steps)); ++i) {
+                        w(r_full + 8 * ra.i, ra.phase);
+                        if (C::kOwn) w(s_empty + 8 * (na & 1u), ((na >> 1) & 1u) ^ 1u);  // the last ones have been read
+                        if (!w.ok) return;
+                        tc_fence_after();
+                        scores(i + 1 == steps);
+                    }
+                }
+                if (C::kOwn && warp == kIssuer) return;
+                w(o_empty, (uc & 1u) ^ 1u);
+                for (int i = 0; i < steps; ++i, ++ng) {
+                    const uint32_t b = ng & 1u, sw = tmem + b * 2 * kNK;
+                    const uint32_t pt = C::kOwn ? tmem + C::kPCol + b * kNK : sw;
+                    const uint32_t st = C::kOwn ? pt + kNK / 2 : sw + kNK;
+                    const bool more = !C::kOwn && i + 2 < steps;
+                    const int n16 = eg + 1 == per ? last16 : kNK / 16;
+                    if (C::kOwn) w(r_full + 8 * rg.i, rg.phase);
+                    if (more) w(r_full + 8 * ra.i, ra.phase);
+                    if (!w(p_full + 8 * b, (ng >> 1) & 1u)) return;
+                    tc_fence_after();
+                    const uint64_t q = dqt + rg.i * kStage;
+                    mma_rows<kNK / 16>(tmem + C::kVCol, pt, q + kSecond, idesc_o, n16, i > 0);
+                    mma_rows<kNK / 16>(tmem + C::kKCol, st, q, idesc_o, n16, i > 0);
+                    mma_commit(r_empty + 8 * rg.i);
+                    if (C::kOwn) mma_commit(p_empty + 8 * b);
+                    if (more) scores(i + 3 == steps);
                     if (i + 1 == steps) mma_commit(o_full);
-                });
-                if (!C::kOwn && more) advance();
-                pos.step();
-                if (++eg == per) eg = 0;
-            }
+                    rg.step();
+                    if (++eg == per) eg = 0;
+                }
+            });
             if (!wait.ok) break;
+            ahead.skip(steps);
+            pos.skip(steps);
+            it += steps;
             ++uc;
         }
         // every product has finished before TMEM is released
