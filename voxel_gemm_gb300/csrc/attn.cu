@@ -78,10 +78,12 @@ __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int l
     const int64_t first = (int64_t)blockIdx.x * (kThreads / lanes);
     constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
     float big = 0.f;
-    for (int64_t r0 = first; r0 < rows; r0 += step) {  // the same trips for the whole block
-        const int64_t r = r0 + threadIdx.x / lanes;
-        const int64_t i = r / a.hq;
-        const int h = (int)(r - i * a.hq);
+    // row r = (i, h), carried along without a division
+    int64_t r = first + threadIdx.x / lanes, i = r / a.hq;
+    int h = (int)(r - i * a.hq);
+    const int64_t di = step / a.hq;
+    const int dh = (int)(step - di * a.hq);
+    for (int64_t r0 = first; r0 < rows; r0 += step, r += step) {  // the same trips for the whole block
         float sum = 0.f, sq = 0.f;
         if (r < rows && lane * 8 < a.d) {
             float o[8], g[8];
@@ -96,23 +98,23 @@ __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int l
             big = fmaxf(big, sq);
         }
         if (r < rows && lane == 0) {
-            const int hs = h / a.gp;
-            float* st = a.stats + ((int64_t)hs * a.n_q + i) * a.gp + (h - hs * a.gp);
+            float* st = a.stats + (((int64_t)(h >> a.gp_log2) * a.n_q + i) << a.gp_log2) + (h & (a.gp - 1));
             st[0] = fmaf(a.lse[(int64_t)h * a.n_q + i], -1.4426950408889634f, kHalf ? kHalfLift : 0.f);
             st[rows] = -sum;
         }
+        i += di;
+        if ((h += dh) >= a.hq) h -= a.hq, ++i;
     }
     if constexpr (kHalf) {
         block_max(sqrtf(big), a.err + 1);
         big = 0.f;
         const int64_t krows = a.n_k * a.hk;
         for (int64_t r0 = first; r0 < krows; r0 += step) {
-            const int64_t r = r0 + threadIdx.x / lanes;
-            const int64_t j = r / a.hk;
+            const int64_t row = r0 + threadIdx.x / lanes, j = row / a.hk;
             float sq = 0.f;
-            if (r < krows && lane * 8 < a.d && valid_key(a, j)) {
+            if (row < krows && lane * 8 < a.d && valid_key(a, j)) {
                 float v[8];
-                load8<T>(head_row<const T>(a.v, j, (int)(r - j * a.hk)) + lane * 8, v);
+                load8<T>(head_row<const T>(a.v, j, (int)(row - j * a.hk)) + lane * 8, v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sq = fmaf(v[i], v[i], sq);
             }
