@@ -194,3 +194,22 @@ def test_on_another_stream():
     s.synchronize()
     ops.vg_adamw_step(u["st"], 1, 1e-2)
     assert torch.equal(t["masters"][0], u["masters"][0]) and torch.equal(t["st"].m, u["st"].m)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_each_operation_is_rounded_by_itself(dtype, bits):
+    """A step from zero moments, then another one, bit for bit as single fp32 operations (each a pass of its own here)
+    give it; with bits = 8 the second step starts from the decoded codes."""
+    t = make([70001], dtype, bits, master=True, seed=3)
+    p, grad = t["masters"][0].clone(), t["grads"][0].float()
+    f32 = lambda x: torch.tensor(x, dtype=torch.float32, device="cuda")  # noqa: E731
+    b1, omb1, b2, omb2 = (f32(x) for x in (H["beta1"], 1 - H["beta1"], H["beta2"], 1 - H["beta2"]))
+    for step in (1, 2):
+        m, v = (x[0].float() for x in moments(t))
+        ops.vg_adamw_step(t["st"], step, H["lr"], H["beta1"], H["beta2"], H["eps"])
+        m = m * b1 + grad * omb1
+        v = v * b2 + (grad * grad) * omb2
+        den = v.sqrt() * f32((1 - H["beta2"] ** step) ** -0.5) + f32(H["eps"])
+        p = p * f32(1 - H["lr"] * t["decay"][0]) - (m / den) * f32(H["lr"] / (1 - H["beta1"] ** step))
+        assert torch.equal(t["masters"][0], p) and torch.equal(t["params"][0], p.to(DT[dtype]))

@@ -5,7 +5,8 @@
 //
 // Every product, sum, root and quotient is rounded once in fp32 (no contraction
 // into fused multiply-adds), so the results do not depend on how the compiler
-// schedules the kernel.
+// schedules the kernel.  (So no f32x2 instructions either: their products and sums came
+// out fused.)
 //
 // 8-bit moments come in blocks of 256 elements that share one power-of-two scale,
 // so that scaling and unscaling are exact:
@@ -23,12 +24,11 @@
 // thread with 16-byte accesses; a warp holds exactly one 256-element block, so the
 // 8-bit scales are warp reductions.  bf16 weights with fp32 masters: 65.0 M with fp32
 // moments 262 us (30 bytes each, 7.4 TB/s, bound by memory); 32.5 M with 8-bit moments
-// 101 us (18 bytes each, 5.8 TB/s, bound by memory and by the rounded roots and
-// quotients about alike).  Two elements to an instruction and the conversion
-// instructions for m's codes brought the latter from 132 us.
+// 107 us (18 bytes each, 5.5 TB/s, bound by memory and by the rounded roots and
+// quotients about alike).  The conversion instructions for m's codes and a maximum
+// that looks for infinities only when it finds one brought the latter from 132 us.
 #include "common.cuh"
 #include "internal.h"
-#include "tc_ptx.cuh"
 
 namespace vg {
 
@@ -220,29 +220,19 @@ __device__ __forceinline__ void step_chunk(const TensorArgs& a, const Hyper& h, 
         decode_u4(cv.x, v);
         decode_u4(cv.y, v + 4);
     }
-    // two elements to an instruction, each operation rounded by itself
-    const auto both = [](float x) { return make_float2(x, x); };
-    const float2 b1 = both(h.b1), omb1 = both(h.omb1), b2 = both(h.b2), omb2 = both(h.omb2), gs = both(h.grad_scale);
-    const float2 bc2 = both(h.inv_sqrt_bc2), eps = both(h.eps), decay = both(a.decay), back = both(-h.step_size);
 #pragma unroll
-    for (int j = 0; j < kPer; j += 2) {
-        float2 mj = make_float2(m[j], m[j + 1]), vj = make_float2(v[j], v[j + 1]);
+    for (int j = 0; j < kPer; ++j) {
         if constexpr (BITS == 8) {
-            mj = ptx::mul2(mj, both(ms));
-            vj = ptx::mul2(vj, both(vs));
-            vj = ptx::mul2(vj, vj);
+            m[j] = __fmul_rn(m[j], ms);
+            v[j] = __fmul_rn(v[j], vs);
+            v[j] = __fmul_rn(v[j], v[j]);
         }
-        const float2 gj = ptx::mul2(make_float2(g[j], g[j + 1]), gs);
-        mj = ptx::add2(ptx::mul2(mj, b1), ptx::mul2(gj, omb1));
-        vj = ptx::add2(ptx::mul2(vj, b2), ptx::mul2(ptx::mul2(gj, gj), omb2));
-        const float2 uj = make_float2(__fsqrt_rn(vj.x), __fsqrt_rn(vj.y));
-        const float2 den = ptx::add2(ptx::mul2(uj, bc2), eps);
-        const float2 q = make_float2(__fdiv_rn(mj.x, den.x), __fdiv_rn(mj.y, den.y));
-        const float2 pj = ptx::add2(ptx::mul2(make_float2(p[j], p[j + 1]), decay), ptx::mul2(q, back));
-        m[j] = mj.x, m[j + 1] = mj.y;
-        v[j] = vj.x, v[j + 1] = vj.y;
-        u[j] = uj.x, u[j + 1] = uj.y;
-        p[j] = pj.x, p[j + 1] = pj.y;
+        const float gj = __fmul_rn(g[j], h.grad_scale);
+        m[j] = __fadd_rn(__fmul_rn(m[j], h.b1), __fmul_rn(gj, h.omb1));
+        v[j] = __fadd_rn(__fmul_rn(v[j], h.b2), __fmul_rn(__fmul_rn(gj, gj), h.omb2));
+        u[j] = __fsqrt_rn(v[j]);
+        const float den = __fadd_rn(__fmul_rn(u[j], h.inv_sqrt_bc2), h.eps);
+        p[j] = __fsub_rn(__fmul_rn(p[j], a.decay), __fmul_rn(__fdiv_rn(m[j], den), h.step_size));
     }
     store8(static_cast<T*>(a.param), i, n, vec, p);
     if (a.master) store8(a.master, i, n, vec, p);
