@@ -260,13 +260,15 @@ int join_keys(const AttnArgs& a, const float* part, const vg_heads& dst, cudaStr
 // How to cut an axis of `tiles` tiles in all (every sample's together) when there are
 // `units` independent tiles of work along the other one, in `batch` samples, and `slots` run at a time.
 // Parts have one size for all samples, so that a call with one long sample and short ones is even
-// too.  Not cut when the units fill the slots (or, with `fill`, when cutting evens out the last
-// wave by less than the parts' fp32 results cost); a part has at least `least` tiles.
+// too; a part has at least `least` tiles.  Not cut when the units fill the slots.  With `fill` it is cut then too where
+// that evens out the last wave by more than the parts' fp32 results and their join cost (some 20 us): in calls of 256
+// tiles (over 100 us) and more per slot.  dK and dV of 5,000 queries over 2,740 keys, 16 heads: 75 us uncut, 82 + 19 in
+// parts; of 25,179 over 5,001 keys: 290 and 241 + 21; of 100,003 over 2,740: 1280 and 1087 + 21.
 struct Cut { int parts, per; };
 Cut cut_axis(int64_t units, int64_t tiles, int batch, int slots, int least, bool fill) {
     if (units <= 0 || tiles <= 0) return {1, 0};
     int64_t want = slots / units;
-    if (fill) {
+    if (fill && units * ((tiles + batch - 1) / batch) >= 256 * (int64_t)slots) {
         double best = 0.0;
         for (int64_t s = std::max<int64_t>(1, want), end = std::max<int64_t>(8, s); s <= end; ++s) {
             const int64_t n = units * s, waves = (n + slots - 1) / slots;
@@ -302,7 +304,11 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
     Cut f, q, k;
     if (p.tc) {
         const int sets = c.hq / p.gp;
-        p.nq = attn_max_tiles(c.n_q, c.batch, p.gp, 256) * sets >= p.sms ? 2 : 1;
+        // Forward, two row tiles a block against one.  d = 64, 16 heads over 2,740 keys: 33.0 us against 31.6 with
+        // 2,500 queries, 49.4 and 48.6 with 5,000, 76.3 and 76.0 with 10,000, 139 and 142 with 25,179 over 5,001 keys,
+        // 601 and 635 with 100,003.  d = 128, where one tile leaves room for one block all the same: 41.8 against 55.4
+        // with 2,500, 61.7 and 85.0 with 5,000.  With 2 queries over 319,057 keys (d = 64) 135 and 97.
+        p.nq = attn_max_tiles(c.n_q, c.batch, p.gp, 256) * sets >= (c.d <= 64 ? 4 : 1) * p.sms ? 2 : 1;
         const int64_t units = attn_max_tiles(c.n_q, c.batch, p.gp, 128 * p.nq) * sets;
         const int slots = p.nq == 1 && c.d <= 64 ? 2 * p.sms : p.sms;
         f = cut_axis(units, tiles(c.n_k, 128), c.batch, slots, 4, false);
