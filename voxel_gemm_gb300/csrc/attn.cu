@@ -125,6 +125,17 @@ __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int l
     }
 }
 
+// Four consecutive elements, 8 or 16 bytes.
+template <typename T>
+__device__ __forceinline__ void put4(T* p, float4 v) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = v;
+    } else {
+        T e[4] = {from_f32<T>(v.x), from_f32<T>(v.y), from_f32<T>(v.z), from_f32<T>(v.w)};
+        *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+    }
+}
+
 // The parts' outputs, each normalised by its own sum, weighed by exp(lse_s - max lse).  A
 // thread has four columns of a row, and with LANES > 1 every LANES-th part: a few rows over
 // many parts (one token's) would otherwise be a long chain of loads in few threads (32 rows,
@@ -185,27 +196,24 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_out(const AttnArgs a) {
     }
     if (!mine) return;
     const float inv = top == -INFINITY ? 1.f : 1.f / sum;
-    T* o = head_row<T>(a.o, i, h) + c;
-    o[0] = from_f32<T>(acc.x * inv);
-    o[1] = from_f32<T>(acc.y * inv);
-    o[2] = from_f32<T>(acc.z * inv);
-    o[3] = from_f32<T>(acc.w * inv);
+    put4(head_row<T>(a.o, i, h) + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     if (c == 0 && a.lse) a.lse[(int64_t)h * a.n_q + i] = (top == -INFINITY ? 0.f : top) + logf(sum);
 }
 
+// The parts' gradients, added in their order; blockIdx.y: which of two tensors of one shape.
+struct Join { const float* part; vg_heads dst; };
 template <typename T, bool kKeys>
-__global__ void __launch_bounds__(kThreads) k_attn_join_sum(const AttnArgs a, const float* part, vg_heads dst) {
+__global__ void __launch_bounds__(kThreads) k_attn_join_sum(const AttnArgs a, Join one, Join two, int lanes_log2) {
     if (!attn_offsets_ok(a)) return;
-    const int q4 = a.d / 4;
+    const Join& j = blockIdx.y == 0 ? one : two;
+    const int c = (threadIdx.x & ((1 << lanes_log2) - 1)) * 4;  // 2^lanes_log2 threads to a row
     const int64_t rows = kKeys ? a.n_k : a.n_q;
     const int heads = kKeys ? a.hk : a.hq;
-    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (e >= rows * heads * q4) return;
-    const int64_t r = e / q4;
-    const int c = (int)(e - r * q4) * 4;
-    const int64_t i = r / heads;
+    const int64_t r = (int64_t)blockIdx.x * (kThreads >> lanes_log2) + (threadIdx.x >> lanes_log2);
+    if (r >= rows * heads || c >= a.d) return;
+    const int64_t i = r < (int64_t(1) << 31) ? (uint32_t)r / (uint32_t)heads : r / heads;
     const int parts = parts_of<kKeys>(a, i);
-    const float* src = part + r * a.d + c;
+    const float* src = j.part + r * a.d + c;
     const int64_t step = rows * heads * a.d;
     float4 acc = *reinterpret_cast<const float4*>(src);
 #pragma unroll 4
@@ -213,11 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_sum(const AttnArgs a, co
         const float4 v = *reinterpret_cast<const float4*>(src + s * step);
         acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
     }
-    T* o = head_row<T>(dst, i, (int)(r - i * heads)) + c;
-    o[0] = from_f32<T>(acc.x);
-    o[1] = from_f32<T>(acc.y);
-    o[2] = from_f32<T>(acc.z);
-    o[3] = from_f32<T>(acc.w);
+    put4(head_row<T>(j.dst, i, (int)(r - i * heads)) + c, acc);
 }
 
 int launched() { return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA; }
@@ -238,19 +242,22 @@ int join_out(const AttnArgs& a, cudaStream_t s) {
     return launched();
 }
 template <typename T, bool kKeys>
-int join_rows(const AttnArgs& a, const float* part, const vg_heads& dst, cudaStream_t s) {
-    const int64_t n = (kKeys ? a.n_k * a.hk : a.n_q * a.hq) * (a.d / 4);
-    const unsigned blocks = (unsigned)((n + kThreads - 1) / kThreads);
-    k_attn_join_sum<T, kKeys><<<blocks, kThreads, 0, s>>>(a, part, dst);
+int join_rows(const AttnArgs& a, const Join& one, const Join& two, int count, cudaStream_t s) {
+    int log2 = 0;
+    while ((4 << log2) < a.d) ++log2;
+    const int64_t rows = kKeys ? a.n_k * a.hk : a.n_q * a.hq, per = kThreads >> log2;
+    const dim3 grid((unsigned)((rows + per - 1) / per), count);
+    k_attn_join_sum<T, kKeys><<<grid, kThreads, 0, s>>>(a, one, two, log2);
     return launched();
 }
 template <typename T>
-int join_queries(const AttnArgs& a, const float* part, const vg_heads& dst, cudaStream_t s) {
-    return join_rows<T, false>(a, part, dst, s);
+int join_queries(const AttnArgs& a, cudaStream_t s) {
+    const Join q{a.part, a.gq};
+    return join_rows<T, false>(a, q, q, 1, s);
 }
 template <typename T>
-int join_keys(const AttnArgs& a, const float* part, const vg_heads& dst, cudaStream_t s) {
-    return join_rows<T, true>(a, part, dst, s);
+int join_keys(const AttnArgs& a, const float* part_dv, cudaStream_t s) {
+    return join_rows<T, true>(a, Join{a.part, a.gk}, Join{part_dv, a.gv}, 2, s);
 }
 
 #define VG_BY_TYPE(f, ...)                                \
@@ -378,7 +385,7 @@ int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
         a.part = reinterpret_cast<float*>(ws + p.off_dq);
         st = p.tc ? attn_tc_dq(a, dtype, p.sms, s) : attn_simt_dq(a, s);
         if (st != VG_OK) return st;
-        if (a.splits > 1 && (st = VG_BY_TYPE(join_queries, a, a.part, a.gq, s)) != VG_OK) return st;
+        if (a.splits > 1 && (st = VG_BY_TYPE(join_queries, a, s)) != VG_OK) return st;
     }
     if (a.n_k > 0) {
         a.splits = p.s_dkv;
@@ -388,10 +395,7 @@ int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
         float* part_dv = reinterpret_cast<float*>(ws + p.off_dv);
         st = p.tc ? attn_tc_dkv(a, part_dv, dtype, p.sms, s) : attn_simt_dkv(a, part_dv, s);
         if (st != VG_OK) return st;
-        if (a.splits > 1) {
-            if ((st = VG_BY_TYPE(join_keys, a, a.part, a.gk, s)) != VG_OK) return st;
-            if ((st = VG_BY_TYPE(join_keys, a, part_dv, a.gv, s)) != VG_OK) return st;
-        }
+        if (a.splits > 1 && (st = VG_BY_TYPE(join_keys, a, part_dv, s)) != VG_OK) return st;
     }
     return VG_OK;
 }
