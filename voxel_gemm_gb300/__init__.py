@@ -1,4 +1,4 @@
-"""GB300-native submanifold sparse 3D convolution (sm_103a).
+"""GB300-native submanifold sparse 3D convolution, and the attention block around it (sm_103a).
 
 The compute path is the C-ABI library ``libvoxelgemm.so`` built from
 ``csrc/`` (declared in ``include/vg.h``); ``ops`` is its thin Python binding.
