@@ -484,17 +484,18 @@ def cross_attn_workspace(n_q, n_k, batch, heads_q, heads_k, head_dim, dtype, bac
 
 
 def _attn(q, k, q_offsets, k_offsets, k_lens, lse, scale, what):
-    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != k.shape[2]:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or qs[2] != ks[2]:
         raise ValueError(f"{what}: q and k are [rows, heads, head_dim] of one head_dim")
+    n_q, hq, d = qs
     batch = q_offsets.numel() - 1
     for t, n, name in ((q_offsets, batch + 1, "q_offsets"), (k_offsets, batch + 1, "k_offsets"),
                        (k_lens, batch, "k_lens")):
         if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda):
             raise ValueError(f"{what}: {name} must be contiguous int32 [{n}] on the GPU")
-    n_q, hq, d = q.shape
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (hq, n_q) or not lse.is_contiguous()):
         raise ValueError(f"{what}: lse must be contiguous float32 [heads_q, n_q]")
-    return AttnStruct(n_q, k.shape[0], batch, hq, k.shape[1], d, _DT.get(q.dtype, -1),
+    return AttnStruct(n_q, ks[0], batch, hq, ks[1], d, _DT.get(q.dtype, -1),
                       d ** -0.5 if scale is None else scale, q_offsets.data_ptr(), k_offsets.data_ptr(),
                       None if k_lens is None else k_lens.data_ptr())
 
