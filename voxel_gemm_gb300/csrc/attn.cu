@@ -311,11 +311,12 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
     Cut f, q, k;
     if (p.tc) {
         const int sets = c.hq / p.gp;
-        // Forward, two row tiles a block against one.  d = 64, 16 heads over 2,740 keys: 33.0 us against 31.6 with
-        // 2,500 queries, 49.4 and 48.6 with 5,000, 76.3 and 76.0 with 10,000, 139 and 142 with 25,179 over 5,001 keys,
-        // 601 and 635 with 100,003.  d = 128, where one tile leaves room for one block all the same: 41.8 against 55.4
-        // with 2,500, 61.7 and 85.0 with 5,000.  With 2 queries over 319,057 keys (d = 64) 135 and 97.
-        p.nq = attn_max_tiles(c.n_q, c.batch, p.gp, 256) * sets >= (c.d <= 64 ? 4 : 1) * p.sms ? 2 : 1;
+        // Forward, two row tiles a block against one, where that leaves no SM without a block.  d = 64, 16 heads over
+        // 2,740 keys: 30.7 us against 31.2 with 2,500 queries, 46.0 and 47.5 with 5,000, 71.6 and 75.5 with 10,000,
+        // 132 and 142 with 25,179 over 5,001 keys, 571 and 635 with 100,003.  d = 128, where one tile leaves room for
+        // one block all the same: 40.0 against 51.7 with 2,500, 60.8 and 80.6 with 5,000.  Below, with 2 queries over
+        // 319,057 keys (d = 64), 135 and 97.
+        p.nq = attn_max_tiles(c.n_q, c.batch, p.gp, 256) * sets >= p.sms ? 2 : 1;
         const int64_t units = attn_max_tiles(c.n_q, c.batch, p.gp, 128 * p.nq) * sets;
         const int slots = p.nq == 1 && c.d <= 64 ? 2 * p.sms : p.sms;
         f = cut_axis(units, tiles(c.n_k, 128), c.batch, slots, 4, false);

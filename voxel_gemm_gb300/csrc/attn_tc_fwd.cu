@@ -28,9 +28,10 @@
 // Bound by the exponentials' warps, of which an SM holds eight: they take some 1,200 cycles
 // for a tile's weights and wait some 700 for the next scores, which lie in the same columns
 // and so come after the product with V (scores beside the weights' own columns took that
-// wait away and made the warps slower by as much: 622 us against 601; four threads to a row in
-// 16 warps, 1361).  100,003 queries over 2 x 1,370 keys, 16 heads of 64, bf16: 601 us
-// (0.93 PFLOP/s); 25,179 over 4 x 1,024, 16 heads of 128, fp16: 117 us (1.2 PFLOP/s).
+// wait away and made the warps slower by as much: 622 us against 601 at the time; four threads
+// to a row in 16 warps, 1361; all of a row's weights stored at once in place of each half
+// when it is done, 571).  100,003 queries over 2 x 1,370 keys, 16 heads of 64, bf16: 571 us
+// (0.98 PFLOP/s); 25,179 over 4 x 1,024, 16 heads of 128, fp16: 118 us (1.2 PFLOP/s).
 // 2 queries over 2 x 159,528 keys: 97 us, 6.7 TB/s, the memory's rate.
 #include "attn_tc.cuh"
 
@@ -284,36 +285,33 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                 tc_fence_after();
                 if (any) {
                     const int left = x.lk - e * kN;                   // valid keys of the tile
-                    uint32_t s[kN / 32][32];
+                    uint32_t s[kN / 32][32], p[kN / 64][32];
+                    float sum;
+                    auto load = [&] {
 #pragma unroll
-                    for (int i = 0; i < kN / 32; ++i) tmem_ld32(t_s + 32 * i, s[i]);
-                    tmem_ld_wait();
+                        for (int i = 0; i < kN / 32; ++i) tmem_ld32(t_s + 32 * i, s[i]);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < kN / 32; ++i) tmem_ld_done(s[i]);
-                    if (left < kN) {
+                        for (int i = 0; i < kN / 32; ++i) tmem_ld_done(s[i]);
+                        if (left < kN) {
 #pragma unroll
-                        for (int i = 0; i < kN; ++i)
-                            if (i >= left) s[i >> 5][i & 31] = 0xff800000u;
-                    }
-                    // P, 64 keys at a time, and its sum
+                            for (int i = 0; i < kN; ++i)
+                                if (i >= left) s[i >> 5][i & 31] = 0xff800000u;
+                        }
+                    };
                     auto weights = [&] {
                         const float base = kLift - (m == -INFINITY ? 0.f : m * c);
                         const float2 c2 = make_float2(c, c), base2 = make_float2(base, base);
                         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                        for (int i = 0; i < kN / 64; ++i) {
-                            uint32_t p[32];
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                float2 x2 = fma2(two(&s[2 * i + (j >> 4)][2 * (j & 15)]), c2, base2);
-                                x2 = make_float2(ex2(x2.x), ex2(x2.y));
-                                acc[j & 1] = add2(acc[j & 1], x2);
-                                p[j] = pack2<BF16>(x2.x, x2.y);
-                            }
-                            tmem_st32(t_s + 32 * i, p);
+                        for (int j = 0; j < kN / 2; ++j) {
+                            float2 x2 = fma2(two(&s[j >> 4][2 * (j & 15)]), c2, base2);
+                            x2 = make_float2(ex2(x2.x), ex2(x2.y));
+                            acc[j & 1] = add2(acc[j & 1], x2);
+                            p[j >> 5][j & 31] = pack2<BF16>(x2.x, x2.y);
                         }
                         const float2 both = add2(acc[0], acc[1]);
-                        return both.x + both.y;
+                        sum = both.x + both.y;
                     };
                     auto renew_max = [&](bool rescale) {
                         float top[kN / 32];
@@ -342,13 +340,16 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                             }
                         }
                     };
-                    float sum;  // weighed twice only where the maximum has to be renewed
+                    // a second pass only where the maximum has to be renewed (P is not yet over the scores)
                     for (bool renew = e == x.lo;; renew = true) {
+                        load();
                         if (renew) renew_max(e > x.lo);
-                        sum = weights();
+                        weights();
                         if (renew || !__any_sync(0xffffffffu, mine && (!(sum <= kMost) || m == -INFINITY))) break;
                     }
                     l += sum;
+#pragma unroll
+                    for (int i = 0; i < kN / 64; ++i) tmem_st32(t_s + 32 * i, p[i]);
                     tmem_st_wait();
                 }
                 tc_fence_before();
