@@ -44,12 +44,13 @@ __device__ __forceinline__ bool valid_key(const AttnArgs& a, int64_t j) {
     return j - a.k_off[b] < a.k_len[b];
 }
 
-// Parts that the results of query row (kKeys: key row) j lie in.
+// Rows of the other axis that the results of query row (kKeys: key row) j are sums over: its sample's valid keys
+// (kKeys: its packed query rows).
 template <bool kKeys>
-__device__ __forceinline__ int parts_of(const AttnArgs& a, int64_t j) {
+__device__ __forceinline__ int64_t summed_rows(const AttnArgs& a, int64_t j) {
     const int b = sample_of(a, kKeys ? a.k_off : a.q_off, j);
-    if (kKeys) return attn_parts(a, (int64_t)(a.q_off[b + 1] - a.q_off[b]) * a.gp);
-    return attn_parts(a, a.k_len ? a.k_len[b] : a.k_off[b + 1] - a.k_off[b]);
+    if (kKeys) return (int64_t)(a.q_off[b + 1] - a.q_off[b]) * a.gp;
+    return a.k_len ? a.k_len[b] : a.k_off[b + 1] - a.k_off[b];
 }
 
 // Largest value of the block into *word, as the bits of a non-negative float (their
@@ -136,10 +137,12 @@ __device__ __forceinline__ void put4(T* p, float4 v) {
     }
 }
 
-// The parts' outputs, each normalised by its own sum, weighed by exp(lse_s - max lse).  A
-// thread has four columns of a row, and with LANES > 1 every LANES-th part: a few rows over
-// many parts (one token's) would otherwise be a long chain of loads in few threads (32 rows,
-// 64 parts: 14 us with one lane, 5 us with eight).
+// The parts' outputs, each normalised by its own sum, weighed by exp(lse_s - max lse).  Every part counts, with a
+// weight of zero too: 0 x its output is 0, or NaN where it holds something that is not finite, as in a call that is not
+// cut.  (A part whose scores are all -inf has no sum to be normalised by and comes as it is.)  The maximum leaves NaN
+// out, so a sum that is NaN says that something is.  A thread has four columns of a row, and with LANES > 1 every
+// LANES-th part: a few rows over many parts (one token's) would otherwise be a long chain of loads in few threads (32
+// rows, 64 parts: 14 us with one lane, 5 us with eight).
 template <typename T, int LANES>
 __global__ void __launch_bounds__(kThreads) k_attn_join_out(const AttnArgs a) {
     constexpr int kItems = kThreads / LANES;  // pieces of rows of a block
@@ -155,7 +158,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_out(const AttnArgs a) {
     const int h = (int)(r - i * a.hq);
     const float* lse = a.part_lse + (int64_t)h * a.n_q + i;
     const int64_t lstep = (int64_t)a.hq * a.n_q;
-    const int parts = mine ? parts_of<false>(a, i) : 0;
+    const int64_t keys = mine ? summed_rows<false>(a, i) : 0;
+    const int parts = mine ? attn_parts(a, keys) : 0;
     float top = -INFINITY;
 #pragma unroll 4
     for (int s = lane; s < parts; s += LANES) top = fmaxf(top, lse[s * lstep]);
@@ -169,12 +173,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_out(const AttnArgs a) {
         const float w = expf(lse[s * lstep] - base);
         const float4 v = *reinterpret_cast<const float4*>(src + s * step);
         sum += w;
-        if (top == -INFINITY) {  // no keys in any part (zeros), or scores of -inf alone (NaN)
-            acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
-        } else if (w != 0.f) {   // a part without keys, or of scores -inf alone, weighs nothing
-            acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
-        }
+        acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
     }
     if constexpr (LANES > 1) {  // the lanes' sums likewise, in their order
         s_top[lane][item] = top;
@@ -185,17 +185,17 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_out(const AttnArgs a) {
         for (int l = 1; l < LANES; ++l) top = fmaxf(top, s_top[l][item]);
         sum = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float all = top == -INFINITY ? 0.f : top;
         for (int l = 0; l < LANES; ++l) {
-            const float w = top == -INFINITY ? 1.f : expf(s_top[l][item] - top);
+            const float w = expf(s_top[l][item] - all);
             const float4 v = s_acc[l][item];
-            if (w == 0.f) continue;
             sum = fmaf(w, s_sum[l][item], sum);
             acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
             acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
         }
     }
     if (!mine) return;
-    const float inv = top == -INFINITY ? 1.f : 1.f / sum;
+    const float inv = keys > 0 ? 1.f / sum : 0.f;  // no keys: zero; only keys of weight zero: NaN
     put4(head_row<T>(a.o, i, h) + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     if (c == 0 && a.lse) a.lse[(int64_t)h * a.n_q + i] = (top == -INFINITY ? 0.f : top) + logf(sum);
 }
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_sum(const AttnArgs a, Jo
     const int64_t r = (int64_t)blockIdx.x * (kThreads >> lanes_log2) + (threadIdx.x >> lanes_log2);
     if (r >= rows * heads || c >= a.d) return;
     const int64_t i = r < (int64_t(1) << 31) ? (uint32_t)r / (uint32_t)heads : r / heads;
-    const int parts = parts_of<kKeys>(a, i);
+    const int parts = attn_parts(a, summed_rows<kKeys>(a, i));
     const float* src = j.part + r * a.d + c;
     const int64_t step = rows * heads * a.d;
     float4 acc = *reinterpret_cast<const float4*>(src);

@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_fwd(const AttnArgs a) {
         const int r = t.first + ty + 16 * i;
         if (r >= t.lq) continue;
         const int64_t row = t.q0 + r;
-        const float inv = hi > lo ? 1.f / l[i] : 0.f;  // no keys: zero; only keys of weight zero: NaN
+        // no keys: zero; only keys of weight zero: NaN (a part of them has no sum to be normalised by)
+        const float inv = hi <= lo ? 0.f : a.splits > 1 && l[i] == 0.f ? 1.f : 1.f / l[i];
         const float lse = hi > lo ? (m[i] + log2f(l[i])) * kLn2 : -INFINITY;
         if (tx == 0) {
             float* dst = a.splits > 1 ? a.part_lse + (size_t)t.part * a.hq * a.n_q : a.lse;

@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                 const int pr = x.first + row;                       // packed row of the sample
                 const int64_t qi = x.q0 + (pr >> a.gp_log2);
                 const int h = x.head * a.gp + (pr & (a.gp - 1));
-                const float inv = x.hi > x.lo ? 1.f / l : 0.f;
+                // a part of weight zero has no sum to be normalised by
+                const float inv = x.hi <= x.lo ? 0.f : a.splits > 1 && l == 0.f ? 1.f : 1.f / l;
                 const float lse = x.hi > x.lo ? (m * c + (log2f(l) - kLift)) * kLn2 : -INFINITY;
                 float* dst_l = a.splits > 1 ? a.part_lse + (size_t)x.part * a.hq * a.n_q : a.lse;
                 if (store && dst_l) dst_l[(int64_t)h * a.n_q + qi] = lse;
