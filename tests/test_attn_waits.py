@@ -1,0 +1,134 @@
+"""The arithmetic of waiting in the tensor-core attention kernels (csrc/attn_waits.h), compiled for the host (CPU only).
+
+The loaders' loops are written out again here over a model of barriers and copies, and made to give up at each of
+their waits in turn."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "voxel_gemm_gb300", "csrc")
+
+
+def run(tmp_path, source):
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no g++")
+    src, exe = tmp_path / "t.cc", tmp_path / "t"
+    src.write_text(source)
+    subprocess.run([cxx, "-std=c++17", "-Wall", "-Werror", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout
+
+
+LOADERS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <map>
+#include <utility>
+#include "attn_waits.h"
+using namespace vg;
+
+// phases that copies (and the zeroing of a tail) complete on each barrier, in order; the last may be in flight
+struct Model {
+    std::map<std::pair<int, int>, int> phases;   // (barrier, slot) -> copies issued
+    int waits = 0, stop;
+    bool ok = true;
+    explicit Model(int stop) : stop(stop) {}
+    bool wait() { if (waits++ == stop) ok = false; return ok; }
+    void copy(int bar, int slot) { ++phases[{bar, slot}]; }
+    void seen(int bar, int slot, unsigned parity) {
+        auto it = phases.find({bar, slot});
+        if (it == phases.end() || it->second < 0) { printf("a wait for no copy\n"); exit(1); }
+        if (((it->second - 1) & 1u) != parity) { printf("wrong phase of barrier %d slot %d\n", bar, slot); exit(1); }
+        it->second = -1;
+    }
+    void all_seen() {
+        for (auto& x : phases)
+            if (x.second != -1) { printf("copy on barrier %d slot %d left in flight (stop %d)\n", x.first.first,
+                                         x.first.second, stop); exit(1); }
+    }
+};
+enum { Q, K, V, TAIL };
+template <int S> void land(Model& m, const Copies<S>& c, int bar) {
+    c.in_flight([&](uint32_t slot, uint32_t parity) { m.seen(bar, slot, parity); });
+}
+
+// forward: K and V of a tile by copies of their own; the sample's last V through the tail's barrier
+template <int S> bool forward(int stop, int units, int tiles, bool cut) {
+    Model m(stop);
+    Copies<1> qs, tails;
+    Copies<S> ks, vs;
+    uint32_t at = 0;
+    for (int u = 0; u < units && m.ok; ++u) {
+        if (!m.wait()) break;
+        m.copy(Q, 0);
+        qs.issued();
+        for (int e = 0; e < tiles; ++e, at = (at + 1) % S) {
+            if (!m.wait()) break;
+            m.copy(K, at);
+            ks.issued();
+            if (!m.wait()) break;
+            const bool last = cut && e + 1 == tiles;
+            m.copy(last ? TAIL : V, last ? 0 : at);
+            if (last) {
+                tails.issued();
+                if (!m.wait()) break;
+                m.copy(V, at);                       // the arrival behind the zeroing
+            }
+            vs.issued();
+        }
+    }
+    land(m, qs, Q), land(m, ks, K), land(m, vs, V), land(m, tails, TAIL);
+    m.all_seen();
+    return m.waits <= stop;
+}
+// backward: one barrier for the two tiles of a step
+template <int S> bool backward(int stop, int units, int sets, int tiles, bool cut) {
+    Model m(stop);
+    Copies<1> qs, tails;
+    Copies<S> steps;
+    uint32_t at = 0;
+    for (int u = 0; u < units && m.ok; ++u) {
+        if (!m.wait()) break;
+        m.copy(Q, 0);
+        qs.issued();
+        for (int h = 0; h < sets && m.ok; ++h)
+            for (int e = 0; e < tiles; ++e, at = (at + 1) % S) {
+                if (!m.wait()) break;
+                const bool last = cut && e + 1 == tiles;
+                m.copy(last ? TAIL : K, last ? 0 : at);
+                if (last) {
+                    tails.issued();
+                    if (!m.wait()) break;
+                    m.copy(K, at);
+                }
+                steps.issued();
+            }
+    }
+    land(m, qs, Q), land(m, steps, K), land(m, tails, TAIL);
+    m.all_seen();
+    return m.waits <= stop;
+}
+int main() {
+    for (int units = 0; units <= 4; ++units)
+        for (int tiles = 1; tiles <= 7; ++tiles)
+            for (int cut = 0; cut < 2; ++cut) {
+                for (int stop = 0; !forward<2>(stop, units, tiles, cut); ++stop) {}
+                for (int stop = 0; !forward<5>(stop, units, tiles, cut); ++stop) {}
+                for (int sets = 1; sets <= 3; ++sets) {
+                    for (int stop = 0; !backward<2>(stop, units, sets, tiles, cut); ++stop) {}
+                    for (int stop = 0; !backward<4>(stop, units, sets, tiles, cut); ++stop) {}
+                    for (int stop = 0; !backward<8>(stop, units, sets, tiles, cut); ++stop) {}
+                }
+            }
+    printf("all seen\n");
+}
+"""
+
+
+def test_no_copy_is_left_in_flight(tmp_path):
+    """Wherever a loader gives up, the copies that it waits for at its end are all that can be in flight."""
+    assert "all seen" in run(tmp_path, LOADERS)

@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "attn.cuh"
+#include "attn_waits.h"
 #include "tc_ptx.cuh"
 
 namespace vg {
@@ -192,6 +193,14 @@ struct Waiter {
         return false;
     }
 };
+
+// Wait for the copies that can still be in flight, whatever became of the block; barriers 8 bytes apart from `bar`.
+template <int S>
+__device__ __forceinline__ void land(Waiter& wait, const Copies<S>& copies, uint32_t bar) {
+    copies.in_flight([&](uint32_t slot, uint32_t parity) {
+        if (!mbar_wait_timed(bar + 8 * slot, parity)) wait.ok = false;
+    });
+}
 
 template <int V> using Const = std::integral_constant<int, V>;
 

@@ -157,10 +157,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring.put(wait, x);
     } else if (warp == kLoader) {
         RingPos<S> pos;
-        uint32_t n = 0, uc = 0, tc = 0;  // tiles and units loaded
+        Copies<1> qs, tails;  // tiles that end the sample's keys land on the tail's barrier
+        Copies<S> kvs;
         while (ring.get(wait, x)) {
             if (x.hi <= x.lo) continue;
-            wait(q_empty, (uc & 1u) ^ 1u);
+            wait(q_empty, (qs.n & 1u) ^ 1u);
             if (!wait.ok) break;
             const int kh = x.head * a.gp / group, row = x.q0 + (x.first >> a.gp_log2);
             one_lane([&] {
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(sG + b * kM * 128, &maps.go, b * 64, x.head * a.gp, row, q_full);
                 }
             });
-            ++uc;
+            qs.issued();
             for (int e = x.lo; e < x.hi; ++e) {
                 const uint32_t k = sKV + 2 * pos.i * C::kTile;
                 wait(kv_empty + 8 * pos.i, pos.phase ^ 1u);
@@ -185,23 +186,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 });
                 if (n16 != left) {  // K rows past the sample's keys may hold anything: 0 x them must be 0 in dS K
-                    wait(tail, tc++ & 1u);
+                    tails.issued();
+                    if (!wait(tail, (tails.n - 1) & 1u)) break;
                     zero_rows(k, left, n16, C::kBlocks, kN * 128);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(kv_full + 8 * pos.i);
                     __syncwarp();
                 }
+                kvs.issued();
                 pos.step();
-                ++n;
             }
         }
         // every copy has landed before the block may exit
-        if (uc > 0 && !mbar_wait_timed(q_full, (uc - 1) & 1u)) wait.ok = false;
-        for (uint32_t i = 0; i < (uint32_t)S && i < n; ++i) {
-            const uint32_t last = n - 1 - i;
-            if (!mbar_wait_timed(kv_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
-        }
+        land(wait, qs, q_full);
+        land(wait, kvs, kv_full);
+        land(wait, tails, tail);
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer || warp == kIssuer2) {
         const int ksteps = (a.d + 15) / 16;
@@ -494,10 +494,11 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         ring.put(wait, x);
     } else if (warp == kLoader) {
         RingPos<S> pos;
-        uint32_t n = 0, uc = 0, tc = 0;  // steps and units loaded
+        Copies<1> keys, tails;  // row tiles that end the sample's queries land on the tail's barrier
+        Copies<S> steps;
         while (ring.get(wait, x)) {
             if (x.hi <= x.lo) continue;
-            wait(k_empty, (uc & 1u) ^ 1u);
+            wait(k_empty, (keys.n & 1u) ^ 1u);
             if (!wait.ok) break;
             one_lane([&] {
                 mbar_arrive_expect_tx(k_full, 2 * C::kKeyTile);
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                     tma_load_3d(sV + b * kM * 128, &maps.v, b * 64, x.head, x.k0 + x.first, k_full);
                 }
             });
-            ++uc;
+            keys.issued();
             for (int hs = 0; hs < sets && wait.ok; ++hs)
                 for (int e = x.lo; e < x.hi; ++e) {
                     const uint32_t q = sQG + 2 * pos.i * C::kRowTile;
@@ -532,7 +533,8 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                     cp_async_arrive_noinc(r_full + 8 * pos.i);
                     __syncwarp();
                     if (n16 != left) {  // rows of the next sample: 0 x them must be 0 in dS^T Q and P^T dO
-                        wait(tail, tc++ & 1u);
+                        tails.issued();
+                        if (!wait(tail, (tails.n - 1) & 1u)) break;
                         zero_rows(q, left, n16, C::kBlocks, kNK * 128);
                         zero_rows(q + C::kRowTile, left, n16, C::kBlocks, kNK * 128);
                         fence_proxy_async_smem();
@@ -540,16 +542,15 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                         if (lane == 0) mbar_arrive(r_full + 8 * pos.i);
                         __syncwarp();
                     }
+                    steps.issued();
                     pos.step();
-                    ++n;
                 }
         }
         // every copy has landed before the block may exit
-        if (uc > 0 && !mbar_wait_timed(k_full, (uc - 1) & 1u)) wait.ok = false;
-        for (uint32_t i = 0; i < (uint32_t)S && i < n; ++i) {
-            const uint32_t last = n - 1 - i;
-            if (!mbar_wait_timed(r_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
-        }
+        land(wait, keys, k_full);
+        land(wait, steps, r_full);
+        land(wait, tails, tail);
+        cp_async_wait_all();  // the statistics of a step whose tiles never landed
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer || (C::kOwn && warp == kIssuer2)) {
         const int ksteps = (a.d + 15) / 16;

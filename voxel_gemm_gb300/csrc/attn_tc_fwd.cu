@@ -144,10 +144,11 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
         ring.put(wait, x);
     } else if (warp == kLoader) {
         RingPos<S> pos;
-        uint32_t n = 0, uc = 0, tc = 0;  // tiles and units loaded
+        Copies<1> qs, tails;  // V tiles that end the sample's keys land on the tail's barrier
+        Copies<S> ks, vs;
         while (ring.get(wait, x)) {
             if (x.hi <= x.lo) continue;
-            wait(q_empty, (uc & 1u) ^ 1u);
+            wait(q_empty, (qs.n & 1u) ^ 1u);
             if (!wait.ok) break;
             const int nq = x.rows > kM ? NQ : 1, kh = x.head * a.gp / group;
             one_lane([&] {
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                         tma_load_3d(sQ + w * C::kTile + b * kM * 128, &maps.q, b * 64, x.head * a.gp,
                                     x.q0 + ((x.first + w * kM) >> a.gp_log2), q_full);
             });
-            ++uc;
+            qs.issued();
             for (int e = x.lo; e < x.hi; ++e) {
                 const uint32_t k = sKV + 2 * pos.i * C::kTile, v = k + C::kTile;
                 wait(k_empty + 8 * pos.i, pos.phase ^ 1u);
@@ -167,6 +168,7 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                     for (int b = 0; b < C::kBlocks; ++b)
                         tma_load_3d(k + b * kN * 128, &maps.k, b * 64, kh, x.k0 + e * kN, k_full + 8 * pos.i);
                 });
+                ks.issued();
                 wait(v_empty + 8 * pos.i, pos.phase ^ 1u);
                 if (!wait.ok) break;
                 const int left = min(kN, x.lk - e * kN), n16 = (left + 15) / 16 * 16;
@@ -177,24 +179,23 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                         tma_load_3d(v + b * kN * 128, &maps.v, b * 64, kh, x.k0 + e * kN, bar);
                 });
                 if (n16 != left) {  // V rows past the sample's keys may hold anything: 0 x them must be 0 in P V
-                    wait(tail, tc++ & 1u);
+                    tails.issued();
+                    if (!wait(tail, (tails.n - 1) & 1u)) break;
                     zero_rows(v, left, n16, C::kBlocks, kN * 128);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(v_full + 8 * pos.i);
                     __syncwarp();
                 }
+                vs.issued();
                 pos.step();
-                ++n;
             }
         }
         // every copy has landed before the block may exit
-        if (uc > 0 && !mbar_wait_timed(q_full, (uc - 1) & 1u)) wait.ok = false;
-        for (uint32_t i = 0; i < (uint32_t)S && i < n; ++i) {
-            const uint32_t last = n - 1 - i;
-            if (!mbar_wait_timed(k_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
-            if (!mbar_wait_timed(v_full + 8 * (last % S), (last / S) & 1u)) wait.ok = false;
-        }
+        land(wait, qs, q_full);
+        land(wait, ks, k_full);
+        land(wait, vs, v_full);
+        land(wait, tails, tail);
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;          // K = 16 steps over the channels
