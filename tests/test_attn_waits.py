@@ -75,7 +75,7 @@ template <int S> bool forward(int stop, int units, int tiles, bool cut) {
             m.copy(last ? TAIL : V, last ? 0 : at);
             if (last) {
                 tails.issued();
-                if (!m.wait()) break;
+                m.wait();
                 m.copy(V, at);                       // the arrival behind the zeroing
             }
             vs.issued();
@@ -102,7 +102,7 @@ template <int S> bool backward(int stop, int units, int sets, int tiles, bool cu
                 m.copy(last ? TAIL : K, last ? 0 : at);
                 if (last) {
                     tails.issued();
-                    if (!m.wait()) break;
+                    m.wait();
                     m.copy(K, at);
                 }
                 steps.issued();

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 });
                 if (n16 != left) {  // K rows past the sample's keys may hold anything: 0 x them must be 0 in dS K
                     tails.issued();
-                    if (!wait(tail, (tails.n - 1) & 1u)) break;
+                    wait(tail, (tails.n - 1) & 1u);
                     zero_rows(k, left, n16, C::kBlocks, kN * 128);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                     __syncwarp();
                     if (n16 != left) {  // rows of the next sample: 0 x them must be 0 in dS^T Q and P^T dO
                         tails.issued();
-                        if (!wait(tail, (tails.n - 1) & 1u)) break;
+                        wait(tail, (tails.n - 1) & 1u);
                         zero_rows(q, left, n16, C::kBlocks, kNK * 128);
                         zero_rows(q + C::kRowTile, left, n16, C::kBlocks, kNK * 128);
                         fence_proxy_async_smem();

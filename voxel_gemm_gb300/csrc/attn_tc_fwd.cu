@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                 });
                 if (n16 != left) {  // V rows past the sample's keys may hold anything: 0 x them must be 0 in P V
                     tails.issued();
-                    if (!wait(tail, (tails.n - 1) & 1u)) break;
+                    wait(tail, (tails.n - 1) & 1u);
                     zero_rows(v, left, n16, C::kBlocks, kN * 128);
                     fence_proxy_async_smem();
                     __syncwarp();
