@@ -132,3 +132,38 @@ int main() {
 def test_no_copy_is_left_in_flight(tmp_path):
     """Wherever a loader gives up, the copies that it waits for at its end are all that can be in flight."""
     assert "all seen" in run(tmp_path, LOADERS)
+
+
+LIMITS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "attn_waits.h"
+using namespace vg;
+
+// The longest unit at `cycles` a step, against the limit of a wait for it.
+void check(const char* what, int splits, int per, int64_t rows, int tile, int64_t sets, double steps) {
+    const int64_t n = unit_steps(splits, per, rows, tile, sets);
+    const double need = steps * 16 * 3000.0;       // 16 times what the slowest step takes
+    if ((double)n < steps || (double)unit_wait_cycles(n) < need || unit_wait_cycles(n) < kWaitCycles) {
+        printf("%s: %.3g steps take %.3g cycles, the wait gives up after %.3g\n", what, steps, need,
+               (double)unit_wait_cycles(n));
+        exit(1);
+    }
+}
+int main() {
+    const int64_t most = (int64_t(1) << 31) - 1;
+    check("one tile", 1, 0, 5, 128, 1, 1);
+    check("250 M packed rows against one tile of keys", 1, 0, 250000000, 64, 1, 250e6 / 64);
+    check("as many rows as offsets allow, 8 head sets", 1, 0, most, 64, 8, 8.0 * most / 64);
+    check("as many keys as offsets allow", 1, 0, most, 128, 1, most / 128.0);
+    check("a part of them", 7, 2400000, most, 128, 1, 2400000);
+    check("65,535 heads of as many rows", 1, 0, most, 64, 65535, 65535.0 * most / 64);
+    if (unit_wait_cycles(INT64_MAX) < 0 || unit_wait_cycles(0) != kWaitCycles) return 1;
+    printf("enough\n");
+}
+"""
+
+
+def test_waits_for_units_last_as_long_as_the_longest(tmp_path):
+    """A wait for a whole unit of work allows for the unit's steps, up to what 31-bit offsets and the heads can ask."""
+    assert "enough" in run(tmp_path, LIMITS)

@@ -35,6 +35,7 @@ struct AttnArgs {
     int splits, per_part, tile;
     float* part;                 // results of the parts (layouts at their kernels)
     float* part_lse;
+    int64_t unit_cycles;         // limit of a wait that lasts as long as a unit of work (tensor cores)
 };
 
 // fp16 has no exponent range to spare: the backward pass's weights (<= 1) carry 2^15.
@@ -171,8 +172,8 @@ int attn_simt_dq(const AttnArgs& a, cudaStream_t s);
 int attn_simt_dkv(const AttnArgs& a, float* part_dv, cudaStream_t s);
 
 // ---- 16-bit path (attn_tc_fwd.cu, attn_tc_bwd.cu); nq: row tiles of a forward block ----
-int attn_tc_fwd(const AttnArgs& a, int dtype, int nq, int sms, cudaStream_t s);
-int attn_tc_dq(const AttnArgs& a, int dtype, int sms, cudaStream_t s);
-int attn_tc_dkv(const AttnArgs& a, float* part_dv, int dtype, int sms, cudaStream_t s);
+int attn_tc_fwd(AttnArgs a, int dtype, int nq, int sms, cudaStream_t s);
+int attn_tc_dq(AttnArgs a, int dtype, int sms, cudaStream_t s);
+int attn_tc_dkv(AttnArgs a, float* part_dv, int dtype, int sms, cudaStream_t s);
 
 }  // namespace vg

@@ -174,19 +174,19 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, bool have, uint32_t
 }
 
 // Bounded waits of a whole warp, which goes on or gives up together; a wait that gives
-// up (after about 2 s of the SM's cycle counter) raises the block's abort flag, and the
+// up (after kWaitCycles or the given limit) raises the block's abort flag, and the
 // warp's later waits return at once.  Every branch is on a vote, so that the compiler knows
 // the warp to be converged and keeps what follows (descriptors, addresses, loop counts) in
 // uniform registers.
 struct Waiter {
     volatile uint32_t* abort;
     bool ok = true;
-    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) {
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, int64_t limit = kWaitCycles) {
         if (!ok || __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return ok;
         const int64_t t0 = clock64();
         while (true) {
             if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-            if (__any_sync(0xffffffffu, *abort != 0 || clock64() - t0 > kWaitCycles)) break;
+            if (__any_sync(0xffffffffu, *abort != 0 || clock64() - t0 > limit)) break;
         }
         *abort = 1;
         ok = false;
@@ -269,11 +269,12 @@ constexpr int kUnitSlots = 4;
 struct UnitRing {
     int4* slots;          // [kUnitSlots][3]
     uint32_t full, empty;  // barriers, 8 bytes apart
+    const AttnArgs& a;     // its unit_cycles bounds both waits: the scheduler's for a slot, and a reader's that is ahead
     uint32_t at = 0;
 
     __device__ __forceinline__ void put(Waiter& wait, const Unit& x) {
         const uint32_t i = at % kUnitSlots;
-        wait(empty + 8 * i, ((at / kUnitSlots) & 1u) ^ 1u);
+        wait(empty + 8 * i, ((at / kUnitSlots) & 1u) ^ 1u, a.unit_cycles);
         if ((threadIdx.x & 31) == 0) {
             const int4* src = reinterpret_cast<const int4*>(&x);
             for (int j = 0; j < 3; ++j) slots[3 * i + j] = src[j];
@@ -285,7 +286,7 @@ struct UnitRing {
     // The next unit; false at the end, or when the wait gave up.
     __device__ __forceinline__ bool get(Waiter& wait, Unit& x) {
         const uint32_t i = at % kUnitSlots;
-        if (!wait(full + 8 * i, (at / kUnitSlots) & 1u)) return false;
+        if (!wait(full + 8 * i, (at / kUnitSlots) & 1u, a.unit_cycles)) return false;
         int4* dst = reinterpret_cast<int4*>(&x);
         for (int j = 0; j < 3; ++j) dst[j] = slots[3 * i + j];
         x.first = uniform(x.first);

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int group = a.hq / a.hk;
     Waiter wait{s_abort};
-    UnitRing ring{s_units, u_full, u_empty};
+    UnitRing ring{s_units, u_full, u_empty, a};
     Unit x;
     if (warp == kScheduler) {
         // unit u = (row tile and part, head set): its rows and its key tiles [lo, hi)
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     // A unit is (part and key tile, key head): rows = key rows of the tile, valid or not, [lo, hi) its row tiles of
     // each head set.  Its steps run over (head set, row tile).
     Waiter wait{s_abort};
-    UnitRing ring{s_units, u_full, u_empty};
+    UnitRing ring{s_units, u_full, u_empty, a};
     Unit x;
     if (warp >= kLoader) reg_shrink<C::kAux>();
     if (warp == kScheduler) {
@@ -766,16 +766,18 @@ int make_maps(AttnMaps* m, const AttnArgs& a, int dtype, int qrows) {
 
 }  // namespace
 
-int attn_tc_dq(const AttnArgs& a, int dtype, int sms, cudaStream_t s) {
+int attn_tc_dq(AttnArgs a, int dtype, int sms, cudaStream_t s) {
     AttnMaps m{};
+    a.unit_cycles = unit_wait_cycles(unit_steps(a.splits, a.per_part, a.n_k, kN, 1));
     const int st = make_maps(&m, a, dtype, kM);
     if (st != VG_OK) return st;
     if (dtype == VG_BF16) return a.d <= 64 ? launch_dq<true, 64>(a, m, sms, s) : launch_dq<true, 128>(a, m, sms, s);
     return a.d <= 64 ? launch_dq<false, 64>(a, m, sms, s) : launch_dq<false, 128>(a, m, sms, s);
 }
 
-int attn_tc_dkv(const AttnArgs& a, float* part_dv, int dtype, int sms, cudaStream_t s) {
+int attn_tc_dkv(AttnArgs a, float* part_dv, int dtype, int sms, cudaStream_t s) {
     AttnMaps m{};
+    a.unit_cycles = unit_wait_cycles(unit_steps(a.splits, a.per_part, a.n_q * a.gp, kNK, a.hq / a.hk / a.gp));
     const int st = make_maps(&m, a, dtype, kNK);
     if (st != VG_OK) return st;
     if (dtype == VG_BF16)

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
 
     const int group = a.hq / a.hk;
     Waiter wait{s_abort};
-    UnitRing ring{s_units, u_full, u_empty};
+    UnitRing ring{s_units, u_full, u_empty, a};
     Unit x;
     if (warp >= kLoader) reg_shrink<C::kAux>();
     if (warp == kScheduler) {
@@ -427,8 +427,9 @@ int attn_make_map(CUtensorMap* map, const vg_heads& h, int64_t rows, int heads, 
     return r == CUDA_SUCCESS ? VG_OK : VG_ERR_UNSUPPORTED;
 }
 
-int attn_tc_fwd(const AttnArgs& a, int dtype, int nq, int sms, cudaStream_t s) {
+int attn_tc_fwd(AttnArgs a, int dtype, int nq, int sms, cudaStream_t s) {
     AttnMaps maps{};
+    a.unit_cycles = unit_wait_cycles(unit_steps(a.splits, a.per_part, a.n_k, kN, 1));
     int st = attn_make_map(&maps.q, a.q, a.n_q, a.hq, a.d, dtype, a.gp, kM / a.gp);
     if (st != VG_OK) return st;
     if (a.n_k > 0) {

@@ -26,4 +26,20 @@ struct Copies {
     }
 };
 
+// A hand-over between two warps takes a step's work, some 1,000 to 3,000 cycles; a wait for one gives up after
+// kWaitCycles.  A wait for the next unit, or for the slot of a unit that is being worked on, lasts as long as
+// a unit, whose number of steps the caller sets: it has kStepCycles more for each of them.
+constexpr int64_t kWaitCycles = 4000000000ll;  // about 2 s of an SM's cycle counter
+constexpr int64_t kStepCycles = 1 << 16;
+
+// Most steps of a unit that runs along `rows` rows in tiles of `tile`, `sets` times, in parts of `per_part` tiles if
+// there is more than one.
+VG_HOST_DEVICE int64_t unit_steps(int splits, int per_part, int64_t rows, int tile, int64_t sets) {
+    return (splits > 1 ? (int64_t)per_part : (rows + tile - 1) / tile) * sets;
+}
+VG_HOST_DEVICE int64_t unit_wait_cycles(int64_t steps) {
+    constexpr int64_t most = INT64_MAX / 4 / kStepCycles;
+    return kWaitCycles + (steps < most ? steps : most) * kStepCycles;
+}
+
 }  // namespace vg

@@ -56,8 +56,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const v
     }
 }
 
-constexpr int64_t kWaitCycles = 4000000000ll;  // about 2 s of an SM's cycle counter
-
 // Time-bounded wait that ignores the abort flag (used to drain in-flight work).
 __device__ __forceinline__ bool mbar_wait_timed(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = globaltimer();
