@@ -76,3 +76,34 @@ def test_no_keys_and_keys_of_weight_zero_in_cut_calls(dtype):
     assert not r["out"][2:5].any() and (r["lse"][:, 2:5] == -math.inf).all()
     assert r["out"][5:].isnan().all() and (r["lse"][:, 5:] == -math.inf).all()
     assert r["out"][:2].isfinite().all() and r["lse"][:, :2].isfinite().all()
+
+
+# ------------------------------------------------------------------ gradients of very different sizes
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("what", ["inf gradient", "large gradient", "inf value", "large value", "without keys"])
+def test_a_sample_does_not_set_another_ones_scale(dtype, what):
+    """Whatever stands in one sample, the gradients of the others are the same bits.  Beside something large the
+    others are small (score gradients of 1e-3), beside something infinite large (of 10 and more)."""
+    lk, size = [90, 0 if what == "without keys" else 200, 150], (0.1, 0.1) if "large" in what else (8.0, 1.0)
+    clean = make([100, 70, 45], lk, 4, 2, 64, dtype, seed=47, g_scale=size[0])
+    clean["v"].mul_(size[1])
+    want = call(clean)
+    dirty = dict(clean, go=clean["go"].clone(), v=clean["v"].clone())
+    if what in ("inf gradient", "without keys"):
+        dirty["go"][110, 1, 3] = math.inf
+    elif what == "large gradient":
+        dirty["go"][100:170] = 6e4
+    elif what == "inf value":
+        dirty["v"][100, 1, 7] = -math.inf
+    else:
+        dirty["v"][90:290] = 6e4
+    got = call(dirty)
+    assert got["status"] == want["status"] == ops.VG_OK
+    k1 = 90 + lk[1]
+    for s in (slice(0, 100), slice(170, 215)):
+        for n in ("out", "grad_q"):
+            assert torch.equal(got[n][s], want[n][s]), n
+    for s in (slice(0, 90), slice(k1, k1 + 150)):
+        for n in ("grad_k", "grad_v"):
+            assert torch.equal(got[n][s], want[n][s]), n
+    compare(want, reference(clean), dtype)

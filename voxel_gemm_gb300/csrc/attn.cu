@@ -37,13 +37,6 @@ __device__ __forceinline__ int sample_of(const AttnArgs& a, const int32_t* off, 
     return lo;
 }
 
-// Whether key row j is one of its sample's valid rows.
-__device__ __forceinline__ bool valid_key(const AttnArgs& a, int64_t j) {
-    if (!a.k_len) return true;
-    const int b = sample_of(a, a.k_off, j);
-    return j - a.k_off[b] < a.k_len[b];
-}
-
 // Rows of the other axis that the results of query row (kKeys: key row) j are sums over: its sample's valid keys
 // (kKeys: its packed query rows).
 template <bool kKeys>
@@ -53,40 +46,100 @@ __device__ __forceinline__ int64_t summed_rows(const AttnArgs& a, int64_t j) {
     return a.k_len ? a.k_len[b] : a.k_off[b + 1] - a.k_off[b];
 }
 
-// Largest value of the block into *word, as the bits of a non-negative float (their
-// order is the floats' own, so the result does not depend on the order of arrival).
-__device__ __forceinline__ void block_max(float x, uint32_t* word) {
-    __shared__ uint32_t s[kThreads / 32];
-    const uint32_t v = __reduce_max_sync(0xffffffffu, __float_as_uint(x));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        uint32_t m = 0;
-        for (int i = 0; i < kThreads / 32; ++i) m = max(m, s[i]);
-        atomicMax(word, m);
+// The largest norm of each sample's rows into dst[2 * sample], as the bits of an fp32 value (of values that are not
+// negative the bits have the same order, so the result does not depend on the order of arrival).  A group of lanes
+// gives its rows in rising order; rows that are not finite, or not valid, do not count.
+struct SampleMax {
+    uint32_t* dst;
+    const int32_t* off;
+    const int32_t* len;  // valid rows of each sample, or null
+    int b = 0;
+    int64_t end = 0, live = 0;  // of sample b: the row past its last one, past its last valid one
+    float big = 0.f;            // squared
+
+    __device__ __forceinline__ void add(const AttnArgs& a, int64_t i, bool writes, float sq) {
+        if (i >= end) {
+            if (writes) flush();
+            big = 0.f;
+            b = sample_of(a, off, i);
+            end = off[b + 1];
+            live = len ? off[b] + len[b] : end;
+        }
+        if (sq < INFINITY && i < live) big = fmaxf(big, sq);
     }
+    __device__ __forceinline__ void flush() const {
+        if (big > 0.f) atomicMax(dst + 2 * b, __float_as_uint(sqrtf(big)));
+    }
+    // By the whole block, at its end: one atomic for all of it if it saw one sample last.
+    __device__ __forceinline__ void finish(bool writes) const {
+        __shared__ uint32_t s_max[kThreads / 32];
+        __shared__ int s_b[kThreads / 32];
+        int same;
+        __match_all_sync(0xffffffffu, b, &same);
+        if (!same && writes) flush();
+        const uint32_t v = __reduce_max_sync(0xffffffffu, same ? __float_as_uint(sqrtf(big)) : 0u);
+        if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = v, s_b[threadIdx.x >> 5] = b;
+        __syncthreads();
+        if (threadIdx.x > 0) return;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            uint32_t m = s_max[i];
+            while (i + 1 < kThreads / 32 && s_b[i + 1] == s_b[i]) m = max(m, s_max[++i]);
+            if (m > 0) atomicMax(dst + 2 * s_b[i], m);
+        }
+    }
+};
+
+// fp16: the largest norm of each sample's valid rows of V, which with that of dO's rows bounds dP.  Rows [first, end)
+// of (key, head).
+template <typename T>
+__device__ __forceinline__ void value_bounds(const AttnArgs& a, int lanes, int64_t first, int64_t end) {
+    const int lane = threadIdx.x & (lanes - 1), groups = kThreads / lanes;
+    SampleMax most{a.bound + 1, a.k_off, a.k_len};
+    for (int64_t r0 = first; r0 < end; r0 += groups) {  // the same trips for the whole block
+        const int64_t r = r0 + threadIdx.x / lanes, j = r / a.hk;
+        float sq = 0.f;
+        if (r < end && lane * 8 < a.d) {
+            float v[8];
+            load8<T>(head_row<const T>(a.v, j, (int)(r - j * a.hk)) + lane * 8, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sq = fmaf(v[i], v[i], sq);
+        }
+        for (int o = 1; o < lanes; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        if (r < end) most.add(a, j, lane == 0, sq);
+    }
+    most.finish(lane == 0);
 }
+
+// Blocks of a kernel over rows, each of which takes `per` rows in a row.
+struct Rows {
+    int blocks = 0;
+    int64_t per = 0;
+};
 
 // stats[packed row] = -lse * log2 e (+ 15 in fp16: the weights' exponent), -sum_d dO O: a group
 // of 1..16 lanes per row, 16-byte loads; reads O and dO once, bound by memory.  fp16: also
-// the largest norms of a row of dO and of a valid row of V, which bound dP.
+// the largest norms of a sample's rows of dO and of its valid rows of V (the blocks behind the first).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int lanes) {
-    const int lane = threadIdx.x & (lanes - 1);
-    const int64_t rows = a.n_q * a.hq;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / lanes);
-    const int64_t first = (int64_t)blockIdx.x * (kThreads / lanes);
+__global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int lanes, Rows queries, Rows values) {
     constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
-    float big = 0.f;
+    if constexpr (kHalf) {
+        if ((int)blockIdx.x >= queries.blocks) {
+            const int64_t first = (int64_t)(blockIdx.x - queries.blocks) * values.per;
+            value_bounds<T>(a, lanes, first, min(first + values.per, a.n_k * a.hk));
+            return;
+        }
+    }
+    const int lane = threadIdx.x & (lanes - 1), groups = kThreads / lanes;
+    const int64_t rows = a.n_q * a.hq;
+    const int64_t first = (int64_t)blockIdx.x * queries.per, end = min(first + queries.per, rows);
+    SampleMax most{a.bound, a.q_off, nullptr};
     // row r = (i, h), carried along without a division
     int64_t r = first + threadIdx.x / lanes, i = r / a.hq;
     int h = (int)(r - i * a.hq);
-    const int64_t di = step / a.hq;
-    const int dh = (int)(step - di * a.hq);
-    for (int64_t r0 = first; r0 < rows; r0 += step, r += step) {  // the same trips for the whole block
+    const int di = groups / a.hq, dh = groups - di * a.hq;
+    for (int64_t r0 = first; r0 < end; r0 += groups, r += groups) {  // the same trips for the whole block
         float sum = 0.f, sq = 0.f;
-        if (r < rows && lane * 8 < a.d) {
+        if (r < end && lane * 8 < a.d) {
             float o[8], g[8];
             load8<T>(head_row<const T>(a.o, i, h) + lane * 8, o);
             load8<T>(head_row<const T>(a.go, i, h) + lane * 8, g);
@@ -96,9 +149,9 @@ __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int l
         for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if constexpr (kHalf) {
             for (int o = 1; o < lanes; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            big = fmaxf(big, sq);
+            if (r < end) most.add(a, i, lane == 0, sq);
         }
-        if (r < rows && lane == 0) {
+        if (r < end && lane == 0) {
             float* st = a.stats + (((int64_t)(h >> a.gp_log2) * a.n_q + i) << a.gp_log2) + (h & (a.gp - 1));
             st[0] = fmaf(a.lse[(int64_t)h * a.n_q + i], -1.4426950408889634f, kHalf ? kHalfLift : 0.f);
             st[rows] = -sum;
@@ -106,24 +159,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int l
         i += di;
         if ((h += dh) >= a.hq) h -= a.hq, ++i;
     }
-    if constexpr (kHalf) {
-        block_max(sqrtf(big), a.err + 1);
-        big = 0.f;
-        const int64_t krows = a.n_k * a.hk;
-        for (int64_t r0 = first; r0 < krows; r0 += step) {
-            const int64_t row = r0 + threadIdx.x / lanes, j = row / a.hk;
-            float sq = 0.f;
-            if (row < krows && lane * 8 < a.d && valid_key(a, j)) {
-                float v[8];
-                load8<T>(head_row<const T>(a.v, j, (int)(row - j * a.hk)) + lane * 8, v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sq = fmaf(v[i], v[i], sq);
-            }
-            for (int o = 1; o < lanes; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            big = fmaxf(big, sq);
-        }
-        block_max(sqrtf(big), a.err + 2);
-    }
+    if constexpr (kHalf) most.finish(lane == 0);
 }
 
 // Four consecutive elements, 8 or 16 bytes.
@@ -226,12 +262,20 @@ __global__ void __launch_bounds__(kThreads) k_attn_join_sum(const AttnArgs a, Jo
 
 int launched() { return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA; }
 
+// At most 16 blocks an SM, `step` rows or a multiple of them for each.
+Rows rows_of(int64_t rows, int step, int sms) {
+    if (rows == 0) return {};
+    const int64_t steps = (rows + step - 1) / step, most = std::min<int64_t>(steps, (int64_t)sms * 16);
+    const int64_t per = (steps + most - 1) / most * step;
+    return {(int)((rows + per - 1) / per), per};
+}
 template <typename T>
-int stats(const AttnArgs& a, cudaStream_t s) {
+int stats(const AttnArgs& a, int sms, cudaStream_t s) {
     int lanes = 1;
     while (lanes * 8 < a.d) lanes <<= 1;
-    const int64_t blocks = (a.n_q * a.hq + kThreads / lanes - 1) / (kThreads / lanes);
-    k_attn_stats<T><<<(unsigned)std::min<int64_t>(blocks, 152 * 16), kThreads, 0, s>>>(a, lanes);
+    const Rows queries = rows_of(a.n_q * a.hq, kThreads / lanes, sms);
+    const Rows values = std::is_same<T, __half>::value ? rows_of(a.n_k * a.hk, kThreads / lanes, sms) : Rows{};
+    k_attn_stats<T><<<queries.blocks + values.blocks, kThreads, 0, s>>>(a, lanes, queries, values);
     return launched();
 }
 template <typename T>
@@ -343,6 +387,8 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
     }
     if (c.backward) {
         size_t o = align_up(vq * sizeof(float2), 256);
+        p.off_bound = 256 + o;
+        if (c.dtype == VG_F16) o += align_up((size_t)c.batch * 8, 256);
         p.off_dq = 256 + o;
         if (p.s_dq > 1) o += align_up(p.s_dq * vq * c.d * 4, 256);
         p.off_dk = 256 + o;
@@ -377,9 +423,10 @@ int attn_bwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s)
     a.err = reinterpret_cast<uint32_t*>(ws);
     a.stats = reinterpret_cast<float*>(ws + 256);
     int st;
-    if (dtype == VG_F16) cudaMemsetAsync(a.err + 1, 0, 8, s);  // the largest norms, taken by the statistics kernel
+    a.bound = reinterpret_cast<uint32_t*>(ws + p.off_bound);
+    if (dtype == VG_F16 && cudaMemsetAsync(a.bound, 0, (size_t)a.batch * 8, s) != cudaSuccess) return VG_ERR_CUDA;
     if (a.n_q > 0) {
-        if ((st = VG_BY_TYPE(stats, a, s)) != VG_OK) return st;
+        if ((st = VG_BY_TYPE(stats, a, p.sms, s)) != VG_OK) return st;
         a.splits = p.s_dq;
         a.per_part = p.per_dq;
         a.tile = p.tc ? 128 : 64;

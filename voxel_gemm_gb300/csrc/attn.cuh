@@ -28,7 +28,8 @@ struct AttnArgs {
     vg_heads q, k, v, o, go, gq, gk, gv;
     float* lse;                  // [hq][n_q]
     // workspace
-    uint32_t* err;               // error record; words 1, 2: fp32 bits of the largest |dO row|, |V row| (fp16)
+    uint32_t* err;               // error record
+    uint32_t* bound;             // fp16: fp32 bits of each sample's largest |dO row| and |V row|
     float* stats;                // [2][hq / gp][n_q * gp], negated: lse * log2 e and sum_d dO O of every packed row
     // The axis that a kernel runs along is cut into parts of `per_part` tiles of `tile` rows, so that a sample has
     // attn_parts of them; splits bounds that number (1: not cut, results go to their place at once).
@@ -148,7 +149,7 @@ struct AttnPlan {
     // most parts of the key axis (forward, dQ) and of the query axis (dK, dV), and the tiles of a part
     int s_fwd = 1, s_dq = 1, s_dkv = 1;
     int per_fwd = 0, per_dq = 0, per_dkv = 0;
-    size_t off_lse = 0, off_dq = 0, off_dk = 0, off_dv = 0, total = 0;
+    size_t off_lse = 0, off_bound = 0, off_dq = 0, off_dk = 0, off_dv = 0, total = 0;
 };
 int attn_plan(const AttnShape& c, AttnPlan* P);
 int attn_fwd(AttnArgs a, const AttnPlan& p, int dtype, char* ws, cudaStream_t s);

@@ -262,7 +262,7 @@ struct Unit {
     int lo, hi;        // tiles of the axis that the unit runs along
     int q0, lq;        // the sample's queries
     int k0, lk;        // its keys: first row, valid rows
-    int unused0, unused1;
+    uint32_t max_go, max_v;  // fp16 backward: bits of the sample's largest |dO row|, |V row|
 };
 constexpr int kUnitSlots = 4;
 

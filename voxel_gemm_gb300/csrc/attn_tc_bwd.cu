@@ -34,8 +34,9 @@
 // P and dS at d = 64 too, 1540 and later 1196 us; 128-wide steps with 16 warps, 1117 us.
 //
 // fp16 has no exponent range to spare: P carries 2^15 (P <= 1), and dP - delta is divided by
-// a power of two above 2 max|dO row| max|V row|, which bounds it; both leave with the
-// fp32 result.  bf16 needs neither.
+// a power of two above 2 max|dO row| max|V row| of its sample, which bounds it; both leave with
+// the fp32 result.  A sample's bound is its own, so that nothing in one sample, however large,
+// takes range from another's.  bf16 needs neither.
 #include "attn_tc.cuh"
 
 namespace vg {
@@ -49,14 +50,19 @@ constexpr int kN = 128;  // columns of dQ's steps
 constexpr int kH = 32;   // columns of its softmax threads
 constexpr int kThreads = 512 + 128;
 
-// The power of two that dP - delta is multiplied by, and its inverse.
+// The power of two that a sample's dP - delta is multiplied by, and its inverse.
 template <bool BF16>
-__device__ __forceinline__ float2 grad_lift(const AttnArgs& a) {
+__device__ __forceinline__ float2 grad_lift(const Unit& x) {
     if constexpr (BF16) return make_float2(1.f, 1.f);
-    const float bound = 2.f * __uint_as_float(a.err[1]) * __uint_as_float(a.err[2]);
+    const float bound = 2.f * __uint_as_float(x.max_go) * __uint_as_float(x.max_v);
     const int e = (int)(__float_as_uint(bound) >> 23) - 127;
     if (!(bound > 0.f) || e > 120 || e < -120) return make_float2(1.f, 1.f);
     return make_float2(__uint_as_float((uint32_t)(126 - e) << 23), __uint_as_float((uint32_t)(128 + e) << 23));
+}
+// The norms that it comes from, of sample b.
+template <bool BF16>
+__device__ __forceinline__ void put_bounds(const AttnArgs& a, int b, Unit& x) {
+    if constexpr (!BF16) x.max_go = a.bound[2 * b], x.max_v = a.bound[2 * b + 1];
 }
 
 template <bool BF16> constexpr float kDrop = BF16 ? 1.f : 1.f / (1 << (int)kHalfLift);  // what P carries, taken out
@@ -151,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x = Unit{t.first, min(kM, t.lq * a.gp - t.first), (int)(u % sets), t.part, 0, 0,
                      t.q0, t.lq, t.k0, t.lk, 0, 0};
             attn_split(a, t.lk, t.part, &x.lo, &x.hi);
+            put_bounds<BF16>(a, t.b, x);
             ring.put(wait, x);
         }
         x.rows = -1;
@@ -257,13 +264,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t t_s = t_lane + quarter * kH, t_p = t_lane + C::kPCol + quarter * (kH / 2);
         const float c = a.scale_log2;
-        const float2 lift = grad_lift<BF16>(a);
         const bool v8ok = lines_ok(a.gq);
         const int row = quad * 32 + lane;  // within the unit
         uint32_t n = 0, uc = 0, sums = 0;  // tiles, units and exchanges done
         while (ring.get(wait, x)) {
             const bool any = x.rows > quad * 32, mine = row < x.rows;  // the warp, the thread has a row
             const int pr = x.first + row;                              // packed row of the sample
+            const float2 lift = grad_lift<BF16>(x);
             float2 st = make_float2(0.f, 0.f);
             if (mine) st = attn_stats(a, ((int64_t)x.head * a.n_q + x.q0) * a.gp + pr);
             const float base = st.x, delta = st.y * lift.x;
@@ -488,6 +495,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
             if (t.b < 0) break;
             x = Unit{t.first, min(kM, t.krows - t.first), (int)(u % a.hk), t.part, 0, 0, t.q0, t.lq, t.k0, t.lk, 0, 0};
             if (t.first < t.lk) attn_split(a, (int64_t)t.lq * a.gp, t.part, &x.lo, &x.hi);
+            put_bounds<BF16>(a, t.b, x);
             ring.put(wait, x);
         }
         x.rows = -1;
@@ -633,13 +641,13 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t t_s = t_lane + w * 2 * kNK;
         const float c = a.scale_log2;
-        const float2 lift = grad_lift<BF16>(a);
-        const float2 c2 = make_float2(c, c), lift2 = make_float2(lift.x, lift.x);
+        const float2 c2 = make_float2(c, c);
         const bool v8ok = lines_ok(w == 0 ? a.gv : a.gk);
         const uint32_t t_p = C::kOwn ? t_lane + C::kPCol + w * kNK : t_s, t_d = C::kOwn ? t_p + kNK / 2 : t_s + kNK;
         uint32_t it = 0, sc = 0, uc = 0;
         while (ring.get(wait, x)) {
             const int rows = x.lq * a.gp, per = x.hi - x.lo, steps = per * sets;
+            const float2 lift = grad_lift<BF16>(x), lift2 = make_float2(lift.x, lift.x);
             // this group's steps of the unit: every second one
             int i = (int)((w ^ it) & 1u), e = x.lo + (per == 1 ? 0 : i);
             for (; i < steps; i += 2) {
