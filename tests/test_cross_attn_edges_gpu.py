@@ -107,3 +107,22 @@ def test_a_sample_does_not_set_another_ones_scale(dtype, what):
         for n in ("grad_k", "grad_v"):
             assert torch.equal(got[n][s], want[n][s]), n
     compare(want, reference(clean), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("keys", [100, 4096])
+def test_a_large_row_leaves_the_others_their_precision(dtype, keys):
+    """A query whose incoming gradient is 3e6 times its neighbours': their gradients hold the bound among
+    themselves.  (K is large, q small: results are far inside fp16's normal range and the weights are even.)"""
+    x = make([130], [keys], 2, 1, 64, dtype, seed=53, q_scale=0.02, g_scale=1e-2)
+    x["k"].mul_(16)
+    x["go"][77] = 3e4
+    r, ref = call(x), reference(x)
+    assert r["status"] == ops.VG_OK
+    others = torch.arange(130, device="cuda") != 77
+    assert ref["grad_q"][others].abs().median() > 2.0 ** -11
+    y = {n: (x[n][others].contiguous() if n in ("q", "go") else x[n]) for n in x}
+    y.update(lq=[129], q_off=base.offsets([129]))
+    slack = reference(y)["slack_q"] ** 0.5
+    assert rel(r["grad_q"][others], ref["grad_q"][others], slack) <= base.GRAD_TOL[dtype]
+    compare(r, ref, dtype, ("out", "lse", "grad_k", "grad_v"))

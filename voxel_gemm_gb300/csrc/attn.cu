@@ -117,8 +117,8 @@ struct Rows {
 };
 
 // stats[packed row] = -lse * log2 e (+ 15 in fp16: the weights' exponent), -sum_d dO O: a group
-// of 1..16 lanes per row, 16-byte loads; reads O and dO once, bound by memory.  fp16: also
-// the largest norms of a sample's rows of dO and of its valid rows of V (the blocks behind the first).
+// of 1..16 lanes per row, 16-byte loads; reads O and dO once, bound by memory.  fp16: also |dO row|,
+// and the largest norms of a sample's rows of dO and of its valid rows of V (the blocks behind the first).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int lanes, Rows queries, Rows values) {
     constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_stats(const AttnArgs a, int l
             float* st = a.stats + (((int64_t)(h >> a.gp_log2) * a.n_q + i) << a.gp_log2) + (h & (a.gp - 1));
             st[0] = fmaf(a.lse[(int64_t)h * a.n_q + i], -1.4426950408889634f, kHalf ? kHalfLift : 0.f);
             st[rows] = -sum;
+            if (kHalf) st[2 * rows] = sqrtf(sq);
         }
         i += di;
         if ((h += dh) >= a.hq) h -= a.hq, ++i;
@@ -386,7 +387,7 @@ int attn_plan(const AttnShape& c, AttnPlan* P) {
         fwd += align_up(p.s_fwd * vq * 4, 256);
     }
     if (c.backward) {
-        size_t o = align_up(vq * sizeof(float2), 256);
+        size_t o = align_up(vq * sizeof(float) * (c.dtype == VG_F16 ? 3 : 2), 256);
         p.off_bound = 256 + o;
         if (c.dtype == VG_F16) o += align_up((size_t)c.batch * 8, 256);
         p.off_dq = 256 + o;

@@ -30,7 +30,8 @@ struct AttnArgs {
     // workspace
     uint32_t* err;               // error record
     uint32_t* bound;             // fp16: fp32 bits of each sample's largest |dO row| and |V row|
-    float* stats;                // [2][hq / gp][n_q * gp], negated: lse * log2 e and sum_d dO O of every packed row
+    // [2][hq / gp][n_q * gp], negated: lse * log2 e and sum_d dO O of every packed row; fp16: a third, |dO row|
+    float* stats;
     // The axis that a kernel runs along is cut into parts of `per_part` tiles of `tile` rows, so that a sample has
     // attn_parts of them; splits bounds that number (1: not cut, results go to their place at once).
     int splits, per_part, tile;

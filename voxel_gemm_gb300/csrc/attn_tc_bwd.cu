@@ -34,9 +34,10 @@
 // P and dS at d = 64 too, 1540 and later 1196 us; 128-wide steps with 16 warps, 1117 us.
 //
 // fp16 has no exponent range to spare: P carries 2^15 (P <= 1), and dP - delta is divided by
-// a power of two above 2 max|dO row| max|V row| of its sample, which bounds it; both leave with
-// the fp32 result.  A sample's bound is its own, so that nothing in one sample, however large,
-// takes range from another's.  bf16 needs neither.
+// a power of two above 2 |dO row| max|V row|, which bounds it; both leave with the fp32 result.
+// V's rows are the sample's; dO's is the row itself in dQ, the sample's largest in dK, whose sums run
+// over rows.  So nothing in one sample, however large, takes range from another's, nor one
+// row from another one's dQ.  bf16 needs neither.
 #include "attn_tc.cuh"
 
 namespace vg {
@@ -50,16 +51,17 @@ constexpr int kN = 128;  // columns of dQ's steps
 constexpr int kH = 32;   // columns of its softmax threads
 constexpr int kThreads = 512 + 128;
 
-// The power of two that a sample's dP - delta is multiplied by, and its inverse.
+// The power of two that dP - delta is multiplied by where |dO row| <= go, and its inverse.
 template <bool BF16>
-__device__ __forceinline__ float2 grad_lift(const Unit& x) {
+__device__ __forceinline__ float2 grad_lift(const Unit& x, float go) {
     if constexpr (BF16) return make_float2(1.f, 1.f);
-    const float bound = 2.f * __uint_as_float(x.max_go) * __uint_as_float(x.max_v);
+    const float bound = 2.f * go * __uint_as_float(x.max_v);
     const int e = (int)(__float_as_uint(bound) >> 23) - 127;
     if (!(bound > 0.f) || e > 120 || e < -120) return make_float2(1.f, 1.f);
     return make_float2(__uint_as_float((uint32_t)(126 - e) << 23), __uint_as_float((uint32_t)(128 + e) << 23));
 }
-// The norms that it comes from, of sample b.
+
+// The norms that the bounds come from, of sample b.
 template <bool BF16>
 __device__ __forceinline__ void put_bounds(const AttnArgs& a, int b, Unit& x) {
     if constexpr (!BF16) x.max_go = a.bound[2 * b], x.max_v = a.bound[2 * b + 1];
@@ -270,9 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ring.get(wait, x)) {
             const bool any = x.rows > quad * 32, mine = row < x.rows;  // the warp, the thread has a row
             const int pr = x.first + row;                              // packed row of the sample
-            const float2 lift = grad_lift<BF16>(x);
-            float2 st = make_float2(0.f, 0.f);
-            if (mine) st = attn_stats(a, ((int64_t)x.head * a.n_q + x.q0) * a.gp + pr);
+            const int64_t at = ((int64_t)x.head * a.n_q + x.q0) * a.gp + pr;
+            const float2 st = mine ? attn_stats(a, at) : make_float2(0.f, 0.f);
+            const float2 lift = grad_lift<BF16>(x, !BF16 && mine ? a.stats[2 * a.n_q * a.hq + at] : 0.f);
             const float base = st.x, delta = st.y * lift.x;
             const float2 c2 = make_float2(c, c), base2 = make_float2(base, base);
             const float2 lift2 = make_float2(lift.x, lift.x), delta2 = make_float2(delta, delta);
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(summed + 8 * quad, sums++ & 1u)) break;
                 sum = -kDrop<BF16> * (slot[0] + slot[kM] + (slot[2 * kM] + slot[3 * kM]));
                 if (mine && quarter == 0)
-                    a.stats[a.n_q * a.hq + ((int64_t)x.head * a.n_q + x.q0) * a.gp + pr] = sum;
+                    a.stats[a.n_q * a.hq + at] = sum;
                 if (n > 0 && !wait(p_empty, (n - 1) & 1u)) break;
                 tc_fence_after();
                 uint32_t d[kH / 2];
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         uint32_t it = 0, sc = 0, uc = 0;
         while (ring.get(wait, x)) {
             const int rows = x.lq * a.gp, per = x.hi - x.lo, steps = per * sets;
-            const float2 lift = grad_lift<BF16>(x), lift2 = make_float2(lift.x, lift.x);
+            const float2 lift = grad_lift<BF16>(x, __uint_as_float(x.max_go)), lift2 = make_float2(lift.x, lift.x);
             // this group's steps of the unit: every second one
             int i = (int)((w ^ it) & 1u), e = x.lo + (per == 1 ? 0 : i);
             for (; i < steps; i += 2) {
