@@ -386,7 +386,22 @@ class SparseMap:
 _Int3 = ctypes.c_int * 3
 
 
-def _heads(t, dtype, shape, what):
+def _on(device, what, *tensors):
+    """Refuse tensors that are not on the GPU of index `device`: kernels take raw addresses and would follow them."""
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{what}: every tensor must be on the GPU, and on one GPU; got one on {t.device}")
+
+
+def _gpu(t, what):
+    """Index of t's GPU."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{what}: every tensor must be on the GPU; got one on {t.device}")
+    return device
+
+
+def _heads(t, dtype, shape, device, what):
     """vg_heads of a [rows, heads, head_dim] tensor (any row and head strides), None for None."""
     if t is None:
         return None
@@ -394,6 +409,8 @@ def _heads(t, dtype, shape, what):
     if t.dtype != dtype or t.shape != shape or (s[2] != 1 and t.numel() > 0):
         raise ValueError(f"{what}: expected {dtype} {list(shape)} with contiguous elements, got {t.dtype} "
                          f"{list(t.shape)} of strides {s}")
+    if t.get_device() != device:
+        _on(device, what, t)
     return HeadsStruct(t.data_ptr(), s[0], s[1])
 
 
@@ -405,12 +422,13 @@ def rope_freqs(head_dim: int, axes: int = 3, theta: float = 10000.0, device="cud
 
 
 def _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags):
-    """(N, heads_q, heads_k, head_dim, dtype, pairs) of a call, checked."""
+    """(N, heads_q, heads_k, head_dim, dtype, pairs, device) of a call, checked."""
     x = q if q is not None else k
     if x is None or x.dim() != 3:
         raise ValueError("q and k are [rows, heads, head_dim]; one of them may be None")
     n, d = x.shape[0], x.shape[2]
     hq, hk = (0 if t is None else t.shape[1] for t in (q, k))
+    device = _gpu(x, "q and k")
     if (coords is None) != (freqs is None):
         raise ValueError("coords and freqs come together")
     pairs = None
@@ -419,13 +437,15 @@ def _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags):
             raise ValueError("coords must be contiguous int32 [rows, 4]")
         if freqs.dtype != torch.float32 or not freqs.is_contiguous() or freqs.numel() != sum(axis_pairs):
             raise ValueError("freqs must be contiguous float32 of sum(axis_pairs) elements")
+        _on(device, "coords and freqs", coords, freqs)
         pairs = _Int3(*axis_pairs)
     for w, h, name in ((q_weight, hq, "q_weight"), (k_weight, hk, "k_weight")):
         if w is not None:
             want = (d,) if flags & VG_QK_SHARED_WEIGHT else (h, d)
             if w.dtype != x.dtype or w.shape != want or not w.is_contiguous():
                 raise ValueError(f"{name} must be contiguous {x.dtype} {list(want)}")
-    return n, hq, hk, d, x.dtype, pairs
+            _on(device, name, w)
+    return n, hq, hk, d, x.dtype, pairs, device
 
 
 def _rope_flags(q_weight, k_weight, flags):
@@ -440,11 +460,12 @@ def vg_qk_norm_rope_fwd(q, k, q_weight, k_weight, coords, freqs, axis_pairs, q_o
     """Norm of each head's queries and keys ([rows, heads, head_dim]; either may be None) and their rotation by
     coords [rows, 4]; weights [heads, head_dim], or [head_dim] for all heads, or None for ones."""
     flags = _rope_flags(q_weight, k_weight, flags)
-    n, hq, hk, d, dt, pairs = _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags)
-    _check(lib().vg_qk_norm_rope_fwd(n, hq, hk, d, _DT.get(dt, -1), _heads(q, dt, (n, hq, d), "q"),
-                                     _heads(k, dt, (n, hk, d), "k"), _p(q_weight), _p(k_weight), _p(coords), _p(freqs),
-                                     pairs, eps, flags, _heads(q_out, dt, (n, hq, d), "q_out"),
-                                     _heads(k_out, dt, (n, hk, d), "k_out"), _s(stream)), "vg_qk_norm_rope_fwd")
+    n, hq, hk, d, dt, pairs, dev = _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags)
+    sq, sk = (n, hq, d), (n, hk, d)
+    _check(lib().vg_qk_norm_rope_fwd(n, hq, hk, d, _DT.get(dt, -1), _heads(q, dt, sq, dev, "q"),
+                                     _heads(k, dt, sk, dev, "k"), _p(q_weight), _p(k_weight), _p(coords), _p(freqs),
+                                     pairs, eps, flags, _heads(q_out, dt, sq, dev, "q_out"),
+                                     _heads(k_out, dt, sk, dev, "k_out"), _s(stream)), "vg_qk_norm_rope_fwd")
 
 
 def vg_qk_norm_rope_bwd(q, k, q_weight, k_weight, coords, freqs, axis_pairs, grad_q_out, grad_k_out, grad_q, grad_k,
@@ -452,13 +473,15 @@ def vg_qk_norm_rope_bwd(q, k, q_weight, k_weight, coords, freqs, axis_pairs, gra
     """Gradients of vg_qk_norm_rope_fwd's inputs and weights (weight gradients None: not wanted; ws then None too)."""
     flags = _rope_flags(q_weight if q_weight is not None else grad_q_weight,
                         k_weight if k_weight is not None else grad_k_weight, flags)
-    n, hq, hk, d, dt, pairs = _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags)
+    n, hq, hk, d, dt, pairs, dev = _rope_shapes(q, k, coords, freqs, axis_pairs, q_weight, k_weight, flags)
     _rope_shapes(q, k, coords, freqs, axis_pairs, grad_q_weight, grad_k_weight, flags)
-    _check(lib().vg_qk_norm_rope_bwd(n, hq, hk, d, _DT.get(dt, -1), _heads(q, dt, (n, hq, d), "q"),
-                                     _heads(k, dt, (n, hk, d), "k"), _p(q_weight), _p(k_weight), _p(coords), _p(freqs),
-                                     pairs, eps, flags, _heads(grad_q_out, dt, (n, hq, d), "grad_q_out"),
-                                     _heads(grad_k_out, dt, (n, hk, d), "grad_k_out"),
-                                     _heads(grad_q, dt, (n, hq, d), "grad_q"), _heads(grad_k, dt, (n, hk, d), "grad_k"),
+    _on(dev, "ws", ws)
+    sq, sk = (n, hq, d), (n, hk, d)
+    _check(lib().vg_qk_norm_rope_bwd(n, hq, hk, d, _DT.get(dt, -1), _heads(q, dt, sq, dev, "q"),
+                                     _heads(k, dt, sk, dev, "k"), _p(q_weight), _p(k_weight), _p(coords), _p(freqs),
+                                     pairs, eps, flags, _heads(grad_q_out, dt, sq, dev, "grad_q_out"),
+                                     _heads(grad_k_out, dt, sk, dev, "grad_k_out"),
+                                     _heads(grad_q, dt, sq, dev, "grad_q"), _heads(grad_k, dt, sk, dev, "grad_k"),
                                      _p(grad_q_weight), _p(grad_k_weight), _p(ws),
                                      0 if ws is None else ws.numel() * ws.element_size(), _s(stream)),
            "vg_qk_norm_rope_bwd")
@@ -483,21 +506,25 @@ def cross_attn_workspace(n_q, n_k, batch, heads_q, heads_k, head_dim, dtype, bac
     return ws
 
 
-def _attn(q, k, q_offsets, k_offsets, k_lens, lse, scale, what):
+def _attn(q, k, q_offsets, k_offsets, k_lens, lse, ws, scale, what):
+    """The call's vg_attn and its GPU's index, checked."""
     qs, ks = q.shape, k.shape
     if len(qs) != 3 or len(ks) != 3 or qs[2] != ks[2]:
         raise ValueError(f"{what}: q and k are [rows, heads, head_dim] of one head_dim")
     n_q, hq, d = qs
+    device = _gpu(q, what)
     batch = q_offsets.numel() - 1
     for t, n, name in ((q_offsets, batch + 1, "q_offsets"), (k_offsets, batch + 1, "k_offsets"),
                        (k_lens, batch, "k_lens")):
-        if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or not t.is_cuda):
-            raise ValueError(f"{what}: {name} must be contiguous int32 [{n}] on the GPU")
+        if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or
+                              t.get_device() != device):
+            raise ValueError(f"{what}: {name} must be contiguous int32 [{n}] on q's GPU")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (hq, n_q) or not lse.is_contiguous()):
         raise ValueError(f"{what}: lse must be contiguous float32 [heads_q, n_q]")
+    _on(device, what, lse, ws)
     return AttnStruct(n_q, ks[0], batch, hq, ks[1], d, _DT.get(q.dtype, -1),
                       d ** -0.5 if scale is None else scale, q_offsets.data_ptr(), k_offsets.data_ptr(),
-                      None if k_lens is None else k_lens.data_ptr())
+                      None if k_lens is None else k_lens.data_ptr()), device
 
 
 def vg_cross_attn_fwd(q, k, v, q_offsets, k_offsets, k_lens, out, lse, ws, scale=None, stream=None) -> None:
@@ -505,23 +532,23 @@ def vg_cross_attn_fwd(q, k, v, q_offsets, k_offsets, k_lens, out, lse, ws, scale
 
     q, out [n_q, heads_q, head_dim]; k, v [n_k, heads_k, head_dim] (any row and head strides); offsets int32
     [batch + 1]; lse float32 [heads_q, n_q] or None; scale head_dim ** -0.5 by default."""
-    a = _attn(q, k, q_offsets, k_offsets, k_lens, lse, scale, "vg_cross_attn_fwd")
+    a, dev = _attn(q, k, q_offsets, k_offsets, k_lens, lse, ws, scale, "vg_cross_attn_fwd")
     sq, sk = (a.n_q, a.heads_q, a.head_dim), (a.n_k, a.heads_k, a.head_dim)
-    _check(lib().vg_cross_attn_fwd(a, _heads(q, q.dtype, sq, "q"), _heads(k, q.dtype, sk, "k"),
-                                   _heads(v, q.dtype, sk, "v"), _heads(out, q.dtype, sq, "out"), _p(lse), _p(ws),
-                                   ws.numel() * ws.element_size(), _s(stream)), "vg_cross_attn_fwd")
+    _check(lib().vg_cross_attn_fwd(a, _heads(q, q.dtype, sq, dev, "q"), _heads(k, q.dtype, sk, dev, "k"),
+                                   _heads(v, q.dtype, sk, dev, "v"), _heads(out, q.dtype, sq, dev, "out"), _p(lse),
+                                   _p(ws), ws.numel() * ws.element_size(), _s(stream)), "vg_cross_attn_fwd")
 
 
 def vg_cross_attn_bwd(q, k, v, q_offsets, k_offsets, k_lens, out, lse, grad_out, grad_q, grad_k, grad_v, ws,
                       scale=None, stream=None) -> None:
     """Gradients of vg_cross_attn_fwd's q, k and v, from its out and lse."""
-    a = _attn(q, k, q_offsets, k_offsets, k_lens, lse, scale, "vg_cross_attn_bwd")
+    a, dev = _attn(q, k, q_offsets, k_offsets, k_lens, lse, ws, scale, "vg_cross_attn_bwd")
     dt, sq, sk = q.dtype, (a.n_q, a.heads_q, a.head_dim), (a.n_k, a.heads_k, a.head_dim)
-    _check(lib().vg_cross_attn_bwd(a, _heads(q, dt, sq, "q"), _heads(k, dt, sk, "k"), _heads(v, dt, sk, "v"),
-                                   _heads(out, dt, sq, "out"), _p(lse), _heads(grad_out, dt, sq, "grad_out"),
-                                   _heads(grad_q, dt, sq, "grad_q"), _heads(grad_k, dt, sk, "grad_k"),
-                                   _heads(grad_v, dt, sk, "grad_v"), _p(ws), ws.numel() * ws.element_size(),
-                                   _s(stream)), "vg_cross_attn_bwd")
+    _check(lib().vg_cross_attn_bwd(a, _heads(q, dt, sq, dev, "q"), _heads(k, dt, sk, dev, "k"),
+                                   _heads(v, dt, sk, dev, "v"), _heads(out, dt, sq, dev, "out"), _p(lse),
+                                   _heads(grad_out, dt, sq, dev, "grad_out"), _heads(grad_q, dt, sq, dev, "grad_q"),
+                                   _heads(grad_k, dt, sk, dev, "grad_k"), _heads(grad_v, dt, sk, dev, "grad_v"),
+                                   _p(ws), ws.numel() * ws.element_size(), _s(stream)), "vg_cross_attn_bwd")
 
 
 def vg_cross_attn_status(ws, stream=None) -> int:
@@ -595,4 +622,5 @@ def vg_adamw_decode(codes, scales, out, second: bool, stream=None) -> None:
             or out.numel() != n or scales.numel() < -(-n // VG_ADAMW_BLOCK) \
             or not (codes.is_contiguous() and scales.is_contiguous() and out.is_contiguous()):
         raise ValueError("vg_adamw_decode: codes uint8 [n], scales float32 [ceil(n / 256)], out float32 [n]")
+    _on(_gpu(codes, "vg_adamw_decode"), "vg_adamw_decode", scales, out)
     _check(lib().vg_adamw_decode(_p(codes), _p(scales), n, int(second), _p(out), _s(stream)), "vg_adamw_decode")
