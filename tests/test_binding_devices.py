@@ -75,3 +75,12 @@ def test_norm_and_rotation(shared):
 def test_decoded_moments():
     refused(lambda **t: ops.vg_adamw_decode(second=False, **t),
             dict(codes=torch.zeros(300, dtype=torch.uint8), scales=torch.zeros(2), out=torch.zeros(300)))
+
+
+def test_parameters_on_two_gpus():
+    """One state is one table and one launch: parameters of two GPUs cannot share it."""
+    a, b = torch.zeros(300), torch.zeros(5)
+    for kinds in ((OnGpu, OnGpu1), (OnGpu1, OnGpu)):
+        p = [gpu(t, kind) for t, kind in zip((a, b), kinds)]
+        with pytest.raises(ValueError, match="one GPU"):
+            ops.AdamWState(p, [gpu(t.clone(), kind) for t, kind in zip((a, b), kinds)])

@@ -573,7 +573,10 @@ class AdamWState:
         if bits not in (8, 32):
             raise VGError(VG_ERR_UNSUPPORTED, "AdamWState")
         self.bits, self.offsets, total = bits, [], 0
+        device = params[0].device if params else torch.device("cuda", torch.cuda.current_device())
         for p, g in zip(params, grads):
+            if p.device != device:
+                raise ValueError("AdamWState: params must be on one GPU (its step is one launch): one state for each")
             if p.dtype not in _DT or g.dtype != p.dtype or g.shape != p.shape or not p.is_contiguous() \
                     or not g.is_contiguous() or not p.is_cuda or g.device != p.device:
                 raise ValueError("AdamWState: params and grads must be contiguous CUDA tensors of one shape and dtype")
@@ -582,13 +585,12 @@ class AdamWState:
         for p, x in zip(params, masters or []):
             if x.dtype != torch.float32 or x.shape != p.shape or not x.is_contiguous() or x.device != p.device:
                 raise ValueError("AdamWState: masters must be contiguous float32 of their parameter's shape")
-        device = params[0].device if params else "cuda"
         code, blocks = torch.uint8 if bits == 8 else torch.float32, total // VG_ADAMW_BLOCK
 
         def arena(t, n, dtype):
             if t is None:
                 return torch.zeros(n, dtype=dtype, device=device)
-            if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or t.device != torch.device(device):
+            if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or t.device != device:
                 raise ValueError(f"AdamWState: an arena must be contiguous {dtype} of {n} elements")
             return t
         self.m, self.v = arena(m, total, code), arena(v, total, code)
