@@ -558,10 +558,12 @@ def vg_cross_attn_status(ws, stream=None) -> int:
 class AdamWState:
     """Moments of many parameters and the table that vg_adamw_step takes.
 
-    params and grads are lists of contiguous tensors of one dtype each (written and read at every step, so they
-    stay where they are); masters, a list of fp32 tensors or None; weight_decay, a number or a list.  The moments
-    lie in two arenas m and v, each tensor's at the next multiple of 256 elements (`offsets`), as fp32 or, with
-    bits = 8, as uint8 codes beside m_scale and v_scale.  Arenas that are not given start at zero."""
+    params and grads are lists of contiguous tensors of one dtype each, written and read at every step where they lay
+    when the state was made (it keeps that memory).  Where a parameter's own .grad was given, a step is refused once
+    it has another one (zero_grad(set_to_none=False) keeps it) or its tensors have moved.  masters is a list of fp32
+    tensors or None; weight_decay, a number or a list.  The moments lie in two arenas m and v, each tensor's at the
+    next multiple of 256 elements (`offsets`), as fp32 or, with bits = 8, as uint8 codes beside m_scale and v_scale.
+    Arenas that are not given start at zero."""
 
     def __init__(self, params, grads, masters=None, bits=32, weight_decay=0.0, m=None, v=None, m_scale=None,
                  v_scale=None):
@@ -596,7 +598,13 @@ class AdamWState:
         self.m, self.v = arena(m, total, code), arena(v, total, code)
         self.m_scale = arena(m_scale, blocks, torch.float32) if bits == 8 else None
         self.v_scale = arena(v_scale, blocks, torch.float32) if bits == 8 else None
-        self._keep = (list(params), list(grads), None if masters is None else list(masters))
+        self._keep = [t.detach() for t in (*params, *grads, *(masters or []))]  # the memory, whoever else lets go of it
+        # parameters that autograd fills: what may be replaced behind the table's back, and where it lay (75 ns a
+        # tensor to look at in each step; buffers of the caller's own cost nothing)
+        self._autograd = [(p, g) for p, g in zip(params, grads) if p.is_leaf and p.grad is g]
+        theirs = [t for p, g, x in zip(params, grads, masters or [None] * len(params)) if p.is_leaf and p.grad is g
+                  for t in (p, g, x) if t is not None]
+        self._moving, self._at = theirs, [t.data_ptr() for t in theirs]
         size = 1 if bits == 8 else 4
 
         def at(t, n):
@@ -610,9 +618,20 @@ class AdamWState:
                                               at(self.v_scale, s), p.numel(), decay[i], _DT[p.dtype])
 
 
+    def check_in_place(self) -> None:
+        """ValueError if autograd's parameters or gradients, or their masters, are not those of the table any more."""
+        for p, g in self._autograd:
+            if p.grad is not g:
+                raise ValueError("AdamWState: a parameter has another .grad than the state was made with; make a new "
+                                 "state, and keep the gradients (zero_grad(set_to_none=False))")
+        if self._at != [t.data_ptr() for t in self._moving]:
+            raise ValueError("AdamWState: a parameter, its gradient or master has moved; make a new state")
+
+
 def vg_adamw_step(state: AdamWState, step: int, lr: float, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=1.0,
                   stream=None) -> None:
     """One AdamW step (counted from 1) over all of the state's parameters, in place."""
+    state.check_in_place()
     _check(lib().vg_adamw_step(state.table, len(state.table), state.bits, step, lr, beta1, beta2, eps, grad_scale,
                                _s(stream)), "vg_adamw_step")
 
