@@ -13,6 +13,7 @@ Forward, backward and the AdamW step run on the library (the product of the cont
 from __future__ import annotations
 
 import argparse
+import math
 import os
 import sys
 
@@ -97,9 +98,12 @@ class VoxelBlock:
     def train_step(self, x, context, target, step, lr):
         """One step of the loss against target [N, channels] (step counts from 1); returns the loss, on the GPU."""
         diff = self.forward(x, context) - target.view(self.y.shape)
-        self.backward(x, context, diff / diff.numel() if diff.dtype == torch.float32 else diff)
-        # 16-bit gradients are kept at the scale of the outputs, inside the type's range; the step divides
-        ops.vg_adamw_step(self.opt, step, lr, grad_scale=1.0 if diff.dtype == torch.float32 else 1 / diff.numel())
+        # The loss's gradient is diff / diff.numel().  In 16 bits the backward pass carries diff / 2^k, with 4^k about
+        # the number of voxels, and the step divides by the rest: the weights' gradients, sums over the voxels, stay
+        # far below 65,504, and the values that they are sums of far above fp16's smallest.
+        scale = 1 / diff.numel() if diff.dtype == torch.float32 else 2.0 ** -round(math.log2(diff.shape[0]) / 2)
+        self.backward(x, context, diff * scale)
+        ops.vg_adamw_step(self.opt, step, lr, grad_scale=1 / (diff.numel() * scale))
         return diff.float().square().mean() / 2
 
     def check(self):
