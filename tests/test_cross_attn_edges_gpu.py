@@ -126,3 +126,124 @@ def test_a_large_row_leaves_the_others_their_precision(dtype, keys):
     slack = reference(y)["slack_q"] ** 0.5
     assert rel(r["grad_q"][others], ref["grad_q"][others], slack) <= base.GRAD_TOL[dtype]
     compare(r, ref, dtype, ("out", "lse", "grad_k", "grad_v"))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("g_scale", [1e-6, 1e-3, 1.0])
+@pytest.mark.parametrize("name", ["grad_q", "grad_k"])
+def test_small_gradients_over_many_keys(dtype, g_scale, name):
+    """Score gradients of 1e-8 to 1e-2 (4,096 keys of even weight) keep their precision.  V, and the other operand
+    of the product with them, are large, so that the result is a normal number of the type; q and K are balanced so
+    that scores stay small."""
+    x = make([40], [4096], 2, 1, 64, dtype, seed=59, g_scale=g_scale)
+    x["v"].mul_(1e3 if g_scale < 1e-4 else 1.0)
+    big, small = ("k", "q") if name == "grad_q" else ("q", "k")
+    x[big].mul_(2e3 if g_scale < 1.0 else 2.0)
+    x[small].mul_(1e-4 if g_scale < 1.0 else 0.1)
+    ref = reference(x)
+    assert ref["lse"].std() < 0.5                                # even weights
+    assert 2.0 ** -11 < ref[name].abs().median() and ref[name].abs().max() < 3e4
+    compare(call(x), ref, dtype, ("out", "lse", name))
+
+
+# ------------------------------------------------------------------ sizes at which the plan changes
+def plan(x):
+    """What the sizes reach: SMs, blocks of two row tiles of queries, key tiles x heads, and the parts of the query
+    axis in dK and dV, from the workspace (two fp32 gradients a part, beside the row statistics)."""
+    (nq, hq, d), (nk, hk, _), batch = x["q"].shape, x["k"].shape, len(x["lq"])
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    group = hq // hk
+    gp = group if group <= 16 and not group & (group - 1) else 1
+    nb = ops.cross_attn_workspace(nq, nk, batch, hq, hk, d, x["q"].dtype, backward=True).numel()
+    parts = max(1, (nb - 256 - 8 * nq * hq) // (2 * nk * hk * d * 4))
+    return sms, (nq * gp // 256) * (hq // gp), (nk // 128) * hk, parts
+
+
+ROUNDINGS = 1.1 * math.sqrt(2) * 0.736 / math.sqrt(3)
+LARGE = [
+    # queries, key rows, query heads, key heads, width, valid keys
+    ([9101, 128, 3000, 1], [700, 1, 937, 65], 16, 16, 64, None),         # 6 and 8 key tiles, with tails
+    ([6000, 4224, 2049], [900, 641, 768], 16, 8, 64, [900, 0, 651]),     # two heads a row; padded; one without keys
+    ([12345], [1000], 8, 4, 40, None),
+    ([3001, 4096], [700, 130], 8, 8, 128, None),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lq,lk,hq,hk,d,valid", LARGE)
+def test_two_row_tiles_and_many_units(dtype, lq, lk, hq, hk, d, valid):
+    """Calls whose forward blocks take two row tiles and whose blocks have several units each, so that every ring
+    wraps and every accumulator is used again.  Two independent roundings (of the weights or score gradients, and of
+    the result), of a relative root mean square of u 0.736 / sqrt(3) each; 10 % for the sample."""
+    if valid:
+        valid = [min(v, n) for v, n in zip(valid, lk)]
+    x = make(lq, lk, hq, hk, d, dtype, valid=valid, seed=61)
+    sms, row_units, key_units, _ = plan(x)
+    assert row_units > 2 * sms or d == 128 and row_units > sms
+    r, ref = call(x), reference(x)
+    compare(r, ref, dtype)
+    for n in ("out", "grad_q", "grad_k", "grad_v"):
+        slack = {"grad_q": ref["slack_q"], "grad_k": ref["slack_k"]}.get(n, 0.0) ** 0.5
+        assert rel(r[n], ref[n], slack) <= ROUNDINGS * base.U[dtype], n
+    again = call(x)
+    for n in base.NAMES:
+        assert torch.equal(r[n], again[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_growing_scores_in_two_row_tiles(dtype, d):
+    """Scores that grow along the keys, by more than exp can hold, while both row tiles of a block are at work, and
+    of which some row tiles have none."""
+    x = make([5000, 130], [900, 300], 8, 8, d, dtype, seed=67)
+    sms, row_units, _, _ = plan(x)
+    assert row_units >= sms
+    x["q"][:] = 0
+    x["q"][:, :, 0] = torch.linspace(0.5, 8, 5130, device="cuda")[:, None]
+    x["q"][2000:2100] = 0                       # rows whose maximum never moves, beside others'
+    x["k"][:900, :, 0] = torch.linspace(-40, 40, 900, device="cuda")[:, None]
+    x["scale"] = 1.0
+    compare(call(x), reference(x), dtype)
+
+
+@pytest.mark.parametrize("dtype,hq,hk", [("bf16", 16, 16), ("f16", 16, 16), ("bf16", 32, 16)])
+def test_key_gradients_cut_to_even_waves(dtype, hq, hk):
+    """So many steps that the query axis of dK and dV is cut although there are as many key tiles as SMs."""
+    lq = [20011, 15000] if hq == hk else [10011, 7500]
+    x = make(lq, [800, 571], hq, hk, 64, dtype, seed=71)
+    sms, _, key_units, parts = plan(x)
+    assert key_units >= sms and parts > 1
+    r, ref = call(x), reference(x)
+    compare(r, ref, dtype)
+    for n in ("out", "grad_q", "grad_k", "grad_v"):
+        slack = {"grad_q": ref["slack_q"], "grad_k": ref["slack_k"]}.get(n, 0.0) ** 0.5
+        assert rel(r[n], ref[n], slack) <= ROUNDINGS * base.U[dtype], n
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_thousands_of_samples(dtype):
+    """3,000 small samples, some without queries or without keys."""
+    lq, lk = [(5 * i) % 7 for i in range(3000)], [(11 * i + 3) % 23 for i in range(3000)]
+    x = make(lq, lk, 2, 1, 32, dtype, seed=73)
+    r = call(x)
+    # the samples side by side, padded: [sample, head, query, key]
+    nq, nk, b = sum(lq), sum(lk), len(lq)
+    rows = torch.full((b, max(lq)), nq, device="cuda")
+    keys = torch.full((b, max(lk)), nk, device="cuda")
+    for i in range(b):
+        rows[i, :lq[i]] = torch.arange(int(x["q_off"][i]), int(x["q_off"][i]) + lq[i], device="cuda")
+        keys[i, :lk[i]] = torch.arange(int(x["k_off"][i]), int(x["k_off"][i]) + lk[i], device="cuda")
+    leaf = {n: x[n].double().requires_grad_() for n in ("q", "k", "v")}
+    pad = lambda t: torch.cat([t, t.new_zeros(1, *t.shape[1:])])  # noqa: E731
+    q, k, v = pad(leaf["q"])[rows], pad(leaf["k"])[keys][:, :, 0], pad(leaf["v"])[keys][:, :, 0]
+    s = torch.einsum("bihd,bjd->bhij", q, k) * x["scale"]
+    s = s.masked_fill((keys == nk)[:, None, None, :], -1e30)
+    p = s.softmax(-1) * (keys < nk)[:, None, None, :]
+    o = torch.einsum("bhij,bjd->bihd", p, v)
+    out = torch.zeros(nq + 1, 2, 32, dtype=torch.float64, device="cuda").index_put((rows,), o)[:nq]
+    out.backward(x["go"].double())
+    assert r["status"] == ops.VG_OK
+    # a sample's one key has no score gradient at all, and what rounding leaves is of the size of the others' error
+    for n, want in (("out", out.detach()), ("grad_q", leaf["q"].grad), ("grad_k", leaf["k"].grad),
+                    ("grad_v", leaf["v"].grad)):
+        assert rel(r[n], want) <= (base.OUT_TOL if n == "out" else base.GRAD_TOL)[dtype], n
