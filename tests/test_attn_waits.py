@@ -67,6 +67,7 @@ template <int S> bool forward(int stop, int units, int tiles, bool cut) {
         m.copy(Q, 0);
         qs.issued();
         for (int e = 0; e < tiles; ++e, at = (at + 1) % S) {
+            if (ks.slot() != at || vs.slot() != at || ks.pass() != (ks.n / S) % 2) { printf("wrong slot\\n"); exit(1); }
             if (!m.wait()) break;
             m.copy(K, at);
             ks.issued();

@@ -196,10 +196,10 @@ struct Waiter {
 
 // Wait for the copies that can still be in flight, whatever became of the block; barriers 8 bytes apart from `bar`.
 template <int S>
-__device__ __forceinline__ void land(Waiter& wait, const Copies<S>& copies, uint32_t bar) {
-    copies.in_flight([&](uint32_t slot, uint32_t parity) {
-        if (!mbar_wait_timed(bar + 8 * slot, parity)) wait.ok = false;
-    });
+__device__ __forceinline__ bool land(const Copies<S>& copies, uint32_t bar) {
+    bool ok = true;
+    copies.in_flight([&](uint32_t slot, uint32_t parity) { ok &= mbar_wait_timed(bar + 8 * slot, parity); });
+    return ok;
 }
 
 template <int V> using Const = std::integral_constant<int, V>;

@@ -208,9 +208,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // every copy has landed before the block may exit
-        land(wait, qs, q_full);
-        land(wait, kvs, kv_full);
-        land(wait, tails, tail);
+        wait.ok &= land(qs, q_full);
+        wait.ok &= land(kvs, kv_full);
+        wait.ok &= land(tails, tail);
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer || warp == kIssuer2) {
         const int ksteps = (a.d + 15) / 16;
@@ -557,9 +557,9 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                 }
         }
         // every copy has landed before the block may exit
-        land(wait, keys, k_full);
-        land(wait, steps, r_full);
-        land(wait, tails, tail);
+        wait.ok &= land(keys, k_full);
+        wait.ok &= land(steps, r_full);
+        wait.ok &= land(tails, tail);
         cp_async_wait_all();  // the statistics of a step whose tiles never landed
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer || (C::kOwn && warp == kIssuer2)) {

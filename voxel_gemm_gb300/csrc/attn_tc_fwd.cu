@@ -143,7 +143,6 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
         x.rows = -1;
         ring.put(wait, x);
     } else if (warp == kLoader) {
-        RingPos<S> pos;
         Copies<1> qs, tails;  // V tiles that end the sample's keys land on the tail's barrier
         Copies<S> ks, vs;
         while (ring.get(wait, x)) {
@@ -160,19 +159,20 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
             });
             qs.issued();
             for (int e = x.lo; e < x.hi; ++e) {
-                const uint32_t k = sKV + 2 * pos.i * C::kTile, v = k + C::kTile;
-                wait(k_empty + 8 * pos.i, pos.phase ^ 1u);
+                const uint32_t at = ks.slot(), parity = ks.pass() ^ 1u;
+                const uint32_t k = sKV + 2 * at * C::kTile, v = k + C::kTile;
+                wait(k_empty + 8 * at, parity);
                 if (!wait.ok) break;
                 one_lane([&] {
-                    mbar_arrive_expect_tx(k_full + 8 * pos.i, C::kTile);
+                    mbar_arrive_expect_tx(k_full + 8 * at, C::kTile);
                     for (int b = 0; b < C::kBlocks; ++b)
-                        tma_load_3d(k + b * kN * 128, &maps.k, b * 64, kh, x.k0 + e * kN, k_full + 8 * pos.i);
+                        tma_load_3d(k + b * kN * 128, &maps.k, b * 64, kh, x.k0 + e * kN, k_full + 8 * at);
                 });
                 ks.issued();
-                wait(v_empty + 8 * pos.i, pos.phase ^ 1u);
+                wait(v_empty + 8 * at, parity);
                 if (!wait.ok) break;
                 const int left = min(kN, x.lk - e * kN), n16 = (left + 15) / 16 * 16;
-                const uint32_t bar = n16 != left ? tail : v_full + 8 * pos.i;
+                const uint32_t bar = n16 != left ? tail : v_full + 8 * at;
                 one_lane([&] {
                     mbar_arrive_expect_tx(bar, C::kTile);
                     for (int b = 0; b < C::kBlocks; ++b)
@@ -184,18 +184,17 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
                     zero_rows(v, left, n16, C::kBlocks, kN * 128);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(v_full + 8 * pos.i);
+                    if (lane == 0) mbar_arrive(v_full + 8 * at);
                     __syncwarp();
                 }
                 vs.issued();
-                pos.step();
             }
         }
         // every copy has landed before the block may exit
-        land(wait, qs, q_full);
-        land(wait, ks, k_full);
-        land(wait, vs, v_full);
-        land(wait, tails, tail);
+        wait.ok &= land(qs, q_full);
+        wait.ok &= land(ks, k_full);
+        wait.ok &= land(vs, v_full);
+        wait.ok &= land(tails, tail);
         if (!wait.ok && lane == 0) atomicOr(a.err, kErrTimeout);
     } else if (warp == kIssuer) {
         const int ksteps = (a.d + 15) / 16;          // K = 16 steps over the channels

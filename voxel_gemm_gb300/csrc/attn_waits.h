@@ -19,6 +19,9 @@ template <int S>
 struct Copies {
     uint32_t n = 0;
     VG_HOST_DEVICE void issued() { ++n; }
+    // Slot of the next copy, and the parity of the pass over the ring that it belongs to.
+    VG_HOST_DEVICE uint32_t slot() const { return n % S; }
+    VG_HOST_DEVICE uint32_t pass() const { return (n / S) & 1u; }
     // f(slot, parity of the phase that its last copy completes)
     template <typename F>
     VG_HOST_DEVICE void in_flight(F f) const {
