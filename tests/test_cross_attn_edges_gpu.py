@@ -247,3 +247,17 @@ def test_thousands_of_samples(dtype):
     for n, want in (("out", out.detach()), ("grad_q", leaf["q"].grad), ("grad_k", leaf["k"].grad),
                     ("grad_v", leaf["v"].grad)):
         assert rel(r[n], want) <= (base.OUT_TOL if n == "out" else base.GRAD_TOL)[dtype], n
+
+
+@pytest.mark.parametrize("dtype,size", [("bf16", 1e24), ("f32", 1e24), ("f16", 3e3)])
+@pytest.mark.parametrize("queries", [3, 5000])
+def test_large_values_under_growing_scores(dtype, size, queries):
+    """Scores that pass the first tile's by up to 40, and values as large as the type's range allows sums of: weights
+    are kept small enough for their products with them."""
+    x = make([queries], [900], 8, 8, 64, dtype, seed=79)
+    x["q"][:] = 0
+    x["q"][:, :, 0] = 1
+    x["k"][:, :, 0] = torch.linspace(0, 40, 900, device="cuda")[:, None]
+    x["scale"] = 1.0
+    x["v"].mul_(size)
+    compare(call(x, backward=False), reference(x), dtype, ("out", "lse"))

@@ -19,9 +19,9 @@
 //
 // The row maximum only keeps the weights in range, and O and l carry the same factor
 // whatever it is.  So it is taken from the first tile and kept: later tiles are weighed
-// with it right away, and only where a row's sum of weights over a tile leaves the range (2^64 in
-// bf16, 2^14 in fp16) are the maximum renewed, O (in TMEM) and l rescaled and the tile
-// weighed again.  P is rounded to the inputs' type for the second product (l sums
+// with it right away, and only where a row's sum of weights over a tile leaves the range (2^32 in
+// bf16, whose products with V, up to 2^90, then stay inside fp32's range; 2^14 in fp16) are the
+// maximum renewed, O (in TMEM) and l rescaled and the tile weighed again.  P is rounded to the inputs' type for the second product (l sums
 // the unrounded values); fp16 weights carry a factor 2^7 more, so that a weight down to
 // 2^-31 of the row's largest is not lost below fp16's range.
 //
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(Cfg<DP, NQ>::kThreads, Cfg<DP, NQ>::kPerSm)
         const uint32_t t_s = t_lane + w * kN, t_o = t_lane + C::kOCol + w * DP;
         const float c = a.scale_log2;
         constexpr float kLift = BF16 ? 0.f : 7.f;            // exponent added to the weights
-        constexpr float kMost = BF16 ? 0x1p64f : 0x1p14f;    // of a tile's sum before the maximum is replaced
+        constexpr float kMost = BF16 ? 0x1p32f : 0x1p14f;    // of a tile's sum before the maximum is replaced
         const bool v8ok = lines_ok(a.o);
         const int row = w * kM + quad * 32 + lane;           // within the unit
         uint32_t sc = 0, oc = 0;
