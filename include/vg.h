@@ -450,8 +450,10 @@ VG_API int vg_qk_norm_rope_bwd(int64_t N, int heads_q, int heads_k, int head_dim
  * sample without valid keys gives out = 0 and lse = -inf, and takes no part in any gradient.
  * heads_q is a multiple of heads_k: query head h reads key head h / (heads_q / heads_k), and
  * the gradient of a key head is the sum over its query heads.
- *   dtype VG_F16 / VG_BF16: tensor cores, fp32 softmax and sums, the scores' weights rounded
- *   to dtype before the second product.  VG_F32: fp32 multiply-adds throughout.
+ *   dtype VG_F16 / VG_BF16: tensor cores, fp32 softmax and sums, the scores' weights (and
+ *   their gradients) rounded to dtype before the second product.  In fp16 those gradients have a
+ *   scale of their own for each query in grad_q, and for each sample in grad_k.
+ *   VG_F32: fp32 multiply-adds throughout.
  *   head_dim is a multiple of 8, at most 128; scale > 0 and finite; lse is [heads_q][n_q].
  * With few query rows the keys are cut into parts that run side by side, with few keys the
  * queries (backward); parts are joined in a fixed order, so every result is the same from
@@ -485,10 +487,13 @@ VG_API int vg_cross_attn_status(void* ws, void* stream);
 
 /* --------------------------------------------------------------------------------------
  * AdamW step over many tensors at once.
- *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
- *   p = p (1 - lr weight_decay) - lr/(1 - beta1^step) m / (sqrt(v)/sqrt(1 - beta2^step) + eps)
- * p is master where given (param then gets p rounded to its dtype), else param.  Every
- * operation is one fp32 rounding, in the order written.
+ *   g = grad * grad_scale
+ *   m = m * beta1 + g * c1,  v = v * beta2 + (g * g) * c2
+ *   p = p * decay - (m / (sqrt(v) * root + eps)) * rate
+ * p is master where given (param, which is then not read, gets p rounded to its dtype), else
+ * param.  c1 = 1 - beta1, c2 = 1 - beta2, decay = 1 - lr weight_decay, root = 1 / sqrt(1 - beta2^step)
+ * and rate = lr / (1 - beta1^step) are computed in 64 bits and rounded once to fp32, as are
+ * beta1, beta2, eps and grad_scale; every operation above is one fp32 rounding, in the order written.
  * state_bits 32: m and v are fp32 [n].  state_bits 8: m and v are codes, uint8 [n], with
  * one fp32 scale for every VG_ADAMW_BLOCK elements in m_scale and v_scale [ceil(n/256)];
  * codes 0 with any scale are zero states.  Scales are powers of two.  A code c stands for

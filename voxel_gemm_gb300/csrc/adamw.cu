@@ -1,12 +1,13 @@
 // AdamW over many tensors in one launch, first and second moments in 32 or 8 bits.
 //
-//   g = grad * grad_scale;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
-//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//   g = grad * grad_scale;  m = m * b1 + g * (1 - b1);  v = v * b2 + (g * g) * (1 - b2)
+//   p = p * (1 - lr wd) - (m / (sqrt(v) * (1 / sqrt(1 - b2^t)) + eps)) * (lr / (1 - b1^t))
 //
-// Every product, sum, root and quotient is rounded once in fp32 (no contraction
-// into fused multiply-adds), so the results do not depend on how the compiler
-// schedules the kernel.  (So no f32x2 instructions either: their products and sums came
-// out fused.)
+// The factors that do not depend on the element are computed on the host in 64 bits and
+// rounded once.  Every product, sum, root and quotient of the kernel is rounded once in fp32,
+// in the order written (no contraction into fused multiply-adds), so the results do not
+// depend on how the compiler schedules it.  (So no f32x2 instructions either: their products
+// and sums came out fused.)
 //
 // 8-bit moments come in blocks of 256 elements that share one power-of-two scale,
 // so that scaling and unscaling are exact:
@@ -22,11 +23,11 @@
 // One pass: each 256-thread block takes a chunk of one tensor (found by bisection in
 // the launch's parameter table, no device-side table and no upload), 8 elements a
 // thread with 16-byte accesses; a warp holds exactly one 256-element block, so the
-// 8-bit scales are warp reductions.  bf16 weights with fp32 masters: 65.0 M with fp32
-// moments 262 us (30 bytes each, 7.4 TB/s, bound by memory); 32.5 M with 8-bit moments
-// 107 us (18 bytes each, 5.5 TB/s, bound by memory and by the rounded roots and
-// quotients about alike).  The conversion instructions for m's codes and a maximum
-// that looks for infinities only when it finds one brought the latter from 132 us.
+// 8-bit scales are warp reductions.  bf16 weights with fp32 masters (which are read in the
+// weights' place): 65.0 M with fp32 moments 262 us (28 bytes each, 6.9 TB/s, bound by
+// memory); 32.5 M with 8-bit moments 107 us (16 bytes each, 4.9 TB/s, bound by the rounded
+// roots and quotients more than by memory).  The conversion instructions for m's codes and a
+// maximum that looks for infinities only when it finds one brought the latter from 132 us.
 #include "common.cuh"
 #include "internal.h"
 

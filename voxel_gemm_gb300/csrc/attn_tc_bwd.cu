@@ -22,15 +22,17 @@
 // cores' rate only from N = 128 on: at N = 64 it takes 48 cycles instead of 32 to read its
 // operands.
 //
-// delta is the sum of dO O, with O as the caller has it, rounded to 16 bits.  Over many keys
-// that is exact enough (O is an average, small beside V), over few it is not: over five
-// keys it adds as much to dQ's error as the rounding of dS.  So a sample of at most one
-// tile of keys gets delta as the row's sum of P dP, which the dQ kernel has in registers
-// there; it hands it to the dK, dV kernel too.
+// delta is the sum of dO O, with O as the caller has it, rounded to 16 bits.  Where many keys
+// share the weight that is exact enough (O is an average, small beside V), over few it is not:
+// over five keys it adds as much to dQ's error as the rounding of dS.  So a sample of at most
+// one tile of keys gets delta as the row's sum of P dP, which the dQ kernel has in registers
+// there; it hands it to the dK, dV kernel too.  A row over more keys that gives nearly all of
+// its weight to a few has the larger error: half an ulp of |dO| |O| in delta, which P weighs.
+// (Its sum of P dP would take a second pass over the keys.)
 //
 // Bound by the exponentials' warps and the hand-overs to and from the issuers (the products
 // alone would take half the time).  100,003 queries over 2 x 1,370 keys, 16 heads of 64,
-// bf16: dQ 690 us (1.2 PFLOP/s), dK and dV 1090 us (1.0 PFLOP/s); the scores' columns for
+// bf16: dQ 692 us (1.2 PFLOP/s), dK and dV 1090 us (1.0 PFLOP/s); fp16: 758 and 1109; the scores' columns for
 // P and dS at d = 64 too, 1540 and later 1196 us; 128-wide steps with 16 warps, 1117 us.
 //
 // fp16 has no exponent range to spare: P carries 2^15 (P <= 1), and dP - delta is divided by

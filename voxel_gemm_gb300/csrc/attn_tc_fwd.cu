@@ -20,17 +20,18 @@
 // The row maximum only keeps the weights in range, and O and l carry the same factor
 // whatever it is.  So it is taken from the first tile and kept: later tiles are weighed
 // with it right away, and only where a row's sum of weights over a tile leaves the range (2^32 in
-// bf16, whose products with V, up to 2^90, then stay inside fp32's range; 2^14 in fp16) are the
-// maximum renewed, O (in TMEM) and l rescaled and the tile weighed again.  P is rounded to the inputs' type for the second product (l sums
-// the unrounded values); fp16 weights carry a factor 2^7 more, so that a weight down to
-// 2^-31 of the row's largest is not lost below fp16's range.
+// bf16, so that products with values of up to 2^90 stay inside fp32's range; 2^14 in fp16) are
+// the maximum renewed, O (in TMEM) and l rescaled and the tile weighed again.  P is rounded to
+// the inputs' type for the second product (l sums the unrounded values); fp16 weights carry a
+// factor 2^7 more, so that a weight down to 2^-31 of the row's largest is not lost below fp16's
+// range.
 //
 // Bound by the exponentials' warps, of which an SM holds eight: they take some 1,200 cycles
 // for a tile's weights and wait some 700 for the next scores, which lie in the same columns
 // and so come after the product with V (scores beside the weights' own columns took that
 // wait away and made the warps slower by as much: 622 us against 601 at the time; four threads
 // to a row in 16 warps, 1361; all of a row's weights stored at once in place of each half
-// when it is done, 571).  100,003 queries over 2 x 1,370 keys, 16 heads of 64, bf16: 571 us
+// when it is done, 571).  100,003 queries over 2 x 1,370 keys, 16 heads of 64, bf16: 573 us
 // (0.98 PFLOP/s); 25,179 over 4 x 1,024, 16 heads of 128, fp16: 118 us (1.2 PFLOP/s).
 // 2 queries over 2 x 159,528 keys: 97 us, 6.7 TB/s, the memory's rate.
 #include "attn_tc.cuh"
