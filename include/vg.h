@@ -529,6 +529,116 @@ VG_API int vg_adamw_step(const vg_adamw_tensor* tensors, int count, int state_bi
 VG_API int vg_adamw_decode(const uint8_t* codes, const float* scales, int64_t n, int second, float* out,
                            void* stream);
 
+/* ======================================================================================
+ * Recurrent-block operators
+ * The other block that networks put between the convolutions mixes the voxel tokens along a
+ * space-filling curve (the order of vg_encode_seq's codes): s + dropout(scan(project(norm(s)))),
+ * with the residual stream s.  The calls below are its norm, its recurrence and its dropout.
+ * ====================================================================================== */
+
+/* Rows of channels: element (row, c) lies at data + row * row_stride + c (stride in elements, a
+ * multiple of 16 bytes and at least the channel count; data 16-byte aligned).  Channel counts
+ * are multiples of 8.  An output may take the place of an input of its own type (the same data
+ * and stride); otherwise it overlaps no other operand. */
+typedef struct {
+    void* data;
+    int64_t row_stride;
+} vg_rows;
+
+/* --------------------------------------------------------------------------------------
+ * Layer norm of each row.
+ *   z = (x - mean) * rstd,  y = z * weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ * weight and bias are [C] of `dtype`, 16-byte aligned; NULL: ones, zeros.  stats [N][2] fp32 is
+ * (mean, rstd), 8-byte aligned; the forward's may be NULL.  C is a multiple of 8, at most 8192.
+ * Statistics and sums are fp32 (squares of the differences from the mean); outputs are rounded
+ * once.  Backward, with g = grad_y * weight:
+ *   grad_x = (g - mean(g) - z * mean(g z)) * rstd  (+ grad_skip, if that is not NULL: the
+ *            gradient that reaches x past the norm, as in a residual stream)
+ *   grad_weight = sum over rows of grad_y z,  grad_bias = sum of grad_y, in a fixed order.
+ * grad_weight and grad_bias may be NULL (not wanted); ws, 256-byte aligned, is needed unless both are.
+ * -------------------------------------------------------------------------------------- */
+VG_API int vg_layer_norm_fwd(int64_t N, int C, int dtype, const vg_rows* x, const void* weight, const void* bias,
+                             double eps, const vg_rows* y, float* stats, void* stream);
+/* Bytes of workspace of the backward pass (0 if the arguments are invalid). */
+VG_API size_t vg_layer_norm_workspace_bytes(int64_t N, int C);
+VG_API int vg_layer_norm_bwd(int64_t N, int C, int dtype, const vg_rows* x, const void* weight, const float* stats,
+                             const vg_rows* grad_y, const vg_rows* grad_skip, const vg_rows* grad_x,
+                             void* grad_weight, void* grad_bias, void* ws, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * Gated linear recurrence of each channel along each sequence.
+ *   a_t = sigmoid(gate_t),  h_t = a_t h_{t-1} + (1 - a_t) x_t,  out_t = h_t
+ * With VG_SCAN_FREE_INPUT, h_t = a_t h_{t-1} + x_t.  Sequence b visits the positions
+ * [offsets[b], offsets[b+1]) upwards, or downwards with VG_SCAN_REVERSE; position p is row
+ * order[p] of gate, x and out (order NULL: row p), where order is a permutation of the rows
+ * (for instance the order of their codes along a curve).  h_{-1} is first[b] (NULL: zeros);
+ * last[b] (NULL: not wanted) receives the state after the last token, first[b] itself where
+ * there are no tokens.  first and last are fp32 [batch][C], 16-byte aligned, and do not overlap.
+ * States and sums are fp32; outputs are rounded once.  A token that is not finite makes its
+ * channel's states up to the end of its sequence infinite or NaN, and touches nothing else.
+ * The positions are cut into tiles that run side by side and hand on their states; they are
+ * joined in a fixed order, so every result is the same from run to run.
+ * Backward: lam_t = grad_out_t + a_{t+1} lam_{t+1}, with grad_last[b] in place of the last term at
+ * the last token;
+ *   grad_x = (1 - a) lam (VG_SCAN_FREE_INPUT: lam),  grad_first = a_0 lam_0,
+ *   grad_gate = a (1 - a) (h_{t-1} - x) lam (VG_SCAN_FREE_INPUT: a (1 - a) h_{t-1} lam).
+ * -------------------------------------------------------------------------------------- */
+#define VG_SCAN_REVERSE    0x1000u
+#define VG_SCAN_FREE_INPUT 0x2000u
+
+typedef struct {
+    int64_t n;                   /* rows: offsets[batch]                                       */
+    int channels, batch, dtype;
+    unsigned flags;
+    const int32_t* offsets;      /* [batch + 1], device                                        */
+    const int32_t* order;        /* [n], device, or NULL                                       */
+} vg_scan;
+
+/* Bytes of workspace of vg_gated_scan_fwd and _bwd (0 if the arguments are invalid; the pointers
+ * are not looked at).  Calls that may overlap on the GPU need a workspace each. */
+VG_API size_t vg_gated_scan_workspace_bytes(const vg_scan* s);
+/* Rows of `carries` (fp32 [rows][C], 16-byte aligned), the states that the forward pass keeps for
+ * the backward pass: one for every 128 positions. */
+VG_API int64_t vg_gated_scan_carry_rows(int64_t n);
+/* ws: 256-byte aligned; its first 4 bytes, the error record, are zero before the first call.
+ * carries may be NULL (no backward pass will follow).  Asynchronous.  Offsets that are no partition of the
+ * positions are found on the device: nothing is written and vg_gated_scan_status says so.  An
+ * entry of order that is no row is reported the same way: nothing is read or written for its
+ * token, and its sequence's results are undefined. */
+VG_API int vg_gated_scan_fwd(const vg_scan* s, const vg_rows* gate, const vg_rows* x, const float* first,
+                             const vg_rows* out, float* last, float* carries, void* ws, size_t ws_bytes,
+                             void* stream);
+/* carries is the forward's; grad_last and grad_first [batch][C] fp32 may be NULL. */
+VG_API int vg_gated_scan_bwd(const vg_scan* s, const vg_rows* gate, const vg_rows* x, const float* first,
+                             const float* carries, const vg_rows* grad_out, const float* grad_last,
+                             const vg_rows* grad_gate, const vg_rows* grad_x, float* grad_first, void* ws,
+                             size_t ws_bytes, void* stream);
+/* One token of each of n sequences: state [n][C] (fp32, 16-byte aligned) is h_{t-1} before and h_t
+ * after the call; flags: 0 or VG_SCAN_FREE_INPUT. */
+VG_API int vg_gated_scan_step(int64_t n, int C, int dtype, unsigned flags, const vg_rows* gate, const vg_rows* x,
+                              float* state, const vg_rows* out, void* stream);
+/* Synchronises `stream`; VG_ERR_INVALID_ARG if a call on ws found bad offsets or a bad order,
+ * VG_ERR_DEVICE_TIMEOUT if a bounded device-side wait gave up, else VG_OK.  Clears the record. */
+VG_API int vg_gated_scan_status(void* ws, void* stream);
+
+/* --------------------------------------------------------------------------------------
+ * Dropout into the residual stream; the mask is computed where it is needed and never stored.
+ *   out[i] = residual[i] + (keep_i ? x[i] / (1 - p) : 0);  backward: grad_x[i] = keep_i ? grad_out[i] / (1 - p) : 0
+ *   (residual's gradient is grad_out itself)
+ * keep_i is w_i >= round(p 2^32), where w_i is word i mod 4 of Philox 4x32 with ten rounds (J. K.
+ * Salmon, M. A. Moraes, R. O. Dror, D. E. Shaw, "Parallel random numbers: as easy as 1, 2, 3",
+ * SC 2011) at key (low, high word of rng[0]) and counter (low, high word of i / 4, low word of
+ * rng[1], call).  rng is on the DEVICE: rng[0] is the seed, rng[1] the step, which a captured
+ * graph can count up itself; `call` tells apart the calls of one step.  The mask depends on
+ * nothing else, so the backward pass takes the same three.  0 <= p <= 1 - 2^-32.  x, residual
+ * (or NULL) and out are n contiguous elements; out may be x or residual itself.  Pointers aligned
+ * to 16 bytes take the wide path, others are served element by element.
+ * -------------------------------------------------------------------------------------- */
+VG_API int vg_dropout_add_fwd(int64_t n, int dtype, const void* x, const void* residual, double p,
+                              const uint64_t* rng, uint32_t call, void* out, void* stream);
+VG_API int vg_dropout_add_bwd(int64_t n, int dtype, const void* grad_out, double p, const uint64_t* rng,
+                              uint32_t call, void* grad_x, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,4 +1,4 @@
-// extern "C" entry points of the attention-block operators declared in
+// extern "C" entry points of the attention- and recurrent-block operators declared in
 // include/vg.h: argument checks and workspace layout.  No memory is allocated here.
 #include <cmath>
 
@@ -53,6 +53,65 @@ int check_rope(int64_t N, int hq, int hk, int d, int dtype, const vg_heads* q, c
     if (bwd && !norm) return VG_OK;  // the rotation's gradient does not read its input
     int st = check_heads(q, N, hq, d, dtype, false);
     return st != VG_OK ? st : check_heads(k, N, hk, d, dtype, false);
+}
+
+// A [rows][c] operand of 16-byte vectors.
+int check_rows(const vg_rows* r, int64_t rows, int c, int dtype) {
+    if (!r) return rows == 0 ? VG_OK : VG_ERR_INVALID_ARG;
+    const vg_heads h{r->data, r->row_stride, 0};
+    return check_heads(&h, rows, 1, c, dtype, false);
+}
+
+// Row and channel counts and the type of a call on rows.
+int check_channels(int64_t N, int c, int dtype) {
+    if (N < 0 || N >= (int64_t(1) << 31) || c <= 0 || !known_dtype(dtype)) return VG_ERR_INVALID_ARG;
+    return c % 8 ? VG_ERR_UNSUPPORTED : VG_OK;
+}
+
+int check_norm(int64_t N, int c, int dtype, const void* weight, const void* bias, double eps) {
+    const int st = check_channels(N, c, dtype);
+    if (st != VG_OK) return st;
+    if (c > kMaxNormChannels) return VG_ERR_UNSUPPORTED;
+    if (!(eps >= 0.0 && eps < INFINITY) || misaligned(weight, 16) || misaligned(bias, 16)) return VG_ERR_INVALID_ARG;
+    return VG_OK;
+}
+
+int check_scan_shape(const vg_scan* s) {
+    if (!s || s->batch <= 0) return VG_ERR_INVALID_ARG;
+    if (s->flags & ~(VG_SCAN_REVERSE | VG_SCAN_FREE_INPUT)) return VG_ERR_UNSUPPORTED;
+    const int st = check_channels(s->n, s->channels, s->dtype);
+    if (st != VG_OK) return st;
+    return s->channels > (1 << 16) ? VG_ERR_UNSUPPORTED : VG_OK;
+}
+
+bool overlap(const void* p, const void* q, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + bytes && b < a + bytes;
+}
+
+// The part of a gated scan's arguments that both passes have.  from / to: the fp32 states per
+// sequence that the pass takes and gives.
+int check_scan(const vg_scan* s, const vg_rows* gate, const vg_rows* x, const float* first, const float* carries,
+               const float* from, const float* to, const void* ws, size_t ws_bytes) {
+    int st = check_scan_shape(s);
+    if (st != VG_OK) return st;
+    if (!s->offsets || misaligned(s->offsets, 4) || misaligned(s->order, 4)) return VG_ERR_INVALID_ARG;
+    if (misaligned(first, 16) || misaligned(carries, 16) || misaligned(from, 16) || misaligned(to, 16))
+        return VG_ERR_INVALID_ARG;
+    const size_t states = (size_t)s->batch * s->channels * 4;
+    if (overlap(first, to, states) || overlap(from, to, states)) return VG_ERR_INVALID_ARG;
+    if ((st = check_rows(gate, s->n, s->channels, s->dtype)) != VG_OK) return st;
+    if ((st = check_rows(x, s->n, s->channels, s->dtype)) != VG_OK) return st;
+    if (!ws || misaligned(ws, 256)) return VG_ERR_INVALID_ARG;
+    return ws_bytes < gated_scan_workspace_bytes(s->n, s->channels) ? VG_ERR_WORKSPACE_TOO_SMALL : VG_OK;
+}
+
+int check_dropout(int64_t n, int dtype, const void* x, double p, const uint64_t* rng, const void* out) {
+    if (n < 0 || !known_dtype(dtype) || !(p >= 0.0 && p <= 1.0 - 0x1p-32)) return VG_ERR_INVALID_ARG;
+    if (n >= (int64_t(1) << 46)) return VG_ERR_UNSUPPORTED;
+    const size_t es = dtype == VG_F32 ? 4 : 2;
+    if (n > 0 && (!x || !out || !rng)) return VG_ERR_INVALID_ARG;
+    return misaligned(x, es) || misaligned(out, es) || misaligned(rng, 8) ? VG_ERR_INVALID_ARG : VG_OK;
 }
 
 QkRope rope_call(int64_t N, int hq, int hk, int d, int dtype, const vg_heads* q, const vg_heads* k, const void* qw,
@@ -118,6 +177,18 @@ AttnArgs attn_args(const vg_attn* c, const vg_heads* q, const vg_heads* k, const
     a.v = v ? *v : none;
     a.o = out ? *out : none;
     return a;
+}
+
+// Read and clear the error record at the head of a workspace.
+int record_status(void* ws, cudaStream_t s) {
+    if (!ws) return VG_ERR_INVALID_ARG;
+    uint32_t h = 0;
+    if (cudaMemcpyAsync(&h, ws, sizeof(h), cudaMemcpyDeviceToHost, s) != cudaSuccess) return VG_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return VG_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, sizeof(h), s) != cudaSuccess) return VG_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return VG_ERR_CUDA;
+    if (h & kErrRange) return VG_ERR_INVALID_ARG;
+    return (h & kErrTimeout) ? VG_ERR_DEVICE_TIMEOUT : VG_OK;
 }
 
 }  // namespace
@@ -228,17 +299,7 @@ int vg_cross_attn_bwd(const vg_attn* a, const vg_heads* q, const vg_heads* k, co
     return attn_bwd(args, p, dt, static_cast<char*>(ws), static_cast<cudaStream_t>(stream));
 }
 
-int vg_cross_attn_status(void* ws, void* stream) {
-    if (!ws) return VG_ERR_INVALID_ARG;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint32_t h = 0;
-    if (cudaMemcpyAsync(&h, ws, sizeof(h), cudaMemcpyDeviceToHost, s) != cudaSuccess) return VG_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return VG_ERR_CUDA;
-    if (cudaMemsetAsync(ws, 0, sizeof(h), s) != cudaSuccess) return VG_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return VG_ERR_CUDA;
-    if (h & kErrRange) return VG_ERR_INVALID_ARG;
-    return (h & kErrTimeout) ? VG_ERR_DEVICE_TIMEOUT : VG_OK;
-}
+int vg_cross_attn_status(void* ws, void* stream) { return record_status(ws, static_cast<cudaStream_t>(stream)); }
 
 int vg_adamw_step(const vg_adamw_tensor* tensors, int count, int state_bits, int64_t step, double lr, double beta1,
                   double beta2, double eps, double grad_scale, void* stream) {
@@ -272,6 +333,150 @@ int vg_adamw_decode(const uint8_t* codes, const float* scales, int64_t n, int se
     if (n > 0 && (!codes || !scales || !out || misaligned(scales, 4) || misaligned(out, 4))) return VG_ERR_INVALID_ARG;
     cudaGetLastError();
     return adamw_decode(codes, scales, n, second, out, static_cast<cudaStream_t>(stream));
+}
+
+int vg_layer_norm_fwd(int64_t N, int C, int dtype, const vg_rows* x, const void* weight, const void* bias, double eps,
+                      const vg_rows* y, float* stats, void* stream) {
+    int st = check_norm(N, C, dtype, weight, bias, eps);
+    if (st != VG_OK) return st;
+    if ((st = check_rows(x, N, C, dtype)) != VG_OK) return st;
+    if ((st = check_rows(y, N, C, dtype)) != VG_OK) return st;
+    if (misaligned(stats, 8)) return VG_ERR_INVALID_ARG;
+    if (N == 0) return VG_OK;
+    cudaGetLastError();
+    LayerNorm a{};
+    a.n = N;
+    a.c = C;
+    a.dtype = dtype;
+    a.x = x;
+    a.y = y;
+    a.weight = weight;
+    a.bias = bias;
+    a.eps = (float)eps;
+    a.stats = stats;
+    a.sms = plan_sms(0);
+    return layer_norm(a, false, static_cast<cudaStream_t>(stream));
+}
+
+size_t vg_layer_norm_workspace_bytes(int64_t N, int C) {
+    return check_norm(N, C, VG_F32, nullptr, nullptr, 0.0) == VG_OK ? layer_norm_workspace_bytes(N, C, plan_sms(0)) : 0;
+}
+
+int vg_layer_norm_bwd(int64_t N, int C, int dtype, const vg_rows* x, const void* weight, const float* stats,
+                      const vg_rows* grad_y, const vg_rows* grad_skip, const vg_rows* grad_x, void* grad_weight,
+                      void* grad_bias, void* ws, size_t ws_bytes, void* stream) {
+    int st = check_norm(N, C, dtype, weight, nullptr, 0.0);
+    if (st != VG_OK) return st;
+    if ((st = check_rows(x, N, C, dtype)) != VG_OK) return st;
+    if ((st = check_rows(grad_y, N, C, dtype)) != VG_OK) return st;
+    if (grad_skip && (st = check_rows(grad_skip, N, C, dtype)) != VG_OK) return st;
+    if ((st = check_rows(grad_x, N, C, dtype)) != VG_OK) return st;
+    if ((N > 0 && !stats) || misaligned(stats, 8)) return VG_ERR_INVALID_ARG;
+    if (grad_weight || grad_bias) {
+        if (misaligned(grad_weight, 16) || misaligned(grad_bias, 16)) return VG_ERR_INVALID_ARG;
+        if (!ws || misaligned(ws, 256)) return VG_ERR_INVALID_ARG;
+        if (ws_bytes < layer_norm_workspace_bytes(N, C, plan_sms(0))) return VG_ERR_WORKSPACE_TOO_SMALL;
+    } else if (N == 0) {
+        return VG_OK;
+    }
+    cudaGetLastError();
+    LayerNorm a{};
+    a.n = N;
+    a.c = C;
+    a.dtype = dtype;
+    a.x = x;
+    a.y = grad_x;
+    a.grad_y = grad_y;
+    a.grad_skip = grad_skip;
+    a.weight = weight;
+    a.stats = const_cast<float*>(stats);
+    a.grad_weight = grad_weight;
+    a.grad_bias = grad_bias;
+    a.partial = static_cast<float*>(ws);
+    a.sms = plan_sms(0);
+    return layer_norm(a, true, static_cast<cudaStream_t>(stream));
+}
+
+size_t vg_gated_scan_workspace_bytes(const vg_scan* s) {
+    return check_scan_shape(s) == VG_OK ? gated_scan_workspace_bytes(s->n, s->channels) : 0;
+}
+
+int64_t vg_gated_scan_carry_rows(int64_t n) { return n > 0 ? (n + kScanCarryRows - 1) / kScanCarryRows : 0; }
+
+int vg_gated_scan_fwd(const vg_scan* s, const vg_rows* gate, const vg_rows* x, const float* first, const vg_rows* out,
+                      float* last, float* carries, void* ws, size_t ws_bytes, void* stream) {
+    int st = check_scan(s, gate, x, first, carries, first, last, ws, ws_bytes);
+    if (st != VG_OK) return st;
+    if ((st = check_rows(out, s->n, s->channels, s->dtype)) != VG_OK) return st;
+    cudaGetLastError();
+    GatedScan g{};
+    g.s = s;
+    g.gate = gate;
+    g.x = x;
+    g.first = first;
+    g.out = out;
+    g.last = last;
+    g.carries = carries;
+    g.ws = static_cast<char*>(ws);
+    g.sms = plan_sms(0);
+    return gated_scan(g, false, static_cast<cudaStream_t>(stream));
+}
+
+int vg_gated_scan_bwd(const vg_scan* s, const vg_rows* gate, const vg_rows* x, const float* first,
+                      const float* carries, const vg_rows* grad_out, const float* grad_last, const vg_rows* grad_gate,
+                      const vg_rows* grad_x, float* grad_first, void* ws, size_t ws_bytes, void* stream) {
+    int st = check_scan(s, gate, x, first, carries, grad_last, grad_first, ws, ws_bytes);
+    if (st != VG_OK) return st;
+    if (s->n > 0 && !carries) return VG_ERR_INVALID_ARG;
+    if ((st = check_rows(grad_out, s->n, s->channels, s->dtype)) != VG_OK) return st;
+    if ((st = check_rows(grad_gate, s->n, s->channels, s->dtype)) != VG_OK) return st;
+    if ((st = check_rows(grad_x, s->n, s->channels, s->dtype)) != VG_OK) return st;
+    cudaGetLastError();
+    GatedScan g{};
+    g.s = s;
+    g.gate = gate;
+    g.x = x;
+    g.first = first;
+    g.carries = const_cast<float*>(carries);
+    g.grad_out = grad_out;
+    g.grad_last = grad_last;
+    g.grad_gate = grad_gate;
+    g.out = grad_x;
+    g.grad_first = grad_first;
+    g.ws = static_cast<char*>(ws);
+    g.sms = plan_sms(0);
+    return gated_scan(g, true, static_cast<cudaStream_t>(stream));
+}
+
+int vg_gated_scan_step(int64_t n, int C, int dtype, unsigned flags, const vg_rows* gate, const vg_rows* x,
+                       float* state, const vg_rows* out, void* stream) {
+    int st = check_channels(n, C, dtype);
+    if (st != VG_OK) return st;
+    if (flags & ~VG_SCAN_FREE_INPUT) return VG_ERR_UNSUPPORTED;
+    if ((st = check_rows(gate, n, C, dtype)) != VG_OK) return st;
+    if ((st = check_rows(x, n, C, dtype)) != VG_OK) return st;
+    if ((st = check_rows(out, n, C, dtype)) != VG_OK) return st;
+    if ((n > 0 && !state) || misaligned(state, 16)) return VG_ERR_INVALID_ARG;
+    if (n == 0) return VG_OK;
+    cudaGetLastError();
+    return gated_scan_step(n, C, dtype, flags != 0, *gate, *x, state, *out, static_cast<cudaStream_t>(stream));
+}
+
+int vg_gated_scan_status(void* ws, void* stream) { return record_status(ws, static_cast<cudaStream_t>(stream)); }
+
+int vg_dropout_add_fwd(int64_t n, int dtype, const void* x, const void* residual, double p, const uint64_t* rng,
+                       uint32_t call, void* out, void* stream) {
+    const int st = check_dropout(n, dtype, x, p, rng, out);
+    if (st != VG_OK) return st;
+    if (misaligned(residual, dtype == VG_F32 ? 4 : 2)) return VG_ERR_INVALID_ARG;
+    if (n == 0) return VG_OK;
+    cudaGetLastError();
+    return dropout_add(n, dtype, x, residual, p, rng, call, out, plan_sms(0), static_cast<cudaStream_t>(stream));
+}
+
+int vg_dropout_add_bwd(int64_t n, int dtype, const void* grad_out, double p, const uint64_t* rng, uint32_t call,
+                       void* grad_x, void* stream) {
+    return vg_dropout_add_fwd(n, dtype, grad_out, nullptr, p, rng, call, grad_x, stream);
 }
 
 }  // extern "C"

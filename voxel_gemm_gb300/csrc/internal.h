@@ -181,4 +181,43 @@ int adamw_step(const vg_adamw_tensor* ts, int count, int bits, int64_t step, dou
                double eps, double grad_scale, cudaStream_t s);
 int adamw_decode(const uint8_t* codes, const float* scales, int64_t n, int second, float* out, cudaStream_t s);
 
+// Column sums, in a fixed order, of fp32 rows [rows][cols] into the first cols_a columns' output a and
+// the others' output b (of dtype; null: not wanted).
+int reduce_rows(const float* partial, int rows, int cols, int cols_a, int dtype, void* a, void* b, cudaStream_t s);
+
+// ---- recurrent-block operators ----
+// One layer norm call (pointers as in vg_layer_norm_fwd / _bwd).
+struct LayerNorm {
+    int64_t n;
+    int c, dtype;
+    const vg_rows *x, *y, *grad_y, *grad_skip;  // backward: y = grad_x
+    const void *weight, *bias;
+    float eps;
+    float* stats;
+    void *grad_weight, *grad_bias;
+    float* partial;  // layer_norm_workspace_bytes
+    int sms;
+};
+constexpr int kMaxNormChannels = 8192;
+size_t layer_norm_workspace_bytes(int64_t n, int c, int sms);
+int layer_norm(const LayerNorm& a, bool bwd, cudaStream_t s);
+
+// One gated scan call (pointers as in vg_gated_scan_fwd / _bwd; backward: out = grad_x).
+struct GatedScan {
+    const vg_scan* s;
+    const vg_rows *gate, *x, *out, *grad_out, *grad_gate;
+    const float *first, *grad_last;
+    float *last, *carries, *grad_first;
+    char* ws;
+    int sms;
+};
+constexpr int kScanCarryRows = 128;
+size_t gated_scan_workspace_bytes(int64_t n, int c);
+int gated_scan(const GatedScan& g, bool bwd, cudaStream_t s);
+int gated_scan_step(int64_t n, int c, int dtype, bool free_input, const vg_rows& gate, const vg_rows& x, float* state,
+                    const vg_rows& out, cudaStream_t s);
+
+int dropout_add(int64_t n, int dtype, const void* x, const void* residual, double p, const uint64_t* rng,
+                uint32_t call, void* out, int sms, cudaStream_t s);
+
 }  // namespace vg

@@ -308,10 +308,10 @@ __global__ void __launch_bounds__(kThreads, per_sm(BWD)) k_qk_norm_rope(const Ro
 }
 
 // Column sums of the blocks' weight-gradient rows, in a fixed order: kReduceRows running
-// sums, then those.  The first cols_q columns are the queries' weights.
+// sums, then those.  The first cols_a columns are the first output's.
 template <typename T>
-__global__ void __launch_bounds__(32 * kReduceRows) k_rope_weight_reduce(const float* __restrict__ partial, int rows,
-                                                                         int cols, int cols_q, T* gwq, T* gwk) {
+__global__ void __launch_bounds__(32 * kReduceRows) k_weight_reduce(const float* __restrict__ partial, int rows,
+                                                                    int cols, int cols_a, T* ga, T* gb) {
     __shared__ float s[kReduceRows][33];
     const int c = blockIdx.x * 32 + (threadIdx.x & 31);
     const int rl = threadIdx.x >> 5;
@@ -326,22 +326,13 @@ __global__ void __launch_bounds__(32 * kReduceRows) k_rope_weight_reduce(const f
         float tot = 0.f;
 #pragma unroll
         for (int i = 0; i < kReduceRows; ++i) tot += s[i][threadIdx.x & 31];
-        if (c < cols_q) {
-            if (gwq) gwq[c] = from_f32<T>(tot);
-        } else if (gwk) {
-            gwk[c - cols_q] = from_f32<T>(tot);
+        if (c < cols_a) {
+            if (ga) ga[c] = from_f32<T>(tot);
+        } else if (gb) {
+            gb[c - cols_a] = from_f32<T>(tot);
         }
     }
 }
-template <typename T>
-int reduce(const RopeArgs& a, int gx, int chunks, void* gwq, void* gwk, cudaStream_t s) {
-    const int rows = a.shared ? gx * chunks : gx;
-    const int cols_q = (a.shared ? 1 : a.hq) * a.d, cols = (a.shared ? 2 : a.ht) * a.d;
-    k_rope_weight_reduce<T><<<(cols + 31) / 32, 32 * kReduceRows, 0, s>>>(a.partial, rows, cols, cols_q,
-                                                                          static_cast<T*>(gwq), static_cast<T*>(gwk));
-    return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
-}
-
 // Lanes of a vector, heads of a block and tokens side by side: as many heads as
 // the block's lane groups hold, in equal chunks, then as many tokens as fit.
 void shape(int ht, int d, int* lanes, int* chunk, int* per) {
@@ -422,9 +413,23 @@ int qk_norm_rope(const QkRope& c, bool bwd, cudaStream_t s) {
              : c.dtype == VG_F16 ? launch<__half>(a, halves, bwd, gx, chunks, smem, s)
                                  : launch<__nv_bfloat16>(a, halves, bwd, gx, chunks, smem, s);
     if (st != VG_OK || !gw) return st;
-    return c.dtype == VG_F32   ? reduce<float>(a, gx, chunks, c.grad_q_weight, c.grad_k_weight, s)
-           : c.dtype == VG_F16 ? reduce<__half>(a, gx, chunks, c.grad_q_weight, c.grad_k_weight, s)
-                               : reduce<__nv_bfloat16>(a, gx, chunks, c.grad_q_weight, c.grad_k_weight, s);
+    return reduce_rows(a.partial, a.shared ? gx * chunks : gx, (a.shared ? 2 : a.ht) * a.d, (a.shared ? 1 : a.hq) * a.d,
+                       c.dtype, c.grad_q_weight, c.grad_k_weight, s);
+}
+
+int reduce_rows(const float* partial, int rows, int cols, int cols_a, int dtype, void* a, void* b, cudaStream_t s) {
+    const int grid = (cols + 31) / 32, threads = 32 * kReduceRows;
+    if (dtype == VG_F32)
+        k_weight_reduce<float><<<grid, threads, 0, s>>>(partial, rows, cols, cols_a, static_cast<float*>(a),
+                                                        static_cast<float*>(b));
+    else if (dtype == VG_F16)
+        k_weight_reduce<__half><<<grid, threads, 0, s>>>(partial, rows, cols, cols_a, static_cast<__half*>(a),
+                                                         static_cast<__half*>(b));
+    else
+        k_weight_reduce<__nv_bfloat16><<<grid, threads, 0, s>>>(partial, rows, cols, cols_a,
+                                                                static_cast<__nv_bfloat16*>(a),
+                                                                static_cast<__nv_bfloat16*>(b));
+    return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 
 }  // namespace vg

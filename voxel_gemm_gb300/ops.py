@@ -30,6 +30,7 @@ VG_NONE = 0xFFFFFFFF
 VG_TILE_ROWS = 128
 VG_ROPE_HALVES, VG_QK_NO_NORM, VG_QK_SHARED_WEIGHT = 0x200, 0x400, 0x800
 VG_ADAMW_BLOCK = 256
+VG_SCAN_REVERSE, VG_SCAN_FREE_INPUT = 0x1000, 0x2000
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvoxelgemm.so")
 _lock = threading.Lock()
@@ -68,6 +69,17 @@ class AdamWTensorStruct(ctypes.Structure):
                 ("dtype", ctypes.c_int)]
 
 
+class RowsStruct(ctypes.Structure):
+    """Mirror of vg_rows (include/vg.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64)]
+
+
+class ScanStruct(ctypes.Structure):
+    """Mirror of vg_scan (include/vg.h)."""
+    _fields_ = [("n", ctypes.c_int64), ("channels", ctypes.c_int), ("batch", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("flags", ctypes.c_uint), ("offsets", ctypes.c_void_p), ("order", ctypes.c_void_p)]
+
+
 class VGError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {vg_strerror(status)} (status {status})")
@@ -87,6 +99,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I, I64, U, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint, ctypes.c_size_t
         D, H = ctypes.c_double, ctypes.POINTER(HeadsStruct)
+        R, SC = ctypes.POINTER(RowsStruct), ctypes.POINTER(ScanStruct)
         sig = {
             "vg_strerror": ([I], ctypes.c_char_p),
             "vg_version": ([], I),
@@ -123,6 +136,17 @@ def lib():
             "vg_cross_attn_status": ([P, P], I),
             "vg_adamw_step": ([ctypes.POINTER(AdamWTensorStruct), I, I, I64, D, D, D, D, D, P], I),
             "vg_adamw_decode": ([P, P, I64, I, P, P], I),
+            "vg_layer_norm_fwd": ([I64, I, I, R, P, P, D, R, P, P], I),
+            "vg_layer_norm_workspace_bytes": ([I64, I], SZ),
+            "vg_layer_norm_bwd": ([I64, I, I, R, P, P, R, R, R, P, P, P, SZ, P], I),
+            "vg_gated_scan_workspace_bytes": ([SC], SZ),
+            "vg_gated_scan_carry_rows": ([I64], I64),
+            "vg_gated_scan_fwd": ([SC, R, R, P, R, P, P, P, SZ, P], I),
+            "vg_gated_scan_bwd": ([SC, R, R, P, P, R, P, R, R, P, P, SZ, P], I),
+            "vg_gated_scan_step": ([I64, I, I, U, R, R, P, R, P], I),
+            "vg_gated_scan_status": ([P, P], I),
+            "vg_dropout_add_fwd": ([I64, I, P, P, D, P, ctypes.c_uint32, P, P], I),
+            "vg_dropout_add_bwd": ([I64, I, P, D, P, ctypes.c_uint32, P, P], I),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -645,3 +669,156 @@ def vg_adamw_decode(codes, scales, out, second: bool, stream=None) -> None:
         raise ValueError("vg_adamw_decode: codes uint8 [n], scales float32 [ceil(n / 256)], out float32 [n]")
     _on(_gpu(codes, "vg_adamw_decode"), "vg_adamw_decode", scales, out)
     _check(lib().vg_adamw_decode(_p(codes), _p(scales), n, int(second), _p(out), _s(stream)), "vg_adamw_decode")
+
+
+# ---------------------------------------------------------------- recurrent-block operators
+def _rows(t, dtype, shape, device, what):
+    """vg_rows of a [rows, channels] tensor (any row stride), None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or (t.stride(1) != 1 and t.numel() > 0):
+        raise ValueError(f"{what}: expected {dtype} {list(shape)} with contiguous elements, got {t.dtype} "
+                         f"{list(t.shape)} of strides {t.stride()}")
+    if t.get_device() != device:
+        _on(device, what, t)
+    return RowsStruct(t.data_ptr(), t.stride(0))
+
+
+def _flat(t, dtype, shape, device, what):
+    """Address of a contiguous tensor, None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != device:
+        _on(device, what, t)
+    return t.data_ptr()
+
+
+def _matrix(x, what):
+    """Shape, dtype and GPU of a [rows, channels] tensor."""
+    if x.dim() != 2:
+        raise ValueError(f"{what}: expected [rows, channels], got {list(x.shape)}")
+    return x.shape, x.dtype, _gpu(x, what)
+
+
+def vg_layer_norm_fwd(x, weight, bias, y, stats, eps=1e-5, stream=None) -> None:
+    """y = (x - mean) rstd weight + bias of each row of x [rows, channels] (any row stride); weight and bias
+    [channels] or None; stats float32 [rows, 2] takes (mean, rstd) for the backward pass, or is None."""
+    (n, c), dt, dev = _matrix(x, "vg_layer_norm_fwd")
+    _check(lib().vg_layer_norm_fwd(n, c, _DT.get(dt, -1), _rows(x, dt, (n, c), dev, "x"),
+                                   _flat(weight, dt, (c,), dev, "weight"), _flat(bias, dt, (c,), dev, "bias"), eps,
+                                   _rows(y, dt, (n, c), dev, "y"), _flat(stats, torch.float32, (n, 2), dev, "stats"),
+                                   _s(stream)), "vg_layer_norm_fwd")
+
+
+def vg_layer_norm_bwd(x, weight, stats, grad_y, grad_skip, grad_x, grad_weight, grad_bias, ws, stream=None) -> None:
+    """Gradients of vg_layer_norm_fwd's x (plus grad_skip, unless None), weight and bias (None: not wanted; with both
+    None, ws may be None too)."""
+    (n, c), dt, dev = _matrix(x, "vg_layer_norm_bwd")
+    s = (n, c)
+    _on(dev, "vg_layer_norm_bwd", ws)
+    _check(lib().vg_layer_norm_bwd(n, c, _DT.get(dt, -1), _rows(x, dt, s, dev, "x"),
+                                   _flat(weight, dt, (c,), dev, "weight"),
+                                   _flat(stats, torch.float32, (n, 2), dev, "stats"),
+                                   _rows(grad_y, dt, s, dev, "grad_y"), _rows(grad_skip, dt, s, dev, "grad_skip"),
+                                   _rows(grad_x, dt, s, dev, "grad_x"),
+                                   _flat(grad_weight, dt, (c,), dev, "grad_weight"),
+                                   _flat(grad_bias, dt, (c,), dev, "grad_bias"), _p(ws),
+                                   0 if ws is None else ws.numel() * ws.element_size(), _s(stream)),
+           "vg_layer_norm_bwd")
+
+
+def layer_norm_workspace(n, channels, device="cuda") -> torch.Tensor:
+    nb = int(lib().vg_layer_norm_workspace_bytes(n, channels))
+    if nb == 0:
+        raise VGError(VG_ERR_INVALID_ARG, "vg_layer_norm_workspace_bytes")
+    return torch.empty(nb, dtype=torch.uint8, device=device)
+
+
+def gated_scan_workspace(n, channels, batch, dtype, device="cuda") -> torch.Tensor:
+    """Workspace of vg_gated_scan_fwd and _bwd, its error record zero."""
+    nb = int(lib().vg_gated_scan_workspace_bytes(ScanStruct(n, channels, batch, _DT.get(dtype, -1), 0, None, None)))
+    if nb == 0:
+        raise VGError(VG_ERR_INVALID_ARG, "vg_gated_scan_workspace_bytes")
+    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def gated_scan_carries(n, channels, device="cuda") -> torch.Tensor:
+    """The states that vg_gated_scan_fwd keeps for vg_gated_scan_bwd."""
+    return torch.empty(int(lib().vg_gated_scan_carry_rows(n)), channels, dtype=torch.float32, device=device)
+
+
+def _scan(gate, offsets, order, carries, ws, flags, what):
+    """(vg_scan, shape, batch, dtype, device, carries' address) of a call, checked."""
+    (n, c), dt, dev = _matrix(gate, what)
+    batch = offsets.numel() - 1
+    f32 = torch.float32
+    rows = -(-n // 128)
+    return (ScanStruct(n, c, batch, _DT.get(dt, -1), flags, _flat(offsets, torch.int32, (batch + 1,), dev, "offsets"),
+                       _flat(order, torch.int32, (n,), dev, "order")), (n, c), (batch, c), dt, dev,
+            _flat(carries, f32, (rows, c), dev, "carries"))
+
+
+def vg_gated_scan_fwd(gate, x, offsets, order, first, out, last, carries, ws, flags=0, stream=None) -> None:
+    """out_t = h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(gate), along each sequence.
+
+    gate, x, out [rows, channels] (any row stride); offsets int32 [batch + 1]; order int32 [rows], the row of each
+    position, or None; first, last float32 [batch, channels], the states before and after, or None; carries
+    (gated_scan_carries) for the backward pass, or None; flags VG_SCAN_REVERSE, VG_SCAN_FREE_INPUT."""
+    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, ws, flags, "vg_gated_scan_fwd")
+    _on(dev, "vg_gated_scan_fwd", ws)
+    _check(lib().vg_gated_scan_fwd(a, _rows(gate, dt, s, dev, "gate"), _rows(x, dt, s, dev, "x"),
+                                   _flat(first, torch.float32, b, dev, "first"), _rows(out, dt, s, dev, "out"),
+                                   _flat(last, torch.float32, b, dev, "last"), kept, _p(ws),
+                                   ws.numel() * ws.element_size(), _s(stream)), "vg_gated_scan_fwd")
+
+
+def vg_gated_scan_bwd(gate, x, offsets, order, first, carries, grad_out, grad_last, grad_gate, grad_x, grad_first, ws,
+                      flags=0, stream=None) -> None:
+    """Gradients of vg_gated_scan_fwd's gate, x and first (None: not wanted), from its carries; grad_last may be None."""
+    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, ws, flags, "vg_gated_scan_bwd")
+    _on(dev, "vg_gated_scan_bwd", ws)
+    _check(lib().vg_gated_scan_bwd(a, _rows(gate, dt, s, dev, "gate"), _rows(x, dt, s, dev, "x"),
+                                   _flat(first, torch.float32, b, dev, "first"), kept,
+                                   _rows(grad_out, dt, s, dev, "grad_out"),
+                                   _flat(grad_last, torch.float32, b, dev, "grad_last"),
+                                   _rows(grad_gate, dt, s, dev, "grad_gate"), _rows(grad_x, dt, s, dev, "grad_x"),
+                                   _flat(grad_first, torch.float32, b, dev, "grad_first"), _p(ws),
+                                   ws.numel() * ws.element_size(), _s(stream)), "vg_gated_scan_bwd")
+
+
+def vg_gated_scan_step(gate, x, state, out, flags=0, stream=None) -> None:
+    """One token of each of the rows' sequences: state float32 [rows, channels] goes from h_{t-1} to h_t, out = h_t."""
+    s, dt, dev = _matrix(gate, "vg_gated_scan_step")
+    _check(lib().vg_gated_scan_step(s[0], s[1], _DT.get(dt, -1), flags, _rows(gate, dt, s, dev, "gate"),
+                                    _rows(x, dt, s, dev, "x"), _flat(state, torch.float32, s, dev, "state"),
+                                    _rows(out, dt, s, dev, "out"), _s(stream)), "vg_gated_scan_step")
+
+
+def vg_gated_scan_status(ws, stream=None) -> int:
+    return lib().vg_gated_scan_status(_p(ws), _s(stream))
+
+
+def _dropout(name, x, residual, p, rng, call, out, stream):
+    dt, dev = x.dtype, _gpu(x, name)
+    if rng.dtype not in (torch.int64, torch.uint64):
+        raise ValueError(f"{name}: rng must be int64 [2] (seed, step)")
+    args = [x.numel(), _dtype_code(x), _flat(x, dt, x.shape, dev, "input")]
+    if name == "vg_dropout_add_fwd":
+        args.append(_flat(residual, dt, x.shape, dev, "residual"))
+    _check(getattr(lib(), name)(*args, p, _flat(rng, rng.dtype, (2,), dev, "rng"), call,
+                                _flat(out, dt, x.shape, dev, "output"), _s(stream)), name)
+
+
+def vg_dropout_add_fwd(x, residual, p, rng, call, out, stream=None) -> None:
+    """out = residual + dropout(x); residual may be None.  rng int64 [2] on the GPU: (seed, step); call, a number that
+    tells this call's mask from the others of the step."""
+    _dropout("vg_dropout_add_fwd", x, residual, p, rng, call, out, stream)
+
+
+def vg_dropout_add_bwd(grad_out, p, rng, call, grad_x, stream=None) -> None:
+    """grad_x = the gradient of vg_dropout_add_fwd's x, with the mask of the same p, rng and call."""
+    _dropout("vg_dropout_add_bwd", grad_out, None, p, rng, call, grad_x, stream)
