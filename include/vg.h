@@ -537,7 +537,7 @@ VG_API int vg_adamw_decode(const uint8_t* codes, const float* scales, int64_t n,
  * ====================================================================================== */
 
 /* Rows of channels: element (row, c) lies at data + row * row_stride + c (stride in elements, a
- * multiple of 16 bytes and at least the channel count; data 16-byte aligned).  Channel counts
+ * multiple of 16 bytes, at least the channel count and below 2^30; data 16-byte aligned).  Channel counts
  * are multiples of 8.  An output may take the place of an input of its own type (the same data
  * and stride); otherwise it overlaps no other operand. */
 typedef struct {

@@ -59,7 +59,9 @@ int check_rope(int64_t N, int hq, int hk, int d, int dtype, const vg_heads* q, c
 int check_rows(const vg_rows* r, int64_t rows, int c, int dtype) {
     if (!r) return rows == 0 ? VG_OK : VG_ERR_INVALID_ARG;
     const vg_heads h{r->data, r->row_stride, 0};
-    return check_heads(&h, rows, 1, c, dtype, false);
+    const int st = check_heads(&h, rows, 1, c, dtype, false);
+    // kernels may hold a row's bytes in 32 bits
+    return st == VG_OK && rows > 1 && r->row_stride >= (int64_t(1) << 30) ? VG_ERR_UNSUPPORTED : st;
 }
 
 // Row and channel counts and the type of a call on rows.
