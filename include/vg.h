@@ -576,8 +576,8 @@ VG_API int vg_layer_norm_bwd(int64_t N, int C, int dtype, const vg_rows* x, cons
  * there are no tokens.  first and last are fp32 [batch][C], 16-byte aligned, and do not overlap.
  * States and sums are fp32; outputs are rounded once.  A token that is not finite makes its
  * channel's states up to the end of its sequence infinite or NaN, and touches nothing else.
- * The positions are cut into tiles that run side by side and hand on their states; they are
- * joined in a fixed order, so every result is the same from run to run.
+ * The positions are cut into parts that run side by side; they are joined in a fixed order, so every
+ * result is the same from run to run.
  * Backward: lam_t = grad_out_t + a_{t+1} lam_{t+1}, with grad_last[b] in place of the last term at
  * the last token;
  *   grad_x = (1 - a) lam (VG_SCAN_FREE_INPUT: lam),  grad_first = a_0 lam_0,
@@ -598,7 +598,7 @@ typedef struct {
  * are not looked at).  Calls that may overlap on the GPU need a workspace each. */
 VG_API size_t vg_gated_scan_workspace_bytes(const vg_scan* s);
 /* Rows of `carries` (fp32 [rows][C], 16-byte aligned), the states that the forward pass keeps for
- * the backward pass: one for every 128 positions. */
+ * the backward pass: one for every 16 positions. */
 VG_API int64_t vg_gated_scan_carry_rows(int64_t n);
 /* ws: 256-byte aligned; its first 4 bytes, the error record, are zero before the first call.
  * carries may be NULL (no backward pass will follow).  Asynchronous.  Offsets that are no partition of the
@@ -617,8 +617,8 @@ VG_API int vg_gated_scan_bwd(const vg_scan* s, const vg_rows* gate, const vg_row
  * after the call; flags: 0 or VG_SCAN_FREE_INPUT. */
 VG_API int vg_gated_scan_step(int64_t n, int C, int dtype, unsigned flags, const vg_rows* gate, const vg_rows* x,
                               float* state, const vg_rows* out, void* stream);
-/* Synchronises `stream`; VG_ERR_INVALID_ARG if a call on ws found bad offsets or a bad order,
- * VG_ERR_DEVICE_TIMEOUT if a bounded device-side wait gave up, else VG_OK.  Clears the record. */
+/* Synchronises `stream`; VG_ERR_INVALID_ARG if a call on ws found bad offsets or a bad order, else
+ * VG_OK.  Clears the record. */
 VG_API int vg_gated_scan_status(void* ws, void* stream);
 
 /* --------------------------------------------------------------------------------------

@@ -103,7 +103,7 @@ def test_scan_operands(ops):
     for bwd in (False, True):
         assert scan_call(ops, big, bwd, nbytes=need - 1) == ops.VG_ERR_WORKSPACE_TOO_SMALL
     assert L.vg_gated_scan_workspace_bytes(None) == 0 and L.vg_gated_scan_status(None, None) == bad
-    assert [L.vg_gated_scan_carry_rows(n) for n in (-5, 0, 1, 128, 129, 1 << 30)] == [0, 0, 1, 1, 2, 1 << 23]
+    assert [L.vg_gated_scan_carry_rows(n) for n in (-5, 0, 1, 16, 17, 1 << 30)] == [0, 0, 1, 1, 2, 1 << 26]
 
 
 def test_step_refusals(ops):

@@ -4,26 +4,15 @@
 // backward: lam_t = dy_t + mu_{t+1}, mu_t = a_t lam_t;  db = lam, da = h_{t-1} lam (- x lam)
 //
 // A run of tokens maps the state that enters it to the one that leaves it, h -> A h + B, and two
-// runs after one another make (A2 A1, A2 B1 + B2): so the positions are cut into tiles that work
-// side by side.  A block takes a tile of 128 positions and 128 bytes of channels: a warp's lanes hold
-// a token's channels, 4 bytes each, and a warp goes along 16 tokens.  It finds the map of its
-// tokens; the block joins the warps' maps in shared memory, publishes the tile's map, collects
-// those of the tiles before it, and each warp goes through its tokens again from the state that
-// enters.  What a token's gate gives stays in registers between the two passes.
-// Bound by memory: gate and x are read once, out written once.  Each warp copies its own tokens of
-// the block's next tile into shared memory while it works on this one.
-//
-// The maps of earlier tiles are collected through a tree: node (l, i) is the map of the 8^l tiles
-// from i 8^l on; tile j reads, at each level, the siblings before its own ancestor, at most 7,
-// and the last tile below a node publishes that node.  So the shape of every sum depends on the
-// sizes alone (the same bits in every run), and a tile waits for about as many hand-overs as there
-// are levels.  A node's word holds A and B, 64 bits that are stored at once; words are all ones
-// before they are written (a NaN that no result has), so the data is its own flag.  Blocks
-// take their tiles in order from a counter, the next one when this one's tokens are there: the
-// first tile that is not done was taken by a block that works on it and has all that it waits for.
-// (Two tiles taken at once at the start left every second tile to a block still waiting for the
-// first, a chain through all blocks: 602k tokens of 512 channels took 4.5 ms.)  Waits are bounded by time; a block that
-// gives up records it and goes on with NaN.
+// runs after one another make (A2 A1, A2 B1 + B2).  So a pass has three steps: every warp finds the
+// map of its 64 tokens (a lane has 4 bytes of channels, two 16-bit ones), and the block those of
+// its 512; the blocks' maps are joined, in a fixed order, into the state that enters each block; every
+// warp goes through its tokens from the state that enters it.  Warps need nothing of one another
+// in between, so loads stream.  Gate and x are read twice, the second time from the end of the data back,
+// whose last 100 MB the L2 still holds.  (A single pass, in which blocks publish their maps
+// and wait for those of the blocks before, reads them once, but the waiting cost more: with a tree of maps, tiles
+// held in shared memory and a tile published ahead, 602k tokens of 512 channels took 950 us forward,
+// 600 with the waits left out, and 4.9 M of 64 channels 1790.)
 //
 // Where a sequence begins, the map is constant (A = -1 marks it, h -> B), so that nothing, not
 // even a NaN, passes from one sequence to the next.  A warp's tokens are the same for all of its
@@ -40,34 +29,28 @@ using namespace ptx;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTokens = 16;                  // of a warp
-constexpr int kTile = kWarps * kTokens;
-constexpr int kRowBytes = 128;               // of a token in a block: 64 16-bit or 32 fp32 channels
-constexpr int kTileBytes = kTile * kRowBytes;
-constexpr int kFan = 3;                      // log2 of a node's children
-constexpr int kSiblings = (1 << kFan) - 1;
-constexpr int kMaxLevels = 8;                // 128 * 8^8 positions are more than 2^31
-constexpr uint64_t kUnset = ~0ull;
-constexpr uint64_t kGiveUpNs = 2000000000;
-static_assert(kTile == kScanCarryRows, "states are kept where the tiles begin");
-static_assert(kMaxLevels <= kWarps, "a warp collects a level");
-constexpr int kFwdStages = 3;                // tiles in shared memory: being read, finished, waited for
-constexpr int kBlocksPerSm = 2;              // by shared memory (96 KB of tiles) and registers (128 a thread)
+constexpr int kTokens = kScanCarryRows;      // looked up and loaded at once; a state is kept for each such run
+constexpr int kRuns = 4;                     // runs of a warp
+constexpr int kWarpTokens = kRuns * kTokens;
+constexpr int kTile = kWarps * kWarpTokens;  // tokens of a block
+constexpr int kFoldTiles = 64;               // up to so many, blocks join the maps before them themselves
+constexpr int kJoinChannels = 8, kJoinParts = 128;  // of a block of k_scan_join
+static_assert(kTokens == 16, "a lane holds the row of one token, half of the lanes none");
 
-// Workspace: word 0 the error record, word 1 this call's verdict on its offsets, word 2 the
-// counter of work units; nodes from byte 256 on.
-struct Tree {
-    int levels;
-    int64_t tiles;
-    int64_t base[kMaxLevels];  // first node of a level, in units of channels
+// Workspace: word 0 the error record, word 1 this call's verdict on its offsets; from byte 256 on the
+// tiles' maps [tiles][c], the warps' [tiles][warps][c] (of the warps before each in its tile), and
+// the states that enter the tiles, fp32 [tiles][c].
+struct Map {
+    float a, b;  // h -> a h + b; a = -1: h -> b
 };
 
 struct ScanArgs {
     int64_t n;
     int c, batch, blocks_c;    // blocks_c: blocks of channels
+    int tiles;
     const int32_t* off;
     const int32_t* order;
-    int reverse, free_input;
+    int reverse;
     const char *gate, *x, *gy;
     char *out, *gg;            // out: grad_x in the backward pass
     uint32_t gate_s, x_s, gy_s, out_s, gg_s;  // strides in bytes
@@ -75,9 +58,8 @@ struct ScanArgs {
     const float* glast;
     float *last, *carries, *gfirst;
     uint32_t* head;
-    uint64_t* nodes;
-    Tree tree;
-    uint32_t units;
+    Map *tile_maps, *warp_maps;
+    float* states;
 };
 
 // ---------------------------------------------------------------- a lane's channels
@@ -88,8 +70,8 @@ __device__ __forceinline__ float2 add_(float2 a, float2 b) { return add2(a, b); 
 __device__ __forceinline__ float add_(float a, float b) { return a + b; }
 __device__ __forceinline__ float2 mul_(float2 a, float2 b) { return mul2(a, b); }
 __device__ __forceinline__ float mul_(float a, float b) { return a * b; }
-__device__ __forceinline__ float2 neg_(float2 a) { return make_float2(-a.x, -a.y); }
-__device__ __forceinline__ float neg_(float a) { return -a; }
+__device__ __forceinline__ float2 sub_(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
+__device__ __forceinline__ float sub_(float a, float b) { return a - b; }
 
 template <typename N> struct Side;
 struct Rest;
@@ -100,13 +82,13 @@ template <> struct Lane<float> {
     static __device__ __forceinline__ float unpack(uint32_t w) { return __uint_as_float(w); }
     static __device__ __forceinline__ uint32_t pack(float x) { return __float_as_uint(x); }
     static __device__ __forceinline__ float fill(float x) { return x; }
-    using Fast = Side<float>;
+    using Gate = Side<float>;
     static __device__ __forceinline__ float load(const float* p) { return *p; }
     static __device__ __forceinline__ void store(float* p, float x) { *p = x; }
 };
 template <typename T> struct Lane16 {
     using Num = float2;
-    using Fast = Rest;
+    using Gate = Rest;
     static constexpr int V = 2;
     static __device__ __forceinline__ float2 fill(float x) { return make_float2(x, x); }
     static __device__ __forceinline__ float2 load(const float* p) { return *reinterpret_cast<const float2*>(p); }
@@ -135,17 +117,15 @@ template <> struct Lane<__nv_bfloat16> : Lane16<__nv_bfloat16> {
 //
 // Side: m = e / (1 + e) with e = exp(-|g|), the smaller of a = sigmoid(g) and 1 - a, held as m
 // (a = m, for g < 0) or as -m (a = 1 - m).  Everything follows without cancellation, but each use
-// has to look at the sign: 13 instructions an element to find a run's map, 8 to apply it.
+// has to look at the sign: twice the instructions.  For fp32.
 //
 // Rest: s = 1 - a = 1 / (1 + exp(g)), and a h = h - s h in one rounding.  Exact at s = 0 and 1,
 // and no coarser than the other where a is near one, so long memories keep their length; near s = 1 what is
-// left of a state is off by 2^-24 of the state (of h_{t-1}, not of what is left).  8 and 5
-// instructions.  The forward pass takes it for 16-bit types, which have a floor of 6 bytes an
-// element, or some 30 instructions; fp32 (12 bytes) and the backward pass (10), whose slope a (1 - a) would
-// lose its small values, take the first.
+// left of a state is off by 2^-24 of the state (of h_{t-1}, not of what is left).  For 16-bit types, whose
+// floor is 6 or 10 bytes an element, some 30 or 50 instructions.
 //
 // 16-bit types take the fast exponential and reciprocal, off by 2 units and |g| / 2^24, and by 1:
-// 1e-6 of m for |g| < 10, where the inputs have 2^-9 or 2^-12.
+// 1e-6 of s for |g| < 10, where the inputs have 2^-9 or 2^-12.
 template <typename N> struct Side {
     using Held = N;
     N m, one;  // one: 1 where a is 1 - m, 0 where it is m
@@ -179,21 +159,41 @@ template <typename N> struct Side {
     static __device__ __forceinline__ float2 slope(float2 m) { return make_float2(slope(m.x), slope(m.y)); }
 
     __device__ __forceinline__ explicit Side(Held held) : m(held), one(near_one(held)) {}
+    // also a (1 - a)
+    static __device__ __forceinline__ Held hold(N g, N& slope_) {
+        const Held m = hold(g);
+        slope_ = slope(m);
+        return m;
+    }
     __device__ __forceinline__ N kept(N h) const { return fma_(m, h, mul_(one, h)); }  // a h
     __device__ __forceinline__ N rest() const { return rest(m, one); }                 // 1 - a
-    __device__ __forceinline__ N slope() const { return slope(m); }                    // a (1 - a)
 };
 struct Rest {
     using Held = float2;
     float2 s, minus;
-    static __device__ __forceinline__ float2 hold(float2 g) {
-        float2 e, s;
-        const float2 y = mul2(g, make_float2(1.4426950408889634f, 1.4426950408889634f));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+    static __device__ __forceinline__ float2 over(float2 e) {  // 1 / (1 + e)
         const float2 d = add2(e, make_float2(1.f, 1.f));
+        float2 s;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
+        return s;
+    }
+    static __device__ __forceinline__ float2 hold(float2 g) {
+        const float2 y = mul2(g, make_float2(1.4426950408889634f, 1.4426950408889634f));
+        float2 e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+        return over(e);
+    }
+    // Also a (1 - a) = exp(g) s s, the exponent bounded so that infinity and zero do not meet.
+    static __device__ __forceinline__ float2 hold(float2 g, float2& slope) {
+        float2 y = mul2(g, make_float2(1.4426950408889634f, 1.4426950408889634f)), e;
+        asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(y.x));  // 126
+        asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(y.y));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+        const float2 s = over(e);
+        slope = mul2(mul2(e, s), s);
         return s;
     }
     __device__ __forceinline__ explicit Rest(Held held) : s(held), minus(mul2(held, make_float2(-1.f, -1.f))) {}
@@ -204,48 +204,6 @@ struct Rest {
 template <bool FREE, typename G, typename N> __device__ __forceinline__ N next_state(const G& g, N x, N h) {
     if constexpr (FREE) return add_(g.kept(h), x);
     return fma_(g.rest(), x, g.kept(h));
-}
-
-// ---------------------------------------------------------------- maps of runs of tokens
-// h -> A h + B; A = -1: h -> B.
-struct Map {
-    float a, b;
-};
-__device__ __forceinline__ float through(Map m, float h) { return m.a < 0.f ? m.b : fmaf(m.a, h, m.b); }
-__device__ __forceinline__ Map then(Map first, Map second) {
-    if (second.a < 0.f) return second;
-    return Map{first.a < 0.f ? -1.f : first.a * second.a, fmaf(second.a, first.b, second.b)};
-}
-__device__ __forceinline__ void publish(uint64_t* node, Map m) {
-    uint64_t w = (uint64_t)__float_as_uint(m.b) << 32 | __float_as_uint(m.a);
-    if (w == kUnset) w = (uint64_t)0x7fc00000u << 32 | 0x7fc00000u;
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(node), "l"(w) : "memory");
-}
-__device__ __forceinline__ uint64_t look(const uint64_t* node) {
-    uint64_t w;
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(node) : "memory");
-    return w;
-}
-__device__ __forceinline__ Map map_of(uint64_t w) {
-    return Map{__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
-}
-// The node's map once it is there.  Where another block gave up (its record is set), or after
-// kGiveUpNs, a constant NaN.
-__device__ __noinline__ uint64_t awaited(const uint64_t* node, uint32_t* record) {
-    const uint64_t t0 = globaltimer();
-    for (int spins = 0;; ++spins) {
-        const uint64_t w = look(node);
-        if (w != kUnset) return w;
-        if ((spins & 63) == 63) {
-            const bool late = globaltimer() - t0 > kGiveUpNs;
-            if (late) atomicOr(record, kErrTimeout);
-            if (late || (*reinterpret_cast<volatile uint32_t*>(record) & kErrTimeout))
-                return (uint64_t)0x7fc00000u << 32 | 0xbf800000u;
-        }
-    }
-}
-__device__ __forceinline__ uint64_t* node_at(const ScanArgs& a, int l, int64_t i, int c) {
-    return a.nodes + a.tree.base[l] + i * a.c + c;
 }
 
 // ---------------------------------------------------------------- beginnings and ends of sequences
@@ -282,7 +240,7 @@ __device__ __forceinline__ Cuts find_cuts(const ScanArgs& a, CutSeqs& s, Within&
     const int64_t hi = lo + count;
     Cuts r{0u, 0u};
     if (lo > w.from && hi < w.to) return r;
-    const bool last = hi == a.n && (count > 0 || (lo == 0 && threadIdx.x < 32));  // the visits' end lies here
+    const bool last = hi == a.n && (count > 0 || (a.n == 0 && threadIdx.x < 32));  // the visits' end lies here
     if (count == 0 && !last) return r;
     // the number of sequences that begin before lo, 32 probes at a time
     int from = 0, to = a.batch;
@@ -329,511 +287,445 @@ __device__ __forceinline__ Cuts find_cuts(const ScanArgs& a, CutSeqs& s, Within&
     return r;
 }
 
-// ---------------------------------------------------------------- the work of a block
-// Maps of the warps (h -> A h + B), sealed ones marked, of two tiles, and the joined maps of the
-// levels' siblings.
-template <int CH, bool BWD>
-struct Joint {
-    float a[2][kWarps][CH], b[2][kWarps][CH];  // in the direction that goes from tile to tile
-    float fa[BWD ? kWarps : 1][CH], fb[BWD ? kWarps : 1][CH];  // backward pass: along the visits
-    CutSeqs seqs[2][kWarps];
-    uint32_t unit;
-    int reached;      // something reaches into the tile
-    float la[1][CH];  // of each level, a and b in turn
-
-    static constexpr size_t bytes(int levels) { return sizeof(Joint) + (2 * (size_t)levels - 1) * CH * 4; }
+// ---------------------------------------------------------------- maps of runs of tokens
+__device__ __forceinline__ float through(Map m, float h) { return m.a < 0.f ? m.b : fmaf(m.a, h, m.b); }
+__device__ __forceinline__ Map then(Map first, Map second) {
+    if (second.a < 0.f) return second;
+    return Map{first.a < 0.f ? -1.f : first.a * second.a, fmaf(second.a, first.b, second.b)};
+}
+// Of a lane's channels.
+template <int V> struct Maps {
+    Map m[V];
 };
+template <int V> __device__ __forceinline__ Maps<V> load_maps(const Map* p) {
+    Maps<V> r;
+    if constexpr (V == 2) {
+        const float4 f = *reinterpret_cast<const float4*>(p);
+        r.m[0] = Map{f.x, f.y};
+        r.m[1] = Map{f.z, f.w};
+    } else {
+        const float2 f = *reinterpret_cast<const float2*>(p);
+        r.m[0] = Map{f.x, f.y};
+    }
+    return r;
+}
+template <int V> __device__ __forceinline__ void store_maps(Map* p, const Maps<V>& r) {
+    if constexpr (V == 2)
+        *reinterpret_cast<float4*>(p) = make_float4(r.m[0].a, r.m[0].b, r.m[1].a, r.m[1].b);
+    else
+        *reinterpret_cast<float2*>(p) = make_float2(r.m[0].a, r.m[0].b);
+}
+template <int V> __device__ __forceinline__ Maps<V> then(const Maps<V>& first, const Maps<V>& second) {
+    Maps<V> r;
+#pragma unroll
+    for (int j = 0; j < V; ++j) r.m[j] = then(first.m[j], second.m[j]);
+    return r;
+}
+template <int V> __device__ __forceinline__ Maps<V> no_change() {
+    Maps<V> r;
+#pragma unroll
+    for (int j = 0; j < V; ++j) r.m[j] = Map{1.f, 0.f};
+    return r;
+}
+__device__ __forceinline__ float through(const Maps<1>& m, float h) { return through(m.m[0], h); }
+__device__ __forceinline__ float2 through(const Maps<2>& m, float2 h) {
+    return make_float2(through(m.m[0], h.x), through(m.m[1], h.y));
+}
+__device__ __forceinline__ Maps<1> maps_of(float a, float b, bool constant) {
+    return Maps<1>{{Map{constant ? -1.f : a, b}}};
+}
+__device__ __forceinline__ Maps<2> maps_of(float2 a, float2 b, bool constant) {
+    return Maps<2>{{Map{constant ? -1.f : a.x, b.x}, Map{constant ? -1.f : a.y, b.y}}};
+}
 
-// A warp's tokens of a unit.
-struct Share {
-    uint32_t v;           // the tile's place in the order of the work
-    int32_t lo, count;    // the warp's first visit, its tokens
-    int32_t c0;           // the block's first channel
-    int32_t row;          // of the token of this lane's number: -1 where there is none
-    Cuts cuts;
-    bool simple;          // all tokens there, nothing begins or ends among them
-    bool reached, sealed; // of the tile: something reaches into it; its map is constant
+// ---------------------------------------------------------------- the tokens of a warp
+// What a lane of a warp knows of its place.
+struct Place {
+    int c;         // its first channel
+    bool real;     // there is such a channel
+    int32_t lo;    // the warp's first visit
+    int32_t rows[2];  // of the visits of this lane's number, and 32 further: -1 where there is none
 };
-template <int CH>
-__device__ __forceinline__ Share share_of(const ScanArgs& a, uint32_t unit, bool from_end) {
-    Share s;
-    s.v = unit / (uint32_t)a.blocks_c;
-    s.c0 = (int)(unit - s.v * (uint32_t)a.blocks_c) * CH;
-    const int64_t tile = from_end ? a.tree.tiles - 1 - s.v : s.v;
-    s.lo = (int32_t)min(tile * kTile + (threadIdx.x >> 5) * kTokens, a.n);
-    s.count = min(kTokens, (int32_t)a.n - s.lo);
+template <typename L>
+__device__ __forceinline__ Place place_of(const ScanArgs& a, int tile, int block_c) {
+    Place p;
     const int lane = threadIdx.x & 31;
-    s.row = -1;
-    if (lane < s.count) {
-        const int32_t p = a.reverse ? (int32_t)a.n - 1 - (s.lo + lane) : s.lo + lane;
-        s.row = p;
-        if (a.order) {
-            s.row = a.order[p];
-            if (s.row < 0 || s.row >= a.n) {
-                s.row = -1;
+    p.c = block_c * 32 * L::V + lane * L::V;
+    p.real = p.c < a.c;
+    p.lo = (int32_t)min((int64_t)tile * kTile + (int)(threadIdx.x >> 5) * kWarpTokens, a.n);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t v = (int64_t)p.lo + i * 32 + lane;
+        p.rows[i] = -1;
+        if (v < a.n) {
+            const int64_t at = a.reverse ? a.n - 1 - v : v;
+            p.rows[i] = a.order ? a.order[at] : (int32_t)at;
+            if (p.rows[i] < 0 || p.rows[i] >= a.n) {
+                p.rows[i] = -1;
                 atomicOr(a.head, kErrRange);
             }
         }
     }
-    return s;
-}
-// Copy the tokens' channels of one operand, [kTokens][128 bytes]; zeros where there is no row or channel.
-template <typename T>
-__device__ __forceinline__ void fetch(uint32_t to, const char* from, uint32_t stride, const Share& s, int c) {
-    const int lane = threadIdx.x & 31, chunk = lane & 7;
-    const int at = s.c0 * (int)sizeof(T) + chunk * 16;
-#pragma unroll
-    for (int i = 0; i < kTokens / 4; ++i) {
-        const int r = i * 4 + (lane >> 3);
-        const int row = __shfl_sync(0xffffffffu, s.row, r);
-        const bool have = row >= 0 && at < c * (int)sizeof(T);
-        cp_async16(to + r * kRowBytes + chunk * 16, have ? from + (uint64_t)(uint32_t)row * stride + at : from, have ? 16 : 0);
-    }
+    return p;
 }
 
-// The block's units: the first at `first`, the others from the counter, one ahead.
-__device__ __forceinline__ uint32_t claim(const ScanArgs& a) { return atomicAdd(a.head + 2, 1u); }
-
-// False if the call's offsets are no partition of the positions.  With one tile (and no launch
-// before this one) the block sees for itself.
-__device__ __forceinline__ bool good_offsets(const ScanArgs& a) {
-    if (a.tree.tiles > 1) return a.head[1] == 0;
-    bool bad = false;
-    for (int64_t i = threadIdx.x; i < a.batch; i += kThreads) {
-        const int32_t p = a.off[i], q = a.off[i + 1];
-        bad |= p > q || (i == 0 && p != 0) || (i == a.batch - 1 && q != a.n);
-    }
-    if (!__syncthreads_or(bad)) return true;
-    if (threadIdx.x == 0) atomicOr(a.head, kErrRange);
-    return false;
-}
-
-// The joined maps of the siblings before tile v's ancestor at a level, waited for.
+// A run of the warp's tokens.
+struct Run {
+    int32_t lo, count;
+    int32_t row;   // of the token of this lane's number, up to kTokens
+    Cuts cuts;
+    bool simple;   // all tokens there, nothing begins or ends among them
+};
 template <int V>
-__device__ __forceinline__ void siblings(const ScanArgs& a, int64_t v, int level, int c, Map (&m)[V]) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) m[j] = Map{1.f, 0.f};
-    if (c >= a.c) return;
-    const int64_t at = v >> (kFan * level);
-    const int before = (int)(at & kSiblings);
-    const uint64_t* node = node_at(a, level, at - before, c);
-    uint64_t w[kSiblings][V];
-#pragma unroll
-    for (int i = 0; i < kSiblings; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) w[i][j] = i < before ? look(node + (int64_t)i * a.c + j) : 0;
-#pragma unroll
-    for (int i = 0; i < kSiblings; ++i)
-        if (i < before) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (w[i][j] == kUnset) w[i][j] = awaited(node + (int64_t)i * a.c + j, a.head);
-                m[j] = then(m[j], map_of(w[i][j]));
-            }
-        }
+__device__ __forceinline__ Run run_of(const ScanArgs& a, const Place& p, int q, CutSeqs& seqs, Within& within,
+                                      const float* in, float* out) {
+    Run r;
+    const int lane = threadIdx.x & 31;
+    r.lo = (int32_t)min((int64_t)p.lo + q * kTokens, a.n);
+    r.count = min(kTokens, (int32_t)a.n - r.lo);
+    r.row = __shfl_sync(0xffffffffu, q < 2 ? p.rows[0] : p.rows[1], (q & 1) * kTokens + (lane & (kTokens - 1)));
+    r.cuts = find_cuts<V>(a, seqs, within, r.lo, r.count, p.c, in, out);
+    r.simple = r.count == kTokens && (r.cuts.begin | r.cuts.end) == 0 && __all_sync(0xffffffffu, r.row >= 0);
+    return r;
 }
-
-// The first warp publishes the tile's map (the joined maps of the warps; BWD: the last one's first), and
-// the nodes that end with the tile, each as soon as the levels below it are there.  (When a block
-// waited for all levels before it published any, each group of 8 tiles waited for the one before:
-// 4.9 M tokens of 64 channels took 7.1 ms.)
-template <int CH, bool BWD>
-__device__ __forceinline__ void publish_nodes(const ScanArgs& a, const Joint<CH, BWD>& s, int parity, uint32_t v,
-                                              int c0, bool sealed) {
-    constexpr int V = CH / 32;
-    const int cl = (int)threadIdx.x * V, c = c0 + cl;
-    Map own[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        own[j] = Map{1.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const int w = BWD ? kWarps - 1 - i : i;
-            own[j] = then(own[j], Map{s.a[parity][w][cl + j], s.b[parity][w][cl + j]});
-        }
-        if (c < a.c) publish(node_at(a, 0, v, c + j), own[j]);
-    }
-    for (int l = 0; l + 1 < a.tree.levels && ((v >> (kFan * l)) & kSiblings) == kSiblings; ++l) {
-        if (!sealed) {
-            Map m[V];
-            siblings<V>(a, v, l, c, m);
-#pragma unroll
-            for (int j = 0; j < V; ++j) own[j] = then(m[j], own[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (c < a.c) publish(node_at(a, l + 1, v >> (kFan * (l + 1)), c + j), own[j]);
-    }
-}
-
-// Collect the maps of the tiles before this one, a level to a warp.
-template <int CH, bool BWD>
-__device__ __forceinline__ void collect(const ScanArgs& a, Joint<CH, BWD>& s, uint32_t v, int c0) {
-    constexpr int V = CH / 32;
-    const int level = kWarps - 1 - (threadIdx.x >> 5), cl = (threadIdx.x & 31) * V;
-    if (level >= a.tree.levels) return;
-    Map m[V];
-    siblings<V>(a, v, level, c0 + cl, m);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        s.la[2 * level][cl + j] = m[j].a;
-        s.la[2 * level + 1][cl + j] = m[j].b;
-    }
-}
-
-// h through a map of the lane's channels.
-__device__ __forceinline__ float step_through(const float* a, const float* b, float h) {
-    return through(Map{*a, *b}, h);
-}
-__device__ __forceinline__ float2 step_through(const float* a, const float* b, float2 h) {
-    const float2 x = *reinterpret_cast<const float2*>(a), y = *reinterpret_cast<const float2*>(b);
-    return make_float2(through(Map{x.x, y.x}, h.x), through(Map{x.y, y.y}, h.y));
-}
-// What enters this warp's tokens, from the levels' maps and those of the warps before it.
-template <typename L, int CH, bool BWD>
-__device__ __forceinline__ typename L::Num entering(const ScanArgs& a, const Joint<CH, BWD>& s, int parity,
-                                                    bool reached) {
-    const int warp = threadIdx.x >> 5, cl = (threadIdx.x & 31) * L::V;
-    typename L::Num h = L::fill(0.f);
-    if (reached)
-        for (int l = a.tree.levels - 1; l >= 0; --l) h = step_through(&s.la[2 * l][cl], &s.la[2 * l + 1][cl], h);
-    if constexpr (BWD) {
-        for (int w = kWarps - 1; w > warp; --w) h = step_through(&s.a[parity][w][cl], &s.b[parity][w][cl], h);
-    } else {
-        for (int w = 0; w < warp; ++w) h = step_through(&s.a[parity][w][cl], &s.b[parity][w][cl], h);
-    }
-    return h;
-}
-
-// A block's first unit (one tile in all: its only one).
-template <typename J>
-__device__ __forceinline__ uint32_t first_unit(const ScanArgs& a, J& s) {
-    if (a.tree.tiles == 1) return blockIdx.x;
-    if (threadIdx.x == 0) s.unit = claim(a);
-    __syncthreads();
-    return s.unit;
-}
-
-__device__ __forceinline__ bool all_rows(const Share& s) {
-    return __all_sync(0xffffffffu, s.row >= 0 || (threadIdx.x & 31) >= kTokens) && s.count == kTokens;
+// A token's word of an operand; zero where there is no row or channel.
+__device__ __forceinline__ uint32_t word(const char* base, uint32_t stride, int32_t row, bool real) {
+    return real && row >= 0 ? *reinterpret_cast<const uint32_t*>(base + (uint64_t)(uint32_t)row * stride) : 0u;
 }
 template <typename L>
 __device__ __forceinline__ void put(char* base, int32_t row, uint32_t stride, typename L::Num x) {
     *reinterpret_cast<uint32_t*>(base + (uint64_t)(uint32_t)row * stride) = L::pack(x);
 }
+__device__ __forceinline__ int32_t row_at(const Run& r, int k) { return __shfl_sync(0xffffffffu, r.row, k); }
 // The states of sequence `seq`, zero where there are none.
 template <typename L>
-__device__ __forceinline__ typename L::Num state_of(const ScanArgs& a, const float* states, int seq, int c) {
-    return states && c < a.c ? L::load(states + (int64_t)seq * a.c + c) : L::fill(0.f);
+__device__ __forceinline__ typename L::Num state_of(const ScanArgs& a, const float* states, int seq, const Place& p) {
+    return states && p.real ? L::load(states + (int64_t)seq * a.c + p.c) : L::fill(0.f);
 }
 
-// A block finds and publishes a tile's map before it finishes the tile before: by the time it wants
-// to know what enters a tile, the blocks of the earlier tiles have long published theirs.  (With one
-// tile at a time all blocks went through their phases in step, and waited together: 602k tokens
-// of 512 channels took 1732 us forward and 1955 backward.)
-template <typename T, bool FREE>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_scan_fwd(const ScanArgs a) {
+// The map of a warp's tokens: of the state along the visits, or (BWD) of the gradient against them.
+template <typename T, bool FREE, bool BWD>
+__device__ __forceinline__ Maps<Lane<T>::V> warp_map(const ScanArgs& a, const Place& p, CutSeqs& seqs) {
     using L = Lane<T>;
     using N = typename L::Num;
-    using G = typename L::Fast;
-    constexpr int CH = 32 * L::V, kStep = kRowBytes / 4, kStage = 2 * kTileBytes;
-    extern __shared__ __align__(128) char s_dyn[];  // [kFwdStages][gate, x][kTile][128 bytes], then the maps
-    using J = Joint<CH, false>;
-    J& s = *reinterpret_cast<J*>(s_dyn + kFwdStages * kStage);
-    if (!good_offsets(a)) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cl = lane * L::V;
-    const bool many = a.tree.tiles > 1;
-    const uint32_t unit = first_unit(a, s);
-    if (unit >= a.units) return;
-    char* const mine = s_dyn + warp * kTokens * kRowBytes;  // this warp's tokens in a stage
-    const auto fetch_all = [&](int stage, const Share& of) {
-        const uint32_t to = smem_u32(mine) + stage * kStage;
-        fetch<T>(to, a.gate, a.gate_s, of, a.c);
-        fetch<T>(to + kTileBytes, a.x, a.x_s, of, a.c);
-    };
+    using G = typename L::Gate;
     Within within;
-    Share now = share_of<CH>(a, unit, false), last{};
-    typename G::Held held[kTokens];  // of the last tile
-    fetch_all(0, now);
-    bool have = true, pending = false;
-
-    for (int turn = 0, stage = 0; have || pending; ++turn) {
-        const int parity = turn & 1, next_stage = stage == kFwdStages - 1 ? 0 : stage + 1;
-        typename G::Held fresh[kTokens];
-        Share ahead{};
-        uint32_t next = a.units;
-        if (have) {
-            const int c = now.c0 + cl;
-            CutSeqs& seqs = s.seqs[parity][warp];
-            now.cuts = find_cuts<L::V>(a, seqs, within, now.lo, now.count, c, a.first, a.last);
-            now.simple = all_rows(now) && (now.cuts.begin | now.cuts.end) == 0;
-            cp_async_wait_all();
-            __syncwarp();
-            if (many && threadIdx.x == 0) next = claim(a);
-            const uint32_t* gw = reinterpret_cast<const uint32_t*>(mine + stage * kStage) + lane;
-            const uint32_t* xw = gw + kTileBytes / 4;
-            N A = L::fill(1.f), B = L::fill(0.f);
-            if (now.simple) {
-#pragma unroll
-                for (int k = 0; k < kTokens; ++k) {
-                    fresh[k] = G::hold(L::unpack(gw[k * kStep]));
-                    const G g(fresh[k]);
-                    B = next_state<FREE>(g, L::unpack(xw[k * kStep]), B);
-                    A = g.kept(A);
-                }
-            } else {
+    const int at = p.real ? p.c * (int)sizeof(T) : 0;
+    const char* const gate = a.gate + at;
+    const char* const x = (BWD ? a.gy : a.x) + at;
+    const uint32_t xs = BWD ? a.gy_s : a.x_s;
+    N A = L::fill(1.f), B = L::fill(0.f);
+    bool constant = false;
 #pragma unroll 1
-                for (int k = 0; k < now.count; ++k) {
-                    if (now.cuts.begin >> k & 1) B = state_of<L>(a, a.first, seqs.begin[k], c);
-                    const G g(G::hold(L::unpack(gw[k * kStep])));
-                    B = next_state<FREE>(g, L::unpack(xw[k * kStep]), B);
-                    A = g.kept(A);
-                }
-                if (now.cuts.begin) A = L::fill(-1.f);
-            }
-            L::store(&s.a[parity][warp][cl], A);
-            L::store(&s.b[parity][warp][cl], B);
-            if (threadIdx.x == 0) {
-                s.reached = many && !(now.cuts.begin & 1);
-                s.unit = next;
-            }
-        }
-        now.sealed = __syncthreads_or(have && now.cuts.begin != 0);
-        if (have) {
-            now.reached = s.reached;
-            next = s.unit;
-            if (next < a.units) {
-                ahead = share_of<CH>(a, next, false);
-                fetch_all(next_stage, ahead);
-            }
-            if (many && warp == 0) publish_nodes<CH, false>(a, s, parity, now.v, now.c0, now.sealed);
-        }
-        if (pending) {
-            const int before = stage == 0 ? kFwdStages - 1 : stage - 1, c = last.c0 + cl;
-            const CutSeqs& seqs = s.seqs[parity ^ 1][warp];
-            if (last.reached) collect<CH, false>(a, s, last.v, last.c0);
-            __syncthreads();
-            N h = entering<L, CH, false>(a, s, parity ^ 1, last.reached);
-            const bool real = c < a.c;
-            if (real && a.carries && warp == 0 && last.count > 0) L::store(a.carries + (int64_t)last.v * a.c + c, h);
-            const uint32_t* gw = reinterpret_cast<const uint32_t*>(mine + before * kStage) + lane;
-            const uint32_t* xw = gw + kTileBytes / 4;
-            char* const out = a.out + c * (int)sizeof(T);
-            if (last.simple) {
+    for (int i = 0; i < kRuns; ++i) {
+        const int q = BWD ? kRuns - 1 - i : i;
+        const Run r = run_of<L::V>(a, p, q, seqs, within, nullptr, nullptr);
+        if (r.simple) {
+            uint32_t gw[kTokens], xw[kTokens];
 #pragma unroll
-                for (int k = 0; k < kTokens; ++k) {
-                    const int32_t row = __shfl_sync(0xffffffffu, last.row, k);
-                    h = next_state<FREE>(G(held[k]), L::unpack(xw[k * kStep]), h);
-                    if (real) put<L>(out, row, a.out_s, h);
-                }
-            } else {
+            for (int k = 0; k < kTokens; ++k) {
+                const int32_t row = row_at(r, k);
+                gw[k] = word(gate, a.gate_s, row, p.real);
+                xw[k] = word(x, xs, row, p.real);
+            }
+#pragma unroll
+            for (int j = 0; j < kTokens; ++j) {
+                const int k = BWD ? kTokens - 1 - j : j;
+                const G g(G::hold(L::unpack(gw[k])));
+                B = BWD ? g.kept(add_(B, L::unpack(xw[k]))) : next_state<FREE>(g, L::unpack(xw[k]), B);
+                A = g.kept(A);
+            }
+        } else {
+            const uint32_t resets = BWD ? r.cuts.end : r.cuts.begin;
+            constant |= resets != 0;
 #pragma unroll 1
-                for (int k = 0; k < last.count; ++k) {
-                    const int32_t row = __shfl_sync(0xffffffffu, last.row, k);
-                    if (last.cuts.begin >> k & 1) h = state_of<L>(a, a.first, seqs.begin[k], c);
-                    const G g(G::hold(L::unpack(gw[k * kStep])));
-                    h = next_state<FREE>(g, L::unpack(xw[k * kStep]), h);
-                    if (real && row >= 0) put<L>(out, row, a.out_s, h);
-                    if (a.last && real && (last.cuts.end >> k & 1))
-                        L::store(a.last + (int64_t)seqs.end(last.cuts, k) * a.c + c, h);
-                }
+            for (int j = 0; j < r.count; ++j) {
+                const int k = BWD ? r.count - 1 - j : j;
+                const int32_t row = row_at(r, k);
+                const G g(G::hold(L::unpack(word(gate, a.gate_s, row, p.real))));
+                const N v = L::unpack(word(x, xs, row, p.real));
+                if (resets >> k & 1)
+                    B = BWD ? state_of<L>(a, a.glast, seqs.end(r.cuts, k), p) : state_of<L>(a, a.first, seqs.begin[k], p);
+                B = BWD ? g.kept(add_(B, v)) : next_state<FREE>(g, v, B);
+                A = g.kept(A);
             }
         }
-        __syncthreads();  // the last tile's maps and stage have been read
-        pending = have;
-        have = next < a.units;
-        last = now;
-        now = ahead;
-#pragma unroll
-        for (int k = 0; k < kTokens; ++k) held[k] = fresh[k];
-        stage = next_stage;
+        __syncwarp();
     }
+    return maps_of(A, B, constant);
 }
 
-// The backward pass takes the tiles from the end, and joins the warps' maps from the last.  The
-// states are found again from those that the forward pass kept at the tiles' beginnings.
-template <typename T, bool FREE>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_scan_bwd(const ScanArgs a) {
-    using L = Lane<T>;
-    using N = typename L::Num;
-    using G = Side<N>;
-    constexpr int CH = 32 * L::V, kStep = kRowBytes / 4, kStage = 3 * kTileBytes;
-    extern __shared__ __align__(128) char s_dyn[];  // [2][gate, x, dy][kTile][128 bytes], then the maps
-    using J = Joint<CH, true>;
-    J& s = *reinterpret_cast<J*>(s_dyn + 2 * kStage);
-    if (!good_offsets(a)) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cl = lane * L::V;
-    const bool many = a.tree.tiles > 1;
-    const uint32_t unit = first_unit(a, s);
-    if (unit >= a.units) return;
-    char* const mine = s_dyn + warp * kTokens * kRowBytes;
-    const auto fetch_all = [&](int stage, const Share& of) {
-        const uint32_t to = smem_u32(mine) + stage * kStage;
-        fetch<T>(to, a.gate, a.gate_s, of, a.c);
-        fetch<T>(to + kTileBytes, a.x, a.x_s, of, a.c);
-        fetch<T>(to + 2 * kTileBytes, a.gy, a.gy_s, of, a.c);
-    };
-    Within within;
-    Share now = share_of<CH>(a, unit, true), last{};
-    N from_before = L::fill(0.f);  // the state that enters the last tile's tokens of this warp
-    fetch_all(0, now);
-    bool have = true, pending = false;
-
-    for (int turn = 0; have || pending; ++turn) {
-        const int parity = turn & 1;
-        Share ahead{};
-        uint32_t next = a.units;
-        N h = L::fill(0.f);
-        if (have) {
-            const int c = now.c0 + cl;
-            CutSeqs& seqs = s.seqs[parity][warp];
-            if (c < a.c && now.count > 0) h = L::load(a.carries + (a.tree.tiles - 1 - now.v) * a.c + c);
-            now.cuts = find_cuts<L::V>(a, seqs, within, now.lo, now.count, c, a.glast, a.gfirst);
-            now.simple = all_rows(now) && (now.cuts.begin | now.cuts.end) == 0;
-            cp_async_wait_all();
-            __syncwarp();
-            if (many && threadIdx.x == 0) next = claim(a);
-            const uint32_t* gw = reinterpret_cast<const uint32_t*>(mine + parity * kStage) + lane;
-            const uint32_t* xw = gw + kTileBytes / 4;
-            const uint32_t* yw = xw + kTileBytes / 4;
-            N A = L::fill(1.f), B = L::fill(0.f), D = L::fill(0.f);
-            if (now.simple) {
-                typename G::Held held[kTokens];
+// Each warp's map in shared memory becomes, for each warp, that of the warps before it (BWD: behind
+// it); `all`: the block's.
+template <int V>
+__device__ __forceinline__ Maps<V> before_warp(const Map (*s_maps)[32 * V], bool bwd, Maps<V>& all) {
+    const int warp = threadIdx.x >> 5, cl = (threadIdx.x & 31) * V;
+    Maps<V> m = no_change<V>(), mine = m;
 #pragma unroll
-                for (int k = 0; k < kTokens; ++k) {
-                    held[k] = G::hold(L::unpack(gw[k * kStep]));
-                    const G g(held[k]);
-                    B = next_state<FREE>(g, L::unpack(xw[k * kStep]), B);
-                    A = g.kept(A);
-                }
-#pragma unroll
-                for (int k = kTokens - 1; k >= 0; --k) D = G(held[k]).kept(add_(D, L::unpack(yw[k * kStep])));
-            } else {
-#pragma unroll 1
-                for (int k = 0; k < now.count; ++k) {
-                    if (now.cuts.begin >> k & 1) B = state_of<L>(a, a.first, seqs.begin[k], c);
-                    const G g(G::hold(L::unpack(gw[k * kStep])));
-                    B = next_state<FREE>(g, L::unpack(xw[k * kStep]), B);
-                    A = g.kept(A);
-                }
-#pragma unroll 1
-                for (int k = now.count - 1; k >= 0; --k) {
-                    if (now.cuts.end >> k & 1) D = state_of<L>(a, a.glast, seqs.end(now.cuts, k), c);
-                    D = G(G::hold(L::unpack(gw[k * kStep]))).kept(add_(D, L::unpack(yw[k * kStep])));
-                }
-            }
-            L::store(&s.fa[warp][cl], now.cuts.begin ? L::fill(-1.f) : A);
-            L::store(&s.fb[warp][cl], B);
-            L::store(&s.a[parity][warp][cl], now.cuts.end ? L::fill(-1.f) : A);
-            L::store(&s.b[parity][warp][cl], D);
-            // the last visit of all is an end, so a tile that is not full is not reached
-            if (threadIdx.x == kThreads - 1)
-                s.reached = many && now.count == kTokens && !(now.cuts.end >> (kTokens - 1) & 1);
-            if (threadIdx.x == 0) s.unit = next;
-        }
-        now.sealed = __syncthreads_or(have && now.cuts.end != 0);
-        if (have) {
-            now.reached = s.reached;
-            next = s.unit;
-            if (many && warp == 0) publish_nodes<CH, true>(a, s, parity, now.v, now.c0, now.sealed);
-            for (int w = 0; w < warp; ++w) h = step_through(&s.fa[w][cl], &s.fb[w][cl], h);
-        }
-        if (pending) {
-            const int c = last.c0 + cl;
-            const CutSeqs& seqs = s.seqs[parity ^ 1][warp];
-            if (last.reached) collect<CH, true>(a, s, last.v, last.c0);
-            __syncthreads();
-            N mu = entering<L, CH, true>(a, s, parity ^ 1, last.reached);
-            const bool real = c < a.c;
-            const uint32_t* gw = reinterpret_cast<const uint32_t*>(mine + (parity ^ 1) * kStage) + lane;
-            const uint32_t* xw = gw + kTileBytes / 4;
-            const uint32_t* yw = xw + kTileBytes / 4;
-            char* const gg = a.gg + c * (int)sizeof(T);
-            char* const gx = a.out + c * (int)sizeof(T);
-            // a token's gradients, from the state before it and the gradient that comes from behind it
-            const auto gradients = [&](const G& g, N x, N y, N before, N& dg, N& dx) {
-                const N lam = add_(mu, y);
-                dg = mul_(mul_(g.slope(), FREE ? before : add_(before, neg_(x))), lam);
-                dx = FREE ? lam : mul_(g.rest(), lam);
-                mu = g.kept(lam);
-            };
-            if (last.simple) {
-                typename G::Held held[kTokens];
-                N before[kTokens], state = from_before;
-#pragma unroll
-                for (int k = 0; k < kTokens; ++k) {
-                    held[k] = G::hold(L::unpack(gw[k * kStep]));
-                    before[k] = state;
-                    state = next_state<FREE>(G(held[k]), L::unpack(xw[k * kStep]), state);
-                }
-#pragma unroll
-                for (int k = kTokens - 1; k >= 0; --k) {
-                    const int32_t row = __shfl_sync(0xffffffffu, last.row, k);
-                    N dg, dx;
-                    gradients(G(held[k]), L::unpack(xw[k * kStep]), L::unpack(yw[k * kStep]), before[k], dg, dx);
-                    if (real) {
-                        put<L>(gg, row, a.gg_s, dg);
-                        put<L>(gx, row, a.out_s, dx);
-                    }
-                }
-            } else {
-                // the state before a token is found from the warp's first one, or the last beginning, each time
-#pragma unroll 1
-                for (int k = last.count - 1; k >= 0; --k) {
-                    N before = from_before;
-                    int from = 0;
-                    const uint32_t until = last.cuts.begin & ((2u << k) - 1);
-                    if (until) {
-                        from = 31 - __clz(until);
-                        before = state_of<L>(a, a.first, seqs.begin[from], c);
-                    }
-#pragma unroll 1
-                    for (int i = from; i < k; ++i)
-                        before = next_state<FREE>(G(G::hold(L::unpack(gw[i * kStep]))), L::unpack(xw[i * kStep]),
-                                                  before);
-                    if (last.cuts.end >> k & 1) mu = state_of<L>(a, a.glast, seqs.end(last.cuts, k), c);
-                    N dg, dx;
-                    gradients(G(G::hold(L::unpack(gw[k * kStep]))), L::unpack(xw[k * kStep]),
-                              L::unpack(yw[k * kStep]), before, dg, dx);
-                    const int32_t row = __shfl_sync(0xffffffffu, last.row, k);
-                    if (real && row >= 0) {
-                        put<L>(gg, row, a.gg_s, dg);
-                        put<L>(gx, row, a.out_s, dx);
-                    }
-                    if (a.gfirst && real && (last.cuts.begin >> k & 1))
-                        L::store(a.gfirst + (int64_t)seqs.begin[k] * a.c + c, mu);
-                }
-            }
-        }
-        __syncthreads();  // the last tile's maps and stage have been read
-        if (next < a.units) {
-            ahead = share_of<CH>(a, next, true);
-            fetch_all(parity ^ 1, ahead);
-        }
-        pending = have;
-        have = next < a.units;
-        last = now;
-        now = ahead;
-        from_before = h;
+    for (int i = 0; i < kWarps; ++i) {
+        const int w = bwd ? kWarps - 1 - i : i;
+        if (w == warp) mine = m;
+        m = then(m, load_maps<V>(&s_maps[w][cl]));
     }
+    all = m;
+    return mine;
 }
 
-// Before the pass: nodes unset, counter at zero, and the verdict on the offsets, which the first
-// block alone reaches (0 and n at the ends, never falling).
-__global__ void __launch_bounds__(1024) k_scan_begin(const ScanArgs a, int64_t words) {
-    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 1024)
-        a.nodes[i] = kUnset;
-    if (blockIdx.x > 0) return;
+// False if the call's offsets are no partition of the positions.
+__device__ __forceinline__ bool good_offsets(const ScanArgs& a) {
     bool bad = false;
-    for (int64_t i = threadIdx.x; i < a.batch; i += 1024) {
+    for (int64_t i = threadIdx.x; i < a.batch; i += kThreads) {
         const int32_t p = a.off[i], q = a.off[i + 1];
         bad |= p > q || (i == 0 && p != 0) || (i == a.batch - 1 && q != a.n);
     }
-    const int any = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-        a.head[1] = any ? 1u : 0u;
-        a.head[2] = 0;
-        if (any) atomicOr(a.head, kErrRange);
+    return !__syncthreads_or(bad);
+}
+
+// Step 1.  (Offsets that are no partition lead it to wrong maps, but to no wrong address; the first
+// block leaves its verdict for step 3.)
+template <typename T, bool FREE, bool BWD>
+__global__ void __launch_bounds__(kThreads, 3) k_scan_map(const ScanArgs a) {
+    using L = Lane<T>;
+    constexpr int V = L::V;
+    __shared__ Map s_maps[kWarps][32 * V];
+    __shared__ CutSeqs s_seqs[kWarps];
+    const int warp = threadIdx.x >> 5, cl = (threadIdx.x & 31) * V;
+    const int tile = blockIdx.x / a.blocks_c, block_c = blockIdx.x - tile * a.blocks_c;
+    const Place p = place_of<L>(a, tile, block_c);
+    store_maps<V>(&s_maps[warp][cl], warp_map<T, FREE, BWD>(a, p, s_seqs[warp]));
+    __syncthreads();
+    Maps<V> all;
+    const Maps<V> mine = before_warp<V>(s_maps, BWD, all);
+    if (p.real) {
+        store_maps<V>(a.warp_maps + ((int64_t)tile * kWarps + warp) * a.c + p.c, mine);
+        if (warp == 0) store_maps<V>(a.tile_maps + (int64_t)tile * a.c + p.c, all);
+    }
+    if (blockIdx.x == 0) {
+        const bool good = good_offsets(a);
+        if (threadIdx.x == 0) {
+            a.head[1] = good ? 0u : 1u;
+            if (!good) atomicOr(a.head, kErrRange);
+        }
+    }
+}
+
+// Step 2, for many tiles: the states that enter them.  kJoinParts threads a channel take a range of
+// tiles each, join the ranges' maps by doubling the distance, and go through their ranges again.
+template <bool BWD>
+__global__ void __launch_bounds__(kJoinChannels* kJoinParts) k_scan_join(const ScanArgs a) {
+    __shared__ Map s[2][kJoinParts][kJoinChannels];
+    const int cl = threadIdx.x % kJoinChannels, part = threadIdx.x / kJoinChannels;
+    const int c = blockIdx.x * kJoinChannels + cl;
+    const int span = (a.tiles + kJoinParts - 1) / kJoinParts;
+    const int t0 = min(part * span, a.tiles), t1 = min(t0 + span, a.tiles);
+    const auto tile = [&](int i) { return (int64_t)(BWD ? a.tiles - 1 - i : i) * a.c + c; };
+    Map m{1.f, 0.f};
+#pragma unroll 8
+    for (int i = t0; i < t1; ++i) m = then(m, a.tile_maps[tile(i)]);
+    int now = 0;
+    s[0][part][cl] = m;
+    __syncthreads();
+    for (int d = 1; d < kJoinParts; d *= 2) {
+        if (part >= d) m = then(s[now][part - d][cl], m);
+        now ^= 1;
+        s[now][part][cl] = m;
+        __syncthreads();
+    }
+    float h = part > 0 ? s[now][part - 1][cl].b : 0.f;  // all maps from the first visit on are constant
+#pragma unroll 8
+    for (int i = t0; i < t1; ++i) {
+        const int64_t at = tile(i);
+        const Map next = a.tile_maps[at];
+        a.states[at] = h;
+        h = through(next, h);
+    }
+}
+
+// What enters this warp's tokens.  One tile: from the maps that the block has found itself.  A few:
+// from the maps of all tiles before, a share of them to each warp.  Many: from k_scan_join.
+template <typename T, bool FREE, bool BWD>
+__device__ __forceinline__ typename Lane<T>::Num entering(const ScanArgs& a, const Place& p, int tile,
+                                                          Map (*s_maps)[32 * Lane<T>::V], CutSeqs& seqs) {
+    using L = Lane<T>;
+    constexpr int V = L::V;
+    const int warp = threadIdx.x >> 5, cl = (threadIdx.x & 31) * V;
+    Maps<V> all;
+    if (a.tiles == 1) {
+        store_maps<V>(&s_maps[warp][cl], warp_map<T, FREE, BWD>(a, p, seqs));
+        __syncthreads();
+        return through(before_warp<V>(s_maps, BWD, all), L::fill(0.f));
+    }
+    const Maps<V> mine = p.real ? load_maps<V>(a.warp_maps + ((int64_t)tile * kWarps + warp) * a.c + p.c) : no_change<V>();
+    if (a.tiles > kFoldTiles)
+        return through(mine, p.real ? L::load(a.states + (int64_t)tile * a.c + p.c) : L::fill(0.f));
+    const int before = BWD ? a.tiles - 1 - tile : tile, span = (before + kWarps - 1) / kWarps;
+    Maps<V> m = no_change<V>();
+    if (p.real) {
+#pragma unroll 4
+        for (int i = warp * span; i < min((warp + 1) * span, before); ++i)
+            m = then(m, load_maps<V>(a.tile_maps + (int64_t)(BWD ? a.tiles - 1 - i : i) * a.c + p.c));
+    }
+    store_maps<V>(&s_maps[warp][cl], m);
+    __syncthreads();
+    before_warp<V>(s_maps, false, all);
+    return through(mine, through(all, L::fill(0.f)));
+}
+
+// Blocks of step 3 come in the order opposite to step 1's.
+__device__ __forceinline__ bool bad_call(const ScanArgs& a) {
+    if (a.tiles > 1) return a.head[1] != 0;
+    const bool good = good_offsets(a);
+    if (!good && threadIdx.x == 0) atomicOr(a.head, kErrRange);
+    return !good;
+}
+
+// Step 3.
+template <typename T, bool FREE>
+__global__ void __launch_bounds__(kThreads, 3) k_scan_fwd(const ScanArgs a) {
+    using L = Lane<T>;
+    using N = typename L::Num;
+    using G = typename L::Gate;
+    __shared__ Map s_maps[kWarps][32 * L::V];
+    __shared__ CutSeqs s_seqs[kWarps];
+    if (bad_call(a)) return;
+    const int unit = gridDim.x - 1 - blockIdx.x;
+    const int tile = unit / a.blocks_c, block_c = unit - tile * a.blocks_c;
+    const Place p = place_of<L>(a, tile, block_c);
+    CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
+    N h = entering<T, FREE, false>(a, p, tile, s_maps, seqs);
+    const int at = p.real ? p.c * (int)sizeof(T) : 0;
+    const char* const gate = a.gate + at;
+    const char* const x = a.x + at;
+    char* const out = a.out + at;
+    Within within;
+#pragma unroll 1
+    for (int q = 0; q < kRuns; ++q) {
+        const Run r = run_of<L::V>(a, p, q, seqs, within, a.first, a.last);
+        if (a.carries && p.real && r.count > 0) L::store(a.carries + (int64_t)(r.lo / kTokens) * a.c + p.c, h);
+        if (r.simple) {
+            uint32_t gw[kTokens], xw[kTokens];
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k) {
+                const int32_t row = row_at(r, k);
+                gw[k] = word(gate, a.gate_s, row, p.real);
+                xw[k] = word(x, a.x_s, row, p.real);
+            }
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k) {
+                const int32_t row = row_at(r, k);
+                h = next_state<FREE>(G(G::hold(L::unpack(gw[k]))), L::unpack(xw[k]), h);
+                if (p.real) put<L>(out, row, a.out_s, h);
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < r.count; ++k) {
+                const int32_t row = row_at(r, k);
+                if (r.cuts.begin >> k & 1) h = state_of<L>(a, a.first, seqs.begin[k], p);
+                const G g(G::hold(L::unpack(word(gate, a.gate_s, row, p.real))));
+                h = next_state<FREE>(g, L::unpack(word(x, a.x_s, row, p.real)), h);
+                if (p.real && row >= 0) put<L>(out, row, a.out_s, h);
+                if (a.last && p.real && (r.cuts.end >> k & 1))
+                    L::store(a.last + (int64_t)seqs.end(r.cuts, k) * a.c + p.c, h);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// The gradients, from the last run to the first; the states of a run's tokens are found again from the
+// one that the forward pass kept at its beginning.
+template <typename T, bool FREE>
+__global__ void __launch_bounds__(kThreads, 2) k_scan_bwd(const ScanArgs a) {
+    using L = Lane<T>;
+    using N = typename L::Num;
+    using G = typename L::Gate;
+    __shared__ Map s_maps[kWarps][32 * L::V];
+    __shared__ CutSeqs s_seqs[kWarps];
+    if (bad_call(a)) return;
+    const int unit = gridDim.x - 1 - blockIdx.x;
+    const int tile = unit / a.blocks_c, block_c = unit - tile * a.blocks_c;
+    const Place p = place_of<L>(a, tile, block_c);
+    CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
+    N mu = entering<T, FREE, true>(a, p, tile, s_maps, seqs);
+    const int at = p.real ? p.c * (int)sizeof(T) : 0;
+    const char* const gate = a.gate + at;
+    const char* const x = a.x + at;
+    const char* const gy = a.gy + at;
+    char* const gg = a.gg + at;
+    char* const gx = a.out + at;
+    // a token's gradients; turn: a (1 - a) (h_{t-1} - x)
+    const auto gradients = [&](const G& g, N y, N turn, N& dg, N& dx) {
+        const N lam = add_(mu, y);
+        dg = mul_(turn, lam);
+        dx = FREE ? lam : mul_(g.rest(), lam);
+        mu = g.kept(lam);
+    };
+    Within within;
+#pragma unroll 1
+    for (int q = kRuns - 1; q >= 0; --q) {
+        const Run r = run_of<L::V>(a, p, q, seqs, within, a.glast, a.gfirst);
+        N state = L::fill(0.f);
+        if (p.real && r.count > 0) state = L::load(a.carries + (int64_t)(r.lo / kTokens) * a.c + p.c);
+        if (r.simple) {
+            typename G::Held held[kTokens];
+            N turn[kTokens];
+            uint32_t gw[kTokens], xw[kTokens], yw[kTokens];
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k) {
+                const int32_t row = row_at(r, k);
+                gw[k] = word(gate, a.gate_s, row, p.real);
+                xw[k] = word(x, a.x_s, row, p.real);
+                yw[k] = word(gy, a.gy_s, row, p.real);
+            }
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k) {
+                const N v = L::unpack(xw[k]);
+                held[k] = G::hold(L::unpack(gw[k]), turn[k]);
+                turn[k] = mul_(turn[k], FREE ? state : sub_(state, v));
+                state = next_state<FREE>(G(held[k]), v, state);
+            }
+#pragma unroll
+            for (int k = kTokens - 1; k >= 0; --k) {
+                const int32_t row = row_at(r, k);
+                N dg, dx;
+                gradients(G(held[k]), L::unpack(yw[k]), turn[k], dg, dx);
+                if (p.real) {
+                    put<L>(gg, row, a.gg_s, dg);
+                    put<L>(gx, row, a.out_s, dx);
+                }
+            }
+        } else {
+            // the state before a token is found from the run's first one, or the last beginning, each time
+#pragma unroll 1
+            for (int k = r.count - 1; k >= 0; --k) {
+                N before = state;
+                int from = 0;
+                const uint32_t until = r.cuts.begin & ((2u << k) - 1);
+                if (until) {
+                    from = 31 - __clz(until);
+                    before = state_of<L>(a, a.first, seqs.begin[from], p);
+                }
+#pragma unroll 1
+                for (int i = from; i < k; ++i) {
+                    const int32_t row = row_at(r, i);
+                    before = next_state<FREE>(G(G::hold(L::unpack(word(gate, a.gate_s, row, p.real)))),
+                                              L::unpack(word(x, a.x_s, row, p.real)), before);
+                }
+                if (r.cuts.end >> k & 1) mu = state_of<L>(a, a.glast, seqs.end(r.cuts, k), p);
+                const int32_t row = row_at(r, k);
+                N dg, dx, turn;
+                const G g(G::hold(L::unpack(word(gate, a.gate_s, row, p.real)), turn));
+                turn = mul_(turn, FREE ? before : sub_(before, L::unpack(word(x, a.x_s, row, p.real))));
+                gradients(g, L::unpack(word(gy, a.gy_s, row, p.real)), turn, dg, dx);
+                if (p.real && row >= 0) {
+                    put<L>(gg, row, a.gg_s, dg);
+                    put<L>(gx, row, a.out_s, dx);
+                }
+                if (a.gfirst && p.real && (r.cuts.begin >> k & 1))
+                    L::store(a.gfirst + (int64_t)seqs.begin[k] * a.c + p.c, mu);
+            }
+        }
+        __syncwarp();
     }
 }
 
@@ -843,7 +735,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(int64_t vectors, int per
                                                         int64_t gate_s, const char* x, int64_t x_s, float* state,
                                                         char* out, int64_t out_s) {
     using L = Lane<T>;
-    using G = Side<typename L::Num>;
+    using G = typename L::Gate;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < vectors; i += (int64_t)gridDim.x * kThreads) {
         const int64_t r = i / per_row;
         const int at = (int)(i - r * per_row);
@@ -868,40 +760,36 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(int64_t vectors, int per
     }
 }
 
-Tree tree_of(int64_t n, int c, int64_t* words) {
-    Tree t{};
-    t.tiles = std::max<int64_t>(1, (n + kTile - 1) / kTile);
-    int64_t at = 0;
-    for (t.levels = 0; t.levels < kMaxLevels; ++t.levels) {
-        if (t.levels > 0 && ((t.tiles - 1) >> (kFan * t.levels)) == 0) break;
-        t.base[t.levels] = at;
-        at += ((t.tiles - 1) >> (kFan * t.levels)) * c + c;
-    }
-    *words = t.tiles > 1 ? at : 0;
-    return t;
-}
+int64_t tiles_of(int64_t n) { return std::max<int64_t>(1, (n + kTile - 1) / kTile); }
 
-template <typename T>
-int launch(const ScanArgs& a, bool bwd, int sms, cudaStream_t s) {
-    constexpr int CH = 32 * Lane<T>::V;
-    const size_t maps = bwd ? Joint<CH, true>::bytes(a.tree.levels) : Joint<CH, false>::bytes(a.tree.levels);
-    const size_t smem = 6 * (size_t)kTileBytes + maps;
-    static_assert(kFwdStages * 2 == 6, "as many operands' tiles as two backward stages");
-    auto kernel = a.free_input ? (bwd ? k_scan_bwd<T, true> : k_scan_fwd<T, true>)
-                               : (bwd ? k_scan_bwd<T, false> : k_scan_fwd<T, false>);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return VG_ERR_CUDA;
-    const int grid = a.tree.tiles == 1 ? (int)a.units : (int)std::min<int64_t>(a.units, (int64_t)sms * kBlocksPerSm);
-    kernel<<<grid, kThreads, smem, s>>>(a);
+template <typename T, bool FREE, bool BWD>
+int launch(const ScanArgs& a, cudaStream_t s) {
+    const unsigned grid = (unsigned)a.tiles * a.blocks_c;
+    if (a.tiles > 1) {
+        k_scan_map<T, FREE, BWD><<<grid, kThreads, 0, s>>>(a);
+        if (cudaPeekAtLastError() != cudaSuccess) return VG_ERR_CUDA;
+    }
+    if (a.tiles > kFoldTiles) {
+        k_scan_join<BWD><<<a.c / kJoinChannels, kJoinChannels * kJoinParts, 0, s>>>(a);
+        if (cudaPeekAtLastError() != cudaSuccess) return VG_ERR_CUDA;
+    }
+    if constexpr (BWD)
+        k_scan_bwd<T, FREE><<<grid, kThreads, 0, s>>>(a);
+    else
+        k_scan_fwd<T, FREE><<<grid, kThreads, 0, s>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+}
+template <typename T>
+int launch(const ScanArgs& a, bool free_input, bool bwd, cudaStream_t s) {
+    if (free_input) return bwd ? launch<T, true, true>(a, s) : launch<T, true, false>(a, s);
+    return bwd ? launch<T, false, true>(a, s) : launch<T, false, false>(a, s);
 }
 
 }  // namespace
 
 size_t gated_scan_workspace_bytes(int64_t n, int c) {
-    int64_t words;
-    tree_of(n, c, &words);
-    return align_up(256 + (size_t)words * 8, 256);
+    const int64_t tiles = tiles_of(n);
+    return align_up(256 + (tiles > 1 ? (size_t)tiles * c * ((1 + kWarps) * sizeof(Map) + sizeof(float)) : 0), 256);
 }
 
 int gated_scan(const GatedScan& q, bool bwd, cudaStream_t s) {
@@ -914,7 +802,6 @@ int gated_scan(const GatedScan& q, bool bwd, cudaStream_t s) {
     a.off = q.s->offsets;
     a.order = q.s->order;
     a.reverse = (q.s->flags & VG_SCAN_REVERSE) != 0;
-    a.free_input = (q.s->flags & VG_SCAN_FREE_INPUT) != 0;
     const auto in = [&](const vg_rows* r, const char** p, uint32_t* stride) {
         *p = r ? static_cast<const char*>(r->data) : nullptr;
         *stride = r && q.s->n > 1 ? (uint32_t)(r->row_stride * es) : 0;
@@ -934,19 +821,16 @@ int gated_scan(const GatedScan& q, bool bwd, cudaStream_t s) {
     a.carries = q.carries;
     a.gfirst = q.grad_first;
     a.head = reinterpret_cast<uint32_t*>(q.ws);
-    a.nodes = reinterpret_cast<uint64_t*>(q.ws + 256);
-    int64_t words;
-    a.tree = tree_of(a.n, a.c, &words);
-    if (a.tree.tiles * a.blocks_c >= (int64_t(1) << 31)) return VG_ERR_UNSUPPORTED;
-    a.units = (uint32_t)(a.tree.tiles * a.blocks_c);
-    if (a.tree.tiles > 1) {
-        const int64_t fill = std::max<int64_t>(1, std::min<int64_t>((words + 4095) / 4096, q.sms));
-        k_scan_begin<<<(unsigned)fill, 1024, 0, s>>>(a, words);
-        if (cudaPeekAtLastError() != cudaSuccess) return VG_ERR_CUDA;
-    }
-    return q.s->dtype == VG_F32   ? launch<float>(a, bwd, q.sms, s)
-           : q.s->dtype == VG_F16 ? launch<__half>(a, bwd, q.sms, s)
-                                  : launch<__nv_bfloat16>(a, bwd, q.sms, s);
+    const int64_t tiles = tiles_of(a.n);
+    if (tiles * a.blocks_c >= (int64_t(1) << 31)) return VG_ERR_UNSUPPORTED;
+    a.tiles = (int)tiles;
+    a.tile_maps = reinterpret_cast<Map*>(q.ws + 256);
+    a.warp_maps = a.tile_maps + tiles * a.c;
+    a.states = reinterpret_cast<float*>(a.warp_maps + tiles * kWarps * a.c);
+    const bool free_input = (q.s->flags & VG_SCAN_FREE_INPUT) != 0;
+    return q.s->dtype == VG_F32   ? launch<float>(a, free_input, bwd, s)
+           : q.s->dtype == VG_F16 ? launch<__half>(a, free_input, bwd, s)
+                                  : launch<__nv_bfloat16>(a, free_input, bwd, s);
 }
 
 int gated_scan_step(int64_t n, int c, int dtype, bool free_input, const vg_rows& gate, const vg_rows& x, float* state,

@@ -30,7 +30,7 @@ VG_NONE = 0xFFFFFFFF
 VG_TILE_ROWS = 128
 VG_ROPE_HALVES, VG_QK_NO_NORM, VG_QK_SHARED_WEIGHT = 0x200, 0x400, 0x800
 VG_ADAMW_BLOCK = 256
-VG_SCAN_REVERSE, VG_SCAN_FREE_INPUT = 0x1000, 0x2000
+VG_SCAN_REVERSE, VG_SCAN_FREE_INPUT, VG_SCAN_CARRY_ROWS = 0x1000, 0x2000, 16
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvoxelgemm.so")
 _lock = threading.Lock()
@@ -756,7 +756,7 @@ def _scan(gate, offsets, order, carries, ws, flags, what):
     (n, c), dt, dev = _matrix(gate, what)
     batch = offsets.numel() - 1
     f32 = torch.float32
-    rows = -(-n // 128)
+    rows = -(-n // VG_SCAN_CARRY_ROWS)
     return (ScanStruct(n, c, batch, _DT.get(dt, -1), flags, _flat(offsets, torch.int32, (batch + 1,), dev, "offsets"),
                        _flat(order, torch.int32, (n,), dev, "order")), (n, c), (batch, c), dt, dev,
             _flat(carries, f32, (rows, c), dev, "carries"))
