@@ -17,6 +17,8 @@
 // Where a sequence begins, the map is constant (A = -1 marks it, h -> B), so that nothing, not
 // even a NaN, passes from one sequence to the next.  A warp's tokens are the same for all of its
 // lanes, so such places cost a branch that no lane takes alone.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
@@ -33,6 +35,9 @@ constexpr int kTokens = kScanCarryRows;      // looked up and loaded at once; a 
 constexpr int kRuns = 4;                     // runs of a warp
 constexpr int kWarpTokens = kRuns * kTokens;
 constexpr int kTile = kWarps * kWarpTokens;  // tokens of a block
+constexpr int kRowBytes = 128, kRunBytes = kTokens * kRowBytes;  // of an operand in a block
+// Shared memory of a block: two runs of `operands` a warp.
+constexpr size_t stage_bytes(int operands) { return (size_t)kWarps * 2 * operands * kRunBytes; }
 constexpr int kFoldTiles = 64;               // up to so many, blocks join the maps before them themselves
 constexpr int kJoinChannels = 8, kJoinParts = 128;  // of a block of k_scan_join
 static_assert(kTokens == 16, "a lane holds the row of one token, half of the lanes none");
@@ -341,57 +346,100 @@ __device__ __forceinline__ Maps<2> maps_of(float2 a, float2 b, bool constant) {
 // ---------------------------------------------------------------- the tokens of a warp
 // What a lane of a warp knows of its place.
 struct Place {
-    int c;         // its first channel
-    bool real;     // there is such a channel
-    int32_t lo;    // the warp's first visit
-    int32_t rows[2];  // of the visits of this lane's number, and 32 further: -1 where there is none
+    int c;       // its first channel
+    bool real;   // there is such a channel
+    int32_t lo;  // the warp's first visit
 };
 template <typename L>
 __device__ __forceinline__ Place place_of(const ScanArgs& a, int tile, int block_c) {
     Place p;
-    const int lane = threadIdx.x & 31;
-    p.c = block_c * 32 * L::V + lane * L::V;
+    p.c = (block_c * 32 + (int)(threadIdx.x & 31)) * L::V;
     p.real = p.c < a.c;
     p.lo = (int32_t)min((int64_t)tile * kTile + (int)(threadIdx.x >> 5) * kWarpTokens, a.n);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t v = (int64_t)p.lo + i * 32 + lane;
-        p.rows[i] = -1;
-        if (v < a.n) {
-            const int64_t at = a.reverse ? a.n - 1 - v : v;
-            p.rows[i] = a.order ? a.order[at] : (int32_t)at;
-            if (p.rows[i] < 0 || p.rows[i] >= a.n) {
-                p.rows[i] = -1;
-                atomicOr(a.head, kErrRange);
-            }
-        }
-    }
     return p;
 }
-
+// The row of the token of this lane's number in run q, as the order names it (unchecked, so that
+// the load need not be waited for here).
+__device__ __forceinline__ int32_t row_of(const ScanArgs& a, const Place& p, int q) {
+    const int lane = threadIdx.x & 31;
+    const int64_t v = (int64_t)p.lo + q * kTokens + lane;
+    if (lane >= kTokens || q < 0 || q >= kRuns || v >= a.n) return -1;
+    const int64_t at = a.reverse ? a.n - 1 - v : v;
+    return a.order ? a.order[at] : (int32_t)at;
+}
 // A run of the warp's tokens.
 struct Run {
     int32_t lo, count;
-    int32_t row;   // of the token of this lane's number, up to kTokens
+    int32_t row;   // of the token of this lane's number, -1 where there is none
     Cuts cuts;
     bool simple;   // all tokens there, nothing begins or ends among them
 };
-template <int V>
-__device__ __forceinline__ Run run_of(const ScanArgs& a, const Place& p, int q, CutSeqs& seqs, Within& within,
-                                      const float* in, float* out) {
-    Run r;
+
+// Copy a run's channels of P operands, [kTokens][128 bytes] each, into a stage; zeros where there is
+// no row or channel.  16 bytes a lane, 8 lanes a token.
+template <typename T, int P>
+__device__ __forceinline__ void fetch(const ScanArgs& a, const char* const (&from)[P], const uint32_t (&stride)[P],
+                                      uint32_t to, int32_t row, int first_channel) {
     const int lane = threadIdx.x & 31;
-    r.lo = (int32_t)min((int64_t)p.lo + q * kTokens, a.n);
-    r.count = min(kTokens, (int32_t)a.n - r.lo);
-    r.row = __shfl_sync(0xffffffffu, q < 2 ? p.rows[0] : p.rows[1], (q & 1) * kTokens + (lane & (kTokens - 1)));
-    r.cuts = find_cuts<V>(a, seqs, within, r.lo, r.count, p.c, in, out);
-    r.simple = r.count == kTokens && (r.cuts.begin | r.cuts.end) == 0 && __all_sync(0xffffffffu, r.row >= 0);
-    return r;
+    const int at = first_channel * (int)sizeof(T) + (lane & 7) * 16;
+    const bool inside = at < a.c * (int)sizeof(T);
+    to += lane * 16;
+#pragma unroll
+    for (int i = 0; i < kTokens / 4; ++i) {
+        const int32_t r = __shfl_sync(0xffffffffu, row, i * 4 + (lane >> 3));
+        const bool have = inside && r >= 0;
+        const uint64_t rr = have ? (uint32_t)r : 0u;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            cp_async16(to + p * kRunBytes + i * 512, from[p] + (inside ? at : 0) + rr * stride[p], have ? 16 : 0);
+    }
 }
-// A token's word of an operand; zero where there is no row or channel.
-__device__ __forceinline__ uint32_t word(const char* base, uint32_t stride, int32_t row, bool real) {
-    return real && row >= 0 ? *reinterpret_cast<const uint32_t*>(base + (uint64_t)(uint32_t)row * stride) : 0u;
+
+// Go through a warp's runs, DOWN from the last: `use(run, words)` with the run's tokens of the first
+// operand at words[k * kStep], the next operand's kRunBytes further, while the next run's are on their way.
+template <typename T, int P, bool DOWN, typename Use>
+__device__ __forceinline__ void for_runs(const ScanArgs& a, const Place& p, const char* const (&from)[P],
+                                         const uint32_t (&stride)[P], char* s_stages, CutSeqs& seqs, const float* in,
+                                         float* out, const Use& use) {
+    constexpr int V = Lane<T>::V;
+    const int lane = threadIdx.x & 31;
+    const uint32_t stages = smem_u32(s_stages);
+    const auto run = [](int i) { return DOWN ? kRuns - 1 - i : i; };
+    const auto check = [&](int32_t row, int i) {
+        const int64_t v = (int64_t)p.lo + run(i) * kTokens + lane;
+        if (i < kRuns && lane < kTokens && v < a.n && (row < 0 || row >= a.n)) {
+            atomicOr(a.head, kErrRange);
+            return -1;
+        }
+        return row;
+    };
+    Within within;
+    int32_t row = check(row_of(a, p, run(0)), 0), next = row_of(a, p, run(1));
+    fetch<T, P>(a, from, stride, stages, row, p.c - lane * V);
+    cp_async_commit();
+#pragma unroll 1
+    for (int i = 0; i < kRuns; ++i) {
+        const int32_t later = i + 2 < kRuns ? row_of(a, p, run(i + 2)) : -1;
+        next = check(next, i + 1);
+        if (i + 1 < kRuns) fetch<T, P>(a, from, stride, stages + ((i + 1) & 1) * P * kRunBytes, next, p.c - lane * V);
+        cp_async_commit();
+        Run r;
+        r.lo = (int32_t)min((int64_t)p.lo + run(i) * kTokens, a.n);
+        r.count = min(kTokens, (int32_t)a.n - r.lo);
+        r.row = row;
+        r.cuts = find_cuts<V>(a, seqs, within, r.lo, r.count, p.c, in, out);
+        r.simple = r.count == kTokens && (r.cuts.begin | r.cuts.end) == 0 &&
+                   __all_sync(0xffffffffu, row >= 0 || lane >= kTokens);
+        cp_async_wait<1>();
+        __syncwarp();
+        use(r, reinterpret_cast<const uint32_t*>(s_stages + (i & 1) * P * kRunBytes) + lane);
+        __syncwarp();
+        row = next;
+        next = later;
+    }
 }
+constexpr int kStep = kRowBytes / 4, kOperand = kRunBytes / 4;  // words from a token, an operand to the next
+
 template <typename L>
 __device__ __forceinline__ void put(char* base, int32_t row, uint32_t stride, typename L::Num x) {
     *reinterpret_cast<uint32_t*>(base + (uint64_t)(uint32_t)row * stride) = L::pack(x);
@@ -405,53 +453,37 @@ __device__ __forceinline__ typename L::Num state_of(const ScanArgs& a, const flo
 
 // The map of a warp's tokens: of the state along the visits, or (BWD) of the gradient against them.
 template <typename T, bool FREE, bool BWD>
-__device__ __forceinline__ Maps<Lane<T>::V> warp_map(const ScanArgs& a, const Place& p, CutSeqs& seqs) {
+__device__ __forceinline__ Maps<Lane<T>::V> warp_map(const ScanArgs& a, const Place& p, char* s_stages,
+                                                     CutSeqs& seqs) {
     using L = Lane<T>;
     using N = typename L::Num;
     using G = typename L::Gate;
-    Within within;
-    const int at = p.real ? p.c * (int)sizeof(T) : 0;
-    const char* const gate = a.gate + at;
-    const char* const x = (BWD ? a.gy : a.x) + at;
-    const uint32_t xs = BWD ? a.gy_s : a.x_s;
     N A = L::fill(1.f), B = L::fill(0.f);
     bool constant = false;
-#pragma unroll 1
-    for (int i = 0; i < kRuns; ++i) {
-        const int q = BWD ? kRuns - 1 - i : i;
-        const Run r = run_of<L::V>(a, p, q, seqs, within, nullptr, nullptr);
-        if (r.simple) {
-            uint32_t gw[kTokens], xw[kTokens];
+    const auto go = [&](auto simple, const Run& r, const uint32_t* w) {
+        const uint32_t resets = BWD ? r.cuts.end : r.cuts.begin;
 #pragma unroll
-            for (int k = 0; k < kTokens; ++k) {
-                const int32_t row = row_at(r, k);
-                gw[k] = word(gate, a.gate_s, row, p.real);
-                xw[k] = word(x, xs, row, p.real);
-            }
-#pragma unroll
-            for (int j = 0; j < kTokens; ++j) {
-                const int k = BWD ? kTokens - 1 - j : j;
-                const G g(G::hold(L::unpack(gw[k])));
-                B = BWD ? g.kept(add_(B, L::unpack(xw[k]))) : next_state<FREE>(g, L::unpack(xw[k]), B);
-                A = g.kept(A);
-            }
-        } else {
-            const uint32_t resets = BWD ? r.cuts.end : r.cuts.begin;
-            constant |= resets != 0;
-#pragma unroll 1
-            for (int j = 0; j < r.count; ++j) {
-                const int k = BWD ? r.count - 1 - j : j;
-                const int32_t row = row_at(r, k);
-                const G g(G::hold(L::unpack(word(gate, a.gate_s, row, p.real))));
-                const N v = L::unpack(word(x, xs, row, p.real));
-                if (resets >> k & 1)
+        for (int j = 0; j < kTokens; ++j) {
+            const int k = BWD ? kTokens - 1 - j : j;
+            if (simple || k < r.count) {
+                const G g(G::hold(L::unpack(w[k * kStep])));
+                const N v = L::unpack(w[kOperand + k * kStep]);
+                if (!simple && (resets >> k & 1))
                     B = BWD ? state_of<L>(a, a.glast, seqs.end(r.cuts, k), p) : state_of<L>(a, a.first, seqs.begin[k], p);
                 B = BWD ? g.kept(add_(B, v)) : next_state<FREE>(g, v, B);
                 A = g.kept(A);
             }
         }
-        __syncwarp();
-    }
+        constant |= resets != 0;
+    };
+    const char* const from[2] = {a.gate, BWD ? a.gy : a.x};
+    const uint32_t stride[2] = {a.gate_s, BWD ? a.gy_s : a.x_s};
+    for_runs<T, 2, BWD>(a, p, from, stride, s_stages, seqs, nullptr, nullptr, [&](const Run& r, const uint32_t* w) {
+        if (r.simple)
+            go(std::true_type{}, r, w);
+        else
+            go(std::false_type{}, r, w);
+    });
     return maps_of(A, B, constant);
 }
 
@@ -489,10 +521,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_scan_map(const ScanArgs a) {
     constexpr int V = L::V;
     __shared__ Map s_maps[kWarps][32 * V];
     __shared__ CutSeqs s_seqs[kWarps];
+    extern __shared__ __align__(128) char s_dyn[];  // [warps][2 stages][operands][tokens][128 bytes]
     const int warp = threadIdx.x >> 5, cl = (threadIdx.x & 31) * V;
     const int tile = blockIdx.x / a.blocks_c, block_c = blockIdx.x - tile * a.blocks_c;
     const Place p = place_of<L>(a, tile, block_c);
-    store_maps<V>(&s_maps[warp][cl], warp_map<T, FREE, BWD>(a, p, s_seqs[warp]));
+    store_maps<V>(&s_maps[warp][cl], warp_map<T, FREE, BWD>(a, p, s_dyn + warp * 4 * kRunBytes, s_seqs[warp]));
     __syncthreads();
     Maps<V> all;
     const Maps<V> mine = before_warp<V>(s_maps, BWD, all);
@@ -545,13 +578,14 @@ __global__ void __launch_bounds__(kJoinChannels* kJoinParts) k_scan_join(const S
 // from the maps of all tiles before, a share of them to each warp.  Many: from k_scan_join.
 template <typename T, bool FREE, bool BWD>
 __device__ __forceinline__ typename Lane<T>::Num entering(const ScanArgs& a, const Place& p, int tile,
-                                                          Map (*s_maps)[32 * Lane<T>::V], CutSeqs& seqs) {
+                                                          Map (*s_maps)[32 * Lane<T>::V], char* s_stages,
+                                                          CutSeqs& seqs) {
     using L = Lane<T>;
     constexpr int V = L::V;
     const int warp = threadIdx.x >> 5, cl = (threadIdx.x & 31) * V;
     Maps<V> all;
     if (a.tiles == 1) {
-        store_maps<V>(&s_maps[warp][cl], warp_map<T, FREE, BWD>(a, p, seqs));
+        store_maps<V>(&s_maps[warp][cl], warp_map<T, FREE, BWD>(a, p, s_stages, seqs));
         __syncthreads();
         return through(before_warp<V>(s_maps, BWD, all), L::fill(0.f));
     }
@@ -587,49 +621,37 @@ __global__ void __launch_bounds__(kThreads, 3) k_scan_fwd(const ScanArgs a) {
     using G = typename L::Gate;
     __shared__ Map s_maps[kWarps][32 * L::V];
     __shared__ CutSeqs s_seqs[kWarps];
+    extern __shared__ __align__(128) char s_dyn[];
     if (bad_call(a)) return;
     const int unit = gridDim.x - 1 - blockIdx.x;
     const int tile = unit / a.blocks_c, block_c = unit - tile * a.blocks_c;
     const Place p = place_of<L>(a, tile, block_c);
     CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
-    N h = entering<T, FREE, false>(a, p, tile, s_maps, seqs);
-    const int at = p.real ? p.c * (int)sizeof(T) : 0;
-    const char* const gate = a.gate + at;
-    const char* const x = a.x + at;
-    char* const out = a.out + at;
-    Within within;
-#pragma unroll 1
-    for (int q = 0; q < kRuns; ++q) {
-        const Run r = run_of<L::V>(a, p, q, seqs, within, a.first, a.last);
-        if (a.carries && p.real && r.count > 0) L::store(a.carries + (int64_t)(r.lo / kTokens) * a.c + p.c, h);
-        if (r.simple) {
-            uint32_t gw[kTokens], xw[kTokens];
+    char* const s_stages = s_dyn + (threadIdx.x >> 5) * 4 * kRunBytes;
+    N h = entering<T, FREE, false>(a, p, tile, s_maps, s_stages, seqs);
+    char* const out = a.out + p.c * (int)sizeof(T);
+    const auto go = [&](auto simple, const Run& r, const uint32_t* w) {
 #pragma unroll
-            for (int k = 0; k < kTokens; ++k) {
-                const int32_t row = row_at(r, k);
-                gw[k] = word(gate, a.gate_s, row, p.real);
-                xw[k] = word(x, a.x_s, row, p.real);
-            }
-#pragma unroll
-            for (int k = 0; k < kTokens; ++k) {
-                const int32_t row = row_at(r, k);
-                h = next_state<FREE>(G(G::hold(L::unpack(gw[k]))), L::unpack(xw[k]), h);
-                if (p.real) put<L>(out, row, a.out_s, h);
-            }
-        } else {
-#pragma unroll 1
-            for (int k = 0; k < r.count; ++k) {
-                const int32_t row = row_at(r, k);
-                if (r.cuts.begin >> k & 1) h = state_of<L>(a, a.first, seqs.begin[k], p);
-                const G g(G::hold(L::unpack(word(gate, a.gate_s, row, p.real))));
-                h = next_state<FREE>(g, L::unpack(word(x, a.x_s, row, p.real)), h);
-                if (p.real && row >= 0) put<L>(out, row, a.out_s, h);
-                if (a.last && p.real && (r.cuts.end >> k & 1))
+        for (int k = 0; k < kTokens; ++k) {
+            const int32_t row = row_at(r, k);
+            if (simple || k < r.count) {
+                if (!simple && (r.cuts.begin >> k & 1)) h = state_of<L>(a, a.first, seqs.begin[k], p);
+                h = next_state<FREE>(G(G::hold(L::unpack(w[k * kStep]))), L::unpack(w[kOperand + k * kStep]), h);
+                if (p.real && (simple || row >= 0)) put<L>(out, row, a.out_s, h);
+                if (!simple && a.last && p.real && (r.cuts.end >> k & 1))
                     L::store(a.last + (int64_t)seqs.end(r.cuts, k) * a.c + p.c, h);
             }
         }
-        __syncwarp();
-    }
+    };
+    const char* const from[2] = {a.gate, a.x};
+    const uint32_t stride[2] = {a.gate_s, a.x_s};
+    for_runs<T, 2, false>(a, p, from, stride, s_stages, seqs, a.first, a.last, [&](const Run& r, const uint32_t* w) {
+        if (a.carries && p.real && r.count > 0) L::store(a.carries + (int64_t)(r.lo / kTokens) * a.c + p.c, h);
+        if (r.simple)
+            go(std::true_type{}, r, w);
+        else
+            go(std::false_type{}, r, w);
+    });
 }
 
 // The gradients, from the last run to the first; the states of a run's tokens are found again from the
@@ -641,92 +663,57 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_bwd(const ScanArgs a) {
     using G = typename L::Gate;
     __shared__ Map s_maps[kWarps][32 * L::V];
     __shared__ CutSeqs s_seqs[kWarps];
+    extern __shared__ __align__(128) char s_dyn[];
     if (bad_call(a)) return;
     const int unit = gridDim.x - 1 - blockIdx.x;
     const int tile = unit / a.blocks_c, block_c = unit - tile * a.blocks_c;
     const Place p = place_of<L>(a, tile, block_c);
     CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
-    N mu = entering<T, FREE, true>(a, p, tile, s_maps, seqs);
-    const int at = p.real ? p.c * (int)sizeof(T) : 0;
-    const char* const gate = a.gate + at;
-    const char* const x = a.x + at;
-    const char* const gy = a.gy + at;
-    char* const gg = a.gg + at;
-    char* const gx = a.out + at;
-    // a token's gradients; turn: a (1 - a) (h_{t-1} - x)
-    const auto gradients = [&](const G& g, N y, N turn, N& dg, N& dx) {
-        const N lam = add_(mu, y);
-        dg = mul_(turn, lam);
-        dx = FREE ? lam : mul_(g.rest(), lam);
-        mu = g.kept(lam);
-    };
-    Within within;
-#pragma unroll 1
-    for (int q = kRuns - 1; q >= 0; --q) {
-        const Run r = run_of<L::V>(a, p, q, seqs, within, a.glast, a.gfirst);
-        N state = L::fill(0.f);
-        if (p.real && r.count > 0) state = L::load(a.carries + (int64_t)(r.lo / kTokens) * a.c + p.c);
-        if (r.simple) {
-            typename G::Held held[kTokens];
-            N turn[kTokens];
-            uint32_t gw[kTokens], xw[kTokens], yw[kTokens];
+    char* const s_stages = s_dyn + (threadIdx.x >> 5) * 6 * kRunBytes;
+    N mu = entering<T, FREE, true>(a, p, tile, s_maps, s_stages, seqs);
+    char* const gg = a.gg + p.c * (int)sizeof(T);
+    char* const gx = a.out + p.c * (int)sizeof(T);
+    const auto go = [&](auto simple, const Run& r, const uint32_t* w, N state) {
+        typename G::Held held[kTokens];
+        N turn[kTokens];  // a (1 - a) (h_{t-1} - x)
 #pragma unroll
-            for (int k = 0; k < kTokens; ++k) {
-                const int32_t row = row_at(r, k);
-                gw[k] = word(gate, a.gate_s, row, p.real);
-                xw[k] = word(x, a.x_s, row, p.real);
-                yw[k] = word(gy, a.gy_s, row, p.real);
+        for (int k = 0; k < kTokens; ++k) {
+            if (simple || k < r.count) {
+                if (!simple && (r.cuts.begin >> k & 1)) state = state_of<L>(a, a.first, seqs.begin[k], p);
+                const N x = L::unpack(w[kOperand + k * kStep]);
+                held[k] = G::hold(L::unpack(w[k * kStep]), turn[k]);
+                turn[k] = mul_(turn[k], FREE ? state : sub_(state, x));
+                state = next_state<FREE>(G(held[k]), x, state);
             }
+        }
 #pragma unroll
-            for (int k = 0; k < kTokens; ++k) {
-                const N v = L::unpack(xw[k]);
-                held[k] = G::hold(L::unpack(gw[k]), turn[k]);
-                turn[k] = mul_(turn[k], FREE ? state : sub_(state, v));
-                state = next_state<FREE>(G(held[k]), v, state);
-            }
-#pragma unroll
-            for (int k = kTokens - 1; k >= 0; --k) {
-                const int32_t row = row_at(r, k);
-                N dg, dx;
-                gradients(G(held[k]), L::unpack(yw[k]), turn[k], dg, dx);
-                if (p.real) {
+        for (int k = kTokens - 1; k >= 0; --k) {
+            const int32_t row = row_at(r, k);
+            if (simple || k < r.count) {
+                if (!simple && (r.cuts.end >> k & 1)) mu = state_of<L>(a, a.glast, seqs.end(r.cuts, k), p);
+                const G g(held[k]);
+                const N lam = add_(mu, L::unpack(w[2 * kOperand + k * kStep]));
+                const N dg = mul_(turn[k], lam), dx = FREE ? lam : mul_(g.rest(), lam);
+                mu = g.kept(lam);
+                if (p.real && (simple || row >= 0)) {
                     put<L>(gg, row, a.gg_s, dg);
                     put<L>(gx, row, a.out_s, dx);
                 }
-            }
-        } else {
-            // the state before a token is found from the run's first one, or the last beginning, each time
-#pragma unroll 1
-            for (int k = r.count - 1; k >= 0; --k) {
-                N before = state;
-                int from = 0;
-                const uint32_t until = r.cuts.begin & ((2u << k) - 1);
-                if (until) {
-                    from = 31 - __clz(until);
-                    before = state_of<L>(a, a.first, seqs.begin[from], p);
-                }
-#pragma unroll 1
-                for (int i = from; i < k; ++i) {
-                    const int32_t row = row_at(r, i);
-                    before = next_state<FREE>(G(G::hold(L::unpack(word(gate, a.gate_s, row, p.real)))),
-                                              L::unpack(word(x, a.x_s, row, p.real)), before);
-                }
-                if (r.cuts.end >> k & 1) mu = state_of<L>(a, a.glast, seqs.end(r.cuts, k), p);
-                const int32_t row = row_at(r, k);
-                N dg, dx, turn;
-                const G g(G::hold(L::unpack(word(gate, a.gate_s, row, p.real)), turn));
-                turn = mul_(turn, FREE ? before : sub_(before, L::unpack(word(x, a.x_s, row, p.real))));
-                gradients(g, L::unpack(word(gy, a.gy_s, row, p.real)), turn, dg, dx);
-                if (p.real && row >= 0) {
-                    put<L>(gg, row, a.gg_s, dg);
-                    put<L>(gx, row, a.out_s, dx);
-                }
-                if (a.gfirst && p.real && (r.cuts.begin >> k & 1))
+                if (!simple && a.gfirst && p.real && (r.cuts.begin >> k & 1))
                     L::store(a.gfirst + (int64_t)seqs.begin[k] * a.c + p.c, mu);
             }
         }
-        __syncwarp();
-    }
+    };
+    const char* const from[3] = {a.gate, a.x, a.gy};
+    const uint32_t stride[3] = {a.gate_s, a.x_s, a.gy_s};
+    for_runs<T, 3, true>(a, p, from, stride, s_stages, seqs, a.glast, a.gfirst, [&](const Run& r, const uint32_t* w) {
+        N state = L::fill(0.f);
+        if (p.real && r.count > 0) state = L::load(a.carries + (int64_t)(r.lo / kTokens) * a.c + p.c);
+        if (r.simple)
+            go(std::true_type{}, r, w, state);
+        else
+            go(std::false_type{}, r, w, state);
+    });
 }
 
 // 16 bytes of a lane's channels.
@@ -762,21 +749,26 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(int64_t vectors, int per
 
 int64_t tiles_of(int64_t n) { return std::max<int64_t>(1, (n + kTile - 1) / kTile); }
 
+template <typename K>
+bool allow(K kernel, size_t smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+}
 template <typename T, bool FREE, bool BWD>
 int launch(const ScanArgs& a, cudaStream_t s) {
     const unsigned grid = (unsigned)a.tiles * a.blocks_c;
     if (a.tiles > 1) {
-        k_scan_map<T, FREE, BWD><<<grid, kThreads, 0, s>>>(a);
+        const auto kernel = k_scan_map<T, FREE, BWD>;
+        if (!allow(kernel, stage_bytes(2))) return VG_ERR_CUDA;
+        kernel<<<grid, kThreads, stage_bytes(2), s>>>(a);
         if (cudaPeekAtLastError() != cudaSuccess) return VG_ERR_CUDA;
     }
     if (a.tiles > kFoldTiles) {
         k_scan_join<BWD><<<a.c / kJoinChannels, kJoinChannels * kJoinParts, 0, s>>>(a);
         if (cudaPeekAtLastError() != cudaSuccess) return VG_ERR_CUDA;
     }
-    if constexpr (BWD)
-        k_scan_bwd<T, FREE><<<grid, kThreads, 0, s>>>(a);
-    else
-        k_scan_fwd<T, FREE><<<grid, kThreads, 0, s>>>(a);
+    const auto kernel = BWD ? k_scan_bwd<T, FREE> : k_scan_fwd<T, FREE>;
+    if (!allow(kernel, stage_bytes(BWD ? 3 : 2))) return VG_ERR_CUDA;
+    kernel<<<grid, kThreads, stage_bytes(BWD ? 3 : 2), s>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 template <typename T>
