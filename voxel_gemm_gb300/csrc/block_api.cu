@@ -105,7 +105,7 @@ int check_scan(const vg_scan* s, const vg_rows* gate, const vg_rows* x, const fl
     if ((st = check_rows(gate, s->n, s->channels, s->dtype)) != VG_OK) return st;
     if ((st = check_rows(x, s->n, s->channels, s->dtype)) != VG_OK) return st;
     if (!ws || misaligned(ws, 256)) return VG_ERR_INVALID_ARG;
-    return ws_bytes < gated_scan_workspace_bytes(s->n, s->channels) ? VG_ERR_WORKSPACE_TOO_SMALL : VG_OK;
+    return ws_bytes < gated_scan_workspace_bytes(s->n, s->channels, s->dtype, plan_sms(0)) ? VG_ERR_WORKSPACE_TOO_SMALL : VG_OK;
 }
 
 int check_dropout(int64_t n, int dtype, const void* x, double p, const uint64_t* rng, const void* out) {
@@ -400,7 +400,7 @@ int vg_layer_norm_bwd(int64_t N, int C, int dtype, const vg_rows* x, const void*
 }
 
 size_t vg_gated_scan_workspace_bytes(const vg_scan* s) {
-    return check_scan_shape(s) == VG_OK ? gated_scan_workspace_bytes(s->n, s->channels) : 0;
+    return check_scan_shape(s) == VG_OK ? gated_scan_workspace_bytes(s->n, s->channels, s->dtype, plan_sms(0)) : 0;
 }
 
 int64_t vg_gated_scan_carry_rows(int64_t n) { return n > 0 ? (n + kScanCarryRows - 1) / kScanCarryRows : 0; }
@@ -420,6 +420,7 @@ int vg_gated_scan_fwd(const vg_scan* s, const vg_rows* gate, const vg_rows* x, c
     g.last = last;
     g.carries = carries;
     g.ws = static_cast<char*>(ws);
+    g.sms = plan_sms(0);
     return gated_scan(g, false, static_cast<cudaStream_t>(stream));
 }
 
@@ -445,6 +446,7 @@ int vg_gated_scan_bwd(const vg_scan* s, const vg_rows* gate, const vg_rows* x, c
     g.out = grad_x;
     g.grad_first = grad_first;
     g.ws = static_cast<char*>(ws);
+    g.sms = plan_sms(0);
     return gated_scan(g, true, static_cast<cudaStream_t>(stream));
 }
 

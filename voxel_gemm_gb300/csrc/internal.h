@@ -209,9 +209,10 @@ struct GatedScan {
     const float *first, *grad_last;
     float *last, *carries, *grad_first;
     char* ws;
+    int sms;
 };
 constexpr int kScanCarryRows = 16;
-size_t gated_scan_workspace_bytes(int64_t n, int c);
+size_t gated_scan_workspace_bytes(int64_t n, int c, int dtype, int sms);
 int gated_scan(const GatedScan& g, bool bwd, cudaStream_t s);
 int gated_scan_step(int64_t n, int c, int dtype, bool free_input, const vg_rows& gate, const vg_rows& x, float* state,
                     const vg_rows& out, cudaStream_t s);

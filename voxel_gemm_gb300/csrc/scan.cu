@@ -32,13 +32,13 @@ using namespace ptx;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = kScanCarryRows;      // looked up and loaded at once; a state is kept for each such run
-constexpr int kRuns = 4;                     // runs of a warp
-constexpr int kWarpTokens = kRuns * kTokens;
-constexpr int kTile = kWarps * kWarpTokens;  // tokens of a block
+constexpr int kHalf = kTokens / 2;
+constexpr int kMaxRuns = 4;                  // runs of a warp (ScanArgs::runs: 1, 2 or 4)
 constexpr int kRowBytes = 128, kRunBytes = kTokens * kRowBytes;  // of an operand in a block
+constexpr int kStep = kRowBytes / 4, kOperand = kRunBytes / 4;  // words from a token, an operand to the next
 // Shared memory of a block: two runs of `operands` a warp.
 constexpr size_t stage_bytes(int operands) { return (size_t)kWarps * 2 * operands * kRunBytes; }
-constexpr int kFoldTiles = 64;               // up to so many, blocks join the maps before them themselves
+constexpr int kFoldTiles = 256;              // up to so many, blocks join the maps before them themselves
 constexpr int kJoinChannels = 8, kJoinParts = 128;  // of a block of k_scan_join
 static_assert(kTokens == 16, "a lane holds the row of one token, half of the lanes none");
 
@@ -52,7 +52,7 @@ struct Map {
 struct ScanArgs {
     int64_t n;
     int c, batch, blocks_c;    // blocks_c: blocks of channels
-    int tiles;
+    int tiles, runs;           // tiles of kWarps * runs * kTokens tokens
     const int32_t* off;
     const int32_t* order;
     int reverse;
@@ -355,7 +355,7 @@ __device__ __forceinline__ Place place_of(const ScanArgs& a, int tile, int block
     Place p;
     p.c = (block_c * 32 + (int)(threadIdx.x & 31)) * L::V;
     p.real = p.c < a.c;
-    p.lo = (int32_t)min((int64_t)tile * kTile + (int)(threadIdx.x >> 5) * kWarpTokens, a.n);
+    p.lo = (int32_t)min(((int64_t)tile * kWarps + (threadIdx.x >> 5)) * a.runs * kTokens, a.n);
     return p;
 }
 // The row of the token of this lane's number in run q, as the order names it (unchecked, so that
@@ -363,7 +363,7 @@ __device__ __forceinline__ Place place_of(const ScanArgs& a, int tile, int block
 __device__ __forceinline__ int32_t row_of(const ScanArgs& a, const Place& p, int q) {
     const int lane = threadIdx.x & 31;
     const int64_t v = (int64_t)p.lo + q * kTokens + lane;
-    if (lane >= kTokens || q < 0 || q >= kRuns || v >= a.n) return -1;
+    if (lane >= kTokens || q < 0 || q >= a.runs || v >= a.n) return -1;
     const int64_t at = a.reverse ? a.n - 1 - v : v;
     return a.order ? a.order[at] : (int32_t)at;
 }
@@ -404,10 +404,10 @@ __device__ __forceinline__ void for_runs(const ScanArgs& a, const Place& p, cons
     constexpr int V = Lane<T>::V;
     const int lane = threadIdx.x & 31;
     const uint32_t stages = smem_u32(s_stages);
-    const auto run = [](int i) { return DOWN ? kRuns - 1 - i : i; };
+    const auto run = [&](int i) { return DOWN ? a.runs - 1 - i : i; };
     const auto check = [&](int32_t row, int i) {
         const int64_t v = (int64_t)p.lo + run(i) * kTokens + lane;
-        if (i < kRuns && lane < kTokens && v < a.n && (row < 0 || row >= a.n)) {
+        if (i < a.runs && lane < kTokens && v < a.n && (row < 0 || row >= a.n)) {
             atomicOr(a.head, kErrRange);
             return -1;
         }
@@ -418,10 +418,10 @@ __device__ __forceinline__ void for_runs(const ScanArgs& a, const Place& p, cons
     fetch<T, P>(a, from, stride, stages, row, p.c - lane * V);
     cp_async_commit();
 #pragma unroll 1
-    for (int i = 0; i < kRuns; ++i) {
-        const int32_t later = i + 2 < kRuns ? row_of(a, p, run(i + 2)) : -1;
+    for (int i = 0; i < a.runs; ++i) {
+        const int32_t later = i + 2 < a.runs ? row_of(a, p, run(i + 2)) : -1;
         next = check(next, i + 1);
-        if (i + 1 < kRuns) fetch<T, P>(a, from, stride, stages + ((i + 1) & 1) * P * kRunBytes, next, p.c - lane * V);
+        if (i + 1 < a.runs) fetch<T, P>(a, from, stride, stages + ((i + 1) & 1) * P * kRunBytes, next, p.c - lane * V);
         cp_async_commit();
         Run r;
         r.lo = (int32_t)min((int64_t)p.lo + run(i) * kTokens, a.n);
@@ -438,8 +438,6 @@ __device__ __forceinline__ void for_runs(const ScanArgs& a, const Place& p, cons
         next = later;
     }
 }
-constexpr int kStep = kRowBytes / 4, kOperand = kRunBytes / 4;  // words from a token, an operand to the next
-
 template <typename L>
 __device__ __forceinline__ void put(char* base, int32_t row, uint32_t stride, typename L::Num x) {
     *reinterpret_cast<uint32_t*>(base + (uint64_t)(uint32_t)row * stride) = L::pack(x);
@@ -674,41 +672,64 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_bwd(const ScanArgs a) {
     char* const gg = a.gg + p.c * (int)sizeof(T);
     char* const gx = a.out + p.c * (int)sizeof(T);
     const auto go = [&](auto simple, const Run& r, const uint32_t* w, N state) {
-        typename G::Held held[kTokens];
-        N turn[kTokens];  // a (1 - a) (h_{t-1} - x)
+        // A half of the run at a time, the second one first, for which the first one's gates are looked at
+        // twice.  (16 tokens at once do not fit 128 registers, and beside 200 KB of shared memory the
+        // L1 has no room for what is spilled: 602k tokens of 512 channels took 935 us.)
+        N from = state;
 #pragma unroll
-        for (int k = 0; k < kTokens; ++k) {
+        for (int k = 0; k < kHalf; ++k) {
             if (simple || k < r.count) {
-                if (!simple && (r.cuts.begin >> k & 1)) state = state_of<L>(a, a.first, seqs.begin[k], p);
-                const N x = L::unpack(w[kOperand + k * kStep]);
-                held[k] = G::hold(L::unpack(w[k * kStep]), turn[k]);
-                turn[k] = mul_(turn[k], FREE ? state : sub_(state, x));
-                state = next_state<FREE>(G(held[k]), x, state);
+                if (!simple && (r.cuts.begin >> k & 1)) from = state_of<L>(a, a.first, seqs.begin[k], p);
+                from = next_state<FREE>(G(G::hold(L::unpack(w[k * kStep]))), L::unpack(w[kOperand + k * kStep]), from);
             }
         }
+#pragma unroll 1
+        for (int b = kHalf; b >= 0; b -= kHalf) {
+            typename G::Held held[kHalf];
+            N turn[kHalf];  // a (1 - a) (h_{t-1} - x)
+            const uint32_t* const u = w + b * kStep;
 #pragma unroll
-        for (int k = kTokens - 1; k >= 0; --k) {
-            const int32_t row = row_at(r, k);
-            if (simple || k < r.count) {
-                if (!simple && (r.cuts.end >> k & 1)) mu = state_of<L>(a, a.glast, seqs.end(r.cuts, k), p);
-                const G g(held[k]);
-                const N lam = add_(mu, L::unpack(w[2 * kOperand + k * kStep]));
-                const N dg = mul_(turn[k], lam), dx = FREE ? lam : mul_(g.rest(), lam);
-                mu = g.kept(lam);
-                if (p.real && (simple || row >= 0)) {
-                    put<L>(gg, row, a.gg_s, dg);
-                    put<L>(gx, row, a.out_s, dx);
+            for (int k = 0; k < kHalf; ++k) {
+                if (simple || b + k < r.count) {
+                    if (!simple && (r.cuts.begin >> (b + k) & 1)) from = state_of<L>(a, a.first, seqs.begin[b + k], p);
+                    const N x = L::unpack(u[kOperand + k * kStep]);
+                    held[k] = G::hold(L::unpack(u[k * kStep]), turn[k]);
+                    turn[k] = mul_(turn[k], FREE ? from : sub_(from, x));
+                    from = next_state<FREE>(G(held[k]), x, from);
                 }
-                if (!simple && a.gfirst && p.real && (r.cuts.begin >> k & 1))
-                    L::store(a.gfirst + (int64_t)seqs.begin[k] * a.c + p.c, mu);
             }
+#pragma unroll
+            for (int k = kHalf - 1; k >= 0; --k) {
+                const int32_t row = row_at(r, b + k);
+                if (simple || b + k < r.count) {
+                    if (!simple && (r.cuts.end >> (b + k) & 1))
+                        mu = state_of<L>(a, a.glast, seqs.end(r.cuts, b + k), p);
+                    const G g(held[k]);
+                    const N lam = add_(mu, L::unpack(u[2 * kOperand + k * kStep]));
+                    const N dg = mul_(turn[k], lam), dx = FREE ? lam : mul_(g.rest(), lam);
+                    mu = g.kept(lam);
+                    if (p.real && (simple || row >= 0)) {
+                        put<L>(gg, row, a.gg_s, dg);
+                        put<L>(gx, row, a.out_s, dx);
+                    }
+                    if (!simple && a.gfirst && p.real && (r.cuts.begin >> (b + k) & 1))
+                        L::store(a.gfirst + (int64_t)seqs.begin[b + k] * a.c + p.c, mu);
+                }
+            }
+            from = state;
         }
     };
     const char* const from[3] = {a.gate, a.x, a.gy};
     const uint32_t stride[3] = {a.gate_s, a.x_s, a.gy_s};
+    const auto carry = [&](int q) {  // the state before run q
+        const int64_t lo = (int64_t)p.lo + q * kTokens;
+        return p.real && q >= 0 && lo < a.n ? L::load(a.carries + lo / kTokens * a.c + p.c) : L::fill(0.f);
+    };
+    int q = a.runs - 1;
+    N coming = carry(q);
     for_runs<T, 3, true>(a, p, from, stride, s_stages, seqs, a.glast, a.gfirst, [&](const Run& r, const uint32_t* w) {
-        N state = L::fill(0.f);
-        if (p.real && r.count > 0) state = L::load(a.carries + (int64_t)(r.lo / kTokens) * a.c + p.c);
+        const N state = coming;
+        coming = carry(--q);
         if (r.simple)
             go(std::true_type{}, r, w, state);
         else
@@ -747,7 +768,22 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(int64_t vectors, int per
     }
 }
 
-int64_t tiles_of(int64_t n) { return std::max<int64_t>(1, (n + kTile - 1) / kTile); }
+// Runs of a warp: as many as leave a round of blocks, for each warp's first run is waited for.
+// (25,179 tokens of 256 channels in bf16, forward: RUNS)
+struct Cut {
+    int runs;
+    int64_t tiles;
+};
+Cut cut_of(int64_t n, int c, int es, int sms) {
+    const int64_t blocks_c = (c * es + kRowBytes - 1) / kRowBytes;
+    Cut r{2 * kMaxRuns, 0};
+    do {
+        r.runs /= 2;
+        const int64_t tile = kWarps * kTokens * r.runs;
+        r.tiles = std::max<int64_t>(1, (n + tile - 1) / tile);
+    } while (r.runs > 1 && r.tiles * blocks_c < 3 * (int64_t)sms);
+    return r;
+}
 
 template <typename K>
 bool allow(K kernel, size_t smem) {
@@ -779,8 +815,8 @@ int launch(const ScanArgs& a, bool free_input, bool bwd, cudaStream_t s) {
 
 }  // namespace
 
-size_t gated_scan_workspace_bytes(int64_t n, int c) {
-    const int64_t tiles = tiles_of(n);
+size_t gated_scan_workspace_bytes(int64_t n, int c, int dtype, int sms) {
+    const int64_t tiles = cut_of(n, c, dtype == VG_F32 ? 4 : 2, sms).tiles;
     return align_up(256 + (tiles > 1 ? (size_t)tiles * c * ((1 + kWarps) * sizeof(Map) + sizeof(float)) : 0), 256);
 }
 
@@ -813,7 +849,9 @@ int gated_scan(const GatedScan& q, bool bwd, cudaStream_t s) {
     a.carries = q.carries;
     a.gfirst = q.grad_first;
     a.head = reinterpret_cast<uint32_t*>(q.ws);
-    const int64_t tiles = tiles_of(a.n);
+    const Cut cut = cut_of(a.n, a.c, es, q.sms);
+    const int64_t tiles = cut.tiles;
+    a.runs = cut.runs;
     if (tiles * a.blocks_c >= (int64_t(1) << 31)) return VG_ERR_UNSUPPORTED;
     a.tiles = (int)tiles;
     a.tile_maps = reinterpret_cast<Map*>(q.ws + 256);
