@@ -33,9 +33,11 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = kScanCarryRows;      // looked up and loaded at once; a state is kept for each such run
 constexpr int kHalf = kTokens / 2;
-constexpr int kMaxRuns = 4;                  // runs of a warp (ScanArgs::runs: 1, 2 or 4)
+constexpr int kMaxRuns = 8;                  // runs of a warp (ScanArgs::runs), at most
 constexpr int kRowBytes = 128, kRunBytes = kTokens * kRowBytes;  // of an operand in a block
 constexpr int kStep = kRowBytes / 4, kOperand = kRunBytes / 4;  // words from a token, an operand to the next
+// Blocks per SM, by their shared memory and registers.
+constexpr int per_sm(bool bwd) { return bwd ? 2 : 3; }
 // Shared memory of a block: two runs of `operands` a warp.
 constexpr size_t stage_bytes(int operands) { return (size_t)kWarps * 2 * operands * kRunBytes; }
 constexpr int kFoldTiles = 256;              // up to so many, blocks join the maps before them themselves
@@ -247,8 +249,9 @@ __device__ __forceinline__ Cuts find_cuts(const ScanArgs& a, CutSeqs& s, Within&
     if (lo > w.from && hi < w.to) return r;
     const bool last = hi == a.n && (count > 0 || (a.n == 0 && threadIdx.x < 32));  // the visits' end lies here
     if (count == 0 && !last) return r;
-    // the number of sequences that begin before lo, 32 probes at a time
-    int from = 0, to = a.batch;
+    // the number of sequences that begin before lo, 32 probes at a time (up to 32 of them: none, for
+    // all are looked at below)
+    int from = 0, to = a.batch > 32 ? a.batch : 0;
     while (to > from) {
         const int step = (to - from + 31) / 32;
         const int b = from + lane * step;
@@ -261,12 +264,7 @@ __device__ __forceinline__ Cuts find_cuts(const ScanArgs& a, CutSeqs& s, Within&
             to = min(to, hit + step);
         }
     }
-    if (from > 0) {
-        w.from = begins(a, from - 1);
-        w.to = begins(a, from);
-        s.entering = sequence(a, from - 1);
-    }
-    // those that begin here, and the one before them, which may end here
+    // those that begin here, and the one before them, which goes on into the visits and may end here
     for (int b0 = max(from - 1, 0);; b0 += 32) {
         const int b = b0 + lane;
         const bool real = b < a.batch;
@@ -275,6 +273,13 @@ __device__ __forceinline__ Cuts find_cuts(const ScanArgs& a, CutSeqs& s, Within&
         const int seq = sequence(a, b);
         const bool begin = real && q > p && p >= lo && p < hi, end = real && q > p && q > lo && q <= hi;
         if (begin) s.begin[p - lo] = seq;
+        const uint32_t over = __ballot_sync(0xffffffffu, real && p < lo && q > lo);
+        if (over) {  // one at most
+            const int l = __ffs(over) - 1;
+            w.from = __shfl_sync(0xffffffffu, p, l);
+            w.to = __shfl_sync(0xffffffffu, q, l);
+            if (lane == l) s.entering = seq;
+        }
         r.begin |= __reduce_or_sync(0xffffffffu, begin ? 1u << (p - lo) : 0u);
         r.end |= __reduce_or_sync(0xffffffffu, end ? 1u << (q - 1 - lo) : 0u);
         uint32_t none = __ballot_sync(0xffffffffu, here && q == p && p >= lo);
@@ -395,49 +400,67 @@ __device__ __forceinline__ void fetch(const ScanArgs& a, const char* const (&fro
     }
 }
 
-// Go through a warp's runs, DOWN from the last: `use(run, words)` with the run's tokens of the first
-// operand at words[k * kStep], the next operand's kRunBytes further, while the next run's are on their way.
-template <typename T, int P, bool DOWN, typename Use>
-__device__ __forceinline__ void for_runs(const ScanArgs& a, const Place& p, const char* const (&from)[P],
-                                         const uint32_t (&stride)[P], char* s_stages, CutSeqs& seqs, const float* in,
-                                         float* out, const Use& use) {
-    constexpr int V = Lane<T>::V;
-    const int lane = threadIdx.x & 31;
-    const uint32_t stages = smem_u32(s_stages);
-    const auto run = [&](int i) { return DOWN ? a.runs - 1 - i : i; };
-    const auto check = [&](int32_t row, int i) {
+// A warp's way through its runs, DOWN from the last, the next run's tokens always on their way.
+template <typename T, int P, bool DOWN>
+struct Walk {
+    static constexpr int V = Lane<T>::V;
+    const ScanArgs& a;
+    const Place& p;
+    const char* from[P];   // operands
+    uint32_t stride[P];
+    char* stages;
+    int32_t row, next;     // this lane's token of the current run, and of the one that follows
+
+    __device__ __forceinline__ int run(int i) const { return DOWN ? a.runs - 1 - i : i; }
+    __device__ __forceinline__ int32_t check(int32_t r, int i) const {
+        const int lane = threadIdx.x & 31;
         const int64_t v = (int64_t)p.lo + run(i) * kTokens + lane;
-        if (i < a.runs && lane < kTokens && v < a.n && (row < 0 || row >= a.n)) {
+        if (i < a.runs && lane < kTokens && v < a.n && (r < 0 || r >= a.n)) {
             atomicOr(a.head, kErrRange);
             return -1;
         }
-        return row;
-    };
-    Within within;
-    int32_t row = check(row_of(a, p, run(0)), 0), next = row_of(a, p, run(1));
-    fetch<T, P>(a, from, stride, stages, row, p.c - lane * V);
-    cp_async_commit();
-#pragma unroll 1
-    for (int i = 0; i < a.runs; ++i) {
-        const int32_t later = i + 2 < a.runs ? row_of(a, p, run(i + 2)) : -1;
-        next = check(next, i + 1);
-        if (i + 1 < a.runs) fetch<T, P>(a, from, stride, stages + ((i + 1) & 1) * P * kRunBytes, next, p.c - lane * V);
-        cp_async_commit();
-        Run r;
-        r.lo = (int32_t)min((int64_t)p.lo + run(i) * kTokens, a.n);
-        r.count = min(kTokens, (int32_t)a.n - r.lo);
-        r.row = row;
-        r.cuts = find_cuts<V>(a, seqs, within, r.lo, r.count, p.c, in, out);
-        r.simple = r.count == kTokens && (r.cuts.begin | r.cuts.end) == 0 &&
-                   __all_sync(0xffffffffu, row >= 0 || lane >= kTokens);
-        cp_async_wait<1>();
-        __syncwarp();
-        use(r, reinterpret_cast<const uint32_t*>(s_stages + (i & 1) * P * kRunBytes) + lane);
-        __syncwarp();
-        row = next;
-        next = later;
+        return r;
     }
-}
+    __device__ __forceinline__ void fetch_run(int i, int32_t r) {
+        fetch<T, P>(a, from, stride, smem_u32(stages) + (i & 1) * P * kRunBytes, r, p.c - (int)(threadIdx.x & 31) * V);
+    }
+    // Send for the first run.
+    __device__ __forceinline__ void start() {
+        const int32_t first = row_of(a, p, run(0));
+        next = row_of(a, p, run(1));
+        row = check(first, 0);
+        fetch_run(0, row);
+        cp_async_commit();
+    }
+    // use(run, words) for each run, with its tokens of the first operand at words[k * kStep], the next
+    // operand's kOperand further.
+    template <typename Use>
+    __device__ __forceinline__ void go(CutSeqs& seqs, const float* in, float* out, const Use& use) {
+        const int lane = threadIdx.x & 31;
+        Within within;
+#pragma unroll 1
+        for (int i = 0; i < a.runs; ++i) {
+            const int32_t later = i + 2 < a.runs ? row_of(a, p, run(i + 2)) : -1;
+            next = check(next, i + 1);
+            if (i + 1 < a.runs) fetch_run(i + 1, next);
+            cp_async_commit();
+            Run r;
+            r.lo = (int32_t)min((int64_t)p.lo + run(i) * kTokens, a.n);
+            r.count = min(kTokens, (int32_t)a.n - r.lo);
+            r.row = row;
+            r.cuts = find_cuts<V>(a, seqs, within, r.lo, r.count, p.c, in, out);
+            r.simple = r.count == kTokens && (r.cuts.begin | r.cuts.end) == 0 &&
+                       __all_sync(0xffffffffu, row >= 0 || lane >= kTokens);
+            cp_async_wait<1>();
+            __syncwarp();
+            use(r, reinterpret_cast<const uint32_t*>(stages + (i & 1) * P * kRunBytes) + lane);
+            __syncwarp();
+            row = next;
+            next = later;
+        }
+    }
+};
+
 template <typename L>
 __device__ __forceinline__ void put(char* base, int32_t row, uint32_t stride, typename L::Num x) {
     *reinterpret_cast<uint32_t*>(base + (uint64_t)(uint32_t)row * stride) = L::pack(x);
@@ -474,9 +497,9 @@ __device__ __forceinline__ Maps<Lane<T>::V> warp_map(const ScanArgs& a, const Pl
         }
         constant |= resets != 0;
     };
-    const char* const from[2] = {a.gate, BWD ? a.gy : a.x};
-    const uint32_t stride[2] = {a.gate_s, BWD ? a.gy_s : a.x_s};
-    for_runs<T, 2, BWD>(a, p, from, stride, s_stages, seqs, nullptr, nullptr, [&](const Run& r, const uint32_t* w) {
+    Walk<T, 2, BWD> walk{a, p, {a.gate, BWD ? a.gy : a.x}, {a.gate_s, BWD ? a.gy_s : a.x_s}, s_stages};
+    walk.start();
+    walk.go(seqs, nullptr, nullptr, [&](const Run& r, const uint32_t* w) {
         if (r.simple)
             go(std::true_type{}, r, w);
         else
@@ -514,7 +537,7 @@ __device__ __forceinline__ bool good_offsets(const ScanArgs& a) {
 // Step 1.  (Offsets that are no partition lead it to wrong maps, but to no wrong address; the first
 // block leaves its verdict for step 3.)
 template <typename T, bool FREE, bool BWD>
-__global__ void __launch_bounds__(kThreads, 3) k_scan_map(const ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, per_sm(false)) k_scan_map(const ScanArgs a) {
     using L = Lane<T>;
     constexpr int V = L::V;
     __shared__ Map s_maps[kWarps][32 * V];
@@ -593,9 +616,19 @@ __device__ __forceinline__ typename Lane<T>::Num entering(const ScanArgs& a, con
     const int before = BWD ? a.tiles - 1 - tile : tile, span = (before + kWarps - 1) / kWarps;
     Maps<V> m = no_change<V>();
     if (p.real) {
-#pragma unroll 4
-        for (int i = warp * span; i < min((warp + 1) * span, before); ++i)
-            m = then(m, load_maps<V>(a.tile_maps + (int64_t)(BWD ? a.tiles - 1 - i : i) * a.c + p.c));
+        constexpr int kAhead = 8;  // loads in flight
+        const int i1 = min((warp + 1) * span, before);
+        for (int i0 = warp * span; i0 < i1; i0 += kAhead) {
+            Maps<V> next[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = min(i0 + j, i1 - 1);
+                next[j] = load_maps<V>(a.tile_maps + (int64_t)(BWD ? a.tiles - 1 - i : i) * a.c + p.c);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i0 + j < i1) m = then(m, next[j]);
+        }
     }
     store_maps<V>(&s_maps[warp][cl], m);
     __syncthreads();
@@ -613,20 +646,26 @@ __device__ __forceinline__ bool bad_call(const ScanArgs& a) {
 
 // Step 3.
 template <typename T, bool FREE>
-__global__ void __launch_bounds__(kThreads, 3) k_scan_fwd(const ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, per_sm(false)) k_scan_fwd(const ScanArgs a) {
     using L = Lane<T>;
     using N = typename L::Num;
     using G = typename L::Gate;
     __shared__ Map s_maps[kWarps][32 * L::V];
     __shared__ CutSeqs s_seqs[kWarps];
     extern __shared__ __align__(128) char s_dyn[];
-    if (bad_call(a)) return;
     const int unit = gridDim.x - 1 - blockIdx.x;
     const int tile = unit / a.blocks_c, block_c = unit - tile * a.blocks_c;
     const Place p = place_of<L>(a, tile, block_c);
     CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
     char* const s_stages = s_dyn + (threadIdx.x >> 5) * 4 * kRunBytes;
+    Walk<T, 2, false> walk{a, p, {a.gate, a.x}, {a.gate_s, a.x_s}, s_stages};
+    if (a.tiles > 1) walk.start();  // before all that has to be waited for
+    if (bad_call(a)) {
+        cp_async_wait_all();
+        return;
+    }
     N h = entering<T, FREE, false>(a, p, tile, s_maps, s_stages, seqs);
+    if (a.tiles == 1) walk.start();
     char* const out = a.out + p.c * (int)sizeof(T);
     const auto go = [&](auto simple, const Run& r, const uint32_t* w) {
 #pragma unroll
@@ -641,9 +680,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_scan_fwd(const ScanArgs a) {
             }
         }
     };
-    const char* const from[2] = {a.gate, a.x};
-    const uint32_t stride[2] = {a.gate_s, a.x_s};
-    for_runs<T, 2, false>(a, p, from, stride, s_stages, seqs, a.first, a.last, [&](const Run& r, const uint32_t* w) {
+    walk.go(seqs, a.first, a.last, [&](const Run& r, const uint32_t* w) {
         if (a.carries && p.real && r.count > 0) L::store(a.carries + (int64_t)(r.lo / kTokens) * a.c + p.c, h);
         if (r.simple)
             go(std::true_type{}, r, w);
@@ -655,20 +692,26 @@ __global__ void __launch_bounds__(kThreads, 3) k_scan_fwd(const ScanArgs a) {
 // The gradients, from the last run to the first; the states of a run's tokens are found again from the
 // one that the forward pass kept at its beginning.
 template <typename T, bool FREE>
-__global__ void __launch_bounds__(kThreads, 2) k_scan_bwd(const ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, per_sm(true)) k_scan_bwd(const ScanArgs a) {
     using L = Lane<T>;
     using N = typename L::Num;
     using G = typename L::Gate;
     __shared__ Map s_maps[kWarps][32 * L::V];
     __shared__ CutSeqs s_seqs[kWarps];
     extern __shared__ __align__(128) char s_dyn[];
-    if (bad_call(a)) return;
     const int unit = gridDim.x - 1 - blockIdx.x;
     const int tile = unit / a.blocks_c, block_c = unit - tile * a.blocks_c;
     const Place p = place_of<L>(a, tile, block_c);
     CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
     char* const s_stages = s_dyn + (threadIdx.x >> 5) * 6 * kRunBytes;
+    Walk<T, 3, true> walk{a, p, {a.gate, a.x, a.gy}, {a.gate_s, a.x_s, a.gy_s}, s_stages};
+    if (a.tiles > 1) walk.start();  // before all that has to be waited for
+    if (bad_call(a)) {
+        cp_async_wait_all();
+        return;
+    }
     N mu = entering<T, FREE, true>(a, p, tile, s_maps, s_stages, seqs);
+    if (a.tiles == 1) walk.start();
     char* const gg = a.gg + p.c * (int)sizeof(T);
     char* const gx = a.out + p.c * (int)sizeof(T);
     const auto go = [&](auto simple, const Run& r, const uint32_t* w, N state) {
@@ -719,15 +762,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_bwd(const ScanArgs a) {
             from = state;
         }
     };
-    const char* const from[3] = {a.gate, a.x, a.gy};
-    const uint32_t stride[3] = {a.gate_s, a.x_s, a.gy_s};
     const auto carry = [&](int q) {  // the state before run q
         const int64_t lo = (int64_t)p.lo + q * kTokens;
         return p.real && q >= 0 && lo < a.n ? L::load(a.carries + lo / kTokens * a.c + p.c) : L::fill(0.f);
     };
     int q = a.runs - 1;
     N coming = carry(q);
-    for_runs<T, 3, true>(a, p, from, stride, s_stages, seqs, a.glast, a.gfirst, [&](const Run& r, const uint32_t* w) {
+    walk.go(seqs, a.glast, a.gfirst, [&](const Run& r, const uint32_t* w) {
         const N state = coming;
         coming = carry(--q);
         if (r.simple)
@@ -768,21 +809,26 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(int64_t vectors, int per
     }
 }
 
-// Runs of a warp: as many as leave a round of blocks, for each warp's first run is waited for.
-// (25,179 tokens of 256 channels in bf16, forward: RUNS)
+// Runs of a warp, 1, 2, 4 .. kMaxRuns: a round of blocks takes about the time of their runs and of three
+// more, in which nothing is at hand yet; the cut that takes the least.  (25,179 tokens of 256
+// channels in bf16: CUTS)
 struct Cut {
     int runs;
     int64_t tiles;
 };
-Cut cut_of(int64_t n, int c, int es, int sms) {
-    const int64_t blocks_c = (c * es + kRowBytes - 1) / kRowBytes;
-    Cut r{2 * kMaxRuns, 0};
-    do {
-        r.runs /= 2;
-        const int64_t tile = kWarps * kTokens * r.runs;
-        r.tiles = std::max<int64_t>(1, (n + tile - 1) / tile);
-    } while (r.runs > 1 && r.tiles * blocks_c < 3 * (int64_t)sms);
-    return r;
+Cut cut_of(int64_t n, int c, int es, bool bwd, int sms) {
+    const int64_t blocks_c = (c * es + kRowBytes - 1) / kRowBytes, slots = (int64_t)sms * per_sm(bwd);
+    Cut best{};
+    int64_t least = INT64_MAX;
+    for (int runs = 1; runs <= kMaxRuns; runs *= 2) {
+        const int64_t tile = (int64_t)kWarps * kTokens * runs, tiles = std::max<int64_t>(1, (n + tile - 1) / tile);
+        const int64_t time = (tiles * blocks_c + slots - 1) / slots * (runs + 3);
+        if (time <= least) {
+            least = time;
+            best = Cut{runs, tiles};
+        }
+    }
+    return best;
 }
 
 template <typename K>
@@ -816,7 +862,8 @@ int launch(const ScanArgs& a, bool free_input, bool bwd, cudaStream_t s) {
 }  // namespace
 
 size_t gated_scan_workspace_bytes(int64_t n, int c, int dtype, int sms) {
-    const int64_t tiles = cut_of(n, c, dtype == VG_F32 ? 4 : 2, sms).tiles;
+    const int es = dtype == VG_F32 ? 4 : 2;
+    const int64_t tiles = std::max(cut_of(n, c, es, false, sms).tiles, cut_of(n, c, es, true, sms).tiles);
     return align_up(256 + (tiles > 1 ? (size_t)tiles * c * ((1 + kWarps) * sizeof(Map) + sizeof(float)) : 0), 256);
 }
 
@@ -849,7 +896,7 @@ int gated_scan(const GatedScan& q, bool bwd, cudaStream_t s) {
     a.carries = q.carries;
     a.gfirst = q.grad_first;
     a.head = reinterpret_cast<uint32_t*>(q.ws);
-    const Cut cut = cut_of(a.n, a.c, es, q.sms);
+    const Cut cut = cut_of(a.n, a.c, es, bwd, q.sms);
     const int64_t tiles = cut.tiles;
     a.runs = cut.runs;
     if (tiles * a.blocks_c >= (int64_t(1) << 31)) return VG_ERR_UNSUPPORTED;
