@@ -6,18 +6,25 @@
 //
 // A dropped element is zero whatever x holds (a selection, not a product).  One group of four
 // words serves four consecutive elements; a thread takes 16-byte vectors, two groups for 16-bit
-// types.
+// types.  Two thirds of the work are the generator's 32-bit products, so what all groups of
+// a call have in common is done once: the keys, and half of the first two rounds, which see only the
+// call and the step.
 #include <cmath>
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc_ptx.cuh"
 
 namespace vg {
 
 namespace {
 
+using namespace ptx;
+
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // vectors of a thread in flight
+constexpr int kUnroll = 2;  // vectors of a thread in flight
+constexpr int kRounds = 10;
+constexpr uint32_t kM0 = 0xD2511F53u, kM1 = 0xCD9E8D57u;
 
 struct DropArgs {
     const void* x;
@@ -29,36 +36,112 @@ struct DropArgs {
     float scale;
 };
 
-// Words of elements 4 g .. 4 g + 3.
-__device__ __forceinline__ uint4 philox(uint64_t g, uint32_t step, uint32_t call, uint32_t k0, uint32_t k1) {
-    uint32_t c0 = (uint32_t)g, c1 = (uint32_t)(g >> 32), c2 = step, c3 = call;
+// Words of elements 4 g .. 4 g + 3, for groups g below 2^32.
+struct Philox {
+    uint32_t k0[kRounds], k1[kRounds];
+    // Of the counters (g, 0, step, call) the first round's second product, and of that the second round's
+    // first, are the same for every g.
+    uint32_t c1, c3, p_hi, p_lo;
+
+    __device__ __forceinline__ Philox(uint64_t seed, uint32_t step, uint32_t call) {
 #pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        const uint64_t p = (uint64_t)0xD2511F53u * c0, q = (uint64_t)0xCD9E8D57u * c2;
-        c0 = (uint32_t)(q >> 32) ^ c1 ^ k0;
-        c1 = (uint32_t)q;
-        c2 = (uint32_t)(p >> 32) ^ c3 ^ k1;
-        c3 = (uint32_t)p;
+        for (int i = 0; i < kRounds; ++i) {
+            k0[i] = (uint32_t)seed + i * 0x9E3779B9u;
+            k1[i] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
+        }
+        const uint64_t q = (uint64_t)kM1 * step;
+        const uint64_t p = (uint64_t)kM0 * ((uint32_t)(q >> 32) ^ k0[0]);  // the groups' high words are 0
+        c1 = (uint32_t)q ^ k0[1];
+        c3 = call ^ k1[0];
+        p_hi = (uint32_t)(p >> 32) ^ k1[1];
+        p_lo = (uint32_t)p;
+    }
+    __device__ __forceinline__ uint4 words(uint32_t g) const {
+        const uint64_t p1 = (uint64_t)kM0 * g;
+        const uint64_t q2 = (uint64_t)kM1 * ((uint32_t)(p1 >> 32) ^ c3);
+        uint32_t a = (uint32_t)(q2 >> 32) ^ c1, b = (uint32_t)q2, c = p_hi ^ (uint32_t)p1, d = p_lo;
+#pragma unroll
+        for (int i = 2; i < kRounds; ++i) {
+            const uint64_t p = (uint64_t)kM0 * a, q = (uint64_t)kM1 * c;
+            a = (uint32_t)(q >> 32) ^ b ^ k0[i];
+            b = (uint32_t)q;
+            c = (uint32_t)(p >> 32) ^ d ^ k1[i];
+            d = (uint32_t)p;
+        }
+        return make_uint4(a, b, c, d);
+    }
+};
+// The same for any group, round by round.
+__device__ __forceinline__ uint4 philox(uint64_t g, uint32_t step, uint32_t call, uint64_t seed) {
+    uint32_t a = (uint32_t)g, b = (uint32_t)(g >> 32), c = step, d = call;
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const uint64_t p = (uint64_t)kM0 * a, q = (uint64_t)kM1 * c;
+        a = (uint32_t)(q >> 32) ^ b ^ k0;
+        b = (uint32_t)q;
+        c = (uint32_t)(p >> 32) ^ d ^ k1;
+        d = (uint32_t)p;
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
-    return make_uint4(c0, c1, c2, c3);
+    return make_uint4(a, b, c, d);
 }
 
-__device__ __forceinline__ float dropped(uint32_t w, const DropArgs& a, float x) {
-    return w >= a.threshold ? x * a.scale : 0.f;
+// One element: its sum with the residual is rounded once to fp32, and once to T.
+template <typename T, bool RES>
+__device__ __forceinline__ void one(const DropArgs& a, int64_t i, uint32_t w) {
+    const float x = w >= a.threshold ? to_f32<T>(static_cast<const T*>(a.x)[i]) : 0.f;
+    const float y = RES ? fmaf(x, a.scale, to_f32<T>(static_cast<const T*>(a.residual)[i])) : x * a.scale;
+    static_cast<T*>(a.out)[i] = from_f32<T>(y);
 }
 
+// A pair of elements of a 16-byte vector.
+__device__ __forceinline__ float2 unpack(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack(uint32_t w, __half) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+__device__ __forceinline__ uint32_t pack(float2 x, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack(float2 x, __half) {
+    const __half2 h = __floats2half2_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <bool RES>
+__device__ __forceinline__ float2 both(const DropArgs& a, float2 x, float2 r, uint32_t w0, uint32_t w1) {
+    x = make_float2(w0 >= a.threshold ? x.x : 0.f, w1 >= a.threshold ? x.y : 0.f);
+    const float2 s = make_float2(a.scale, a.scale);
+    if constexpr (RES) return fma2(x, s, r);
+    return mul2(x, s);
+}
+template <typename T, bool RES>
+__device__ __forceinline__ uint4 vector(const DropArgs& a, const Philox& gen, uint32_t v, uint4 x, uint4 r) {
+    if constexpr (sizeof(T) == 4) {
+        const uint4 w = gen.words(v);
+        const auto f = [](uint32_t lo, uint32_t hi) { return make_float2(__uint_as_float(lo), __uint_as_float(hi)); };
+        const float2 y = both<RES>(a, f(x.x, x.y), f(r.x, r.y), w.x, w.y);
+        const float2 z = both<RES>(a, f(x.z, x.w), f(r.z, r.w), w.z, w.w);
+        return make_uint4(__float_as_uint(y.x), __float_as_uint(y.y), __float_as_uint(z.x), __float_as_uint(z.y));
+    } else {
+        const uint4 w = gen.words(2 * v), u = gen.words(2 * v + 1);
+        return make_uint4(pack(both<RES>(a, unpack(x.x, T()), unpack(r.x, T()), w.x, w.y), T()),
+                          pack(both<RES>(a, unpack(x.y, T()), unpack(r.y, T()), w.z, w.w), T()),
+                          pack(both<RES>(a, unpack(x.z, T()), unpack(r.z, T()), u.x, u.y), T()),
+                          pack(both<RES>(a, unpack(x.w, T()), unpack(r.w, T()), u.z, u.w), T()));
+    }
+}
+
+// Aligned pointers, fewer than 2^34 elements.
 template <typename T, bool RES>
 __global__ void __launch_bounds__(kThreads) k_dropout_vec(const DropArgs a) {
     constexpr int W = 16 / (int)sizeof(T);
-    const uint64_t seed = a.rng[0];
-    const uint32_t step = (uint32_t)a.rng[1], k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+    const Philox gen(a.rng[0], (uint32_t)a.rng[1], a.call);
     const uint4* x = static_cast<const uint4*>(a.x);
     const uint4* r = static_cast<const uint4*>(a.residual);
     uint4* out = static_cast<uint4*>(a.out);
-    const int64_t vectors = a.n / W;
-    const int64_t stride = (int64_t)gridDim.x * kThreads * kUnroll;
+    const int64_t vectors = a.n / W, stride = (int64_t)gridDim.x * kThreads * kUnroll;
     for (int64_t v0 = ((int64_t)blockIdx.x * kUnroll) * kThreads + threadIdx.x; v0 < vectors; v0 += stride) {
         uint4 xv[kUnroll], rv[kUnroll];
 #pragma unroll
@@ -66,59 +149,36 @@ __global__ void __launch_bounds__(kThreads) k_dropout_vec(const DropArgs a) {
             const int64_t v = v0 + u * kThreads;
             if (v < vectors) {
                 xv[u] = x[v];
-                if constexpr (RES) rv[u] = r[v];
+                rv[u] = RES ? r[v] : make_uint4(0, 0, 0, 0);
             }
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t v = v0 + u * kThreads;
-            if (v >= vectors) break;
-            uint4 o;
-            const T* xe = reinterpret_cast<const T*>(&xv[u]);
-            const T* re = reinterpret_cast<const T*>(&rv[u]);
-            T* oe = reinterpret_cast<T*>(&o);
-#pragma unroll
-            for (int h = 0; h < W / 4; ++h) {
-                const uint4 w = philox((uint64_t)v * (W / 4) + h, step, a.call, k0, k1);
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float y = dropped(ws[j], a, to_f32<T>(xe[4 * h + j]));
-                    if constexpr (RES) y += to_f32<T>(re[4 * h + j]);
-                    oe[4 * h + j] = from_f32<T>(y);
-                }
-            }
-            out[v] = o;
+            if (v < vectors) out[v] = vector<T, RES>(a, gen, (uint32_t)v, xv[u], rv[u]);
         }
     }
     // the elements behind the last whole vector: one thread each
     const int64_t i = vectors * W + threadIdx.x;
     if (blockIdx.x == 0 && i < a.n) {
-        const uint4 w = philox((uint64_t)i / 4, step, a.call, k0, k1);
+        const uint4 w = gen.words((uint32_t)(i / 4));
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        float y = dropped(ws[i & 3], a, to_f32<T>(static_cast<const T*>(a.x)[i]));
-        if constexpr (RES) y += to_f32<T>(static_cast<const T*>(a.residual)[i]);
-        static_cast<T*>(a.out)[i] = from_f32<T>(y);
+        one<T, RES>(a, i, ws[i & 3]);
     }
 }
 
-// Pointers that are not aligned to 16 bytes: a thread takes a group of four elements.
+// Other calls: a thread takes a group of four elements.
 template <typename T, bool RES>
 __global__ void __launch_bounds__(kThreads) k_dropout_any(const DropArgs a) {
     const uint64_t seed = a.rng[0];
-    const uint32_t step = (uint32_t)a.rng[1], k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+    const uint32_t step = (uint32_t)a.rng[1];
     const int64_t groups = (a.n + 3) / 4;
     for (int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x; g < groups; g += (int64_t)gridDim.x * kThreads) {
-        const uint4 w = philox((uint64_t)g, step, a.call, k0, k1);
+        const uint4 w = philox((uint64_t)g, step, a.call, seed);
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t i = 4 * g + j;
-            if (i >= a.n) break;
-            float y = dropped(ws[j], a, to_f32<T>(static_cast<const T*>(a.x)[i]));
-            if constexpr (RES) y += to_f32<T>(static_cast<const T*>(a.residual)[i]);
-            static_cast<T*>(a.out)[i] = from_f32<T>(y);
-        }
+        for (int j = 0; j < 4; ++j)
+            if (4 * g + j < a.n) one<T, RES>(a, 4 * g + j, ws[j]);
     }
 }
 
@@ -126,9 +186,9 @@ template <typename T>
 int launch(const DropArgs& a, int sms, cudaStream_t s) {
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
                            reinterpret_cast<uintptr_t>(a.out);
-    const bool wide = (bits & 15) == 0;
+    const bool wide = (bits & 15) == 0 && a.n < (int64_t(1) << 34);
     const int64_t per = wide ? (int64_t)kThreads * kUnroll * (16 / (int)sizeof(T)) : (int64_t)kThreads * 4;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((a.n + per - 1) / per, (int64_t)sms * 6));
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((a.n + per - 1) / per, (int64_t)sms * 8));
     if (wide)
         a.residual ? k_dropout_vec<T, true><<<grid, kThreads, 0, s>>>(a)
                    : k_dropout_vec<T, false><<<grid, kThreads, 0, s>>>(a);

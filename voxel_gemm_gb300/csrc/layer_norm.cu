@@ -31,10 +31,16 @@ constexpr int kMaxSmem = 227 * 1024;
 // Ring places of a lane, by its vectors of a row.
 constexpr int stages(int nv, bool bwd) { return nv == 1 ? (bwd ? 4 : 6) : nv == 2 ? (bwd ? 3 : 4) : nv <= 4 ? 3 : 2; }
 
+// Blocks per SM, by their registers (64, 80, 128 a thread).
+constexpr int per_sm(int nv) { return nv == 1 ? 4 : nv == 2 ? 3 : 2; }
+
 struct Rows {
     const void* p;
-    int64_t stride;
+    uint32_t stride;  // in bytes
 };
+__device__ __forceinline__ const char* at(const Rows& r, uint32_t row, int byte) {
+    return static_cast<const char*>(r.p) + (uint64_t)row * r.stride + byte;
+}
 
 struct LnArgs {
     int64_t n;
@@ -55,28 +61,72 @@ __device__ __forceinline__ float lanes_sum(float x, int lanes) {
     return x;
 }
 
-template <typename T>
-__device__ __forceinline__ void unpack(uint4 v, float (&x)[16 / sizeof(T)]) {
-    const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-    for (int j = 0; j < 16 / (int)sizeof(T); ++j) x[j] = to_f32<T>(e[j]);
+// 16 bytes as pairs of fp32, which the paired instructions work on.
+template <typename T> struct Vec {
+    static constexpr int H = 8 / (int)sizeof(T);  // pairs
+    float2 v[H];
+};
+__device__ __forceinline__ float2 pair_of(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&x)[16 / sizeof(T)]) {
-    uint4 v;
-    T* e = reinterpret_cast<T*>(&v);
-#pragma unroll
-    for (int j = 0; j < 16 / (int)sizeof(T); ++j) e[j] = from_f32<T>(x[j]);
-    return v;
+__device__ __forceinline__ float2 pair_of(uint32_t w, __half) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+__device__ __forceinline__ uint32_t word_of(float2 x, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t word_of(float2 x, __half) {
+    const __half2 h = __floats2half2_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T> __device__ __forceinline__ Vec<T> unpack(uint4 q) {
+    Vec<T> r;
+    if constexpr (sizeof(T) == 4) {
+        r.v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+        r.v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+    } else {
+        r.v[0] = pair_of(q.x, T());
+        r.v[1] = pair_of(q.y, T());
+        r.v[2] = pair_of(q.z, T());
+        r.v[3] = pair_of(q.w, T());
+    }
+    return r;
+}
+template <typename T> __device__ __forceinline__ uint4 pack(const Vec<T>& r) {
+    if constexpr (sizeof(T) == 4)
+        return make_uint4(__float_as_uint(r.v[0].x), __float_as_uint(r.v[0].y), __float_as_uint(r.v[1].x),
+                          __float_as_uint(r.v[1].y));
+    else
+        return make_uint4(word_of(r.v[0], T()), word_of(r.v[1], T()), word_of(r.v[2], T()), word_of(r.v[3], T()));
+}
+template <typename T> __device__ __forceinline__ Vec<T> filled(float x) {
+    Vec<T> r;
+#pragma unroll
+    for (int j = 0; j < Vec<T>::H; ++j) r.v[j] = make_float2(x, x);
+    return r;
+}
+// A vector kept for the whole run: unpacked while there are few.
+template <typename T, bool OPEN> struct Kept {
+    Vec<T> r;
+    __device__ __forceinline__ void set(uint4 q) { r = unpack<T>(q); }
+    __device__ __forceinline__ Vec<T> get() const { return r; }
+};
+template <typename T> struct Kept<T, false> {
+    uint4 q;
+    __device__ __forceinline__ void set(uint4 x) { q = x; }
+    __device__ __forceinline__ Vec<T> get() const { return unpack<T>(q); }
+};
 
-template <typename T, int NV, bool BWD>
-__global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 3 : 2) k_layer_norm(const LnArgs a) {
+// PARTS operands: 1 forward, 2 backward, 3 with a skipped gradient.
+template <typename T, int NV, int PARTS>
+__global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArgs a) {
+    constexpr bool BWD = PARTS > 1;
     extern __shared__ uint4 s_ring[];  // [stages][x, dy, skip][NV][kThreads]
     __shared__ float2 s_sum[2][kWarps];
     __shared__ float s_count[kWarps];
-    constexpr int V = 16 / (int)sizeof(T), kStages = stages(NV, BWD);
-    const int parts = BWD ? (a.skip.p ? 3 : 2) : 1;
+    using W = Vec<T>;
+    constexpr int V = 16 / (int)sizeof(T), H = W::H, kStages = stages(NV, BWD);
+    constexpr bool kOpen = NV <= (BWD ? 1 : 2);
+    constexpr int kPlace = PARTS * NV * kThreads;
     const int lane = threadIdx.x & (a.lanes - 1), sub = threadIdx.x / a.lanes;
     const int per = kThreads / a.lanes, warp = threadIdx.x >> 5;
     const int width = min(a.lanes, 32);
@@ -94,81 +144,77 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 3 : 2) k_lay
     const float warp_count = warps > 1 ? s_count[warp] : (float)a.c;
     const float inv_count = warp_count > 0.f ? 1.f / warp_count : 0.f;
 
-    uint4 w[NV], b[NV];
+    Kept<T, kOpen> w[NV], b[BWD ? 1 : NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float ones[V], zeros[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) ones[j] = 1.f, zeros[j] = 0.f;
-        w[i] = pack<T>(ones);
-        b[i] = pack<T>(zeros);
-        if (i < mine) {
-            if (a.w) w[i] = static_cast<const uint4*>(a.w)[i * a.lanes + lane];
-            if (!BWD && a.b) b[i] = static_cast<const uint4*>(a.b)[i * a.lanes + lane];
-        }
+        w[i].set(a.w && i < mine ? static_cast<const uint4*>(a.w)[i * a.lanes + lane] : pack<T>(filled<T>(1.f)));
+        if constexpr (!BWD)
+            b[i].set(a.b && i < mine ? static_cast<const uint4*>(a.b)[i * a.lanes + lane] : make_uint4(0, 0, 0, 0));
     }
-    constexpr int kAcc = BWD ? NV * V : 1;
-    float gw[kAcc], gb[kAcc];
+    constexpr int kAcc = BWD ? NV : 1;
+    W gw[kAcc], gb[kAcc];
 #pragma unroll
-    for (int j = 0; j < kAcc; ++j) gw[j] = gb[j] = 0.f;
+    for (int i = 0; i < kAcc; ++i) gw[i] = gb[i] = filled<T>(0.f);
 
     // the block's rows [r0, r1); this group's are r0 + sub, + per, ..; all groups take as many turns
-    const int64_t r0 = (int64_t)blockIdx.x * a.range, r1 = min(r0 + a.range, a.n);
+    const uint32_t r0 = (uint32_t)((int64_t)blockIdx.x * a.range), r1 = (uint32_t)min((int64_t)r0 + a.range, a.n);
     const int turns = r1 > r0 ? (int)((r1 - r0 + per - 1) / per) : 0;
     const uint32_t ring = smem_u32(s_ring + threadIdx.x);
-    const int place_size = parts * NV * kThreads;
-    int fetched = 0;
+    const int byte = lane * 16, step = a.lanes * 16;  // of the lane's first vector, and to the next
+    uint32_t row = r0 + sub, ahead = row;             // this turn's, and the next to be sent for (r1 + 2^24 fits)
     auto fetch_next = [&](int place) {
-        const int64_t r = r0 + sub + (int64_t)fetched * per;
-        if (r < r1) {
-            const uint32_t to = ring + place * place_size * 16;
-            const T* xp = static_cast<const T*>(a.x.p) + r * a.x.stride + lane * V;
-            const T* gp = BWD ? static_cast<const T*>(a.gy.p) + r * a.gy.stride + lane * V : nullptr;
-            const T* sp = BWD && parts == 3 ? static_cast<const T*>(a.skip.p) + r * a.skip.stride + lane * V : nullptr;
+        if (ahead < r1) {
+            const uint32_t to = ring + place * kPlace * 16;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (i < mine) {
-                    cp_async16(to + i * kThreads * 16, xp + i * a.lanes * V, 16);
-                    if constexpr (BWD) {
-                        cp_async16(to + (NV + i) * kThreads * 16, gp + i * a.lanes * V, 16);
-                        if (parts == 3) cp_async16(to + (2 * NV + i) * kThreads * 16, sp + i * a.lanes * V, 16);
-                    }
-                }
+            for (int p = 0; p < PARTS; ++p) {
+                const char* from = at(p == 0 ? a.x : p == 1 ? a.gy : a.skip, ahead, byte);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (i < mine) cp_async16(to + (p * NV + i) * kThreads * 16, from + i * step, 16);
             }
         }
-        ++fetched;
+        ahead += per;
         cp_async_commit();
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch_next(i);
 
     int place = 0;
-    for (int t = 0; t < turns; ++t) {
-        const int64_t r = r0 + sub + (int64_t)t * per;
-        const bool have = r < r1;
+    float2 st = make_float2(0.f, 0.f);
+    const float2* const stats = reinterpret_cast<const float2*>(a.stats);
+    if (BWD && row < r1) st = stats[row];
+#pragma unroll 1
+    for (int t = 0; t < turns; ++t, row += per) {
+        const bool have = row < r1;
         cp_async_wait<kStages - 2>();
         fetch_next(place == 0 ? kStages - 1 : place - 1);  // the place before this one has been read and used
-        const uint4* from = s_ring + place * place_size + threadIdx.x;
-        float x[NV][V];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            unpack<T>(have && i < mine ? from[i * kThreads] : make_uint4(0, 0, 0, 0), x[i]);
-        }
+        const uint4* from = s_ring + place * kPlace + threadIdx.x;
+        const auto vec = [&](int part, int i) {
+            return unpack<T>(have && i < mine ? from[(part * NV + i) * kThreads] : make_uint4(0, 0, 0, 0));
+        };
         if constexpr (!BWD) {
-            float sum = 0.f;
+            W x[NV];
+            float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                x[i] = vec(0, i);
 #pragma unroll
-                for (int j = 0; j < V; ++j) sum += x[i][j];
-            sum = lanes_sum(sum, width);
-            float mean = sum * inv_count, m2 = 0.f;
+                for (int j = 0; j < H; ++j) sum2 = add2(sum2, x[i].v[j]);
+            }
+            float sum = lanes_sum(sum2.x + sum2.y, width);
+            float mean = sum * inv_count;
+            float2 m22 = make_float2(0.f, 0.f);
+            const float2 off2 = make_float2(-mean, -mean);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (i < mine) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) m2 += (x[i][j] - mean) * (x[i][j] - mean);
+                    for (int j = 0; j < H; ++j) {
+                        const float2 d = add2(x[i].v[j], off2);
+                        m22 = fma2(d, d, m22);
+                    }
                 }
-            m2 = lanes_sum(m2, width);
+            float m2 = lanes_sum(m22.x + m22.y, width);
             if (warps > 1) {
                 float2* buf = s_sum[t & 1];
                 if ((threadIdx.x & 31) == 0) buf[warp] = make_float2(sum, m2);
@@ -186,74 +232,71 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 3 : 2) k_lay
             }
             const float rstd = rsqrtf(m2 * a.inv_c + a.eps);
             if (have) {
-                if (a.stats && lane == 0) *reinterpret_cast<float2*>(a.stats + 2 * r) = make_float2(mean, rstd);
-                T* yp = static_cast<T*>(const_cast<void*>(a.y.p)) + r * a.y.stride + lane * V;
+                if (stats && lane == 0) reinterpret_cast<float2*>(a.stats)[row] = make_float2(mean, rstd);
+                char* const y = const_cast<char*>(at(a.y, row, byte));
+                const float2 r2 = make_float2(rstd, rstd), n2 = make_float2(-mean, -mean);
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if (i < mine) {
-                        float wf[V], bf[V], y[V];
-                        unpack<T>(w[i], wf);
-                        unpack<T>(b[i], bf);
+                        const W wf = w[i].get(), bf = b[i].get();
+                        W o;
 #pragma unroll
-                        for (int j = 0; j < V; ++j) y[j] = (x[i][j] - mean) * rstd * wf[j] + bf[j];
-                        *reinterpret_cast<uint4*>(yp + i * a.lanes * V) = pack<T>(y);
+                        for (int j = 0; j < H; ++j)
+                            o.v[j] = fma2(mul2(add2(x[i].v[j], n2), r2), wf.v[j], bf.v[j]);
+                        *reinterpret_cast<uint4*>(y + i * step) = pack<T>(o);
                     }
             }
         } else {
-            float2 st = make_float2(0.f, 0.f);
-            if (have) st = *reinterpret_cast<const float2*>(a.stats + 2 * r);
-            const float mean = st.x, rstd = st.y;
-            float s1 = 0.f, s2 = 0.f;
+            const float2 r2 = make_float2(st.y, st.y), n2 = make_float2(-st.x, -st.x);
+            const float rstd = st.y;
+            if (row + per < r1) st = stats[row + per];
+            float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float g[V], wf[V];
-                unpack<T>(have && i < mine ? from[(NV + i) * kThreads] : make_uint4(0, 0, 0, 0), g);
-                unpack<T>(w[i], wf);
+                const W x = vec(0, i), g = vec(1, i), wf = w[i].get();
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float z = (x[i][j] - mean) * rstd;
-                    gw[i * V + j] += g[j] * z;
-                    gb[i * V + j] += g[j];
-                    const float gz = g[j] * wf[j];
-                    s1 += gz;
-                    s2 += gz * z;
+                for (int j = 0; j < H; ++j) {
+                    const float2 z = mul2(add2(x.v[j], n2), r2);
+                    gw[i].v[j] = fma2(g.v[j], z, gw[i].v[j]);
+                    gb[i].v[j] = add2(gb[i].v[j], g.v[j]);
+                    const float2 gz = mul2(g.v[j], wf.v[j]);
+                    s1 = add2(s1, gz);
+                    s2 = fma2(gz, z, s2);
                 }
             }
-            s1 = lanes_sum(s1, width);
-            s2 = lanes_sum(s2, width);
+            float a1 = lanes_sum(s1.x + s1.y, width), a2 = lanes_sum(s2.x + s2.y, width);
             if (warps > 1) {
                 float2* buf = s_sum[t & 1];
-                if ((threadIdx.x & 31) == 0) buf[warp] = make_float2(s1, s2);
+                if ((threadIdx.x & 31) == 0) buf[warp] = make_float2(a1, a2);
                 __syncthreads();
                 const int w0 = warp & ~(warps - 1);
-                s1 = s2 = 0.f;
+                a1 = a2 = 0.f;
                 for (int k = 0; k < warps; ++k) {
-                    s1 += buf[w0 + k].x;
-                    s2 += buf[w0 + k].y;
+                    a1 += buf[w0 + k].x;
+                    a2 += buf[w0 + k].y;
                 }
             }
-            s1 *= a.inv_c;
-            s2 *= a.inv_c;
-            if (have) {
-                T* yp = static_cast<T*>(const_cast<void*>(a.y.p)) + r * a.y.stride + lane * V;
+            a1 *= -a.inv_c * rstd;
+            a2 *= -a.inv_c * rstd;
+            if (have) {  // dx = rstd g - z (mean(g z) rstd) - mean(g) rstd, from the ring once more
+                const float2 c1 = make_float2(a1, a1), c2 = make_float2(a2, a2);
+                char* const y = const_cast<char*>(at(a.y, row, byte));
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if (i < mine) {
-                        float g[V], wf[V], y[V];
-                        unpack<T>(from[(NV + i) * kThreads], g);
-                        unpack<T>(w[i], wf);
+                        const W x = vec(0, i), g = vec(1, i), wf = w[i].get();
+                        W o;
 #pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            const float z = (x[i][j] - mean) * rstd;
-                            y[j] = (g[j] * wf[j] - s1 - z * s2) * rstd;
+                        for (int j = 0; j < H; ++j) {
+                            const float2 z = mul2(add2(x.v[j], n2), r2);
+                            o.v[j] = fma2(z, c2, fma2(mul2(g.v[j], wf.v[j]), r2, c1));
                         }
-                        if (parts == 3) {
-                            float k[V];
-                            unpack<T>(from[(2 * NV + i) * kThreads], k);
+                        if constexpr (PARTS == 3) {
+                            const W k = vec(2, i);
 #pragma unroll
-                            for (int j = 0; j < V; ++j) y[j] += k[j];
+                            for (int j = 0; j < H; ++j) o.v[j] = add2(o.v[j], k.v[j]);
                         }
-                        *reinterpret_cast<uint4*>(yp + i * a.lanes * V) = pack<T>(y);
+                        *reinterpret_cast<uint4*>(y + i * step) = pack<T>(o);
                     }
             }
         }
@@ -268,11 +311,11 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 3 : 2) k_lay
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (i < mine) {
-                    float* to = s_acc + (size_t)sub * 2 * a.c + (i * a.lanes + lane) * V;
+                    float2* to = reinterpret_cast<float2*>(s_acc + (size_t)sub * 2 * a.c + (i * a.lanes + lane) * V);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        to[j] = gw[i * V + j];
-                        to[a.c + j] = gb[i * V + j];
+                    for (int j = 0; j < H; ++j) {
+                        to[j] = gw[i].v[j];
+                        to[a.c / 2 + j] = gb[i].v[j];
                     }
                 }
             __syncthreads();
@@ -286,9 +329,13 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? 4 : NV == 2 ? 3 : 2) k_lay
     }
 }
 
-// Lanes of a row and vectors of a lane: the fewest idle places with at most `most` vectors a lane
-// (twice, then four times as many for the widest rows); among equals the most lanes of one warp.
-void shape(int vectors, int most, int* lanes, int* nv) {
+// Lanes of a row and vectors of a lane, up to 4, or 2 in the backward pass where several warps hold a
+// row (twice that for the widest): the fewest idle places; among equals the most lanes of one warp.
+// (bf16, 602k rows of 1024: forward and backward pass 1026 us with 4 vectors in one warp, 1115 with 2 in two,
+// 1183 with 1 in four.  150k rows of 4096: backward pass 736 us with 2 in eight warps, 1030 with 4 in
+// four; forward 431 with 4 in four, 638 with 2 in eight.)
+void shape(int vectors, bool bwd, int* lanes, int* nv) {
+    int most = bwd && vectors > 4 * 32 ? 2 : 4;
     while ((vectors + kThreads - 1) / kThreads > most) most *= 2;
     int best = 1 << 30;
     for (int l = 1; l <= kThreads; l <<= 1) {
@@ -312,11 +359,11 @@ struct Launch {
 
 Launch plan(int64_t n, int c, int es, int parts, bool bwd, int sms) {
     Launch l{};
-    shape(c * es / 16, bwd ? 2 : 4, &l.lanes, &l.nv);
+    shape(c * es / 16, bwd, &l.lanes, &l.nv);
     const int per = kThreads / l.lanes;
     l.smem = (size_t)stages(l.nv, bwd) * parts * l.nv * kThreads * 16;
     if (bwd) l.smem = std::max(l.smem, (size_t)per * 2 * c * 4);
-    l.per_sm = std::max(1, std::min<int>(l.nv == 1 ? 4 : l.nv == 2 ? 3 : 2, kMaxSmem / (int)(l.smem + 1536)));
+    l.per_sm = std::max(1, std::min<int>(per_sm(l.nv), kMaxSmem / (int)(l.smem + 1536)));
     const int64_t turns = std::max<int64_t>(1, (n + per - 1) / per);
     const int64_t cap = (int64_t)sms * l.per_sm;
     l.range = (turns + std::min(turns, cap) - 1) / std::min(turns, cap) * per;
@@ -325,8 +372,8 @@ Launch plan(int64_t n, int c, int es, int parts, bool bwd, int sms) {
 }
 
 template <typename T, int NV>
-int launch(const LnArgs& a, const Launch& l, bool bwd, cudaStream_t s) {
-    auto kernel = bwd ? k_layer_norm<T, NV, true> : k_layer_norm<T, NV, false>;
+int launch(const LnArgs& a, const Launch& l, int parts, cudaStream_t s) {
+    const auto kernel = parts == 1 ? k_layer_norm<T, NV, 1> : parts == 2 ? k_layer_norm<T, NV, 2> : k_layer_norm<T, NV, 3>;
     if (l.smem > 40 * 1024 &&  // with the static part, above what every block may have
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.smem) != cudaSuccess)
         return VG_ERR_CUDA;
@@ -334,14 +381,14 @@ int launch(const LnArgs& a, const Launch& l, bool bwd, cudaStream_t s) {
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 template <typename T>
-int launch(const LnArgs& a, const Launch& l, bool bwd, cudaStream_t s) {
+int launch(const LnArgs& a, const Launch& l, int parts, cudaStream_t s) {
     switch (l.nv) {
-        case 1: return launch<T, 1>(a, l, bwd, s);
-        case 2: return launch<T, 2>(a, l, bwd, s);
-        case 3: return launch<T, 3>(a, l, bwd, s);
-        case 4: return launch<T, 4>(a, l, bwd, s);
+        case 1: return launch<T, 1>(a, l, parts, s);
+        case 2: return launch<T, 2>(a, l, parts, s);
+        case 3: return launch<T, 3>(a, l, parts, s);
+        case 4: return launch<T, 4>(a, l, parts, s);
     }
-    if constexpr (sizeof(T) == 4) return launch<T, 8>(a, l, bwd, s);  // more than 4096 channels in fp32
+    if constexpr (sizeof(T) == 4) return launch<T, 8>(a, l, parts, s);  // more than 4096 channels in fp32
     return VG_ERR_UNSUPPORTED;
 }
 
@@ -356,7 +403,10 @@ size_t layer_norm_workspace_bytes(int64_t n, int c, int sms) {
 }
 
 int layer_norm(const LayerNorm& q, bool bwd, cudaStream_t s) {
-    const auto rows = [](const vg_rows* r) { return r ? Rows{r->data, r->row_stride} : Rows{}; };
+    const int es = q.dtype == VG_F32 ? 4 : 2, parts = bwd ? (q.grad_skip ? 3 : 2) : 1;
+    const auto rows = [&](const vg_rows* r) {
+        return r ? Rows{r->data, q.n > 1 ? (uint32_t)(r->row_stride * es) : 0u} : Rows{};
+    };
     LnArgs a{};
     a.n = q.n;
     a.c = q.c;
@@ -371,12 +421,12 @@ int layer_norm(const LayerNorm& q, bool bwd, cudaStream_t s) {
     a.inv_c = 1.f / (float)q.c;
     const bool sums = bwd && (q.grad_weight || q.grad_bias);
     a.partial = sums ? q.partial : nullptr;
-    const Launch l = plan(q.n, q.c, q.dtype == VG_F32 ? 4 : 2, bwd ? (q.grad_skip ? 3 : 2) : 1, bwd, q.sms);
+    const Launch l = plan(q.n, q.c, es, parts, bwd, q.sms);
     a.lanes = l.lanes;
     a.range = l.range;
-    const int st = q.dtype == VG_F32   ? launch<float>(a, l, bwd, s)
-                   : q.dtype == VG_F16 ? launch<__half>(a, l, bwd, s)
-                                       : launch<__nv_bfloat16>(a, l, bwd, s);
+    const int st = q.dtype == VG_F32   ? launch<float>(a, l, parts, s)
+                   : q.dtype == VG_F16 ? launch<__half>(a, l, parts, s)
+                                       : launch<__nv_bfloat16>(a, l, parts, s);
     if (st != VG_OK || !sums) return st;
     return reduce_rows(a.partial, l.grid, 2 * q.c, q.c, q.dtype, q.grad_weight, q.grad_bias, s);
 }
