@@ -5,10 +5,15 @@
     out = y + softmax(scale q k^T) v over the states of the voxel's own sample
     loss = mean((out - target)^2) / 2
 
-Forward, backward and the AdamW step run on the library (the product of the context with
-[Wk, Wv] and its gradient are plain matrix products).  Seeded synthetic inputs:
+With --scan a recurrent part follows, which mixes each sample's voxels along a Hilbert curve:
+
+    [g, u] = layer norm(out) W,  h_t = sigmoid(g_t) h_{t-1} + (1 - sigmoid(g_t)) u_t,  out += dropout(h)
+
+Forward, backward and the AdamW step run on the library (the products of the context with
+[Wk, Wv], of the norm with W, and their gradients are plain matrix products).  Seeded synthetic inputs:
 
     python examples/train_block.py [--workload NAME] [--heads H] [--states M] [--steps K] [--bits 8|32] [--lr LR]
+                                   [--scan] [--dropout P]
 """
 from __future__ import annotations
 
@@ -30,14 +35,59 @@ def offsets(lengths):
     return torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
 
 
+class CurveScan:
+    """out = z + dropout(scan(layer norm(z) W)) for tokens z [N, channels], along a Hilbert curve through each sample's
+    voxels; params are the norm's weight and bias, and W [channels, 2 channels].  A step's dropout masks are
+    those of rng = (seed, step)."""
+
+    CALL = 0  # the number of this dropout among those of a step
+
+    def __init__(self, coords, grid, channels, dtype, q_off, dropout, randn, seed):
+        n = coords.shape[0]
+        bits = max(max(grid[1:]) - 1, 1).bit_length()
+        codes = torch.empty(n, dtype=torch.int64, device="cuda")
+        ops.vg_encode_seq(coords, bits, ops.VG_CURVE_HILBERT, codes)
+        self.order, self.off, self.p = torch.argsort(codes).int(), q_off, dropout
+        self.rng = torch.tensor([seed, 0], device="cuda")
+
+        def empty(*shape, dt=dtype):
+            return torch.empty(*shape, dtype=dt, device="cuda")
+        self.params = [empty(channels).fill_(1), empty(channels).zero_(), randn(channels, 2 * channels, std=channels ** -0.5)]
+        self.norm, self.h, self.out, self.d_h, self.d_z = (empty(n, channels) for _ in range(5))
+        self.stats, self.d_gu = empty(n, 2, dt=torch.float32), empty(n, 2 * channels)
+        self.carries = ops.gated_scan_carries(n, channels)
+        self.norm_ws = ops.layer_norm_workspace(n, channels)
+        self.scan_ws = ops.gated_scan_workspace(n, channels, q_off.numel() - 1, dtype)
+
+    def forward(self, z):
+        self.z, (w, b, proj) = z, self.params
+        ops.vg_layer_norm_fwd(z, w, b, self.norm, self.stats)
+        self.gate, self.u = (self.norm @ proj).chunk(2, 1)
+        ops.vg_gated_scan_fwd(self.gate, self.u, self.off, self.order, None, self.h, None, self.carries, self.scan_ws)
+        ops.vg_dropout_add_fwd(self.h, z, self.p, self.rng, self.CALL, self.out)
+        return self.out
+
+    def backward(self, grad_out, grads):
+        """Gradients of params into `grads`; of z, returned."""
+        d_w, d_b, d_proj = grads
+        ops.vg_dropout_add_bwd(grad_out, self.p, self.rng, self.CALL, self.d_h)
+        d_gate, d_u = self.d_gu.chunk(2, 1)
+        ops.vg_gated_scan_bwd(self.gate, self.u, self.off, self.order, None, self.carries, self.d_h, None, d_gate, d_u,
+                              None, self.scan_ws)
+        torch.matmul(self.norm.t(), self.d_gu, out=d_proj)
+        ops.vg_layer_norm_bwd(self.z, self.params[0], self.stats, self.d_gu @ self.params[2].t(), grad_out, self.d_z,
+                              d_w, d_b, self.norm_ws)
+        return self.d_z
+
+
 class VoxelBlock:
     """The block over a fixed set of voxels, its buffers, parameters and optimizer state.
 
     coords [N, 4] (batch element, x, y, z), rows of a batch element together; state_lengths, the encoder states of
-    each batch element; heads query heads share kv_heads key and value heads."""
+    each batch element; heads query heads share kv_heads key and value heads; scan adds the recurrent part."""
 
     def __init__(self, coords, grid, channels, dtype, state_lengths, heads, kv_heads, state_width, bits=32, seed=0,
-                 weight_decay=0.0):
+                 weight_decay=0.0, scan=False, dropout=0.0):
         n, m, d = coords.shape[0], int(sum(state_lengths)), channels // heads
         g = torch.Generator(device="cuda").manual_seed(seed)
 
@@ -56,6 +106,8 @@ class VoxelBlock:
         self.q_w, self.k_w = empty(heads, d).fill_(1), empty(kv_heads, d).fill_(1)
         self.kv_w = randn(state_width, 2 * kv_heads * d, std=state_width ** -0.5)
         self.params = [self.conv_w, self.conv_b, self.q_w, self.k_w, self.kv_w]
+        self.scan = CurveScan(coords, grid, channels, dtype, self.q_off, dropout, randn, seed) if scan else None
+        self.params += self.scan.params if scan else []
         self.grads = [torch.empty_like(p) for p in self.params]
         masters = None if dtype == torch.float32 else [p.float() for p in self.params]
         self.opt = ops.AdamWState(self.params, self.grads, masters=masters, bits=bits, weight_decay=weight_decay)
@@ -78,11 +130,14 @@ class VoxelBlock:
         ops.vg_qk_norm_rope_fwd(None, self.kv[:, 0], None, self.k_w, None, None, None, None, self.kn)
         ops.vg_cross_attn_fwd(self.qn, self.kn, self.kv[:, 1], self.q_off, self.k_off, None, self.att, self.lse,
                               self.attn_ws)
-        return self.y + self.att
+        out = self.y + self.att
+        return out if self.scan is None else self.scan.forward(out.view(x.shape)).view(out.shape)
 
     def backward(self, x, context, grad_out):
         """Gradients of the parameters into self.grads; of x, returned."""
-        d_w, d_b, d_qw, d_kw, d_kvw = self.grads
+        d_w, d_b, d_qw, d_kw, d_kvw = self.grads[:5]
+        if self.scan is not None:
+            grad_out = self.scan.backward(grad_out.reshape(x.shape), self.grads[5:]).view(grad_out.shape)
         ops.vg_cross_attn_bwd(self.qn, self.kn, self.kv[:, 1], self.q_off, self.k_off, None, self.att, self.lse,
                               grad_out, self.d_qn, self.d_kn, self.d_kv[:, 1], self.attn_ws)
         ops.vg_qk_norm_rope_bwd(None, self.kv[:, 0], None, self.k_w, None, None, None, None, self.d_kn, None,
@@ -104,12 +159,17 @@ class VoxelBlock:
         scale = 1 / diff.numel() if diff.dtype == torch.float32 else 2.0 ** -round(math.log2(diff.shape[0]) / 2)
         self.backward(x, context, diff * scale)
         ops.vg_adamw_step(self.opt, step, lr, grad_scale=1 / (diff.numel() * scale))
+        if self.scan is not None:
+            self.scan.rng[1] += 1
         return diff.float().square().mean() / 2
 
     def check(self):
         """Raise if a kernel recorded an error."""
-        for name, st in (("neighbour map", self.map.status()), ("convolution", ops.vg_conv_status(self.conv_ws)),
-                         ("attention", ops.vg_cross_attn_status(self.attn_ws))):
+        status = [("neighbour map", self.map.status()), ("convolution", ops.vg_conv_status(self.conv_ws)),
+                  ("attention", ops.vg_cross_attn_status(self.attn_ws))]
+        if self.scan is not None:
+            status.append(("scan", ops.vg_gated_scan_status(self.scan.scan_ws)))
+        for name, st in status:
             if st != ops.VG_OK:
                 raise ops.VGError(st, name)
 
@@ -136,11 +196,14 @@ def main(argv=None):
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--bits", type=int, default=8, choices=(8, 32), help="bits of the optimizer's moments")
     ap.add_argument("--lr", type=float, default=3e-3)
+    ap.add_argument("--scan", action="store_true", help="add the recurrent part along a Hilbert curve")
+    ap.add_argument("--dropout", type=float, default=0.1, help="of the recurrent part")
     a = ap.parse_args(argv)
     wl = synth.WORKLOADS[a.workload]
     lengths = [a.states] * wl.B
     coords, x, context, target = make_inputs(wl, lengths, a.state_width)
-    block = VoxelBlock(coords, wl.grid, wl.cin, x.dtype, lengths, a.heads, a.kv_heads, a.state_width, a.bits)
+    block = VoxelBlock(coords, wl.grid, wl.cin, x.dtype, lengths, a.heads, a.kv_heads, a.state_width, a.bits,
+                       scan=a.scan, dropout=a.dropout)
     print(f"{a.workload}: {coords.shape[0]} voxels, {sum(lengths)} states")
     for step in range(1, a.steps + 1):
         loss = block.train_step(x, context, target, step, a.lr)
