@@ -28,6 +28,23 @@ constexpr int kGatherUnitCounter = 32;
 // Bound on mbarrier polls before a kernel gives up (~seconds at GB300 clocks).
 constexpr uint32_t kSpinLimit = 1u << 26;
 
+// Launch a kernel that may start before the one in front of it on the stream has ended (ptx::wait_for_previous).
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                                A... args) {
+    cudaLaunchAttribute overlap{};
+    overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    overlap.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &overlap;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 __host__ __device__ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // -------- element conversion --------

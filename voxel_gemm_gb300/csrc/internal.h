@@ -182,8 +182,10 @@ int adamw_step(const vg_adamw_tensor* ts, int count, int bits, int64_t step, dou
 int adamw_decode(const uint8_t* codes, const float* scales, int64_t n, int second, float* out, cudaStream_t s);
 
 // Column sums, in a fixed order, of fp32 rows [rows][cols] into the first cols_a columns' output a and
-// the others' output b (of dtype; null: not wanted).
-int reduce_rows(const float* partial, int rows, int cols, int cols_a, int dtype, void* a, void* b, cudaStream_t s);
+// the others' output b (of dtype; null: not wanted).  overlap: the kernel before it on the stream is the
+// one that writes the rows, and lets it start early.
+int reduce_rows(const float* partial, int rows, int cols, int cols_a, int dtype, void* a, void* b, bool overlap,
+                cudaStream_t s);
 
 // ---- recurrent-block operators ----
 // One layer norm call (pointers as in vg_layer_norm_fwd / _bwd).

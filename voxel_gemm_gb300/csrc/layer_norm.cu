@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
     }
     cp_async_wait_all();
     if constexpr (BWD) {
+        dependents_may_start();  // now, not before: the sums' blocks would take the place of these
         if (a.partial) {
             // one row of dw and one of db per block: the rows held side by side are added in order
             __syncthreads();
@@ -428,7 +429,7 @@ int layer_norm(const LayerNorm& q, bool bwd, cudaStream_t s) {
                    : q.dtype == VG_F16 ? launch<__half>(a, l, parts, s)
                                        : launch<__nv_bfloat16>(a, l, parts, s);
     if (st != VG_OK || !sums) return st;
-    return reduce_rows(a.partial, l.grid, 2 * q.c, q.c, q.dtype, q.grad_weight, q.grad_bias, s);
+    return reduce_rows(a.partial, l.grid, 2 * q.c, q.c, q.dtype, q.grad_weight, q.grad_bias, true, s);
 }
 
 }  // namespace vg

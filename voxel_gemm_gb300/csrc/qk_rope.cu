@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(32 * kReduceRows) k_weight_reduce(const float*
     const int c = blockIdx.x * 32 + (threadIdx.x & 31);
     const int rl = threadIdx.x >> 5;
     float sum = 0.f;
+    wait_for_previous();
     if (c < cols) {
 #pragma unroll 8
         for (int row = rl; row < rows; row += kReduceRows) sum += partial[(size_t)row * cols + c];
@@ -414,22 +415,25 @@ int qk_norm_rope(const QkRope& c, bool bwd, cudaStream_t s) {
                                  : launch<__nv_bfloat16>(a, halves, bwd, gx, chunks, smem, s);
     if (st != VG_OK || !gw) return st;
     return reduce_rows(a.partial, a.shared ? gx * chunks : gx, (a.shared ? 2 : a.ht) * a.d, (a.shared ? 1 : a.hq) * a.d,
-                       c.dtype, c.grad_q_weight, c.grad_k_weight, s);
+                       c.dtype, c.grad_q_weight, c.grad_k_weight, false, s);
 }
 
-int reduce_rows(const float* partial, int rows, int cols, int cols_a, int dtype, void* a, void* b, cudaStream_t s) {
-    const int grid = (cols + 31) / 32, threads = 32 * kReduceRows;
-    if (dtype == VG_F32)
-        k_weight_reduce<float><<<grid, threads, 0, s>>>(partial, rows, cols, cols_a, static_cast<float*>(a),
-                                                        static_cast<float*>(b));
-    else if (dtype == VG_F16)
-        k_weight_reduce<__half><<<grid, threads, 0, s>>>(partial, rows, cols, cols_a, static_cast<__half*>(a),
-                                                         static_cast<__half*>(b));
-    else
-        k_weight_reduce<__nv_bfloat16><<<grid, threads, 0, s>>>(partial, rows, cols, cols_a,
-                                                                static_cast<__nv_bfloat16*>(a),
-                                                                static_cast<__nv_bfloat16*>(b));
+template <typename T>
+static int reduce_rows(const float* partial, int rows, int cols, int cols_a, void* a, void* b, bool overlap,
+                       cudaStream_t s) {
+    const unsigned grid = (cols + 31) / 32, threads = 32 * kReduceRows;
+    T *ta = static_cast<T*>(a), *tb = static_cast<T*>(b);
+    if (overlap)
+        return launch_after(k_weight_reduce<T>, grid, threads, 0, s, partial, rows, cols, cols_a, ta, tb) == cudaSuccess
+                   ? VG_OK : VG_ERR_CUDA;
+    k_weight_reduce<T><<<grid, threads, 0, s>>>(partial, rows, cols, cols_a, ta, tb);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+}
+int reduce_rows(const float* partial, int rows, int cols, int cols_a, int dtype, void* a, void* b, bool overlap,
+                cudaStream_t s) {
+    return dtype == VG_F32   ? reduce_rows<float>(partial, rows, cols, cols_a, a, b, overlap, s)
+           : dtype == VG_F16 ? reduce_rows<__half>(partial, rows, cols, cols_a, a, b, overlap, s)
+                             : reduce_rows<__nv_bfloat16>(partial, rows, cols, cols_a, a, b, overlap, s);
 }
 
 }  // namespace vg

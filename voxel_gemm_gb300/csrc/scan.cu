@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(false)) k_scan_map(const Scan
     __shared__ Map s_maps[kWarps][32 * V];
     __shared__ CutSeqs s_seqs[kWarps];
     extern __shared__ __align__(128) char s_dyn[];  // [warps][2 stages][operands][tokens][128 bytes]
+    dependents_may_start();
     const int warp = threadIdx.x >> 5, cl = (threadIdx.x & 31) * V;
     const int tile = blockIdx.x / a.blocks_c, block_c = blockIdx.x - tile * a.blocks_c;
     const Place p = place_of<L>(a, tile, block_c);
@@ -573,6 +574,8 @@ __global__ void __launch_bounds__(kJoinChannels* kJoinParts) k_scan_join(const S
     const int span = (a.tiles + kJoinParts - 1) / kJoinParts;
     const int t0 = min(part * span, a.tiles), t1 = min(t0 + span, a.tiles);
     const auto tile = [&](int i) { return (int64_t)(BWD ? a.tiles - 1 - i : i) * a.c + c; };
+    dependents_may_start();
+    wait_for_previous();
     Map m{1.f, 0.f};
 #pragma unroll 8
     for (int i = t0; i < t1; ++i) m = then(m, a.tile_maps[tile(i)]);
@@ -636,12 +639,20 @@ __device__ __forceinline__ typename Lane<T>::Num entering(const ScanArgs& a, con
     return through(mine, through(all, L::fill(0.f)));
 }
 
-// Blocks of step 3 come in the order opposite to step 1's.
-__device__ __forceinline__ bool bad_call(const ScanArgs& a) {
-    if (a.tiles > 1) return a.head[1] != 0;
+// Blocks of step 3 come in the order opposite to step 1's, and send for their first tokens while
+// the steps before still run.  False if the call's offsets are bad.
+template <typename W>
+__device__ __forceinline__ bool begin_step(const ScanArgs& a, W& walk) {
+    if (a.tiles > 1) {
+        walk.start();
+        wait_for_previous();
+        if (a.head[1] == 0) return true;
+        cp_async_wait_all();
+        return false;
+    }
     const bool good = good_offsets(a);
     if (!good && threadIdx.x == 0) atomicOr(a.head, kErrRange);
-    return !good;
+    return good;
 }
 
 // Step 3.
@@ -659,11 +670,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(false)) k_scan_fwd(const Scan
     CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
     char* const s_stages = s_dyn + (threadIdx.x >> 5) * 4 * kRunBytes;
     Walk<T, 2, false> walk{a, p, {a.gate, a.x}, {a.gate_s, a.x_s}, s_stages};
-    if (a.tiles > 1) walk.start();  // before all that has to be waited for
-    if (bad_call(a)) {
-        cp_async_wait_all();
-        return;
-    }
+    if (!begin_step(a, walk)) return;
     N h = entering<T, FREE, false>(a, p, tile, s_maps, s_stages, seqs);
     if (a.tiles == 1) walk.start();
     char* const out = a.out + p.c * (int)sizeof(T);
@@ -705,11 +712,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(true)) k_scan_bwd(const ScanA
     CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
     char* const s_stages = s_dyn + (threadIdx.x >> 5) * 6 * kRunBytes;
     Walk<T, 3, true> walk{a, p, {a.gate, a.x, a.gy}, {a.gate_s, a.x_s, a.gy_s}, s_stages};
-    if (a.tiles > 1) walk.start();  // before all that has to be waited for
-    if (bad_call(a)) {
-        cp_async_wait_all();
-        return;
-    }
+    if (!begin_step(a, walk)) return;
     N mu = entering<T, FREE, true>(a, p, tile, s_maps, s_stages, seqs);
     if (a.tiles == 1) walk.start();
     char* const gg = a.gg + p.c * (int)sizeof(T);
@@ -845,12 +848,14 @@ int launch(const ScanArgs& a, cudaStream_t s) {
         if (cudaPeekAtLastError() != cudaSuccess) return VG_ERR_CUDA;
     }
     if (a.tiles > kFoldTiles) {
-        k_scan_join<BWD><<<a.c / kJoinChannels, kJoinChannels * kJoinParts, 0, s>>>(a);
-        if (cudaPeekAtLastError() != cudaSuccess) return VG_ERR_CUDA;
+        if (launch_after(k_scan_join<BWD>, a.c / kJoinChannels, kJoinChannels * kJoinParts, 0, s, a) != cudaSuccess)
+            return VG_ERR_CUDA;
     }
     const auto kernel = BWD ? k_scan_bwd<T, FREE> : k_scan_fwd<T, FREE>;
-    if (!allow(kernel, stage_bytes(BWD ? 3 : 2))) return VG_ERR_CUDA;
-    kernel<<<grid, kThreads, stage_bytes(BWD ? 3 : 2), s>>>(a);
+    const size_t smem = stage_bytes(BWD ? 3 : 2);
+    if (!allow(kernel, smem)) return VG_ERR_CUDA;
+    if (a.tiles > 1) return launch_after(kernel, grid, kThreads, smem, s, a) == cudaSuccess ? VG_OK : VG_ERR_CUDA;
+    kernel<<<grid, kThreads, smem, s>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? VG_OK : VG_ERR_CUDA;
 }
 template <typename T>

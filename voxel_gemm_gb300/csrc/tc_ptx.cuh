@@ -65,6 +65,13 @@ __device__ __forceinline__ bool mbar_wait_timed(uint32_t bar, uint32_t parity) {
     return true;
 }
 
+// ---------------------------------------------------------------- launches that overlap
+// A kernel launched with launch_after may start while the one before it on the stream still runs:
+// after that one's blocks have all said dependents_may_start (or ended).  wait_for_previous returns when the
+// kernel before is complete and what it wrote can be read (at once, if launched in the plain way).
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- copies
 // 16-byte global->shared copy; src_bytes = 0 writes 16 zero bytes.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {

@@ -676,12 +676,13 @@ def _rows(t, dtype, shape, device, what):
     """vg_rows of a [rows, channels] tensor (any row stride), None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or (t.stride(1) != 1 and t.numel() > 0):
+    s = t.stride()
+    if t.dtype != dtype or t.shape != shape or (s[1] != 1 and t.numel() > 0):
         raise ValueError(f"{what}: expected {dtype} {list(shape)} with contiguous elements, got {t.dtype} "
-                         f"{list(t.shape)} of strides {t.stride()}")
+                         f"{list(t.shape)} of strides {s}")
     if t.get_device() != device:
         _on(device, what, t)
-    return RowsStruct(t.data_ptr(), t.stride(0))
+    return RowsStruct(t.data_ptr(), s[0])
 
 
 def _flat(t, dtype, shape, device, what):
