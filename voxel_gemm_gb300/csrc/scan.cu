@@ -192,11 +192,11 @@ struct Rest {
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
         return over(e);
     }
-    // Also a (1 - a) = exp(g) s s, the exponent bounded so that infinity and zero do not meet.
+    // Also a (1 - a) = exp(g) s s, the exponent bounded so that infinity and zero do not meet (at the bound s is 0).
     static __device__ __forceinline__ float2 hold(float2 g, float2& slope) {
         float2 y = mul2(g, make_float2(1.4426950408889634f, 1.4426950408889634f)), e;
-        asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(y.x));  // 126
-        asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(y.y));
+        asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(y.x));  // 127
+        asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(y.y));
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
         const float2 s = over(e);
@@ -298,10 +298,11 @@ __device__ __forceinline__ Cuts find_cuts(const ScanArgs& a, CutSeqs& s, Within&
 }
 
 // ---------------------------------------------------------------- maps of runs of tokens
-__device__ __forceinline__ float through(Map m, float h) { return m.a < 0.f ? m.b : fmaf(m.a, h, m.b); }
+__device__ __forceinline__ bool constant(Map m) { return m.a < -0.5f; }
+__device__ __forceinline__ float through(Map m, float h) { return constant(m) ? m.b : fmaf(m.a, h, m.b); }
 __device__ __forceinline__ Map then(Map first, Map second) {
-    if (second.a < 0.f) return second;
-    return Map{first.a < 0.f ? -1.f : first.a * second.a, fmaf(second.a, first.b, second.b)};
+    if (constant(second)) return second;
+    return Map{constant(first) ? -1.f : first.a * second.a, fmaf(second.a, first.b, second.b)};
 }
 // Of a lane's channels.
 template <int V> struct Maps {
@@ -388,15 +389,16 @@ __device__ __forceinline__ void fetch(const ScanArgs& a, const char* const (&fro
     const int lane = threadIdx.x & 31;
     const int at = first_channel * (int)sizeof(T) + (lane & 7) * 16;
     const bool inside = at < a.c * (int)sizeof(T);
+    const char* const nowhere = reinterpret_cast<const char*>(a.head);  // not read
     to += lane * 16;
 #pragma unroll
     for (int i = 0; i < kTokens / 4; ++i) {
         const int32_t r = __shfl_sync(0xffffffffu, row, i * 4 + (lane >> 3));
         const bool have = inside && r >= 0;
-        const uint64_t rr = have ? (uint32_t)r : 0u;
+        const uint64_t rr = (uint32_t)r;
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            cp_async16(to + p * kRunBytes + i * 512, from[p] + (inside ? at : 0) + rr * stride[p], have ? 16 : 0);
+            cp_async16(to + p * kRunBytes + i * 512, have ? from[p] + at + rr * stride[p] : nowhere, have ? 16 : 0);
     }
 }
 

@@ -696,17 +696,26 @@ def _flat(t, dtype, shape, device, what):
     return t.data_ptr()
 
 
-def _matrix(x, what):
+def _current(device, stream, what):
+    """Refuse tensors of another GPU than the call's: kernels are launched on the current one."""
+    if torch.cuda.is_initialized() and device != torch._C._cuda_getDevice() or \
+            stream is not None and device != stream.device_index:
+        raise ValueError(f"{what}: the tensors are on GPU {device}, which is not the current GPU or not the stream's")
+
+
+def _matrix(x, stream, what):
     """Shape, dtype and GPU of a [rows, channels] tensor."""
     if x.dim() != 2:
         raise ValueError(f"{what}: expected [rows, channels], got {list(x.shape)}")
-    return x.shape, x.dtype, _gpu(x, what)
+    device = _gpu(x, what)
+    _current(device, stream, what)
+    return x.shape, x.dtype, device
 
 
 def vg_layer_norm_fwd(x, weight, bias, y, stats, eps=1e-5, stream=None) -> None:
     """y = (x - mean) rstd weight + bias of each row of x [rows, channels] (any row stride); weight and bias
     [channels] or None; stats float32 [rows, 2] takes (mean, rstd) for the backward pass, or is None."""
-    (n, c), dt, dev = _matrix(x, "vg_layer_norm_fwd")
+    (n, c), dt, dev = _matrix(x, stream, "vg_layer_norm_fwd")
     _check(lib().vg_layer_norm_fwd(n, c, _DT.get(dt, -1), _rows(x, dt, (n, c), dev, "x"),
                                    _flat(weight, dt, (c,), dev, "weight"), _flat(bias, dt, (c,), dev, "bias"), eps,
                                    _rows(y, dt, (n, c), dev, "y"), _flat(stats, torch.float32, (n, 2), dev, "stats"),
@@ -716,7 +725,7 @@ def vg_layer_norm_fwd(x, weight, bias, y, stats, eps=1e-5, stream=None) -> None:
 def vg_layer_norm_bwd(x, weight, stats, grad_y, grad_skip, grad_x, grad_weight, grad_bias, ws, stream=None) -> None:
     """Gradients of vg_layer_norm_fwd's x (plus grad_skip, unless None), weight and bias (None: not wanted; with both
     None, ws may be None too)."""
-    (n, c), dt, dev = _matrix(x, "vg_layer_norm_bwd")
+    (n, c), dt, dev = _matrix(x, stream, "vg_layer_norm_bwd")
     s = (n, c)
     _on(dev, "vg_layer_norm_bwd", ws)
     _check(lib().vg_layer_norm_bwd(n, c, _DT.get(dt, -1), _rows(x, dt, s, dev, "x"),
@@ -752,9 +761,9 @@ def gated_scan_carries(n, channels, device="cuda") -> torch.Tensor:
     return torch.empty(int(lib().vg_gated_scan_carry_rows(n)), channels, dtype=torch.float32, device=device)
 
 
-def _scan(gate, offsets, order, carries, ws, flags, what):
+def _scan(gate, offsets, order, carries, ws, flags, stream, what):
     """(vg_scan, shape, batch, dtype, device, carries' address) of a call, checked."""
-    (n, c), dt, dev = _matrix(gate, what)
+    (n, c), dt, dev = _matrix(gate, stream, what)
     batch = offsets.numel() - 1
     f32 = torch.float32
     rows = -(-n // VG_SCAN_CARRY_ROWS)
@@ -769,7 +778,7 @@ def vg_gated_scan_fwd(gate, x, offsets, order, first, out, last, carries, ws, fl
     gate, x, out [rows, channels] (any row stride); offsets int32 [batch + 1]; order int32 [rows], the row of each
     position, or None; first, last float32 [batch, channels], the states before and after, or None; carries
     (gated_scan_carries) for the backward pass, or None; flags VG_SCAN_REVERSE, VG_SCAN_FREE_INPUT."""
-    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, ws, flags, "vg_gated_scan_fwd")
+    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, ws, flags, stream, "vg_gated_scan_fwd")
     _on(dev, "vg_gated_scan_fwd", ws)
     _check(lib().vg_gated_scan_fwd(a, _rows(gate, dt, s, dev, "gate"), _rows(x, dt, s, dev, "x"),
                                    _flat(first, torch.float32, b, dev, "first"), _rows(out, dt, s, dev, "out"),
@@ -780,7 +789,7 @@ def vg_gated_scan_fwd(gate, x, offsets, order, first, out, last, carries, ws, fl
 def vg_gated_scan_bwd(gate, x, offsets, order, first, carries, grad_out, grad_last, grad_gate, grad_x, grad_first, ws,
                       flags=0, stream=None) -> None:
     """Gradients of vg_gated_scan_fwd's gate, x and first (None: not wanted), from its carries; grad_last may be None."""
-    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, ws, flags, "vg_gated_scan_bwd")
+    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, ws, flags, stream, "vg_gated_scan_bwd")
     _on(dev, "vg_gated_scan_bwd", ws)
     _check(lib().vg_gated_scan_bwd(a, _rows(gate, dt, s, dev, "gate"), _rows(x, dt, s, dev, "x"),
                                    _flat(first, torch.float32, b, dev, "first"), kept,
@@ -793,7 +802,7 @@ def vg_gated_scan_bwd(gate, x, offsets, order, first, carries, grad_out, grad_la
 
 def vg_gated_scan_step(gate, x, state, out, flags=0, stream=None) -> None:
     """One token of each of the rows' sequences: state float32 [rows, channels] goes from h_{t-1} to h_t, out = h_t."""
-    s, dt, dev = _matrix(gate, "vg_gated_scan_step")
+    s, dt, dev = _matrix(gate, stream, "vg_gated_scan_step")
     _check(lib().vg_gated_scan_step(s[0], s[1], _DT.get(dt, -1), flags, _rows(gate, dt, s, dev, "gate"),
                                     _rows(x, dt, s, dev, "x"), _flat(state, torch.float32, s, dev, "state"),
                                     _rows(out, dt, s, dev, "out"), _s(stream)), "vg_gated_scan_step")
@@ -805,6 +814,7 @@ def vg_gated_scan_status(ws, stream=None) -> int:
 
 def _dropout(name, x, residual, p, rng, call, out, stream):
     dt, dev = x.dtype, _gpu(x, name)
+    _current(dev, stream, name)
     if rng.dtype not in (torch.int64, torch.uint64):
         raise ValueError(f"{name}: rng must be int64 [2] (seed, step)")
     args = [x.numel(), _dtype_code(x), _flat(x, dt, x.shape, dev, "input")]
