@@ -8,12 +8,15 @@
 // 16-byte vectors a lane, so the row's sums are shuffles, and beyond 32 lanes one exchange in
 // shared memory: the squares are taken from the mean of the warp's own elements and moved to
 // the row's mean afterwards, M2 = sum over warps (M2_w + n_w (mean_w - mean)^2), so there is no
-// difference of large numbers and no second exchange.  A block of 256 threads runs along a range
-// of rows.  Every lane copies its vectors of the next rows into its own places of a ring in shared
+// difference of large numbers and no second exchange.  Blocks of 256 threads go through the rows side
+// by side.  Every lane copies its vectors of the next rows into its own places of a ring in shared
 // memory (asynchronously, without a barrier: no lane reads another's), so that the loads in flight
 // cost no registers; the weights, and in the backward pass the sums of dw and db, stay in
 // registers.  Those sums leave as one fp32 row per block, added in a fixed order by a second
 // kernel, so they do not change from run to run.
+//
+// GB300, bf16: 602,492 rows of 1024 forward 368 us (6.7 TB/s), backward 545 and 5 (6.8 TB/s); 319,057 rows
+// of 128 forward 33 us, backward with a skipped gradient 52 and 4 (72 us of memory traffic in all).
 #include "common.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
@@ -28,8 +31,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSmem = 227 * 1024;
 
-// Ring places of a lane, by its vectors of a row.
-constexpr int stages(int nv, bool bwd) { return nv == 1 ? (bwd ? 4 : 6) : nv == 2 ? (bwd ? 3 : 4) : nv <= 4 ? 3 : 2; }
+// Ring places of a lane, by its vectors of a row: one or two rows on their way.  (More make memory
+// slower: with two in place of one, 602k rows of 1024 took 413 us forward, so 368.)
+constexpr int stages(int nv) { return nv == 1 ? 3 : 2; }
 
 // Blocks per SM, by their registers (64, 80, 128 a thread).
 constexpr int per_sm(int nv) { return nv == 1 ? 4 : nv == 2 ? 3 : 2; }
@@ -46,7 +50,6 @@ struct LnArgs {
     int64_t n;
     int c;
     int lanes;      // lanes of a row: a power of two, at most kThreads
-    int64_t range;  // rows of a block
     Rows x, y;      // y: dx in the backward pass
     Rows gy, skip;
     const void* w;
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
     __shared__ float2 s_sum[2][kWarps];
     __shared__ float s_count[kWarps];
     using W = Vec<T>;
-    constexpr int V = 16 / (int)sizeof(T), H = W::H, kStages = stages(NV, BWD);
+    constexpr int V = 16 / (int)sizeof(T), H = W::H, kStages = stages(NV);
     constexpr bool kOpen = NV <= (BWD ? 1 : 2);
     constexpr int kPlace = PARTS * NV * kThreads;
     const int lane = threadIdx.x & (a.lanes - 1), sub = threadIdx.x / a.lanes;
@@ -156,12 +159,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
 #pragma unroll
     for (int i = 0; i < kAcc; ++i) gw[i] = gb[i] = filled<T>(0.f);
 
-    // the block's rows [r0, r1); this group's are r0 + sub, + per, ..; all groups take as many turns
-    const uint32_t r0 = (uint32_t)((int64_t)blockIdx.x * a.range), r1 = (uint32_t)min((int64_t)r0 + a.range, a.n);
-    const int turns = r1 > r0 ? (int)((r1 - r0 + per - 1) / per) : 0;
+    // this group's rows are blockIdx.x * per + sub, + the whole grid's, ..; all groups of a block take
+    // as many turns.  (Rows that are far apart in time lie far apart: with a range of rows to each block
+    // 602k rows of 1024 took 1021 us for both passes, so 968.)
+    const uint32_t r0 = blockIdx.x * per, r1 = (uint32_t)a.n, hop = gridDim.x * per;
+    const int turns = r1 > r0 ? (int)((r1 - r0 + hop - 1) / hop) : 0;
     const uint32_t ring = smem_u32(s_ring + threadIdx.x);
     const int byte = lane * 16, step = a.lanes * 16;  // of the lane's first vector, and to the next
-    uint32_t row = r0 + sub, ahead = row;             // this turn's, and the next to be sent for (r1 + 2^24 fits)
+    uint32_t row = r0 + sub, ahead = row;             // this turn's, and the next to be sent for (32 bits leave 2^31 behind the last row)
     auto fetch_next = [&](int place) {
         if (ahead < r1) {
             const uint32_t to = ring + place * kPlace * 16;
@@ -173,9 +178,11 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
                     if (i < mine) cp_async16(to + (p * NV + i) * kThreads * 16, from + i * step, 16);
             }
         }
-        ahead += per;
+        ahead += hop;
         cp_async_commit();
     };
+    for (int k = 0; k < kStages * PARTS; ++k)  // places that no row fills: zeros
+        for (int i = mine; i < NV; ++i) s_ring[(k * NV + i) * kThreads + threadIdx.x] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch_next(i);
 
@@ -184,14 +191,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
     const float2* const stats = reinterpret_cast<const float2*>(a.stats);
     if (BWD && row < r1) st = stats[row];
 #pragma unroll 1
-    for (int t = 0; t < turns; ++t, row += per) {
+    for (int t = 0; t < turns; ++t, row += hop) {
         const bool have = row < r1;
         cp_async_wait<kStages - 2>();
         fetch_next(place == 0 ? kStages - 1 : place - 1);  // the place before this one has been read and used
         const uint4* from = s_ring + place * kPlace + threadIdx.x;
-        const auto vec = [&](int part, int i) {
-            return unpack<T>(have && i < mine ? from[(part * NV + i) * kThreads] : make_uint4(0, 0, 0, 0));
-        };
+        // (Without a row: whatever was there.  It enters the sums of this group's lanes alone, which then
+        // go nowhere.)
+        const auto vec = [&](int part, int i) { return unpack<T>(from[(part * NV + i) * kThreads]); };
         if constexpr (!BWD) {
             W x[NV];
             float2 sum2 = make_float2(0.f, 0.f);
@@ -247,18 +254,20 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
                     }
             }
         } else {
-            const float2 r2 = make_float2(st.y, st.y), n2 = make_float2(-st.x, -st.x);
             const float rstd = st.y;
-            if (row + per < r1) st = stats[row + per];
+            const float2 r2 = make_float2(rstd, rstd), n2 = make_float2(-st.x * rstd, -st.x * rstd);
+            if (row + hop < r1) st = stats[row + hop];
             float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const W x = vec(0, i), g = vec(1, i), wf = w[i].get();
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
-                    const float2 z = mul2(add2(x.v[j], n2), r2);
-                    gw[i].v[j] = fma2(g.v[j], z, gw[i].v[j]);
-                    gb[i].v[j] = add2(gb[i].v[j], g.v[j]);
+                    const float2 z = fma2(x.v[j], r2, n2);
+                    if (have) {
+                        gw[i].v[j] = fma2(g.v[j], z, gw[i].v[j]);
+                        gb[i].v[j] = add2(gb[i].v[j], g.v[j]);
+                    }
                     const float2 gz = mul2(g.v[j], wf.v[j]);
                     s1 = add2(s1, gz);
                     s2 = fma2(gz, z, s2);
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
                         W o;
 #pragma unroll
                         for (int j = 0; j < H; ++j) {
-                            const float2 z = mul2(add2(x.v[j], n2), r2);
+                            const float2 z = fma2(x.v[j], r2, n2);
                             o.v[j] = fma2(z, c2, fma2(mul2(g.v[j], wf.v[j]), r2, c1));
                         }
                         if constexpr (PARTS == 3) {
@@ -331,10 +340,10 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
 }
 
 // Lanes of a row and vectors of a lane, up to 4, or 2 in the backward pass where several warps hold a
-// row (twice that for the widest): the fewest idle places; among equals the most lanes of one warp.
-// (bf16, 602k rows of 1024: forward and backward pass 1026 us with 4 vectors in one warp, 1115 with 2 in two,
-// 1183 with 1 in four.  150k rows of 4096: backward pass 736 us with 2 in eight warps, 1030 with 4 in
-// four; forward 431 with 4 in four, 638 with 2 in eight.)
+// row (twice that for the widest): the fewest idle places; among equals the fewest lanes from 8 (128 bytes) on,
+// which leaves fewer exchanges a row.  (bf16, both passes: 319k rows of 256 161 us with 8 lanes, 166 with
+// 32.  602k rows of 1024: 1026 with 4 vectors in one warp, 1115 with 2 in two, 1183 with 1 in four.  150k rows of
+// 4096: backward pass 736 with 2 in eight warps, 1030 with 4 in four; forward 431 with 4 in four, 638 with 2 in eight.)
 void shape(int vectors, bool bwd, int* lanes, int* nv) {
     int most = bwd && vectors > 4 * 32 ? 2 : 4;
     while ((vectors + kThreads - 1) / kThreads > most) most *= 2;
@@ -343,7 +352,7 @@ void shape(int vectors, bool bwd, int* lanes, int* nv) {
         const int k = (vectors + l - 1) / l;
         if (k > most) continue;
         const int used = k <= 4 ? k : 8;  // compiled: 1, 2, 3, 4, 8
-        if (l * used < best || (l * used == best && l <= 32)) {
+        if (l * used < best || (l * used == best && l <= 8)) {
             best = l * used;
             *lanes = l;
             *nv = used;
@@ -353,8 +362,7 @@ void shape(int vectors, bool bwd, int* lanes, int* nv) {
 }
 
 struct Launch {
-    int lanes, nv, per_sm, grid;
-    int64_t range;
+    int lanes, nv, grid;
     size_t smem;
 };
 
@@ -362,13 +370,10 @@ Launch plan(int64_t n, int c, int es, int parts, bool bwd, int sms) {
     Launch l{};
     shape(c * es / 16, bwd, &l.lanes, &l.nv);
     const int per = kThreads / l.lanes;
-    l.smem = (size_t)stages(l.nv, bwd) * parts * l.nv * kThreads * 16;
+    l.smem = (size_t)stages(l.nv) * parts * l.nv * kThreads * 16;
     if (bwd) l.smem = std::max(l.smem, (size_t)per * 2 * c * 4);
-    l.per_sm = std::max(1, std::min<int>(per_sm(l.nv), kMaxSmem / (int)(l.smem + 1536)));
-    const int64_t turns = std::max<int64_t>(1, (n + per - 1) / per);
-    const int64_t cap = (int64_t)sms * l.per_sm;
-    l.range = (turns + std::min(turns, cap) - 1) / std::min(turns, cap) * per;
-    l.grid = (int)std::max<int64_t>(1, (n + l.range - 1) / l.range);
+    const int blocks = std::max(1, std::min<int>(per_sm(l.nv), kMaxSmem / (int)(l.smem + 1536)));
+    l.grid = (int)std::max<int64_t>(1, std::min((n + per - 1) / per, (int64_t)sms * blocks));
     return l;
 }
 
@@ -424,7 +429,6 @@ int layer_norm(const LayerNorm& q, bool bwd, cudaStream_t s) {
     a.partial = sums ? q.partial : nullptr;
     const Launch l = plan(q.n, q.c, es, parts, bwd, q.sms);
     a.lanes = l.lanes;
-    a.range = l.range;
     const int st = q.dtype == VG_F32   ? launch<float>(a, l, parts, s)
                    : q.dtype == VG_F16 ? launch<__half>(a, l, parts, s)
                                        : launch<__nv_bfloat16>(a, l, parts, s);

@@ -5,14 +5,20 @@
 //
 // A run of tokens maps the state that enters it to the one that leaves it, h -> A h + B, and two
 // runs after one another make (A2 A1, A2 B1 + B2).  So a pass has three steps: every warp finds the
-// map of its 64 tokens (a lane has 4 bytes of channels, two 16-bit ones), and the block those of
-// its 512; the blocks' maps are joined, in a fixed order, into the state that enters each block; every
-// warp goes through its tokens from the state that enters it.  Warps need nothing of one another
-// in between, so loads stream.  Gate and x are read twice, the second time from the end of the data back,
-// whose last 100 MB the L2 still holds.  (A single pass, in which blocks publish their maps
-// and wait for those of the blocks before, reads them once, but the waiting cost more: with a tree of maps, tiles
-// held in shared memory and a tile published ahead, 602k tokens of 512 channels took 950 us forward,
-// 600 with the waits left out, and 4.9 M of 64 channels 1790.)
+// map of its tokens (up to 256; a lane has 4 bytes of channels, two 16-bit ones), and the block those of
+// its warps; the blocks' maps are joined, in a fixed order, into the state that enters each block; every
+// warp goes through its tokens from the state that enters it.  A warp copies its next 16 tokens into shared memory
+// while it works on these, and needs nothing of other warps, so loads stream.  The forward pass
+// keeps the state before every 16th token, from which the backward pass finds the others again.
+//
+// Bound by memory.  Gate and x (backward: gate and dy) are read twice, the second time from the end of the
+// data back, whose last 100 MB the L2 still holds: 602,492 tokens of 512 channels in bf16 take 205 us for
+// the maps (6.0 TB/s), 8 for the join and 285 for the pass (6.5 TB/s), backward 205, 10 and 530 (6.1 TB/s).
+// A single pass, in which blocks publish their maps and wait for those of the blocks before, reads them once, but
+// the waiting cost more: with a tree of maps, tiles held in shared memory and each tile's map published before the
+// last tile was finished, the forward pass took 950 us, 600 with the waits left out; 4.9 M tokens of 64 channels
+// took 1790, so 520.  Smaller pieces that stay in the L2 between the steps gain nothing either: with all of
+// its data there the last step is as slow (8.4 M more elements cost 6.5 us).
 //
 // Where a sequence begins, the map is constant (A = -1 marks it, h -> B), so that nothing, not
 // even a NaN, passes from one sequence to the next.  A warp's tokens are the same for all of its
@@ -33,7 +39,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = kScanCarryRows;      // looked up and loaded at once; a state is kept for each such run
 constexpr int kHalf = kTokens / 2;
-constexpr int kMaxRuns = 8;                  // runs of a warp (ScanArgs::runs), at most
+constexpr int kMaxRuns = 16;                 // runs of a warp (ScanArgs::runs), at most
 constexpr int kRowBytes = 128, kRunBytes = kTokens * kRowBytes;  // of an operand in a block
 constexpr int kStep = kRowBytes / 4, kOperand = kRunBytes / 4;  // words from a token, an operand to the next
 // Blocks per SM, by their shared memory and registers.
@@ -41,7 +47,7 @@ constexpr int per_sm(bool bwd) { return bwd ? 2 : 3; }
 // Shared memory of a block: two runs of `operands` a warp.
 constexpr size_t stage_bytes(int operands) { return (size_t)kWarps * 2 * operands * kRunBytes; }
 constexpr int kFoldTiles = 256;              // up to so many, blocks join the maps before them themselves
-constexpr int kJoinChannels = 8, kJoinParts = 128;  // of a block of k_scan_join
+constexpr int kJoinChannels = 4, kJoinParts = 256;  // of a block of k_scan_join
 static_assert(kTokens == 16, "a lane holds the row of one token, half of the lanes none");
 
 // Workspace: word 0 the error record, word 1 this call's verdict on its offsets; from byte 256 on the
@@ -578,9 +584,20 @@ __global__ void __launch_bounds__(kJoinChannels* kJoinParts) k_scan_join(const S
     const auto tile = [&](int i) { return (int64_t)(BWD ? a.tiles - 1 - i : i) * a.c + c; };
     dependents_may_start();
     wait_for_previous();
+    // `use(i, map)` for the range's tiles, some loads ahead
+    const auto each = [&](const auto& use) {
+        constexpr int kAhead = 8;
+        for (int i0 = t0; i0 < t1; i0 += kAhead) {
+            Map next[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) next[j] = a.tile_maps[tile(min(i0 + j, t1 - 1))];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i0 + j < t1) use(i0 + j, next[j]);
+        }
+    };
     Map m{1.f, 0.f};
-#pragma unroll 8
-    for (int i = t0; i < t1; ++i) m = then(m, a.tile_maps[tile(i)]);
+    each([&](int, Map next) { m = then(m, next); });
     int now = 0;
     s[0][part][cl] = m;
     __syncthreads();
@@ -591,13 +608,10 @@ __global__ void __launch_bounds__(kJoinChannels* kJoinParts) k_scan_join(const S
         __syncthreads();
     }
     float h = part > 0 ? s[now][part - 1][cl].b : 0.f;  // all maps from the first visit on are constant
-#pragma unroll 8
-    for (int i = t0; i < t1; ++i) {
-        const int64_t at = tile(i);
-        const Map next = a.tile_maps[at];
-        a.states[at] = h;
+    each([&](int i, Map next) {
+        a.states[tile(i)] = h;
         h = through(next, h);
-    }
+    });
 }
 
 // What enters this warp's tokens.  One tile: from the maps that the block has found itself.  A few:
@@ -814,9 +828,10 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(int64_t vectors, int per
     }
 }
 
-// Runs of a warp, 1, 2, 4 .. kMaxRuns: a round of blocks takes about the time of their runs and of three
-// more, in which nothing is at hand yet; the cut that takes the least.  (25,179 tokens of 256
-// channels in bf16: CUTS)
+// Runs of a warp, 1, 2, 4 .. kMaxRuns: the cut with the least time, reckoned in runs as those of the SM that has the
+// most of them, and three more for each round of blocks, in which nothing is at hand yet.  (bf16, both passes:
+// 25,179 tokens of 256 channels 63 us with 1 run a warp, 56 with 2, 54 with 2 forward and 4 backward; 319,057 of
+// 128 208 us with 4, 211 with 8, 218 with 16; 602,492 of 512 1260 us with 4, 1246 with 8, 1234 with 16.)
 struct Cut {
     int runs;
     int64_t tiles;
@@ -827,8 +842,9 @@ Cut cut_of(int64_t n, int c, int es, bool bwd, int sms) {
     int64_t least = INT64_MAX;
     for (int runs = 1; runs <= kMaxRuns; runs *= 2) {
         const int64_t tile = (int64_t)kWarps * kTokens * runs, tiles = std::max<int64_t>(1, (n + tile - 1) / tile);
-        const int64_t time = (tiles * blocks_c + slots - 1) / slots * (runs + 3);
-        if (time <= least) {
+        const int64_t blocks = tiles * blocks_c;
+        const int64_t time = (blocks + sms - 1) / sms * runs + (blocks + slots - 1) / slots * 3;
+        if (time < least) {
             least = time;
             best = Cut{runs, tiles};
         }
