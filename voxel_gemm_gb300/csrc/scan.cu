@@ -11,14 +11,14 @@
 // while it works on these, and needs nothing of other warps, so loads stream.  The forward pass
 // keeps the state before every 16th token, from which the backward pass finds the others again.
 //
-// Bound by memory.  Gate and x (backward: gate and dy) are read twice, the second time from the end of the
-// data back, whose last 100 MB the L2 still holds: 602,492 tokens of 512 channels in bf16 take 205 us for
-// the maps (6.0 TB/s), 8 for the join and 285 for the pass (6.5 TB/s), backward 205, 10 and 530 (6.1 TB/s).
-// A single pass, in which blocks publish their maps and wait for those of the blocks before, reads them once, but
-// the waiting cost more: with a tree of maps, tiles held in shared memory and each tile's map published before the
-// last tile was finished, the forward pass took 950 us, 600 with the waits left out; 4.9 M tokens of 64 channels
-// took 1790, so 520.  Smaller pieces that stay in the L2 between the steps gain nothing either: with all of
-// its data there the last step is as slow (8.4 M more elements cost 6.5 us).
+// Bound by memory.  Gate and x (backward: gate and dy) are read twice: 602,492 tokens of 512 channels in
+// bf16 take 205 us for the maps (6.0 TB/s), 10 for the join and 290 for the pass (6.6 TB/s), backward 205, 10
+// and 530 (6.0 TB/s).  A single pass, in which blocks publish their maps and wait for those of the blocks before,
+// reads them once, but the waiting cost more: with a tree of maps, tiles held in shared memory and each tile's map
+// published before the last tile was finished, the forward pass took 950 us, 600 with the waits left out; 4.9 M
+// tokens of 64 channels took 1790, so 520.  Smaller pieces that stay in the L2 between the steps gain nothing
+// either: with all of its data there the last step is as slow (8.4 M more elements cost 6.5 us).  Blocks that
+// go from unit to unit without a pause, each warp's next tokens sent for across them, took 581 and 851 us.
 //
 // Where a sequence begins, the map is constant (A = -1 marks it, h -> B), so that nothing, not
 // even a NaN, passes from one sequence to the next.  A warp's tokens are the same for all of its
@@ -655,8 +655,8 @@ __device__ __forceinline__ typename Lane<T>::Num entering(const ScanArgs& a, con
     return through(mine, through(all, L::fill(0.f)));
 }
 
-// Blocks of step 3 come in the order opposite to step 1's, and send for their first tokens while
-// the steps before still run.  False if the call's offsets are bad.
+// Blocks of step 3 send for their first tokens while the steps before still run.  False if the call's
+// offsets are bad.
 template <typename W>
 __device__ __forceinline__ bool begin_step(const ScanArgs& a, W& walk) {
     if (a.tiles > 1) {
@@ -680,8 +680,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(false)) k_scan_fwd(const Scan
     __shared__ Map s_maps[kWarps][32 * L::V];
     __shared__ CutSeqs s_seqs[kWarps];
     extern __shared__ __align__(128) char s_dyn[];
-    const int unit = gridDim.x - 1 - blockIdx.x;
-    const int tile = unit / a.blocks_c, block_c = unit - tile * a.blocks_c;
+    const int tile = blockIdx.x / a.blocks_c, block_c = blockIdx.x - tile * a.blocks_c;
     const Place p = place_of<L>(a, tile, block_c);
     CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
     char* const s_stages = s_dyn + (threadIdx.x >> 5) * 4 * kRunBytes;
@@ -722,8 +721,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(true)) k_scan_bwd(const ScanA
     __shared__ Map s_maps[kWarps][32 * L::V];
     __shared__ CutSeqs s_seqs[kWarps];
     extern __shared__ __align__(128) char s_dyn[];
-    const int unit = gridDim.x - 1 - blockIdx.x;
-    const int tile = unit / a.blocks_c, block_c = unit - tile * a.blocks_c;
+    const int tile = blockIdx.x / a.blocks_c, block_c = blockIdx.x - tile * a.blocks_c;
     const Place p = place_of<L>(a, tile, block_c);
     CutSeqs& seqs = s_seqs[threadIdx.x >> 5];
     char* const s_stages = s_dyn + (threadIdx.x >> 5) * 6 * kRunBytes;
