@@ -38,7 +38,7 @@ using namespace ptx;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = kScanCarryRows;      // looked up and loaded at once; a state is kept for each such run
-constexpr int kHalf = kTokens / 2;
+constexpr int kHalf = kTokens / 2;           // unrolled: two times 16 tokens of straight code did not stay in the instruction cache
 constexpr int kMaxRuns = 16;                 // runs of a warp (ScanArgs::runs), at most
 constexpr int kRowBytes = 128, kRunBytes = kTokens * kRowBytes;  // of an operand in a block
 constexpr int kStep = kRowBytes / 4, kOperand = kRunBytes / 4;  // words from a token, an operand to the next
@@ -86,28 +86,9 @@ __device__ __forceinline__ float mul_(float a, float b) { return a * b; }
 __device__ __forceinline__ float2 sub_(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 __device__ __forceinline__ float sub_(float a, float b) { return a - b; }
 
-template <typename N> struct Side;
-struct Rest;
-template <typename T> struct Lane;
-template <> struct Lane<float> {
-    using Num = float;
-    static constexpr int V = 1;
-    static __device__ __forceinline__ float unpack(uint32_t w) { return __uint_as_float(w); }
-    static __device__ __forceinline__ uint32_t pack(float x) { return __float_as_uint(x); }
-    static __device__ __forceinline__ float fill(float x) { return x; }
-    using Gate = Side<float>;
-    static __device__ __forceinline__ float load(const float* p) { return *p; }
-    static __device__ __forceinline__ void store(float* p, float x) { *p = x; }
-};
-template <typename T> struct Lane16 {
-    using Num = float2;
-    using Gate = Rest;
-    static constexpr int V = 2;
-    static __device__ __forceinline__ float2 fill(float x) { return make_float2(x, x); }
-    static __device__ __forceinline__ float2 load(const float* p) { return *reinterpret_cast<const float2*>(p); }
-    static __device__ __forceinline__ void store(float* p, float2 x) { *reinterpret_cast<float2*>(p) = x; }
-};
-template <> struct Lane<__half> : Lane16<__half> {
+// Two 16-bit numbers of a word.
+template <typename T> struct Pair;
+template <> struct Pair<__half> {
     static __device__ __forceinline__ float2 unpack(uint32_t w) {
         return __half22float2(*reinterpret_cast<const __half2*>(&w));
     }
@@ -116,7 +97,7 @@ template <> struct Lane<__half> : Lane16<__half> {
         return *reinterpret_cast<const uint32_t*>(&h);
     }
 };
-template <> struct Lane<__nv_bfloat16> : Lane16<__nv_bfloat16> {
+template <> struct Pair<__nv_bfloat16> {
     static __device__ __forceinline__ float2 unpack(uint32_t w) {
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
@@ -126,97 +107,182 @@ template <> struct Lane<__nv_bfloat16> : Lane16<__nv_bfloat16> {
     }
 };
 
-// What a token's gate does to a state.  Two forms:
+// What a token's gate does to a state.  No form lets a h lose what is small beside h, nor 1 - a what is small beside 1.
 //
-// Side: m = e / (1 + e) with e = exp(-|g|), the smaller of a = sigmoid(g) and 1 - a, held as m
-// (a = m, for g < 0) or as -m (a = 1 - m).  Everything follows without cancellation, but each use
-// has to look at the sign: twice the instructions.  For fp32.
+// Side, for fp32: m = e / (1 + e) with e = exp(-|g|), the smaller of a = sigmoid(g) and 1 - a, held as m
+// (a = m, for g < 0) or as -m (a = 1 - m).  Each use has to look at the sign.
 //
-// Rest: s = 1 - a = 1 / (1 + exp(g)), and a h = h - s h in one rounding.  Exact at s = 0 and 1,
-// and no coarser than the other where a is near one, so long memories keep their length; near s = 1 what is
-// left of a state is off by 2^-24 of the state (of h_{t-1}, not of what is left).  For 16-bit types, whose
-// floor is 6 or 10 bytes an element, some 30 or 50 instructions.
+// 16-bit types, with s = 1 - a = 1 / (1 + e), e = exp(g), do with fewer instructions.  s is good to 2^-22 of its size, and
+// h - s h has what an open gate leaves; of a nearly closed one's it misses what the rounding of s to 32 bits took, s d with
+// the reciprocal's residual d = s (1 + e) - 1, which one fused operation finds from s - 1 (s - 1 is exact for
+// s >= 1/2, and below its rounding is a share 2^-25 of s).
+// Rest adds s d h where a run of tokens has a gate below -3 (CLOSED): four instructions a pair of gates and one a use.
+// Above, h - s h alone is good to 3e-6 of a h.  (Without it all of a was lost at gates below -17, and 0.1 % of it at
+// -10; with it for every run 100,000 tokens of 256 channels took 54 and 90 us, forward and backward, so 50 and 77.)
+// The backward pass holds 16 gates, as one number each: Halves, 1 - a for an open gate and -a, a = e s, for the others.
 //
-// 16-bit types take the fast exponential and reciprocal, off by 2 units and |g| / 2^24, and by 1:
-// 1e-6 of s for |g| < 10, where the inputs have 2^-9 or 2^-12.
-template <typename N> struct Side {
-    using Held = N;
-    N m, one;  // one: 1 where a is 1 - m, 0 where it is m
-    static __device__ __forceinline__ float with_side(float m, float g) {
+// 16-bit types take the fast exponential and reciprocal, off by 2 units and |g| / 2^23, and by 1 (and exact at 1):
+// 1e-6 of a and s for |g| < 10, where the inputs have 2^-9 or 2^-12.  Gates are bounded at 88, where s is
+// already 0, so that the exponential stays finite.
+struct Side {
+    float m, one;  // one: 1 where a is 1 - m, 0 where it is m
+    static __device__ __forceinline__ uint32_t sign(float x) { return (int32_t)__float_as_uint(x) >> 31; }  // 0 or all ones
+    static __device__ __forceinline__ float hold(uint32_t word) {
+        const float g = __uint_as_float(word), e = expf(-fabsf(g)), m = e / (1.f + e);
         return __uint_as_float((__float_as_uint(m) & 0x7fffffffu) | (~__float_as_uint(g) & 0x80000000u));
     }
-    static __device__ __forceinline__ float hold(float g) {
-        const float e = expf(-fabsf(g));
-        return with_side(e / (1.f + e), g);
-    }
-    static __device__ __forceinline__ float2 hold(float2 g) {
-        float2 e, r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(fabsf(g.x) * -1.4426950408889634f));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(fabsf(g.y) * -1.4426950408889634f));
-        const float2 d = add2(e, make_float2(1.f, 1.f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
-        const float2 m = mul2(e, r);
-        return make_float2(with_side(m.x, g.x), with_side(m.y, g.y));
-    }
-    static __device__ __forceinline__ float near_one(float m) {
-        return __uint_as_float((uint32_t)((int32_t)__float_as_uint(m) >> 31) & 0x3f800000u);
-    }
-    static __device__ __forceinline__ float2 near_one(float2 m) { return make_float2(near_one(m.x), near_one(m.y)); }
-    static __device__ __forceinline__ float rest(float m, float one) { return (1.f - one) - m; }
-    static __device__ __forceinline__ float2 rest(float2 m, float2 one) {
-        const float2 n = make_float2(-1.f, -1.f), u = make_float2(1.f, 1.f);
-        return fma2(m, n, fma2(one, n, u));
-    }
-    static __device__ __forceinline__ float slope(float m) { return fmaf(-fabsf(m), fabsf(m), fabsf(m)); }
-    static __device__ __forceinline__ float2 slope(float2 m) { return make_float2(slope(m.x), slope(m.y)); }
-
-    __device__ __forceinline__ explicit Side(Held held) : m(held), one(near_one(held)) {}
-    // also a (1 - a)
-    static __device__ __forceinline__ Held hold(N g, N& slope_) {
-        const Held m = hold(g);
-        slope_ = slope(m);
+    // also a (1 - a) and 1 - a
+    static __device__ __forceinline__ float hold(uint32_t word, float& slope, float& rest) {
+        const float m = hold(word);
+        slope = fmaf(-fabsf(m), fabsf(m), fabsf(m));
+        rest = Side(m).rest();
         return m;
     }
-    __device__ __forceinline__ N kept(N h) const { return fma_(m, h, mul_(one, h)); }  // a h
-    __device__ __forceinline__ N rest() const { return rest(m, one); }                 // 1 - a
+    __device__ __forceinline__ explicit Side(uint32_t word) : Side(hold(word)) {}
+    __device__ __forceinline__ explicit Side(float held) : m(held) { one = __uint_as_float(sign(held) & 0x3f800000u); }
+    __device__ __forceinline__ float kept(float h) const { return fmaf(m, h, one * h); }  // a h
+    __device__ __forceinline__ float rest() const { return (1.f - one) - m; }             // 1 - a
+    __device__ __forceinline__ float rest_of(float h) const { return rest() * h; }
 };
-struct Rest {
-    using Held = float2;
-    float2 s, minus;
-    static __device__ __forceinline__ float2 over(float2 e) {  // 1 / (1 + e)
+
+__device__ __forceinline__ float2 negated(float2 x) { return mul2(x, make_float2(-1.f, -1.f)); }
+// Two gates' exp(g), and s.
+template <typename T> struct Exp {
+    float2 e, s;
+    // Bounded at 88 (NaN stays).
+    static __device__ __forceinline__ uint32_t bounded(uint32_t word) {
+        if constexpr (std::is_same_v<T, __half>)
+            asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(word) : "r"(0x55805580u));
+        else
+            asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(word) : "r"(0x42b042b0u));
+        return word;
+    }
+    // The smaller ones of two words' numbers, passing over NaN.
+    static __device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) {
+        if constexpr (std::is_same_v<T, __half>)
+            asm("min.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        else
+            asm("min.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        return a;
+    }
+    __device__ __forceinline__ explicit Exp(uint32_t word) {
+        const float2 y = mul2(Pair<T>::unpack(word), make_float2(1.4426950408889634f, 1.4426950408889634f));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
         const float2 d = add2(e, make_float2(1.f, 1.f));
-        float2 s;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
-        return s;
     }
-    static __device__ __forceinline__ float2 hold(float2 g) {
-        const float2 y = mul2(g, make_float2(1.4426950408889634f, 1.4426950408889634f));
-        float2 e;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
-        return over(e);
+};
+template <typename T, bool CLOSED> struct Rest {
+    float2 s, minus, missed;
+    __device__ __forceinline__ explicit Rest(uint32_t word) {
+        const Exp<T> x(CLOSED ? Exp<T>::bounded(word) : word);
+        s = x.s;
+        minus = negated(s);
+        if constexpr (CLOSED) missed = mul2(fma2(x.e, s, add2(s, make_float2(-1.f, -1.f))), s);
     }
-    // Also a (1 - a) = exp(g) s s, the exponent bounded so that infinity and zero do not meet (at the bound s is 0).
-    static __device__ __forceinline__ float2 hold(float2 g, float2& slope) {
-        float2 y = mul2(g, make_float2(1.4426950408889634f, 1.4426950408889634f)), e;
-        asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(y.x));  // 127
-        asm("min.NaN.f32 %0, %0, 0f42FE0000;" : "+f"(y.y));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
-        const float2 s = over(e);
-        slope = mul2(mul2(e, s), s);
-        return s;
+    __device__ __forceinline__ float2 kept(float2 h) const {
+        const float2 left = fma2(minus, h, h);
+        if constexpr (CLOSED) return fma2(missed, h, left);
+        return left;
     }
-    __device__ __forceinline__ explicit Rest(Held held) : s(held), minus(mul2(held, make_float2(-1.f, -1.f))) {}
-    __device__ __forceinline__ float2 kept(float2 h) const { return fma2(minus, h, h); }
     __device__ __forceinline__ float2 rest() const { return s; }
 };
+template <bool CLOSED> struct Halves {
+    float2 v;
+    uint32_t closed_x, closed_y;  // all ones where v is -a
+    template <typename T>
+    static __device__ __forceinline__ float2 hold(uint32_t word, float2& slope, float2& rest) {
+        const Exp<T> x(Exp<T>::bounded(word));
+        const float2 a = mul2(x.e, x.s);
+        slope = mul2(a, x.s);
+        rest = x.s;
+        if constexpr (!CLOSED) return x.s;
+        return make_float2(x.e.x < 1.f ? -a.x : x.s.x, x.e.y < 1.f ? -a.y : x.s.y);
+    }
+    __device__ __forceinline__ explicit Halves(float2 held) : v(held) {
+        closed_x = CLOSED ? Side::sign(held.x) : 0u;
+        closed_y = CLOSED ? Side::sign(held.y) : 0u;
+    }
+    static __device__ __forceinline__ float2 masked(float2 h, uint32_t x, uint32_t y) {
+        return make_float2(__uint_as_float(__float_as_uint(h.x) & x), __uint_as_float(__float_as_uint(h.y) & y));
+    }
+    __device__ __forceinline__ float2 kept(float2 h) const {
+        return fma2(negated(v), h, CLOSED ? masked(h, ~closed_x, ~closed_y) : h);
+    }
+    __device__ __forceinline__ float2 rest_of(float2 h) const {
+        if constexpr (!CLOSED) return mul2(v, h);
+        return fma2(v, h, masked(h, closed_x, closed_y));
+    }
+};
+
+// A lane's word of T, its gates (CLOSED: nearly closed ones may be among them; Kept: as the backward pass holds them),
+// and its states.
+template <typename T> struct Lane : Pair<T> {
+    using Num = float2;
+    template <bool CLOSED> using Gate = Rest<T, CLOSED>;
+    template <bool CLOSED> using Kept = Halves<CLOSED>;
+    static constexpr int V = 2;
+    template <bool CLOSED> static __device__ __forceinline__ float2 hold(uint32_t gate, float2& slope, float2& rest) {
+        return Halves<CLOSED>::template hold<T>(gate, slope, rest);
+    }
+    // Whether a gate of a run's tokens, for any lane, is below -3.
+    static __device__ __forceinline__ bool any_closed(const uint32_t* w) {
+        uint32_t least[kTokens];
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) least[k] = w[k * kStep];
+#pragma unroll
+        for (int d = kTokens / 2; d > 0; d /= 2)
+#pragma unroll
+            for (int k = 0; k < d; ++k) least[k] = Exp<T>::smaller(least[k], least[k + d]);
+        const float2 g = Pair<T>::unpack(least[0]);
+        return __any_sync(0xffffffffu, fminf(g.x, g.y) < -3.f);
+    }
+    // Numbers in place of a token's gate and input.
+    static __device__ __forceinline__ void stash(uint32_t* w, float2 x) {
+        w[0] = __float_as_uint(x.x);
+        w[kOperand] = __float_as_uint(x.y);
+    }
+    static __device__ __forceinline__ float2 stashed(const uint32_t* w) {
+        return make_float2(__uint_as_float(w[0]), __uint_as_float(w[kOperand]));
+    }
+    static __device__ __forceinline__ float2 fill(float x) { return make_float2(x, x); }
+    static __device__ __forceinline__ float2 load(const float* p) { return *reinterpret_cast<const float2*>(p); }
+    static __device__ __forceinline__ void store(float* p, float2 x) { *reinterpret_cast<float2*>(p) = x; }
+};
+template <> struct Lane<float> {
+    using Num = float;
+    template <bool CLOSED> using Gate = Side;
+    template <bool CLOSED> using Kept = Side;
+    static constexpr int V = 1;
+    template <bool CLOSED> static __device__ __forceinline__ float hold(uint32_t gate, float& slope, float& rest) {
+        return Side::hold(gate, slope, rest);
+    }
+    static __device__ __forceinline__ bool any_closed(const uint32_t*) { return true; }
+    static __device__ __forceinline__ void stash(uint32_t* w, float x) { w[0] = __float_as_uint(x); }
+    static __device__ __forceinline__ float stashed(const uint32_t* w) { return __uint_as_float(w[0]); }
+    static __device__ __forceinline__ float unpack(uint32_t w) { return __uint_as_float(w); }
+    static __device__ __forceinline__ uint32_t pack(float x) { return __float_as_uint(x); }
+    static __device__ __forceinline__ float fill(float x) { return x; }
+    static __device__ __forceinline__ float load(const float* p) { return *p; }
+    static __device__ __forceinline__ void store(float* p, float x) { *p = x; }
+};
+// go(simple, closed, ..) for a run, by what its tokens are.
+template <typename L, typename R, typename Go>
+__device__ __forceinline__ void by_kind(const R& r, const uint32_t* w, const Go& go) {
+    if (!r.simple)
+        go(std::false_type{}, std::true_type{});
+    else if (L::any_closed(w))
+        go(std::true_type{}, std::true_type{});
+    else
+        go(std::true_type{}, std::false_type{});
+}
+
 // The state after a token.
-template <bool FREE, typename G, typename N> __device__ __forceinline__ N next_state(const G& g, N x, N h) {
+template <bool FREE, typename G, typename N> __device__ __forceinline__ N next_state(const G& g, N rest, N x, N h) {
     if constexpr (FREE) return add_(g.kept(h), x);
-    return fma_(g.rest(), x, g.kept(h));
+    return fma_(rest, x, g.kept(h));
 }
 
 // ---------------------------------------------------------------- beginnings and ends of sequences
@@ -461,7 +527,7 @@ struct Walk {
                        __all_sync(0xffffffffu, row >= 0 || lane >= kTokens);
             cp_async_wait<1>();
             __syncwarp();
-            use(r, reinterpret_cast<const uint32_t*>(stages + (i & 1) * P * kRunBytes) + lane);
+            use(r, reinterpret_cast<uint32_t*>(stages + (i & 1) * P * kRunBytes) + lane);
             __syncwarp();
             row = next;
             next = later;
@@ -486,21 +552,24 @@ __device__ __forceinline__ Maps<Lane<T>::V> warp_map(const ScanArgs& a, const Pl
                                                      CutSeqs& seqs) {
     using L = Lane<T>;
     using N = typename L::Num;
-    using G = typename L::Gate;
     N A = L::fill(1.f), B = L::fill(0.f);
     bool constant = false;
-    const auto go = [&](auto simple, const Run& r, const uint32_t* w) {
+    const auto go = [&](auto simple, auto closed, const Run& r, const uint32_t* w) {
         const uint32_t resets = BWD ? r.cuts.end : r.cuts.begin;
+#pragma unroll 1
+        for (int b = 0; b < kTokens; b += kHalf) {
 #pragma unroll
-        for (int j = 0; j < kTokens; ++j) {
-            const int k = BWD ? kTokens - 1 - j : j;
-            if (simple || k < r.count) {
-                const G g(G::hold(L::unpack(w[k * kStep])));
-                const N v = L::unpack(w[kOperand + k * kStep]);
-                if (!simple && (resets >> k & 1))
-                    B = BWD ? state_of<L>(a, a.glast, seqs.end(r.cuts, k), p) : state_of<L>(a, a.first, seqs.begin[k], p);
-                B = BWD ? g.kept(add_(B, v)) : next_state<FREE>(g, v, B);
-                A = g.kept(A);
+            for (int j = 0; j < kHalf; ++j) {
+                const int k = BWD ? kTokens - 1 - b - j : b + j;
+                if (simple || k < r.count) {
+                    const typename L::template Gate<closed> g(w[k * kStep]);
+                    const N v = L::unpack(w[kOperand + k * kStep]);
+                    if (!simple && (resets >> k & 1))
+                        B = BWD ? state_of<L>(a, a.glast, seqs.end(r.cuts, k), p)
+                                : state_of<L>(a, a.first, seqs.begin[k], p);
+                    B = BWD ? g.kept(add_(B, v)) : next_state<FREE>(g, g.rest(), v, B);
+                    A = g.kept(A);
+                }
             }
         }
         constant |= resets != 0;
@@ -508,10 +577,7 @@ __device__ __forceinline__ Maps<Lane<T>::V> warp_map(const ScanArgs& a, const Pl
     Walk<T, 2, BWD> walk{a, p, {a.gate, BWD ? a.gy : a.x}, {a.gate_s, BWD ? a.gy_s : a.x_s}, s_stages};
     walk.start();
     walk.go(seqs, nullptr, nullptr, [&](const Run& r, const uint32_t* w) {
-        if (r.simple)
-            go(std::true_type{}, r, w);
-        else
-            go(std::false_type{}, r, w);
+        by_kind<L>(r, w, [&](auto simple, auto closed) { go(simple, closed, r, w); });
     });
     return maps_of(A, B, constant);
 }
@@ -676,7 +742,6 @@ template <typename T, bool FREE>
 __global__ void __launch_bounds__(kThreads, per_sm(false)) k_scan_fwd(const ScanArgs a) {
     using L = Lane<T>;
     using N = typename L::Num;
-    using G = typename L::Gate;
     __shared__ Map s_maps[kWarps][32 * L::V];
     __shared__ CutSeqs s_seqs[kWarps];
     extern __shared__ __align__(128) char s_dyn[];
@@ -689,13 +754,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(false)) k_scan_fwd(const Scan
     N h = entering<T, FREE, false>(a, p, tile, s_maps, s_stages, seqs);
     if (a.tiles == 1) walk.start();
     char* const out = a.out + p.c * (int)sizeof(T);
-    const auto go = [&](auto simple, const Run& r, const uint32_t* w) {
+    const auto go = [&](auto simple, auto closed, const Run& r, const uint32_t* w) {
 #pragma unroll
         for (int k = 0; k < kTokens; ++k) {
             const int32_t row = row_at(r, k);
             if (simple || k < r.count) {
                 if (!simple && (r.cuts.begin >> k & 1)) h = state_of<L>(a, a.first, seqs.begin[k], p);
-                h = next_state<FREE>(G(G::hold(L::unpack(w[k * kStep]))), L::unpack(w[kOperand + k * kStep]), h);
+                const typename L::template Gate<closed> g(w[k * kStep]);
+                h = next_state<FREE>(g, g.rest(), L::unpack(w[kOperand + k * kStep]), h);
                 if (p.real && (simple || row >= 0)) put<L>(out, row, a.out_s, h);
                 if (!simple && a.last && p.real && (r.cuts.end >> k & 1))
                     L::store(a.last + (int64_t)seqs.end(r.cuts, k) * a.c + p.c, h);
@@ -704,10 +770,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(false)) k_scan_fwd(const Scan
     };
     walk.go(seqs, a.first, a.last, [&](const Run& r, const uint32_t* w) {
         if (a.carries && p.real && r.count > 0) L::store(a.carries + (int64_t)(r.lo / kTokens) * a.c + p.c, h);
-        if (r.simple)
-            go(std::true_type{}, r, w);
-        else
-            go(std::false_type{}, r, w);
+        by_kind<L>(r, w, [&](auto simple, auto closed) { go(simple, closed, r, w); });
     });
 }
 
@@ -717,7 +780,6 @@ template <typename T, bool FREE>
 __global__ void __launch_bounds__(kThreads, per_sm(true)) k_scan_bwd(const ScanArgs a) {
     using L = Lane<T>;
     using N = typename L::Num;
-    using G = typename L::Gate;
     __shared__ Map s_maps[kWarps][32 * L::V];
     __shared__ CutSeqs s_seqs[kWarps];
     extern __shared__ __align__(128) char s_dyn[];
@@ -731,42 +793,45 @@ __global__ void __launch_bounds__(kThreads, per_sm(true)) k_scan_bwd(const ScanA
     if (a.tiles == 1) walk.start();
     char* const gg = a.gg + p.c * (int)sizeof(T);
     char* const gx = a.out + p.c * (int)sizeof(T);
-    const auto go = [&](auto simple, const Run& r, const uint32_t* w, N state) {
-        // A half of the run at a time, the second one first, for which the first one's gates are looked at
-        // twice.  (16 tokens at once do not fit 128 registers, and beside 200 KB of shared memory the
-        // L1 has no room for what is spilled: 602k tokens of 512 channels took 935 us.)
-        N from = state;
+    const auto go = [&](auto simple, auto closed, const Run& r, uint32_t* w, N from) {
+        using G = typename L::template Kept<closed>;
+        // Up the run, the gates held and a (1 - a) (h_{t-1} - x) put where this lane has read a token's gate and
+        // input; then down.  (What is held of 16 tokens leaves no registers for these as well, and beside 200 KB of
+        // shared memory the L1 has no room for what would be spilled.)  `held` is the half in hand, `other` the other one.
+        N held[kHalf], other[kHalf];
 #pragma unroll
-        for (int k = 0; k < kHalf; ++k) {
-            if (simple || k < r.count) {
-                if (!simple && (r.cuts.begin >> k & 1)) from = state_of<L>(a, a.first, seqs.begin[k], p);
-                from = next_state<FREE>(G(G::hold(L::unpack(w[k * kStep]))), L::unpack(w[kOperand + k * kStep]), from);
-            }
-        }
+        for (int k = 0; k < kHalf; ++k) held[k] = L::fill(0.f);
 #pragma unroll 1
-        for (int b = kHalf; b >= 0; b -= kHalf) {
-            typename G::Held held[kHalf];
-            N turn[kHalf];  // a (1 - a) (h_{t-1} - x)
-            const uint32_t* const u = w + b * kStep;
+        for (int b = 0; b < kTokens; b += kHalf) {
+            uint32_t* const half = w + b * kStep;
+#pragma unroll
+            for (int k = 0; k < kHalf; ++k) other[k] = held[k];
 #pragma unroll
             for (int k = 0; k < kHalf; ++k) {
                 if (simple || b + k < r.count) {
                     if (!simple && (r.cuts.begin >> (b + k) & 1)) from = state_of<L>(a, a.first, seqs.begin[b + k], p);
-                    const N x = L::unpack(u[kOperand + k * kStep]);
-                    held[k] = G::hold(L::unpack(u[k * kStep]), turn[k]);
-                    turn[k] = mul_(turn[k], FREE ? from : sub_(from, x));
-                    from = next_state<FREE>(G(held[k]), x, from);
+                    uint32_t* const u = half + k * kStep;
+                    const N x = L::unpack(u[kOperand]);
+                    N slope, rest;
+                    held[k] = L::template hold<closed>(u[0], slope, rest);
+                    L::stash(u, mul_(slope, FREE ? from : sub_(from, x)));
+                    from = next_state<FREE>(G(held[k]), rest, x, from);
                 }
             }
+        }
+#pragma unroll 1
+        for (int b = kTokens - kHalf; b >= 0; b -= kHalf) {
+            const uint32_t* const half = w + b * kStep;
 #pragma unroll
             for (int k = kHalf - 1; k >= 0; --k) {
                 const int32_t row = row_at(r, b + k);
                 if (simple || b + k < r.count) {
                     if (!simple && (r.cuts.end >> (b + k) & 1))
                         mu = state_of<L>(a, a.glast, seqs.end(r.cuts, b + k), p);
+                    const uint32_t* const u = half + k * kStep;
                     const G g(held[k]);
-                    const N lam = add_(mu, L::unpack(u[2 * kOperand + k * kStep]));
-                    const N dg = mul_(turn[k], lam), dx = FREE ? lam : mul_(g.rest(), lam);
+                    const N lam = add_(mu, L::unpack(u[2 * kOperand]));
+                    const N dg = mul_(L::stashed(u), lam), dx = FREE ? lam : g.rest_of(lam);
                     mu = g.kept(lam);
                     if (p.real && (simple || row >= 0)) {
                         put<L>(gg, row, a.gg_s, dg);
@@ -776,7 +841,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(true)) k_scan_bwd(const ScanA
                         L::store(a.gfirst + (int64_t)seqs.begin[b + k] * a.c + p.c, mu);
                 }
             }
-            from = state;
+#pragma unroll
+            for (int k = 0; k < kHalf; ++k) held[k] = other[k];
         }
     };
     const auto carry = [&](int q) {  // the state before run q
@@ -785,13 +851,10 @@ __global__ void __launch_bounds__(kThreads, per_sm(true)) k_scan_bwd(const ScanA
     };
     int q = a.runs - 1;
     N coming = carry(q);
-    walk.go(seqs, a.glast, a.gfirst, [&](const Run& r, const uint32_t* w) {
+    walk.go(seqs, a.glast, a.gfirst, [&](const Run& r, uint32_t* w) {
         const N state = coming;
         coming = carry(--q);
-        if (r.simple)
-            go(std::true_type{}, r, w, state);
-        else
-            go(std::false_type{}, r, w, state);
+        by_kind<L>(r, w, [&](auto simple, auto closed) { go(simple, closed, r, w, state); });
     });
 }
 
@@ -801,7 +864,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(int64_t vectors, int per
                                                         int64_t gate_s, const char* x, int64_t x_s, float* state,
                                                         char* out, int64_t out_s) {
     using L = Lane<T>;
-    using G = typename L::Gate;
+    using G = typename L::template Gate<true>;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < vectors; i += (int64_t)gridDim.x * kThreads) {
         const int64_t r = i / per_row;
         const int at = (int)(i - r * per_row);
@@ -816,8 +879,8 @@ __global__ void __launch_bounds__(kThreads) k_scan_step(int64_t vectors, int per
         uint32_t* xw = reinterpret_cast<uint32_t*>(&xv);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const G g(G::hold(L::unpack(gw[j])));
-            hn[j] = next_state<FREE>(g, L::unpack(xw[j]), hn[j]);
+            const G g(gw[j]);
+            hn[j] = next_state<FREE>(g, g.rest(), L::unpack(xw[j]), hn[j]);
             gw[j] = L::pack(hn[j]);
         }
 #pragma unroll
