@@ -594,8 +594,9 @@ typedef struct {
     const int32_t* order;        /* [n], device, or NULL                                       */
 } vg_scan;
 
-/* Bytes of workspace of vg_gated_scan_fwd and _bwd (0 if the arguments are invalid; the pointers
- * are not looked at).  Calls that may overlap on the GPU need a workspace each. */
+/* Bytes of workspace of vg_gated_scan_fwd and _bwd (0 if the arguments are invalid; the pointers, flags
+ * and batch make no difference).  No less for more rows of as many channels: a workspace for the most rows
+ * serves calls of fewer.  Calls that may overlap on the GPU need a workspace each. */
 VG_API size_t vg_gated_scan_workspace_bytes(const vg_scan* s);
 /* Rows of `carries` (fp32 [rows][C], 16-byte aligned), the states that the forward pass keeps for
  * the backward pass: one for every 16 positions. */

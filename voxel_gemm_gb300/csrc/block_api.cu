@@ -420,6 +420,7 @@ int vg_gated_scan_fwd(const vg_scan* s, const vg_rows* gate, const vg_rows* x, c
     g.last = last;
     g.carries = carries;
     g.ws = static_cast<char*>(ws);
+    g.ws_bytes = ws_bytes;
     g.sms = plan_sms(0);
     return gated_scan(g, false, static_cast<cudaStream_t>(stream));
 }
@@ -446,6 +447,7 @@ int vg_gated_scan_bwd(const vg_scan* s, const vg_rows* gate, const vg_rows* x, c
     g.out = grad_x;
     g.grad_first = grad_first;
     g.ws = static_cast<char*>(ws);
+    g.ws_bytes = ws_bytes;
     g.sms = plan_sms(0);
     return gated_scan(g, true, static_cast<cudaStream_t>(stream));
 }

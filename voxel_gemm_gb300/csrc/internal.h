@@ -211,9 +211,11 @@ struct GatedScan {
     const float *first, *grad_last;
     float *last, *carries, *grad_first;
     char* ws;
+    size_t ws_bytes;
     int sms;
 };
 constexpr int kScanCarryRows = 16;
+// No less for more tokens of as many channels.
 size_t gated_scan_workspace_bytes(int64_t n, int c, int dtype, int sms);
 int gated_scan(const GatedScan& g, bool bwd, cudaStream_t s);
 int gated_scan_step(int64_t n, int c, int dtype, bool free_input, const vg_rows& gate, const vg_rows& x, float* state,

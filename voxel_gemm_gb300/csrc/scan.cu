@@ -913,6 +913,28 @@ Cut cut_of(int64_t n, int c, int es, bool bwd, int sms) {
     return best;
 }
 
+// The most tiles that cut_of gives any call of up to n tokens, or a few times that: never fewer for more tokens, so that one
+// workspace serves all shorter calls.  With b = tiles * blocks_c, a cut of `runs` is taken only where its time, at least
+// b runs / sms + 3 b / slots, is at most that of `more` runs, below (b' / sms + 1) more + 3 (b' / slots + 1) with
+// b' <= b runs / more + blocks_c; solved for the tiles.
+int64_t most_tiles(int64_t n, int c, int es, bool bwd, int sms) {
+    const int64_t blocks_c = (c * es + kRowBytes - 1) / kRowBytes, slots = (int64_t)sms * per_sm(bwd);
+    int64_t most = 1;
+    for (int runs = 1; runs <= kMaxRuns; runs *= 2) {
+        const int64_t tile = (int64_t)kWarps * kTokens * runs;
+        int64_t tiles = (n + tile - 1) / tile;
+        for (int more = 2 * runs; more <= kMaxRuns; more *= 2)
+            tiles = std::min(tiles, ((more + 3) * slots + blocks_c * (more * per_sm(bwd) + 3)) * more /
+                                        (3 * blocks_c * (more - runs)));
+        most = std::max(most, tiles);
+    }
+    return most;
+}
+// Of a call of so many tiles; more for more of them.
+size_t workspace_of(int64_t tiles, int c) {
+    return align_up(256 + (tiles > 1 ? (size_t)tiles * c * ((1 + kWarps) * sizeof(Map) + sizeof(float)) : 0), 256);
+}
+
 template <typename K>
 bool allow(K kernel, size_t smem) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
@@ -947,8 +969,7 @@ int launch(const ScanArgs& a, bool free_input, bool bwd, cudaStream_t s) {
 
 size_t gated_scan_workspace_bytes(int64_t n, int c, int dtype, int sms) {
     const int es = dtype == VG_F32 ? 4 : 2;
-    const int64_t tiles = std::max(cut_of(n, c, es, false, sms).tiles, cut_of(n, c, es, true, sms).tiles);
-    return align_up(256 + (tiles > 1 ? (size_t)tiles * c * ((1 + kWarps) * sizeof(Map) + sizeof(float)) : 0), 256);
+    return workspace_of(std::max(most_tiles(n, c, es, false, sms), most_tiles(n, c, es, true, sms)), c);
 }
 
 int gated_scan(const GatedScan& q, bool bwd, cudaStream_t s) {
@@ -984,6 +1005,7 @@ int gated_scan(const GatedScan& q, bool bwd, cudaStream_t s) {
     const int64_t tiles = cut.tiles;
     a.runs = cut.runs;
     if (tiles * a.blocks_c >= (int64_t(1) << 31)) return VG_ERR_UNSUPPORTED;
+    if (workspace_of(tiles, a.c) > q.ws_bytes) return VG_ERR_WORKSPACE_TOO_SMALL;
     a.tiles = (int)tiles;
     a.tile_maps = reinterpret_cast<Map*>(q.ws + 256);
     a.warp_maps = a.tile_maps + tiles * a.c;

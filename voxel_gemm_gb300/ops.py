@@ -747,7 +747,7 @@ def layer_norm_workspace(n, channels, device="cuda") -> torch.Tensor:
 
 
 def gated_scan_workspace(n, channels, batch, dtype, device="cuda") -> torch.Tensor:
-    """Workspace of vg_gated_scan_fwd and _bwd, its error record zero."""
+    """Workspace of vg_gated_scan_fwd and _bwd, its error record zero; it serves calls of fewer rows too."""
     nb = int(lib().vg_gated_scan_workspace_bytes(ScanStruct(n, channels, batch, _DT.get(dtype, -1), 0, None, None)))
     if nb == 0:
         raise VGError(VG_ERR_INVALID_ARG, "vg_gated_scan_workspace_bytes")
