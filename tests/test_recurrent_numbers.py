@@ -1,0 +1,35 @@
+"""Numbers that the C entry points would take only in part are refused (CPU only; no call here is complete)."""
+import pytest
+import torch
+
+from test_binding_devices import gpu
+
+from voxel_gemm_gb300 import ops
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from voxel_gemm_gb300 import build
+    build.build()
+
+
+@pytest.mark.parametrize("call", [-1, 2 ** 32, 2 ** 32 + 3, 2 ** 64])
+def test_a_call_number_beyond_32_bits(call):
+    """Its mask would be another call's.  (On the CPU: what is on the GPU only by name would be refused later.)"""
+    x, rng = gpu(torch.zeros(64)), gpu(torch.zeros(2, dtype=torch.int64))
+    bad = torch.zeros(64)                       # were the number taken, this operand would be refused by name of the GPU
+    with pytest.raises(ValueError, match="32 bits"):
+        ops.vg_dropout_add_fwd(x, None, 0.5, rng, call, bad)
+    with pytest.raises(ValueError, match="32 bits"):
+        ops.vg_dropout_add_bwd(x, 0.5, rng, call, bad)
+
+
+@pytest.mark.parametrize("flags", [-1, 2 ** 32, 2 ** 32 + ops.VG_SCAN_REVERSE])
+def test_flags_beyond_32_bits(flags):
+    x, off = gpu(torch.zeros(4, 64)), gpu(torch.tensor([0, 4], dtype=torch.int32))
+    ws, bad = gpu(torch.zeros(4096, dtype=torch.uint8)), torch.zeros(4, 64)
+    for f in (lambda: ops.vg_gated_scan_fwd(x, x, off, None, None, bad, None, None, ws, flags=flags),
+              lambda: ops.vg_gated_scan_bwd(x, x, off, None, None, None, x, None, x, bad, None, ws, flags=flags),
+              lambda: ops.vg_gated_scan_step(x, x, x, bad, flags=flags)):
+        with pytest.raises(ValueError, match="32 bits"):
+            f()

@@ -739,6 +739,13 @@ def vg_layer_norm_bwd(x, weight, stats, grad_y, grad_skip, grad_x, grad_weight, 
            "vg_layer_norm_bwd")
 
 
+def _word(number, what):
+    """A whole number that C takes as one of 32 bits (ctypes would cut off the rest)."""
+    if not 0 <= number < 1 << 32:
+        raise ValueError(f"{what} must be a whole number of 32 bits, got {number}")
+    return number
+
+
 def layer_norm_workspace(n, channels, device="cuda") -> torch.Tensor:
     nb = int(lib().vg_layer_norm_workspace_bytes(n, channels))
     if nb == 0:
@@ -767,7 +774,7 @@ def _scan(gate, offsets, order, carries, ws, flags, stream, what):
     batch = offsets.numel() - 1
     f32 = torch.float32
     rows = -(-n // VG_SCAN_CARRY_ROWS)
-    return (ScanStruct(n, c, batch, _DT.get(dt, -1), flags, _flat(offsets, torch.int32, (batch + 1,), dev, "offsets"),
+    return (ScanStruct(n, c, batch, _DT.get(dt, -1), _word(flags, "flags"), _flat(offsets, torch.int32, (batch + 1,), dev, "offsets"),
                        _flat(order, torch.int32, (n,), dev, "order")), (n, c), (batch, c), dt, dev,
             _flat(carries, f32, (rows, c), dev, "carries"))
 
@@ -803,7 +810,7 @@ def vg_gated_scan_bwd(gate, x, offsets, order, first, carries, grad_out, grad_la
 def vg_gated_scan_step(gate, x, state, out, flags=0, stream=None) -> None:
     """One token of each of the rows' sequences: state float32 [rows, channels] goes from h_{t-1} to h_t, out = h_t."""
     s, dt, dev = _matrix(gate, stream, "vg_gated_scan_step")
-    _check(lib().vg_gated_scan_step(s[0], s[1], _DT.get(dt, -1), flags, _rows(gate, dt, s, dev, "gate"),
+    _check(lib().vg_gated_scan_step(s[0], s[1], _DT.get(dt, -1), _word(flags, "flags"), _rows(gate, dt, s, dev, "gate"),
                                     _rows(x, dt, s, dev, "x"), _flat(state, torch.float32, s, dev, "state"),
                                     _rows(out, dt, s, dev, "out"), _s(stream)), "vg_gated_scan_step")
 
@@ -820,13 +827,13 @@ def _dropout(name, x, residual, p, rng, call, out, stream):
     args = [x.numel(), _dtype_code(x), _flat(x, dt, x.shape, dev, "input")]
     if name == "vg_dropout_add_fwd":
         args.append(_flat(residual, dt, x.shape, dev, "residual"))
-    _check(getattr(lib(), name)(*args, p, _flat(rng, rng.dtype, (2,), dev, "rng"), call,
+    _check(getattr(lib(), name)(*args, p, _flat(rng, rng.dtype, (2,), dev, "rng"), _word(call, "call"),
                                 _flat(out, dt, x.shape, dev, "output"), _s(stream)), name)
 
 
 def vg_dropout_add_fwd(x, residual, p, rng, call, out, stream=None) -> None:
-    """out = residual + dropout(x); residual may be None.  rng int64 [2] on the GPU: (seed, step); call, a number that
-    tells this call's mask from the others of the step."""
+    """out = residual + dropout(x); residual may be None.  rng int64 [2] on the GPU: (seed, step); call, a number of
+    32 bits that tells this call's mask from the others of the step."""
     _dropout("vg_dropout_add_fwd", x, residual, p, rng, call, out, stream)
 
 
