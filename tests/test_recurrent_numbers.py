@@ -1,4 +1,6 @@
 """Numbers that the C entry points would take only in part are refused (CPU only; no call here is complete)."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -33,3 +35,15 @@ def test_flags_beyond_32_bits(flags):
               lambda: ops.vg_gated_scan_step(x, x, x, bad, flags=flags)):
         with pytest.raises(ValueError, match="32 bits"):
             f()
+
+
+def test_no_workspace():
+    """The library's status, as for any other argument that is missing."""
+    x, off = gpu(torch.zeros(4, 64)), gpu(torch.tensor([0, 4], dtype=torch.int32))
+    h, kept = gpu(torch.zeros(1, 64)), gpu(torch.zeros(1, 64))
+    s = SimpleNamespace(cuda_stream=0, device_index=0)
+    for f in (lambda: ops.vg_gated_scan_fwd(x, x, off, None, None, x, h, kept, None, stream=s),
+              lambda: ops.vg_gated_scan_bwd(x, x, off, None, None, kept, x, None, x, x, h, None, stream=s)):
+        with pytest.raises(ops.VGError) as e:
+            f()
+        assert e.value.status == ops.VG_ERR_INVALID_ARG

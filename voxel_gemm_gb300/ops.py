@@ -790,7 +790,7 @@ def vg_gated_scan_fwd(gate, x, offsets, order, first, out, last, carries, ws, fl
     _check(lib().vg_gated_scan_fwd(a, _rows(gate, dt, s, dev, "gate"), _rows(x, dt, s, dev, "x"),
                                    _flat(first, torch.float32, b, dev, "first"), _rows(out, dt, s, dev, "out"),
                                    _flat(last, torch.float32, b, dev, "last"), kept, _p(ws),
-                                   ws.numel() * ws.element_size(), _s(stream)), "vg_gated_scan_fwd")
+                                   0 if ws is None else ws.numel() * ws.element_size(), _s(stream)), "vg_gated_scan_fwd")
 
 
 def vg_gated_scan_bwd(gate, x, offsets, order, first, carries, grad_out, grad_last, grad_gate, grad_x, grad_first, ws,
@@ -804,7 +804,7 @@ def vg_gated_scan_bwd(gate, x, offsets, order, first, carries, grad_out, grad_la
                                    _flat(grad_last, torch.float32, b, dev, "grad_last"),
                                    _rows(grad_gate, dt, s, dev, "grad_gate"), _rows(grad_x, dt, s, dev, "grad_x"),
                                    _flat(grad_first, torch.float32, b, dev, "grad_first"), _p(ws),
-                                   ws.numel() * ws.element_size(), _s(stream)), "vg_gated_scan_bwd")
+                                   0 if ws is None else ws.numel() * ws.element_size(), _s(stream)), "vg_gated_scan_bwd")
 
 
 def vg_gated_scan_step(gate, x, state, out, flags=0, stream=None) -> None:
