@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
             }
         } else {
             const float rstd = st.y;
-            const float2 r2 = make_float2(rstd, rstd), n2 = make_float2(-st.x * rstd, -st.x * rstd);
+            const float2 r2 = make_float2(rstd, rstd), n2 = make_float2(-st.x, -st.x);
             if (row + hop < r1) st = stats[row + hop];
             float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
                 const W x = vec(0, i), g = vec(1, i), wf = w[i].get();
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
-                    const float2 z = fma2(x.v[j], r2, n2);
+                    const float2 z = mul2(add2(x.v[j], n2), r2);  // as forward: mean rstd would be rounded too
                     if (have) {
                         gw[i].v[j] = fma2(g.v[j], z, gw[i].v[j]);
                         gb[i].v[j] = add2(gb[i].v[j], g.v[j]);
@@ -285,25 +285,31 @@ __global__ void __launch_bounds__(kThreads, per_sm(NV)) k_layer_norm(const LnArg
                     a2 += buf[w0 + k].y;
                 }
             }
-            a1 *= -a.inv_c * rstd;
+            a1 *= -a.inv_c;
             a2 *= -a.inv_c * rstd;
-            if (have) {  // dx = rstd g - z (mean(g z) rstd) - mean(g) rstd, from the ring once more
+            if (have) {  // dx = rstd (g - mean(g) - (x - mean) (mean(g z) rstd)), from the ring once more
                 const float2 c1 = make_float2(a1, a1), c2 = make_float2(a2, a2);
                 char* const y = const_cast<char*>(at(a.y, row, byte));
+                int place_again = 0;
+                asm volatile("" : "+r"(place_again));  // read again: what is kept since the sums would spill
+                const auto vec = [&](int part, int i) {
+                    return unpack<T>(from[place_again + (part * NV + i) * kThreads]);
+                };
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if (i < mine) {
                         const W x = vec(0, i), g = vec(1, i), wf = w[i].get();
                         W o;
 #pragma unroll
-                        for (int j = 0; j < H; ++j) {
-                            const float2 z = fma2(x.v[j], r2, n2);
-                            o.v[j] = fma2(z, c2, fma2(mul2(g.v[j], wf.v[j]), r2, c1));
-                        }
+                        for (int j = 0; j < H; ++j)
+                            o.v[j] = fma2(add2(x.v[j], n2), c2, fma2(g.v[j], wf.v[j], c1));
                         if constexpr (PARTS == 3) {
                             const W k = vec(2, i);
 #pragma unroll
-                            for (int j = 0; j < H; ++j) o.v[j] = add2(o.v[j], k.v[j]);
+                            for (int j = 0; j < H; ++j) o.v[j] = fma2(o.v[j], r2, k.v[j]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < H; ++j) o.v[j] = mul2(o.v[j], r2);
                         }
                         *reinterpret_cast<uint4*>(y + i * step) = pack<T>(o);
                     }
