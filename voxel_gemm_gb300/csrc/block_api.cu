@@ -463,7 +463,8 @@ int vg_gated_scan_step(int64_t n, int C, int dtype, unsigned flags, const vg_row
     if ((n > 0 && !state) || misaligned(state, 16)) return VG_ERR_INVALID_ARG;
     if (n == 0) return VG_OK;
     cudaGetLastError();
-    return gated_scan_step(n, C, dtype, flags != 0, *gate, *x, state, *out, static_cast<cudaStream_t>(stream));
+    return gated_scan_step(n, C, dtype, flags != 0, *gate, *x, state, *out, plan_sms(0),
+                           static_cast<cudaStream_t>(stream));
 }
 
 int vg_gated_scan_status(void* ws, void* stream) { return record_status(ws, static_cast<cudaStream_t>(stream)); }

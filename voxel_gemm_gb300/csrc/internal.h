@@ -219,7 +219,7 @@ constexpr int kScanCarryRows = 16;
 size_t gated_scan_workspace_bytes(int64_t n, int c, int dtype, int sms);
 int gated_scan(const GatedScan& g, bool bwd, cudaStream_t s);
 int gated_scan_step(int64_t n, int c, int dtype, bool free_input, const vg_rows& gate, const vg_rows& x, float* state,
-                    const vg_rows& out, cudaStream_t s);
+                    const vg_rows& out, int sms, cudaStream_t s);
 
 int dropout_add(int64_t n, int dtype, const void* x, const void* residual, double p, const uint64_t* rng,
                 uint32_t call, void* out, int sms, cudaStream_t s);

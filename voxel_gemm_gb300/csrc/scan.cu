@@ -1017,10 +1017,10 @@ int gated_scan(const GatedScan& q, bool bwd, cudaStream_t s) {
 }
 
 int gated_scan_step(int64_t n, int c, int dtype, bool free_input, const vg_rows& gate, const vg_rows& x, float* state,
-                    const vg_rows& out, cudaStream_t s) {
+                    const vg_rows& out, int sms, cudaStream_t s) {
     const int v = dtype == VG_F32 ? 4 : 8;
     const int64_t vectors = n * (c / v);
-    const int grid = (int)std::min<int64_t>((vectors + kThreads - 1) / kThreads, 152 * 8);
+    const int grid = (int)std::min<int64_t>((vectors + kThreads - 1) / kThreads, (int64_t)sms * 8);
     const auto run = [&](auto kernel) {
         kernel<<<grid, kThreads, 0, s>>>(vectors, c / v, c, static_cast<const char*>(gate.data),
                                          gate.row_stride * 16 / v, static_cast<const char*>(x.data),
