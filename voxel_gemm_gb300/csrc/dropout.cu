@@ -101,19 +101,7 @@ __device__ __forceinline__ void one(const DropArgs& a, int64_t i, uint32_t w) {
     static_cast<T*>(a.out)[i] = from_f32<T>(y);
 }
 
-// A pair of elements of a 16-byte vector.
-__device__ __forceinline__ float2 unpack(uint32_t w, __nv_bfloat16) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ float2 unpack(uint32_t w, __half) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
-__device__ __forceinline__ uint32_t pack(float2 x, __nv_bfloat16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack(float2 x, __half) {
-    const __half2 h = __floats2half2_rn(x.x, x.y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
+// A pair of elements.
 template <bool RES>
 __device__ __forceinline__ float2 both(const DropArgs& a, float2 x, float2 r, uint32_t w0, uint32_t w1) {
     x = make_float2(w0 >= a.threshold ? x.x : 0.f, w1 >= a.threshold ? x.y : 0.f);
@@ -131,10 +119,11 @@ __device__ __forceinline__ uint4 vector(const DropArgs& a, const Philox& gen, ui
         return make_uint4(__float_as_uint(y.x), __float_as_uint(y.y), __float_as_uint(z.x), __float_as_uint(z.y));
     } else {
         const uint4 w = gen.words(2 * v), u = gen.words(2 * v + 1);
-        return make_uint4(pack(both<RES>(a, unpack(x.x, T()), unpack(r.x, T()), w.x, w.y), T()),
-                          pack(both<RES>(a, unpack(x.y, T()), unpack(r.y, T()), w.z, w.w), T()),
-                          pack(both<RES>(a, unpack(x.z, T()), unpack(r.z, T()), u.x, u.y), T()),
-                          pack(both<RES>(a, unpack(x.w, T()), unpack(r.w, T()), u.z, u.w), T()));
+        using P = Pair<T>;
+        return make_uint4(P::pack(both<RES>(a, P::unpack(x.x), P::unpack(r.x), w.x, w.y)),
+                          P::pack(both<RES>(a, P::unpack(x.y), P::unpack(r.y), w.z, w.w)),
+                          P::pack(both<RES>(a, P::unpack(x.z), P::unpack(r.z), u.x, u.y)),
+                          P::pack(both<RES>(a, P::unpack(x.w), P::unpack(r.w), u.z, u.w)));
     }
 }
 

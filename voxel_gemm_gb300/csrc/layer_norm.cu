@@ -69,28 +69,16 @@ template <typename T> struct Vec {
     static constexpr int H = 8 / (int)sizeof(T);  // pairs
     float2 v[H];
 };
-__device__ __forceinline__ float2 pair_of(uint32_t w, __nv_bfloat16) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ float2 pair_of(uint32_t w, __half) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
-__device__ __forceinline__ uint32_t word_of(float2 x, __nv_bfloat16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t word_of(float2 x, __half) {
-    const __half2 h = __floats2half2_rn(x.x, x.y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 template <typename T> __device__ __forceinline__ Vec<T> unpack(uint4 q) {
     Vec<T> r;
     if constexpr (sizeof(T) == 4) {
         r.v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
         r.v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
     } else {
-        r.v[0] = pair_of(q.x, T());
-        r.v[1] = pair_of(q.y, T());
-        r.v[2] = pair_of(q.z, T());
-        r.v[3] = pair_of(q.w, T());
+        r.v[0] = Pair<T>::unpack(q.x);
+        r.v[1] = Pair<T>::unpack(q.y);
+        r.v[2] = Pair<T>::unpack(q.z);
+        r.v[3] = Pair<T>::unpack(q.w);
     }
     return r;
 }
@@ -99,7 +87,7 @@ template <typename T> __device__ __forceinline__ uint4 pack(const Vec<T>& r) {
         return make_uint4(__float_as_uint(r.v[0].x), __float_as_uint(r.v[0].y), __float_as_uint(r.v[1].x),
                           __float_as_uint(r.v[1].y));
     else
-        return make_uint4(word_of(r.v[0], T()), word_of(r.v[1], T()), word_of(r.v[2], T()), word_of(r.v[3], T()));
+        return make_uint4(Pair<T>::pack(r.v[0]), Pair<T>::pack(r.v[1]), Pair<T>::pack(r.v[2]), Pair<T>::pack(r.v[3]));
 }
 template <typename T> __device__ __forceinline__ Vec<T> filled(float x) {
     Vec<T> r;

@@ -86,27 +86,6 @@ __device__ __forceinline__ float mul_(float a, float b) { return a * b; }
 __device__ __forceinline__ float2 sub_(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 __device__ __forceinline__ float sub_(float a, float b) { return a - b; }
 
-// Two 16-bit numbers of a word.
-template <typename T> struct Pair;
-template <> struct Pair<__half> {
-    static __device__ __forceinline__ float2 unpack(uint32_t w) {
-        return __half22float2(*reinterpret_cast<const __half2*>(&w));
-    }
-    static __device__ __forceinline__ uint32_t pack(float2 x) {
-        const __half2 h = __floats2half2_rn(x.x, x.y);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-};
-template <> struct Pair<__nv_bfloat16> {
-    static __device__ __forceinline__ float2 unpack(uint32_t w) {
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    }
-    static __device__ __forceinline__ uint32_t pack(float2 x) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-};
-
 // What a token's gate does to a state.  No form lets a h lose what is small beside h, nor 1 - a what is small beside 1.
 //
 // Side, for fp32: m = e / (1 + e) with e = exp(-|g|), the smaller of a = sigmoid(g) and 1 - a, held as m

@@ -768,7 +768,7 @@ def gated_scan_carries(n, channels, device="cuda") -> torch.Tensor:
     return torch.empty(int(lib().vg_gated_scan_carry_rows(n)), channels, dtype=torch.float32, device=device)
 
 
-def _scan(gate, offsets, order, carries, ws, flags, stream, what):
+def _scan(gate, offsets, order, carries, flags, stream, what):
     """(vg_scan, shape, batch, dtype, device, carries' address) of a call, checked."""
     (n, c), dt, dev = _matrix(gate, stream, what)
     batch = offsets.numel() - 1
@@ -785,7 +785,7 @@ def vg_gated_scan_fwd(gate, x, offsets, order, first, out, last, carries, ws, fl
     gate, x, out [rows, channels] (any row stride); offsets int32 [batch + 1]; order int32 [rows], the row of each
     position, or None; first, last float32 [batch, channels], the states before and after, or None; carries
     (gated_scan_carries) for the backward pass, or None; flags VG_SCAN_REVERSE, VG_SCAN_FREE_INPUT."""
-    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, ws, flags, stream, "vg_gated_scan_fwd")
+    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, flags, stream, "vg_gated_scan_fwd")
     _on(dev, "vg_gated_scan_fwd", ws)
     _check(lib().vg_gated_scan_fwd(a, _rows(gate, dt, s, dev, "gate"), _rows(x, dt, s, dev, "x"),
                                    _flat(first, torch.float32, b, dev, "first"), _rows(out, dt, s, dev, "out"),
@@ -796,7 +796,7 @@ def vg_gated_scan_fwd(gate, x, offsets, order, first, out, last, carries, ws, fl
 def vg_gated_scan_bwd(gate, x, offsets, order, first, carries, grad_out, grad_last, grad_gate, grad_x, grad_first, ws,
                       flags=0, stream=None) -> None:
     """Gradients of vg_gated_scan_fwd's gate, x and first (None: not wanted), from its carries; grad_last may be None."""
-    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, ws, flags, stream, "vg_gated_scan_bwd")
+    a, s, b, dt, dev, kept = _scan(gate, offsets, order, carries, flags, stream, "vg_gated_scan_bwd")
     _on(dev, "vg_gated_scan_bwd", ws)
     _check(lib().vg_gated_scan_bwd(a, _rows(gate, dt, s, dev, "gate"), _rows(x, dt, s, dev, "x"),
                                    _flat(first, torch.float32, b, dev, "first"), kept,
