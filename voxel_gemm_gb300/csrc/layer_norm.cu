@@ -15,8 +15,9 @@
 // registers.  Those sums leave as one fp32 row per block, added in a fixed order by a second
 // kernel, so they do not change from run to run.
 //
-// GB300, bf16: 602,492 rows of 1024 forward 368 us (6.7 TB/s), backward 545 and 5 (6.8 TB/s); 319,057 rows
-// of 128 forward 33 us, backward with a skipped gradient 52 and 4 (72 us of memory traffic in all).
+// GB300, bf16: 602,492 rows of 1024 forward 362 us (6.8 TB/s), backward 535 and 5 (6.9 TB/s; fp16, where four vectors a lane
+// spill, 576); 319,057 rows of 128 forward 33 us, backward with a skipped gradient 53 in all (72 us of memory
+// traffic).
 #include "common.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"

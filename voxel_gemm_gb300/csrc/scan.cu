@@ -11,14 +11,15 @@
 // while it works on these, and needs nothing of other warps, so loads stream.  The forward pass
 // keeps the state before every 16th token, from which the backward pass finds the others again.
 //
-// Bound by memory.  Gate and x (backward: gate and dy) are read twice: 602,492 tokens of 512 channels in
-// bf16 take 205 us for the maps (6.0 TB/s), 10 for the join and 290 for the pass (6.6 TB/s), backward 205, 10
-// and 530 (6.0 TB/s).  A single pass, in which blocks publish their maps and wait for those of the blocks before,
-// reads them once, but the waiting cost more: with a tree of maps, tiles held in shared memory and each tile's map
-// published before the last tile was finished, the forward pass took 950 us, 600 with the waits left out; 4.9 M
-// tokens of 64 channels took 1790, so 520.  Smaller pieces that stay in the L2 between the steps gain nothing
-// either: with all of its data there the last step is as slow (8.4 M more elements cost 6.5 us).  Blocks that
-// go from unit to unit without a pause, each warp's next tokens sent for across them, took 581 and 851 us.
+// Gate and x (backward: gate and dy) are read twice: 602,492 tokens of 512 channels in bf16 take 204 us for the
+// maps (6.1 TB/s), 7 for the join and 299 for the pass (6.4 TB/s), backward 202, 7 and 514 (6.2 TB/s); the maps issue in
+// 73 % of the cycles, the passes in 60.  Single passes, in which blocks publish their maps and wait for those of the blocks
+// before, were built first and read everything once: with a tree of maps, tiles held in shared memory and each tile's map
+// published before the last tile was finished, the forward pass took 950 us, and 600 with the waits left out, so that
+// its body too was slower than these steps; 4.9 M tokens of 64 channels took 1790, so 520.  None has been built around the
+// present body.  Smaller pieces that stay in the L2 between the steps gain nothing: with all of its data there the last
+// step is as slow (8.4 M more elements cost 6.5 us).  Blocks that go from unit to unit without a pause, each warp's next
+// tokens sent for across them, took 581 and 851 us.
 //
 // Where a sequence begins, the map is constant (A = -1 marks it, h -> B), so that nothing, not
 // even a NaN, passes from one sequence to the next.  A warp's tokens are the same for all of its
