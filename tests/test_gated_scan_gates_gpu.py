@@ -124,3 +124,29 @@ def test_gates_beyond_the_exponentials_range(dtype):
             assert r[name].isfinite().all(), name
         shut = x["gate"] < 0
         assert (r["grad_gate"].float().abs() <= 1e-30).all() and (r["grad_x"][~shut].float().abs() <= 1e-30).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("lengths,shift", [([40, 500, 60, 3000, 9], 0.0), ([40, 500, 60, 3000, 9], -4.0), ([900, 70_000], 2.0)])
+def test_16_bit_tokens_that_are_not_finite(dtype, lengths, shift):
+    """They reach their channel's later states of their sequence and the gradients of its gates, and nothing else."""
+    c, ends = 72, torch.tensor(lengths).cumsum(0).tolist()
+    x = make(lengths, c, dtype, state=True, seed=6, memory=(shift, shift + 4.0))
+    want = call(x)
+    x["x"] = x["x"].contiguous()
+    hit = torch.zeros_like(want["out"], dtype=torch.bool)
+    for row, col, v in ((45, 3, float("nan")), (ends[0] + 100, 4, float("inf")), (ends[-1] - 5, 71, -float("inf"))):
+        x["x"][row, col] = v
+        hit[row:next(e for e in ends if e > row), col] = True
+    got = call(x)
+    assert torch.equal(got["out"][~hit], want["out"][~hit]) and not got["out"][hit].isfinite().any()
+    assert torch.equal(got["grad_x"], want["grad_x"]) and torch.equal(got["grad_first"], want["grad_first"])
+    assert torch.equal(got["grad_gate"][~hit], want["grad_gate"][~hit])
+    y = make(lengths, c, dtype, state=True, seed=6, memory=(shift, shift + 4.0))
+    row, start = ends[0] + 300, ends[0]
+    y["grad_out"][row, 9] = float("nan")
+    got, hit = call(y), torch.zeros_like(hit)
+    hit[start:row + 1, 9] = True
+    assert torch.equal(got["out"], want["out"])
+    for name in ("grad_x", "grad_gate"):
+        assert torch.equal(got[name][~hit], want[name][~hit]) and not got[name][hit].isfinite().any(), name

@@ -39,7 +39,7 @@ using namespace ptx;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = kScanCarryRows;      // looked up and loaded at once; a state is kept for each such run
-constexpr int kHalf = kTokens / 2;           // unrolled: two times 16 tokens of straight code did not stay in the instruction cache
+constexpr int kHalf = kTokens / 2;           // unrolled: more straight code did not stay in the instruction cache
 constexpr int kMaxRuns = 16;                 // runs of a warp (ScanArgs::runs), at most
 constexpr int kRowBytes = 128, kRunBytes = kTokens * kRowBytes;  // of an operand in a block
 constexpr int kStep = kRowBytes / 4, kOperand = kRunBytes / 4;  // words from a token, an operand to the next

@@ -774,7 +774,8 @@ def _scan(gate, offsets, order, carries, flags, stream, what):
     batch = offsets.numel() - 1
     f32 = torch.float32
     rows = -(-n // VG_SCAN_CARRY_ROWS)
-    return (ScanStruct(n, c, batch, _DT.get(dt, -1), _word(flags, "flags"), _flat(offsets, torch.int32, (batch + 1,), dev, "offsets"),
+    return (ScanStruct(n, c, batch, _DT.get(dt, -1), _word(flags, "flags"),
+                       _flat(offsets, torch.int32, (batch + 1,), dev, "offsets"),
                        _flat(order, torch.int32, (n,), dev, "order")), (n, c), (batch, c), dt, dev,
             _flat(carries, f32, (rows, c), dev, "carries"))
 
